@@ -19,17 +19,17 @@ BLOCK = 1088  # bytes of one packed (16 columns, 128 rows) block: 1024 of codes,
 def listed():
     return [
         # one token through a small layer: the call whose launch and latency count most
-        _moe("moe one token, small experts", M=1, D=2048, F=768, E=64, k=4, renorm=True, residual=False),
+        _moe("moe one token small experts", M=1, D=2048, F=768, E=64, k=4, renorm=True, residual=False),
         # one token through a layer of the size of the dense projections elsewhere in this repository
         _moe("moe one token", M=1, D=5120, F=1408, E=64, k=8, renorm=True, residual=True),
         # a 6-token draft and its base, weights of the whole softmax, odd counts of everything
-        _moe("moe verify 7, odd sizes", M=7, D=2176, F=896, E=37, k=3, renorm=False, residual=False),
+        _moe("moe verify 7 odd sizes", M=7, D=2176, F=896, E=37, k=3, renorm=False, residual=False),
         # the longest verify step: 16 rows that together reach most experts
         _moe("moe verify 16", M=16, D=5120, F=1408, E=96, k=6, renorm=True, residual=True),
         # plain decode of one short sequence: latency
-        _attn("attention one token, short", count=1, new=1, length=611, q_heads=32, kv_heads=8, dim=128, page=16),
+        _attn("attention one token short", count=1, new=1, length=611, q_heads=32, kv_heads=8, dim=128, page=16),
         # the verify step of a 7-token draft far into one sequence
-        _attn("attention verify 8, long", count=1, new=8, length=32771, q_heads=32, kv_heads=8, dim=128, page=64),
+        _attn("attention verify 8 long", count=1, new=8, length=32771, q_heads=32, kv_heads=8, dim=128, page=64),
         # sixteen sequences of all lengths, some with no new token this step
         _attn("attention ragged batch", count=16, new=3, length=9001, q_heads=24, kv_heads=4, dim=64, page=16,
               ragged=True),
@@ -37,13 +37,13 @@ def listed():
         _attn("attention window and sinks", count=2, new=16, length=100003, q_heads=16, kv_heads=4, dim=256, page=32,
               window=4096, sinks=4),
         # one row, a small vocabulary, the usual filters: latency
-        _sample("sample one row, small", rows=1, vocab=32000, k=50, p=0.9, minp=0.0),
+        _sample("sample one row small", rows=1, vocab=32000, k=50, p=0.9, minp=0.0),
         # one row of the full vocabulary, nucleus alone: the whole distribution counts
-        _sample("sample one row, nucleus", rows=1, vocab=248320, k=0, p=0.95, minp=0.0),
+        _sample("sample one row nucleus", rows=1, vocab=248320, k=0, p=0.95, minp=0.0),
         # every row of a long verify step with settings of its own
-        _sample("sample 16 rows, mixed", rows=16, vocab=248320, k=200, p=0.9, minp=0.02, mixed=True),
+        _sample("sample 16 rows mixed", rows=16, vocab=248320, k=200, p=0.9, minp=0.02, mixed=True),
         # an odd vocabulary with tokens that a grammar forbids, flat temperature
-        _sample("sample 7 rows, masked", rows=7, vocab=50261, k=0, p=1.0, minp=0.05, masked=True),
+        _sample("sample 7 rows masked", rows=7, vocab=50261, k=0, p=1.0, minp=0.05, masked=True),
     ]
 
 
