@@ -18,6 +18,7 @@ __all__ = [
     "w4g128_probe_read", "w4g128_probe_copy", "w4g128_probe_sink_bytes", "w4g128_gemv_noalloc",
     "w4g128_noalloc_status", "w4g128_selftest_wait", "w4g128_gemm_add_rmsnorm", "w4g128_decode_step_host",
     "w4g128_schedule", "DecodeStep",
+    "w4g128_sample", "SampleArgs", "SampleStep", "MAX_SAMPLE_ROWS", "MAX_VOCAB",
     "MAX_M", "MAX_MATRICES", "SELFTEST_WS_BYTES", "SCHEDULE_FIELDS",
 ]
 
@@ -27,6 +28,8 @@ MAX_M = 16          # W4G128_MAX_M
 MAX_MATRICES = 512  # W4G128_MAX_MATRICES
 SELFTEST_WS_BYTES = 512  # W4G128_SELFTEST_WS_BYTES
 SCHEDULE_FIELDS = 8  # W4G128_SCHEDULE_FIELDS
+MAX_SAMPLE_ROWS = 4096  # W4G128_MAX_SAMPLE_ROWS
+MAX_VOCAB = 524160      # W4G128_MAX_VOCAB
 
 _lib = None
 
@@ -42,12 +45,11 @@ class _Matrix(ctypes.Structure):
                 ("K", ctypes.c_int), ("N", ctypes.c_int)]
 
 
-def exported_symbols():
-    """Names of every function the public headers (include/*.h) declare."""
+def exported_symbols(headers=("w4g128.h", "w4g128_probe.h")):
+    """Names of every function the named public headers of include/ declare
+    (the weight stream's by default; w4g128_ops.h: the operators around it)."""
     names = []
-    for fn in sorted(os.listdir(_INCLUDE)):
-        if not fn.endswith(".h"):
-            continue
+    for fn in headers:
         with open(os.path.join(_INCLUDE, fn)) as f:
             for line in f:
                 line = line.strip()
@@ -133,6 +135,8 @@ def _declare(L):
     L.w4g128_gemm_add_rmsnorm.argtypes = [p, p, p, p, ctypes.c_float, p, p, i, i, i, i, p, sz, p]
     L.w4g128_schedule.restype = i
     L.w4g128_schedule.argtypes = [ctypes.POINTER(_Matrix), i, i, ctypes.POINTER(ctypes.c_longlong), i]
+    L.w4g128_sample.restype = i
+    L.w4g128_sample.argtypes = [ctypes.POINTER(SampleArgs), p]
     return L
 
 
@@ -330,3 +334,82 @@ class DecodeStep:
                            self._ws, self._wb, self._stream)
         if rc != 0:
             raise W4G128Error("w4g128_decode_step_host", rc)
+
+
+class _Args(ctypes.Structure):
+    """Argument struct of an operator of include/w4g128_ops.h, filled from
+    keywords.  A tensor becomes its device pointer (the struct keeps the tensor
+    alive); it has to be on a GPU, of the element size that the field holds,
+    and reach at least as far as the sizes say (W4G128_ERR_INVALID_ARG).  Plain
+    integers are raw pointers and are not checked."""
+
+    _fn = ""
+    _itemsize = {}  # tensor field: bytes of an element
+
+    def __init__(self, **fields):
+        known = {f[0] for f in self._fields_}
+        for name in fields:
+            if name not in known:
+                raise TypeError(f"{type(self).__name__} has no field {name!r}")
+        super().__init__(**{k: (_ptr(v) if k in self._itemsize else v) for k, v in fields.items()})
+        self._keep = {k: v for k, v in fields.items() if k in self._itemsize and hasattr(v, "data_ptr")}
+        for name, t in self._keep.items():
+            size = self._itemsize[name]
+            if not t.is_cuda or (size and t.element_size() != size):
+                raise W4G128Error(f"{self._fn} ({name})", 1)
+            need = self._reach(name)
+            # the last element that the tensor's own storage holds behind its first
+            have = t.untyped_storage().nbytes() - t.storage_offset() * t.element_size()
+            if need * max(size, 1) > have:
+                raise W4G128Error(f"{self._fn} ({name})", 1)
+
+    def _reach(self, name):
+        """Elements (bytes where the field has no element size) that the call may touch from `name` on."""
+        return 0
+
+
+class _Step:
+    """An operator call whose arguments are marshalled once, like DecodeStep:
+    the struct, the workspace and the stream are fixed, `run` is one C call."""
+
+    _entry = ""
+
+    def __init__(self, args, ws=None, stream=None):
+        self._keep = (args, ws)  # the buffers outlive the step
+        self._args = ctypes.byref(args)
+        self._fn = getattr(lib(), self._entry)
+        s = _stream(stream)
+        self._rest = (s,) if ws is None else (_ptr(ws), _nbytes(ws), s)
+
+    def run(self):
+        rc = self._fn(self._args, *self._rest)
+        if rc != 0:
+            raise W4G128Error(self._entry, rc)
+
+
+class SampleArgs(_Args):
+    """w4g128_sample_args: logits bf16 (row r at r * row_stride), temperature,
+    top_p, min_p, u float32 [rows], top_k int32 [rows] (each filter may be
+    None), tokens int32 [rows], logprobs float32 [rows] or None."""
+
+    _fn = "w4g128_sample"
+    _fields_ = [("logits", ctypes.c_void_p), ("row_stride", ctypes.c_longlong), ("temperature", ctypes.c_void_p),
+                ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p), ("min_p", ctypes.c_void_p),
+                ("u", ctypes.c_void_p), ("tokens", ctypes.c_void_p), ("logprobs", ctypes.c_void_p),
+                ("rows", ctypes.c_int), ("vocab", ctypes.c_int)]
+    _itemsize = {"logits": 2, "temperature": 4, "top_k": 4, "top_p": 4, "min_p": 4, "u": 4, "tokens": 4,
+                 "logprobs": 4}
+
+    def _reach(self, name):
+        return (self.rows - 1) * self.row_stride + self.vocab if name == "logits" else self.rows
+
+
+def w4g128_sample(args, stream=None):
+    """One token per row (see include/w4g128_ops.h); args: SampleArgs."""
+    _check("w4g128_sample", lib().w4g128_sample(ctypes.byref(args), _stream(stream)))
+
+
+class SampleStep(_Step):
+    """w4g128_sample with its arguments marshalled once: SampleStep(args).run()."""
+
+    _entry = "w4g128_sample"

@@ -4,8 +4,8 @@
 
 #include <cstdint>
 
-#include "w4g128.h"
 #include "w4g128_internal.h"
+#include "w4g128_ops.h"
 
 namespace {
 
@@ -76,6 +76,7 @@ const char* w4g128_status_string(int status) {
     case W4G128_ERR_DEVICE: return "current device is not compute capability 10.3 (sm_103)";
     case W4G128_ERR_TIMEOUT: return "a bounded device-side wait timed out";
     case W4G128_ERR_INTERNAL: return "a kernel found its launch inconsistent and skipped its work";
+    case W4G128_ERR_CACHE: return "a length, row offset or page id in device memory is out of range";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,516 @@
+// Token sampling (w4g128_sample): temperature, top-k, top-p, min-p and the
+// draw itself, one launch, one read of the logits.
+//
+// A bf16 logit has at most 65536 values, so the row's whole distribution is a
+// histogram over 16-bit keys ordered like the values, and every token with the
+// same value has the same weight: the sort, the softmax and the cumulative sum
+// over the vocabulary become a scan over bins.  One row is one cluster of 8
+// CTAs.  Each counts its slice of the row into its own 65536 16-bit counters
+// (128 KB of shared memory; a slice has at most 65535 tokens), then merges an
+// eighth of the bins from the 8 copies over distributed shared memory, weighs
+// them and scans (count, mass).  The filters keep prefixes of the order, so
+// each is one point of the scan that one thread finds and tells the cluster.
+// The chosen bin and the rank within it lead back to the token: the copies
+// hold each slice's count of that bin, so one CTA re-reads its slice.
+//
+// Masses are exact integers (weights as 62-bit fractions of the largest, sums
+// in 128 bits): prefix sums agree to the bit whatever their order, so exactly
+// one thread owns each crossing.  FP64 runs at 2 operations a cycle and SM
+// here, so the weights come from an fp32 pair evaluation (exp2_neg) instead:
+// about 1e-14 relative, with 35 full-rate operations a bin.
+//
+// Bound: latency.  A row of 248320 logits is 0.5 MB, 0.1 us of HBM; the chain
+// load, count, merge, scan and four cluster barriers is what takes time.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "w4g128_ops.h"
+#include "w4g128_internal.h"
+#include "w4g128_ptx.cuh"
+
+namespace w4g128 {
+namespace {
+
+typedef unsigned __int128 u128;
+
+constexpr int kCtas = 8;          // cluster size: CTAs per row
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 65536;
+constexpr int kUnitBins = 8;      // bins per thread: 8 CTAs x 1024 threads x 8 = 65536
+constexpr size_t kHistBytes = kBins * 2;
+constexpr uint32_t kMinusInf = 0x007Fu;  // key of -inf: what is not above it is never chosen
+constexpr uint32_t kPlusInf = 0xFF80u;
+
+static_assert(kCtas * kThreads * kUnitBins == kBins, "one unit per thread");
+// a slice: its share of the 16-byte vectors and the ragged ends of up to 7 tokens
+static_assert((W4G128_MAX_VOCAB / 8 + kCtas - 1) / kCtas * 8 + 14 <= 65535, "a slice's count of one bin fits 16 bits");
+
+// The order-preserving key of a bf16 pattern; -0 becomes +0, NaN becomes 0.
+__device__ __forceinline__ uint32_t key_of(uint32_t b) {
+  if ((b & 0x7FFFu) > 0x7F80u) return 0u;
+  if (b == 0x8000u) b = 0u;
+  return (b & 0x8000u) ? (b ^ 0xFFFFu) : (b | 0x8000u);
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  const uint32_t b = (key & 0x8000u) ? (key ^ 0x8000u) : (key ^ 0xFFFFu);
+  return __uint_as_float(b << 16);
+}
+
+struct Pair {  // an unevaluated sum hi + lo, |lo| <= ulp(hi) / 2
+  float hi, lo;
+};
+__device__ __forceinline__ Pair two_sum(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ Pair two_prod(float a, float b) {
+  const float p = __fmul_rn(a, b);
+  return {p, __fmaf_rn(a, b, -p)};
+}
+
+// 2^-y as a fraction of 2^62, for y = y.hi + y.lo >= 0 (0 from y = 62.5 on).
+// y = k / 32 + r with |r| <= 1/64; 2^-r = e^z, z = -r ln 2, |z| <= 0.011, by
+// the first six terms of its series (the next one is below 3e-15), the sum
+// carried as a pair; times 2^(-(k mod 32) / 32) from the table, and shifted.
+__device__ __forceinline__ uint64_t exp2_neg(Pair y, const float2* table) {
+  if (!(y.hi < 62.5f)) return 0ull;
+  const float kf = rintf(y.hi * 32.f);
+  const int k = static_cast<int>(kf);
+  const Pair r = two_sum(__fsub_rn(y.hi, kf * 0.03125f), y.lo);  // the difference is exact
+  // ln 2 as a pair
+  constexpr float kL = 0.693147182464599609375f, kLl = -1.904654323148236e-9f;
+  Pair z = two_prod(-r.hi, kL);
+  z.lo = __fadd_rn(z.lo, __fmaf_rn(-r.hi, kLl, -r.lo * kL));
+  const Pair s = two_prod(z.hi, z.hi);
+  const float cube = __fmul_rn(s.hi, z.hi);
+  float tail = __fmaf_rn(z.hi, 1.f / 120.f, 1.f / 24.f);
+  tail = __fmaf_rn(tail, z.hi, 1.f / 6.f);
+  tail = __fmul_rn(tail, cube);
+  const Pair a = two_sum(1.f, z.hi);
+  const Pair b = two_sum(a.hi, 0.5f * s.hi);
+  float lo = __fadd_rn(__fadd_rn(a.lo, b.lo), z.lo);
+  lo = __fadd_rn(lo, __fmaf_rn(z.hi, z.lo, 0.5f * s.lo));
+  lo = __fadd_rn(lo, tail);
+  const Pair e = two_sum(b.hi, lo);
+  const float2 t = table[k & 31];
+  const Pair m = two_prod(e.hi, t.x);
+  const float mlo = __fadd_rn(m.lo, __fmaf_rn(e.hi, t.y, e.lo * t.x));
+  const float scale = __int_as_float((127 + 62 - (k >> 5)) << 23);  // 2^(62 - floor), floor <= 62
+  return static_cast<uint64_t>(__float2ll_rn(m.hi * scale) + __float2ll_rn(mlo * scale));
+}
+
+struct Params {
+  const uint16_t* logits;
+  long long row_stride;
+  const float* temperature;
+  const int* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* u;
+  int* tokens;
+  float* logprobs;
+  int vocab;
+};
+
+struct Sum {  // a number of tokens and their mass
+  uint32_t n;
+  u128 m;
+};
+__device__ __forceinline__ u128 shfl_up128(u128 v, int d) {
+  const uint64_t lo = __shfl_up_sync(~0u, static_cast<uint64_t>(v), d);
+  const uint64_t hi = __shfl_up_sync(~0u, static_cast<uint64_t>(v >> 64), d);
+  return (static_cast<u128>(hi) << 64) | lo;
+}
+
+// floor(z f / 2^64), and whether that is exact.
+__device__ __forceinline__ u128 scaled_floor(u128 z, uint64_t f, bool* exact) {
+  const uint64_t zl = static_cast<uint64_t>(z), zh = static_cast<uint64_t>(z >> 64);
+  const u128 low = static_cast<u128>(zl) * f;
+  *exact = static_cast<uint64_t>(low) == 0ull;
+  return static_cast<u128>(zh) * f + (low >> 64);  // zh < 2^18
+}
+
+__device__ __forceinline__ double as_double(u128 v) {
+  return static_cast<double>(static_cast<uint64_t>(v >> 64)) * 18446744073709551616.0 +
+         static_cast<double>(static_cast<uint64_t>(v));
+}
+
+// floor(d / w) for a quotient known to be below 2^20 (w > 0).
+__device__ __forceinline__ uint32_t small_quotient(u128 d, uint64_t w) {
+  uint32_t q = static_cast<uint32_t>(as_double(d) / static_cast<double>(w));
+  while (static_cast<u128>(q) * w > d) --q;
+  while (static_cast<u128>(q + 1) * w <= d) ++q;
+  return q;
+}
+
+template <class T>
+__device__ __forceinline__ T* peer(T* p, uint32_t rank) {
+  return static_cast<T*>(__cluster_map_shared_rank(p, rank));
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  cluster_arrive_release();
+  cluster_wait_acquire();
+}
+
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
+  extern __shared__ __align__(16) uint32_t hist[];  // bin b: bits 16 (b & 1) .. of word b / 2
+  __shared__ float2 table[32];
+  __shared__ Pair s_rate;                 // log2(e) / temperature
+  __shared__ uint32_t s_red[kWarps];
+  __shared__ uint32_t s_max[kCtas];
+  __shared__ Sum s_warp[kWarps], s_ok[kWarps], s_tot[kCtas], s_totok[kCtas];
+  __shared__ Sum s_topk, s_topp;          // what each filter keeps
+  __shared__ uint32_t s_key, s_rank;      // the chosen bin, and the token's place among its equals
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = cluster_ctarank();
+  const int row = blockIdx.x / kCtas;
+
+  cluster_arrive_relaxed();  // every CTA of the cluster runs before any writes into another
+  for (int i = tid; i < kBins / 8; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
+  if (tid < 32) {
+    const double t = exp2(-tid / 32.0);
+    const float hi = static_cast<float>(t);
+    table[tid] = make_float2(hi, static_cast<float>(t - static_cast<double>(hi)));
+  }
+  grid_dependency_wait();
+
+  float T = p.temperature ? p.temperature[row] : 1.f;
+  const bool greedy = !(T > 0.f);
+  if (greedy) T = 1.f;
+  if (tid == 32) {
+    const double c = 1.4426950408889634 / static_cast<double>(T);
+    const float hi = static_cast<float>(c);
+    s_rate = {hi, static_cast<float>(c - static_cast<double>(hi))};
+  }
+  __syncthreads();
+
+  // Count the slice: 16-byte vectors inside the row, the ragged ends by CTA 0
+  // and the last CTA, so that slices are index ranges in rank order.
+  const uint16_t* base = p.logits + static_cast<long long>(row) * p.row_stride;
+  const int head = min(p.vocab, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(base) & 15u)) & 15u) / 2);
+  const int nvec = (p.vocab - head) / 8;
+  const int v0 = static_cast<int>(static_cast<long long>(nvec) * rank / kCtas);
+  const int v1 = static_cast<int>(static_cast<long long>(nvec) * (rank + 1) / kCtas);
+  const int e0 = rank == 0 ? 0 : head + 8 * v0;
+  const int e1 = rank == kCtas - 1 ? p.vocab : head + 8 * v1;
+  uint32_t top = 0;
+  auto count = [&](uint32_t bits) {
+    const uint32_t k = key_of(bits);
+    if (k > kMinusInf) {
+      atomicAdd(&hist[k >> 1], (k & 1u) ? 0x10000u : 1u);
+      top = max(top, k);
+    }
+  };
+  const uint4* vec = reinterpret_cast<const uint4*>(base + head);
+  for (int i = v0 + tid; i < v1; i += kThreads) {
+    const uint4 v = __ldg(vec + i);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      count(q[j] & 0xFFFFu);
+      count(q[j] >> 16);
+    }
+  }
+  if (rank == 0 && tid < head) count(base[tid]);
+  if (rank == kCtas - 1 && head + 8 * nvec + tid < p.vocab) count(base[head + 8 * nvec + tid]);
+  top = __reduce_max_sync(~0u, top);
+  if (lane == 0) s_red[warp] = top;
+  __syncthreads();
+  cluster_wait_acquire();
+  if (warp == 0) {
+    top = __reduce_max_sync(~0u, s_red[lane]);
+    if (lane < kCtas) *peer(&s_max[rank], lane) = top;
+  }
+  cluster_sync_all();
+
+  uint32_t maxkey = 0;
+#pragma unroll
+  for (int j = 0; j < kCtas; ++j) maxkey = max(maxkey, s_max[j]);
+
+  // Merge, weigh and scan.  Units fall with (rank, tid): the order of the draw.
+  const int unit = kBins / kUnitBins - 1 - (static_cast<int>(rank) * kThreads + tid);
+  const float vmax = value_of(maxkey);
+  const Pair rate = s_rate;
+  auto weight = [&](uint32_t key) -> uint64_t {
+    if (key == maxkey) return 1ull << 62;
+    if (maxkey == kPlusInf) return 0ull;
+    const Pair d = two_sum(vmax, -value_of(key));
+    Pair y = two_prod(d.hi, rate.hi);
+    y.lo = __fadd_rn(y.lo, __fmaf_rn(d.hi, rate.lo, d.lo * rate.hi));
+    return exp2_neg(two_sum(y.hi, y.lo), table);
+  };
+  const float minp = (p.min_p && !greedy) ? p.min_p[row] : 0.f;
+  const bool use_minp = minp > 0.f;
+  const uint64_t least = use_minp ? static_cast<uint64_t>(fminf(minp, 1.f) * 4611686018427387904.f) : 0ull;
+  uint32_t c[kUnitBins] = {};  // c[i]: bin 8 unit + i
+  Sum mine{0u, 0}, ok{0u, 0};
+  if (static_cast<uint32_t>(unit) * kUnitBins <= maxkey) {
+#pragma unroll
+    for (int j = 0; j < kCtas; ++j) {
+      const uint4 v = reinterpret_cast<const uint4*>(peer(hist, j))[unit];
+      c[0] += v.x & 0xFFFFu; c[1] += v.x >> 16; c[2] += v.y & 0xFFFFu; c[3] += v.y >> 16;
+      c[4] += v.z & 0xFFFFu; c[5] += v.z >> 16; c[6] += v.w & 0xFFFFu; c[7] += v.w >> 16;
+    }
+#pragma unroll
+    for (int i = 0; i < kUnitBins; ++i) {
+      if (c[i]) {
+        const uint64_t w = weight(unit * kUnitBins + i);
+        const u128 m = static_cast<u128>(w) * c[i];
+        mine.n += c[i];
+        mine.m += m;
+        if (w >= least) {
+          ok.n += c[i];
+          ok.m += m;
+        }
+      }
+    }
+  }
+  Sum inc = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t n = __shfl_up_sync(~0u, inc.n, d);
+    const u128 m = shfl_up128(inc.m, d);
+    if (lane >= d) {
+      inc.n += n;
+      inc.m += m;
+    }
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  if (use_minp) {  // the same for every thread of the cluster
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t n = __shfl_up_sync(~0u, ok.n, d);
+      const u128 m = shfl_up128(ok.m, d);
+      if (lane >= d) {
+        ok.n += n;
+        ok.m += m;
+      }
+    }
+    if (lane == 31) s_ok[warp] = ok;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    Sum t = s_warp[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t n = __shfl_up_sync(~0u, t.n, d);
+      const u128 m = shfl_up128(t.m, d);
+      if (lane >= d) {
+        t.n += n;
+        t.m += m;
+      }
+    }
+    s_warp[lane] = t;  // inclusive
+    __syncwarp();
+    if (lane < kCtas) *peer(&s_tot[rank], lane) = s_warp[kWarps - 1];
+  } else if (warp == 1 && use_minp) {
+    Sum t = s_ok[lane];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      t.n += __shfl_xor_sync(~0u, t.n, d);
+      const uint64_t lo = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m), d);
+      const uint64_t hi = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m >> 64), d);
+      t.m += (static_cast<u128>(hi) << 64) | lo;
+    }
+    if (lane < kCtas) *peer(&s_totok[rank], lane) = t;
+  }
+  cluster_sync_all();
+
+  Sum before{0u, 0}, total{0u, 0}, passed{0u, 0};  // before: of the bins above this thread's
+#pragma unroll
+  for (int j = 0; j < kCtas; ++j) {
+    if (j == static_cast<int>(rank)) before = total;
+    total.n += s_tot[j].n;
+    total.m += s_tot[j].m;
+    if (use_minp) {
+      passed.n += s_totok[j].n;
+      passed.m += s_totok[j].m;
+    }
+  }
+  if (total.n == 0u) {  // no remote access is outstanding
+    if (rank == 0 && tid == 0) {
+      p.tokens[row] = -1;
+      if (p.logprobs) p.logprobs[row] = __int_as_float(0xFF800000);
+    }
+    return;
+  }
+  if (warp > 0) {
+    before.n += s_warp[warp - 1].n;
+    before.m += s_warp[warp - 1].m;
+  }
+  before.n += inc.n - mine.n;
+  before.m += inc.m - mine.m;
+
+  // top-k: the kept count and mass
+  const int kreq = greedy ? 1 : (p.top_k ? p.top_k[row] : 0);
+  Sum kept = total;
+  if (kreq > 0 && static_cast<uint32_t>(kreq) < total.n) {
+    const uint32_t K = static_cast<uint32_t>(kreq);
+    if (before.n < K && K <= before.n + mine.n) {
+      uint32_t left = K - before.n;
+      u128 m = before.m;
+#pragma unroll
+      for (int i = kUnitBins - 1; i >= 0; --i) {
+        const uint32_t take = min(left, c[i]);
+        if (take) m += static_cast<u128>(weight(unit * kUnitBins + i)) * take;
+        left -= take;
+      }
+      for (int j = 0; j < kCtas; ++j) *peer(&s_topk, j) = Sum{K, m};
+    }
+    cluster_sync_all();
+    kept = s_topk;
+  }
+  // top-p: the tokens whose predecessors' mass is below the fraction
+  const float top_p = (p.top_p && !greedy) ? p.top_p[row] : 1.f;
+  if (top_p < 1.f) {
+    const uint64_t f = top_p > 0.f ? static_cast<uint64_t>(static_cast<double>(top_p) * 18446744073709551616.0) : 0ull;
+    bool exact;
+    u128 goal = scaled_floor(kept.m, f, &exact);
+    if (!exact || goal == 0) goal += 1;  // before < fraction as integers: before < ceil; the first token stays
+    const uint32_t limit = kept.n;
+    if (before.m < goal && goal <= before.m + mine.m) {
+      Sum k = before;
+      bool open = true;
+#pragma unroll
+      for (int i = kUnitBins - 1; i >= 0; --i) {
+        if (open && c[i]) {
+          const uint64_t w = weight(unit * kUnitBins + i);
+          if (w > 0ull && k.m + static_cast<u128>(w) * c[i] >= goal) {
+            const uint32_t take = small_quotient(goal - k.m - 1, w) + 1;  // ceil((goal - before) / w)
+            k.n += take;
+            k.m += static_cast<u128>(w) * take;
+            open = false;
+          } else {
+            k.n += c[i];
+            k.m += static_cast<u128>(w) * c[i];
+          }
+        }
+      }
+      // top-k ends inside a bin: it may keep fewer of equal tokens
+      if (k.n > limit) k = kept;
+      for (int j = 0; j < kCtas; ++j) *peer(&s_topp, j) = k;
+    }
+    cluster_sync_all();
+    kept = s_topp;
+  }
+  if (use_minp) {
+    if (minp > 1.f) passed = Sum{1u, static_cast<u128>(1ull << 62)};
+    if (passed.n < kept.n) kept = passed;
+  }
+
+  // The draw.
+  float uu = p.u[row];
+  if (!(uu > 0.f)) uu = 0.f;
+  const uint64_t f = uu < 1.f ? static_cast<uint64_t>(static_cast<double>(uu) * 18446744073709551616.0) : ~0ull;
+  bool exact;
+  const u128 goal = scaled_floor(kept.m, f, &exact);  // below kept.m
+  if (before.m <= goal && goal < before.m + mine.m) {
+    u128 m = before.m;
+    bool open = true;
+#pragma unroll
+    for (int i = kUnitBins - 1; i >= 0; --i) {
+      if (open && c[i]) {
+        const uint64_t w = weight(unit * kUnitBins + i);
+        const u128 next = m + static_cast<u128>(w) * c[i];
+        if (goal < next) {
+          const uint32_t j = small_quotient(goal - m, w);
+          for (int r = 0; r < kCtas; ++r) {
+            *peer(&s_key, r) = static_cast<uint32_t>(unit * kUnitBins + i);
+            *peer(&s_rank, r) = j;
+          }
+          if (p.logprobs) {
+            // log(w / kept): near 1 from the exact remainder, so that it keeps its relative precision
+            const double z = as_double(kept.m);
+            const float gone = static_cast<float>(as_double(kept.m - w) / z);
+            p.logprobs[row] =
+                gone < 0.5f ? log1pf(-gone) : logf(static_cast<float>(static_cast<double>(w) / z));
+          }
+          open = false;
+        }
+        m = next;
+      }
+    }
+  }
+  cluster_sync_all();
+
+  // Back to the token: the (rank)-th occurrence of the key in index order.
+  const uint32_t key = s_key;
+  uint32_t nth = s_rank, own = 0;
+  bool here = true;
+  for (int j = 0; j <= static_cast<int>(rank); ++j) {
+    const uint32_t n = (peer(hist, j)[key >> 1] >> ((key & 1u) * 16)) & 0xFFFFu;
+    if (j == static_cast<int>(rank)) own = n;
+    else if (nth < n) here = false;
+    else nth -= n;
+    if (!here) break;
+  }
+  here = here && nth < own;
+  if (here) {  // the same for every thread of the CTA
+    const int per = (e1 - e0 + kThreads - 1) / kThreads;
+    const int a = min(e1, e0 + tid * per), b = min(e1, a + per);
+    uint32_t n = 0;
+    for (int i = a; i < b; ++i) n += key_of(base[i]) == key;
+    uint32_t pre = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(~0u, pre, d);
+      if (lane >= d) pre += v;
+    }
+    if (lane == 31) s_red[warp] = pre;
+    __syncthreads();
+    uint32_t off = 0;
+    for (int j = 0; j < warp; ++j) off += s_red[j];
+    uint32_t at = off + pre - n;
+    if (at <= nth && nth < at + n) {
+      for (int i = a; i < b; ++i) {
+        if (key_of(base[i]) == key) {
+          if (at == nth) p.tokens[row] = i;
+          ++at;
+        }
+      }
+    }
+  }
+  cluster_sync_all();  // no CTA leaves while another reads its counters
+}
+
+}  // namespace
+}  // namespace w4g128
+
+extern "C" int w4g128_sample(const w4g128_sample_args* a, void* stream) {
+  using namespace w4g128;
+  if (a == nullptr || a->logits == nullptr || a->u == nullptr || a->tokens == nullptr) return W4G128_ERR_INVALID_ARG;
+  if (a->rows < 1 || a->rows > W4G128_MAX_SAMPLE_ROWS) return W4G128_ERR_INVALID_ARG;
+  if (a->vocab < 1 || a->vocab > W4G128_MAX_VOCAB || a->row_stride < a->vocab) return W4G128_ERR_SHAPE;
+  auto off = [](const void* q, uintptr_t n) { return (reinterpret_cast<uintptr_t>(q) & (n - 1)) != 0; };
+  if (off(a->logits, 2) || off(a->temperature, 4) || off(a->top_k, 4) || off(a->top_p, 4) || off(a->min_p, 4) ||
+      off(a->u, 4) || off(a->tokens, 4) || off(a->logprobs, 4))
+    return W4G128_ERR_ALIGN;
+  const int fault = fault_hook();
+  if (fault != W4G128_OK) return fault;
+  if (!device_is_sm103()) return W4G128_ERR_DEVICE;
+  const Params p{a->logits, a->row_stride, a->temperature, a->top_k, a->top_p, a->min_p, a->u,
+                 a->tokens, a->logprobs, a->vocab};
+  if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(kHistBytes)) != cudaSuccess) {
+    cudaGetLastError();
+    return W4G128_ERR_CUDA;
+  }
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(a->rows) * kCtas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kHistBytes;
+  if (cudaLaunchKernelEx(&cfg, sample_kernel, p) != cudaSuccess) {
+    cudaGetLastError();
+    return W4G128_ERR_CUDA;
+  }
+  return W4G128_OK;
+}
