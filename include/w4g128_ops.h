@@ -67,6 +67,80 @@ typedef struct {
  * other arrays 4). */
 W4G128_API int w4g128_sample(const w4g128_sample_args* args, void* stream);
 
+/* ------------------------------------------------------------------------
+ * ATTENTION OF NEW TOKENS OVER A PAGED CACHE
+ *
+ * For each of `count` sequences, the attention of its 0 .. max_new (at most
+ * 16) newest tokens over everything the sequence has in a paged key/value
+ * cache, the new tokens themselves included: a decode step (one token), or
+ * the verify step of a draft.  Sequence b owns the rows row_offsets[b] ..
+ * row_offsets[b + 1] - 1 of q, k_new, v_new and out, n of them; lens[b] is its
+ * length with them, so its row i stands at position p = lens[b] - n + i and
+ *   out[h] = sum_j softmax_j(scale q[h] . k_j[h / (q_heads / kv_heads)]) v_j
+ * over the positions j <= p with p - j < window (window = 0: all) or
+ * j < sinks.  Position j of sequence b is slot j % page_size of page
+ * page_table[b][j / page_size].  First the new rows' k_new and v_new are
+ * written to their places (k_new = v_new = NULL: they are there already); the
+ * call itself reads them from k_new and v_new, not from the cache.
+ *
+ * A row at a negative position (more rows than the length) sees nothing: its
+ * out is 0 and its key and value are not written.  Rows of no sequence are
+ * left as they are.  Pages that no row of a sequence sees are not read, and
+ * their table entries may hold anything.  Masked positions take no part in a
+ * row's result whatever they hold, infinities and NaN included.
+ *
+ * Row m's bits depend on its own position, query and visible keys and values
+ * alone, not on the other rows or sequences of the call, given the same
+ * max_len, window, sinks and head_dim: a verify pass reproduces the
+ * one-token steps (the split of a sequence into fixed chunks of positions
+ * follows from those arguments).  Scores, the softmax statistics and the
+ * output are held in fp32; the softmax weights enter the second product
+ * rounded to bf16 and are summed as rounded, so they add up to 1. */
+typedef struct {
+  const w4g128_bf16* q;     /* row r, head h at r * q_row + h * head_dim */
+  const w4g128_bf16* k_new; /* row r, head h at r * kv_row + h * head_dim; or NULL, with v_new */
+  const w4g128_bf16* v_new;
+  w4g128_bf16* k_cache;     /* page g, slot s, head h at g * page_stride + s * slot_stride + h * head_stride */
+  w4g128_bf16* v_cache;     /* the same strides */
+  const int* page_table;    /* sequence b at b * table_row; ceil(max_len / page_size) entries */
+  const int* row_offsets;   /* [count + 1], rising, within 0 .. rows */
+  const int* lens;          /* [count], 0 .. max_len */
+  w4g128_bf16* out;         /* row r, head h at r * out_row + h * head_dim */
+  long long q_row, kv_row, out_row;                  /* elements, as all strides */
+  long long page_stride, slot_stride, head_stride;
+  long long table_row;
+  int rows;      /* of q, k_new, v_new and out: 1 .. 2^20 */
+  int count;     /* sequences, 1 .. W4G128_MAX_SEQUENCES */
+  int q_heads;   /* a multiple of kv_heads, at most 16 times as many */
+  int kv_heads;  /* 1 .. 256 */
+  int head_dim;  /* 64, 128 or 256 */
+  int pages;     /* pages of the cache */
+  int page_size; /* a multiple of 16 */
+  int max_len;   /* the longest length that the table can hold, 1 .. 2^24: sizes the split and the workspace */
+  int max_new;   /* most new rows of a sequence, 1 .. 16 */
+  int window;    /* 0: none */
+  int sinks;     /* first positions that stay visible behind the window; 0 without a window */
+  float scale;   /* finite */
+} w4g128_attend_args;
+
+#define W4G128_MAX_SEQUENCES 1024
+
+/* Workspace bytes of w4g128_attend for these sizes: a status word and the
+ * fp32 partial results of each chunk.  0 for arguments it would refuse. */
+W4G128_API size_t w4g128_attend_workspace_bytes(const w4g128_attend_args* args);
+
+/* The attention above.  q, k_new, v_new, the caches and out: 16-byte aligned,
+ * their strides multiples of 8 elements; the int arrays 4 bytes; ws 16.  out
+ * must overlap nothing else.  lens, row_offsets and the table are read on the
+ * device, so a captured call follows them from replay to replay.  A sequence
+ * whose length or row range lies outside the bounds above is left out, and a
+ * page id outside 0 .. pages - 1 counts as a page that no row sees and takes
+ * no new rows; both leave W4G128_ERR_CACHE in the workspace's status word
+ * (w4g128_workspace_status).  Returns W4G128_ERR_INVALID_ARG,
+ * W4G128_ERR_SHAPE, W4G128_ERR_ALIGN or W4G128_ERR_WORKSPACE for what breaks
+ * the bounds above. */
+W4G128_API int w4g128_attend(const w4g128_attend_args* args, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

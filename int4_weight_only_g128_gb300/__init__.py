@@ -19,6 +19,7 @@ __all__ = [
     "w4g128_noalloc_status", "w4g128_selftest_wait", "w4g128_gemm_add_rmsnorm", "w4g128_decode_step_host",
     "w4g128_schedule", "DecodeStep",
     "w4g128_sample", "SampleArgs", "SampleStep", "MAX_SAMPLE_ROWS", "MAX_VOCAB",
+    "w4g128_attend", "w4g128_attend_workspace_bytes", "AttendArgs", "AttendStep", "MAX_SEQUENCES", "ERR_CACHE",
     "MAX_M", "MAX_MATRICES", "SELFTEST_WS_BYTES", "SCHEDULE_FIELDS",
 ]
 
@@ -30,6 +31,8 @@ SELFTEST_WS_BYTES = 512  # W4G128_SELFTEST_WS_BYTES
 SCHEDULE_FIELDS = 8  # W4G128_SCHEDULE_FIELDS
 MAX_SAMPLE_ROWS = 4096  # W4G128_MAX_SAMPLE_ROWS
 MAX_VOCAB = 524160      # W4G128_MAX_VOCAB
+MAX_SEQUENCES = 1024    # W4G128_MAX_SEQUENCES
+ERR_CACHE = 9           # W4G128_ERR_CACHE
 
 _lib = None
 
@@ -137,6 +140,10 @@ def _declare(L):
     L.w4g128_schedule.argtypes = [ctypes.POINTER(_Matrix), i, i, ctypes.POINTER(ctypes.c_longlong), i]
     L.w4g128_sample.restype = i
     L.w4g128_sample.argtypes = [ctypes.POINTER(SampleArgs), p]
+    L.w4g128_attend_workspace_bytes.restype = sz
+    L.w4g128_attend_workspace_bytes.argtypes = [ctypes.POINTER(AttendArgs)]
+    L.w4g128_attend.restype = i
+    L.w4g128_attend.argtypes = [ctypes.POINTER(AttendArgs), p, sz, p]
     return L
 
 
@@ -413,3 +420,46 @@ class SampleStep(_Step):
     """w4g128_sample with its arguments marshalled once: SampleStep(args).run()."""
 
     _entry = "w4g128_sample"
+
+
+class AttendArgs(_Args):
+    """w4g128_attend_args: bf16 q, k_new, v_new (or None), k_cache, v_cache,
+    out and int32 page_table, row_offsets, lens; strides in elements."""
+
+    _fn = "w4g128_attend"
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_new", "v_new", "k_cache", "v_cache", "page_table",
+                                               "row_offsets", "lens", "out")] + \
+               [(n, ctypes.c_longlong) for n in ("q_row", "kv_row", "out_row", "page_stride", "slot_stride",
+                                                 "head_stride", "table_row")] + \
+               [(n, ctypes.c_int) for n in ("rows", "count", "q_heads", "kv_heads", "head_dim", "pages", "page_size",
+                                            "max_len", "max_new", "window", "sinks")] + [("scale", ctypes.c_float)]
+    _itemsize = {"q": 2, "k_new": 2, "v_new": 2, "k_cache": 2, "v_cache": 2, "page_table": 4, "row_offsets": 4,
+                 "lens": 4, "out": 2}
+
+    def _reach(self, name):
+        if name in ("q", "out"):
+            return (self.rows - 1) * (self.q_row if name == "q" else self.out_row) + self.q_heads * self.head_dim
+        if name in ("k_new", "v_new"):
+            return (self.rows - 1) * self.kv_row + self.kv_heads * self.head_dim
+        if name in ("k_cache", "v_cache"):
+            return (self.pages - 1) * self.page_stride + (self.page_size - 1) * self.slot_stride + \
+                (self.kv_heads - 1) * self.head_stride + self.head_dim
+        if name == "page_table":
+            return (self.count - 1) * self.table_row + (self.max_len - 1) // max(self.page_size, 1) + 1
+        return self.count + 1 if name == "row_offsets" else self.count
+
+
+def w4g128_attend_workspace_bytes(args):
+    return int(lib().w4g128_attend_workspace_bytes(ctypes.byref(args)))
+
+
+def w4g128_attend(args, ws, ws_bytes=None, stream=None):
+    """Attention of each sequence's new tokens over its pages (see include/w4g128_ops.h); args: AttendArgs."""
+    wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("w4g128_attend", lib().w4g128_attend(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
+
+
+class AttendStep(_Step):
+    """w4g128_attend with its arguments marshalled once: AttendStep(args, ws).run()."""
+
+    _entry = "w4g128_attend"

@@ -1,0 +1,664 @@
+// Attention of 1..16 new tokens per sequence over a paged cache
+// (w4g128_attend): split over the positions, joined by a second kernel.
+//
+// Rows of one key/value head (new tokens x query heads that share it) are the
+// 16-row tiles of a warp MMA (m16n8k16, bf16 -> fp32): with at most 256 rows
+// against every position, the work is the cache's bytes, and the point is to
+// read each byte once and keep enough of them in flight.
+//   * A sequence is cut into chunks of C positions at multiples of C; one CTA
+//     takes one (chunk, head, up to 64 rows).  C follows from max_len and the
+//     window alone, so a row's sums never depend on the rows beside it.
+//   * The CTA's 4 groups of warps take the chunk's 16-position tiles in turn,
+//     each with its own ring of cp.async stages and its own running maximum
+//     and sum: no barrier of the whole CTA until the end.  A group is RT warps,
+//     one per 16 rows, sharing the group's tiles.
+//   * A tile lies in one page (page sizes are multiples of 16): one table
+//     lookup per tile, made before the loop.
+//   * S = Q K^T lands in the registers that P V wants it in; K comes by
+//     ldmatrix, V by ldmatrix.trans, from rows whose 16-byte pieces are
+//     exchanged by the low bits of the position, free of bank conflicts.
+// Positions masked for some row hold arbitrary bits, and 0 x NaN is NaN: tiles
+// at a mask's edge are searched for non-finite values, which are then applied
+// to the rows that see them one by one.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "w4g128_ops.h"
+#include "w4g128_internal.h"
+#include "w4g128_ptx.cuh"
+#include "w4g128_status.cuh"
+
+namespace w4g128 {
+namespace {
+
+constexpr int kTile = 16;        // positions per tile
+constexpr int kKvGroups = 4;     // warp groups of a CTA, each with tiles of its own
+constexpr int kMaxChunk = 1024;  // positions per chunk, at most
+constexpr size_t kStatusBytes = 256;
+constexpr float kNone = -INFINITY;
+
+struct Params {
+  const uint16_t *q, *k_new, *v_new;
+  uint16_t *k_cache, *v_cache;
+  const int *table, *offsets, *lens;
+  uint16_t* out;
+  long long q_row, kv_row, out_row, page_stride, slot_stride, head_stride, table_row;
+  int rows, count, q_heads, kv_heads, group, pages, page_size, max_len, max_new, window, sinks;
+  int chunk, splits;  // positions per chunk; chunks a sequence may need
+  float scale2;       // scale * log2(e)
+  unsigned long long* status;
+  float* part;        // [count][splits][kv_heads][max_new * group][head_dim]: unnormalised sums
+  float2* stat;       // [count][splits][kv_heads][max_new * group]: maximum (base 2) and sum
+};
+
+// What the rows of one sequence see.
+struct Seq {
+  bool ok;
+  int first_row, n, len, start;  // start: the first new row's position (negative rows are empty)
+  int first;                     // the first real row's position
+  int lo, sink;                  // visible to some row: [0, sink) and [lo, len)
+  int sink_chunks, lo_chunk, chunks;
+  __device__ int chunk_id(int z) const { return z < sink_chunks ? z : lo_chunk + z - sink_chunks; }
+};
+
+__device__ __forceinline__ Seq sequence(const Params& p, int b) {
+  Seq s;
+  s.first_row = p.offsets[b];
+  s.n = p.offsets[b + 1] - s.first_row;
+  s.len = p.lens[b];
+  s.ok = s.first_row >= 0 && s.n >= 0 && s.n <= p.max_new && s.first_row <= p.rows - s.n && s.len >= 0 &&
+         s.len <= p.max_len;
+  s.start = s.len - s.n;
+  s.first = max(s.start, 0);
+  s.lo = p.window > 0 ? max(0, s.first - p.window + 1) : 0;
+  s.sink = p.window > 0 ? min(p.sinks, s.lo) : 0;
+  s.lo_chunk = s.lo / p.chunk;
+  s.sink_chunks = min((s.sink + p.chunk - 1) / p.chunk, s.lo_chunk);
+  s.chunks = s.ok && s.n > 0 && s.len > 0 ? s.sink_chunks + (s.len - 1) / p.chunk - s.lo_chunk + 1 : 0;
+  return s;
+}
+
+__device__ __forceinline__ bool visible(const Params& p, int row_pos, int pos) {
+  return pos <= row_pos && (p.window == 0 || row_pos - pos < p.window || pos < p.sinks);
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// 16 bytes, or zeros
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float exp2_fast(float x) {  // 2 ulp
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+__device__ __forceinline__ bool non_finite2(uint32_t v) {  // either bf16 of the word
+  return (v & 0x7F80u) == 0x7F80u || (v & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ uint32_t finite_or_zero2(uint32_t v) {
+  if ((v & 0x7F80u) == 0x7F80u) v &= 0xFFFF0000u;
+  if ((v & 0x7F800000u) == 0x7F800000u) v &= 0x0000FFFFu;
+  return v;
+}
+
+template <int D, int RT>
+struct Shape {
+  static constexpr int kThreads = kKvGroups * RT * 32;
+  static constexpr int kRowBytes = 2 * D;
+  static constexpr int kTileBytes = kTile * kRowBytes;  // K or V of one tile
+  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
+  static constexpr int kRing = kKvGroups * kStages * 2 * kTileBytes;
+  static constexpr int kJoin = (kKvGroups - 1) * RT * 16 * (D + 2) * 4;  // three groups' sums, maxima and sums of weights
+  static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+};
+
+template <int D, int RT>
+__global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __grid_constant__ Params p) {
+  using S = Shape<D, RT>;
+  constexpr int kSteps = D / 16;
+  constexpr int kChunks16 = D / 8;  // 16-byte pieces of a row
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int s_page[kMaxChunk / kTile];
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int kg = warp / RT, rt = warp % RT;
+  const int row_groups = (p.max_new * p.group + 16 * RT - 1) / (16 * RT);
+  const int head = blockIdx.y / row_groups, rg = blockIdx.y % row_groups;
+  const int b = blockIdx.z, z = blockIdx.x;
+
+  grid_dependency_wait();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) status_clear(p.status);
+  const Seq s = sequence(p, b);
+  if (!s.ok) {
+    if (z == 0 && blockIdx.y == 0 && tid == 0) status_error(p.status, W4G128_ERR_CACHE);
+    return;
+  }
+  const int live_rows = s.n * p.group;
+  if (rg * 16 * RT >= live_rows) return;
+  const bool direct = p.splits == 1;
+  if (z >= s.chunks && !(direct && z == 0)) return;  // (direct: empty rows are written as zeros)
+
+  const int p0 = s.chunks ? s.chunk_id(z) * p.chunk : 0;
+  const int p1 = s.chunks ? min(p0 + p.chunk, s.len) : 0;
+  const int fresh = p.k_new != nullptr ? s.first : s.len;  // positions from here on come from k_new, v_new
+
+  // this chunk's page ids; -1: not a page
+  const int tiles = (p1 - p0 + kTile - 1) / kTile;
+  for (int t = tid; t < tiles; t += S::kThreads) {
+    const int a = p0 + t * kTile;
+    const bool seen = a < s.sink || (a + kTile > s.lo && a < s.len);
+    int id = seen ? p.table[static_cast<long long>(b) * p.table_row + a / p.page_size] : -1;
+    if (seen && (id < 0 || id >= p.pages)) {
+      id = -1;
+      status_error(p.status, W4G128_ERR_CACHE);
+    }
+    s_page[t] = id;
+  }
+  __syncthreads();
+
+  // The new rows go to their pages; nobody reads those slots in this call.
+  if (rg == 0 && p1 > fresh) {
+    const int a = max(p0, fresh);
+    for (int i = tid; i < (p1 - a) * kChunks16; i += S::kThreads) {
+      const int pos = a + i / kChunks16, c = i % kChunks16;
+      const int id = s_page[(pos - p0) / kTile];
+      if (id < 0) continue;
+      const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
+                            static_cast<long long>(head) * D + c * 8;
+      const long long dst = static_cast<long long>(id) * p.page_stride + (pos % p.page_size) * p.slot_stride +
+                            head * p.head_stride + c * 8;
+      *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
+      *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
+    }
+  }
+
+  // Q: this lane's part of the A fragments of rows r and r + 8.
+  const int r = lane >> 2, c = lane & 3;
+  const int row0 = (rg * RT + rt) * 16 + r;
+  int pos_a = -1, pos_b = -1;  // the rows' positions
+  uint32_t qf[kSteps][4];
+  {
+    const uint32_t* qa = nullptr;
+    const uint32_t* qb = nullptr;
+    if (row0 < live_rows) {
+      pos_a = s.start + row0 / p.group;
+      qa = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row0 / p.group) * p.q_row +
+                                             static_cast<long long>(head * p.group + row0 % p.group) * D);
+    }
+    const int row1 = row0 + 8;
+    if (row1 < live_rows) {
+      pos_b = s.start + row1 / p.group;
+      qb = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row1 / p.group) * p.q_row +
+                                             static_cast<long long>(head * p.group + row1 % p.group) * D);
+    }
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      qf[k][0] = qa ? __ldg(qa + k * 8 + c) : 0u;
+      qf[k][1] = qb ? __ldg(qb + k * 8 + c) : 0u;
+      qf[k][2] = qa ? __ldg(qa + k * 8 + 4 + c) : 0u;
+      qf[k][3] = qb ? __ldg(qb + k * 8 + 4 + c) : 0u;
+    }
+  }
+
+  float acc[D / 8][4];
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  float m_a = kNone, m_b = kNone, l_a = 0.f, l_b = 0.f;
+
+  const uint32_t ring = smem_addr(smem) + kg * S::kStages * 2 * S::kTileBytes;
+  const uint8_t* ring_ptr = smem + kg * S::kStages * 2 * S::kTileBytes;
+  const int gl = rt * 32 + lane;  // thread within the group
+  auto group_sync = [&] {
+    if constexpr (RT == 1) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RT * 32) : "memory");
+  };
+  // The group's tiles that some row sees, in rising order.
+  auto next_tile = [&](int t) {
+    while (t < tiles) {
+      const int a = p0 + t * kTile;
+      if (a < s.sink || a + kTile > s.lo) break;
+      t += kKvGroups;
+    }
+    return t;
+  };
+  auto issue = [&](int t, int stage) {
+    if (t < tiles) {
+      const int a = p0 + t * kTile, id = s_page[t];
+      const uint32_t dst = ring + stage * 2 * S::kTileBytes;
+      const long long page = static_cast<long long>(max(id, 0)) * p.page_stride + head * p.head_stride;
+      const int slot = a % p.page_size;
+#pragma unroll
+      for (int i = 0; i < kTile * kChunks16 / (RT * 32); ++i) {
+        const int e = i * RT * 32 + gl;
+        const int j = e / kChunks16, ch = e % kChunks16, pos = a + j;
+        const bool is_new = pos >= fresh;
+        const bool real = pos < s.len && (is_new || id >= 0);
+        const long long src = is_new ? static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
+                                           static_cast<long long>(head) * D
+                                     : page + static_cast<long long>(slot + j) * p.slot_stride;
+        const uint32_t at = dst + j * S::kRowBytes + ((ch ^ (j & 7)) << 4);
+        const uint16_t* kb = is_new ? p.k_new : p.k_cache;
+        const uint16_t* vb = is_new ? p.v_new : p.v_cache;
+        cp_async16_or_zero(at, real ? kb + src + ch * 8 : p.k_cache, real);
+        cp_async16_or_zero(at + S::kTileBytes, real ? vb + src + ch * 8 : p.k_cache, real);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  int ahead = next_tile(kg);  // (chunks start at multiples of 64: a tile's group follows from its position)
+  int t = ahead;
+#pragma unroll
+  for (int i = 0; i < S::kStages - 1; ++i) {
+    issue(ahead, i);
+    ahead = next_tile(ahead + (ahead < tiles ? kKvGroups : 0));
+  }
+  int stage = 0;
+  const int last_pos = s.len - 1;  // of the sequence's last row
+  while (t < tiles) {
+    cp_async_wait_group<S::kStages - 2>();
+    group_sync();  // the tile is there for the group, and the stage refilled next is read out
+    issue(ahead, stage == 0 ? S::kStages - 1 : stage - 1);
+    ahead = next_tile(ahead + (ahead < tiles ? kKvGroups : 0));
+
+    const uint32_t kt = ring + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
+    const int a = p0 + t * kTile;
+    float sc[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) {
+      uint32_t kb[4];
+      const int j = (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
+      ldmatrix4(kb, kt + j * S::kRowBytes + ((ch ^ (j & 7)) << 4));
+      mma(sc[0], qf[k], kb[0], kb[1]);
+      mma(sc[1], qf[k], kb[2], kb[3]);
+    }
+    // every row sees the whole tile
+    const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && s_page[t] >= 0 &&
+                        (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sc[h][i] *= p.scale2;
+    const bool page_ok = s_page[t] >= 0;
+    auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && (page_ok || pos >= fresh); };
+    if (!inside) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!sees(i < 2 ? pos_a : pos_b, a + h * 8 + 2 * c + (i & 1))) sc[h][i] = kNone;
+    }
+    float ta = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+    float tb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
+      tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
+    }
+    if (__any_sync(~0u, ta > m_a || tb > m_b)) {  // (otherwise the factors below are 1)
+      const float na = fmaxf(m_a, ta), nb = fmaxf(m_b, tb);
+      const float fa = exp2_fast(m_a - (na == kNone ? 0.f : na)), fb = exp2_fast(m_b - (nb == kNone ? 0.f : nb));
+      const float ga = na == m_a ? 1.f : fa, gb = nb == m_b ? 1.f : fb;
+      m_a = na;
+      m_b = nb;
+      l_a *= ga;
+      l_b *= gb;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        acc[i][0] *= ga;
+        acc[i][1] *= ga;
+        acc[i][2] *= gb;
+        acc[i][3] *= gb;
+      }
+    }
+    const float ra = m_a == kNone ? 0.f : m_a, rb = m_b == kNone ? 0.f : m_b;
+    uint32_t pf[4];
+    pf[0] = pack_bf16(exp2_fast(sc[0][0] - ra), exp2_fast(sc[0][1] - ra));
+    pf[1] = pack_bf16(exp2_fast(sc[0][2] - rb), exp2_fast(sc[0][3] - rb));
+    pf[2] = pack_bf16(exp2_fast(sc[1][0] - ra), exp2_fast(sc[1][1] - ra));
+    pf[3] = pack_bf16(exp2_fast(sc[1][2] - rb), exp2_fast(sc[1][3] - rb));
+    l_a += (low_f(pf[0]) + high_f(pf[0])) + (low_f(pf[2]) + high_f(pf[2]));
+    l_b += (low_f(pf[1]) + high_f(pf[1])) + (low_f(pf[3]) + high_f(pf[3]));
+
+    bool odd = false;  // non-finite values in a tile that not every row sees whole
+    if (!inside) {
+      const uint4* v = reinterpret_cast<const uint4*>(ring_ptr + stage * 2 * S::kTileBytes + S::kTileBytes);
+      for (int i = lane; i < S::kTileBytes / 16; i += 32) {
+        const uint4 u = v[i];
+        odd |= non_finite2(u.x) || non_finite2(u.y) || non_finite2(u.z) || non_finite2(u.w);
+      }
+      odd = __any_sync(~0u, odd);
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      uint32_t vb[4];
+      const int j = (lane & 7) + (((lane >> 3) & 1) << 3), ch = 2 * i + (lane >> 4);
+      ldmatrix4_trans(vb, vt + j * S::kRowBytes + ((ch ^ (j & 7)) << 4));
+      if (odd) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vb[e] = finite_or_zero2(vb[e]);
+      }
+      mma(acc[2 * i], pf, vb[0], vb[1]);
+      mma(acc[2 * i + 1], pf, vb[2], vb[3]);
+    }
+    if (odd) {
+      const uint8_t* v = ring_ptr + stage * 2 * S::kTileBytes + S::kTileBytes;
+      for (int j = 0; j < kTile; ++j) {
+        const uint32_t wa = j < 8 ? pf[0] : pf[2], wb = j < 8 ? pf[1] : pf[3];
+        const int from = (lane & ~3) | ((j & 7) >> 1);
+        const uint32_t ua = __shfl_sync(~0u, wa, from), ub = __shfl_sync(~0u, wb, from);
+        const float fa = (j & 1) ? high_f(ua) : low_f(ua), fb = (j & 1) ? high_f(ub) : low_f(ub);
+        const bool va = sees(pos_a, a + j), vb = sees(pos_b, a + j);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          const uint32_t u = *reinterpret_cast<const uint32_t*>(v + j * S::kRowBytes + ((i ^ (j & 7)) << 4) + 4 * c);
+          if ((u & 0x7F80u) == 0x7F80u) {
+            if (va) acc[i][0] += fa * low_f(u);
+            if (vb) acc[i][2] += fb * low_f(u);
+          }
+          if ((u & 0x7F800000u) == 0x7F800000u) {
+            if (va) acc[i][1] += fa * high_f(u);
+            if (vb) acc[i][3] += fb * high_f(u);
+          }
+        }
+      }
+    }
+    t = next_tile(t + kKvGroups);
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+  }
+#pragma unroll
+  for (int d = 1; d < 4; d <<= 1) {
+    l_a += __shfl_xor_sync(~0u, l_a, d);
+    l_b += __shfl_xor_sync(~0u, l_b, d);
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // the ring becomes the exchange
+
+  // Join the four groups in order: groups 1..3 leave theirs, group 0 adds.
+  float* ex = reinterpret_cast<float*>(smem);
+  constexpr int kExWarp = 16 * (D + 2);
+  if (kg > 0) {
+    float* e = ex + ((kg - 1) * RT + rt) * kExWarp;
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+      reinterpret_cast<float4*>(e)[i * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    if (c == 0) {
+      float2* st = reinterpret_cast<float2*>(e + 16 * D);
+      st[r] = make_float2(m_a, l_a);
+      st[r + 8] = make_float2(m_b, l_b);
+    }
+  }
+  __syncthreads();
+  if (kg > 0) return;
+  float2 sa[kKvGroups], sb[kKvGroups];
+  sa[0] = make_float2(m_a, l_a);
+  sb[0] = make_float2(m_b, l_b);
+  float top_a = m_a, top_b = m_b;
+#pragma unroll
+  for (int g = 1; g < kKvGroups; ++g) {
+    const float2* st = reinterpret_cast<const float2*>(ex + ((g - 1) * RT + rt) * kExWarp + 16 * D);
+    sa[g] = st[r];
+    sb[g] = st[r + 8];
+    top_a = fmaxf(top_a, sa[g].x);
+    top_b = fmaxf(top_b, sb[g].x);
+  }
+  const float ra = top_a == kNone ? 0.f : top_a, rb = top_b == kNone ? 0.f : top_b;
+  float wa = exp2_fast(sa[0].x - ra), wb = exp2_fast(sb[0].x - rb);
+  l_a = sa[0].y * wa;
+  l_b = sb[0].y * wb;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    acc[i][0] *= wa;
+    acc[i][1] *= wa;
+    acc[i][2] *= wb;
+    acc[i][3] *= wb;
+  }
+#pragma unroll
+  for (int g = 1; g < kKvGroups; ++g) {
+    wa = exp2_fast(sa[g].x - ra);
+    wb = exp2_fast(sb[g].x - rb);
+    l_a = fmaf(sa[g].y, wa, l_a);
+    l_b = fmaf(sb[g].y, wb, l_b);
+    const float4* e = reinterpret_cast<const float4*>(ex + ((g - 1) * RT + rt) * kExWarp);
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) {
+      const float4 v = e[i * 32 + lane];
+      acc[i][0] = fmaf(v.x, wa, acc[i][0]);
+      acc[i][1] = fmaf(v.y, wa, acc[i][1]);
+      acc[i][2] = fmaf(v.z, wb, acc[i][2]);
+      acc[i][3] = fmaf(v.w, wb, acc[i][3]);
+    }
+  }
+
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int row = row0 + 8 * half;
+    if (row >= live_rows) continue;
+    const float l = half ? l_b : l_a;
+    if (direct) {
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible position: zeros
+      uint32_t* o = reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + row / p.group) * p.out_row +
+                                                static_cast<long long>(head * p.group + row % p.group) * D);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i * 4 + c] = pack_bf16(acc[i][2 * half] * inv, acc[i][2 * half + 1] * inv);
+    } else {
+      const long long at =
+          ((static_cast<long long>(b) * p.splits + z) * p.kv_heads + head) * (p.max_new * p.group) + row;
+      float2* o = reinterpret_cast<float2*>(p.part + at * D);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) o[i * 4 + c] = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
+      if (c == 0) p.stat[at] = make_float2(half ? top_b : top_a, l);
+    }
+  }
+}
+
+// Joins a row's chunks: 4 warps take the chunks by their number mod 4, each
+// sums its own in rising order, and the four sums are added in order.
+template <int D>
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p) {
+  constexpr int kPer = D / 32;
+  __shared__ float s_sum[4][D];
+  __shared__ float2 s_stat[4];
+  grid_dependency_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
+  const Seq s = sequence(p, b);
+  if (!s.ok || i >= s.n) return;
+  const int head = hq / p.group, row = i * p.group + hq % p.group;
+  const long long step = static_cast<long long>(p.kv_heads) * (p.max_new * p.group);
+  const long long at0 = (static_cast<long long>(b) * p.splits * p.kv_heads + head) * (p.max_new * p.group) + row;
+
+  float top = kNone;
+  for (int z = threadIdx.x; z < s.chunks; z += 128) top = fmaxf(top, p.stat[at0 + z * step].x);
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+  if (lane == 0) s_stat[warp].x = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(s_stat[0].x, s_stat[1].x), fmaxf(s_stat[2].x, s_stat[3].x));
+  const float ref = top == kNone ? 0.f : top;
+  __syncthreads();
+
+  float sum[kPer] = {}, l = 0.f;
+  for (int z = 0; z < s.chunks; ++z) {
+    if ((s.chunk_id(z) & 3) != warp) continue;
+    const float2 st = p.stat[at0 + z * step];
+    const float w = exp2_fast(st.x - ref);
+    const float* o = p.part + (at0 + z * step) * D + lane * kPer;
+    l = fmaf(st.y, w, l);
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) sum[k] = fmaf(o[k], w, sum[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) s_sum[warp][lane * kPer + k] = sum[k];
+  if (lane == 0) s_stat[warp].y = l;
+  __syncthreads();
+  l = (s_stat[0].y + s_stat[1].y) + (s_stat[2].y + s_stat[3].y);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + i) * p.out_row +
+                                              static_cast<long long>(hq) * D);
+  for (int k = threadIdx.x; k < D / 2; k += 128) {
+    const float x = (s_sum[0][2 * k] + s_sum[1][2 * k]) + (s_sum[2][2 * k] + s_sum[3][2 * k]);
+    const float y = (s_sum[0][2 * k + 1] + s_sum[1][2 * k + 1]) + (s_sum[2][2 * k + 1] + s_sum[3][2 * k + 1]);
+    out[k] = pack_bf16(x * inv, y * inv);
+  }
+}
+
+// Positions per chunk: a rule on the longest span that a call's rows may see.
+int chunk_for(const w4g128_attend_args& a) {
+  long long span = a.max_len;
+  if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
+  if (span <= 1024) return 64;
+  if (span <= 4096) return 128;
+  if (span <= 65536) return 256;
+  if (span <= 262144) return 512;
+  return kMaxChunk;
+}
+
+// Most chunks that a sequence's rows can see: all of them, or the window's
+// span of at most window + max_new - 1 positions and the sinks' chunks.
+int splits_for(const w4g128_attend_args& a, int chunk) {
+  const long long all = (static_cast<long long>(a.max_len) + chunk - 1) / chunk;
+  if (a.window == 0) return static_cast<int>(all);
+  const long long span = (static_cast<long long>(a.window) + a.max_new - 1 + chunk - 1) / chunk + 1;
+  const long long sinks = (static_cast<long long>(a.sinks) + chunk - 1) / chunk;
+  return static_cast<int>(std::min(all, span + sinks));
+}
+
+int check(const w4g128_attend_args* a) {
+  if (a == nullptr || a->q == nullptr || a->k_cache == nullptr || a->v_cache == nullptr || a->page_table == nullptr ||
+      a->row_offsets == nullptr || a->lens == nullptr || a->out == nullptr || (a->k_new == nullptr) != (a->v_new == nullptr))
+    return W4G128_ERR_INVALID_ARG;
+  if (a->rows < 1 || a->rows > (1 << 20) || a->count < 1 || a->count > W4G128_MAX_SEQUENCES || a->max_new < 1 ||
+      a->max_new > W4G128_MAX_M || a->window < 0 || a->sinks < 0 || (a->sinks > 0 && a->window == 0) ||
+      !std::isfinite(a->scale))
+    return W4G128_ERR_INVALID_ARG;
+  if (a->kv_heads < 1 || a->kv_heads > 256 || a->q_heads < a->kv_heads || a->q_heads % a->kv_heads != 0 ||
+      a->q_heads / a->kv_heads > 16 || (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256))
+    return W4G128_ERR_SHAPE;
+  if (a->pages < 1 || a->page_size < 16 || a->page_size % 16 != 0 || a->max_len < 1 || a->max_len > (1 << 24))
+    return W4G128_ERR_SHAPE;
+  const long long dim = a->head_dim;
+  if (a->q_row < a->q_heads * dim || a->out_row < a->q_heads * dim || (a->k_new && a->kv_row < a->kv_heads * dim) ||
+      a->slot_stride < dim || a->page_stride < dim || a->head_stride < dim ||
+      a->table_row < (a->max_len - 1) / a->page_size + 1)
+    return W4G128_ERR_SHAPE;
+  auto off = [](const void* q, uintptr_t n) { return (reinterpret_cast<uintptr_t>(q) & (n - 1)) != 0; };
+  if (off(a->q, 16) || off(a->k_new, 16) || off(a->v_new, 16) || off(a->k_cache, 16) || off(a->v_cache, 16) ||
+      off(a->out, 16) || off(a->page_table, 4) || off(a->row_offsets, 4) || off(a->lens, 4))
+    return W4G128_ERR_ALIGN;
+  for (long long v : {a->q_row, a->kv_row, a->out_row, a->page_stride, a->slot_stride, a->head_stride})
+    if (v % 8 != 0) return W4G128_ERR_ALIGN;
+  return W4G128_OK;
+}
+
+size_t bytes_for(const w4g128_attend_args& a) {
+  const int splits = splits_for(a, chunk_for(a));
+  if (splits == 1) return kStatusBytes;
+  return kStatusBytes + static_cast<size_t>(a.count) * splits * a.q_heads * a.max_new * (a.head_dim + 2) * 4;
+}
+
+template <int D, int RT>
+cudaError_t launch_attend(cudaLaunchConfig_t& cfg, const Params& p) {
+  using S = Shape<D, RT>;
+  const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+  if (e != cudaSuccess) return e;
+  const int row_groups = (p.max_new * p.group + 16 * RT - 1) / (16 * RT);
+  cfg.gridDim = dim3(p.splits, p.kv_heads * row_groups, p.count);
+  cfg.blockDim = dim3(S::kThreads);
+  cfg.dynamicSmemBytes = S::kBytes;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<D, RT>, p);
+}
+
+template <int D>
+cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
+  const int rows = p.max_new * p.group;
+  cudaError_t e;
+  if (rows <= 16) e = launch_attend<D, 1>(cfg, p);
+  else if (rows <= 32 || D == 256) e = launch_attend<D, 2>(cfg, p);  // (4 x 16 rows of 256 do not fit the registers)
+  else if constexpr (D != 256) e = launch_attend<D, 4>(cfg, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+}
+
+}  // namespace
+}  // namespace w4g128
+
+extern "C" {
+
+size_t w4g128_attend_workspace_bytes(const w4g128_attend_args* args) {
+  return w4g128::check(args) == W4G128_OK ? w4g128::bytes_for(*args) : 0;
+}
+
+int w4g128_attend(const w4g128_attend_args* a, void* ws, size_t ws_bytes, void* stream) {
+  using namespace w4g128;
+  int rc = check(a);
+  if (rc != W4G128_OK) return rc;
+  if (ws == nullptr) return W4G128_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(ws) & 15u) != 0) return W4G128_ERR_ALIGN;
+  if (ws_bytes < bytes_for(*a)) return W4G128_ERR_WORKSPACE;
+  rc = fault_hook();
+  if (rc != W4G128_OK) return rc;
+  if (!device_is_sm103()) return W4G128_ERR_DEVICE;
+  Params p;
+  p.q = a->q; p.k_new = a->k_new; p.v_new = a->v_new; p.k_cache = a->k_cache; p.v_cache = a->v_cache;
+  p.table = a->page_table; p.offsets = a->row_offsets; p.lens = a->lens; p.out = a->out;
+  p.q_row = a->q_row; p.kv_row = a->kv_row; p.out_row = a->out_row;
+  p.page_stride = a->page_stride; p.slot_stride = a->slot_stride; p.head_stride = a->head_stride;
+  p.table_row = a->table_row;
+  p.rows = a->rows; p.count = a->count; p.q_heads = a->q_heads; p.kv_heads = a->kv_heads;
+  p.group = a->q_heads / a->kv_heads;
+  p.pages = a->pages; p.page_size = a->page_size; p.max_len = a->max_len; p.max_new = a->max_new;
+  p.window = a->window; p.sinks = a->sinks;
+  p.chunk = chunk_for(*a);
+  p.splits = splits_for(*a, p.chunk);
+  p.scale2 = a->scale * 1.44269504088896340736f;
+  auto* base = static_cast<uint8_t*>(ws);
+  p.status = reinterpret_cast<unsigned long long*>(base);
+  p.part = reinterpret_cast<float*>(base + kStatusBytes);
+  p.stat = reinterpret_cast<float2*>(p.part + static_cast<size_t>(p.count) * p.splits * p.q_heads * p.max_new * a->head_dim);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = a->head_dim == 64 ? launch_dim<64>(cfg, p)
+                        : a->head_dim == 128 ? launch_dim<128>(cfg, p) : launch_dim<256>(cfg, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return W4G128_ERR_CUDA;
+  }
+  return W4G128_OK;
+}
+
+}  // extern "C"

@@ -33,13 +33,13 @@ def test_every_operator_is_exported(L):
 
 def test_constants_match_the_header():
     text = header()
-    for name in ("MAX_SAMPLE_ROWS", "MAX_VOCAB"):
+    for name in ("MAX_SAMPLE_ROWS", "MAX_VOCAB", "MAX_SEQUENCES", "ERR_CACHE"):
         assert re.search(rf"#define W4G128_{name} {getattr(w, name)}\b", text), name
 
 
 def test_structs_match_the_header():
     """Field names and order of each argument struct."""
-    for cls, name in ((w.SampleArgs, "w4g128_sample_args"),):
+    for cls, name in ((w.SampleArgs, "w4g128_sample_args"), (w.AttendArgs, "w4g128_attend_args")):
         body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", header()).group(1)
         body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
         fields = [f.split()[-1].lstrip("*") for line in body.split(";") if line.strip()
@@ -70,6 +70,51 @@ def test_sample_refusals(L):
     assert ei.value.status == E_SHAPE
 
 
+def attend_args(**kw):
+    a = dict(q=FAKE, k_new=FAKE, v_new=FAKE, k_cache=FAKE, v_cache=FAKE, page_table=FAKE, row_offsets=FAKE, lens=FAKE,
+             out=FAKE, q_row=512, kv_row=128, out_row=512, page_stride=2048, slot_stride=128, head_stride=64,
+             table_row=8, rows=4, count=1, q_heads=8, kv_heads=2, head_dim=64, pages=8, page_size=16, max_len=100,
+             max_new=4, window=0, sinks=0, scale=0.125)
+    a.update(kw)
+    return w.AttendArgs(**a)
+
+
+def attend(ws=FAKE, ws_bytes=1 << 40, **kw):
+    return w.lib().w4g128_attend(ctypes.byref(attend_args(**kw)), ws, ws_bytes, None)
+
+
+def test_attend_refusals(L):
+    assert L.w4g128_attend(None, FAKE, 1 << 40, None) == E_INVALID
+    for f in ("q", "k_new", "v_new", "k_cache", "v_cache", "page_table", "row_offsets", "lens", "out"):
+        assert attend(**{f: None}) == E_INVALID, f
+    assert attend(ws=None) == E_INVALID
+    for kw in (dict(rows=0), dict(rows=(1 << 20) + 1), dict(count=0), dict(count=w.MAX_SEQUENCES + 1), dict(max_new=0),
+               dict(max_new=17), dict(window=-1), dict(sinks=-1, window=5), dict(sinks=4),
+               dict(scale=float("nan")), dict(scale=float("inf"))):
+        assert attend(**kw) == E_INVALID, kw
+    for kw in (dict(q_heads=7), dict(q_heads=34, q_row=4096), dict(kv_heads=0), dict(head_dim=96), dict(head_dim=32),
+               dict(pages=0), dict(page_size=8), dict(page_size=24), dict(max_len=0), dict(max_len=(1 << 24) + 1),
+               dict(max_len=129), dict(q_row=504), dict(out_row=504), dict(kv_row=120), dict(slot_stride=56),
+               dict(head_stride=56), dict(page_stride=32)):
+        assert attend(**kw) == E_SHAPE, kw
+    for f in ("q", "k_new", "v_new", "k_cache", "v_cache", "out"):
+        assert attend(**{f: FAKE + 8}) == E_ALIGN, f
+    for f in ("page_table", "row_offsets", "lens"):
+        assert attend(**{f: FAKE + 2}) == E_ALIGN, f
+    for f, v in (("q_row", 516), ("kv_row", 132), ("out_row", 516), ("page_stride", 2052), ("slot_stride", 132),
+                 ("head_stride", 68)):
+        assert attend(**{f: v}) == E_ALIGN, f
+    assert attend(ws=FAKE + 8) == E_ALIGN
+    need = w.w4g128_attend_workspace_bytes(attend_args())
+    assert need > 0 and attend(ws_bytes=need - 1) == E_WS
+    assert w.w4g128_attend_workspace_bytes(attend_args(max_new=0)) == 0
+    # the longest cache with the most rows does not overflow the query
+    big = attend_args(max_len=1 << 24, count=1024, max_new=16, table_row=1 << 20, q_heads=256, q_row=1 << 15,
+                      kv_heads=16, head_dim=128, slot_stride=2048, head_stride=128, page_stride=1 << 15, kv_row=2048,
+                      out_row=1 << 15)
+    assert w.w4g128_attend_workspace_bytes(big) > 1 << 40
+
+
 def test_tensors_are_checked_by_the_binding():
     torch = pytest.importorskip("torch")
     logits = torch.zeros(100, dtype=torch.bfloat16)
@@ -84,3 +129,4 @@ def test_no_device_is_reported():
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
     assert sample() == E_DEVICE
+    assert attend() == E_DEVICE
