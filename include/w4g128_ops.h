@@ -141,6 +141,56 @@ W4G128_API size_t w4g128_attend_workspace_bytes(const w4g128_attend_args* args);
  * the bounds above. */
 W4G128_API int w4g128_attend(const w4g128_attend_args* args, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * MIXTURE OF EXPERTS
+ *
+ * The whole feed-forward layer of E experts for M rows (1 .. W4G128_MAX_M),
+ * each expert's three projections in the packed int4-g128 format:
+ *   logit[m][e] = sum_d x[m][d] router[e][d]                        (fp32)
+ *   S(m)        = the top_k experts of the largest logits, the lower one
+ *                 first among equals (a NaN logit ranks last)
+ *   p[m][e]     = exp(logit[m][e]) / sum exp(logit[m][e']), the sum over S(m)
+ *                 (renormalize = 1) or over all experts (renormalize = 0)
+ *   a[m][e][f]  = bf16( silu(g_f) u_f ), (g, u) = x[m] . dequant(gate_up_e)
+ *   y[m][n]     = bf16( residual[m][n] + sum_{e in S(m)} p[m][e] (a[m][e] . dequant(down_e))[n] )
+ * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)); the
+ * activations a are rounded to bf16 because they are the operand of the second
+ * product.  Only the experts that some row picks are read, each once.
+ *
+ * gate_up_e is a K = D, N = 2 F matrix (F gate columns, then F up columns),
+ * down_e a K = F, N = D one, each packed as w4g128_pack writes it; the E
+ * matrices follow one another without gaps, expert e at e *
+ * w4g128_packed_bytes(K, N).  Row m of y depends on row m of x and residual
+ * alone and is bitwise the same whatever M and the other rows are. */
+typedef struct {
+  const w4g128_bf16* x;        /* [M][D] */
+  const w4g128_bf16* residual; /* [M][D], or NULL: 0.  May be y */
+  w4g128_bf16* y;              /* [M][D]; not x */
+  const w4g128_bf16* router;   /* [E][D] */
+  const void* gate_up;         /* E packed matrices, K = D, N = 2 F */
+  const void* down;            /* E packed matrices, K = F, N = D */
+  int M;
+  int D;           /* a multiple of 128, 128 .. 65536 */
+  int F;           /* a multiple of 128, 128 .. 65536 */
+  int E;           /* 1 .. W4G128_MAX_EXPERTS */
+  int top_k;       /* 1 .. min(E, W4G128_MAX_TOP_K) */
+  int renormalize; /* 0 or 1 */
+} w4g128_moe_args;
+
+#define W4G128_MAX_EXPERTS 512
+#define W4G128_MAX_TOP_K 16
+
+/* Workspace bytes of w4g128_moe for these sizes (status word, logits, the
+ * experts' activations and outputs).  0 for arguments it would refuse. */
+W4G128_API size_t w4g128_moe_workspace_bytes(const w4g128_moe_args* args);
+
+/* The layer above.  All pointers and ws 16-byte aligned.  Returns
+ * W4G128_ERR_INVALID_ARG (null pointers, M, top_k or renormalize out of
+ * range, y = x), W4G128_ERR_SHAPE, W4G128_ERR_ALIGN, W4G128_ERR_WORKSPACE.
+ * The device-side waits are bounded as in w4g128.h: a wait that gives up
+ * leaves W4G128_ERR_TIMEOUT in the status word. */
+W4G128_API int w4g128_moe(const w4g128_moe_args* args, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,7 @@ __all__ = [
     "w4g128_schedule", "DecodeStep",
     "w4g128_sample", "SampleArgs", "SampleStep", "MAX_SAMPLE_ROWS", "MAX_VOCAB",
     "w4g128_attend", "w4g128_attend_workspace_bytes", "AttendArgs", "AttendStep", "MAX_SEQUENCES", "ERR_CACHE",
+    "w4g128_moe", "w4g128_moe_workspace_bytes", "MoEArgs", "MoEStep", "MAX_EXPERTS", "MAX_TOP_K",
     "MAX_M", "MAX_MATRICES", "SELFTEST_WS_BYTES", "SCHEDULE_FIELDS",
 ]
 
@@ -33,6 +34,8 @@ MAX_SAMPLE_ROWS = 4096  # W4G128_MAX_SAMPLE_ROWS
 MAX_VOCAB = 524160      # W4G128_MAX_VOCAB
 MAX_SEQUENCES = 1024    # W4G128_MAX_SEQUENCES
 ERR_CACHE = 9           # W4G128_ERR_CACHE
+MAX_EXPERTS = 512       # W4G128_MAX_EXPERTS
+MAX_TOP_K = 16          # W4G128_MAX_TOP_K
 
 _lib = None
 
@@ -144,6 +147,10 @@ def _declare(L):
     L.w4g128_attend_workspace_bytes.argtypes = [ctypes.POINTER(AttendArgs)]
     L.w4g128_attend.restype = i
     L.w4g128_attend.argtypes = [ctypes.POINTER(AttendArgs), p, sz, p]
+    L.w4g128_moe_workspace_bytes.restype = sz
+    L.w4g128_moe_workspace_bytes.argtypes = [ctypes.POINTER(MoEArgs)]
+    L.w4g128_moe.restype = i
+    L.w4g128_moe.argtypes = [ctypes.POINTER(MoEArgs), p, sz, p]
     return L
 
 
@@ -463,3 +470,36 @@ class AttendStep(_Step):
     """w4g128_attend with its arguments marshalled once: AttendStep(args, ws).run()."""
 
     _entry = "w4g128_attend"
+
+
+class MoEArgs(_Args):
+    """w4g128_moe_args: bf16 x, residual (or None), y [M][D] and router [E][D];
+    gate_up and down: E packed matrices one after another."""
+
+    _fn = "w4g128_moe"
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "residual", "y", "router", "gate_up", "down")] + \
+               [(n, ctypes.c_int) for n in ("M", "D", "F", "E", "top_k", "renormalize")]
+    _itemsize = {"x": 2, "residual": 2, "y": 2, "router": 2, "gate_up": 0, "down": 0}
+
+    def _reach(self, name):
+        if name == "gate_up":
+            return self.E * self.D * self.F * 17 // 16
+        if name == "down":
+            return self.E * self.D * self.F * 17 // 32
+        return self.D * (self.E if name == "router" else self.M)
+
+
+def w4g128_moe_workspace_bytes(args):
+    return int(lib().w4g128_moe_workspace_bytes(ctypes.byref(args)))
+
+
+def w4g128_moe(args, ws, ws_bytes=None, stream=None):
+    """The mixture-of-experts layer (see include/w4g128_ops.h); args: MoEArgs."""
+    wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check("w4g128_moe", lib().w4g128_moe(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
+
+
+class MoEStep(_Step):
+    """w4g128_moe with its arguments marshalled once: MoEStep(args, ws).run()."""
+
+    _entry = "w4g128_moe"

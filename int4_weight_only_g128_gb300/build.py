@@ -20,7 +20,7 @@ LIB_DEBUG = os.path.join(BUILD, "libw4g128_debug.so")
 
 SOURCES = ["w4g128_api.cu", "w4g128_pack.cu", "w4g128_stream.cu", "w4g128_probe.cu", "w4g128_noalloc.cu",
            "w4g128_quant.cu", "w4g128_selftest.cu", "w4g128_hostio.cu",
-           "w4g128_sample.cu", "w4g128_attend.cu"]
+           "w4g128_sample.cu", "w4g128_attend.cu", "w4g128_moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]

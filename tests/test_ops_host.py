@@ -33,13 +33,14 @@ def test_every_operator_is_exported(L):
 
 def test_constants_match_the_header():
     text = header()
-    for name in ("MAX_SAMPLE_ROWS", "MAX_VOCAB", "MAX_SEQUENCES", "ERR_CACHE"):
+    for name in ("MAX_SAMPLE_ROWS", "MAX_VOCAB", "MAX_SEQUENCES", "ERR_CACHE", "MAX_EXPERTS", "MAX_TOP_K"):
         assert re.search(rf"#define W4G128_{name} {getattr(w, name)}\b", text), name
 
 
 def test_structs_match_the_header():
     """Field names and order of each argument struct."""
-    for cls, name in ((w.SampleArgs, "w4g128_sample_args"), (w.AttendArgs, "w4g128_attend_args")):
+    for cls, name in ((w.SampleArgs, "w4g128_sample_args"), (w.AttendArgs, "w4g128_attend_args"),
+                      (w.MoEArgs, "w4g128_moe_args")):
         body = re.search(r"typedef struct \{([^}]*)\} " + name + ";", header()).group(1)
         body = re.sub(r"/\*.*?\*/", "", body, flags=re.S)
         fields = [f.split()[-1].lstrip("*") for line in body.split(";") if line.strip()
@@ -115,6 +116,58 @@ def test_attend_refusals(L):
     assert w.w4g128_attend_workspace_bytes(big) > 1 << 40
 
 
+def moe_args(**kw):
+    a = dict(x=FAKE, residual=None, y=FAKE + 0x1000, router=FAKE, gate_up=FAKE, down=FAKE, M=2, D=256, F=128, E=4,
+             top_k=2, renormalize=1)
+    a.update(kw)
+    return w.MoEArgs(**a)
+
+
+def moe(ws=FAKE, ws_bytes=1 << 40, **kw):
+    return w.lib().w4g128_moe(ctypes.byref(moe_args(**kw)), ws, ws_bytes, None)
+
+
+def test_moe_refusals(L):
+    assert L.w4g128_moe(None, FAKE, 1 << 40, None) == E_INVALID
+    for f in ("x", "y", "router", "gate_up", "down"):
+        assert moe(**{f: None}) == E_INVALID, f
+    assert moe(ws=None) == E_INVALID
+    for kw in (dict(M=0), dict(M=17), dict(top_k=0), dict(top_k=5), dict(top_k=17, E=32), dict(renormalize=2),
+               dict(renormalize=-1), dict(y=FAKE)):
+        assert moe(**kw) == E_INVALID, kw
+    for kw in (dict(D=0), dict(D=192), dict(D=65536 + 128), dict(F=64), dict(F=200), dict(F=65536 + 128), dict(E=0),
+               dict(E=w.MAX_EXPERTS + 1)):
+        assert moe(**kw) == E_SHAPE, kw
+    for f in ("x", "residual", "y", "router", "gate_up", "down"):
+        assert moe(**{f: FAKE + 0x2008}) == E_ALIGN, f
+    assert moe(ws=FAKE + 8) == E_ALIGN
+    need = w.w4g128_moe_workspace_bytes(moe_args())
+    assert need > 0 and moe(ws_bytes=need - 1) == E_WS
+    assert w.w4g128_moe_workspace_bytes(moe_args(M=0)) == 0
+    assert w.w4g128_moe_workspace_bytes(moe_args(M=16, D=65536, F=65536, E=512, top_k=16)) > 256 * 65536 * 6
+
+
+_FAULT_CHILD = """
+import ctypes, sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import test_ops_host as t
+print(t.sample(), t.attend(), t.moe(), t.moe(M=0))
+"""
+
+
+@pytest.mark.parametrize("mode,status", [("launch", E_CUDA), ("workspace", E_WS)])
+def test_host_fault_hook(mode, status):
+    """W4G128_FAULT reaches the operators too, after their argument checks."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", _FAULT_CHILD.format(root=root)], capture_output=True, text=True,
+                         env=dict(os.environ, W4G128_FAULT=mode), timeout=120)
+    assert out.returncode == 0, out.stderr
+    assert [int(v) for v in out.stdout.split()] == [status] * 3 + [E_INVALID]
+
+
 def test_tensors_are_checked_by_the_binding():
     torch = pytest.importorskip("torch")
     logits = torch.zeros(100, dtype=torch.bfloat16)
@@ -130,3 +183,4 @@ def test_no_device_is_reported():
         pytest.skip("a GPU is present")
     assert sample() == E_DEVICE
     assert attend() == E_DEVICE
+    assert moe() == E_DEVICE
