@@ -187,8 +187,8 @@ W4G128_API size_t w4g128_moe_workspace_bytes(const w4g128_moe_args* args);
 /* The layer above.  All pointers and ws 16-byte aligned.  Returns
  * W4G128_ERR_INVALID_ARG (null pointers, M, top_k or renormalize out of
  * range, y = x), W4G128_ERR_SHAPE, W4G128_ERR_ALIGN, W4G128_ERR_WORKSPACE.
- * The device-side waits are bounded as in w4g128.h: a wait that gives up
- * leaves W4G128_ERR_TIMEOUT in the status word. */
+ * The kernels wait for one another by launch order alone; the status word
+ * reads W4G128_OK after the call. */
 W4G128_API int w4g128_moe(const w4g128_moe_args* args, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -9,24 +9,34 @@
 // known on the device only, so every CTA of an expert kernel derives the lists
 // itself from the M x E logits (top-k per row, one warp each).
 //
-// A unit is (picked expert, 16 output columns), its depth K = 128 G rows cut
-// into G groups.  A CTA takes a contiguous range of units and its 8 warps take
-// the range's (unit, group) items in turn, each through its own ring of bulk
-// copies (one 1088-byte block, or a gate and an up block, per stage).  The
-// item's product is one warp MMA per packed word: the 16 columns are the A
-// operand (bf16 128 + q, exact: one shift and one LOP3 per operand register),
-// the rows that picked the expert are the B columns.  The bias of 128 and the
-// group minimum need X = sum_k x, which an MMA with an all-ones A gives in the
-// very registers that need it:
-//   sum_k x w = scale sum_k x (128 + q) + (min - 128 scale) X.
-// Group g of a unit is summed by whichever warp holds it into partial g mod 8
-// in rising order, and the 8 partials are added in order: bits do not depend
-// on the grid, nor on which other rows share the expert.
+// A unit is (picked expert, one or two tiles of 16 output columns), its depth
+// K = 128 G rows cut into G groups.  A CTA takes a contiguous range of units
+// and its 8 warps take the range's (unit, group) items in turn, each through
+// its own ring of bulk copies (two 1088-byte blocks per stage: a gate and an
+// up block, or two neighbours of the down projection).  The item's product is
+// one warp MMA per packed word: the 16 columns are the A operand, the rows
+// that picked the expert the B columns.
+//   gate and up: x as fp16, each (row, group) scaled by a power of two (exact
+//     within 2^29 of the group's largest value), weights as fp16 1024 + q and
+//     1024 + 16 q, both from one word with one shift and four LOP3;
+//   down: activations as bf16 (their range is not known when they are
+//     rounded), weights as bf16 128 + q, with two more shifts a word.
+// The bias and the group minimum are undone by X = sum_k x per (row, group):
+//   sum_k x w = scale sum_k x (bias + q) + (min - bias scale) X;
+// the route kernel leaves X of x, and the activations come with the sums of
+// their 16-column tiles (an all-ones A would give X for free of addresses, but
+// costs a third of the tensor work, which measured 41% busy: dropped).
+// The groups g of a unit fall into 8 parts by g mod 8, summed in rising order,
+// and the parts are added as ((0 + 4) + (2 + 6)) + ((1 + 5) + (3 + 7)), whether
+// 8 warps hold one part each or 2 warps four each: bits do not depend on the
+// grid, nor on which other rows share the expert.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "w4g128_ops.h"
 #include "w4g128_internal.h"
@@ -41,8 +51,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kParts = 8;             // partial sums of a unit
 constexpr size_t kStatusBytes = 256;
-constexpr uint32_t kBias = 0x43004300u;  // bf16 128.0 twice
-constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
+constexpr uint32_t kBias16 = 0x64006400u;   // fp16 1024.0 twice
+constexpr uint32_t kBiasB16 = 0x43004300u;  // bf16 128.0 twice
 
 struct Params {
   const uint16_t *x, *residual, *router;
@@ -52,8 +62,10 @@ struct Params {
   unsigned* status;
   float* logits;   // [M][E]
   float* weights;  // [M][top_k], picks in rising expert order
-  uint8_t* xp;     // [M][D / 128][256]: x in operand order
-  uint8_t* act;    // [M top_k][F / 128][256]: activations in operand order
+  uint8_t* xp;     // [M][D / 128][256]: x as scaled fp16 in operand order
+  float2* xs;      // [M][D / 128]: X, and the factor that undoes the scale
+  uint8_t* act;    // [M top_k][F / 128][256]: activations (bf16) in operand order
+  float* acts;     // [M top_k][F / 16]: sums of 16 activations
   float* part;     // [M top_k][D]
 };
 
@@ -111,12 +123,45 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
     p.logits[tid * p.E + e] = t;
   }
 
+  // x in operand order: 16 lanes per (row, group); rows follow one another in
+  // whole groups.  The scale puts the group's largest magnitude in [2^14, 2^15).
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(p.x);
-  const int units = p.M * n;  // 16 bytes each
-  for (int u = e * kThreads + tid; u < units; u += p.E * kThreads) {
-    const int group = u / 16, i = u / 4 % 4, c = u % 4;  // (rows follow one another in whole groups)
-    const uint32_t* src = xw + group * 64 + 16 * i + c;
-    reinterpret_cast<uint4*>(p.xp)[u] = make_uint4(__ldg(src), __ldg(src + 4), __ldg(src + 8), __ldg(src + 12));
+  const int units = p.M * n;  // 16 bytes each, a multiple of 16
+  for (int u0 = (e * kWarps + warp) * 32; u0 < units; u0 += p.E * kThreads) {
+    const int u = u0 + lane;
+    const bool real = u < units;  // (all 16 lanes of a group or none)
+    const int group = u / 16, i = u / 4 % 4, c = u % 4;
+    uint32_t v[4] = {};
+    if (real) {
+      const uint32_t* src = xw + static_cast<long long>(group) * 64 + 16 * i + c;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = __ldg(src + 4 * j);
+    }
+    float top = 0.f, X = 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      top = fmaxf(top, fmaxf(fabsf(low_f(v[j])), fabsf(high_f(v[j]))));
+      X += low_f(v[j]) + high_f(v[j]);
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) {
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+      X += __shfl_xor_sync(~0u, X, d);
+    }
+    // 2^s with s = 14 - exponent(top), kept where 2^s and 2^-s are normal
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    const int s = min(max(14 - ex, -113), 126);
+    const float up = __int_as_float((127 + s) << 23);
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 q = __floats2half2_rn(low_f(v[j]) * up, high_f(v[j]) * up);
+      h[j] = *reinterpret_cast<const uint32_t*>(&q);
+    }
+    if (real) {
+      reinterpret_cast<uint4*>(p.xp)[u] = make_uint4(h[0], h[1], h[2], h[3]);
+      if (lane % 16 == 0) p.xs[group] = make_float2(X, __int_as_float((127 - s) << 23));
+    }
   }
 }
 
@@ -154,6 +199,7 @@ __device__ void make_lists(const Params& p, Lists& s) {
     for (int i = 0; i < kPer; ++i) {
       const int e = i * 32 + lane;
       rank[i] = 0u;
+      if (i * 32 >= p.E) continue;  // (for every lane)
       if (e < p.E) {
         v[i] = __ldcg(p.logits + m * p.E + e);
         rank[i] = rank_of(v[i]);
@@ -167,6 +213,7 @@ __device__ void make_lists(const Params& p, Lists& s) {
       float val = 0.f;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= p.E) break;
         if (rank[i] > best) {
           best = rank[i];
           at = i * 32 + lane;
@@ -177,8 +224,10 @@ __device__ void make_lists(const Params& p, Lists& s) {
       const int e = static_cast<int>(__reduce_min_sync(~0u, best == win ? static_cast<unsigned>(at) : ~0u));
       val = __shfl_sync(~0u, val, e & 31);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
+      for (int i = 0; i < kPer; ++i) {
+        if (i * 32 >= p.E) break;
         if (i * 32 + lane == e) rank[i] = 0u;
+      }
       if (j == 0) {
         top = val;
         if (!p.renormalize) {
@@ -242,35 +291,69 @@ __device__ void make_lists(const Params& p, Lists& s) {
 }
 
 // ---------------------------------------------------------------- expert streams
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <bool BF16>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// PHASE 0: gate and up (two tiles per unit); 1: down.  NT: 8-row B tiles.
-template <int PHASE, int NT>
+// The A fragment of one packed word.  fp16: columns r as 1024 + q, columns
+// r + 8 as 1024 + 16 q.  bf16: 128 + q.
+template <bool BF16>
+__device__ __forceinline__ void operand(uint32_t w, uint32_t (&a)[4]) {
+  if constexpr (BF16) {
+    a[0] = lop3_and_or(w, 0x000F000Fu, kBiasB16);
+    a[1] = lop3_and_or(w >> 4, 0x000F000Fu, kBiasB16);
+    a[2] = lop3_and_or(w >> 8, 0x000F000Fu, kBiasB16);
+    a[3] = lop3_and_or(w >> 12, 0x000F000Fu, kBiasB16);
+  } else {
+    const uint32_t v = w >> 8;
+    a[0] = lop3_and_or(w, 0x000F000Fu, kBias16);
+    a[1] = lop3_and_or(w, 0x00F000F0u, kBias16);
+    a[2] = lop3_and_or(v, 0x000F000Fu, kBias16);
+    a[3] = lop3_and_or(v, 0x00F000F0u, kBias16);
+  }
+}
+
+constexpr int kTiles = 2;  // of 16 columns, per item
+constexpr int kStage = kTiles * kBlockBytes;
+constexpr int kCols = kTiles * kTileN;
+template <int NT>  // 8-row B tiles
 struct Stream {
-  static constexpr int kTiles = PHASE == 0 ? 2 : 1;
-  static constexpr int kStage = kTiles * kBlockBytes;
-  static constexpr int kStages = PHASE == 0 ? 4 : 8;
+  static constexpr int kStages = NT == 1 ? 5 : 4;
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kCols = kTiles * kTileN;
-  static constexpr int kPartFloats = kParts * NT * 8 * kCols;  // one unit's partials, [part][row][column]
-  static constexpr int kBytes = kRing + 2 * kPartFloats * 4 + kWarps * kStages * 8;
+  static constexpr int kPart = NT * 8 * kCols;  // floats that a warp leaves of a unit: [row][column]
+  static constexpr int kBytes = kRing + 2 * kWarps * kPart * 4;
 };
 
-template <int PHASE, int NT>
+// A picked expert's rows, from one lane's point of view: its B row (r of each
+// 8-row tile) in operand order, and where the sums of rows 2c, 2c + 1 are.
+// Columns beyond the count repeat the last row; nothing of theirs is kept.
+template <int NT>
+struct Rows {
+  const uint8_t* x[NT];
+  const float* sums[NT][2];
+};
+
+// PHASE 0: gate and up, a unit is a gate tile and its up tile; 1: down, a unit
+// is two neighbouring tiles.  TEAM: warps that share a unit.
+template <int PHASE, int NT, int TEAM>
 __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_constant__ Params p) {
-  using S = Stream<PHASE, NT>;
+  using S = Stream<NT>;
+  constexpr bool kBf16 = PHASE == 1;
+  constexpr int kTeams = kWarps / TEAM;
+  constexpr int kMine = kParts / TEAM;  // parts of a unit that one warp sums
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Lists lists;
-  float* parts = reinterpret_cast<float*>(smem + S::kRing);
-  const uint32_t bars = smem_addr(smem + S::kRing + 2 * S::kPartFloats * 4);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid < kWarps * S::kStages) mbar_init(bars + 8 * tid, 1);
-  fence_mbar_init();
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);  // (uniform, and known to be)
+  const int team = warp / TEAM, member = warp % TEAM;
 
   // The logits: of the preceding kernel (phase 0), or of the one before, which
   // had completed when the preceding one let this one launch (phase 1).
@@ -282,58 +365,82 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   if (PHASE == 0 && blockIdx.x == 0)
     for (int i = tid; i < p.M * p.top_k; i += kThreads) p.weights[i] = lists.weight[i];
 
-  const int K = PHASE == 0 ? p.D : p.F, N = PHASE == 0 ? 2 * p.F : p.D;
+  const int K = PHASE == 0 ? p.D : p.F;
   const int G = K / kGroup;
-  const int tiles = PHASE == 0 ? p.F / kTileN : p.D / kTileN;  // units of an expert
-  const long long units = static_cast<long long>(lists.experts) * tiles;
-  const long long u0 = units * blockIdx.x / gridDim.x;
-  const int nu = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x - u0);
+  const int per = PHASE == 0 ? p.F / kTileN : p.D / kCols;  // units of an expert
+  const int units = lists.experts * per;
+  const int share = blockIdx.x * kTeams + team, shares = gridDim.x * kTeams;
+  const int u0 = static_cast<int>(static_cast<long long>(units) * share / shares);
+  const int nu = static_cast<int>(static_cast<long long>(units) * (share + 1) / shares) - u0;
   const uint8_t* weights = PHASE == 0 ? p.gate_up : p.down;
-  const long long expert_bytes = static_cast<long long>(N / kTileN) * G * kBlockBytes;
-  const uint64_t policy = l2_policy_evict_first();
-  const uint32_t ring = smem_addr(smem) + warp * S::kStages * S::kStage;
-  const uint8_t* ring_ptr = smem + warp * S::kStages * S::kStage;
-  const uint32_t bar = bars + 8 * warp * S::kStages;
-  bool good = true;
+  const long long quad_bytes = static_cast<long long>(G) * kQuadBytes;
+  const long long expert_bytes = (PHASE == 0 ? p.F / 32 : p.D / 64) * quad_bytes;
+  const uint32_t ring = smem_addr(smem) + warp * S::kStages * kStage;
+  const uint8_t* ring_ptr = smem + warp * S::kStages * kStage;
 
-  // This warp's items are numbers warp, warp + 8, .. of the CTA's (unit, group) list.
-  struct Cursor {
-    int unit, group;
-  };
-  auto advance = [&](Cursor& c) {
-    c.group += kWarps;
-    while (c.group >= G) {
-      c.group -= G;
-      ++c.unit;
-    }
-  };
-  auto issue = [&](const Cursor& c, int stage) {  // one lane
-    const long long u = u0 + c.unit;
-    const int a = static_cast<int>(u / tiles), t = static_cast<int>(u % tiles);
-    const uint8_t* base = weights + lists.expert[a] * expert_bytes + static_cast<long long>(c.group) * kQuadBytes;
-    const long long quad = static_cast<long long>(G) * kQuadBytes;
-    mbar_arrive_expect_tx(bar + 8 * stage, S::kStage);
-    const uint32_t dst = ring + stage * S::kStage;
-    bulk_g2s(dst, base + (t / kQuadTiles) * quad + (t % kQuadTiles) * kBlockBytes, kBlockBytes, bar + 8 * stage, policy);
+  // A warp's items: in each unit of its team the groups of its parts, part by
+  // part in the order in which they are added.  The members take turns from
+  // unit to unit, so that they stay even where the groups do not divide.
+  auto turn = [&](int u) { return static_cast<int>(static_cast<unsigned>(member - u * G) % TEAM); };
+  auto part_at = [](int m, int i) { return m + 4 * (i & 1) + 2 * (i >> 1); };
+
+  // The copies run kStages items ahead.
+  int c_unit = 0, c_turn = turn(0), c_i = 0, c_group = c_turn;
+  int c_expert = u0 / per, c_at = u0 % per;
+  const uint8_t *c_src = nullptr, *c_src2 = nullptr;
+  auto place = [&] {  // this lane's 16 bytes in group 0 of the unit's tiles
+    const uint8_t* base = weights + lists.expert[c_expert] * expert_bytes + 16 * lane;
     if (PHASE == 0) {
-      const int t2 = t + tiles;
-      bulk_g2s(dst + kBlockBytes, base + (t2 / kQuadTiles) * quad + (t2 % kQuadTiles) * kBlockBytes, kBlockBytes,
-               bar + 8 * stage, policy);
+      const int t2 = c_at + per;
+      c_src = base + (c_at / kQuadTiles) * quad_bytes + (c_at % kQuadTiles) * kBlockBytes;
+      c_src2 = base + (t2 / kQuadTiles) * quad_bytes + (t2 % kQuadTiles) * kBlockBytes;
+    } else {
+      c_src = base + (c_at / 2) * quad_bytes + (c_at % 2) * kStage;
     }
   };
-  Cursor head{0, warp};  // next to issue
-  while (head.group >= G) {
-    head.group -= G;
-    ++head.unit;
-  }
-  Cursor cur = head;
-  if (lane == 0) {
-#pragma unroll 1
-    for (int i = 0; i < S::kStages; ++i) {
-      if (head.unit < nu) issue(head, i);
-      advance(head);
+  auto settle = [&] {  // to the warp's next item, once c_group is past the depth
+    while (c_group >= G && c_unit < nu) {
+      if (++c_i == kMine) {
+        c_i = 0;
+        if (++c_unit == nu) return;
+        if (++c_at == per) {
+          c_at = 0;
+          ++c_expert;
+        }
+        c_turn = turn(c_unit);
+        place();
+      }
+      c_group = part_at(c_turn, c_i);
     }
+  };
+  auto copy = [&](int stage) {
+    if (c_unit < nu) {
+      const uint32_t dst = ring + stage * kStage + 16 * lane;
+      const int off = c_group * kQuadBytes;
+      if (PHASE == 0) {
+        cp_async16(dst, c_src + off);
+        cp_async16(dst + 512, c_src + off + 512);
+        cp_async16(dst + kBlockBytes, c_src2 + off);
+        cp_async16(dst + kBlockBytes + 512, c_src2 + off + 512);
+        // the 64 bytes of scales and minima behind each: 4 + 4 lanes
+        if (lane < 4) cp_async16(dst + 1024, c_src + off + 1024);
+        else if (lane < 8) cp_async16(dst + kBlockBytes + 1024 - 64, c_src2 + off + 1024 - 64);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cp_async16(dst + 512 * i, c_src + off + 512 * i);
+        if (lane < (kStage - 2048) / 16) cp_async16(dst + 2048, c_src + off + 2048);
+      }
+      c_group += kParts;
+      settle();
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  if (nu > 0) {
+    place();
+    settle();
   }
+#pragma unroll 1
+  for (int i = 0; i < S::kStages; ++i) copy(i);
   if (PHASE == 1) {
     grid_dependency_wait();  // the weights are on their way while the activations are finished
     grid_dependents_launch();
@@ -341,134 +448,172 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 
   const int r = lane >> 2, c = lane & 3;
   int stage = 0;
-  uint32_t parity = 0;
+  int at = u0 % per, a = u0 / per;
+  int first = 0, count = 0;
+  Rows<NT> rows = {};
+  float* parts = reinterpret_cast<float*>(smem + S::kRing) + team * 2 * TEAM * S::kPart;  // two halves that take turns
+
+  // One item: d += .., for NA of the B tiles.
+  auto item = [&](auto na, int group, float (&acc)[kTiles][NT][4]) {
+    constexpr int NA = decltype(na)::value;
+    uint4 xv[NA][4];
+    float2 xs[NA][2];  // X, and (phase 0) the factor of the products
+#pragma unroll
+    for (int n = 0; n < NA; ++n) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xv[n][i] = *reinterpret_cast<const uint4*>(rows.x[n] + group * 256 + i * 64);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (PHASE == 0) {
+          xs[n][k] = reinterpret_cast<const float2*>(rows.sums[n][k])[group];
+        } else {
+          const float4 v = reinterpret_cast<const float4*>(rows.sums[n][k])[group * 2];
+          const float4 w = reinterpret_cast<const float4*>(rows.sums[n][k])[group * 2 + 1];
+          xs[n][k].x = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
+        }
+      }
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
+    __syncwarp();
+    const uint8_t* st = ring_ptr + stage * kStage;
+    float d[kTiles][NA][4] = {};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 q[kTiles];
+#pragma unroll
+      for (int t = 0; t < kTiles; ++t) q[t] = *reinterpret_cast<const uint4*>(st + t * kBlockBytes + 512 * h + 16 * lane);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = 4 * h + j;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          uint32_t w[4];
+          operand<kBf16>(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, w);
+#pragma unroll
+          for (int n = 0; n < NA; ++n)
+            mma<kBf16>(d[t][n], w, s % 2 ? xv[n][s / 2].z : xv[n][s / 2].x, s % 2 ? xv[n][s / 2].w : xv[n][s / 2].y);
+        }
+      }
+    }
+    uint2 meta[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) meta[t] = *reinterpret_cast<const uint2*>(st + t * kBlockBytes + kCodeBytes + 8 * r);
+    __syncwarp();  // the stage is read out
+    copy(stage);
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      float s0 = low_f(meta[t].x), s1 = low_f(meta[t].y);
+      const float b0 = fmaf(kBf16 ? -128.f : -1024.f, s0, high_f(meta[t].x));
+      const float b1 = fmaf(kBf16 ? -128.f : -64.f, s1, high_f(meta[t].y));
+      if (!kBf16) s1 *= 0.0625f;  // these columns carry 16 q
+#pragma unroll
+      for (int n = 0; n < NA; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float f0 = kBf16 ? s0 : s0 * xs[n][k].y, f1 = kBf16 ? s1 : s1 * xs[n][k].y;
+          acc[t][n][k] = fmaf(f0, d[t][n][k], fmaf(b0, xs[n][k].x, acc[t][n][k]));
+          acc[t][n][2 + k] = fmaf(f1, d[t][n][2 + k], fmaf(b1, xs[n][k].x, acc[t][n][2 + k]));
+        }
+    }
+  };
+  using One = std::integral_constant<int, 1>;
+  using Two = std::integral_constant<int, 2>;
+
+  int expert_seen = -1;
   for (int u = 0; u < nu; ++u) {
-    const int a = static_cast<int>((u0 + u) / tiles);
-    const int first = lists.first[a], count = lists.first[a + 1] - first;
-    float* part = parts + (u & 1) * S::kPartFloats;
-    if (cur.unit == u) {
-      const uint8_t* row[NT];  // this lane's B row (r of each 8-row tile) in operand order
+    if (a != expert_seen) {
+      expert_seen = a;
+      first = lists.first[a];
+      count = lists.first[a + 1] - first;
+      auto source = [&](int i) {
+        const int pick = lists.pick[first + min(i, count - 1)];
+        return static_cast<long long>(PHASE == 0 ? pick / p.top_k : pick);
+      };
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int i = n * 8 + r;
-        const int pick = i < count ? lists.pick[first + i] : 0;
-        row[n] = i < count ? (PHASE == 0 ? p.xp + static_cast<long long>(pick / p.top_k) * p.D * 2
-                                         : p.act + static_cast<long long>(pick) * p.F * 2) + 16 * c
-                           : nullptr;
+        rows.x[n] = (PHASE == 0 ? p.xp : p.act) + source(n * 8 + r) * K * 2 + 16 * c;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const long long m = source(n * 8 + 2 * c + k);
+          rows.sums[n][k] = PHASE == 0 ? reinterpret_cast<const float*>(p.xs) + m * (G * 2) : p.acts + m * (G * 8);
+        }
       }
-      const bool two = NT == 2 && count > 8;
-      float acc[S::kTiles][NT][4];
-#pragma unroll
-      for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[t][n][0] = acc[t][n][1] = acc[t][n][2] = acc[t][n][3] = 0.f;
-      const int slot = cur.group % kParts;
-      while (cur.unit == u) {
-        uint4 xv[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            xv[n][i] = row[n] ? *reinterpret_cast<const uint4*>(row[n] + cur.group * 256 + i * 64) : make_uint4(0, 0, 0, 0);
-        // (after a wait has given up, the copies still in flight get a short one each)
-        good = mbar_wait_bounded(bar + 8 * stage, parity, good ? kDefaultWaitNs : 1000000ull) && good;
-        const uint8_t* st = ring_ptr + stage * S::kStage;
-        float d[S::kTiles][NT][4] = {}, X[NT][4] = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint4 q[S::kTiles];
-#pragma unroll
-          for (int t = 0; t < S::kTiles; ++t)
-            q[t] = *reinterpret_cast<const uint4*>(st + t * kBlockBytes + 512 * h + 16 * lane);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int s = 4 * h + j;
-            uint32_t b[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-              const uint4 v = xv[n][s / 2];
-              b[n][0] = s % 2 ? v.z : v.x;
-              b[n][1] = s % 2 ? v.w : v.y;
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n == 0 || two) mma(X[n], kOnes, kOnes, kOnes, kOnes, b[n][0], b[n][1]);
-#pragma unroll
-            for (int t = 0; t < S::kTiles; ++t) {
-              const uint32_t w = j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w;
-              const uint32_t a0 = lop3_and_or(w, 0x000F000Fu, kBias), a1 = lop3_and_or(w >> 4, 0x000F000Fu, kBias);
-              const uint32_t a2 = lop3_and_or(w >> 8, 0x000F000Fu, kBias), a3 = lop3_and_or(w >> 12, 0x000F000Fu, kBias);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                if (n == 0 || two) mma(d[t][n], a0, a1, a2, a3, b[n][0], b[n][1]);
-            }
-          }
-        }
-        uint2 meta[S::kTiles];
-#pragma unroll
-        for (int t = 0; t < S::kTiles; ++t)
-          meta[t] = *reinterpret_cast<const uint2*>(st + t * kBlockBytes + kCodeBytes + 8 * r);
-        __syncwarp();  // the stage is read out
-        if (lane == 0 && head.unit < nu) {
-          fence_proxy_async_smem();
-          issue(head, stage);
-        }
-        if (lane == 0) advance(head);
-        if (++stage == S::kStages) {
-          stage = 0;
-          parity ^= 1;
-        }
-#pragma unroll
-        for (int t = 0; t < S::kTiles; ++t) {
-          const float s0 = low_f(meta[t].x), s1 = low_f(meta[t].y);
-          const float b0 = fmaf(-128.f, s0, high_f(meta[t].x)), b1 = fmaf(-128.f, s1, high_f(meta[t].y));
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            acc[t][n][0] = fmaf(s0, d[t][n][0], fmaf(b0, X[n][0], acc[t][n][0]));
-            acc[t][n][1] = fmaf(s0, d[t][n][1], fmaf(b0, X[n][1], acc[t][n][1]));
-            acc[t][n][2] = fmaf(s1, d[t][n][2], fmaf(b1, X[n][0], acc[t][n][2]));
-            acc[t][n][3] = fmaf(s1, d[t][n][3], fmaf(b1, X[n][1], acc[t][n][3]));
-          }
-        }
-        advance(cur);
-      }
-#pragma unroll
-      for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int m = n * 8 + 2 * c + (i & 1);
-            if (m < count) part[(slot * NT * 8 + m) * S::kCols + t * kTileN + r + 8 * (i >> 1)] = acc[t][n][i];
-          }
     }
-    // One barrier per unit: the other half of the buffer is free again once
-    // every warp is past the next one.
-    __syncthreads();
-    const int o = (tid + 32 * (u & 7)) % kThreads;  // the folding warps take turns
-    if (o < count * kTileN) {
+    float* part = parts + (u & 1) * TEAM * S::kPart;
+    const int mine = turn(u);
+    float sum[kTiles][NT][4];
+#pragma unroll
+    for (int q = 0; q < (kMine + 1) / 2; ++q) {
+      float two[kTiles][NT][4];
+#pragma unroll
+      for (int h = 0; h < (kMine > 1 ? 2 : 1); ++h) {
+        float acc[kTiles][NT][4] = {};
+        const int v = part_at(mine, 2 * q + h);
+        if (NT == 2 && count > 8) {
+          if constexpr (NT == 2)
+            for (int g = v; g < G; g += kParts) item(Two{}, g, acc);
+        } else {
+          for (int g = v; g < G; g += kParts) item(One{}, g, acc);
+        }
+#pragma unroll
+        for (int i = 0; i < kTiles * NT * 4; ++i) (&two[0][0][0])[i] = h == 0 ? (&acc[0][0][0])[i] : (&two[0][0][0])[i] + (&acc[0][0][0])[i];
+      }
+#pragma unroll
+      for (int i = 0; i < kTiles * NT * 4; ++i) (&sum[0][0][0])[i] = q == 0 ? (&two[0][0][0])[i] : (&sum[0][0][0])[i] + (&two[0][0][0])[i];
+    }
+    float* out = part + mine * S::kPart;
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = n * 8 + 2 * c + (i & 1);
+          if (m < count) out[m * kCols + t * kTileN + r + 8 * (i >> 1)] = sum[t][n][i];
+        }
+    // One barrier of the team per unit: the other half of the buffer is free
+    // again once every member is past the next one.
+    if constexpr (TEAM == kWarps) __syncthreads();
+    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
+    const int tt = member * 32 + lane;
+    auto join = [&](const float* q) {  // (parts beyond the depth are 0)
+      if constexpr (TEAM == 2) return q[0] + q[S::kPart];
+      else
+        return ((q[0] + q[4 * S::kPart]) + (q[2 * S::kPart] + q[6 * S::kPart])) +
+               ((q[S::kPart] + q[5 * S::kPart]) + (q[3 * S::kPart] + q[7 * S::kPart]));
+    };
+    if (PHASE == 0) {
+      const int o = (tt + 32 * (u % TEAM)) % (TEAM * 32);  // the folding warps take turns
       const int m = o / kTileN, col = o % kTileN;
-      const int pick = lists.pick[first + m];
-      const int n = static_cast<int>((u0 + u) % tiles) * kTileN + col;
-      const int used = G < kParts ? G : kParts;
-      float v = 0.f, w = 0.f;
-      for (int k = 0; k < used; ++k) {
-        const float* q = part + (k * NT * 8 + m) * S::kCols + col;
-        v += q[0];
-        if (PHASE == 0) w += q[kTileN];
+      if (o / 32 * 2 < count) {  // whole warps
+        float act = 0.f;
+        if (m < count) {
+          const int pick = lists.pick[first + m];
+          const float v = join(part + m * kCols + col), w = join(part + m * kCols + col + kTileN);
+          const __nv_bfloat16 b = __float2bfloat16_rn(v / (1.f + expf(-v)) * w);
+          act = __bfloat162float(b);
+          // columns 16 at + col: k step at % 8 of the group
+          uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + at / 8 * 256 + at % 8 / 2 * 64 + col % 8 / 2 * 16 +
+                         (at % 2 * 2 + col / 8) * 4 + (col & 1) * 2;
+          *reinterpret_cast<__nv_bfloat16*>(dst) = b;
+        }
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) act += __shfl_xor_sync(~0u, act, k);
+        if (m < count && col == 0)
+          p.acts[static_cast<long long>(lists.pick[first + m]) * (p.F / kTileN) + at] = act;
       }
-      if (PHASE == 0) {
-        const float act = v / (1.f + expf(-v)) * w;
-        const int k = n % kGroup, s = k / 16, h = k % 16 / 8, cc = k % 8 / 2;
-        uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + n / kGroup * 256 + s / 2 * 64 + cc * 16 +
-                       (s % 2 * 2 + h) * 4 + (k & 1) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(act);
-      } else {
-        p.part[static_cast<long long>(pick) * p.D + n] = v;
+    } else {
+      for (int o = (tt + 32 * (u % TEAM)) % (TEAM * 32); o < count * kCols; o += TEAM * 32) {
+        const int m = o / kCols, col = o % kCols;
+        p.part[static_cast<long long>(lists.pick[first + m]) * p.D + at * kCols + col] = join(part + m * kCols + col);
       }
+    }
+    if (++at == per) {
+      at = 0;
+      ++a;
     }
   }
-  if (!good) atomicCAS(p.status, 0u, static_cast<unsigned>(W4G128_ERR_TIMEOUT));
 }
 
 // ---------------------------------------------------------------- combine
@@ -513,7 +658,7 @@ int check(const w4g128_moe_args* a) {
 }
 
 struct Layout {
-  size_t logits, weights, xp, act, part, total;
+  size_t logits, weights, xp, xs, act, acts, part, total;
 };
 Layout layout(const w4g128_moe_args& a) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
@@ -522,22 +667,34 @@ Layout layout(const w4g128_moe_args& a) {
   l.logits = kStatusBytes;
   l.weights = l.logits + up(M * a.E * 4);
   l.xp = l.weights + up(picks * 4);
-  l.act = l.xp + up(M * a.D * 2);
-  l.part = l.act + up(picks * a.F * 2);
+  l.xs = l.xp + up(M * a.D * 2);
+  l.act = l.xs + up(M * (a.D / 128) * 8);
+  l.acts = l.act + up(picks * a.F * 2);
+  l.part = l.acts + up(picks * (a.F / 16) * 4);
   l.total = l.part + up(picks * a.D * 4);
   return l;
 }
 
-template <int PHASE, int NT>
-cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
-  using S = Stream<PHASE, NT>;
-  const cudaError_t e = cudaFuncSetAttribute(expert_kernel<PHASE, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
+template <int PHASE, int NT, int TEAM>
+cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, long long units) {
+  constexpr int kBytes = Stream<NT>::kBytes;
+  const cudaError_t e =
+      cudaFuncSetAttribute(expert_kernel<PHASE, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
-  const long long units = static_cast<long long>(std::min(p.M * p.top_k, p.E)) * (PHASE == 0 ? p.F : p.D) / kTileN;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(2 * sms, units)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
-  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, NT>, p);
+  cfg.dynamicSmemBytes = kBytes;
+  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, NT, TEAM>, p);
+}
+
+template <int NT>
+cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
+  const long long most = std::min(p.M * p.top_k, p.E);  // picked experts
+  const cudaError_t e = launch_expert<0, NT, 8>(cfg, p, sms, most * (p.F / kTileN));
+  if (e != cudaSuccess) return e;
+  const long long units = most * (p.D / kCols);
+  // small teams where every team has several units
+  return units >= 16 * sms ? launch_expert<1, NT, 2>(cfg, p, sms, units) : launch_expert<1, NT, 8>(cfg, p, sms, units);
 }
 
 cudaError_t launch(const Params& p, cudaStream_t stream) {
@@ -558,9 +715,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   else if (p.M <= 4) e = cudaLaunchKernelEx(&cfg, route_kernel<4>, p);
   else e = cudaLaunchKernelEx(&cfg, route_kernel<16>, p);
   if (e != cudaSuccess) return e;
-  e = p.M <= 8 ? launch_expert<0, 1>(cfg, p, sms) : launch_expert<0, 2>(cfg, p, sms);
-  if (e != cudaSuccess) return e;
-  e = p.M <= 8 ? launch_expert<1, 1>(cfg, p, sms) : launch_expert<1, 2>(cfg, p, sms);
+  e = p.M <= 8 ? launch_experts<1>(cfg, p, sms) : launch_experts<2>(cfg, p, sms);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((p.D / 4 + 127) / 128, p.M);
   cfg.blockDim = dim3(128);
@@ -598,7 +753,9 @@ int w4g128_moe(const w4g128_moe_args* a, void* ws, size_t ws_bytes, void* stream
   p.logits = reinterpret_cast<float*>(base + l.logits);
   p.weights = reinterpret_cast<float*>(base + l.weights);
   p.xp = base + l.xp;
+  p.xs = reinterpret_cast<float2*>(base + l.xs);
   p.act = base + l.act;
+  p.acts = reinterpret_cast<float*>(base + l.acts);
   p.part = reinterpret_cast<float*>(base + l.part);
   if (launch(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();

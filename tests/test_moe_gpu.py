@@ -2,8 +2,9 @@
 bits, from the canonical codes, scales and minima.
 
 The bound.  One product sum_k x w of depth K = 128 G is built as scale d +
-(min - 128 scale) X per group, d = sum x (128 + q), X = sum x: with
-B = sum_k |x_k| (|min| + 271 scale), the 16 MMAs of a group err by at most
+(min - b scale) X per group, d = sum x (b + q), X = sum x, with a bias b of
+1024 (gate and up) or 128 (down): with B = sum_k |x_k| (|min| + (2 b + 15)
+scale), the 16 MMAs of a group err by at most
 2 * 24 roundings of that size (a tensor core may truncate: 2^-23 each), the
 sum over groups and parts by G + 8 more, so e(K) = (G + 56) 2^-23 B.  An
 activation a = silu(g) u moves by 1.1 |u| e_g + |silu(g)| e_u (|silu'| <= 1.1),
@@ -40,12 +41,12 @@ class Experts:
         for e in range(E):
             w.w4g128_pack(self.codes[e], self.scales[e], self.mins[e], K, N, self.packed[e * self.each:], stream=None)
 
-    def matrix(self, e):
-        """(w, |min| + 271 scale) [K][N] in 64 bits."""
+    def matrix(self, e, bias):
+        """(w, |min| + (2 bias + 15) scale) [K][N] in 64 bits."""
         shift = torch.arange(0, 32, 4, device="cuda", dtype=torch.int32)[None, :, None]
         q = ((self.codes[e][:, None] >> shift) & 15).reshape(self.K, self.N).double()
         s, m = (t[e].double().repeat_interleave(128, 0) for t in (self.scales, self.mins))
-        return m + q * s, m.abs() + 271 * s
+        return m + q * s, m.abs() + (2 * bias + 15) * s
 
 
 class Layer:
@@ -107,13 +108,13 @@ class Layer:
             rows, place = torch.nonzero(pick == e, as_tuple=True)
             if not rows.numel():
                 continue
-            W, B = self.gate_up.matrix(e)
+            W, B = self.gate_up.matrix(e, 1024)
             h, eh = x[rows] @ W, eps(self.D) * (x[rows].abs() @ B)
             gate, up, eg, eu = h[:, :self.F], h[:, self.F:], eh[:, :self.F], eh[:, self.F:]
             silu = gate * torch.sigmoid(gate)
             act = silu * up
             ea = 1.1 * up.abs() * eg + silu.abs() * eu + 1.1 * eg * eu + (2.0 ** -8 + 2.0 ** -20) * act.abs()
-            W, B = self.down.matrix(e)
+            W, B = self.down.matrix(e, 128)
             o = act @ W
             eo = ea @ W.abs() + eps(self.F) * ((act.abs() + ea) @ B)
             pe = p[rows, place][:, None]
@@ -134,7 +135,8 @@ class Layer:
 
 SHAPES = [(1, 128, 128, 1, 1), (1, 256, 128, 4, 2), (2, 128, 384, 5, 5), (3, 640, 256, 7, 3), (8, 512, 128, 16, 4),
           (9, 384, 640, 12, 2), (13, 1152, 384, 37, 3), (16, 256, 256, 3, 2), (16, 512, 512, 64, 6), (5, 1280, 1024, 9, 4),
-          (16, 128, 128, 512, 16), (1, 2048, 768, 24, 16)]
+          (16, 128, 128, 512, 16), (1, 2048, 768, 24, 16),
+          (16, 2048, 1408, 40, 5)]
 
 
 @pytest.mark.gpu
@@ -145,7 +147,8 @@ def test_against_reference(shape, renorm, residual):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", [(16, 512, 256, 8, 3), (7, 1152, 640, 40, 5), (12, 256, 128, 2, 1)], ids=str)
+@pytest.mark.parametrize("shape", [(16, 512, 256, 8, 3), (7, 1152, 640, 40, 5), (12, 256, 128, 2, 1), (16, 2048, 384, 40, 5)],
+                         ids=str)
 def test_a_row_alone_gives_the_same_bits(shape):
     layer = Layer(*shape, seed=4)
     y = layer.run()
