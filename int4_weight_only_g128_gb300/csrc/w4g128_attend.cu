@@ -8,10 +8,13 @@
 //   * A sequence is cut into chunks of C positions at multiples of C; one CTA
 //     takes one (chunk, head, up to 64 rows).  C follows from max_len and the
 //     window alone, so a row's sums never depend on the rows beside it.
-//   * The CTA's 4 groups of warps take the chunk's 16-position tiles in turn,
+//   * The CTA's groups of warps take the chunk's 16-position tiles in turn,
 //     each with its own ring of cp.async stages and its own running maximum
 //     and sum: no barrier of the whole CTA until the end.  A group is RT warps,
-//     one per 16 rows, sharing the group's tiles.
+//     one per 16 rows, sharing the group's tiles; with 256-wide heads two warps
+//     share a row tile, each with half of the depth of Q K^T (the halves are
+//     exchanged) and half of the columns of P V, so that a warp's registers
+//     stay at 128 and an SM holds 16 warps.
 //   * A tile lies in one page (page sizes are multiples of 16): one table
 //     lookup per tile, made before the loop.
 //   * S = Q K^T lands in the registers that P V wants it in; K comes by
@@ -36,7 +39,6 @@ namespace w4g128 {
 namespace {
 
 constexpr int kTile = 16;        // positions per tile
-constexpr int kKvGroups = 4;     // warp groups of a CTA, each with tiles of its own
 constexpr int kMaxChunk = 1024;  // positions per chunk, at most
 constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
@@ -127,32 +129,47 @@ __device__ __forceinline__ uint32_t finite_or_zero2(uint32_t v) {
   return v;
 }
 
+// KG groups of warps with tiles of their own, RT row tiles, DS warps per row tile.
 template <int D, int RT>
 struct Shape {
-  static constexpr int kThreads = kKvGroups * RT * 32;
+  static constexpr int kDs = D == 256 ? 2 : 1;
+  static constexpr int kKg = D == 256 ? 2 : 4;
+  static constexpr int kGroup = RT * kDs * 32;  // threads of a group
+  static constexpr int kThreads = kKg * kGroup;
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kTileBytes = kTile * kRowBytes;  // K or V of one tile
-  static constexpr int kStages = D == 256 ? 2 : D == 128 ? 3 : 4;
-  static constexpr int kRing = kKvGroups * kStages * 2 * kTileBytes;
-  static constexpr int kJoin = (kKvGroups - 1) * RT * 16 * (D + 2) * 4;  // three groups' sums, maxima and sums of weights
+  // stages: what 512 threads an SM (128 registers each) leave room for
+  static constexpr int kStages = RT == 1 ? (D == 64 ? 3 : 2) : RT == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 6 : 5);
+  static constexpr int kRing = kKg * kStages * 2 * kTileBytes;
+  static constexpr int kHalf = D / kDs;  // columns of a warp
+  static constexpr int kLeft = 16 * (kHalf + 2) * 4;  // a warp's sums, maxima and sums of weights
+  static constexpr int kJoin = (kKg - 1) * RT * kDs * kLeft;
   static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kExchange = kDs == 2 ? kKg * RT * 2 * 2 * 32 : 1;  // float4: [group][row tile][turn][half]..
 };
 
 template <int D, int RT>
-__global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Shape<D, RT>::kThreads, 512 / Shape<D, RT>::kThreads)
+attend_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, RT>;
-  constexpr int kSteps = D / 16;
-  constexpr int kChunks16 = D / 8;  // 16-byte pieces of a row
+  constexpr int kSteps = S::kHalf / 16;     // of Q K^T, per warp
+  constexpr int kPieces = D / 8;            // 16-byte pieces of a row
+  constexpr int kPer = kTile * kPieces / S::kGroup;  // pieces of a K tile that one thread copies
+  constexpr int kRows = S::kGroup / kPieces;         // rows between them
+  static_assert(S::kGroup % kPieces == 0 && kTile % kRows == 0, "a thread copies one column of pieces");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int s_page[kMaxChunk / kTile];
+  __shared__ float4 s_half[S::kExchange][2];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int kg = warp / RT, rt = warp % RT;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);
+  const int kg = warp / (RT * S::kDs), rt = warp / S::kDs % RT, half = warp % S::kDs;
   const int row_groups = (p.max_new * p.group + 16 * RT - 1) / (16 * RT);
   const int head = blockIdx.y / row_groups, rg = blockIdx.y % row_groups;
   const int b = blockIdx.z, z = blockIdx.x;
 
   grid_dependency_wait();
+  grid_dependents_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) status_clear(p.status);
   const Seq s = sequence(p, b);
   if (!s.ok) {
@@ -180,27 +197,11 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
     }
     s_page[t] = id;
   }
-  __syncthreads();
-
-  // The new rows go to their pages; nobody reads those slots in this call.
-  if (rg == 0 && p1 > fresh) {
-    const int a = max(p0, fresh);
-    for (int i = tid; i < (p1 - a) * kChunks16; i += S::kThreads) {
-      const int pos = a + i / kChunks16, c = i % kChunks16;
-      const int id = s_page[(pos - p0) / kTile];
-      if (id < 0) continue;
-      const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
-                            static_cast<long long>(head) * D + c * 8;
-      const long long dst = static_cast<long long>(id) * p.page_stride + (pos % p.page_size) * p.slot_stride +
-                            head * p.head_stride + c * 8;
-      *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
-      *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
-    }
-  }
 
   // Q: this lane's part of the A fragments of rows r and r + 8.
   const int r = lane >> 2, c = lane & 3;
   const int row0 = (rg * RT + rt) * 16 + r;
+  const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
   int pos_a = -1, pos_b = -1;  // the rows' positions
   uint32_t qf[kSteps][4];
   {
@@ -209,13 +210,13 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
     if (row0 < live_rows) {
       pos_a = s.start + row0 / p.group;
       qa = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row0 / p.group) * p.q_row +
-                                             static_cast<long long>(head * p.group + row0 % p.group) * D);
+                                             static_cast<long long>(head * p.group + row0 % p.group) * D + half * S::kHalf);
     }
     const int row1 = row0 + 8;
     if (row1 < live_rows) {
       pos_b = s.start + row1 / p.group;
       qb = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row1 / p.group) * p.q_row +
-                                             static_cast<long long>(head * p.group + row1 % p.group) * D);
+                                             static_cast<long long>(head * p.group + row1 % p.group) * D + half * S::kHalf);
     }
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
@@ -225,48 +226,65 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
       qf[k][3] = qb ? __ldg(qb + k * 8 + 4 + c) : 0u;
     }
   }
+  __syncthreads();
 
-  float acc[D / 8][4];
+  float acc[S::kHalf / 8][4];
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+  for (int i = 0; i < S::kHalf / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
   float m_a = kNone, m_b = kNone, l_a = 0.f, l_b = 0.f;
 
   const uint32_t ring = smem_addr(smem) + kg * S::kStages * 2 * S::kTileBytes;
-  const uint8_t* ring_ptr = smem + kg * S::kStages * 2 * S::kTileBytes;
-  const int gl = rt * 32 + lane;  // thread within the group
   auto group_sync = [&] {
-    if constexpr (RT == 1) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(RT * 32) : "memory");
+    if constexpr (S::kGroup == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(S::kGroup) : "memory");
   };
   // The group's tiles that some row sees, in rising order.
   auto next_tile = [&](int t) {
-    while (t < tiles) {
-      const int a = p0 + t * kTile;
-      if (a < s.sink || a + kTile > s.lo) break;
-      t += kKvGroups;
+    if (p.window > 0) {
+      while (t < tiles) {
+        const int a = p0 + t * kTile;
+        if (a < s.sink || a + kTile > s.lo) break;
+        t += S::kKg;
+      }
     }
     return t;
   };
+
+  // A thread copies one column of 16-byte pieces: rows j0, j0 + kRows, ..  The
+  // pieces of a row are exchanged by the row's low bits.
+  const int gl = (warp % (RT * S::kDs)) * 32 + lane;
+  const int ch = gl % kPieces, j0 = gl / kPieces;
+  const uint16_t* k_base = p.k_cache + head * p.head_stride + j0 * p.slot_stride + ch * 8;
+  const long long v_off = p.v_cache - p.k_cache;
+  const long long row_step = kRows * p.slot_stride;
   auto issue = [&](int t, int stage) {
     if (t < tiles) {
       const int a = p0 + t * kTile, id = s_page[t];
-      const uint32_t dst = ring + stage * 2 * S::kTileBytes;
-      const long long page = static_cast<long long>(max(id, 0)) * p.page_stride + head * p.head_stride;
-      const int slot = a % p.page_size;
+      const uint32_t dst = ring + stage * 2 * S::kTileBytes + j0 * S::kRowBytes;
+      if (a + kTile <= fresh && id >= 0) {  // a whole tile of the cache
+        const uint16_t* src = k_base + id * p.page_stride + (a % p.page_size) * p.slot_stride;
 #pragma unroll
-      for (int i = 0; i < kTile * kChunks16 / (RT * 32); ++i) {
-        const int e = i * RT * 32 + gl;
-        const int j = e / kChunks16, ch = e % kChunks16, pos = a + j;
-        const bool is_new = pos >= fresh;
-        const bool real = pos < s.len && (is_new || id >= 0);
-        const long long src = is_new ? static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
-                                           static_cast<long long>(head) * D
-                                     : page + static_cast<long long>(slot + j) * p.slot_stride;
-        const uint32_t at = dst + j * S::kRowBytes + ((ch ^ (j & 7)) << 4);
-        const uint16_t* kb = is_new ? p.k_new : p.k_cache;
-        const uint16_t* vb = is_new ? p.v_new : p.v_cache;
-        cp_async16_or_zero(at, real ? kb + src + ch * 8 : p.k_cache, real);
-        cp_async16_or_zero(at + S::kTileBytes, real ? vb + src + ch * 8 : p.k_cache, real);
+        for (int i = 0; i < kPer; ++i) {
+          const uint32_t at = dst + i * kRows * S::kRowBytes + ((ch ^ ((j0 + i * kRows) & 7)) << 4);
+          cp_async16(at, src);
+          cp_async16(at + S::kTileBytes, src + v_off);
+          src += row_step;
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kPer; ++i) {
+          const int j = j0 + i * kRows, pos = a + j;
+          const bool is_new = pos >= fresh;
+          const bool real = pos < s.len && (is_new || id >= 0);
+          const long long src =
+              is_new ? static_cast<long long>(s.first_row + pos - s.start) * p.kv_row + static_cast<long long>(head) * D
+                     : id * p.page_stride + (a % p.page_size + j) * p.slot_stride + head * p.head_stride;
+          const uint32_t at = dst + i * kRows * S::kRowBytes + ((ch ^ (j & 7)) << 4);
+          const uint16_t* kb = is_new ? p.k_new : p.k_cache;
+          const uint16_t* vb = is_new ? p.v_new : p.v_cache;
+          cp_async16_or_zero(at, real ? kb + src + ch * 8 : p.k_cache, real);
+          cp_async16_or_zero(at + S::kTileBytes, real ? vb + src + ch * 8 : p.k_cache, real);
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -274,122 +292,164 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
 
   int ahead = next_tile(kg);  // (chunks start at multiples of 64: a tile's group follows from its position)
   int t = ahead;
-#pragma unroll
+#pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) {
     issue(ahead, i);
-    ahead = next_tile(ahead + (ahead < tiles ? kKvGroups : 0));
+    ahead = next_tile(ahead + S::kKg);
   }
-  int stage = 0;
+
+  // The new rows go to their pages; nobody reads those slots in this call.
+  if (rg == 0 && p1 > fresh) {
+    const int a = max(p0, fresh);
+    for (int i = tid; i < (p1 - a) * kPieces; i += S::kThreads) {
+      const int pos = a + i / kPieces, piece = i % kPieces;
+      const int id = s_page[(pos - p0) / kTile];
+      if (id < 0) continue;
+      const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
+                            static_cast<long long>(head) * D + piece * 8;
+      const long long dst = id * p.page_stride + (pos % p.page_size) * p.slot_stride + head * p.head_stride + piece * 8;
+      *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
+      *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
+    }
+  }
+
+  // ldmatrix: this lane's row of a K and of a V tile, and its pieces 0, 2, 4, 6
+  // (the others follow at constant distances).
+  const int kj = (lane & 7) + ((lane >> 4) << 3), vj = (lane & 7) + (((lane >> 3) & 1) << 3);
+  uint32_t k_at[4], v_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    k_at[i] = kj * S::kRowBytes + half * 2 * S::kHalf + (((2 * i + ((lane >> 3) & 1)) ^ (kj & 7)) << 4);
+    v_at[i] = vj * S::kRowBytes + half * 2 * S::kHalf + (((2 * i + (lane >> 4)) ^ (vj & 7)) << 4) + S::kTileBytes;
+  }
   const int last_pos = s.len - 1;  // of the sequence's last row
+  int stage = 0;
+  [[maybe_unused]] int flip = 0;
   while (t < tiles) {
     cp_async_wait_group<S::kStages - 2>();
     group_sync();  // the tile is there for the group, and the stage refilled next is read out
     issue(ahead, stage == 0 ? S::kStages - 1 : stage - 1);
-    ahead = next_tile(ahead + (ahead < tiles ? kKvGroups : 0));
-
-    const uint32_t kt = ring + stage * 2 * S::kTileBytes, vt = kt + S::kTileBytes;
+    ahead = next_tile(ahead + S::kKg);
+    const uint32_t tile = ring + stage * 2 * S::kTileBytes;
     const int a = p0 + t * kTile;
-    float sc[2][4] = {};
+    if (busy) {
+      float sc[2][4] = {};
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      uint32_t kb[4];
-      const int j = (lane & 7) + ((lane >> 4) << 3), ch = 2 * k + ((lane >> 3) & 1);
-      ldmatrix4(kb, kt + j * S::kRowBytes + ((ch ^ (j & 7)) << 4));
-      mma(sc[0], qf[k], kb[0], kb[1]);
-      mma(sc[1], qf[k], kb[2], kb[3]);
-    }
-    // every row sees the whole tile
-    const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && s_page[t] >= 0 &&
-                        (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sc[h][i] *= p.scale2;
-    const bool page_ok = s_page[t] >= 0;
-    auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && (page_ok || pos >= fresh); };
-    if (!inside) {
+      for (int k = 0; k < kSteps; ++k) {
+        uint32_t kb[4];
+        ldmatrix4(kb, tile + k_at[k & 3] + (k >> 2) * 128);
+        mma(sc[0], qf[k], kb[0], kb[1]);
+        mma(sc[1], qf[k], kb[2], kb[3]);
+      }
+      if constexpr (S::kDs == 2) {  // the other half of the depth
+        float4* ex = &s_half[(((kg * RT + rt) * 2 + flip) * 2) * 32][0];
+        ex[(half * 32 + lane) * 2] = make_float4(sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
+        ex[(half * 32 + lane) * 2 + 1] = make_float4(sc[1][0], sc[1][1], sc[1][2], sc[1][3]);
+        asm volatile("bar.sync %0, 64;" ::"r"(S::kKg + 1 + kg * RT + rt) : "memory");
+        const float4 u = ex[((half ^ 1) * 32 + lane) * 2], v = ex[((half ^ 1) * 32 + lane) * 2 + 1];
+        sc[0][0] += u.x; sc[0][1] += u.y; sc[0][2] += u.z; sc[0][3] += u.w;
+        sc[1][0] += v.x; sc[1][1] += v.y; sc[1][2] += v.z; sc[1][3] += v.w;
+        flip ^= 1;  // (the next tile's exchange leaves this one alone)
+      }
+      const bool page_ok = s_page[t] >= 0;
+      // every row sees the whole tile
+      const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && page_ok &&
+                          (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!sees(i < 2 ? pos_a : pos_b, a + h * 8 + 2 * c + (i & 1))) sc[h][i] = kNone;
-    }
-    float ta = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-    float tb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+        for (int i = 0; i < 4; ++i) sc[h][i] *= p.scale2;
+      auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && (page_ok || pos >= fresh); };
+      if (!inside) {
 #pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
-      tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
-    }
-    if (__any_sync(~0u, ta > m_a || tb > m_b)) {  // (otherwise the factors below are 1)
-      const float na = fmaxf(m_a, ta), nb = fmaxf(m_b, tb);
-      const float fa = exp2_fast(m_a - (na == kNone ? 0.f : na)), fb = exp2_fast(m_b - (nb == kNone ? 0.f : nb));
-      const float ga = na == m_a ? 1.f : fa, gb = nb == m_b ? 1.f : fb;
-      m_a = na;
-      m_b = nb;
-      l_a *= ga;
-      l_b *= gb;
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) {
-        acc[i][0] *= ga;
-        acc[i][1] *= ga;
-        acc[i][2] *= gb;
-        acc[i][3] *= gb;
+          for (int i = 0; i < 4; ++i)
+            if (!sees(i < 2 ? pos_a : pos_b, a + h * 8 + 2 * c + (i & 1))) sc[h][i] = kNone;
       }
-    }
-    const float ra = m_a == kNone ? 0.f : m_a, rb = m_b == kNone ? 0.f : m_b;
-    uint32_t pf[4];
-    pf[0] = pack_bf16(exp2_fast(sc[0][0] - ra), exp2_fast(sc[0][1] - ra));
-    pf[1] = pack_bf16(exp2_fast(sc[0][2] - rb), exp2_fast(sc[0][3] - rb));
-    pf[2] = pack_bf16(exp2_fast(sc[1][0] - ra), exp2_fast(sc[1][1] - ra));
-    pf[3] = pack_bf16(exp2_fast(sc[1][2] - rb), exp2_fast(sc[1][3] - rb));
-    l_a += (low_f(pf[0]) + high_f(pf[0])) + (low_f(pf[2]) + high_f(pf[2]));
-    l_b += (low_f(pf[1]) + high_f(pf[1])) + (low_f(pf[3]) + high_f(pf[3]));
+      float ta = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+      float tb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
+        tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
+      }
+      if (__any_sync(~0u, ta > m_a || tb > m_b)) {  // (otherwise the factors below are 1)
+        const float na = fmaxf(m_a, ta), nb = fmaxf(m_b, tb);
+        const float fa = exp2_fast(m_a - (na == kNone ? 0.f : na)), fb = exp2_fast(m_b - (nb == kNone ? 0.f : nb));
+        const float ga = na == m_a ? 1.f : fa, gb = nb == m_b ? 1.f : fb;
+        m_a = na;
+        m_b = nb;
+        l_a *= ga;
+        l_b *= gb;
+#pragma unroll
+        for (int i = 0; i < S::kHalf / 8; ++i) {
+          acc[i][0] *= ga;
+          acc[i][1] *= ga;
+          acc[i][2] *= gb;
+          acc[i][3] *= gb;
+        }
+      }
+      const float ra = m_a == kNone ? 0.f : m_a, rb = m_b == kNone ? 0.f : m_b;
+      uint32_t pf[4];
+      pf[0] = pack_bf16(exp2_fast(sc[0][0] - ra), exp2_fast(sc[0][1] - ra));
+      pf[1] = pack_bf16(exp2_fast(sc[0][2] - rb), exp2_fast(sc[0][3] - rb));
+      pf[2] = pack_bf16(exp2_fast(sc[1][0] - ra), exp2_fast(sc[1][1] - ra));
+      pf[3] = pack_bf16(exp2_fast(sc[1][2] - rb), exp2_fast(sc[1][3] - rb));
+      l_a += (low_f(pf[0]) + high_f(pf[0])) + (low_f(pf[2]) + high_f(pf[2]));
+      l_b += (low_f(pf[1]) + high_f(pf[1])) + (low_f(pf[3]) + high_f(pf[3]));
 
-    bool odd = false;  // non-finite values in a tile that not every row sees whole
-    if (!inside) {
-      const uint4* v = reinterpret_cast<const uint4*>(ring_ptr + stage * 2 * S::kTileBytes + S::kTileBytes);
-      for (int i = lane; i < S::kTileBytes / 16; i += 32) {
-        const uint4 u = v[i];
-        odd |= non_finite2(u.x) || non_finite2(u.y) || non_finite2(u.z) || non_finite2(u.w);
+      bool odd = false;  // non-finite values in a tile that not every row sees whole
+      const uint8_t* v_tile = smem + (kg * S::kStages + stage) * 2 * S::kTileBytes + S::kTileBytes;
+      if (!inside) {
+        const uint4* v = reinterpret_cast<const uint4*>(v_tile);
+        for (int i = lane; i < S::kTileBytes / 16; i += 32) {
+          const uint4 u = v[i];
+          odd |= non_finite2(u.x) || non_finite2(u.y) || non_finite2(u.z) || non_finite2(u.w);
+        }
+        odd = __any_sync(~0u, odd);
       }
-      odd = __any_sync(~0u, odd);
-    }
+      if (!odd) {
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      uint32_t vb[4];
-      const int j = (lane & 7) + (((lane >> 3) & 1) << 3), ch = 2 * i + (lane >> 4);
-      ldmatrix4_trans(vb, vt + j * S::kRowBytes + ((ch ^ (j & 7)) << 4));
-      if (odd) {
+        for (int i = 0; i < S::kHalf / 16; ++i) {
+          uint32_t vb[4];
+          ldmatrix4_trans(vb, tile + v_at[i & 3] + (i >> 2) * 128);
+          mma(acc[2 * i], pf, vb[0], vb[1]);
+          mma(acc[2 * i + 1], pf, vb[2], vb[3]);
+        }
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vb[e] = finite_or_zero2(vb[e]);
-      }
-      mma(acc[2 * i], pf, vb[0], vb[1]);
-      mma(acc[2 * i + 1], pf, vb[2], vb[3]);
-    }
-    if (odd) {
-      const uint8_t* v = ring_ptr + stage * 2 * S::kTileBytes + S::kTileBytes;
-      for (int j = 0; j < kTile; ++j) {
-        const uint32_t wa = j < 8 ? pf[0] : pf[2], wb = j < 8 ? pf[1] : pf[3];
-        const int from = (lane & ~3) | ((j & 7) >> 1);
-        const uint32_t ua = __shfl_sync(~0u, wa, from), ub = __shfl_sync(~0u, wb, from);
-        const float fa = (j & 1) ? high_f(ua) : low_f(ua), fb = (j & 1) ? high_f(ub) : low_f(ub);
-        const bool va = sees(pos_a, a + j), vb = sees(pos_b, a + j);
+        for (int i = 0; i < S::kHalf / 16; ++i) {
+          uint32_t vb[4];
+          ldmatrix4_trans(vb, tile + v_at[i & 3] + (i >> 2) * 128);
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u = *reinterpret_cast<const uint32_t*>(v + j * S::kRowBytes + ((i ^ (j & 7)) << 4) + 4 * c);
-          if ((u & 0x7F80u) == 0x7F80u) {
-            if (va) acc[i][0] += fa * low_f(u);
-            if (vb) acc[i][2] += fb * low_f(u);
-          }
-          if ((u & 0x7F800000u) == 0x7F800000u) {
-            if (va) acc[i][1] += fa * high_f(u);
-            if (vb) acc[i][3] += fb * high_f(u);
+          for (int e = 0; e < 4; ++e) vb[e] = finite_or_zero2(vb[e]);
+          mma(acc[2 * i], pf, vb[0], vb[1]);
+          mma(acc[2 * i + 1], pf, vb[2], vb[3]);
+        }
+        for (int j = 0; j < kTile; ++j) {
+          const uint32_t wa = j < 8 ? pf[0] : pf[2], wb = j < 8 ? pf[1] : pf[3];
+          const int from = (lane & ~3) | ((j & 7) >> 1);
+          const uint32_t ua = __shfl_sync(~0u, wa, from), ub = __shfl_sync(~0u, wb, from);
+          const float fa = (j & 1) ? high_f(ua) : low_f(ua), fb = (j & 1) ? high_f(ub) : low_f(ub);
+          const bool va = sees(pos_a, a + j), vb = sees(pos_b, a + j);
+#pragma unroll
+          for (int i = 0; i < S::kHalf / 8; ++i) {
+            const uint32_t u = *reinterpret_cast<const uint32_t*>(v_tile + j * S::kRowBytes + half * 2 * S::kHalf +
+                                                                  ((i ^ (j & 7)) << 4) + 4 * c);
+            if ((u & 0x7F80u) == 0x7F80u) {
+              if (va) acc[i][0] += fa * low_f(u);
+              if (vb) acc[i][2] += fb * low_f(u);
+            }
+            if ((u & 0x7F800000u) == 0x7F800000u) {
+              if (va) acc[i][1] += fa * high_f(u);
+              if (vb) acc[i][3] += fb * high_f(u);
+            }
           }
         }
       }
     }
-    t = next_tile(t + kKvGroups);
+    t = next_tile(t + S::kKg);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
 #pragma unroll
@@ -400,29 +460,30 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring becomes the exchange
 
-  // Join the four groups in order: groups 1..3 leave theirs, group 0 adds.
+  // Join the groups in order: the others leave theirs, group 0 adds.
   float* ex = reinterpret_cast<float*>(smem);
-  constexpr int kExWarp = 16 * (D + 2);
+  constexpr int kLeft = S::kLeft / 4;
+  const int slot = rt * S::kDs + half;
   if (kg > 0) {
-    float* e = ex + ((kg - 1) * RT + rt) * kExWarp;
+    float* e = ex + ((kg - 1) * RT * S::kDs + slot) * kLeft;
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i)
+    for (int i = 0; i < S::kHalf / 8; ++i)
       reinterpret_cast<float4*>(e)[i * 32 + lane] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
     if (c == 0) {
-      float2* st = reinterpret_cast<float2*>(e + 16 * D);
+      float2* st = reinterpret_cast<float2*>(e + 16 * S::kHalf);
       st[r] = make_float2(m_a, l_a);
       st[r + 8] = make_float2(m_b, l_b);
     }
   }
   __syncthreads();
   if (kg > 0) return;
-  float2 sa[kKvGroups], sb[kKvGroups];
+  float2 sa[S::kKg], sb[S::kKg];
   sa[0] = make_float2(m_a, l_a);
   sb[0] = make_float2(m_b, l_b);
   float top_a = m_a, top_b = m_b;
 #pragma unroll
-  for (int g = 1; g < kKvGroups; ++g) {
-    const float2* st = reinterpret_cast<const float2*>(ex + ((g - 1) * RT + rt) * kExWarp + 16 * D);
+  for (int g = 1; g < S::kKg; ++g) {
+    const float2* st = reinterpret_cast<const float2*>(ex + ((g - 1) * RT * S::kDs + slot) * kLeft + 16 * S::kHalf);
     sa[g] = st[r];
     sb[g] = st[r + 8];
     top_a = fmaxf(top_a, sa[g].x);
@@ -433,21 +494,21 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
   l_a = sa[0].y * wa;
   l_b = sb[0].y * wb;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {
+  for (int i = 0; i < S::kHalf / 8; ++i) {
     acc[i][0] *= wa;
     acc[i][1] *= wa;
     acc[i][2] *= wb;
     acc[i][3] *= wb;
   }
 #pragma unroll
-  for (int g = 1; g < kKvGroups; ++g) {
+  for (int g = 1; g < S::kKg; ++g) {
     wa = exp2_fast(sa[g].x - ra);
     wb = exp2_fast(sb[g].x - rb);
     l_a = fmaf(sa[g].y, wa, l_a);
     l_b = fmaf(sb[g].y, wb, l_b);
-    const float4* e = reinterpret_cast<const float4*>(ex + ((g - 1) * RT + rt) * kExWarp);
+    const float4* e = reinterpret_cast<const float4*>(ex + ((g - 1) * RT * S::kDs + slot) * kLeft);
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
+    for (int i = 0; i < S::kHalf / 8; ++i) {
       const float4 v = e[i * 32 + lane];
       acc[i][0] = fmaf(v.x, wa, acc[i][0]);
       acc[i][1] = fmaf(v.y, wa, acc[i][1]);
@@ -457,23 +518,23 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads) attend_kernel(const __
   }
 
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int row = row0 + 8 * half;
+  for (int side = 0; side < 2; ++side) {
+    const int row = row0 + 8 * side;
     if (row >= live_rows) continue;
-    const float l = half ? l_b : l_a;
+    const float l = side ? l_b : l_a;
     if (direct) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible position: zeros
       uint32_t* o = reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + row / p.group) * p.out_row +
-                                                static_cast<long long>(head * p.group + row % p.group) * D);
+                                                static_cast<long long>(head * p.group + row % p.group) * D + half * S::kHalf);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i * 4 + c] = pack_bf16(acc[i][2 * half] * inv, acc[i][2 * half + 1] * inv);
+      for (int i = 0; i < S::kHalf / 8; ++i) o[i * 4 + c] = pack_bf16(acc[i][2 * side] * inv, acc[i][2 * side + 1] * inv);
     } else {
       const long long at =
           ((static_cast<long long>(b) * p.splits + z) * p.kv_heads + head) * (p.max_new * p.group) + row;
-      float2* o = reinterpret_cast<float2*>(p.part + at * D);
+      float2* o = reinterpret_cast<float2*>(p.part + at * D + half * S::kHalf);
 #pragma unroll
-      for (int i = 0; i < D / 8; ++i) o[i * 4 + c] = make_float2(acc[i][2 * half], acc[i][2 * half + 1]);
-      if (c == 0) p.stat[at] = make_float2(half ? top_b : top_a, l);
+      for (int i = 0; i < S::kHalf / 8; ++i) o[i * 4 + c] = make_float2(acc[i][2 * side], acc[i][2 * side + 1]);
+      if (c == 0 && half == 0) p.stat[at] = make_float2(side ? top_b : top_a, l);
     }
   }
 }
@@ -504,16 +565,37 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   const float ref = top == kNone ? 0.f : top;
   __syncthreads();
 
+  // this warp's chunks: numbers = warp mod 4, four loads in flight
   float sum[kPer] = {}, l = 0.f;
-  for (int z = 0; z < s.chunks; ++z) {
-    if ((s.chunk_id(z) & 3) != warp) continue;
-    const float2 st = p.stat[at0 + z * step];
-    const float w = exp2_fast(st.x - ref);
-    const float* o = p.part + (at0 + z * step) * D + lane * kPer;
-    l = fmaf(st.y, w, l);
+  const int sinks = s.sink_chunks;
+  auto add = [&](int z0, int z1, int id0) {  // chunks z0 .. z1 - 1 are numbers id0 ..
+    int z = z0 + ((warp - id0) & 3);
+    for (; z < z1; z += 16) {
+      float2 st[4];
+      float v[4][kPer];
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) sum[k] = fmaf(o[k], w, sum[k]);
-  }
+      for (int j = 0; j < 4; ++j) {
+        const long long at = at0 + min(z + 4 * j, z1 - 1) * step;
+        st[j] = z + 4 * j < z1 ? p.stat[at] : make_float2(kNone, 0.f);
+        const float* o = p.part + at * D + lane * kPer;
+        if constexpr (kPer == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(o);
+        else
+#pragma unroll
+          for (int k = 0; k < kPer; k += 4) *reinterpret_cast<float4*>(&v[j][k]) = *reinterpret_cast<const float4*>(o + k);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (z + 4 * j < z1) {
+          const float w = exp2_fast(st[j].x - ref);
+          l = fmaf(st[j].y, w, l);
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k]);
+        }
+      }
+    }
+  };
+  add(0, sinks, 0);
+  add(sinks, s.chunks, s.lo_chunk);
 #pragma unroll
   for (int k = 0; k < kPer; ++k) s_sum[warp][lane * kPer + k] = sum[k];
   if (lane == 0) s_stat[warp].y = l;
@@ -529,15 +611,15 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   }
 }
 
-// Positions per chunk: a rule on the longest span that a call's rows may see.
+// Positions per chunk: a power of two that gives one sequence's heads about
+// kTarget CTAs over the longest span that its rows may see.
+constexpr int kTarget = 256;
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
-  if (span <= 1024) return 64;
-  if (span <= 4096) return 128;
-  if (span <= 65536) return 256;
-  if (span <= 262144) return 512;
-  return kMaxChunk;
+  int chunk = 64;
+  while (chunk < kMaxChunk && static_cast<long long>(chunk) * kTarget < span * a.kv_heads) chunk *= 2;
+  return chunk;
 }
 
 // Most chunks that a sequence's rows can see: all of them, or the window's
@@ -598,10 +680,8 @@ cudaError_t launch_attend(cudaLaunchConfig_t& cfg, const Params& p) {
 template <int D>
 cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
   const int rows = p.max_new * p.group;
-  cudaError_t e;
-  if (rows <= 16) e = launch_attend<D, 1>(cfg, p);
-  else if (rows <= 32 || D == 256) e = launch_attend<D, 2>(cfg, p);  // (4 x 16 rows of 256 do not fit the registers)
-  else if constexpr (D != 256) e = launch_attend<D, 4>(cfg, p);
+  const cudaError_t e = rows <= 16 ? launch_attend<D, 1>(cfg, p) : rows <= 32 ? launch_attend<D, 2>(cfg, p)
+                                                                              : launch_attend<D, 4>(cfg, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
   cfg.blockDim = dim3(128);
