@@ -42,6 +42,7 @@ constexpr int kTile = 16;        // positions per tile
 constexpr int kMaxChunk = 1024;  // positions per chunk, at most
 constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
+constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
 
 struct Params {
   const uint16_t *q, *k_new, *v_new;
@@ -51,7 +52,8 @@ struct Params {
   long long q_row, kv_row, out_row, page_stride, slot_stride, head_stride, table_row;
   int rows, count, q_heads, kv_heads, group, pages, page_size, max_len, max_new, window, sinks;
   int chunk, splits;  // positions per chunk; chunks a sequence may need
-  float scale2;       // scale * log2(e)
+  float scale2;       // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
+  uint32_t flip_q, keep_q;
   unsigned long long* status;
   float* part;        // [count][splits][kv_heads][max_new * group][head_dim]: unnormalised sums
   float2* stat;       // [count][splits][kv_heads][max_new * group]: maximum (base 2) and sum
@@ -139,12 +141,15 @@ struct Shape {
   static constexpr int kRowBytes = 2 * D;
   static constexpr int kTileBytes = kTile * kRowBytes;  // K or V of one tile
   // stages: what 512 threads an SM (128 registers each) leave room for
-  static constexpr int kStages = RT == 1 ? (D == 64 ? 3 : 2) : RT == 2 ? (D == 64 ? 4 : 3) : (D == 64 ? 6 : 5);
+  static constexpr int kStages = RT == 1 ? (D == 64 ? 3 : 2) : RT == 2 ? (D == 64 ? 4 : D == 128 ? 3 : 2)
+                                                                       : (D == 64 ? 6 : D == 128 ? 5 : 4);
+  static constexpr bool kQInRegs = D == 64;  // else its fragments are read from shared memory for each tile
+  static constexpr int kQBytes = kQInRegs ? 0 : RT * 16 * kRowBytes;
   static constexpr int kRing = kKg * kStages * 2 * kTileBytes;
   static constexpr int kHalf = D / kDs;  // columns of a warp
   static constexpr int kLeft = 16 * (kHalf + 2) * 4;  // a warp's sums, maxima and sums of weights
   static constexpr int kJoin = (kKg - 1) * RT * kDs * kLeft;
-  static constexpr int kBytes = kRing > kJoin ? kRing : kJoin;
+  static constexpr int kBytes = kQBytes + (kRing > kJoin ? kRing : kJoin);
   static constexpr int kExchange = kDs == 2 ? kKg * RT * 2 * 2 * 32 : 1;  // float4: [group][row tile][turn][half]..
 };
 
@@ -158,7 +163,7 @@ attend_kernel(const __grid_constant__ Params p) {
   constexpr int kRows = S::kGroup / kPieces;         // rows between them
   static_assert(S::kGroup % kPieces == 0 && kTile % kRows == 0, "a thread copies one column of pieces");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int s_page[kMaxChunk / kTile];
+  __shared__ long long s_tile[kMaxChunk / kTile];  // a tile's first element in the caches, or -1: not a page
   __shared__ float4 s_half[S::kExchange][2];
 
   const int tid = threadIdx.x, lane = tid & 31;
@@ -185,45 +190,57 @@ attend_kernel(const __grid_constant__ Params p) {
   const int p1 = s.chunks ? min(p0 + p.chunk, s.len) : 0;
   const int fresh = p.k_new != nullptr ? s.first : s.len;  // positions from here on come from k_new, v_new
 
-  // this chunk's page ids; -1: not a page
+  // where this chunk's tiles are
   const int tiles = (p1 - p0 + kTile - 1) / kTile;
   for (int t = tid; t < tiles; t += S::kThreads) {
     const int a = p0 + t * kTile;
     const bool seen = a < s.sink || (a + kTile > s.lo && a < s.len);
-    int id = seen ? p.table[static_cast<long long>(b) * p.table_row + a / p.page_size] : -1;
-    if (seen && (id < 0 || id >= p.pages)) {
-      id = -1;
-      status_error(p.status, W4G128_ERR_CACHE);
-    }
-    s_page[t] = id;
+    const int id = seen ? p.table[static_cast<long long>(b) * p.table_row + a / p.page_size] : -1;
+    const bool ok = id >= 0 && id < p.pages;
+    if (seen && !ok) status_error(p.status, W4G128_ERR_CACHE);
+    s_tile[t] = ok ? id * p.page_stride + (a % p.page_size) * p.slot_stride + head * p.head_stride : -1;
   }
 
   // Q: this lane's part of the A fragments of rows r and r + 8.
   const int r = lane >> 2, c = lane & 3;
   const int row0 = (rg * RT + rt) * 16 + r;
   const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
-  int pos_a = -1, pos_b = -1;  // the rows' positions
-  uint32_t qf[kSteps][4];
-  {
+  const int pos_a = row0 < live_rows ? s.start + row0 / p.group : -1;  // the rows' positions
+  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.group : -1;
+  // (a negative scale goes into q's signs, a scale of 0 makes q 0)
+  uint32_t qf[S::kQInRegs ? kSteps : 1][4];
+  if constexpr (!S::kQInRegs) {
+    for (int i = tid; i < RT * 16 * kPieces; i += S::kThreads) {
+      const int j = i / kPieces, piece = i % kPieces, row = rg * RT * 16 + j;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (row < live_rows)
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<long long>(s.first_row + row / p.group) * p.q_row +
+                                                 static_cast<long long>(head * p.group + row % p.group) * D + piece * 8));
+      v.x = (v.x & p.keep_q) ^ p.flip_q;
+      v.y = (v.y & p.keep_q) ^ p.flip_q;
+      v.z = (v.z & p.keep_q) ^ p.flip_q;
+      v.w = (v.w & p.keep_q) ^ p.flip_q;
+      *reinterpret_cast<uint4*>(smem + j * S::kRowBytes + ((piece ^ (j & 7)) << 4)) = v;
+    }
+  } else {
     const uint32_t* qa = nullptr;
     const uint32_t* qb = nullptr;
     if (row0 < live_rows) {
-      pos_a = s.start + row0 / p.group;
       qa = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row0 / p.group) * p.q_row +
                                              static_cast<long long>(head * p.group + row0 % p.group) * D + half * S::kHalf);
     }
     const int row1 = row0 + 8;
     if (row1 < live_rows) {
-      pos_b = s.start + row1 / p.group;
       qb = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row1 / p.group) * p.q_row +
                                              static_cast<long long>(head * p.group + row1 % p.group) * D + half * S::kHalf);
     }
+    const uint32_t flip = p.flip_q, keep = p.keep_q;
 #pragma unroll
     for (int k = 0; k < kSteps; ++k) {
-      qf[k][0] = qa ? __ldg(qa + k * 8 + c) : 0u;
-      qf[k][1] = qb ? __ldg(qb + k * 8 + c) : 0u;
-      qf[k][2] = qa ? __ldg(qa + k * 8 + 4 + c) : 0u;
-      qf[k][3] = qb ? __ldg(qb + k * 8 + 4 + c) : 0u;
+      qf[k][0] = qa ? (__ldg(qa + k * 8 + c) & keep) ^ flip : 0u;
+      qf[k][1] = qb ? (__ldg(qb + k * 8 + c) & keep) ^ flip : 0u;
+      qf[k][2] = qa ? (__ldg(qa + k * 8 + 4 + c) & keep) ^ flip : 0u;
+      qf[k][3] = qb ? (__ldg(qb + k * 8 + 4 + c) & keep) ^ flip : 0u;
     }
   }
   __syncthreads();
@@ -231,9 +248,11 @@ attend_kernel(const __grid_constant__ Params p) {
   float acc[S::kHalf / 8][4];
 #pragma unroll
   for (int i = 0; i < S::kHalf / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  float m_a = kNone, m_b = kNone, l_a = 0.f, l_b = 0.f;
+  // running maxima of the raw scores of rows r and r + 8, and the sums of the
+  // weights (sum[0] and sum[2]: a product with ones)
+  float m_a = kNone, m_b = kNone, sum[4] = {};
 
-  const uint32_t ring = smem_addr(smem) + kg * S::kStages * 2 * S::kTileBytes;
+  const uint32_t ring = smem_addr(smem) + S::kQBytes + kg * S::kStages * 2 * S::kTileBytes;
   auto group_sync = [&] {
     if constexpr (S::kGroup == 32) __syncwarp();
     else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(S::kGroup) : "memory");
@@ -254,20 +273,24 @@ attend_kernel(const __grid_constant__ Params p) {
   // pieces of a row are exchanged by the row's low bits.
   const int gl = (warp % (RT * S::kDs)) * 32 + lane;
   const int ch = gl % kPieces, j0 = gl / kPieces;
-  const uint16_t* k_base = p.k_cache + head * p.head_stride + j0 * p.slot_stride + ch * 8;
+  const uint16_t* k_base = p.k_cache + j0 * p.slot_stride + ch * 8;
   const long long v_off = p.v_cache - p.k_cache;
   const long long row_step = kRows * p.slot_stride;
+  uint32_t put[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    put[i] = ring + (j0 + i * kRows) * S::kRowBytes + ((ch ^ ((j0 + i * kRows) & 7)) << 4);
   auto issue = [&](int t, int stage) {
     if (t < tiles) {
-      const int a = p0 + t * kTile, id = s_page[t];
-      const uint32_t dst = ring + stage * 2 * S::kTileBytes + j0 * S::kRowBytes;
-      if (a + kTile <= fresh && id >= 0) {  // a whole tile of the cache
-        const uint16_t* src = k_base + id * p.page_stride + (a % p.page_size) * p.slot_stride;
+      const int a = p0 + t * kTile;
+      const long long where = s_tile[t];
+      const uint32_t dst = stage * 2 * S::kTileBytes;
+      if (a + kTile <= fresh && where >= 0) {  // a whole tile of the cache
+        const uint16_t* src = k_base + where;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const uint32_t at = dst + i * kRows * S::kRowBytes + ((ch ^ ((j0 + i * kRows) & 7)) << 4);
-          cp_async16(at, src);
-          cp_async16(at + S::kTileBytes, src + v_off);
+          cp_async16(put[i] + dst, src);
+          cp_async16(put[i] + dst + S::kTileBytes, src + v_off);
           src += row_step;
         }
       } else {
@@ -275,15 +298,15 @@ attend_kernel(const __grid_constant__ Params p) {
         for (int i = 0; i < kPer; ++i) {
           const int j = j0 + i * kRows, pos = a + j;
           const bool is_new = pos >= fresh;
-          const bool real = pos < s.len && (is_new || id >= 0);
-          const long long src =
-              is_new ? static_cast<long long>(s.first_row + pos - s.start) * p.kv_row + static_cast<long long>(head) * D
-                     : id * p.page_stride + (a % p.page_size + j) * p.slot_stride + head * p.head_stride;
-          const uint32_t at = dst + i * kRows * S::kRowBytes + ((ch ^ (j & 7)) << 4);
+          const bool real = pos < s.len && (is_new || where >= 0);
+          const long long src = is_new ? static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
+                                             static_cast<long long>(head) * D + ch * 8
+                                       : where + j * p.slot_stride + ch * 8;
+          const uint32_t at = ring + dst + j * S::kRowBytes + ((ch ^ (j & 7)) << 4);
           const uint16_t* kb = is_new ? p.k_new : p.k_cache;
           const uint16_t* vb = is_new ? p.v_new : p.v_cache;
-          cp_async16_or_zero(at, real ? kb + src + ch * 8 : p.k_cache, real);
-          cp_async16_or_zero(at + S::kTileBytes, real ? vb + src + ch * 8 : p.k_cache, real);
+          cp_async16_or_zero(at, real ? kb + src : p.k_cache, real);
+          cp_async16_or_zero(at + S::kTileBytes, real ? vb + src : p.k_cache, real);
         }
       }
     }
@@ -303,11 +326,11 @@ attend_kernel(const __grid_constant__ Params p) {
     const int a = max(p0, fresh);
     for (int i = tid; i < (p1 - a) * kPieces; i += S::kThreads) {
       const int pos = a + i / kPieces, piece = i % kPieces;
-      const int id = s_page[(pos - p0) / kTile];
-      if (id < 0) continue;
+      const long long where = s_tile[(pos - p0) / kTile];
+      if (where < 0) continue;
       const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
                             static_cast<long long>(head) * D + piece * 8;
-      const long long dst = id * p.page_stride + (pos % p.page_size) * p.slot_stride + head * p.head_stride + piece * 8;
+      const long long dst = where + (pos - p0) % kTile * p.slot_stride + piece * 8;
       *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
       *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
     }
@@ -322,6 +345,7 @@ attend_kernel(const __grid_constant__ Params p) {
     k_at[i] = kj * S::kRowBytes + half * 2 * S::kHalf + (((2 * i + ((lane >> 3) & 1)) ^ (kj & 7)) << 4);
     v_at[i] = vj * S::kRowBytes + half * 2 * S::kHalf + (((2 * i + (lane >> 4)) ^ (vj & 7)) << 4) + S::kTileBytes;
   }
+  const uint32_t q_tile = smem_addr(smem) + rt * 16 * S::kRowBytes - S::kTileBytes;
   const int last_pos = s.len - 1;  // of the sequence's last row
   int stage = 0;
   [[maybe_unused]] int flip = 0;
@@ -333,14 +357,24 @@ attend_kernel(const __grid_constant__ Params p) {
     const uint32_t tile = ring + stage * 2 * S::kTileBytes;
     const int a = p0 + t * kTile;
     if (busy) {
-      float sc[2][4] = {};
+      float sc[2][4] = {}, odd_k[2][4] = {};  // two chains of products each
 #pragma unroll
       for (int k = 0; k < kSteps; ++k) {
-        uint32_t kb[4];
+        uint32_t kb[4], qk[4];
         ldmatrix4(kb, tile + k_at[k & 3] + (k >> 2) * 128);
-        mma(sc[0], qf[k], kb[0], kb[1]);
-        mma(sc[1], qf[k], kb[2], kb[3]);
+        if constexpr (S::kQInRegs) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qk[i] = qf[k][i];
+        } else {  // (rows and pieces lie as in a V tile)
+          ldmatrix4(qk, q_tile + v_at[k & 3] + (k >> 2) * 128);
+        }
+        mma((k & 1) ? odd_k[0] : sc[0], qk, kb[0], kb[1]);
+        mma((k & 1) ? odd_k[1] : sc[1], qk, kb[2], kb[3]);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sc[h][i] += odd_k[h][i];
       if constexpr (S::kDs == 2) {  // the other half of the depth
         float4* ex = &s_half[(((kg * RT + rt) * 2 + flip) * 2) * 32][0];
         ex[(half * 32 + lane) * 2] = make_float4(sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
@@ -351,14 +385,10 @@ attend_kernel(const __grid_constant__ Params p) {
         sc[1][0] += v.x; sc[1][1] += v.y; sc[1][2] += v.z; sc[1][3] += v.w;
         flip ^= 1;  // (the next tile's exchange leaves this one alone)
       }
-      const bool page_ok = s_page[t] >= 0;
+      const bool page_ok = s_tile[t] >= 0;
       // every row sees the whole tile
       const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && page_ok &&
                           (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sc[h][i] *= p.scale2;
       auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && (page_ok || pos >= fresh); };
       if (!inside) {
 #pragma unroll
@@ -376,12 +406,12 @@ attend_kernel(const __grid_constant__ Params p) {
       }
       if (__any_sync(~0u, ta > m_a || tb > m_b)) {  // (otherwise the factors below are 1)
         const float na = fmaxf(m_a, ta), nb = fmaxf(m_b, tb);
-        const float fa = exp2_fast(m_a - (na == kNone ? 0.f : na)), fb = exp2_fast(m_b - (nb == kNone ? 0.f : nb));
-        const float ga = na == m_a ? 1.f : fa, gb = nb == m_b ? 1.f : fb;
+        const float ga = na == m_a ? 1.f : exp2_fast((m_a - na) * p.scale2);
+        const float gb = nb == m_b ? 1.f : exp2_fast((m_b - nb) * p.scale2);
         m_a = na;
         m_b = nb;
-        l_a *= ga;
-        l_b *= gb;
+        sum[0] *= ga;
+        sum[2] *= gb;
 #pragma unroll
         for (int i = 0; i < S::kHalf / 8; ++i) {
           acc[i][0] *= ga;
@@ -390,17 +420,17 @@ attend_kernel(const __grid_constant__ Params p) {
           acc[i][3] *= gb;
         }
       }
-      const float ra = m_a == kNone ? 0.f : m_a, rb = m_b == kNone ? 0.f : m_b;
+      const float ra = m_a == kNone ? 0.f : -m_a * p.scale2, rb = m_b == kNone ? 0.f : -m_b * p.scale2;
+      auto weight = [&](float x, float ref) { return exp2_fast(fmaf(x, p.scale2, ref)); };
       uint32_t pf[4];
-      pf[0] = pack_bf16(exp2_fast(sc[0][0] - ra), exp2_fast(sc[0][1] - ra));
-      pf[1] = pack_bf16(exp2_fast(sc[0][2] - rb), exp2_fast(sc[0][3] - rb));
-      pf[2] = pack_bf16(exp2_fast(sc[1][0] - ra), exp2_fast(sc[1][1] - ra));
-      pf[3] = pack_bf16(exp2_fast(sc[1][2] - rb), exp2_fast(sc[1][3] - rb));
-      l_a += (low_f(pf[0]) + high_f(pf[0])) + (low_f(pf[2]) + high_f(pf[2]));
-      l_b += (low_f(pf[1]) + high_f(pf[1])) + (low_f(pf[3]) + high_f(pf[3]));
+      pf[0] = pack_bf16(weight(sc[0][0], ra), weight(sc[0][1], ra));
+      pf[1] = pack_bf16(weight(sc[0][2], rb), weight(sc[0][3], rb));
+      pf[2] = pack_bf16(weight(sc[1][0], ra), weight(sc[1][1], ra));
+      pf[3] = pack_bf16(weight(sc[1][2], rb), weight(sc[1][3], rb));
+      mma(sum, pf, kOnes, kOnes);
 
       bool odd = false;  // non-finite values in a tile that not every row sees whole
-      const uint8_t* v_tile = smem + (kg * S::kStages + stage) * 2 * S::kTileBytes + S::kTileBytes;
+      const uint8_t* v_tile = smem + S::kQBytes + (kg * S::kStages + stage) * 2 * S::kTileBytes + S::kTileBytes;
       if (!inside) {
         const uint4* v = reinterpret_cast<const uint4*>(v_tile);
         for (int i = lane; i < S::kTileBytes / 16; i += 32) {
@@ -452,16 +482,15 @@ attend_kernel(const __grid_constant__ Params p) {
     t = next_tile(t + S::kKg);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    l_a += __shfl_xor_sync(~0u, l_a, d);
-    l_b += __shfl_xor_sync(~0u, l_b, d);
-  }
+  float l_a = sum[0], l_b = sum[2];
+  // from here on the maxima are those of the exponents
+  if (m_a != kNone) m_a *= p.scale2;
+  if (m_b != kNone) m_b *= p.scale2;
   asm volatile("cp.async.wait_group 0;" ::: "memory");
   __syncthreads();  // the ring becomes the exchange
 
   // Join the groups in order: the others leave theirs, group 0 adds.
-  float* ex = reinterpret_cast<float*>(smem);
+  float* ex = reinterpret_cast<float*>(smem + S::kQBytes);
   constexpr int kLeft = S::kLeft / 4;
   const int slot = rt * S::kDs + half;
   if (kg > 0) {
@@ -720,7 +749,9 @@ int w4g128_attend(const w4g128_attend_args* a, void* ws, size_t ws_bytes, void* 
   p.window = a->window; p.sinks = a->sinks;
   p.chunk = chunk_for(*a);
   p.splits = splits_for(*a, p.chunk);
-  p.scale2 = a->scale * 1.44269504088896340736f;
+  p.scale2 = a->scale == 0.f ? 1.f : std::fabs(a->scale) * 1.44269504088896340736f;
+  p.flip_q = a->scale < 0.f ? 0x80008000u : 0u;
+  p.keep_q = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
   auto* base = static_cast<uint8_t*>(ws);
   p.status = reinterpret_cast<unsigned long long*>(base);
   p.part = reinterpret_cast<float*>(base + kStatusBytes);
