@@ -1,13 +1,17 @@
 // The mixture-of-experts layer on packed int4-g128 experts (w4g128_moe), for
 // 1..16 rows: four programmatic dependent launches,
-//   route    logits of every (row, expert), and x in MMA operand order;
+//   route    one cluster of 8 CTAs: the logits of every (row, expert), the
+//            picks and weights of each row, the list of picked experts with the
+//            rows that each serves; the other CTAs put x in MMA operand order;
 //   expert 0 gate and up of the picked experts, silu(g) u -> activations;
 //   expert 1 down of the picked experts -> fp32 rows per (row, pick);
 //   combine  weighted sum over a row's picks, residual, bf16.
-// The bytes are the picked experts' weights, read once: the expert kernels
-// are grouped weight streams.  Which experts, and which rows each serves, is
-// known on the device only, so every CTA of an expert kernel derives the lists
-// itself from the M x E logits (top-k per row, one warp each).
+// The bytes are the picked experts' weights, read once: the expert kernels are
+// grouped weight streams.  One persistent kernel with grid barriers in place
+// of the last three launches measured slower (43.1 us against 38.9 us for one
+// row, 5120 x 1408, 8 of 64 experts): a cooperative launch starts 2.7 us after
+// the routing, and a barrier costs 2 us more than the slowest CTA, where the
+// next launch's CTAs are on the SMs with their first copies already.
 //
 // A unit is (picked expert, one or two tiles of 16 output columns), its depth
 // K = 128 G rows cut into G groups.  A CTA takes a contiguous range of units
@@ -54,19 +58,30 @@ constexpr size_t kStatusBytes = 256;
 constexpr uint32_t kBias16 = 0x64006400u;   // fp16 1024.0 twice
 constexpr uint32_t kBiasB16 = 0x43004300u;  // bf16 128.0 twice
 
+// Picked experts in rising order with the picks (row * top_k + place, places in
+// rising expert order) that each serves.
+struct Lists {
+  int experts;
+  uint16_t expert[kMaxPicks];     // of a picked expert
+  uint16_t first[kMaxPicks + 2];  // its first entry (one more; padded to whole words)
+  uint16_t pick[kMaxPicks];       // entries
+};
+static_assert(sizeof(Lists) % 4 == 0, "copied by words");
+
 struct Params {
   const uint16_t *x, *residual, *router;
   uint16_t* y;
   const uint8_t *gate_up, *down;
   int M, D, F, E, top_k, renormalize;
   unsigned* status;
-  float* logits;   // [M][E]
-  float* weights;  // [M][top_k], picks in rising expert order
-  uint8_t* xp;     // [M][D / 128][256]: x as scaled fp16 in operand order
-  float2* xs;      // [M][D / 128]: X, and the factor that undoes the scale
-  uint8_t* act;    // [M top_k][F / 128][256]: activations (bf16) in operand order
-  float* acts;     // [M top_k][F / 16]: sums of 16 activations
-  float* part;     // [M top_k][D]
+  unsigned* next;     // [2]: units handed out beyond the first ones, of each expert kernel
+  Lists* lists;
+  float* weights;     // [M][top_k], by pick
+  uint8_t* xp;        // [M][D / 128][256]: x as scaled fp16 in operand order
+  float2* xs;         // [M][D / 128]: X, and the factor that undoes the scale
+  uint8_t* act;       // [M top_k][F / 128][256]: activations (bf16) in operand order
+  float* acts;        // [M top_k][F / 16]: sums of 16 activations
+  float* part;        // [M top_k][D]
 };
 
 __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
@@ -77,57 +92,151 @@ __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v &
 // 16 s + 2c, 16 s + 2c + 1 | 16 s + 8 + 2c, + 1 for s = 2i, then for s = 2i + 1.
 
 // ---------------------------------------------------------------- route
-// One CTA per expert; a thread sums its 8-value pieces of the depth for every
-// row, then lanes and warps in a fixed order.
-template <int MT>
-__global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__ Params p) {
-  __shared__ float s_sum[kWarps][MT];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, e = blockIdx.x;
-  grid_dependency_wait();
-  grid_dependents_launch();
-  if (e == 0 && tid == 0) *reinterpret_cast<unsigned long long*>(p.status) = 0ull;
+constexpr int kRouteCtas = 8;  // of the cluster that routes
+constexpr int kRouteThreads = 512;
 
-  const uint4* w = reinterpret_cast<const uint4*>(p.router + static_cast<long long>(e) * p.D);
-  const uint4* x = reinterpret_cast<const uint4*>(p.x);
-  const int n = p.D / 8;
-  float sum[MT];
+// The cluster splits the depth: each CTA multiplies its slice for every row and
+// expert with the warp MMA (x rows by 8 experts; a lane's 16 bytes are operand
+// registers as they are, since x and the router agree on the order of the
+// depth), and leaves the sums with the CTA that finishes the row.
+struct RouteShared {
+  float sums[kRouteCtas * 2 * W4G128_MAX_EXPERTS];  // [slice][row / 8][expert], slices * E <= 8 * 512
+  // CTA 0: every row's picks
+  uint16_t chosen[kMaxPicks];
+  alignas(4) uint16_t rows[W4G128_MAX_EXPERTS];   // bit m: row m picked it
+  uint16_t index[W4G128_MAX_EXPERTS];             // its place among the picked
+};
+
+// Rising with the value; NaN below everything, and 0 is left for "taken".
+__device__ __forceinline__ uint32_t rank_of(float v) {
+  if (v != v) return 1u;
+  const uint32_t b = __float_as_uint(v + 0.f);  // -0 ranks as +0
+  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+// One warp: the picks of row m from the sums of its logits; experts i * 32 +
+// lane, i < PER.
+template <int PER>
+__device__ __forceinline__ void pick_row(const Params& p, int m, int slices, const RouteShared& s, uint16_t* chosen) {
+  const int lane = threadIdx.x & 31;
+  float v[PER];
+  uint32_t rank[PER];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) sum[m] = 0.f;
-  for (int i = tid; i < n; i += kThreads) {
-    const uint4 wv = __ldg(w + i);
-    const uint32_t ws[4] = {wv.x, wv.y, wv.z, wv.w};
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      if (m < p.M) {
-        const uint4 xv = __ldg(x + static_cast<long long>(m) * n + i);
-        const uint32_t xs[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          sum[m] = fmaf(low_f(xs[j]), low_f(ws[j]), sum[m]);
-          sum[m] = fmaf(high_f(xs[j]), high_f(ws[j]), sum[m]);
-        }
-      }
+  for (int i = 0; i < PER; ++i) {
+    const int e = i * 32 + lane;
+    rank[i] = 0u;
+    v[i] = 0.f;
+    if (e < p.E) {
+#pragma unroll 8
+      for (int j = 0; j < slices; ++j) v[i] += s.sums[(j * 2 + m / 8) * p.E + e];
+      rank[i] = rank_of(v[i]);
     }
   }
+  float all = 0.f, top = 0.f, mine = 0.f;  // mine: the exponential of this lane's pick
+  int my_expert = 0;
+  for (int j = 0; j < p.top_k; ++j) {
+    uint32_t best = 0u;
+    int at = 0;
+    float val = 0.f;
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+    for (int i = 0; i < PER; ++i) {
+      if (rank[i] > best) {
+        best = rank[i];
+        at = i * 32 + lane;
+        val = v[i];
+      }
+    }
+    const uint32_t win = __reduce_max_sync(~0u, best);
+    const int e = static_cast<int>(__reduce_min_sync(~0u, best == win ? static_cast<unsigned>(at) : ~0u));
+    val = __shfl_sync(~0u, val, e & 31);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum[m] += __shfl_xor_sync(~0u, sum[m], d);
-    if (lane == 0) s_sum[warp][m] = sum[m];
+    for (int i = 0; i < PER; ++i)
+      if (i * 32 + lane == e) rank[i] = 0u;
+    if (j == 0) {
+      top = val;
+      if (!p.renormalize) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i * 32 + lane < p.E) all += expf(v[i] - top);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
+      }
+    }
+    const float x = expf(val - top);
+    if (p.renormalize) all += x;  // the same in every lane, by falling logit
+    if (lane == j) {
+      mine = x;
+      my_expert = e;
+    }
+  }
+  int place = 0;  // by rising expert
+  for (int j = 0; j < p.top_k; ++j) place += __shfl_sync(~0u, my_expert, j) < my_expert;
+  if (lane < p.top_k) {
+    chosen[m * p.top_k + place] = static_cast<uint16_t>(my_expert);
+    p.weights[m * p.top_k + place] = mine / all;
+  }
+}
+
+// CTA 0: the lists from every row's picks.
+__device__ __forceinline__ void make_lists(const Params& p, RouteShared& s) {
+  const int tid = threadIdx.x, lane = tid & 31, picks = p.M * p.top_k;
+  for (int i = tid; i < picks; i += kRouteThreads) {
+    const int e = s.chosen[i];  // two experts' marks share a word
+    atomicOr(reinterpret_cast<unsigned*>(s.rows) + e / 2, (1u << (i / p.top_k)) << (e % 2 * 16));
   }
   __syncthreads();
-  if (tid < p.M) {
-    float t = 0.f;
+  if (tid < 32) {
+    int experts = 0, entries = 0;
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const unsigned rows = e < p.E ? s.rows[e] : 0u;
+      const unsigned any = __ballot_sync(~0u, rows != 0u);
+      if (any == 0u) continue;
+      int n = __popc(rows);
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) t += s_sum[j][tid];
-    p.logits[tid * p.E + e] = t;
+      for (int d = 1; d < 32; d <<= 1) {
+        const int t = __shfl_up_sync(~0u, n, d);
+        if (lane >= d) n += t;
+      }
+      if (rows) {
+        const int a = experts + __popc(any & ((1u << lane) - 1u));
+        const int first = entries + n - __popc(rows);
+        p.lists->expert[a] = static_cast<uint16_t>(e);
+        p.lists->first[a] = static_cast<uint16_t>(first);
+        s.index[e] = static_cast<uint16_t>(first);
+      }
+      experts += __popc(any);
+      entries += __shfl_sync(~0u, n, 31);
+    }
+    if (lane == 0) {
+      p.lists->experts = experts;
+      p.lists->first[experts] = static_cast<uint16_t>(entries);
+    }
   }
+  __syncthreads();
+  for (int i = tid; i < picks; i += kRouteThreads) {
+    const int e = s.chosen[i], m = i / p.top_k;
+    p.lists->pick[s.index[e] + __popc(s.rows[e] & ((1u << m) - 1u))] = static_cast<uint16_t>(i);
+  }
+}
 
-  // x in operand order: 16 lanes per (row, group); rows follow one another in
-  // whole groups.  The scale puts the group's largest magnitude in [2^14, 2^15).
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// x in operand order, by the CTAs behind the routing cluster: 16 lanes per
+// (row, group); rows follow one another in whole groups.  The scale puts the
+// group's largest magnitude in [2^14, 2^15).
+__device__ __forceinline__ void pack_x(const Params& p) {
+  const int lane = threadIdx.x & 31;
+  const int warp = (blockIdx.x - kRouteCtas) * (kRouteThreads / 32) + threadIdx.x / 32;
+  const int warps = (gridDim.x - kRouteCtas) * (kRouteThreads / 32);
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(p.x);
-  const int units = p.M * n;  // 16 bytes each, a multiple of 16
-  for (int u0 = (e * kWarps + warp) * 32; u0 < units; u0 += p.E * kThreads) {
+  const int units = p.M * (p.D / 8);  // 16 bytes each, a multiple of 16
+  for (int u0 = warp * 32; u0 < units; u0 += warps * 32) {
     const int u = u0 + lane;
     const bool real = u < units;  // (all 16 lanes of a group or none)
     const int group = u / 16, i = u / 4 % 4, c = u % 4;
@@ -165,129 +274,90 @@ __global__ void __launch_bounds__(kThreads) route_kernel(const __grid_constant__
   }
 }
 
-// ---------------------------------------------------------------- the lists
-// Picked experts in rising order with the picks (row * top_k + place, places in
-// rising expert order) that each serves.
-struct Lists {
-  uint16_t expert[kMaxPicks];      // of a picked expert
-  uint16_t first[kMaxPicks + 1];   // its first entry
-  uint16_t pick[kMaxPicks];        // entries
-  float weight[kMaxPicks];         // by pick
-  int experts;
-  // scratch
-  uint16_t chosen[kMaxPicks];      // by pick: the expert
-  alignas(4) uint16_t rows[W4G128_MAX_EXPERTS];  // bit m: row m picked it
-  uint16_t index[W4G128_MAX_EXPERTS];  // its place among the picked
-};
-
-// Rising with the value; NaN below everything, and 0 is left for "taken".
-__device__ __forceinline__ uint32_t rank_of(float v) {
-  if (v != v) return 1u;
-  const uint32_t b = __float_as_uint(v + 0.f);  // -0 ranks as +0
-  return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ void make_lists(const Params& p, Lists& s) {
+// WIDE: more than 8 rows.
+template <bool WIDE>
+__global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThreads)
+route_kernel(const __grid_constant__ Params p) {
+  __shared__ RouteShared s;
+  constexpr int kRouteWarps = kRouteThreads / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int kPer = W4G128_MAX_EXPERTS / 32;
-  for (int e = tid; e < p.E; e += kThreads) s.rows[e] = 0;
-  __syncthreads();
-  for (int m = warp; m < p.M; m += kWarps) {
-    float v[kPer];
-    uint32_t rank[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = i * 32 + lane;
-      rank[i] = 0u;
-      if (i * 32 >= p.E) continue;  // (for every lane)
-      if (e < p.E) {
-        v[i] = __ldcg(p.logits + m * p.E + e);
-        rank[i] = rank_of(v[i]);
-      }
+  cluster_arrive_relaxed();  // every CTA of the cluster runs before any writes into another
+  if (blockIdx.x >= kRouteCtas) {
+    grid_dependency_wait();
+    grid_dependents_launch();
+    pack_x(p);
+    cluster_wait_acquire();
+    return;
+  }
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int r = lane >> 2, c = lane & 3;
+  // tiles of 8 experts; where there are few, up to 4 warps share one and split its depth
+  const int tiles = (p.E + 7) / 8;
+  const int sub = tiles * 4 <= kRouteWarps ? 4 : tiles * 2 <= kRouteWarps ? 2 : 1;
+  const int slices = kRouteCtas * sub, slice = rank * sub + warp % sub;
+  const int steps = p.D / 32, k0 = steps * slice / slices, k1 = steps * (slice + 1) / slices;
+  // the router does not depend on the kernels before: into the L2 while they finish
+  for (int t = warp / sub; t < tiles; t += kRouteWarps / sub) {
+    const char* w = reinterpret_cast<const char*>(p.router + static_cast<long long>(min(t * 8 + lane % 8, p.E - 1)) * p.D);
+    for (int at = k0 * 64 + lane / 8 * 128; at < k1 * 64; at += 512)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(w + at));
+  }
+  grid_dependency_wait();
+  grid_dependents_launch();
+  if (rank == 0) {
+    if (tid == 0) {
+      *reinterpret_cast<unsigned long long*>(p.status) = 0ull;
+      p.next[0] = p.next[1] = 0u;
     }
-    float all = 0.f, top = 0.f, mine = 0.f;  // mine: this lane's pick's exponential
-    int my_expert = 0;
-    for (int j = 0; j < p.top_k; ++j) {
-      uint32_t best = 0u;
-      int at = 0;
-      float val = 0.f;
+    for (int e = tid; e < W4G128_MAX_EXPERTS / 2; e += kRouteThreads) reinterpret_cast<uint32_t*>(s.rows)[e] = 0u;
+  }
+  const uint4* xa = reinterpret_cast<const uint4*>(p.x + static_cast<long long>(min(r, p.M - 1)) * p.D) + c;
+  const uint4* xb = reinterpret_cast<const uint4*>(p.x + static_cast<long long>(min(r + 8, p.M - 1)) * p.D) + c;
+  bool waited = false;
+  for (int t = warp / sub; t < tiles; t += kRouteWarps / sub) {
+    // rows and experts beyond the last repeat it; nothing of theirs is kept
+    const uint4* w = reinterpret_cast<const uint4*>(p.router + static_cast<long long>(min(t * 8 + r, p.E - 1)) * p.D) + c;
+    float d[4] = {};
+    constexpr int kBatch = WIDE ? 5 : 8;  // steps in flight
+    for (int k = k0; k < k1; k += kBatch) {
+      uint4 a[kBatch], b[kBatch], v[kBatch];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i * 32 >= p.E) break;
-        if (rank[i] > best) {
-          best = rank[i];
-          at = i * 32 + lane;
-          val = v[i];
+      for (int i = 0; i < kBatch; ++i) {
+        if (k + i < k1) {
+          v[i] = __ldg(w + (k + i) * 4);
+          a[i] = __ldg(xa + (k + i) * 4);
+          b[i] = WIDE ? __ldg(xb + (k + i) * 4) : make_uint4(0, 0, 0, 0);
         }
       }
-      const uint32_t win = __reduce_max_sync(~0u, best);
-      const int e = static_cast<int>(__reduce_min_sync(~0u, best == win ? static_cast<unsigned>(at) : ~0u));
-      val = __shfl_sync(~0u, val, e & 31);
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i * 32 >= p.E) break;
-        if (i * 32 + lane == e) rank[i] = 0u;
-      }
-      if (j == 0) {
-        top = val;
-        if (!p.renormalize) {
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            if (i * 32 + lane < p.E) all += expf(v[i] - top);
-#pragma unroll
-          for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(~0u, all, d);
+      for (int i = 0; i < kBatch; ++i) {
+        if (k + i < k1) {
+          mma_bf16(d, a[i].x, b[i].x, a[i].y, b[i].y, v[i].x, v[i].y);
+          mma_bf16(d, a[i].z, b[i].z, a[i].w, b[i].w, v[i].z, v[i].w);
         }
       }
-      const float x = expf(val - top);
-      if (p.renormalize) all += x;  // the same in every lane, by falling logit
-      if (lane == j) {
-        mine = x;
-        my_expert = e;
-      }
     }
-    // places by rising expert
-    int place = 0;
-    for (int j = 0; j < p.top_k; ++j) place += __shfl_sync(~0u, my_expert, j) < my_expert;
-    if (lane < p.top_k) {
-      s.chosen[m * p.top_k + place] = static_cast<uint16_t>(my_expert);
-      s.weight[m * p.top_k + place] = mine / all;
-      // two rows' marks share a word
-      atomicOr(reinterpret_cast<unsigned*>(s.rows) + my_expert / 2, (1u << m) << (my_expert % 2 * 16));
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int experts = 0, picks = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const unsigned rows = e < p.E ? s.rows[e] : 0u;
-      const unsigned any = __ballot_sync(~0u, rows != 0u);
-      int n = __popc(rows);
+    if (!waited) cluster_wait_acquire();
+    waited = true;
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int t = __shfl_up_sync(~0u, n, d);
-        if (lane >= d) n += t;
-      }
-      if (rows) {
-        const int a = experts + __popc(any & ((1u << lane) - 1u));
-        s.expert[a] = static_cast<uint16_t>(e);
-        s.index[e] = static_cast<uint16_t>(a);
-        s.first[a] = static_cast<uint16_t>(picks + n - __popc(rows));
-      }
-      experts += __popc(any);
-      picks += __shfl_sync(~0u, n, 31);
-    }
-    if (lane == 0) {
-      s.experts = experts;
-      s.first[experts] = static_cast<uint16_t>(picks);
+    for (int i = 0; i < 4; ++i) {
+      const int m = r + 8 * (i >> 1), e = t * 8 + 2 * c + (i & 1);
+      if (m < p.M && e < p.E)
+        *static_cast<float*>(__cluster_map_shared_rank(&s.sums[(slice * 2 + (m >> 3)) * p.E + e], m & 7)) = d[i];
     }
   }
-  __syncthreads();
-  for (int i = tid; i < p.M * p.top_k; i += kThreads) {
-    const int e = s.chosen[i], m = i / p.top_k;
-    s.pick[s.first[s.index[e]] + __popc(s.rows[e] & ((1u << m) - 1u))] = static_cast<uint16_t>(i);
+  if (!waited) cluster_wait_acquire();
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  const int m = rank + 8 * warp;  // two warps, a row each
+  if (warp < 2 && m < p.M) {
+    uint16_t* chosen = static_cast<uint16_t*>(__cluster_map_shared_rank(s.chosen, 0));
+    if (p.E <= 128) pick_row<4>(p, m, slices, s, chosen);
+    else pick_row<W4G128_MAX_EXPERTS / 32>(p, m, slices, s, chosen);
   }
-  __syncthreads();
+  cluster_arrive_release();
+  cluster_wait_acquire();
+  if (rank == 0) make_lists(p, s);
 }
 
 // ---------------------------------------------------------------- expert streams
@@ -322,11 +392,11 @@ __device__ __forceinline__ void operand(uint32_t w, uint32_t (&a)[4]) {
 }
 
 constexpr int kTiles = 2;  // of 16 columns, per item
+constexpr int kStages = 3;  // items of a warp on their way
 constexpr int kStage = kTiles * kBlockBytes;
 constexpr int kCols = kTiles * kTileN;
 template <int NT>  // 8-row B tiles
 struct Stream {
-  static constexpr int kStages = NT == 1 ? 5 : 4;
   static constexpr int kRing = kWarps * kStages * kStage;
   static constexpr int kPart = NT * 8 * kCols;  // floats that a warp leaves of a unit: [row][column]
   static constexpr int kBytes = kRing + 2 * kWarps * kPart * 4;
@@ -349,34 +419,45 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   constexpr bool kBf16 = PHASE == 1;
   constexpr int kTeams = kWarps / TEAM;
   constexpr int kMine = kParts / TEAM;  // parts of a unit that one warp sums
+  constexpr int kQueue = 8;             // units of a team that are known: the current one and the next
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Lists lists;
+  __shared__ int s_unit[kTeams][kQueue];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // (uniform, and known to be)
   const int team = warp / TEAM, member = warp % TEAM;
 
-  // The logits: of the preceding kernel (phase 0), or of the one before, which
+  // The lists: of the preceding kernel (phase 0), or of the one before, which
   // had completed when the preceding one let this one launch (phase 1).
   if (PHASE == 0) {
     grid_dependency_wait();
     grid_dependents_launch();
   }
-  make_lists(p, lists);
-  if (PHASE == 0 && blockIdx.x == 0)
-    for (int i = tid; i < p.M * p.top_k; i += kThreads) p.weights[i] = lists.weight[i];
+  for (int i = tid; i < static_cast<int>(sizeof(Lists) / 4); i += kThreads)
+    reinterpret_cast<uint32_t*>(&lists)[i] = __ldcg(reinterpret_cast<const uint32_t*>(p.lists) + i);
 
   const int K = PHASE == 0 ? p.D : p.F;
   const int G = K / kGroup;
+  // A team's units: share, share + shares, .. at first, so that the teams work
+  // side by side; then whatever is next (the counter), because SMs differ in
+  // how fast they stream (by a third, measured with 18 units a team).  A unit is drawn `lead`
+  // units before it is worked on, so that the copies can run ahead of it;
+  // where a warp may find no item in a unit, all units are handed out evenly.
+  const int share = blockIdx.x + gridDim.x * team, shares = gridDim.x * kTeams;
+  const int fewest = max(G / kParts * kMine, 1);  // items of a warp in a unit
+  const int lead = 1 + (kStages + 1 + fewest - 1) / fewest;
+  const bool drawn = G >= kParts && lead < kQueue;
+  static_assert(kStages + 2 < kQueue, "the longest lead fits the queue");
+  if (member == 0 && lane < kQueue) s_unit[team][lane] = share + lane * shares;
+  __syncthreads();
   const int per = PHASE == 0 ? p.F / kTileN : p.D / kCols;  // units of an expert
   const int units = lists.experts * per;
-  const int share = blockIdx.x * kTeams + team, shares = gridDim.x * kTeams;
-  const int u0 = static_cast<int>(static_cast<long long>(units) * share / shares);
-  const int nu = static_cast<int>(static_cast<long long>(units) * (share + 1) / shares) - u0;
+  auto unit_at = [&](int n) { return drawn ? s_unit[team][n % kQueue] : share + n * shares; };
   const uint8_t* weights = PHASE == 0 ? p.gate_up : p.down;
   const long long quad_bytes = static_cast<long long>(G) * kQuadBytes;
   const long long expert_bytes = (PHASE == 0 ? p.F / 32 : p.D / 64) * quad_bytes;
-  const uint32_t ring = smem_addr(smem) + warp * S::kStages * kStage;
-  const uint8_t* ring_ptr = smem + warp * S::kStages * kStage;
+  const uint32_t ring = smem_addr(smem) + warp * kStages * kStage;
+  const uint8_t* ring_ptr = smem + warp * kStages * kStage;
 
   // A warp's items: in each unit of its team the groups of its parts, part by
   // part in the order in which they are added.  The members take turns from
@@ -384,37 +465,37 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   auto turn = [&](int u) { return static_cast<int>(static_cast<unsigned>(member - u * G) % TEAM); };
   auto part_at = [](int m, int i) { return m + 4 * (i & 1) + 2 * (i >> 1); };
 
-  // The copies run kStages items ahead.
-  int c_unit = 0, c_turn = turn(0), c_i = 0, c_group = c_turn;
-  int c_expert = u0 / per, c_at = u0 % per;
+  // The copies run kStages items ahead: the unit's number in the team's order,
+  // the part's and the group, and this lane's 16 bytes in group 0 of its tiles.
+  int c_n = 0, c_turn = turn(0), c_i = 0, c_group = c_turn;
+  bool c_more = unit_at(0) < units;
   const uint8_t *c_src = nullptr, *c_src2 = nullptr;
-  auto place = [&] {  // this lane's 16 bytes in group 0 of the unit's tiles
-    const uint8_t* base = weights + lists.expert[c_expert] * expert_bytes + 16 * lane;
+  auto place = [&] {
+    const int u = unit_at(c_n), at = u % per;
+    const uint8_t* base = weights + lists.expert[u / per] * expert_bytes + 16 * lane;
     if (PHASE == 0) {
-      const int t2 = c_at + per;
-      c_src = base + (c_at / kQuadTiles) * quad_bytes + (c_at % kQuadTiles) * kBlockBytes;
+      const int t2 = at + per;
+      c_src = base + (at / kQuadTiles) * quad_bytes + (at % kQuadTiles) * kBlockBytes;
       c_src2 = base + (t2 / kQuadTiles) * quad_bytes + (t2 % kQuadTiles) * kBlockBytes;
     } else {
-      c_src = base + (c_at / 2) * quad_bytes + (c_at % 2) * kStage;
+      c_src = base + (at / 2) * quad_bytes + (at % 2) * kStage;
     }
   };
   auto settle = [&] {  // to the warp's next item, once c_group is past the depth
-    while (c_group >= G && c_unit < nu) {
+    while (c_group >= G && c_more) {
       if (++c_i == kMine) {
         c_i = 0;
-        if (++c_unit == nu) return;
-        if (++c_at == per) {
-          c_at = 0;
-          ++c_expert;
-        }
-        c_turn = turn(c_unit);
+        ++c_n;
+        c_more = unit_at(c_n) < units;
+        if (!c_more) return;
+        c_turn = turn(c_n);
         place();
       }
       c_group = part_at(c_turn, c_i);
     }
   };
   auto copy = [&](int stage) {
-    if (c_unit < nu) {
+    if (c_more) {
       const uint32_t dst = ring + stage * kStage + 16 * lane;
       const int off = c_group * kQuadBytes;
       if (PHASE == 0) {
@@ -435,12 +516,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (nu > 0) {
+  if (c_more) {
     place();
     settle();
   }
 #pragma unroll 1
-  for (int i = 0; i < S::kStages; ++i) copy(i);
+  for (int i = 0; i < kStages; ++i) copy(i);
   if (PHASE == 1) {
     grid_dependency_wait();  // the weights are on their way while the activations are finished
     grid_dependents_launch();
@@ -448,7 +529,6 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 
   const int r = lane >> 2, c = lane & 3;
   int stage = 0;
-  int at = u0 % per, a = u0 / per;
   int first = 0, count = 0;
   Rows<NT> rows = {};
   float* parts = reinterpret_cast<float*>(smem + S::kRing) + team * 2 * TEAM * S::kPart;  // two halves that take turns
@@ -473,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
         }
       }
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
     __syncwarp();
     const uint8_t* st = ring_ptr + stage * kStage;
     float d[kTiles][NA][4] = {};
@@ -500,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     for (int t = 0; t < kTiles; ++t) meta[t] = *reinterpret_cast<const uint2*>(st + t * kBlockBytes + kCodeBytes + 8 * r);
     __syncwarp();  // the stage is read out
     copy(stage);
-    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    stage = stage + 1 == kStages ? 0 : stage + 1;
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       float s0 = low_f(meta[t].x), s1 = low_f(meta[t].y);
@@ -521,7 +601,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   using Two = std::integral_constant<int, 2>;
 
   int expert_seen = -1;
-  for (int u = 0; u < nu; ++u) {
+  for (int u = 0;; ++u) {
+    const int unit = unit_at(u);
+    if (unit >= units) break;
+    const int a = unit / per, at = unit % per;
+    int draw = 0;
+    if (drawn && member == 0 && lane == 0 && u + lead >= kQueue) draw = static_cast<int>(atomicAdd(p.next + PHASE, 1u));
     if (a != expert_seen) {
       expert_seen = a;
       first = lists.first[a];
@@ -572,10 +657,12 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
           const int m = n * 8 + 2 * c + (i & 1);
           if (m < count) out[m * kCols + t * kTileN + r + 8 * (i >> 1)] = sum[t][n][i];
         }
-    // One barrier of the team per unit: the other half of the buffer is free
-    // again once every member is past the next one.
-    if constexpr (TEAM == kWarps) __syncthreads();
-    else asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
+    // One barrier of the team per unit: the other half of the buffer, and the
+    // drawn unit's place in the queue, are free again once every member is past
+    // the next one.
+    if (drawn && member == 0 && lane == 0 && u + lead >= kQueue)
+      s_unit[team][(u + lead) % kQueue] = kQueue * shares + draw;
+    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
     const int tt = member * 32 + lane;
     auto join = [&](const float* q) {  // (parts beyond the depth are 0)
       if constexpr (TEAM == 2) return q[0] + q[S::kPart];
@@ -609,10 +696,6 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
         p.part[static_cast<long long>(lists.pick[first + m]) * p.D + at * kCols + col] = join(part + m * kCols + col);
       }
     }
-    if (++at == per) {
-      at = 0;
-      ++a;
-    }
   }
 }
 
@@ -622,6 +705,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
   const int m = blockIdx.y, i = blockIdx.x * 128 + threadIdx.x;  // 4 columns
   if (i >= p.D / 4) return;
   float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
   for (int j = 0; j < p.top_k; ++j) {
     const float w = p.weights[m * p.top_k + j];
     const float4 v = reinterpret_cast<const float4*>(p.part + static_cast<long long>(m * p.top_k + j) * p.D)[i];
@@ -639,7 +723,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
     s.w += high_f(r.y);
   }
   const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
-  *reinterpret_cast<uint2*>(p.y + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  *reinterpret_cast<uint2*>(p.y + at) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 int check(const w4g128_moe_args* a) {
@@ -658,14 +743,14 @@ int check(const w4g128_moe_args* a) {
 }
 
 struct Layout {
-  size_t logits, weights, xp, xs, act, acts, part, total;
+  size_t lists, weights, xp, xs, act, acts, part, total;
 };
 Layout layout(const w4g128_moe_args& a) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
   const size_t M = a.M, picks = M * a.top_k;
   Layout l;
-  l.logits = kStatusBytes;
-  l.weights = l.logits + up(M * a.E * 4);
+  l.lists = kStatusBytes;
+  l.weights = l.lists + up(sizeof(Lists));
   l.xp = l.weights + up(picks * 4);
   l.xs = l.xp + up(M * a.D * 2);
   l.act = l.xs + up(M * (a.D / 128) * 8);
@@ -693,7 +778,7 @@ cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
   const cudaError_t e = launch_expert<0, NT, 8>(cfg, p, sms, most * (p.F / kTileN));
   if (e != cudaSuccess) return e;
   const long long units = most * (p.D / kCols);
-  // small teams where every team has several units
+  // small teams where every team then has several units
   return units >= 16 * sms ? launch_expert<1, NT, 2>(cfg, p, sms, units) : launch_expert<1, NT, 8>(cfg, p, sms, units);
 }
 
@@ -709,11 +794,9 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(p.E);
-  cfg.blockDim = dim3(kThreads);
-  if (p.M == 1) e = cudaLaunchKernelEx(&cfg, route_kernel<1>, p);
-  else if (p.M <= 4) e = cudaLaunchKernelEx(&cfg, route_kernel<4>, p);
-  else e = cudaLaunchKernelEx(&cfg, route_kernel<16>, p);
+  cfg.gridDim = dim3(kRouteCtas * (1 + (p.M * (p.D / 8) + kRouteCtas * kRouteThreads - 1) / (kRouteCtas * kRouteThreads)));
+  cfg.blockDim = dim3(kRouteThreads);
+  e = p.M <= 8 ? cudaLaunchKernelEx(&cfg, route_kernel<false>, p) : cudaLaunchKernelEx(&cfg, route_kernel<true>, p);
   if (e != cudaSuccess) return e;
   e = p.M <= 8 ? launch_experts<1>(cfg, p, sms) : launch_experts<2>(cfg, p, sms);
   if (e != cudaSuccess) return e;
@@ -750,7 +833,8 @@ int w4g128_moe(const w4g128_moe_args* a, void* ws, size_t ws_bytes, void* stream
   p.down = static_cast<const uint8_t*>(a->down);
   p.M = a->M; p.D = a->D; p.F = a->F; p.E = a->E; p.top_k = a->top_k; p.renormalize = a->renormalize;
   p.status = reinterpret_cast<unsigned*>(base);
-  p.logits = reinterpret_cast<float*>(base + l.logits);
+  p.next = reinterpret_cast<unsigned*>(base + 16);
+  p.lists = reinterpret_cast<Lists*>(base + l.lists);
   p.weights = reinterpret_cast<float*>(base + l.weights);
   p.xp = base + l.xp;
   p.xs = reinterpret_cast<float2*>(base + l.xs);
