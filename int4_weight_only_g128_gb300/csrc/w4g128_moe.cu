@@ -13,12 +13,12 @@
 // the routing, and a barrier costs 2 us more than the slowest CTA, where the
 // next launch's CTAs are on the SMs with their first copies already.
 //
-// A unit is (picked expert, one or two tiles of 16 output columns), its depth
-// K = 128 G rows cut into G groups.  A CTA takes a contiguous range of units
-// and its 8 warps take the range's (unit, group) items in turn, each through
-// its own ring of bulk copies (two 1088-byte blocks per stage: a gate and an
-// up block, or two neighbours of the down projection).  The item's product is
-// one warp MMA per packed word: the 16 columns are the A operand, the rows
+// A unit is (picked expert, 2 or 4 tiles of 16 output columns), its depth K =
+// 128 G rows cut into G groups.  A team of 2, 4 or 8 warps works on a unit and
+// takes its (unit, group) items in turn, each warp through a ring of its own
+// filled by cp.async (bulk copies cost a fence and some forty instructions of
+// one lane per item: 409 instructions an item against 265).  The item's product
+// is one warp MMA per packed word: the 16 columns are the A operand, the rows
 // that picked the expert the B columns.
 //   gate and up: x as fp16, each (row, group) scaled by a power of two (exact
 //     within 2^29 of the group's largest value), weights as fp16 1024 + q and
@@ -59,12 +59,14 @@ constexpr uint32_t kBias16 = 0x64006400u;   // fp16 1024.0 twice
 constexpr uint32_t kBiasB16 = 0x43004300u;  // bf16 128.0 twice
 
 // Picked experts in rising order with the picks (row * top_k + place, places in
-// rising expert order) that each serves.
+// rising expert order) that each serves: one entry for up to 8 rows, what an
+// MMA has B columns for.  An expert of more rows has two entries; its weights
+// are then dequantised twice, and read twice, side by side, from the L2.
 struct Lists {
-  int experts;
-  uint16_t expert[kMaxPicks];     // of a picked expert
-  uint16_t first[kMaxPicks + 2];  // its first entry (one more; padded to whole words)
-  uint16_t pick[kMaxPicks];       // entries
+  int entries;
+  uint16_t expert[kMaxPicks];
+  uint16_t first[kMaxPicks + 2];  // an entry's first pick (one more; padded to whole words)
+  uint16_t pick[kMaxPicks];
 };
 static_assert(sizeof(Lists) % 4 == 0, "copied by words");
 
@@ -186,31 +188,39 @@ __device__ __forceinline__ void make_lists(const Params& p, RouteShared& s) {
   }
   __syncthreads();
   if (tid < 32) {
-    int experts = 0, entries = 0;
+    int entries = 0, before = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int e = e0 + lane;
       const unsigned rows = e < p.E ? s.rows[e] : 0u;
       const unsigned any = __ballot_sync(~0u, rows != 0u);
       if (any == 0u) continue;
-      int n = __popc(rows);
+      // picks below, and experts' second entries above bit 16
+      const int own = __popc(rows), mine = own + (own > 8 ? 1 << 16 : 0);
+      int n = mine;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const int t = __shfl_up_sync(~0u, n, d);
         if (lane >= d) n += t;
       }
+      const int all = __shfl_sync(~0u, n, 31);
+      n -= mine;
       if (rows) {
-        const int a = experts + __popc(any & ((1u << lane) - 1u));
-        const int first = entries + n - __popc(rows);
+        const int a = entries + __popc(any & ((1u << lane) - 1u)) + (n >> 16);
+        const int first = before + (n & 0xFFFF);
         p.lists->expert[a] = static_cast<uint16_t>(e);
         p.lists->first[a] = static_cast<uint16_t>(first);
         s.index[e] = static_cast<uint16_t>(first);
+        if (own > 8) {
+          p.lists->expert[a + 1] = static_cast<uint16_t>(e);
+          p.lists->first[a + 1] = static_cast<uint16_t>(first + 8);
+        }
       }
-      experts += __popc(any);
-      entries += __shfl_sync(~0u, n, 31);
+      entries += __popc(any) + (all >> 16);
+      before += all & 0xFFFF;
     }
     if (lane == 0) {
-      p.lists->experts = experts;
-      p.lists->first[experts] = static_cast<uint16_t>(entries);
+      p.lists->entries = entries;
+      p.lists->first[entries] = static_cast<uint16_t>(before);
     }
   }
   __syncthreads();
@@ -391,38 +401,32 @@ __device__ __forceinline__ void operand(uint32_t w, uint32_t (&a)[4]) {
   }
 }
 
-constexpr int kTiles = 2;  // of 16 columns, per item
-constexpr int kStages = 3;  // items of a warp on their way
-constexpr int kStage = kTiles * kBlockBytes;
-constexpr int kCols = kTiles * kTileN;
-template <int NT>  // 8-row B tiles
+// TILES of 16 columns per item: 2, or 4 where there are units enough for every
+// team to have several (half the loads of x and half the work per unit).
+template <int TILES>
 struct Stream {
+  static constexpr int kStage = TILES * kBlockBytes;
+  static constexpr int kStages = TILES == 2 ? 3 : 2;  // items of a warp on their way
   static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kPart = NT * 8 * kCols;  // floats that a warp leaves of a unit: [row][column]
+  static constexpr int kCols = TILES * kTileN;
+  static constexpr int kPart = 8 * kCols;  // floats that a warp leaves of a unit: [row][column]
   static constexpr int kBytes = kRing + 2 * kWarps * kPart * 4;
 };
 
-// A picked expert's rows, from one lane's point of view: its B row (r of each
-// 8-row tile) in operand order, and where the sums of rows 2c, 2c + 1 are.
-// Columns beyond the count repeat the last row; nothing of theirs is kept.
-template <int NT>
-struct Rows {
-  const uint8_t* x[NT];
-  const float* sums[NT][2];
-};
-
-// PHASE 0: gate and up, a unit is a gate tile and its up tile; 1: down, a unit
-// is two neighbouring tiles.  TEAM: warps that share a unit.
-template <int PHASE, int NT, int TEAM>
+// PHASE 0: gate and up, a unit is TILES / 2 gate tiles and their up tiles; 1:
+// down, a unit is TILES neighbouring tiles.  TEAM: warps that share a unit.
+template <int PHASE, int TILES, int TEAM>
 __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_constant__ Params p) {
-  using S = Stream<NT>;
+  using S = Stream<TILES>;
   constexpr bool kBf16 = PHASE == 1;
+  constexpr int kSide = PHASE == 0 ? TILES / 2 : TILES;  // neighbouring tiles
   constexpr int kTeams = kWarps / TEAM;
   constexpr int kMine = kParts / TEAM;  // parts of a unit that one warp sums
   constexpr int kQueue = 8;             // units of a team that are known: the current one and the next
+  constexpr uint32_t kEnd = ~0u;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Lists lists;
-  __shared__ int s_unit[kTeams][kQueue];
+  __shared__ uint32_t s_unit[kTeams][kQueue];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // (uniform, and known to be)
   const int team = warp / TEAM, member = warp % TEAM;
@@ -440,24 +444,28 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   const int G = K / kGroup;
   // A team's units: share, share + shares, .. at first, so that the teams work
   // side by side; then whatever is next (the counter), because SMs differ in
-  // how fast they stream (by a third, measured with 18 units a team).  A unit is drawn `lead`
-  // units before it is worked on, so that the copies can run ahead of it;
-  // where a warp may find no item in a unit, all units are handed out evenly.
+  // how fast they stream (by a third, measured).  A unit is drawn `lead` units
+  // before it is worked on, so that the copies can run ahead of it; where a
+  // warp may find no item in a unit, all units are handed out evenly.
   const int share = blockIdx.x + gridDim.x * team, shares = gridDim.x * kTeams;
   const int fewest = max(G / kParts * kMine, 1);  // items of a warp in a unit
-  const int lead = 1 + (kStages + 1 + fewest - 1) / fewest;
+  const int lead = 1 + (S::kStages + fewest) / fewest;
   const bool drawn = G >= kParts && lead < kQueue;
-  static_assert(kStages + 2 < kQueue, "the longest lead fits the queue");
-  if (member == 0 && lane < kQueue) s_unit[team][lane] = share + lane * shares;
+  static_assert(S::kStages + 2 < kQueue, "the longest lead fits the queue");
+  const int per = (PHASE == 0 ? p.F : p.D) / (kSide * kTileN);  // units of an entry
   __syncthreads();
-  const int per = PHASE == 0 ? p.F / kTileN : p.D / kCols;  // units of an expert
-  const int units = lists.experts * per;
-  auto unit_at = [&](int n) { return drawn ? s_unit[team][n % kQueue] : share + n * shares; };
+  const int units = lists.entries * per;
+  auto locate = [&](int u) -> uint32_t {  // entry and place, or the end
+    return u < units ? static_cast<uint32_t>(u / per) << 16 | static_cast<uint32_t>(u % per) : kEnd;
+  };
+  if (member == 0 && lane < kQueue) s_unit[team][lane] = locate(share + lane * shares);
+  __syncthreads();
+  auto unit_at = [&](int n) { return drawn ? s_unit[team][n % kQueue] : locate(share + n * shares); };
   const uint8_t* weights = PHASE == 0 ? p.gate_up : p.down;
   const long long quad_bytes = static_cast<long long>(G) * kQuadBytes;
   const long long expert_bytes = (PHASE == 0 ? p.F / 32 : p.D / 64) * quad_bytes;
-  const uint32_t ring = smem_addr(smem) + warp * kStages * kStage;
-  const uint8_t* ring_ptr = smem + warp * kStages * kStage;
+  const uint32_t ring = smem_addr(smem) + warp * S::kStages * S::kStage;
+  const uint8_t* ring_ptr = smem + warp * S::kStages * S::kStage;
 
   // A warp's items: in each unit of its team the groups of its parts, part by
   // part in the order in which they are added.  The members take turns from
@@ -468,26 +476,23 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   // The copies run kStages items ahead: the unit's number in the team's order,
   // the part's and the group, and this lane's 16 bytes in group 0 of its tiles.
   int c_n = 0, c_turn = turn(0), c_i = 0, c_group = c_turn;
-  bool c_more = unit_at(0) < units;
+  uint32_t c_unit = unit_at(0);
   const uint8_t *c_src = nullptr, *c_src2 = nullptr;
   auto place = [&] {
-    const int u = unit_at(c_n), at = u % per;
-    const uint8_t* base = weights + lists.expert[u / per] * expert_bytes + 16 * lane;
+    const int t = static_cast<int>(c_unit & 0xFFFFu) * kSide;
+    const uint8_t* base = weights + lists.expert[c_unit >> 16] * expert_bytes + 16 * lane;
+    c_src = base + (t / kQuadTiles) * quad_bytes + (t % kQuadTiles) * kBlockBytes;
     if (PHASE == 0) {
-      const int t2 = at + per;
-      c_src = base + (at / kQuadTiles) * quad_bytes + (at % kQuadTiles) * kBlockBytes;
+      const int t2 = t + p.F / kTileN;
       c_src2 = base + (t2 / kQuadTiles) * quad_bytes + (t2 % kQuadTiles) * kBlockBytes;
-    } else {
-      c_src = base + (at / 2) * quad_bytes + (at % 2) * kStage;
     }
   };
   auto settle = [&] {  // to the warp's next item, once c_group is past the depth
-    while (c_group >= G && c_more) {
+    while (c_group >= G && c_unit != kEnd) {
       if (++c_i == kMine) {
         c_i = 0;
-        ++c_n;
-        c_more = unit_at(c_n) < units;
-        if (!c_more) return;
+        c_unit = unit_at(++c_n);
+        if (c_unit == kEnd) return;
         c_turn = turn(c_n);
         place();
       }
@@ -495,33 +500,29 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     }
   };
   auto copy = [&](int stage) {
-    if (c_more) {
-      const uint32_t dst = ring + stage * kStage + 16 * lane;
+    if (c_unit != kEnd) {
+      const uint32_t dst = ring + stage * S::kStage + 16 * lane;
       const int off = c_group * kQuadBytes;
-      if (PHASE == 0) {
-        cp_async16(dst, c_src + off);
-        cp_async16(dst + 512, c_src + off + 512);
-        cp_async16(dst + kBlockBytes, c_src2 + off);
-        cp_async16(dst + kBlockBytes + 512, c_src2 + off + 512);
-        // the 64 bytes of scales and minima behind each: 4 + 4 lanes
-        if (lane < 4) cp_async16(dst + 1024, c_src + off + 1024);
-        else if (lane < 8) cp_async16(dst + kBlockBytes + 1024 - 64, c_src2 + off + 1024 - 64);
-      } else {
+      constexpr int kRun = kSide * kBlockBytes;  // contiguous bytes
 #pragma unroll
-        for (int i = 0; i < 4; ++i) cp_async16(dst + 512 * i, c_src + off + 512 * i);
-        if (lane < (kStage - 2048) / 16) cp_async16(dst + 2048, c_src + off + 2048);
+      for (int i = 0; i < kRun / 512; ++i) {
+        cp_async16(dst + 512 * i, c_src + off + 512 * i);
+        if (PHASE == 0) cp_async16(dst + kRun + 512 * i, c_src2 + off + 512 * i);
       }
+      constexpr int kRest = kRun % 512, kAt = kRun - kRest;  // a few lanes more, for each side
+      if (lane < kRest / 16) cp_async16(dst + kAt, c_src + off + kAt);
+      if (PHASE == 0 && lane < kRest / 16) cp_async16(dst + kRun + kAt, c_src2 + off + kAt);
       c_group += kParts;
       settle();
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  if (c_more) {
+  if (c_unit != kEnd) {
     place();
     settle();
   }
 #pragma unroll 1
-  for (int i = 0; i < kStages; ++i) copy(i);
+  for (int i = 0; i < S::kStages; ++i) copy(i);
   if (PHASE == 1) {
     grid_dependency_wait();  // the weights are on their way while the activations are finished
     grid_dependents_launch();
@@ -530,170 +531,159 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   const int r = lane >> 2, c = lane & 3;
   int stage = 0;
   int first = 0, count = 0;
-  Rows<NT> rows = {};
+  // This lane's B row (r) in operand order, and where the sums of rows 2c and
+  // 2c + 1 are.  Columns beyond the count repeat the last row; nothing of
+  // theirs is kept.
+  const uint8_t* x_row = nullptr;
+  const float *sums0 = nullptr, *sums1 = nullptr;
   float* parts = reinterpret_cast<float*>(smem + S::kRing) + team * 2 * TEAM * S::kPart;  // two halves that take turns
 
-  // One item: d += .., for NA of the B tiles.
-  auto item = [&](auto na, int group, float (&acc)[kTiles][NT][4]) {
-    constexpr int NA = decltype(na)::value;
-    uint4 xv[NA][4];
-    float2 xs[NA][2];  // X, and (phase 0) the factor of the products
+  auto item = [&](int group, float (&acc)[TILES][4]) {
+    uint4 xv[4];
+    float2 xs[2];  // X, and (phase 0) the factor of the products
 #pragma unroll
-    for (int n = 0; n < NA; ++n) {
+    for (int i = 0; i < 4; ++i) xv[i] = *reinterpret_cast<const uint4*>(x_row + group * 256 + i * 64);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) xv[n][i] = *reinterpret_cast<const uint4*>(rows.x[n] + group * 256 + i * 64);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (PHASE == 0) {
-          xs[n][k] = reinterpret_cast<const float2*>(rows.sums[n][k])[group];
-        } else {
-          const float4 v = reinterpret_cast<const float4*>(rows.sums[n][k])[group * 2];
-          const float4 w = reinterpret_cast<const float4*>(rows.sums[n][k])[group * 2 + 1];
-          xs[n][k].x = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
-        }
+    for (int k = 0; k < 2; ++k) {
+      const float* sums = k ? sums1 : sums0;
+      if (PHASE == 0) {
+        xs[k] = reinterpret_cast<const float2*>(sums)[group];
+      } else {
+        const float4 v = reinterpret_cast<const float4*>(sums)[group * 2];
+        const float4 w = reinterpret_cast<const float4*>(sums)[group * 2 + 1];
+        xs[k].x = ((v.x + v.y) + (v.z + v.w)) + ((w.x + w.y) + (w.z + w.w));
       }
     }
-    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
     __syncwarp();
-    const uint8_t* st = ring_ptr + stage * kStage;
-    float d[kTiles][NA][4] = {};
+    const uint8_t* st = ring_ptr + stage * S::kStage;
+    float d[TILES][4] = {};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint4 q[kTiles];
+      uint4 q[TILES];
 #pragma unroll
-      for (int t = 0; t < kTiles; ++t) q[t] = *reinterpret_cast<const uint4*>(st + t * kBlockBytes + 512 * h + 16 * lane);
+      for (int t = 0; t < TILES; ++t) q[t] = *reinterpret_cast<const uint4*>(st + t * kBlockBytes + 512 * h + 16 * lane);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int s = 4 * h + j;
+        const uint32_t b0 = s % 2 ? xv[s / 2].z : xv[s / 2].x, b1 = s % 2 ? xv[s / 2].w : xv[s / 2].y;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
+        for (int t = 0; t < TILES; ++t) {
           uint32_t w[4];
           operand<kBf16>(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, w);
-#pragma unroll
-          for (int n = 0; n < NA; ++n)
-            mma<kBf16>(d[t][n], w, s % 2 ? xv[n][s / 2].z : xv[n][s / 2].x, s % 2 ? xv[n][s / 2].w : xv[n][s / 2].y);
+          mma<kBf16>(d[t], w, b0, b1);
         }
       }
     }
-    uint2 meta[kTiles];
+    uint2 meta[TILES];
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) meta[t] = *reinterpret_cast<const uint2*>(st + t * kBlockBytes + kCodeBytes + 8 * r);
+    for (int t = 0; t < TILES; ++t) meta[t] = *reinterpret_cast<const uint2*>(st + t * kBlockBytes + kCodeBytes + 8 * r);
     __syncwarp();  // the stage is read out
     copy(stage);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) {
+    for (int t = 0; t < TILES; ++t) {
       float s0 = low_f(meta[t].x), s1 = low_f(meta[t].y);
       const float b0 = fmaf(kBf16 ? -128.f : -1024.f, s0, high_f(meta[t].x));
       const float b1 = fmaf(kBf16 ? -128.f : -64.f, s1, high_f(meta[t].y));
       if (!kBf16) s1 *= 0.0625f;  // these columns carry 16 q
 #pragma unroll
-      for (int n = 0; n < NA; ++n)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float f0 = kBf16 ? s0 : s0 * xs[n][k].y, f1 = kBf16 ? s1 : s1 * xs[n][k].y;
-          acc[t][n][k] = fmaf(f0, d[t][n][k], fmaf(b0, xs[n][k].x, acc[t][n][k]));
-          acc[t][n][2 + k] = fmaf(f1, d[t][n][2 + k], fmaf(b1, xs[n][k].x, acc[t][n][2 + k]));
-        }
+      for (int k = 0; k < 2; ++k) {
+        const float f0 = kBf16 ? s0 : s0 * xs[k].y, f1 = kBf16 ? s1 : s1 * xs[k].y;
+        acc[t][k] = fmaf(f0, d[t][k], fmaf(b0, xs[k].x, acc[t][k]));
+        acc[t][2 + k] = fmaf(f1, d[t][2 + k], fmaf(b1, xs[k].x, acc[t][2 + k]));
+      }
     }
   };
-  using One = std::integral_constant<int, 1>;
-  using Two = std::integral_constant<int, 2>;
 
-  int expert_seen = -1;
+  int seen = -1;
   for (int u = 0;; ++u) {
-    const int unit = unit_at(u);
-    if (unit >= units) break;
-    const int a = unit / per, at = unit % per;
+    const uint32_t unit = unit_at(u);
+    if (unit == kEnd) break;
+    const int a = static_cast<int>(unit >> 16), at = static_cast<int>(unit & 0xFFFFu) * kSide;  // entry, first tile
+    const bool draws = drawn && member == 0 && lane == 0 && u + lead >= kQueue;
     int draw = 0;
-    if (drawn && member == 0 && lane == 0 && u + lead >= kQueue) draw = static_cast<int>(atomicAdd(p.next + PHASE, 1u));
-    if (a != expert_seen) {
-      expert_seen = a;
+    if (draws) draw = static_cast<int>(atomicAdd(p.next + PHASE, 1u));
+    if (a != seen) {
+      seen = a;
       first = lists.first[a];
       count = lists.first[a + 1] - first;
       auto source = [&](int i) {
         const int pick = lists.pick[first + min(i, count - 1)];
         return static_cast<long long>(PHASE == 0 ? pick / p.top_k : pick);
       };
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        rows.x[n] = (PHASE == 0 ? p.xp : p.act) + source(n * 8 + r) * K * 2 + 16 * c;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const long long m = source(n * 8 + 2 * c + k);
-          rows.sums[n][k] = PHASE == 0 ? reinterpret_cast<const float*>(p.xs) + m * (G * 2) : p.acts + m * (G * 8);
-        }
-      }
+      x_row = (PHASE == 0 ? p.xp : p.act) + source(r) * K * 2 + 16 * c;
+      const float* base = PHASE == 0 ? reinterpret_cast<const float*>(p.xs) : p.acts;
+      sums0 = base + source(2 * c) * (PHASE == 0 ? G * 2 : G * 8);
+      sums1 = base + source(2 * c + 1) * (PHASE == 0 ? G * 2 : G * 8);
     }
     float* part = parts + (u & 1) * TEAM * S::kPart;
     const int mine = turn(u);
-    float sum[kTiles][NT][4];
+    float sum[TILES][4];
 #pragma unroll
     for (int q = 0; q < (kMine + 1) / 2; ++q) {
-      float two[kTiles][NT][4];
+      float two[TILES][4];
 #pragma unroll
       for (int h = 0; h < (kMine > 1 ? 2 : 1); ++h) {
-        float acc[kTiles][NT][4] = {};
-        const int v = part_at(mine, 2 * q + h);
-        if (NT == 2 && count > 8) {
-          if constexpr (NT == 2)
-            for (int g = v; g < G; g += kParts) item(Two{}, g, acc);
-        } else {
-          for (int g = v; g < G; g += kParts) item(One{}, g, acc);
-        }
+        float acc[TILES][4] = {};
+        for (int g = part_at(mine, 2 * q + h); g < G; g += kParts) item(g, acc);
 #pragma unroll
-        for (int i = 0; i < kTiles * NT * 4; ++i) (&two[0][0][0])[i] = h == 0 ? (&acc[0][0][0])[i] : (&two[0][0][0])[i] + (&acc[0][0][0])[i];
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) two[t][i] = h == 0 ? acc[t][i] : two[t][i] + acc[t][i];
       }
 #pragma unroll
-      for (int i = 0; i < kTiles * NT * 4; ++i) (&sum[0][0][0])[i] = q == 0 ? (&two[0][0][0])[i] : (&sum[0][0][0])[i] + (&two[0][0][0])[i];
+      for (int t = 0; t < TILES; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[t][i] = q == 0 ? two[t][i] : sum[t][i] + two[t][i];
     }
-    float* out = part + mine * S::kPart;
+    float* out = part + mine * S::kPart + 2 * c * S::kCols + r;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t)
+    for (int k = 0; k < 2; ++k)
+      if (2 * c + k < count)
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = n * 8 + 2 * c + (i & 1);
-          if (m < count) out[m * kCols + t * kTileN + r + 8 * (i >> 1)] = sum[t][n][i];
+        for (int t = 0; t < TILES; ++t) {
+          out[k * S::kCols + t * kTileN] = sum[t][k];
+          out[k * S::kCols + t * kTileN + 8] = sum[t][2 + k];
         }
     // One barrier of the team per unit: the other half of the buffer, and the
     // drawn unit's place in the queue, are free again once every member is past
     // the next one.
-    if (drawn && member == 0 && lane == 0 && u + lead >= kQueue)
-      s_unit[team][(u + lead) % kQueue] = kQueue * shares + draw;
+    if (draws) s_unit[team][(u + lead) % kQueue] = locate(kQueue * shares + draw);
     asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
-    const int tt = member * 32 + lane;
     auto join = [&](const float* q) {  // (parts beyond the depth are 0)
       if constexpr (TEAM == 2) return q[0] + q[S::kPart];
+      else if constexpr (TEAM == 4) return (q[0] + q[2 * S::kPart]) + (q[S::kPart] + q[3 * S::kPart]);
       else
         return ((q[0] + q[4 * S::kPart]) + (q[2 * S::kPart] + q[6 * S::kPart])) +
                ((q[S::kPart] + q[5 * S::kPart]) + (q[3 * S::kPart] + q[7 * S::kPart]));
     };
+    // the folding warps take turns
+    const int from = ((member + u) % TEAM) * 32 + lane;
     if (PHASE == 0) {
-      const int o = (tt + 32 * (u % TEAM)) % (TEAM * 32);  // the folding warps take turns
-      const int m = o / kTileN, col = o % kTileN;
-      if (o / 32 * 2 < count) {  // whole warps
+      constexpr int kGate = kSide * kTileN;  // columns of activations
+      for (int o = from; o / 32 * 32 < count * kGate; o += TEAM * 32) {  // whole warps
+        const int m = o / kGate, col = o % kGate, n = at * kTileN + col;
         float act = 0.f;
+        int pick = 0;
         if (m < count) {
-          const int pick = lists.pick[first + m];
-          const float v = join(part + m * kCols + col), w = join(part + m * kCols + col + kTileN);
+          pick = lists.pick[first + m];
+          const float v = join(part + m * S::kCols + col), w = join(part + m * S::kCols + col + kGate);
           const __nv_bfloat16 b = __float2bfloat16_rn(v / (1.f + expf(-v)) * w);
           act = __bfloat162float(b);
-          // columns 16 at + col: k step at % 8 of the group
-          uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + at / 8 * 256 + at % 8 / 2 * 64 + col % 8 / 2 * 16 +
-                         (at % 2 * 2 + col / 8) * 4 + (col & 1) * 2;
+          // column n: k step n / 16 % 8 of its group
+          uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + n / 128 * 256 + n / 32 % 4 * 64 + n % 8 / 2 * 16 +
+                         (n / 16 % 2 * 2 + n / 8 % 2) * 4 + (n & 1) * 2;
           *reinterpret_cast<__nv_bfloat16*>(dst) = b;
         }
 #pragma unroll
         for (int k = 8; k > 0; k >>= 1) act += __shfl_xor_sync(~0u, act, k);
-        if (m < count && col == 0)
-          p.acts[static_cast<long long>(lists.pick[first + m]) * (p.F / kTileN) + at] = act;
+        if (m < count && n % 16 == 0) p.acts[static_cast<long long>(pick) * (p.F / kTileN) + n / 16] = act;
       }
     } else {
-      for (int o = (tt + 32 * (u % TEAM)) % (TEAM * 32); o < count * kCols; o += TEAM * 32) {
-        const int m = o / kCols, col = o % kCols;
-        p.part[static_cast<long long>(lists.pick[first + m]) * p.D + at * kCols + col] = join(part + m * kCols + col);
+      for (int o = from; o < count * S::kCols; o += TEAM * 32) {
+        const int m = o / S::kCols, col = o % S::kCols;
+        p.part[static_cast<long long>(lists.pick[first + m]) * p.D + at * kTileN + col] = join(part + m * S::kCols + col);
       }
     }
   }
@@ -760,26 +750,27 @@ Layout layout(const w4g128_moe_args& a) {
   return l;
 }
 
-template <int PHASE, int NT, int TEAM>
+template <int PHASE, int TILES, int TEAM>
 cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, long long units) {
-  constexpr int kBytes = Stream<NT>::kBytes;
+  constexpr int kBytes = Stream<TILES>::kBytes;
   const cudaError_t e =
-      cudaFuncSetAttribute(expert_kernel<PHASE, NT, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+      cudaFuncSetAttribute(expert_kernel<PHASE, TILES, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(2 * sms, units)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
-  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, NT, TEAM>, p);
+  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, TILES, TEAM>, p);
 }
 
-template <int NT>
+// Wide items, and small teams in the down projection, where each team then has
+// at least 4 units.
 cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
   const long long most = std::min(p.M * p.top_k, p.E);  // picked experts
-  const cudaError_t e = launch_expert<0, NT, 8>(cfg, p, sms, most * (p.F / kTileN));
+  const long long gate = most * (p.F / 32), down = most * (p.D / 64);
+  const cudaError_t e = gate >= 8 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
+                                        : launch_expert<0, 2, 8>(cfg, p, sms, 2 * gate);
   if (e != cudaSuccess) return e;
-  const long long units = most * (p.D / kCols);
-  // small teams where every team then has several units
-  return units >= 16 * sms ? launch_expert<1, NT, 2>(cfg, p, sms, units) : launch_expert<1, NT, 8>(cfg, p, sms, units);
+  return down >= 16 * sms ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
 }
 
 cudaError_t launch(const Params& p, cudaStream_t stream) {
@@ -798,7 +789,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kRouteThreads);
   e = p.M <= 8 ? cudaLaunchKernelEx(&cfg, route_kernel<false>, p) : cudaLaunchKernelEx(&cfg, route_kernel<true>, p);
   if (e != cudaSuccess) return e;
-  e = p.M <= 8 ? launch_experts<1>(cfg, p, sms) : launch_experts<2>(cfg, p, sms);
+  e = launch_experts(cfg, p, sms);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((p.D / 4 + 127) / 128, p.M);
   cfg.blockDim = dim3(128);
