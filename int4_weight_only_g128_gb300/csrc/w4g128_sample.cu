@@ -4,23 +4,25 @@
 // A bf16 logit has at most 65536 values, so the row's whole distribution is a
 // histogram over 16-bit keys ordered like the values, and every token with the
 // same value has the same weight: the sort, the softmax and the cumulative sum
-// over the vocabulary become a scan over bins.  One row is one cluster of 8
-// CTAs.  Each counts its slice of the row into its own 65536 16-bit counters
-// (128 KB of shared memory; a slice has at most 65535 tokens), then merges an
-// eighth of the bins from the 8 copies over distributed shared memory, weighs
+// over the vocabulary become a scan over bins.  One row is one cluster of 16, 8
+// or 4 CTAs.  Each counts its slice of the row into its own 65536 16-bit
+// counters (128 KB of shared memory; a slice has at most 65535 tokens), merges
+// its share of the bins from all copies over distributed shared memory, weighs
 // them and scans (count, mass).  The filters keep prefixes of the order, so
 // each is one point of the scan that one thread finds and tells the cluster.
-// The chosen bin and the rank within it lead back to the token: the copies
-// hold each slice's count of that bin, so one CTA re-reads its slice.
+// The chosen bin and the rank within it lead back to the token: every CTA
+// counts the bin in its slice once more, and the one that holds the rank finds
+// the place.
 //
 // Masses are exact integers (weights as 62-bit fractions of the largest, sums
 // in 128 bits): prefix sums agree to the bit whatever their order, so exactly
-// one thread owns each crossing.  FP64 runs at 2 operations a cycle and SM
-// here, so the weights come from an fp32 pair evaluation (exp2_neg) instead:
-// about 1e-14 relative, with 35 full-rate operations a bin.
+// one thread owns each crossing, and the cluster's size changes no result.
+// FP64 runs at 2 operations a cycle and SM here, so the weights come from an
+// fp32 pair evaluation (exp2_neg) instead: about 1e-14 relative, with 35
+// full-rate operations a bin.
 //
 // Bound: latency.  A row of 248320 logits is 0.5 MB, 0.1 us of HBM; the chain
-// load, count, merge, scan and four cluster barriers is what takes time.
+// load, count, merge, scan and five cluster barriers is what takes time.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -34,18 +36,42 @@ namespace {
 
 typedef unsigned __int128 u128;
 
-constexpr int kCtas = 8;          // cluster size: CTAs per row
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536;
-constexpr int kUnitBins = 8;      // bins per thread: 8 CTAs x 1024 threads x 8 = 65536
-constexpr size_t kHistBytes = kBins * 2;
+constexpr size_t kHistBytes = kBins * 2;  // 16-bit counters; later the weights of a CTA's share of the bins
+constexpr size_t smem_for(int ctas) { return kHistBytes + kBins / ctas * 4; }  // and their merged counts
 constexpr uint32_t kMinusInf = 0x007Fu;  // key of -inf: what is not above it is never chosen
 constexpr uint32_t kPlusInf = 0xFF80u;
 
-static_assert(kCtas * kThreads * kUnitBins == kBins, "one unit per thread");
 // a slice: its share of the 16-byte vectors and the ragged ends of up to 7 tokens
-static_assert((W4G128_MAX_VOCAB / 8 + kCtas - 1) / kCtas * 8 + 14 <= 65535, "a slice's count of one bin fits 16 bits");
+constexpr bool slice_fits(int vocab, int ctas) { return (vocab / 8 + ctas - 1) / ctas * 8 + 14 <= 65535; }
+static_assert(slice_fits(W4G128_MAX_VOCAB, 8), "a slice's count of one bin fits 16 bits");
+
+// 2^(-j / 32) as unevaluated sums of two floats, by square roots of 1/2.
+constexpr double root(double v) {
+  double r = 1.0;
+  for (int i = 0; i < 60; ++i) r = 0.5 * (r + v / r);  // Newton's iteration
+  return r;
+}
+struct Table {
+  float hi[32], lo[32];
+};
+constexpr Table make_table() {
+  double half[5] = {};  // 2^(-1/2), 2^(-1/4), .. 2^(-1/32)
+  half[0] = root(0.5);
+  for (int i = 1; i < 5; ++i) half[i] = root(half[i - 1]);
+  Table t = {};
+  for (int j = 0; j < 32; ++j) {
+    double v = 1.0;
+    for (int i = 0; i < 5; ++i)
+      if (j >> (4 - i) & 1) v *= half[i];
+    t.hi[j] = static_cast<float>(v);
+    t.lo[j] = static_cast<float>(v - static_cast<double>(t.hi[j]));
+  }
+  return t;
+}
+__constant__ Table c_table = make_table();
 
 // The order-preserving key of a bf16 pattern; -0 becomes +0, NaN becomes 0.
 __device__ __forceinline__ uint32_t key_of(uint32_t b) {
@@ -132,17 +158,23 @@ __device__ __forceinline__ u128 scaled_floor(u128 z, uint64_t f, bool* exact) {
   return static_cast<u128>(zh) * f + (low >> 64);  // zh < 2^18
 }
 
-__device__ __forceinline__ double as_double(u128 v) {
-  return static_cast<double>(static_cast<uint64_t>(v >> 64)) * 18446744073709551616.0 +
-         static_cast<double>(static_cast<uint64_t>(v));
+__device__ __forceinline__ float as_float(u128 v) {
+  return fmaf(static_cast<float>(static_cast<uint64_t>(v >> 64)), 18446744073709551616.f,
+              static_cast<float>(static_cast<uint64_t>(v)));
 }
 
-// floor(d / w) for a quotient known to be below 2^20 (w > 0).
+// floor(d / w) for a quotient known to be below 2^20 (w > 0): the float
+// quotient is off by less than 1.
 __device__ __forceinline__ uint32_t small_quotient(u128 d, uint64_t w) {
-  uint32_t q = static_cast<uint32_t>(as_double(d) / static_cast<double>(w));
+  uint32_t q = static_cast<uint32_t>(as_float(d) / static_cast<float>(w));
   while (static_cast<u128>(q) * w > d) --q;
   while (static_cast<u128>(q + 1) * w <= d) ++q;
   return q;
+}
+
+// A fraction in [0, 1) in units of 2^-64 (exact from 2^-40 up).
+__device__ __forceinline__ uint64_t fraction64(float v) {
+  return static_cast<uint64_t>(v * 18446744073709551616.f);
 }
 
 template <class T>
@@ -154,48 +186,51 @@ __device__ __forceinline__ void cluster_sync_all() {
   cluster_wait_acquire();
 }
 
-__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
-  extern __shared__ __align__(16) uint32_t hist[];  // bin b: bits 16 (b & 1) .. of word b / 2
+template <int CTAS>
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
+  constexpr int kShare = kBins / CTAS;        // bins that a CTA merges
+  constexpr int kUnit = kShare / kThreads;    // of them, one thread's: consecutive ones
+  extern __shared__ __align__(16) uint32_t smem[];
+  uint32_t* hist = smem;                                        // bin b: bits 16 (b & 1) .. of word b / 2
+  uint64_t* weights = reinterpret_cast<uint64_t*>(smem);        // [kShare], over the counters once they are merged
+  uint32_t* counts = smem + kBins / 2;                          // [kShare]
+  static_assert(kShare * 8 <= static_cast<int>(kHistBytes), "the weights fit over the counters");
   __shared__ float2 table[32];
   __shared__ Pair s_rate;                 // log2(e) / temperature
   __shared__ uint32_t s_red[kWarps];
-  __shared__ uint32_t s_max[kCtas];
-  __shared__ Sum s_warp[kWarps], s_ok[kWarps], s_tot[kCtas], s_totok[kCtas];
+  __shared__ uint32_t s_max[CTAS], s_own[CTAS];
+  __shared__ Sum s_warp[kWarps], s_ok[kWarps], s_tot[CTAS], s_totok[CTAS];
   __shared__ Sum s_topk, s_topp;          // what each filter keeps
   __shared__ uint32_t s_key, s_rank;      // the chosen bin, and the token's place among its equals
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = cluster_ctarank();
-  const int row = blockIdx.x / kCtas;
+  const int row = blockIdx.x / CTAS;
 
   cluster_arrive_relaxed();  // every CTA of the cluster runs before any writes into another
   for (int i = tid; i < kBins / 8; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0, 0, 0, 0);
-  if (tid < 32) {
-    const double t = exp2(-tid / 32.0);
-    const float hi = static_cast<float>(t);
-    table[tid] = make_float2(hi, static_cast<float>(t - static_cast<double>(hi)));
-  }
+  if (tid < 32) table[tid] = make_float2(c_table.hi[tid], c_table.lo[tid]);
   grid_dependency_wait();
 
   float T = p.temperature ? p.temperature[row] : 1.f;
   const bool greedy = !(T > 0.f);
   if (greedy) T = 1.f;
-  if (tid == 32) {
+  __syncthreads();
+  if (tid == kThreads - 1) {  // (needed two barriers from here)
     const double c = 1.4426950408889634 / static_cast<double>(T);
     const float hi = static_cast<float>(c);
     s_rate = {hi, static_cast<float>(c - static_cast<double>(hi))};
   }
-  __syncthreads();
 
   // Count the slice: 16-byte vectors inside the row, the ragged ends by CTA 0
   // and the last CTA, so that slices are index ranges in rank order.
   const uint16_t* base = p.logits + static_cast<long long>(row) * p.row_stride;
   const int head = min(p.vocab, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(base) & 15u)) & 15u) / 2);
   const int nvec = (p.vocab - head) / 8;
-  const int v0 = static_cast<int>(static_cast<long long>(nvec) * rank / kCtas);
-  const int v1 = static_cast<int>(static_cast<long long>(nvec) * (rank + 1) / kCtas);
-  const int e0 = rank == 0 ? 0 : head + 8 * v0;
-  const int e1 = rank == kCtas - 1 ? p.vocab : head + 8 * v1;
+  const int v0 = static_cast<int>(static_cast<long long>(nvec) * rank / CTAS);
+  const int v1 = static_cast<int>(static_cast<long long>(nvec) * (rank + 1) / CTAS);
+  const int tail = head + 8 * nvec;
+  const bool first = rank == 0, last = rank == CTAS - 1;
   uint32_t top = 0;
   auto count = [&](uint32_t bits) {
     const uint32_t k = key_of(bits);
@@ -205,66 +240,96 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
     }
   };
   const uint4* vec = reinterpret_cast<const uint4*>(base + head);
-  for (int i = v0 + tid; i < v1; i += kThreads) {
-    const uint4 v = __ldg(vec + i);
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  for (int i = v0 + tid; i < v1; i += 4 * kThreads) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j * kThreads < v1) v[j] = __ldg(vec + i + j * kThreads);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      count(q[j] & 0xFFFFu);
-      count(q[j] >> 16);
+      if (i + j * kThreads < v1) {
+        const uint32_t q[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          count(q[k] & 0xFFFFu);
+          count(q[k] >> 16);
+        }
+      }
     }
   }
-  if (rank == 0 && tid < head) count(base[tid]);
-  if (rank == kCtas - 1 && head + 8 * nvec + tid < p.vocab) count(base[head + 8 * nvec + tid]);
+  if (first && tid < head) count(base[tid]);
+  if (last && tail + tid < p.vocab) count(base[tail + tid]);
   top = __reduce_max_sync(~0u, top);
   if (lane == 0) s_red[warp] = top;
   __syncthreads();
   cluster_wait_acquire();
   if (warp == 0) {
     top = __reduce_max_sync(~0u, s_red[lane]);
-    if (lane < kCtas) *peer(&s_max[rank], lane) = top;
+    if (lane < CTAS) *peer(&s_max[rank], lane) = top;
   }
   cluster_sync_all();
 
   uint32_t maxkey = 0;
 #pragma unroll
-  for (int j = 0; j < kCtas; ++j) maxkey = max(maxkey, s_max[j]);
+  for (int j = 0; j < CTAS; ++j) maxkey = max(maxkey, s_max[j]);
 
-  // Merge, weigh and scan.  Units fall with (rank, tid): the order of the draw.
-  const int unit = kBins / kUnitBins - 1 - (static_cast<int>(rank) * kThreads + tid);
+  // Merge.  A CTA's bins lie below those of the rank before: the order of the
+  // draw falls with (rank, position from the top of the share).
+  const uint32_t low_bin = kBins - (rank + 1) * kShare;  // its lowest bin
+  for (int u = tid; u < kShare / 8; u += kThreads) {     // 8 bins each
+    uint32_t c[8] = {};
+    if (low_bin + 8 * u <= maxkey) {
+#pragma unroll
+      for (int j = 0; j < CTAS; ++j) {
+        const uint4 v = reinterpret_cast<const uint4*>(peer(hist, j))[low_bin / 8 + u];
+        c[0] += v.x & 0xFFFFu; c[1] += v.x >> 16; c[2] += v.y & 0xFFFFu; c[3] += v.y >> 16;
+        c[4] += v.z & 0xFFFFu; c[5] += v.z >> 16; c[6] += v.w & 0xFFFFu; c[7] += v.w >> 16;
+      }
+    }
+    reinterpret_cast<uint4*>(counts)[2 * u] = make_uint4(c[0], c[1], c[2], c[3]);
+    reinterpret_cast<uint4*>(counts)[2 * u + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+  }
+  cluster_sync_all();  // the counters have been read by all
+
+  // Weigh the occupied bins, neighbours by neighbouring threads.
   const float vmax = value_of(maxkey);
   const Pair rate = s_rate;
-  auto weight = [&](uint32_t key) -> uint64_t {
-    if (key == maxkey) return 1ull << 62;
-    if (maxkey == kPlusInf) return 0ull;
-    const Pair d = two_sum(vmax, -value_of(key));
-    Pair y = two_prod(d.hi, rate.hi);
-    y.lo = __fadd_rn(y.lo, __fmaf_rn(d.hi, rate.lo, d.lo * rate.hi));
-    return exp2_neg(two_sum(y.hi, y.lo), table);
-  };
+  for (int i = tid; i < kShare; i += kThreads) {
+    if (counts[i]) {
+      const uint32_t key = low_bin + i;
+      uint64_t w = 1ull << 62;
+      if (key != maxkey) {
+        if (maxkey == kPlusInf) {
+          w = 0ull;
+        } else {
+          const Pair d = two_sum(vmax, -value_of(key));
+          Pair y = two_prod(d.hi, rate.hi);
+          y.lo = __fadd_rn(y.lo, __fmaf_rn(d.hi, rate.lo, d.lo * rate.hi));
+          w = exp2_neg(two_sum(y.hi, y.lo), table);
+        }
+      }
+      weights[i] = w;
+    }
+  }
+  __syncthreads();
+
+  // Scan, one unit per thread, from the top of the share.
+  const int unit0 = kShare - (tid + 1) * kUnit;  // the unit's lowest bin, within the share
   const float minp = (p.min_p && !greedy) ? p.min_p[row] : 0.f;
   const bool use_minp = minp > 0.f;
   const uint64_t least = use_minp ? static_cast<uint64_t>(fminf(minp, 1.f) * 4611686018427387904.f) : 0ull;
-  uint32_t c[kUnitBins] = {};  // c[i]: bin 8 unit + i
   Sum mine{0u, 0}, ok{0u, 0};
-  if (static_cast<uint32_t>(unit) * kUnitBins <= maxkey) {
 #pragma unroll
-    for (int j = 0; j < kCtas; ++j) {
-      const uint4 v = reinterpret_cast<const uint4*>(peer(hist, j))[unit];
-      c[0] += v.x & 0xFFFFu; c[1] += v.x >> 16; c[2] += v.y & 0xFFFFu; c[3] += v.y >> 16;
-      c[4] += v.z & 0xFFFFu; c[5] += v.z >> 16; c[6] += v.w & 0xFFFFu; c[7] += v.w >> 16;
-    }
-#pragma unroll
-    for (int i = 0; i < kUnitBins; ++i) {
-      if (c[i]) {
-        const uint64_t w = weight(unit * kUnitBins + i);
-        const u128 m = static_cast<u128>(w) * c[i];
-        mine.n += c[i];
-        mine.m += m;
-        if (w >= least) {
-          ok.n += c[i];
-          ok.m += m;
-        }
+  for (int i = kUnit - 1; i >= 0; --i) {
+    const uint32_t c = counts[unit0 + i];
+    if (c) {
+      const uint64_t w = weights[unit0 + i];
+      const u128 m = static_cast<u128>(w) * c;
+      mine.n += c;
+      mine.m += m;
+      if (w >= least) {
+        ok.n += c;
+        ok.m += m;
       }
     }
   }
@@ -305,7 +370,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
     }
     s_warp[lane] = t;  // inclusive
     __syncwarp();
-    if (lane < kCtas) *peer(&s_tot[rank], lane) = s_warp[kWarps - 1];
+    if (lane < CTAS) *peer(&s_tot[rank], lane) = s_warp[kWarps - 1];
   } else if (warp == 1 && use_minp) {
     Sum t = s_ok[lane];
 #pragma unroll
@@ -315,13 +380,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
       const uint64_t hi = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m >> 64), d);
       t.m += (static_cast<u128>(hi) << 64) | lo;
     }
-    if (lane < kCtas) *peer(&s_totok[rank], lane) = t;
+    if (lane < CTAS) *peer(&s_totok[rank], lane) = t;
   }
   cluster_sync_all();
 
   Sum before{0u, 0}, total{0u, 0}, passed{0u, 0};  // before: of the bins above this thread's
 #pragma unroll
-  for (int j = 0; j < kCtas; ++j) {
+  for (int j = 0; j < CTAS; ++j) {
     if (j == static_cast<int>(rank)) before = total;
     total.n += s_tot[j].n;
     total.m += s_tot[j].m;
@@ -352,13 +417,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
     if (before.n < K && K <= before.n + mine.n) {
       uint32_t left = K - before.n;
       u128 m = before.m;
-#pragma unroll
-      for (int i = kUnitBins - 1; i >= 0; --i) {
-        const uint32_t take = min(left, c[i]);
-        if (take) m += static_cast<u128>(weight(unit * kUnitBins + i)) * take;
+      for (int i = kUnit - 1; left > 0u; --i) {
+        const uint32_t take = min(left, counts[unit0 + i]);
+        if (take) m += static_cast<u128>(weights[unit0 + i]) * take;
         left -= take;
       }
-      for (int j = 0; j < kCtas; ++j) *peer(&s_topk, j) = Sum{K, m};
+      for (int j = 0; j < CTAS; ++j) *peer(&s_topk, j) = Sum{K, m};
     }
     cluster_sync_all();
     kept = s_topk;
@@ -366,32 +430,28 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
   // top-p: the tokens whose predecessors' mass is below the fraction
   const float top_p = (p.top_p && !greedy) ? p.top_p[row] : 1.f;
   if (top_p < 1.f) {
-    const uint64_t f = top_p > 0.f ? static_cast<uint64_t>(static_cast<double>(top_p) * 18446744073709551616.0) : 0ull;
     bool exact;
-    u128 goal = scaled_floor(kept.m, f, &exact);
+    u128 goal = scaled_floor(kept.m, top_p > 0.f ? fraction64(top_p) : 0ull, &exact);
     if (!exact || goal == 0) goal += 1;  // before < fraction as integers: before < ceil; the first token stays
-    const uint32_t limit = kept.n;
     if (before.m < goal && goal <= before.m + mine.m) {
       Sum k = before;
-      bool open = true;
-#pragma unroll
-      for (int i = kUnitBins - 1; i >= 0; --i) {
-        if (open && c[i]) {
-          const uint64_t w = weight(unit * kUnitBins + i);
-          if (w > 0ull && k.m + static_cast<u128>(w) * c[i] >= goal) {
-            const uint32_t take = small_quotient(goal - k.m - 1, w) + 1;  // ceil((goal - before) / w)
-            k.n += take;
-            k.m += static_cast<u128>(w) * take;
-            open = false;
-          } else {
-            k.n += c[i];
-            k.m += static_cast<u128>(w) * c[i];
-          }
+      for (int i = kUnit - 1; i >= 0; --i) {
+        const uint32_t c = counts[unit0 + i];
+        if (c == 0u) continue;
+        const uint64_t w = weights[unit0 + i];
+        const u128 m = static_cast<u128>(w) * c;
+        if (w > 0ull && k.m + m >= goal) {
+          const uint32_t take = small_quotient(goal - k.m - 1, w) + 1;  // ceil((goal - before) / w)
+          k.n += take;
+          k.m += static_cast<u128>(w) * take;
+          break;
         }
+        k.n += c;
+        k.m += m;
       }
       // top-k ends inside a bin: it may keep fewer of equal tokens
-      if (k.n > limit) k = kept;
-      for (int j = 0; j < kCtas; ++j) *peer(&s_topp, j) = k;
+      if (k.n > kept.n) k = kept;
+      for (int j = 0; j < CTAS; ++j) *peer(&s_topp, j) = k;
     }
     cluster_sync_all();
     kept = s_topp;
@@ -404,76 +464,138 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads, 1) sam
   // The draw.
   float uu = p.u[row];
   if (!(uu > 0.f)) uu = 0.f;
-  const uint64_t f = uu < 1.f ? static_cast<uint64_t>(static_cast<double>(uu) * 18446744073709551616.0) : ~0ull;
   bool exact;
-  const u128 goal = scaled_floor(kept.m, f, &exact);  // below kept.m
+  const u128 goal = scaled_floor(kept.m, uu < 1.f ? fraction64(uu) : ~0ull, &exact);  // below kept.m
   if (before.m <= goal && goal < before.m + mine.m) {
     u128 m = before.m;
-    bool open = true;
-#pragma unroll
-    for (int i = kUnitBins - 1; i >= 0; --i) {
-      if (open && c[i]) {
-        const uint64_t w = weight(unit * kUnitBins + i);
-        const u128 next = m + static_cast<u128>(w) * c[i];
-        if (goal < next) {
-          const uint32_t j = small_quotient(goal - m, w);
-          for (int r = 0; r < kCtas; ++r) {
-            *peer(&s_key, r) = static_cast<uint32_t>(unit * kUnitBins + i);
-            *peer(&s_rank, r) = j;
-          }
-          if (p.logprobs) {
-            // log(w / kept): near 1 from the exact remainder, so that it keeps its relative precision
-            const double z = as_double(kept.m);
-            const float gone = static_cast<float>(as_double(kept.m - w) / z);
-            p.logprobs[row] =
-                gone < 0.5f ? log1pf(-gone) : logf(static_cast<float>(static_cast<double>(w) / z));
-          }
-          open = false;
+    for (int i = kUnit - 1; i >= 0; --i) {
+      const uint32_t c = counts[unit0 + i];
+      if (c == 0u) continue;
+      const uint64_t w = weights[unit0 + i];
+      const u128 next = m + static_cast<u128>(w) * c;
+      if (goal < next) {
+        const uint32_t j = small_quotient(goal - m, w);
+        for (int r = 0; r < CTAS; ++r) {
+          *peer(&s_key, r) = low_bin + unit0 + i;
+          *peer(&s_rank, r) = j;
         }
-        m = next;
+        if (p.logprobs) {
+          // log(w / kept): near 1 from the exact remainder, so that it keeps its relative precision
+          const float gone = as_float(kept.m - w) / as_float(kept.m);
+          p.logprobs[row] = gone < 0.5f ? log1pf(-gone) : logf(static_cast<float>(w) / as_float(kept.m));
+        }
+        break;
       }
+      m = next;
     }
   }
   cluster_sync_all();
 
-  // Back to the token: the (rank)-th occurrence of the key in index order.
+  // Back to the token: the (rank)-th occurrence of the key in index order.  A
+  // thread holds consecutive vectors, the ragged ends belong to the first and
+  // the last thread of the first and the last CTA.
   const uint32_t key = s_key;
-  uint32_t nth = s_rank, own = 0;
-  bool here = true;
-  for (int j = 0; j <= static_cast<int>(rank); ++j) {
-    const uint32_t n = (peer(hist, j)[key >> 1] >> ((key & 1u) * 16)) & 0xFFFFu;
-    if (j == static_cast<int>(rank)) own = n;
-    else if (nth < n) here = false;
-    else nth -= n;
-    if (!here) break;
-  }
-  here = here && nth < own;
-  if (here) {  // the same for every thread of the CTA
-    const int per = (e1 - e0 + kThreads - 1) / kThreads;
-    const int a = min(e1, e0 + tid * per), b = min(e1, a + per);
-    uint32_t n = 0;
-    for (int i = a; i < b; ++i) n += key_of(base[i]) == key;
-    uint32_t pre = n;
+  const int per = (v1 - v0 + kThreads - 1) / kThreads;
+  const int a = min(v1, v0 + tid * per), b = min(v1, a + per);
+  const bool owns_head = first && tid == 0, owns_tail = last && tid == kThreads - 1;
+  uint32_t n = 0;
+  if (owns_head)
+    for (int i = 0; i < head; ++i) n += key_of(base[i]) == key;
+#pragma unroll 4
+  for (int i = a; i < b; ++i) {
+    const uint4 v = __ldg(vec + i);
+    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t v = __shfl_up_sync(~0u, pre, d);
-      if (lane >= d) pre += v;
-    }
-    if (lane == 31) s_red[warp] = pre;
-    __syncthreads();
-    uint32_t off = 0;
-    for (int j = 0; j < warp; ++j) off += s_red[j];
-    uint32_t at = off + pre - n;
-    if (at <= nth && nth < at + n) {
-      for (int i = a; i < b; ++i) {
-        if (key_of(base[i]) == key) {
-          if (at == nth) p.tokens[row] = i;
-          ++at;
-        }
-      }
-    }
+    for (int k = 0; k < 4; ++k) n += (key_of(q[k] & 0xFFFFu) == key) + (key_of(q[k] >> 16) == key);
   }
-  cluster_sync_all();  // no CTA leaves while another reads its counters
+  if (owns_tail)
+    for (int i = tail; i < p.vocab; ++i) n += key_of(base[i]) == key;
+  uint32_t pre = n;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t v = __shfl_up_sync(~0u, pre, d);
+    if (lane >= d) pre += v;
+  }
+  if (lane == 31) s_red[warp] = pre;
+  __syncthreads();
+  uint32_t at = pre - n;
+  if (warp == 0) {
+    const uint32_t all = __reduce_add_sync(~0u, s_red[lane]);
+    if (lane < CTAS) *peer(&s_own[rank], lane) = all;
+  }
+  for (int j = 0; j < warp; ++j) at += s_red[j];
+  cluster_sync_all();  // no remote access is left
+  uint32_t nth = s_rank;
+  for (int j = 0; j < static_cast<int>(rank); ++j) at += s_own[j];
+  if (at <= nth && nth < at + n) {
+    auto look = [&](uint32_t bits, int index) {
+      if (key_of(bits) == key && at++ == nth) p.tokens[row] = index;
+    };
+    if (owns_head)
+      for (int i = 0; i < head; ++i) look(base[i], i);
+    for (int i = head + 8 * a; i < head + 8 * b; ++i) look(base[i], i);
+    if (owns_tail)
+      for (int i = tail; i < p.vocab; ++i) look(base[i], i);
+  }
+}
+
+template <int CTAS>
+cudaError_t configure(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* cluster, int rows) {
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel<CTAS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem_for(CTAS)));
+  if (e == cudaSuccess && CTAS > 8)
+    e = cudaFuncSetAttribute(sample_kernel<CTAS>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cluster->id = cudaLaunchAttributeClusterDimension;
+  cluster->val.clusterDim.x = CTAS;
+  cluster->val.clusterDim.y = 1;
+  cluster->val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * CTAS);
+  cfg.dynamicSmemBytes = smem_for(CTAS);
+  return e;
+}
+
+// Clusters of this size that the device holds at once (0: none).
+template <int CTAS>
+int held() {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.blockDim = dim3(kThreads);
+  if (configure<CTAS>(cfg, attr, 1) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, sample_kernel<CTAS>, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
+
+// The largest cluster of which the device holds one for each row at once, so
+// that no row waits for another: 16 CTAs halve the counting of 8; beyond that
+// 4, where a slice still fits (half as many rows at once wait twice as long).
+int cluster_for(int rows, int vocab) {
+  static const int most16 = held<16>(), most8 = held<8>();  // every device that runs this is the same
+  if (rows <= most16) return 16;
+  if (rows <= most8 || !slice_fits(vocab, 4)) return 8;
+  return 4;
+}
+
+template <int CTAS>
+cudaError_t launch(const Params& p, int rows, cudaStream_t stream) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  cfg.blockDim = dim3(kThreads);
+  const cudaError_t e = configure<CTAS>(cfg, attr + 1, rows);
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, sample_kernel<CTAS>, p);
 }
 
 }  // namespace
@@ -493,22 +615,12 @@ extern "C" int w4g128_sample(const w4g128_sample_args* a, void* stream) {
   if (!device_is_sm103()) return W4G128_ERR_DEVICE;
   const Params p{a->logits, a->row_stride, a->temperature, a->top_k, a->top_p, a->min_p, a->u,
                  a->tokens, a->logprobs, a->vocab};
-  if (cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kHistBytes)) != cudaSuccess) {
-    cudaGetLastError();
-    return W4G128_ERR_CUDA;
-  }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(a->rows) * kCtas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kHistBytes;
-  if (cudaLaunchKernelEx(&cfg, sample_kernel, p) != cudaSuccess) {
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int ctas = cluster_for(a->rows, a->vocab);
+  const cudaError_t e = ctas == 16  ? launch<16>(p, a->rows, s)
+                        : ctas == 8 ? launch<8>(p, a->rows, s)
+                                    : launch<4>(p, a->rows, s);
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return W4G128_ERR_CUDA;
   }
