@@ -4,11 +4,13 @@
 // A bf16 logit has at most 65536 values, so the row's whole distribution is a
 // histogram over 16-bit keys ordered like the values, and every token with the
 // same value has the same weight: the sort, the softmax and the cumulative sum
-// over the vocabulary become a scan over bins.  One row is one cluster of 16, 8
-// or 4 CTAs.  Each counts its slice of the row into its own 65536 16-bit
-// counters (128 KB of shared memory; a slice has at most 65535 tokens), merges
-// its share of the bins from all copies over distributed shared memory, weighs
-// them and scans (count, mass).  The filters keep prefixes of the order, so
+// over the vocabulary become a scan over bins.  One row is one cluster of 16, 8,
+// 6 or 4 CTAs.  Each counts its slice of the row into its own 65536 16-bit
+// counters (128 KB of shared memory; a slice has at most 65535 tokens) and marks
+// the units of 8 bins that it touched, a few hundred of 8192 in an ordinary row.
+// The touched units of all copies, in order, are cut evenly among the CTAs; each
+// merges its run over distributed shared memory, weighs the bins and scans
+// (count, mass).  The filters keep prefixes of the order, so
 // each is one point of the scan that one thread finds and tells the cluster.
 // The chosen bin and the rank within it lead back to the token: every CTA
 // counts the bin in its slice once more, and the one that holds the rank finds
@@ -22,7 +24,7 @@
 // full-rate operations a bin.
 //
 // Bound: latency.  A row of 248320 logits is 0.5 MB, 0.1 us of HBM; the chain
-// load, count, merge, scan and five cluster barriers is what takes time.
+// load, count, merge, scan and five or six cluster barriers is what takes time.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -39,8 +41,12 @@ typedef unsigned __int128 u128;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536;
-constexpr size_t kHistBytes = kBins * 2;  // 16-bit counters; later the weights of a CTA's share of the bins
-constexpr size_t smem_for(int ctas) { return kHistBytes + kBins / ctas * 4; }  // and their merged counts
+constexpr int kUnit = 8;                  // bins that are marked, merged and handed out together
+constexpr int kUnits = kBins / kUnit;
+constexpr int kWords = kUnits / 32;       // of the marks
+constexpr size_t kHistBytes = kBins * 2;  // 16-bit counters; later the weights of a long run
+constexpr int run_units(int ctas) { return (kUnits + ctas - 1) / ctas; }  // at most
+constexpr size_t smem_for(int ctas) { return kHistBytes + run_units(ctas) * kUnit * 4; }  // and a run's merged counts
 constexpr uint32_t kMinusInf = 0x007Fu;  // key of -inf: what is not above it is never chosen
 constexpr uint32_t kPlusInf = 0xFF80u;
 
@@ -188,18 +194,22 @@ __device__ __forceinline__ void cluster_sync_all() {
 
 template <int CTAS>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
-  constexpr int kShare = kBins / CTAS;        // bins that a CTA merges
-  constexpr int kUnit = kShare / kThreads;    // of them, one thread's: consecutive ones
+  constexpr int kRunUnits = (kUnits + CTAS - 1) / CTAS;  // at most
+  constexpr int kMost = kRunUnits * kUnit;               // bins of a run
   extern __shared__ __align__(16) uint32_t smem[];
-  uint32_t* hist = smem;                                        // bin b: bits 16 (b & 1) .. of word b / 2
-  uint64_t* weights = reinterpret_cast<uint64_t*>(smem);        // [kShare], over the counters once they are merged
-  uint32_t* counts = smem + kBins / 2;                          // [kShare]
-  static_assert(kShare * 8 <= static_cast<int>(kHistBytes), "the weights fit over the counters");
+  uint32_t* hist = smem;                // bin b: bits 16 (b & 1) .. of word b / 2
+  uint32_t* counts = smem + kBins / 2;  // of the run's bins, falling
+  static_assert(kMost * 8 <= static_cast<int>(kHistBytes), "a run's weights fit over the counters");
+  __shared__ uint32_t s_marks[kWords];  // unit kUnits - 1 - i: bit i % 32 of word i / 32
+  __shared__ uint16_t s_run[kRunUnits];  // the run's units, falling
+  __shared__ uint64_t s_weight[kThreads];      // of a short run's bins
+  __shared__ uint32_t s_word[kWords / 32];
   __shared__ float2 table[32];
   __shared__ Pair s_rate;                 // log2(e) / temperature
   __shared__ uint32_t s_red[kWarps];
   __shared__ uint32_t s_max[CTAS], s_own[CTAS];
   __shared__ Sum s_warp[kWarps], s_ok[kWarps], s_tot[CTAS], s_totok[CTAS];
+  __shared__ Sum s_before, s_total, s_passed;  // of the CTAs before this one, and of all
   __shared__ Sum s_topk, s_topp;          // what each filter keeps
   __shared__ uint32_t s_key, s_rank;      // the chosen bin, and the token's place among its equals
 
@@ -262,6 +272,13 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   top = __reduce_max_sync(~0u, top);
   if (lane == 0) s_red[warp] = top;
   __syncthreads();
+  // mark the touched units, the highest first
+#pragma unroll
+  for (int i = 0; i < kUnits / kThreads; ++i) {
+    const uint4 v = reinterpret_cast<const uint4*>(hist)[kUnits - 1 - (i * kThreads + tid)];
+    const uint32_t any = __ballot_sync(~0u, (v.x | v.y | v.z | v.w) != 0u);
+    if (lane == 0) s_marks[i * kWarps + warp] = any;
+  }
   cluster_wait_acquire();
   if (warp == 0) {
     top = __reduce_max_sync(~0u, s_red[lane]);
@@ -272,31 +289,76 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   uint32_t maxkey = 0;
 #pragma unroll
   for (int j = 0; j < CTAS; ++j) maxkey = max(maxkey, s_max[j]);
-
-  // Merge.  A CTA's bins lie below those of the rank before: the order of the
-  // draw falls with (rank, position from the top of the share).
-  const uint32_t low_bin = kBins - (rank + 1) * kShare;  // its lowest bin
-  for (int u = tid; u < kShare / 8; u += kThreads) {     // 8 bins each
-    uint32_t c[8] = {};
-    if (low_bin + 8 * u <= maxkey) {
-#pragma unroll
-      for (int j = 0; j < CTAS; ++j) {
-        const uint4 v = reinterpret_cast<const uint4*>(peer(hist, j))[low_bin / 8 + u];
-        c[0] += v.x & 0xFFFFu; c[1] += v.x >> 16; c[2] += v.y & 0xFFFFu; c[3] += v.y >> 16;
-        c[4] += v.z & 0xFFFFu; c[5] += v.z >> 16; c[6] += v.w & 0xFFFFu; c[7] += v.w >> 16;
-      }
+  if (maxkey == 0u) {  // nothing is allowed, and no remote access is outstanding
+    if (rank == 0 && tid == 0) {
+      p.tokens[row] = -1;
+      if (p.logprobs) p.logprobs[row] = __int_as_float(0xFF800000);
     }
-    reinterpret_cast<uint4*>(counts)[2 * u] = make_uint4(c[0], c[1], c[2], c[3]);
-    reinterpret_cast<uint4*>(counts)[2 * u + 1] = make_uint4(c[4], c[5], c[6], c[7]);
+    return;
   }
-  cluster_sync_all();  // the counters have been read by all
+
+  // All touched units, and this CTA's run of them.
+  uint32_t marks = 0, ahead = 0;
+  if (tid < kWords) {
+#pragma unroll
+    for (int j = 0; j < CTAS; ++j) marks |= peer(s_marks, j)[tid];
+    ahead = __popc(marks);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(~0u, ahead, d);
+      if (lane >= d) ahead += v;
+    }
+    if (lane == 31) s_word[warp] = ahead;
+    ahead -= __popc(marks);
+  }
+  __syncthreads();
+  uint32_t touched = 0;
+#pragma unroll
+  for (int j = 0; j < kWords / 32; ++j) {
+    if (j < warp) ahead += s_word[j];
+    touched += s_word[j];
+  }
+  const int r0 = static_cast<int>(touched * rank / CTAS), r1 = static_cast<int>(touched * (rank + 1) / CTAS);
+  if (tid < kWords) {
+    while (marks) {
+      const int bit = __ffs(marks) - 1, i = static_cast<int>(ahead) - r0;
+      if (i >= 0 && i < r1 - r0) s_run[i] = static_cast<uint16_t>(kUnits - 1 - (tid * 32 + bit));
+      marks &= marks - 1;
+      ++ahead;
+    }
+  }
+  __syncthreads();
+
+  // Merge: one thread per (unit, copy).
+  constexpr int kLanes = CTAS > 8 ? 16 : CTAS > 4 ? 8 : 4;
+  const int bins = (r1 - r0) * kUnit;
+  for (int u0 = warp * (32 / kLanes); u0 < r1 - r0; u0 += kWarps * (32 / kLanes)) {
+    const int u = u0 + lane / kLanes, j = lane % kLanes;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (u < r1 - r0 && j < CTAS) v = reinterpret_cast<const uint4*>(peer(hist, j))[s_run[u]];
+    uint32_t c[8] = {v.x & 0xFFFFu, v.x >> 16, v.y & 0xFFFFu, v.y >> 16, v.z & 0xFFFFu, v.z >> 16, v.w & 0xFFFFu, v.w >> 16};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int d = 1; d < kLanes; d <<= 1) c[i] += __shfl_xor_sync(~0u, c[i], d);
+    if (u < r1 - r0) {  // falling
+      if (j == 0) reinterpret_cast<uint4*>(counts)[2 * u] = make_uint4(c[7], c[6], c[5], c[4]);
+      if (j == 1) reinterpret_cast<uint4*>(counts)[2 * u + 1] = make_uint4(c[3], c[2], c[1], c[0]);
+    }
+  }
+  // A long run's weights take the counters' place once all have read them.
+  const bool shortrun = (touched + CTAS - 1) / CTAS * kUnit <= kThreads;  // the same for the whole cluster
+  uint64_t* weights = shortrun ? s_weight : reinterpret_cast<uint64_t*>(hist);
+  if (shortrun) __syncthreads();
+  else cluster_sync_all();
+  auto key_at = [&](int i) { return static_cast<uint32_t>(s_run[i / kUnit]) * kUnit + (kUnit - 1 - i % kUnit); };
 
   // Weigh the occupied bins, neighbours by neighbouring threads.
   const float vmax = value_of(maxkey);
   const Pair rate = s_rate;
-  for (int i = tid; i < kShare; i += kThreads) {
+  for (int i = tid; i < bins; i += kThreads) {
     if (counts[i]) {
-      const uint32_t key = low_bin + i;
+      const uint32_t key = key_at(i);
       uint64_t w = 1ull << 62;
       if (key != maxkey) {
         if (maxkey == kPlusInf) {
@@ -313,17 +375,17 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   }
   __syncthreads();
 
-  // Scan, one unit per thread, from the top of the share.
-  const int unit0 = kShare - (tid + 1) * kUnit;  // the unit's lowest bin, within the share
+  // Scan, some neighbouring bins per thread.
+  const int per_thread = (bins + kThreads - 1) / kThreads;
+  const int b0 = min(bins, tid * per_thread), b1 = min(bins, b0 + per_thread);
   const float minp = (p.min_p && !greedy) ? p.min_p[row] : 0.f;
   const bool use_minp = minp > 0.f;
   const uint64_t least = use_minp ? static_cast<uint64_t>(fminf(minp, 1.f) * 4611686018427387904.f) : 0ull;
   Sum mine{0u, 0}, ok{0u, 0};
-#pragma unroll
-  for (int i = kUnit - 1; i >= 0; --i) {
-    const uint32_t c = counts[unit0 + i];
+  for (int i = b0; i < b1; ++i) {
+    const uint32_t c = counts[i];
     if (c) {
-      const uint64_t w = weights[unit0 + i];
+      const uint64_t w = weights[i];
       const u128 m = static_cast<u128>(w) * c;
       mine.n += c;
       mine.m += m;
@@ -357,6 +419,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     if (lane == 31) s_ok[warp] = ok;
   }
   __syncthreads();
+  auto sum_all = [&](Sum t) {  // over a warp
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+      t.n += __shfl_xor_sync(~0u, t.n, d);
+      const uint64_t lo = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m), d);
+      const uint64_t hi = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m >> 64), d);
+      t.m += (static_cast<u128>(hi) << 64) | lo;
+    }
+    return t;
+  };
   if (warp == 0) {
     Sum t = s_warp[lane];
 #pragma unroll
@@ -372,36 +444,25 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     __syncwarp();
     if (lane < CTAS) *peer(&s_tot[rank], lane) = s_warp[kWarps - 1];
   } else if (warp == 1 && use_minp) {
-    Sum t = s_ok[lane];
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) {
-      t.n += __shfl_xor_sync(~0u, t.n, d);
-      const uint64_t lo = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m), d);
-      const uint64_t hi = __shfl_xor_sync(~0u, static_cast<uint64_t>(t.m >> 64), d);
-      t.m += (static_cast<u128>(hi) << 64) | lo;
-    }
+    const Sum t = sum_all(s_ok[lane]);
     if (lane < CTAS) *peer(&s_totok[rank], lane) = t;
   }
   cluster_sync_all();
-
-  Sum before{0u, 0}, total{0u, 0}, passed{0u, 0};  // before: of the bins above this thread's
-#pragma unroll
-  for (int j = 0; j < CTAS; ++j) {
-    if (j == static_cast<int>(rank)) before = total;
-    total.n += s_tot[j].n;
-    total.m += s_tot[j].m;
-    if (use_minp) {
-      passed.n += s_totok[j].n;
-      passed.m += s_totok[j].m;
+  if (warp == 0) {
+    const Sum none{0u, 0};
+    const Sum t = lane < CTAS ? s_tot[lane] : none;
+    const Sum all = sum_all(t), up = sum_all(lane < static_cast<int>(rank) ? t : none);
+    if (lane == 0) {
+      s_total = all;
+      s_before = up;
     }
+  } else if (warp == 1 && use_minp) {
+    const Sum t = sum_all(lane < CTAS ? s_totok[lane] : Sum{0u, 0});
+    if (lane == 0) s_passed = t;
   }
-  if (total.n == 0u) {  // no remote access is outstanding
-    if (rank == 0 && tid == 0) {
-      p.tokens[row] = -1;
-      if (p.logprobs) p.logprobs[row] = __int_as_float(0xFF800000);
-    }
-    return;
-  }
+  __syncthreads();
+  const Sum total = s_total;
+  Sum passed = s_passed, before = s_before;  // before: of the bins above this thread's
   if (warp > 0) {
     before.n += s_warp[warp - 1].n;
     before.m += s_warp[warp - 1].m;
@@ -417,9 +478,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     if (before.n < K && K <= before.n + mine.n) {
       uint32_t left = K - before.n;
       u128 m = before.m;
-      for (int i = kUnit - 1; left > 0u; --i) {
-        const uint32_t take = min(left, counts[unit0 + i]);
-        if (take) m += static_cast<u128>(weights[unit0 + i]) * take;
+      for (int i = b0; left > 0u; ++i) {
+        const uint32_t take = min(left, counts[i]);
+        if (take) m += static_cast<u128>(weights[i]) * take;
         left -= take;
       }
       for (int j = 0; j < CTAS; ++j) *peer(&s_topk, j) = Sum{K, m};
@@ -435,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     if (!exact || goal == 0) goal += 1;  // before < fraction as integers: before < ceil; the first token stays
     if (before.m < goal && goal <= before.m + mine.m) {
       Sum k = before;
-      for (int i = kUnit - 1; i >= 0; --i) {
-        const uint32_t c = counts[unit0 + i];
+      for (int i = b0; i < b1; ++i) {
+        const uint32_t c = counts[i];
         if (c == 0u) continue;
-        const uint64_t w = weights[unit0 + i];
+        const uint64_t w = weights[i];
         const u128 m = static_cast<u128>(w) * c;
         if (w > 0ull && k.m + m >= goal) {
           const uint32_t take = small_quotient(goal - k.m - 1, w) + 1;  // ceil((goal - before) / w)
@@ -468,15 +529,15 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   const u128 goal = scaled_floor(kept.m, uu < 1.f ? fraction64(uu) : ~0ull, &exact);  // below kept.m
   if (before.m <= goal && goal < before.m + mine.m) {
     u128 m = before.m;
-    for (int i = kUnit - 1; i >= 0; --i) {
-      const uint32_t c = counts[unit0 + i];
+    for (int i = b0; i < b1; ++i) {
+      const uint32_t c = counts[i];
       if (c == 0u) continue;
-      const uint64_t w = weights[unit0 + i];
+      const uint64_t w = weights[i];
       const u128 next = m + static_cast<u128>(w) * c;
       if (goal < next) {
         const uint32_t j = small_quotient(goal - m, w);
         for (int r = 0; r < CTAS; ++r) {
-          *peer(&s_key, r) = low_bin + unit0 + i;
+          *peer(&s_key, r) = key_at(i);
           *peer(&s_rank, r) = j;
         }
         if (p.logprobs) {
@@ -575,13 +636,14 @@ int held() {
 }
 
 // The largest cluster of which the device holds one for each row at once, so
-// that no row waits for another: 16 CTAs halve the counting of 8; beyond that
-// 4, where a slice still fits (half as many rows at once wait twice as long).
+// that no row waits for another (16 CTAs halve the counting of 8); beyond that
+// 4, where a slice still fits.
 int cluster_for(int rows, int vocab) {
-  static const int most16 = held<16>(), most8 = held<8>();  // every device that runs this is the same
+  static const int most16 = held<16>(), most8 = held<8>(), most6 = held<6>();  // (devices that run this are alike)
   if (rows <= most16) return 16;
-  if (rows <= most8 || !slice_fits(vocab, 4)) return 8;
-  return 4;
+  if (rows <= most8) return 8;
+  if (rows <= most6 && slice_fits(vocab, 6)) return 6;
+  return slice_fits(vocab, 4) ? 4 : 8;
 }
 
 template <int CTAS>
@@ -619,6 +681,7 @@ extern "C" int w4g128_sample(const w4g128_sample_args* a, void* stream) {
   const int ctas = cluster_for(a->rows, a->vocab);
   const cudaError_t e = ctas == 16  ? launch<16>(p, a->rows, s)
                         : ctas == 8 ? launch<8>(p, a->rows, s)
+                        : ctas == 6 ? launch<6>(p, a->rows, s)
                                     : launch<4>(p, a->rows, s);
   if (e != cudaSuccess) {
     cudaGetLastError();
