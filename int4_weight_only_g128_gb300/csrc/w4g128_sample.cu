@@ -53,6 +53,9 @@ constexpr uint32_t kPlusInf = 0xFF80u;
 // a slice: its share of the 16-byte vectors and the ragged ends of up to 7 tokens
 constexpr bool slice_fits(int vocab, int ctas) { return (vocab / 8 + ctas - 1) / ctas * 8 + 14 <= 65535; }
 static_assert(slice_fits(W4G128_MAX_VOCAB, 8), "a slice's count of one bin fits 16 bits");
+static_assert(kWords % 32 == 0 && kWarps == 32, "a warp per 32 words of marks, in blocks of 32 words");
+constexpr int kBlocks = 8;  // of 1024 vectors, a slice's at most
+static_assert(65535 / 8 <= kBlocks * kThreads, "a slice's vectors");
 
 // 2^(-j / 32) as unevaluated sums of two floats, by square roots of 1/2.
 constexpr double root(double v) {
@@ -146,6 +149,12 @@ struct Params {
   int vocab;
 };
 
+struct Settings {
+  Pair rate;  // log2(e) / temperature
+  float min_p, top_p, u;
+  int top_k;
+};
+
 struct Sum {  // a number of tokens and their mass
   uint32_t n;
   u128 m;
@@ -203,11 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   __shared__ uint32_t s_marks[kWords];  // unit kUnits - 1 - i: bit i % 32 of word i / 32
   __shared__ uint16_t s_run[kRunUnits];  // the run's units, falling
   __shared__ uint64_t s_weight[kThreads];      // of a short run's bins
+  __shared__ uint2 s_all[kWords];              // the marks of all copies, and the marked units before the word
   __shared__ uint32_t s_word[kWords / 32];
   __shared__ float2 table[32];
-  __shared__ Pair s_rate;                 // log2(e) / temperature
+  __shared__ Settings s_set;
   __shared__ uint32_t s_red[kWarps];
   __shared__ uint32_t s_max[CTAS], s_own[CTAS];
+  __shared__ uint16_t s_block[kBlocks][kWarps];  // the chosen bin's tokens, by block and warp
+  __shared__ uint32_t s_ends[2];                 // and in the ragged ends
   __shared__ Sum s_warp[kWarps], s_ok[kWarps], s_tot[CTAS], s_totok[CTAS];
   __shared__ Sum s_before, s_total, s_passed;  // of the CTAs before this one, and of all
   __shared__ Sum s_topk, s_topp;          // what each filter keeps
@@ -222,15 +234,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   if (tid < 32) table[tid] = make_float2(c_table.hi[tid], c_table.lo[tid]);
   grid_dependency_wait();
 
-  float T = p.temperature ? p.temperature[row] : 1.f;
-  const bool greedy = !(T > 0.f);
-  if (greedy) T = 1.f;
-  __syncthreads();
-  if (tid == kThreads - 1) {  // (needed two barriers from here)
-    const double c = 1.4426950408889634 / static_cast<double>(T);
-    const float hi = static_cast<float>(c);
-    s_rate = {hi, static_cast<float>(c - static_cast<double>(hi))};
+  // The row's settings, read once: a load where each is used would cost its latency there.
+  const bool reads = tid == kThreads - 1;
+  float T = 1.f;
+  Settings set = {{0.f, 0.f}, 0.f, 1.f, 0.f, 0};
+  if (reads) {
+    if (p.temperature) T = p.temperature[row];
+    if (p.min_p) set.min_p = p.min_p[row];
+    if (p.top_p) set.top_p = p.top_p[row];
+    if (p.top_k) set.top_k = p.top_k[row];
+    set.u = p.u[row];
   }
+  __syncthreads();
 
   // Count the slice: 16-byte vectors inside the row, the ragged ends by CTA 0
   // and the last CTA, so that slices are index ranges in rank order.
@@ -267,6 +282,19 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
       }
     }
   }
+  if (reads) {  // (for behind the next barriers)
+    const bool greedy = !(T > 0.f);
+    if (greedy) {
+      T = 1.f;
+      set.min_p = 0.f;
+      set.top_p = 1.f;
+      set.top_k = 1;
+    }
+    const double c = 1.4426950408889634 / static_cast<double>(T);
+    const float hi = static_cast<float>(c);
+    set.rate = {hi, static_cast<float>(c - static_cast<double>(hi))};
+    s_set = set;
+  }
   if (first && tid < head) count(base[tid]);
   if (last && tail + tid < p.vocab) count(base[tail + tid]);
   top = __reduce_max_sync(~0u, top);
@@ -297,35 +325,34 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     return;
   }
 
-  // All touched units, and this CTA's run of them.
-  uint32_t marks = 0, ahead = 0;
+  // All touched units, and this CTA's run of them: unit i of all goes to place i - r0.
   if (tid < kWords) {
+    uint32_t marks = 0;
 #pragma unroll
     for (int j = 0; j < CTAS; ++j) marks |= peer(s_marks, j)[tid];
-    ahead = __popc(marks);
+    uint32_t ahead = __popc(marks);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t v = __shfl_up_sync(~0u, ahead, d);
       if (lane >= d) ahead += v;
     }
     if (lane == 31) s_word[warp] = ahead;
-    ahead -= __popc(marks);
+    s_all[tid] = make_uint2(marks, ahead - __popc(marks));
   }
   __syncthreads();
-  uint32_t touched = 0;
+  uint32_t touched = 0, ahead[kWords / 32];
 #pragma unroll
   for (int j = 0; j < kWords / 32; ++j) {
-    if (j < warp) ahead += s_word[j];
+    ahead[j] = touched;
     touched += s_word[j];
   }
   const int r0 = static_cast<int>(touched * rank / CTAS), r1 = static_cast<int>(touched * (rank + 1) / CTAS);
-  if (tid < kWords) {
-    while (marks) {
-      const int bit = __ffs(marks) - 1, i = static_cast<int>(ahead) - r0;
-      if (i >= 0 && i < r1 - r0) s_run[i] = static_cast<uint16_t>(kUnits - 1 - (tid * 32 + bit));
-      marks &= marks - 1;
-      ++ahead;
-    }
+#pragma unroll
+  for (int k = 0; k < kWords / 32; ++k) {  // word k * 32 + warp, bit lane
+    const uint2 w = s_all[k * kWarps + warp];
+    const int i = static_cast<int>(ahead[k] + w.y + __popc(w.x & ((1u << lane) - 1u))) - r0;
+    if ((w.x >> lane & 1u) && i >= 0 && i < r1 - r0)
+      s_run[i] = static_cast<uint16_t>(kUnits - 1 - ((k * kWarps + warp) * 32 + lane));
   }
   __syncthreads();
 
@@ -355,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
 
   // Weigh the occupied bins, neighbours by neighbouring threads.
   const float vmax = value_of(maxkey);
-  const Pair rate = s_rate;
+  const Pair rate = s_set.rate;
   for (int i = tid; i < bins; i += kThreads) {
     if (counts[i]) {
       const uint32_t key = key_at(i);
@@ -378,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   // Scan, some neighbouring bins per thread.
   const int per_thread = (bins + kThreads - 1) / kThreads;
   const int b0 = min(bins, tid * per_thread), b1 = min(bins, b0 + per_thread);
-  const float minp = (p.min_p && !greedy) ? p.min_p[row] : 0.f;
+  const float minp = s_set.min_p;
   const bool use_minp = minp > 0.f;
   const uint64_t least = use_minp ? static_cast<uint64_t>(fminf(minp, 1.f) * 4611686018427387904.f) : 0ull;
   Sum mine{0u, 0}, ok{0u, 0};
@@ -471,7 +498,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   before.m += inc.m - mine.m;
 
   // top-k: the kept count and mass
-  const int kreq = greedy ? 1 : (p.top_k ? p.top_k[row] : 0);
+  const int kreq = s_set.top_k;
   Sum kept = total;
   if (kreq > 0 && static_cast<uint32_t>(kreq) < total.n) {
     const uint32_t K = static_cast<uint32_t>(kreq);
@@ -489,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
     kept = s_topk;
   }
   // top-p: the tokens whose predecessors' mass is below the fraction
-  const float top_p = (p.top_p && !greedy) ? p.top_p[row] : 1.f;
+  const float top_p = s_set.top_p;
   if (top_p < 1.f) {
     bool exact;
     u128 goal = scaled_floor(kept.m, top_p > 0.f ? fraction64(top_p) : 0ull, &exact);
@@ -523,10 +550,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   }
 
   // The draw.
-  float uu = p.u[row];
+  float uu = s_set.u;
   if (!(uu > 0.f)) uu = 0.f;
   bool exact;
   const u128 goal = scaled_floor(kept.m, uu < 1.f ? fraction64(uu) : ~0ull, &exact);  // below kept.m
+  uint64_t drawn = 0;  // the weight, where it is this thread's
   if (before.m <= goal && goal < before.m + mine.m) {
     u128 m = before.m;
     for (int i = b0; i < b1; ++i) {
@@ -540,11 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
           *peer(&s_key, r) = key_at(i);
           *peer(&s_rank, r) = j;
         }
-        if (p.logprobs) {
-          // log(w / kept): near 1 from the exact remainder, so that it keeps its relative precision
-          const float gone = as_float(kept.m - w) / as_float(kept.m);
-          p.logprobs[row] = gone < 0.5f ? log1pf(-gone) : logf(static_cast<float>(w) / as_float(kept.m));
-        }
+        drawn = w;
         break;
       }
       m = next;
@@ -552,51 +576,100 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   }
   cluster_sync_all();
 
-  // Back to the token: the (rank)-th occurrence of the key in index order.  A
-  // thread holds consecutive vectors, the ragged ends belong to the first and
-  // the last thread of the first and the last CTA.
+  if (drawn != 0 && p.logprobs) {
+    // log(w / kept): near 1 from the exact remainder, so that it keeps its relative precision
+    const float gone = as_float(kept.m - drawn) / as_float(kept.m);
+    p.logprobs[row] = gone < 0.5f ? log1pf(-gone) : logf(static_cast<float>(drawn) / as_float(kept.m));
+  }
+
+  // Back to the token: the (rank)-th occurrence of the key in index order, by
+  // blocks of 1024 vectors; the ragged ends are the first CTA's block before and
+  // the last CTA's block behind the vectors.
   const uint32_t key = s_key;
-  const int per = (v1 - v0 + kThreads - 1) / kThreads;
-  const int a = min(v1, v0 + tid * per), b = min(v1, a + per);
-  const bool owns_head = first && tid == 0, owns_tail = last && tid == kThreads - 1;
-  uint32_t n = 0;
-  if (owns_head)
-    for (int i = 0; i < head; ++i) n += key_of(base[i]) == key;
-#pragma unroll 4
-  for (int i = a; i < b; ++i) {
-    const uint4 v = __ldg(vec + i);
-    const uint32_t q[4] = {v.x, v.y, v.z, v.w};
+  const int blocks = (v1 - v0 + kThreads - 1) / kThreads;
+  // by their bit patterns: +0 and -0 are one key
+  const uint32_t bits1 = (key & 0x8000u) ? (key ^ 0x8000u) : (key ^ 0xFFFFu);
+  const uint32_t pattern = bits1 * 0x10001u, mask = bits1 == 0u ? 0x7FFF7FFFu : ~0u;
+  auto hits = [&](const uint4& v) {  // bit i: value i of the vector
+    const uint32_t x[4] = {(v.x & mask) ^ pattern, (v.y & mask) ^ pattern, (v.z & mask) ^ pattern, (v.w & mask) ^ pattern};
+    uint32_t any = 0, m = 0;  // any: a half of a word is 0
 #pragma unroll
-    for (int k = 0; k < 4; ++k) n += (key_of(q[k] & 0xFFFFu) == key) + (key_of(q[k] >> 16) == key);
-  }
-  if (owns_tail)
-    for (int i = tail; i < p.vocab; ++i) n += key_of(base[i]) == key;
-  uint32_t pre = n;
+    for (int k = 0; k < 4; ++k) any |= (x[k] - 0x00010001u) & ~x[k];
+    if (any & 0x80008000u) {
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const uint32_t v = __shfl_up_sync(~0u, pre, d);
-    if (lane >= d) pre += v;
+      for (int k = 0; k < 4; ++k)
+        m |= ((x[k] & 0xFFFFu) == 0u ? 1u << (2 * k) : 0u) | (x[k] < 0x10000u ? 2u << (2 * k) : 0u);
+    }
+    return m;
+  };
+  uint64_t found = 0;  // 8 bits a block
+  uint32_t ends = 0;   // of the ragged ends, this thread's value
+  if (first && tid < head) ends = key_of(base[tid]) == key;
+  if (last && tail + tid < p.vocab) ends |= (key_of(base[tail + tid]) == key) << 1;
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const int i = v0 + j * kThreads + tid;
+    if (i < v1) found |= static_cast<uint64_t>(hits(__ldg(vec + i))) << (8 * j);
   }
-  if (lane == 31) s_red[warp] = pre;
+  const uint32_t in_head = __popc(__ballot_sync(~0u, ends & 1u)), in_tail = __popc(__ballot_sync(~0u, ends & 2u));
+  if (tid == 0) {  // (fewer than 8 values: warp 0's)
+    s_ends[0] = in_head;
+    s_ends[1] = in_tail;
+  }
+  for (int j = 0; j < blocks; ++j) {
+    const uint32_t n = __reduce_add_sync(~0u, __popc(static_cast<uint32_t>(found >> (8 * j)) & 0xFFu));
+    if (lane == 0) s_block[j][warp] = n;
+  }
   __syncthreads();
-  uint32_t at = pre - n;
   if (warp == 0) {
-    const uint32_t all = __reduce_add_sync(~0u, s_red[lane]);
-    if (lane < CTAS) *peer(&s_own[rank], lane) = all;
+    uint32_t n = 0;
+    for (int j = 0; j < blocks; ++j) n += s_block[j][lane];
+    n = __reduce_add_sync(~0u, n) + s_ends[0] + s_ends[1];
+    if (lane < CTAS) *peer(&s_own[rank], lane) = n;
   }
-  for (int j = 0; j < warp; ++j) at += s_red[j];
   cluster_sync_all();  // no remote access is left
   uint32_t nth = s_rank;
-  for (int j = 0; j < static_cast<int>(rank); ++j) at += s_own[j];
-  if (at <= nth && nth < at + n) {
-    auto look = [&](uint32_t bits, int index) {
-      if (key_of(bits) == key && at++ == nth) p.tokens[row] = index;
-    };
-    if (owns_head)
-      for (int i = 0; i < head; ++i) look(base[i], i);
-    for (int i = head + 8 * a; i < head + 8 * b; ++i) look(base[i], i);
-    if (owns_tail)
-      for (int i = tail; i < p.vocab; ++i) look(base[i], i);
+  for (int j = 0; j < static_cast<int>(rank); ++j) {
+    if (nth < s_own[j]) return;
+    nth -= s_own[j];
+  }
+  if (nth >= s_own[rank]) return;
+  if (first) {
+    if (nth < s_ends[0]) {
+      const uint32_t heads = __ballot_sync(~0u, ends & 1u);
+      if (warp == 0 && (ends & 1u) && __popc(heads & ((1u << lane) - 1u)) == static_cast<int>(nth)) p.tokens[row] = tid;
+      return;
+    }
+    nth -= s_ends[0];
+  }
+  for (int j = 0; j < blocks; ++j) {
+    const uint32_t mine_n = s_block[j][lane];
+    const uint32_t all = __reduce_add_sync(~0u, mine_n);
+    if (nth >= all) {
+      nth -= all;
+      continue;
+    }
+    const uint32_t below = __reduce_add_sync(~0u, lane < warp ? mine_n : 0u);
+    const uint32_t bits = static_cast<uint32_t>(found >> (8 * j)) & 0xFFu;
+    uint32_t pre = __popc(bits);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t v = __shfl_up_sync(~0u, pre, d);
+      if (lane >= d) pre += v;
+    }
+    pre += below;
+    const uint32_t at = pre - __popc(bits);
+    if (at <= nth && nth < pre) {
+      uint32_t rest = bits;
+      for (uint32_t i = at; i < nth; ++i) rest &= rest - 1;
+      p.tokens[row] = head + 8 * (v0 + j * kThreads + tid) + __ffs(rest) - 1;
+    }
+    return;
+  }
+  // behind the vectors
+  if (warp == 0) {
+    const uint32_t tails = __ballot_sync(~0u, ends & 2u);
+    if ((ends & 2u) && __popc(tails & ((1u << lane) - 1u)) == static_cast<int>(nth)) p.tokens[row] = tail + tid;
   }
 }
 
