@@ -90,10 +90,10 @@ W4G128_API int w4g128_sample(const w4g128_sample_args* args, void* stream);
  * row's result whatever they hold, infinities and NaN included.
  *
  * Row m's bits depend on its own position, query and visible keys and values
- * alone, not on the other rows or sequences of the call, given the same
- * max_len, window, sinks and head_dim: a verify pass reproduces the
- * one-token steps (the split of a sequence into fixed chunks of positions
- * follows from those arguments).  Scores, the softmax statistics and the
+ * alone, not on the other rows of the call nor on max_new, given the same
+ * count, kv_heads, head_dim, max_len, window and sinks: a verify pass
+ * reproduces the one-token steps (the split of a sequence into fixed chunks of
+ * positions follows from those arguments).  Scores, the softmax statistics and the
  * output are held in fp32; the softmax weights enter the second product
  * rounded to bf16 and are summed as rounded, so they add up to 1. */
 typedef struct {

@@ -6,8 +6,8 @@
 // against every position, the work is the cache's bytes, and the point is to
 // read each byte once and keep enough of them in flight.
 //   * A sequence is cut into chunks of C positions at multiples of C; one CTA
-//     takes one (chunk, head, up to 64 rows).  C follows from max_len and the
-//     window alone, so a row's sums never depend on the rows beside it.
+//     takes one (chunk, head, up to 64 rows).  C follows from the cache's and
+//     the batch's shape alone, so a row's sums never depend on the rows beside it.
 //   * The CTA's groups of warps take the chunk's 16-position tiles in turn,
 //     each with its own ring of cp.async stages and its own running maximum
 //     and sum: no barrier of the whole CTA until the end.  A group is RT warps,
@@ -39,7 +39,7 @@ namespace w4g128 {
 namespace {
 
 constexpr int kTile = 16;        // positions per tile
-constexpr int kMaxChunk = 1024;  // positions per chunk, at most
+constexpr int kMaxChunk = 2048;  // positions per chunk, at most
 constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
@@ -640,14 +640,22 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   }
 }
 
-// Positions per chunk: a power of two that gives one sequence's heads about
-// kTarget CTAs over the longest span that its rows may see.
-constexpr int kTarget = 256;
+// Positions per chunk: the smallest power of two that keeps the call's chunks
+// (span x heads x sequences) at a few for each SM.  One sequence: 352, what two
+// CTAs of 32 rows an SM hold.  A batch: 608, as its sequences have lengths of
+// their own, half of max_len on average.  A window: 152, its spans are full and
+// its CTAs short.  Measured (attend kernel): one sequence of 32771, 8 heads of
+// 128, 32 rows: 30.3 us at chunks of 1024, 37.6 at 2048, 32.5 at 512 (CTAs of a
+// third more overhead); 16 sequences of up to 9008, 4 heads of 64: 19.6 us at
+// 1024, 24.5 at 256; two of window 4096, 4 heads of 256, 64 rows: 24.6 us at
+// 256, 31.2 at 128, 44.4 at 64.
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
+  const long long all = span * a.kv_heads * a.count;
+  const int target = a.window > 0 ? 152 : a.count == 1 ? 352 : 608;
   int chunk = 64;
-  while (chunk < kMaxChunk && static_cast<long long>(chunk) * kTarget < span * a.kv_heads) chunk *= 2;
+  while (chunk < kMaxChunk && static_cast<long long>(chunk) * target < all) chunk *= 2;
   return chunk;
 }
 

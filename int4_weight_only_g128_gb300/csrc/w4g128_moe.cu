@@ -1,14 +1,15 @@
 // The mixture-of-experts layer on packed int4-g128 experts (w4g128_moe), for
-// 1..16 rows: four programmatic dependent launches,
+// 1..16 rows: three or four programmatic dependent launches,
 //   route    one cluster of 8 CTAs: the logits of every (row, expert), the
 //            picks and weights of each row, the list of picked experts with the
 //            rows that each serves; the other CTAs put x in MMA operand order;
 //   expert 0 gate and up of the picked experts, silu(g) u -> activations;
 //   expert 1 down of the picked experts -> fp32 rows per (row, pick);
-//   combine  weighted sum over a row's picks, residual, bf16.
+//   combine  weighted sum over a row's picks, residual, bf16 (one or two rows:
+//            by the CTAs of expert 1).
 // The bytes are the picked experts' weights, read once: the expert kernels are
 // grouped weight streams.  One persistent kernel with grid barriers in place
-// of the last three launches measured slower (43.1 us against 38.9 us for one
+// of the expert kernels measured slower (43.1 us against 38.9 us for one
 // row, 5120 x 1408, 8 of 64 experts): a cooperative launch starts 2.7 us after
 // the routing, and a barrier costs 2 us more than the slowest CTA, where the
 // next launch's CTAs are on the SMs with their first copies already.
@@ -84,6 +85,7 @@ struct Params {
   uint8_t* act;       // [M top_k][F / 128][256]: activations (bf16) in operand order
   float* acts;        // [M top_k][F / 16]: sums of 16 activations
   float* part;        // [M top_k][D]
+  unsigned* done;     // [D / 32]: finished entries of the columns of a unit of expert 1
 };
 
 __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
@@ -244,6 +246,7 @@ __device__ __forceinline__ void pack_x(const Params& p) {
   const int lane = threadIdx.x & 31;
   const int warp = (blockIdx.x - kRouteCtas) * (kRouteThreads / 32) + threadIdx.x / 32;
   const int warps = (gridDim.x - kRouteCtas) * (kRouteThreads / 32);
+  for (int i = warp * 32 + lane; i < p.D / 32; i += warps * 32) p.done[i] = 0u;
   const uint32_t* xw = reinterpret_cast<const uint32_t*>(p.x);
   const int units = p.M * (p.D / 8);  // 16 bytes each, a multiple of 16
   for (int u0 = warp * 32; u0 < units; u0 += warps * 32) {
@@ -413,9 +416,70 @@ struct Stream {
   static constexpr int kBytes = kRing + 2 * kWarps * kPart * 4;
 };
 
+template <int TEAM>
+__device__ __forceinline__ void team_barrier(int team) {
+  asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
+}
+
+// Two neighbouring columns of y: the sum of the row's picks, and the residual.
+__device__ __forceinline__ void add_picks(const Params& p, int m, int n) {
+  float2 s = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int j = 0; j < p.top_k; ++j) {
+    const float w = __ldcg(p.weights + m * p.top_k + j);
+    const float2 v = __ldcg(reinterpret_cast<const float2*>(p.part + static_cast<long long>(m * p.top_k + j) * p.D + n));
+    s.x = fmaf(w, v.x, s.x);
+    s.y = fmaf(w, v.y, s.y);
+  }
+  const long long at = static_cast<long long>(m) * p.D + n;
+  if (p.residual) {
+    const uint32_t r = *reinterpret_cast<const uint32_t*>(p.residual + at);
+    s.x += low_f(r);
+    s.y += high_f(r);
+  }
+  const __nv_bfloat162 y = __floats2bfloat162_rn(s.x, s.y);
+  *reinterpret_cast<uint32_t*>(p.y + at) = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Params p) {
+  grid_dependency_wait();
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i < p.D / 2) add_picks(p, blockIdx.y, 2 * i);
+}
+
+// The same within expert 1, for one or two rows: a team counts its finished
+// units by their columns, 32 at a time or at its end, and who counts a column's
+// last entry adds up.  A launch less (small experts, one row: 18.8 -> 14.7 us);
+// with more rows the few teams that finish last add up everything, which took
+// longer than the launch (16 rows of 5120: 137 -> 162 us).
+template <int COLS, int TEAM>
+__device__ __forceinline__ void count_units(const Params& p, int entries, uint16_t* places, uint32_t* s_count, int team,
+                                            int member, int finished) {
+  const int lane = threadIdx.x & 31;
+  team_barrier<TEAM>(team);  // every member has written its rows
+  if (member == 0) {
+    bool last = false;
+    uint16_t place = 0;
+    if (lane < finished) {
+      place = places[lane];
+      __threadfence();
+      last = atomicAdd(p.done + place, 1u) == static_cast<unsigned>(entries) - 1u;
+      __threadfence();
+    }
+    const uint32_t mask = __ballot_sync(~0u, last);
+    if (last) places[__popc(mask & ((1u << lane) - 1u))] = place;
+    if (lane == 0) *s_count = __popc(mask);
+  }
+  team_barrier<TEAM>(team);
+  const int each = p.M * COLS / 2, total = static_cast<int>(*s_count) * each;
+  for (int o = member * 32 + lane; o < total; o += TEAM * 32)
+    add_picks(p, o % each / (COLS / 2), places[o / each] * COLS + o % (COLS / 2) * 2);
+}
+
 // PHASE 0: gate and up, a unit is TILES / 2 gate tiles and their up tiles; 1:
 // down, a unit is TILES neighbouring tiles.  TEAM: warps that share a unit.
-template <int PHASE, int TILES, int TEAM>
+// ADD: the rows' picks are added up here.
+template <int PHASE, int TILES, int TEAM, bool ADD>
 __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_constant__ Params p) {
   using S = Stream<TILES>;
   constexpr bool kBf16 = PHASE == 1;
@@ -427,6 +491,8 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ Lists lists;
   __shared__ uint32_t s_unit[kTeams][kQueue];
+  __shared__ uint16_t s_place[kTeams][32];  // places of finished units
+  __shared__ uint32_t s_last[kTeams];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);  // (uniform, and known to be)
   const int team = warp / TEAM, member = warp % TEAM;
@@ -596,6 +662,8 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     }
   };
 
+
+  [[maybe_unused]] int finished = 0;  // units that the team has not counted yet
   int seen = -1;
   for (int u = 0;; ++u) {
     const uint32_t unit = unit_at(u);
@@ -650,7 +718,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     // drawn unit's place in the queue, are free again once every member is past
     // the next one.
     if (draws) s_unit[team][(u + lead) % kQueue] = locate(kQueue * shares + draw);
-    asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(TEAM * 32) : "memory");
+    team_barrier<TEAM>(team);
     auto join = [&](const float* q) {  // (parts beyond the depth are 0)
       if constexpr (TEAM == 2) return q[0] + q[S::kPart];
       else if constexpr (TEAM == 4) return (q[0] + q[2 * S::kPart]) + (q[S::kPart] + q[3 * S::kPart]);
@@ -685,36 +753,17 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
         const int m = o / S::kCols, col = o % S::kCols;
         p.part[static_cast<long long>(lists.pick[first + m]) * p.D + at * kTileN + col] = join(part + m * S::kCols + col);
       }
+      if constexpr (ADD) {
+        if (member == 0 && lane == 0) s_place[team][finished] = static_cast<uint16_t>(at / kSide);
+        if (++finished == 32) {
+          count_units<S::kCols, TEAM>(p, lists.entries, s_place[team], &s_last[team], team, member, finished);
+          finished = 0;
+        }
+      }
     }
   }
-}
-
-// ---------------------------------------------------------------- combine
-__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Params p) {
-  grid_dependency_wait();
-  const int m = blockIdx.y, i = blockIdx.x * 128 + threadIdx.x;  // 4 columns
-  if (i >= p.D / 4) return;
-  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int j = 0; j < p.top_k; ++j) {
-    const float w = p.weights[m * p.top_k + j];
-    const float4 v = reinterpret_cast<const float4*>(p.part + static_cast<long long>(m * p.top_k + j) * p.D)[i];
-    s.x = fmaf(w, v.x, s.x);
-    s.y = fmaf(w, v.y, s.y);
-    s.z = fmaf(w, v.z, s.z);
-    s.w = fmaf(w, v.w, s.w);
-  }
-  const long long at = static_cast<long long>(m) * p.D + 4 * i;
-  if (p.residual) {
-    const uint2 r = *reinterpret_cast<const uint2*>(p.residual + at);
-    s.x += low_f(r.x);
-    s.y += high_f(r.x);
-    s.z += low_f(r.y);
-    s.w += high_f(r.y);
-  }
-  const __nv_bfloat162 a = __floats2bfloat162_rn(s.x, s.y), b = __floats2bfloat162_rn(s.z, s.w);
-  *reinterpret_cast<uint2*>(p.y + at) =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  if constexpr (ADD)
+    if (finished > 0) count_units<S::kCols, TEAM>(p, lists.entries, s_place[team], &s_last[team], team, member, finished);
 }
 
 int check(const w4g128_moe_args* a) {
@@ -733,7 +782,7 @@ int check(const w4g128_moe_args* a) {
 }
 
 struct Layout {
-  size_t lists, weights, xp, xs, act, acts, part, total;
+  size_t lists, weights, xp, xs, act, acts, part, done, total;
 };
 Layout layout(const w4g128_moe_args& a) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
@@ -746,20 +795,21 @@ Layout layout(const w4g128_moe_args& a) {
   l.act = l.xs + up(M * (a.D / 128) * 8);
   l.acts = l.act + up(picks * a.F * 2);
   l.part = l.acts + up(picks * (a.F / 16) * 4);
-  l.total = l.part + up(picks * a.D * 4);
+  l.done = l.part + up(picks * a.D * 4);
+  l.total = l.done + up(a.D / 32 * 4);
   return l;
 }
 
-template <int PHASE, int TILES, int TEAM>
+template <int PHASE, int TILES, int TEAM, bool ADD = false>
 cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, long long units) {
   constexpr int kBytes = Stream<TILES>::kBytes;
   const cudaError_t e =
-      cudaFuncSetAttribute(expert_kernel<PHASE, TILES, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+      cudaFuncSetAttribute(expert_kernel<PHASE, TILES, TEAM, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(2 * sms, units)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = kBytes;
-  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, TILES, TEAM>, p);
+  return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, TILES, TEAM, ADD>, p);
 }
 
 // Wide items, and small teams in the down projection, where each team then has
@@ -767,10 +817,16 @@ cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, lon
 cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
   const long long most = std::min(p.M * p.top_k, p.E);  // picked experts
   const long long gate = most * (p.F / 32), down = most * (p.D / 64);
-  const cudaError_t e = gate >= 8 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
-                                        : launch_expert<0, 2, 8>(cfg, p, sms, 2 * gate);
+  cudaError_t e = gate >= 8 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
+                                  : launch_expert<0, 2, 8>(cfg, p, sms, 2 * gate);
   if (e != cudaSuccess) return e;
-  return down >= 16 * sms ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
+  if (p.M <= 2) return launch_expert<1, 2, 8, true>(cfg, p, sms, 2 * down);
+  e = down >= 16 * sms ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
+  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3((p.D / 2 + 127) / 128, p.M);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, combine_kernel, p);
 }
 
 cudaError_t launch(const Params& p, cudaStream_t stream) {
@@ -789,12 +845,7 @@ cudaError_t launch(const Params& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kRouteThreads);
   e = p.M <= 8 ? cudaLaunchKernelEx(&cfg, route_kernel<false>, p) : cudaLaunchKernelEx(&cfg, route_kernel<true>, p);
   if (e != cudaSuccess) return e;
-  e = launch_experts(cfg, p, sms);
-  if (e != cudaSuccess) return e;
-  cfg.gridDim = dim3((p.D / 4 + 127) / 128, p.M);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, combine_kernel, p);
+  return launch_experts(cfg, p, sms);
 }
 
 }  // namespace
@@ -832,6 +883,7 @@ int w4g128_moe(const w4g128_moe_args* a, void* ws, size_t ws_bytes, void* stream
   p.act = base + l.act;
   p.acts = reinterpret_cast<float*>(base + l.acts);
   p.part = reinterpret_cast<float*>(base + l.part);
+  p.done = reinterpret_cast<unsigned*>(base + l.done);
   if (launch(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
     cudaGetLastError();
     return W4G128_ERR_CUDA;

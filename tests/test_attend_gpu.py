@@ -187,9 +187,9 @@ def test_a_row_alone_gives_the_same_bits(dim, window, sinks):
     together = c.run().clone()
     for b, (n, new) in enumerate(seqs):
         for i in (0, new // 2, new - 1):
-            one = Call([(n - new + i + 1, 1)], seed=5, **kw)
+            one = Call([(n - new + i + 1, 1), (0, 0), (0, 0), (0, 0)], seed=5, **kw)
             one.k_cache, one.v_cache, one.pages = c.k_cache, c.v_cache, c.pages
-            one.table = c.table[b:b + 1].clone()
+            one.table = c.table[b:b + 1].repeat(4, 1)
             r = c.offsets[b] + i
             one.q[0], one.k_new[0], one.v_new[0] = c.q[r], c.k_new[r], c.v_new[r]
             assert torch.equal(one.run()[0], together[r]), (b, i)
