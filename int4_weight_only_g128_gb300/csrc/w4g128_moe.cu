@@ -176,8 +176,18 @@ __device__ __forceinline__ void pick_row(const Params& p, int m, int slices, con
   int place = 0;  // by rising expert
   for (int j = 0; j < p.top_k; ++j) place += __shfl_sync(~0u, my_expert, j) < my_expert;
   if (lane < p.top_k) {
-    chosen[m * p.top_k + place] = static_cast<uint16_t>(my_expert);
     p.weights[m * p.top_k + place] = mine / all;
+    if (chosen != nullptr) {
+      chosen[m * p.top_k + place] = static_cast<uint16_t>(my_expert);
+    } else {  // one row: its picks are the lists
+      p.lists->expert[place] = static_cast<uint16_t>(my_expert);
+      p.lists->first[place] = static_cast<uint16_t>(place);
+      p.lists->pick[place] = static_cast<uint16_t>(place);
+      if (lane == 0) {
+        p.lists->entries = p.top_k;
+        p.lists->first[p.top_k] = static_cast<uint16_t>(p.top_k);
+      }
+    }
   }
 }
 
@@ -364,10 +374,11 @@ route_kernel(const __grid_constant__ Params p) {
   cluster_wait_acquire();
   const int m = rank + 8 * warp;  // two warps, a row each
   if (warp < 2 && m < p.M) {
-    uint16_t* chosen = static_cast<uint16_t*>(__cluster_map_shared_rank(s.chosen, 0));
+    uint16_t* chosen = p.M == 1 ? nullptr : static_cast<uint16_t*>(__cluster_map_shared_rank(s.chosen, 0));
     if (p.E <= 128) pick_row<4>(p, m, slices, s, chosen);
     else pick_row<W4G128_MAX_EXPERTS / 32>(p, m, slices, s, chosen);
   }
+  if (p.M == 1) return;  // (nothing is left in another CTA)
   cluster_arrive_release();
   cluster_wait_acquire();
   if (rank == 0) make_lists(p, s);
@@ -820,7 +831,7 @@ cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
   cudaError_t e = gate >= 8 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
                                   : launch_expert<0, 2, 8>(cfg, p, sms, 2 * gate);
   if (e != cudaSuccess) return e;
-  if (p.M <= 2) return launch_expert<1, 2, 8, true>(cfg, p, sms, 2 * down);
+  if (p.M <= 2) return launch_expert<1, 2, 4, true>(cfg, p, sms, 2 * down);
   e = down >= 16 * sms ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((p.D / 2 + 127) / 128, p.M);
