@@ -6,7 +6,9 @@ The bound.  One product sum_k x w of depth K = 128 G is built as scale d +
 1024 (gate and up) or 128 (down): with B = sum_k |x_k| (|min| + (2 b + 15)
 scale), the 16 MMAs of a group err by at most
 2 * 24 roundings of that size (a tensor core may truncate: 2^-23 each), the
-sum over groups and parts by G + 8 more, so e(K) = (G + 56) 2^-23 B.  An
+sum over groups and parts by G + 8 more, so e(K) = (G + 56) 2^-23 B.  x enters
+the first product as fp16 scaled by its row's largest value, off by at most
+2^-40 of that.  An
 activation a = silu(g) u moves by 1.1 |u| e_g + |silu(g)| e_u (|silu'| <= 1.1),
 4 fp32 roundings and exp's 2 ulp, and is rounded to bf16 (2^-8); the down
 product carries these through |w| and adds its own e(F); the weights p, from
@@ -110,6 +112,7 @@ class Layer:
                 continue
             W, B = self.gate_up.matrix(e, 1024)
             h, eh = x[rows] @ W, eps(self.D) * (x[rows].abs() @ B)
+            eh = eh + 2.0 ** -40 * x[rows].abs().amax(-1, keepdim=True) * W.abs().sum(0)
             gate, up, eg, eu = h[:, :self.F], h[:, self.F:], eh[:, :self.F], eh[:, self.F:]
             silu = gate * torch.sigmoid(gate)
             act = silu * up
