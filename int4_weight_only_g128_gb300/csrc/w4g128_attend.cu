@@ -174,7 +174,6 @@ attend_kernel(const __grid_constant__ Params p) {
   const int b = blockIdx.z, z = blockIdx.x;
 
   grid_dependency_wait();
-  grid_dependents_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) status_clear(p.status);
   const Seq s = sequence(p, b);
   if (!s.ok) {
