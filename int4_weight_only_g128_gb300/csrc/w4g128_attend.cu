@@ -54,7 +54,7 @@ struct Params {
   int chunk, splits;  // positions per chunk; chunks a sequence may need
   float scale2;       // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
   uint32_t flip_q, keep_q;
-  unsigned long long* status;
+  unsigned long long *status, *pending;
   float* part;        // [count][splits][kv_heads][max_new * group][head_dim]: unnormalised sums
   float2* stat;       // [count][splits][kv_heads][max_new * group]: maximum (base 2) and sum
 };
@@ -84,6 +84,19 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
   s.sink_chunks = min((s.sink + p.chunk - 1) / p.chunk, s.lo_chunk);
   s.chunks = s.ok && s.n > 0 && s.len > 0 ? s.sink_chunks + (s.len - 1) / p.chunk - s.lo_chunk + 1 : 0;
   return s;
+}
+
+// The sequence's length and rows, and the pages that its rows see.
+__device__ __forceinline__ bool in_range(const Params& p, int b) {
+  const Seq s = sequence(p, b);
+  bool ok = s.ok;
+  if (ok && s.n > 0) {
+    for (int a = 0; a < s.len; a += kTile) {
+      const int id = p.table[static_cast<long long>(b) * p.table_row + a / p.page_size];
+      ok = ok && ((a >= s.sink && a + kTile <= s.lo) || (id >= 0 && id < p.pages));
+    }
+  }
+  return ok;
 }
 
 __device__ __forceinline__ bool visible(const Params& p, int row_pos, int pos) {
@@ -174,15 +187,20 @@ attend_kernel(const __grid_constant__ Params p) {
   const int b = blockIdx.z, z = blockIdx.x;
 
   grid_dependency_wait();
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && tid == 0) status_clear(p.status);
+  const bool direct = p.splits == 1;  // (max_len is at most a chunk: this kernel is the call)
+  if (direct && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
+    bool bad = false;
+    for (int i = tid; i < p.count; i += S::kThreads) bad |= !in_range(p, i);
+    if (__syncthreads_or(bad)) bad = true;
+    if (tid == 0) st_relaxed_u64(p.status, bad ? W4G128_ERR_CACHE : W4G128_OK);
+  }
   const Seq s = sequence(p, b);
   if (!s.ok) {
-    if (z == 0 && blockIdx.y == 0 && tid == 0) status_error(p.status, W4G128_ERR_CACHE);
+    if (z == 0 && blockIdx.y == 0 && tid == 0) note_error(p.pending, W4G128_ERR_CACHE);
     return;
   }
   const int live_rows = s.n * p.group;
   if (rg * 16 * RT >= live_rows) return;
-  const bool direct = p.splits == 1;
   if (z >= s.chunks && !(direct && z == 0)) return;  // (direct: empty rows are written as zeros)
 
   const int p0 = s.chunks ? s.chunk_id(z) * p.chunk : 0;
@@ -196,7 +214,7 @@ attend_kernel(const __grid_constant__ Params p) {
     const bool seen = a < s.sink || (a + kTile > s.lo && a < s.len);
     const int id = seen ? p.table[static_cast<long long>(b) * p.table_row + a / p.page_size] : -1;
     const bool ok = id >= 0 && id < p.pages;
-    if (seen && !ok) status_error(p.status, W4G128_ERR_CACHE);
+    if (seen && !ok) note_error(p.pending, W4G128_ERR_CACHE);
     s_tile[t] = ok ? id * p.page_stride + (a % p.page_size) * p.slot_stride + head * p.head_stride : -1;
   }
 
@@ -577,6 +595,7 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
+  if (b == 0 && i == 0 && hq == 0 && threadIdx.x == 0) publish_errors(p.status, p.pending);
   const Seq s = sequence(p, b);
   if (!s.ok || i >= s.n) return;
   const int head = hq / p.group, row = i * p.group + hq % p.group;
@@ -761,6 +780,7 @@ int w4g128_attend(const w4g128_attend_args* a, void* ws, size_t ws_bytes, void* 
   p.keep_q = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
   auto* base = static_cast<uint8_t*>(ws);
   p.status = reinterpret_cast<unsigned long long*>(base);
+  p.pending = p.status + 1;
   p.part = reinterpret_cast<float*>(base + kStatusBytes);
   p.stat = reinterpret_cast<float2*>(p.part + static_cast<size_t>(p.count) * p.splits * p.q_heads * p.max_new * a->head_dim);
   cudaLaunchAttribute attr[1];

@@ -1,7 +1,10 @@
-// The status word of an operator call (byte 0 of its workspace's first 64-bit
-// word, as w4g128_workspace_status reads it), tagged with the launch that wrote
-// it: a CTA that fails and the CTA that clears the word may come in any order,
-// without a launch that zeroes it.
+// Errors that an operator's kernels find in device memory, on their way to the
+// status word (the first word of the workspace, as w4g128_workspace_status
+// reads it).  Any CTA of the first kernel may note one in a pending word; the
+// last kernel of the call moves it to the status word and leaves "none" behind.
+// The pending word needs no zeroing: without its mark it counts as "none".  (A
+// tag of the launch in its place fails in a CUDA graph, whose replays all have
+// the same grid number.)
 #pragma once
 #include <cstdint>
 
@@ -9,35 +12,23 @@
 
 namespace w4g128 {
 
-// The upper 56 bits of this launch's words: its grid number through an odd
-// multiplier, so that leftover workspace bytes are unlikely to look like it.
-__device__ __forceinline__ unsigned long long launch_tag() {
-  unsigned long long g;
-  asm volatile("mov.u64 %0, %%gridid;" : "=l"(g));
-  return ((g + 1ull) * 0x9E3779B97F4A7C15ull) & ~0xFFull;
-}
+constexpr unsigned long long kPendingMark = 0x50656E64696E6700ull;  // "Pending" above the code's byte
 
-// One thread of the launch: the word says "no error" unless a thread of this
-// launch has failed.
-__device__ __forceinline__ void status_clear(unsigned long long* word) {
-  const unsigned long long tag = launch_tag();
-  unsigned long long cur = ld_relaxed_u64(word);
-  while ((cur & ~0xFFull) != tag) {
-    const unsigned long long prev = atomicCAS(word, cur, tag);
+// The first error of a call stays.
+__device__ __forceinline__ void note_error(unsigned long long* pending, unsigned code) {
+  unsigned long long cur = ld_relaxed_u64(pending);
+  while ((cur & ~0xFFull) != kPendingMark || (cur & 0xFFull) == 0ull) {
+    const unsigned long long prev = atomicCAS(pending, cur, kPendingMark | code);
     if (prev == cur) return;
     cur = prev;
   }
 }
 
-// The first failure of this launch stays.
-__device__ __forceinline__ void status_error(unsigned long long* word, unsigned code) {
-  const unsigned long long tag = launch_tag();
-  unsigned long long cur = ld_relaxed_u64(word);
-  while ((cur & ~0xFFull) != tag || (cur & 0xFFull) == 0ull) {
-    const unsigned long long prev = atomicCAS(word, cur, tag | code);
-    if (prev == cur) return;
-    cur = prev;
-  }
+// One thread of the last kernel.
+__device__ __forceinline__ void publish_errors(unsigned long long* status, unsigned long long* pending) {
+  const unsigned long long v = ld_relaxed_u64(pending);
+  st_relaxed_u64(status, (v & ~0xFFull) == kPendingMark ? v & 0xFFull : 0ull);
+  st_relaxed_u64(pending, kPendingMark);
 }
 
 }  // namespace w4g128

@@ -334,3 +334,74 @@ def test_workspace_is_not_exceeded():
     w.w4g128_attend(args, whole[4096:], ws_bytes=nb)
     torch.cuda.synchronize()
     assert (whole[:4096] == 0x5A).all() and (whole[4096 + nb:] == 0x5A).all()
+
+
+@pytest.mark.gpu
+def test_status_of_replayed_calls():
+    """A replay with a length out of range reports it, the next good one does not."""
+    c = Call([(100, 2), (60, 1)], max_len=112, seed=11)
+    want = c.run().clone()
+    args = c.args()
+    ws = torch.empty(w.w4g128_attend_workspace_bytes(args), dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.w4g128_attend(args, ws)
+    for length, status in ((60, 0), (500, w.ERR_CACHE), (60, 0), (-1, w.ERR_CACHE), (60, 0)):
+        c.lens[1] = length
+        g.replay()
+        torch.cuda.synchronize()
+        assert w.w4g128_workspace_status(ws) == status, length
+    assert torch.equal(c.out.view(c.rows, c.Hq, c.D), want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
+def test_scales(dim, scale):
+    """Negative scales prefer the smallest scores, 0 makes every visible position count the same."""
+    c = Call([(300, 4), (40, 16)], dim=dim, seed=12, window=150, sinks=2)
+    c.scale = scale
+    c.check()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    calls = [Call([(3000, 8)], q_heads=16, kv_heads=4, dim=128, seed=s) for s in (13, 14)]
+    want = [c.run().clone() for c in calls]
+    steps, streams = [], [torch.cuda.Stream() for _ in calls]
+    for c, s in zip(calls, streams):
+        c.out.fill_(7.0)
+        a = c.args()
+        steps.append(w.AttendStep(a, torch.empty(w.w4g128_attend_workspace_bytes(a), dtype=torch.uint8, device="cuda"),
+                                  stream=s))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st in steps:
+            st.run()
+    torch.cuda.synchronize()
+    for c, o in zip(calls, want):
+        assert torch.equal(c.out.view(c.rows, c.Hq, c.D)[:8], o[:8])
+
+
+@pytest.mark.gpu
+def test_pages_shared_by_sequences():
+    """Two sequences with a common prefix in the same pages, each with new tokens of its own."""
+    c = Call([(70, 3), (68, 1)], page=16, seed=15)
+    c.table[1, :4] = c.table[0, :4]  # positions 0..63; both sequences' new tokens lie behind
+    c.check()
+
+
+@pytest.mark.gpu
+def test_errors_of_calls_of_one_chunk():
+    """Short caches take a single kernel, which reports by itself."""
+    c = Call([(40, 2), (30, 1), (0, 0)], max_len=48, seed=16)
+    clean = c.check().clone()
+    for field, at, wrong in ((c.lens, 1, 49), (c.lens, 1, -7), (c.table, (1, 0), c.pages), (c.table, (1, 1), -1),
+                             (c.offsets_d, 2, 1)):
+        keep = field[at].item()
+        field[at] = wrong
+        got = c.run(status=w.ERR_CACHE)
+        assert torch.equal(got[:2], clean[:2])
+        field[at] = keep
+    c.table[1, 2] = -9  # behind the length: not seen
+    assert torch.equal(c.run(), clean)

@@ -139,7 +139,7 @@ class Layer:
 SHAPES = [(1, 128, 128, 1, 1), (1, 256, 128, 4, 2), (2, 128, 384, 5, 5), (3, 640, 256, 7, 3), (8, 512, 128, 16, 4),
           (9, 384, 640, 12, 2), (13, 1152, 384, 37, 3), (16, 256, 256, 3, 2), (16, 512, 512, 64, 6), (5, 1280, 1024, 9, 4),
           (16, 128, 128, 512, 16), (1, 2048, 768, 24, 16),
-          (16, 2048, 1408, 40, 5)]
+          (16, 2048, 1408, 40, 5), (2, 8192, 128, 2, 1), (3, 128, 8192, 2, 2), (1, 16384, 256, 2, 2)]
 
 
 @pytest.mark.gpu
@@ -244,3 +244,36 @@ def test_streams_graph_replay_and_reused_workspace():
         torch.cuda.synchronize()
         assert w.w4g128_workspace_status(ws) == 0
         assert torch.equal(y, layer.run())
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    layers = [Layer(3, 1024, 512, 16, 4, seed=s) for s in (8, 9)]
+    want = [m.run().clone() for m in layers]
+    ys, steps = [], []
+    for m in layers:
+        y = torch.zeros_like(want[0])
+        a = m.args(y)
+        ys.append(y)
+        steps.append(w.MoEStep(a, torch.empty(w.w4g128_moe_workspace_bytes(a), dtype=torch.uint8, device="cuda"),
+                               stream=torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s in steps:
+            s.run()
+    torch.cuda.synchronize()
+    assert torch.equal(ys[0], want[0]) and torch.equal(ys[1], want[1])
+
+
+@pytest.mark.gpu
+def test_logits_that_are_not_numbers_rank_last():
+    """A router row of NaN: its expert is picked only where no other is left."""
+    layer = Layer(2, 128, 128, 4, 2, seed=10)
+    layer.router[1] = float("nan")
+    layer.router[2] = float("nan")
+    got = layer.run()
+    layer.router[1] = layer.router[0]
+    layer.router[2] = layer.router[0]
+    ref = Layer(2, 128, 128, 4, 2, seed=10)
+    ref.router[1:3] = -1e30 * torch.sign(ref.x[0].float()).bfloat16()  # far below for row 0
+    assert torch.equal(got[0], ref.run()[0])

@@ -237,3 +237,30 @@ def test_null_filters_streams_and_graph_replay():
         for r in range(2):
             t, _, near = reference(logits[r].double().cpu().numpy(), 1.0, 0, 1.0, 0.0, float(u[r]))
             assert near or tokens[r].item() == t
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,V", [(1, 262144), (9, 262144), (16, 262144), (24, 50000), (40, 300000), (300, 777),
+                                    (w.MAX_SAMPLE_ROWS, 64)])
+def test_many_rows(rows, V):
+    """More rows than fit on the GPU at once, and every cluster size."""
+    rng = np.random.default_rng(rows)
+    z = rng.normal(0, 3, (rows, V)).astype(np.float32)
+    few = np.arange(rows) if rows <= 64 else np.array([0, 1, rows // 2, rows - 1])
+    u = rng.random(rows)
+    tok, lp, zz = draw(z, T=0.9, k=50, p=0.9, u=u)
+    for r in few:
+        t, l, near = reference(zz[r], float(np.float32(0.9)), 50, float(np.float32(0.9)), 0.0, float(np.float32(u[r])))
+        assert near or (tok[r] == t and abs(lp[r] - l) <= 4 * 2.0 ** -23 * abs(l) + 1e-45), r
+
+
+@pytest.mark.gpu
+def test_the_cluster_size_changes_no_bit():
+    """The same row alone, among 9, 16 and 30: 16, 8, 6 and 4 CTAs."""
+    rng = np.random.default_rng(21)
+    z = rng.normal(0, 3, (30, 100000))
+    u = rng.random(30)
+    t30, l30, _ = draw(z, T=1.1, p=0.97, u=u)
+    for n in (1, 9, 16):
+        t, l, _ = draw(z[:n], T=1.1, p=0.97, u=u[:n])
+        assert np.array_equal(t, t30[:n]) and np.array_equal(l.view(np.int32), l30[:n].view(np.int32))
