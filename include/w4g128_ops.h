@@ -151,11 +151,13 @@ W4G128_API int w4g128_attend(const w4g128_attend_args* args, void* ws, size_t ws
  *                 first among equals (a NaN logit ranks last)
  *   p[m][e]     = exp(logit[m][e]) / sum exp(logit[m][e']), the sum over S(m)
  *                 (renormalize = 1) or over all experts (renormalize = 0)
- *   a[m][e][f]  = bf16( silu(g_f) u_f ), (g, u) = x[m] . dequant(gate_up_e)
+ *   a[m][e][f]  = r( silu(g_f) u_f ), (g, u) = x[m] . dequant(gate_up_e)
  *   y[m][n]     = bf16( residual[m][n] + sum_{e in S(m)} p[m][e] (a[m][e] . dequant(down_e))[n] )
- * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)); the
- * activations a are rounded to bf16 because they are the operand of the second
- * product.  Only the experts that some row picks are read, each once.
+ * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)).  The
+ * activations a are the operand of the second product and rounded for it: r
+ * keeps 11 significant bits (fp16 scaled by the largest of 16 neighbours), and
+ * nothing below 2^-39 of the largest activation of the row and expert.  Only
+ * the experts that some row picks are read, each once.
  *
  * gate_up_e is a K = D, N = 2 F matrix (F gate columns, then F up columns),
  * down_e a K = F, N = D one, each packed as w4g128_pack writes it; the E

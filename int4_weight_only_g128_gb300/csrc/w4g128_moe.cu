@@ -21,12 +21,16 @@
 // one lane per item: 409 instructions an item against 265).  The item's product
 // is one warp MMA per packed word: the 16 columns are the A operand, the rows
 // that picked the expert the B columns.
-//   gate and up: x as fp16, each row scaled by the power of two that puts its
-//     largest magnitude in [2^14, 2^15) (values down to 2^-31 of it are exact,
-//     smaller ones off by at most 2^-40 of it), weights as fp16 1024 + q and
-//     1024 + 16 q, both from one word with one shift and four LOP3;
-//   down: activations as bf16 (their range is not known when they are
-//     rounded), weights as bf16 128 + q, with two more shifts a word.
+// x and the activations enter as fp16, a row scaled by the power of two that
+// puts its largest magnitude in [2^14, 2^15); the weights as fp16 1024 + q and
+// 1024 + 16 q, both from one word with one shift and four LOP3 (bf16 takes two
+// shifts more: 48.4 against 46.6 us, the down projection of 16 rows of 5120).
+//   gate and up: x is bf16; values down to 2^-31 of the row's largest are
+//     exact, smaller ones off by at most 2^-40 of it;
+//   down: an activation is rounded to fp16 where it is computed, scaled by its
+//     16-column tile's largest, since the row's is not known yet (2^-12
+//     relative, an eighth of bf16's rounding); the tile's exponent goes along,
+//     and the operand is brought to the row's exponent when it is used.
 // The bias and the group minimum are undone by X = sum_k x per (row, group):
 //   sum_k x w = scale sum_k x (bias + q) + (min - bias scale) X,
 // and an MMA with an all-ones A leaves X in the registers that need it, once
@@ -58,10 +62,8 @@ constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kParts = 8;             // partial sums of a unit
 constexpr size_t kStatusBytes = 256;
-constexpr uint32_t kBias16 = 0x64006400u;   // fp16 1024.0 twice
-constexpr uint32_t kBiasB16 = 0x43004300u;  // bf16 128.0 twice
-constexpr uint32_t kOne16 = 0x3C003C00u;    // fp16 1.0 twice
-constexpr uint32_t kOneB16 = 0x3F803F80u;   // bf16 1.0 twice
+constexpr uint32_t kBias = 0x64006400u;  // fp16 1024.0 twice
+constexpr uint32_t kOne = 0x3C003C00u;   // fp16 1.0 twice
 
 // Picked experts in rising order with the picks (row * top_k + place, places in
 // rising expert order) that each serves: one entry for up to 8 rows, what an
@@ -86,7 +88,9 @@ struct Params {
   float* weights;     // [M][top_k], by pick
   uint8_t* xp;        // [M][D / 128][256]: x as scaled fp16 in operand order
   float* unscale;     // [M]: the factor that undoes the scale
-  uint8_t* act;       // [M top_k][F / 128][256]: activations (bf16) in operand order
+  uint8_t* act;       // [M top_k][F / 128][256]: activations as scaled fp16 in operand order
+  uint8_t* act_exp;   // [M top_k][F / 16]: the biased exponents of the tiles' largest
+  unsigned* act_top;  // [M top_k]: the largest of them
   float* part;        // [M top_k][D]
   unsigned* done;     // [D / 32]: finished entries of the columns of a unit of expert 1
 };
@@ -252,6 +256,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// For a biased exponent e of a largest magnitude: 2^s that brings it to [2^14,
+// 2^15), and 2^-s, both normal for 15 <= e <= 254.
+__device__ __forceinline__ float scale_up(int e) { return __int_as_float((268 - e) << 23); }
+__device__ __forceinline__ float scale_back(int e) { return __int_as_float((e - 14) << 23); }
+__device__ __forceinline__ int exponent_of(float top) {
+  return min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
+}
+
 // x in operand order, by the clusters behind the routing one, a row a CTA.  The scale puts the row's largest magnitude in [2^14, 2^15).
 __device__ __forceinline__ void pack_x(const Params& p) {
   __shared__ float s_top[kRouteThreads / 32];
@@ -274,11 +286,9 @@ __device__ __forceinline__ void pack_x(const Params& p) {
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < kRouteThreads / 32; ++j) top = fmaxf(top, s_top[j]);
-    // 2^s with s = 14 - exponent(top), kept where 2^s and 2^-s are normal
-    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-    const int s = min(max(14 - ex, -113), 126);
-    const float up = __int_as_float((127 + s) << 23);
-    if (tid == 0) p.unscale[m] = __int_as_float((127 - s) << 23);
+    const int e = exponent_of(top);
+    const float up = scale_up(e);
+    if (tid == 0) p.unscale[m] = scale_back(e);
     const uint32_t* words = reinterpret_cast<const uint32_t*>(x);
     for (int u = tid; u < units; u += kRouteThreads) {
       const int group = u / 16, i = u / 4 % 4, c = u % 4;
@@ -329,6 +339,7 @@ route_kernel(const __grid_constant__ Params p) {
       *reinterpret_cast<unsigned long long*>(p.status) = 0ull;
       p.next[0] = p.next[1] = 0u;
     }
+    if (tid < p.M * p.top_k) p.act_top[tid] = 0u;
     for (int e = tid; e < W4G128_MAX_EXPERTS / 2; e += kRouteThreads) reinterpret_cast<uint32_t*>(s.rows)[e] = 0u;
   }
   const uint4* xa = reinterpret_cast<const uint4*>(p.x + static_cast<long long>(min(r, p.M - 1)) * p.D) + c;
@@ -382,34 +393,24 @@ route_kernel(const __grid_constant__ Params p) {
 }
 
 // ---------------------------------------------------------------- expert streams
-template <bool BF16>
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  if constexpr (BF16)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// The A fragment of one packed word.  fp16: columns r as 1024 + q, columns
-// r + 8 as 1024 + 16 q.  bf16: 128 + q.
-template <bool BF16>
+// The A fragment of one packed word: columns r as 1024 + q, columns r + 8 as 1024 + 16 q.
 __device__ __forceinline__ void operand(uint32_t w, uint32_t (&a)[4]) {
-  if constexpr (BF16) {
-    a[0] = lop3_and_or(w, 0x000F000Fu, kBiasB16);
-    a[1] = lop3_and_or(w >> 4, 0x000F000Fu, kBiasB16);
-    a[2] = lop3_and_or(w >> 8, 0x000F000Fu, kBiasB16);
-    a[3] = lop3_and_or(w >> 12, 0x000F000Fu, kBiasB16);
-  } else {
-    const uint32_t v = w >> 8;
-    a[0] = lop3_and_or(w, 0x000F000Fu, kBias16);
-    a[1] = lop3_and_or(w, 0x00F000F0u, kBias16);
-    a[2] = lop3_and_or(v, 0x000F000Fu, kBias16);
-    a[3] = lop3_and_or(v, 0x00F000F0u, kBias16);
-  }
+  const uint32_t v = w >> 8;
+  a[0] = lop3_and_or(w, 0x000F000Fu, kBias);
+  a[1] = lop3_and_or(w, 0x00F000F0u, kBias);
+  a[2] = lop3_and_or(v, 0x000F000Fu, kBias);
+  a[3] = lop3_and_or(v, 0x00F000F0u, kBias);
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // TILES of 16 columns per item: 2, or 4 where there are units enough for every
@@ -490,7 +491,6 @@ __device__ __forceinline__ void count_units(const Params& p, int entries, uint16
 template <int PHASE, int TILES, int TEAM, bool ADD>
 __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_constant__ Params p) {
   using S = Stream<TILES>;
-  constexpr bool kBf16 = PHASE == 1;
   constexpr int kSide = PHASE == 0 ? TILES / 2 : TILES;  // neighbouring tiles
   constexpr int kTeams = kWarps / TEAM;
   constexpr int kMine = kParts / TEAM;  // parts of a unit that one warp sums
@@ -612,34 +612,61 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 
   // This lane's part of an item's B operand: of row r of the entry.  Columns
   // beyond the entry's rows repeat the last row; nothing of theirs is kept.
+  struct Operand {
+    uint4 v[4];
+    uint2 exps;  // PHASE 1: of the group's 8 tiles
+    int scale;   // of the row: PHASE 0 the bits of what undoes it, 1 the exponent
+  };
   int x_entry = -1;
-  const uint8_t* x_row = nullptr;
-  auto load_x = [&](uint32_t which, uint4 (&v)[4]) {
+  const uint8_t *x_row = nullptr, *x_exps = nullptr;
+  const int* x_scale = nullptr;
+  auto load_x = [&](uint32_t which, Operand& x) {  // (nothing here waits for a load)
     if (which == kEnd) return;
-    const int a = static_cast<int>(which >> 16);
+    const int a = static_cast<int>(which >> 16), group = static_cast<int>(which & 0xFFFFu);
     if (a != x_entry) {
       x_entry = a;
       const int pick = lists.pick[min(lists.first[a] + r, lists.first[a + 1] - 1)];
-      x_row = (PHASE == 0 ? p.xp : p.act) + static_cast<long long>(PHASE == 0 ? pick / p.top_k : pick) * K * 2 + 16 * c;
+      const int row = PHASE == 0 ? pick / p.top_k : pick;
+      x_row = (PHASE == 0 ? p.xp : p.act) + static_cast<long long>(row) * K * 2 + 16 * c;
+      x_scale = (PHASE == 0 ? reinterpret_cast<const int*>(p.unscale) : reinterpret_cast<const int*>(p.act_top)) + row;
+      if (PHASE == 1) x_exps = p.act_exp + static_cast<long long>(row) * (G * 8);
     }
-    const uint8_t* x = x_row + (which & 0xFFFFu) * 256;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = *reinterpret_cast<const uint4*>(x + i * 64);
+    for (int i = 0; i < 4; ++i) x.v[i] = *reinterpret_cast<const uint4*>(x_row + group * 256 + i * 64);
+    if (PHASE == 1) x.exps = *reinterpret_cast<const uint2*>(x_exps + group * 8);
+    x.scale = *x_scale;
   };
   __syncwarp();
   int next_slot = 1;  // of the item after the current one
-  uint4 xv[4] = {};
-  load_x(s_item[warp][0], xv);
+  Operand x = {};
+  load_x(s_item[warp][0], x);
+  int scale = 0;  // of row r of the unit in hand
 
   auto item = [&](float (&acc)[TILES][4]) {
-    uint4 xn[4];
+    Operand xn = {};
     load_x(s_item[warp][next_slot], xn);
     next_slot = next_slot == S::kStages ? 0 : next_slot + 1;
+    scale = x.scale;
+    if (PHASE == 1) {  // a tile is a k step: to the row's exponent
+#pragma unroll
+      for (int s = 0; s < 8; ++s) {
+        const int e = static_cast<int>((s < 4 ? x.exps.x : x.exps.y) >> (8 * (s % 4)) & 0xFFu);
+        const float f = __int_as_float(max(127 + e - x.scale, 0) << 23);
+        const __half2 h = __floats2half2_rn(f, f);
+        const uint32_t f2 = *reinterpret_cast<const uint32_t*>(&h);
+        if (s % 2) {
+          x.v[s / 2].z = hmul2(x.v[s / 2].z, f2);
+          x.v[s / 2].w = hmul2(x.v[s / 2].w, f2);
+        } else {
+          x.v[s / 2].x = hmul2(x.v[s / 2].x, f2);
+          x.v[s / 2].y = hmul2(x.v[s / 2].y, f2);
+        }
+      }
+    }
     asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
     __syncwarp();
     const uint8_t* st = ring_ptr + stage * S::kStage;
     float d[TILES][4] = {}, X[4] = {};
-    constexpr uint32_t kOne = kBf16 ? kOneB16 : kOne16;
     const uint32_t ones[4] = {kOne, kOne, kOne, kOne};
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -649,13 +676,13 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int s = 4 * h + j;
-        const uint32_t b0 = s % 2 ? xv[s / 2].z : xv[s / 2].x, b1 = s % 2 ? xv[s / 2].w : xv[s / 2].y;
-        mma<kBf16>(X, ones, b0, b1);
+        const uint32_t b0 = s % 2 ? x.v[s / 2].z : x.v[s / 2].x, b1 = s % 2 ? x.v[s / 2].w : x.v[s / 2].y;
+        mma(X, ones, b0, b1);
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
           uint32_t w[4];
-          operand<kBf16>(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, w);
-          mma<kBf16>(d[t], w, b0, b1);
+          operand(j == 0 ? q[t].x : j == 1 ? q[t].y : j == 2 ? q[t].z : q[t].w, w);
+          mma(d[t], w, b0, b1);
         }
       }
     }
@@ -668,17 +695,16 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 #pragma unroll
     for (int t = 0; t < TILES; ++t) {
       float s0 = low_f(meta[t].x), s1 = low_f(meta[t].y);
-      const float b0 = fmaf(kBf16 ? -128.f : -1024.f, s0, high_f(meta[t].x));
-      const float b1 = fmaf(kBf16 ? -128.f : -64.f, s1, high_f(meta[t].y));
-      if (!kBf16) s1 *= 0.0625f;  // these columns carry 16 q
+      const float b0 = fmaf(-1024.f, s0, high_f(meta[t].x));
+      const float b1 = fmaf(-64.f, s1, high_f(meta[t].y));
+      s1 *= 0.0625f;  // these columns carry 16 q
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         acc[t][k] = fmaf(s0, d[t][k], fmaf(b0, X[k], acc[t][k]));
         acc[t][2 + k] = fmaf(s1, d[t][2 + k], fmaf(b1, X[k], acc[t][2 + k]));
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) xv[i] = xn[i];
+    x = xn;
   };
 
   [[maybe_unused]] int finished = 0;  // units that the team has not counted yet
@@ -710,15 +736,18 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 #pragma unroll
         for (int i = 0; i < 4; ++i) sum[t][i] = q == 0 ? two[t][i] : sum[t][i] + two[t][i];
     }
+    const float back = PHASE == 0 ? __int_as_float(scale) : scale_back(max(scale, 15));
     float* out = part + mine * S::kPart + 2 * c * S::kCols + r;
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k) {
+      const float f = __shfl_sync(~0u, back, (2 * c + k) * 4);  // of row 2c + k (a warp without items: of no matter)
       if (2 * c + k < count)
 #pragma unroll
         for (int t = 0; t < TILES; ++t) {
-          out[k * S::kCols + t * kTileN] = sum[t][k];
-          out[k * S::kCols + t * kTileN + 8] = sum[t][2 + k];
+          out[k * S::kCols + t * kTileN] = sum[t][k] * f;
+          out[k * S::kCols + t * kTileN + 8] = sum[t][2 + k] * f;
         }
+    }
     // One barrier of the team per unit: the other half of the buffer, and the
     // drawn unit's place in the queue, are free again once every member is past
     // the next one.
@@ -735,15 +764,24 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     const int from = ((member + u) % TEAM) * 32 + lane;
     if (PHASE == 0) {
       constexpr int kGate = kSide * kTileN;  // columns of activations
-      for (int o = from; o < count * kGate; o += TEAM * 32) {
+      const unsigned tile_lanes = 0xFFFFu << (lane & 16);
+      for (int o = from; o < count * kGate; o += TEAM * 32) {  // 16 lanes a tile
         const int m = o / kGate, col = o % kGate, n = at * kTileN + col;
         const int pick = lists.pick[first + m];
-        const float f = __ldcg(p.unscale + pick / p.top_k);
-        const float v = join(part + m * S::kCols + col) * f, w = join(part + m * S::kCols + col + kGate) * f;
+        const float v = join(part + m * S::kCols + col), w = join(part + m * S::kCols + col + kGate);
+        const float act = v / (1.f + expf(-v)) * w;
+        float top = fabsf(act);
+#pragma unroll
+        for (int k = 8; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(tile_lanes, top, k));
+        const int e = exponent_of(top);
         // column n: k step n / 16 % 8 of its group
         uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + n / 128 * 256 + n / 32 % 4 * 64 + n % 8 / 2 * 16 +
                        (n / 16 % 2 * 2 + n / 8 % 2) * 4 + (n & 1) * 2;
-        *reinterpret_cast<__nv_bfloat16*>(dst) = __float2bfloat16_rn(v / (1.f + expf(-v)) * w);
+        *reinterpret_cast<__half*>(dst) = __float2half_rn(act * scale_up(e));
+        if (lane % 16 == 0) {
+          p.act_exp[static_cast<long long>(pick) * (p.F / kTileN) + n / kTileN] = static_cast<uint8_t>(e);
+          atomicMax(p.act_top + pick, static_cast<unsigned>(e));
+        }
       }
     } else {
       for (int o = from; o < count * S::kCols; o += TEAM * 32) {
@@ -779,7 +817,7 @@ int check(const w4g128_moe_args* a) {
 }
 
 struct Layout {
-  size_t lists, weights, xp, unscale, act, part, done, total;
+  size_t lists, weights, xp, unscale, act, act_exp, act_top, part, done, total;
 };
 Layout layout(const w4g128_moe_args& a) {
   auto up = [](size_t n) { return (n + 255) & ~static_cast<size_t>(255); };
@@ -790,7 +828,9 @@ Layout layout(const w4g128_moe_args& a) {
   l.xp = l.weights + up(picks * 4);
   l.unscale = l.xp + up(M * a.D * 2);
   l.act = l.unscale + up(M * 4);
-  l.part = l.act + up(picks * a.F * 2);
+  l.act_exp = l.act + up(picks * a.F * 2);
+  l.act_top = l.act_exp + up(picks * (a.F / 16));
+  l.part = l.act_top + up(picks * 4);
   l.done = l.part + up(picks * a.D * 4);
   l.total = l.done + up(a.D / 32 * 4);
   return l;
@@ -878,6 +918,8 @@ int w4g128_moe(const w4g128_moe_args* a, void* ws, size_t ws_bytes, void* stream
   p.xp = base + l.xp;
   p.unscale = reinterpret_cast<float*>(base + l.unscale);
   p.act = base + l.act;
+  p.act_exp = base + l.act_exp;
+  p.act_top = reinterpret_cast<unsigned*>(base + l.act_top);
   p.part = reinterpret_cast<float*>(base + l.part);
   p.done = reinterpret_cast<unsigned*>(base + l.done);
   if (launch(p, static_cast<cudaStream_t>(stream)) != cudaSuccess) {

@@ -3,15 +3,17 @@ bits, from the canonical codes, scales and minima.
 
 The bound.  One product sum_k x w of depth K = 128 G is built as scale d +
 (min - b scale) X per group, d = sum x (b + q), X = sum x, with a bias b of
-1024 (gate and up) or 128 (down): with B = sum_k |x_k| (|min| + (2 b + 15)
-scale), the 16 MMAs of a group err by at most
+1024: with B = sum_k |x_k| (|min| + (2 b + 15) scale), the 16 MMAs of a group
+err by at most
 2 * 24 roundings of that size (a tensor core may truncate: 2^-23 each), the
 sum over groups and parts by G + 8 more, so e(K) = (G + 56) 2^-23 B.  x enters
 the first product as fp16 scaled by its row's largest value, off by at most
 2^-40 of that.  An
 activation a = silu(g) u moves by 1.1 |u| e_g + |silu(g)| e_u (|silu'| <= 1.1),
-4 fp32 roundings and exp's 2 ulp, and is rounded to bf16 (2^-8); the down
-product carries these through |w| and adds its own e(F); the weights p, from
+4 fp32 roundings and exp's 2 ulp, and is rounded to 11 bits (2^-11) with at
+most 2^-38 of the row's largest besides (twice: where it is stored and where it
+is brought to the row's exponent); the down product carries these through |w|
+and adds its own e(F); the weights p, from
 logits within (D / 8 + 16) 2^-24 sum|x r|, twice that relative plus 2^-20; the
 sum over picks 2^-20 relative; the output rounds once, 2^-8.
 
@@ -116,8 +118,9 @@ class Layer:
             gate, up, eg, eu = h[:, :self.F], h[:, self.F:], eh[:, :self.F], eh[:, self.F:]
             silu = gate * torch.sigmoid(gate)
             act = silu * up
-            ea = 1.1 * up.abs() * eg + silu.abs() * eu + 1.1 * eg * eu + (2.0 ** -8 + 2.0 ** -20) * act.abs()
-            W, B = self.down.matrix(e, 128)
+            ea = 1.1 * up.abs() * eg + silu.abs() * eu + 1.1 * eg * eu + (2.0 ** -11 + 2.0 ** -20) * act.abs()
+            ea = ea + 2.0 ** -38 * (act.abs() + ea).amax(-1, keepdim=True)
+            W, B = self.down.matrix(e, 1024)
             o = act @ W
             eo = ea @ W.abs() + eps(self.F) * ((act.abs() + ea) @ B)
             pe = p[rows, place][:, None]
