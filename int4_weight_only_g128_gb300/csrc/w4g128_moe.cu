@@ -15,7 +15,7 @@
 // next launch's CTAs are on the SMs with their first copies already.
 //
 // A unit is (picked expert, 2 or 4 tiles of 16 output columns), its depth K =
-// 128 G rows cut into G groups.  A team of 2, 4 or 8 warps works on a unit and
+// 128 G rows cut into G groups.  A team of 4 or 8 warps works on a unit and
 // takes its (unit, group) items in turn, each warp through a ring of its own
 // filled by cp.async (bulk copies cost a fence and some forty instructions of
 // one lane per item: 409 instructions an item against 265).  The item's product
@@ -39,7 +39,7 @@
 // whole item ahead.
 // The groups g of a unit fall into 8 parts by g mod 8, summed in rising order,
 // and the parts are added as ((0 + 4) + (2 + 6)) + ((1 + 5) + (3 + 7)), whether
-// 8 warps hold one part each or 2 warps four each: bits do not depend on the
+// 8 warps hold one part each or 4 warps two each: bits do not depend on the
 // grid, nor on which other rows share the expert.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   constexpr int kSide = PHASE == 0 ? TILES / 2 : TILES;  // neighbouring tiles
   constexpr int kTeams = kWarps / TEAM;
   constexpr int kMine = kParts / TEAM;  // parts of a unit that one warp sums
+  static_assert(TEAM == 4 || TEAM == 8, "the order of the parts' sums");
   constexpr int kQueue = 8;             // units of a team that are known: the current one and the next
   constexpr uint32_t kEnd = ~0u;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   // part in the order in which they are added.  The members take turns from
   // unit to unit, so that they stay even where the groups do not divide.
   auto turn = [&](int u) { return static_cast<int>(static_cast<unsigned>(member - u * G) % TEAM); };
-  auto part_at = [](int m, int i) { return m + 4 * (i & 1) + 2 * (i >> 1); };
+  auto part_at = [](int m, int i) { return m + 4 * i; };
 
   // The copies run kStages items ahead: the unit's number in the team's order,
   // the part's and the group, and this lane's 16 bytes in group 0 of its tiles.
@@ -720,21 +721,13 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     const int mine = turn(u);
     float sum[TILES][4];
 #pragma unroll
-    for (int q = 0; q < (kMine + 1) / 2; ++q) {
-      float two[TILES][4];
-#pragma unroll
-      for (int h = 0; h < (kMine > 1 ? 2 : 1); ++h) {
-        float acc[TILES][4] = {};
-        for (int g = part_at(mine, 2 * q + h); g < G; g += kParts) item(acc);
-#pragma unroll
-        for (int t = 0; t < TILES; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) two[t][i] = h == 0 ? acc[t][i] : two[t][i] + acc[t][i];
-      }
+    for (int h = 0; h < kMine; ++h) {
+      float acc[TILES][4] = {};
+      for (int g = part_at(mine, h); g < G; g += kParts) item(acc);
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sum[t][i] = q == 0 ? two[t][i] : sum[t][i] + two[t][i];
+        for (int i = 0; i < 4; ++i) sum[t][i] = h == 0 ? acc[t][i] : sum[t][i] + acc[t][i];
     }
     const float back = PHASE == 0 ? __int_as_float(scale) : scale_back(max(scale, 15));
     float* out = part + mine * S::kPart + 2 * c * S::kCols + r;
@@ -754,8 +747,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     if (draws) s_unit[team][(u + lead) % kQueue] = locate(kQueue * shares + draw);
     team_barrier<TEAM>(team);
     auto join = [&](const float* q) {  // (parts beyond the depth are 0)
-      if constexpr (TEAM == 2) return q[0] + q[S::kPart];
-      else if constexpr (TEAM == 4) return (q[0] + q[2 * S::kPart]) + (q[S::kPart] + q[3 * S::kPart]);
+      if constexpr (TEAM == 4) return (q[0] + q[2 * S::kPart]) + (q[S::kPart] + q[3 * S::kPart]);
       else
         return ((q[0] + q[4 * S::kPart]) + (q[2 * S::kPart] + q[6 * S::kPart])) +
                ((q[S::kPart] + q[5 * S::kPart]) + (q[3 * S::kPart] + q[7 * S::kPart]));
