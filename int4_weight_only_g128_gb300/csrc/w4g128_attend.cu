@@ -658,23 +658,22 @@ __global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Param
   }
 }
 
-// Positions per chunk: the smallest power of two that keeps the call's chunks
-// (span x heads x sequences) at a few for each SM.  One sequence: 352, what two
-// CTAs of 32 rows an SM hold.  A batch: 608, as its sequences have lengths of
-// their own, half of max_len on average.  A window: 152, its spans are full and
-// its CTAs short.  Measured (attend kernel): one sequence of 32771, 8 heads of
-// 128, 32 rows: 30.3 us at chunks of 1024, 37.6 at 2048, 32.5 at 512 (CTAs of a
-// third more overhead); 16 sequences of up to 9008, 4 heads of 64: 19.6 us at
-// 1024, 24.5 at 256; two of window 4096, 4 heads of 256, 64 rows: 24.6 us at
-// 256, 31.2 at 128, 44.4 at 64.
+// Positions per chunk: the multiple of 64 that cuts the call's positions (span
+// x heads x sequences) into a few chunks for each SM.  One sequence: 304, as
+// many CTAs of 32 rows as the GPU holds at once.  A batch: 608, as its sequences
+// have lengths of their own, half of max_len on average.  A window: 152, its
+// spans are full and its CTAs short.  Measured, per call: one sequence of 32771,
+// 8 heads of 128, 32 rows: 33.1 us at 304, 34.0 at 264, 47.1 at 352 and 41.2 at
+// 592 (a second wave); 16 sequences of up to 9008, 4 heads of 64: 21.6 us at 608,
+// 23.1 at 760, 25.6 at 400; two of window 4096, 4 heads of 256, 64 rows: 27.1 us
+// at 152, 29.7 at 120, 39.4 at 180.
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
   const long long all = span * a.kv_heads * a.count;
-  const int target = a.window > 0 ? 152 : a.count == 1 ? 352 : 608;
-  int chunk = 64;
-  while (chunk < kMaxChunk && static_cast<long long>(chunk) * target < all) chunk *= 2;
-  return chunk;
+  const int target = a.window > 0 ? 152 : a.count == 1 ? 304 : 608;
+  const long long chunk = (all + 64LL * target - 1) / (64LL * target) * 64;
+  return static_cast<int>(std::min<long long>(chunk, kMaxChunk));
 }
 
 // Most chunks that a sequence's rows can see: all of them, or the window's
