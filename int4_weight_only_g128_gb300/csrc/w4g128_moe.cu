@@ -69,13 +69,13 @@ constexpr uint32_t kOne = 0x3C003C00u;   // fp16 1.0 twice
 // rising expert order) that each serves: one entry for up to 8 rows, what an
 // MMA has B columns for.  An expert of more rows has two entries; its weights
 // are then dequantised twice, and read twice, side by side, from the L2.
-struct Lists {
+struct alignas(16) Lists {
   int entries;
   uint16_t expert[kMaxPicks];
-  uint16_t first[kMaxPicks + 2];  // an entry's first pick (one more; padded to whole words)
+  uint16_t first[kMaxPicks + 2];  // an entry's first pick, and one more
   uint16_t pick[kMaxPicks];
 };
-static_assert(sizeof(Lists) % 4 == 0, "copied by words");
+static_assert(sizeof(Lists) / 16 <= kThreads, "copied by one 16-byte load per thread");
 
 struct Params {
   const uint16_t *x, *residual, *router;
@@ -513,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     grid_dependency_wait();
     grid_dependents_launch();
   }
-  for (int i = tid; i < static_cast<int>(sizeof(Lists) / 4); i += kThreads)
-    reinterpret_cast<uint32_t*>(&lists)[i] = __ldcg(reinterpret_cast<const uint32_t*>(p.lists) + i);
+  if (tid < static_cast<int>(sizeof(Lists) / 16))
+    reinterpret_cast<uint4*>(&lists)[tid] = __ldcg(reinterpret_cast<const uint4*>(p.lists) + tid);
 
   const int K = PHASE == 0 ? p.D : p.F;
   const int G = K / kGroup;
@@ -761,11 +761,9 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
         const int m = o / kGate, col = o % kGate, n = at * kTileN + col;
         const int pick = lists.pick[first + m];
         const float v = join(part + m * S::kCols + col), w = join(part + m * S::kCols + col + kGate);
-        const float act = v / (1.f + expf(-v)) * w;
-        float top = fabsf(act);
-#pragma unroll
-        for (int k = 8; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(tile_lanes, top, k));
-        const int e = exponent_of(top);
+        const float act = v * __frcp_rn(1.f + expf(-v)) * w;
+        // (magnitudes order like their bits)
+        const int e = exponent_of(__uint_as_float(__reduce_max_sync(tile_lanes, __float_as_uint(act) & 0x7FFFFFFFu)));
         // column n: k step n / 16 % 8 of its group
         uint8_t* dst = p.act + static_cast<long long>(pick) * p.F * 2 + n / 128 * 256 + n / 32 % 4 * 64 + n % 8 / 2 * 16 +
                        (n / 16 % 2 * 2 + n / 8 % 2) * 4 + (n & 1) * 2;
