@@ -20,6 +20,12 @@
 //   * S = Q K^T lands in the registers that P V wants it in; K comes by
 //     ldmatrix, V by ldmatrix.trans, from rows whose 16-byte pieces are
 //     exchanged by the low bits of the position, free of bank conflicts.
+// Measured, one sequence of 32771, 8 heads of 128, 8 new tokens of 32 query
+// heads (134 MB): 33.1 us a call, 60% of the measured copy rate; the tile loop
+// streams at about 5.3 TB/s, the rest is each CTA's start (length, table, first
+// tiles: 3 us), the join of its groups and the second kernel (4 us).  The tensor
+// pipe is 29% busy, 430 instructions a warp and tile.  64 rows of 256-wide heads
+// are bound by the tile loop's latency instead (27.1 us against 7.9 us of MMA).
 // Positions masked for some row hold arbitrary bits, and 0 x NaN is NaN: tiles
 // at a mask's edge are searched for non-finite values, which are then applied
 // to the rows that see them one by one.
