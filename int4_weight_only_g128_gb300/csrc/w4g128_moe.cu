@@ -271,7 +271,8 @@ __device__ __forceinline__ int exponent_of(float top) {
   return min(max(static_cast<int>(__float_as_uint(top) >> 23), 15), 254);
 }
 
-// x in operand order, by the clusters behind the routing one, a row a CTA.  The scale puts the row's largest magnitude in [2^14, 2^15).
+// x in operand order, by the clusters behind the routing one, a row a CTA.  The
+// scale puts the row's largest magnitude in [2^14, 2^15).
 __device__ __forceinline__ void pack_x(const Params& p) {
   __shared__ float s_top[kRouteThreads / 32];
   const int tid = threadIdx.x, cta = blockIdx.x - kRouteCtas;
@@ -465,7 +466,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pa
 
 // The same within expert 1, for one or two rows: a team counts its finished
 // units by their columns, 32 at a time or at its end, and who counts a column's
-// last entry adds up.  A launch less (small experts, one row: 18.8 -> 14.7 us);
+// last entry adds up.  A launch less (small experts, one row: 18.8 -> 16.2 us);
 // with more rows the few teams that finish last add up everything, which took
 // longer than the launch (16 rows of 5120: 137 -> 162 us).
 template <int COLS, int TEAM>
@@ -652,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
 
   auto item = [&](float (&acc)[TILES][4]) {
     Operand xn = {};
+    __syncwarp();  // the descriptor below may be of the copies just issued
     load_x(s_item[warp][next_slot], xn);
     next_slot = next_slot == S::kStages ? 0 : next_slot + 1;
     scale = x.scale;

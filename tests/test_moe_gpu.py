@@ -153,7 +153,8 @@ def test_against_reference(shape, renorm, residual):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("shape", [(16, 512, 256, 8, 3), (7, 1152, 640, 40, 5), (12, 256, 128, 2, 1), (16, 2048, 384, 40, 5)],
+@pytest.mark.parametrize("shape", [(16, 512, 256, 8, 3), (7, 1152, 640, 40, 5), (12, 256, 128, 2, 1), (16, 2048, 384, 40, 5),
+                                   (16, 384, 256, 2, 2), (2, 640, 1152, 9, 4)],
                          ids=str)
 def test_a_row_alone_gives_the_same_bits(shape):
     layer = Layer(*shape, seed=4)
