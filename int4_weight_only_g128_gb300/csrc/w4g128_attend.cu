@@ -181,6 +181,7 @@ attend_kernel(const __grid_constant__ Params p) {
   constexpr int kPer = kTile * kPieces / S::kGroup;  // pieces of a K tile that one thread copies
   constexpr int kRows = S::kGroup / kPieces;         // rows between them
   static_assert(S::kGroup % kPieces == 0 && kTile % kRows == 0, "a thread copies one column of pieces");
+  static_assert(kMaxChunk / kTile <= S::kThreads, "one thread per tile of a chunk");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_tile[kMaxChunk / kTile];  // a tile's first element in the caches, or -1: not a page
   __shared__ float4 s_half[S::kExchange][2];
@@ -200,6 +201,12 @@ attend_kernel(const __grid_constant__ Params p) {
     if (__syncthreads_or(bad)) bad = true;
     if (tid == 0) st_relaxed_u64(p.status, bad ? W4G128_ERR_CACHE : W4G128_OK);
   }
+  // Without a window this chunk's positions are known before the length is: its
+  // page ids come along with it.
+  const int ahead_pos = z * p.chunk + tid * kTile;
+  int ahead_id = -1;
+  if (p.window == 0 && tid < p.chunk / kTile && ahead_pos < p.max_len)
+    ahead_id = p.table[static_cast<long long>(b) * p.table_row + ahead_pos / p.page_size];
   const Seq s = sequence(p, b);
   if (!s.ok) {
     if (z == 0 && blockIdx.y == 0 && tid == 0) note_error(p.pending, W4G128_ERR_CACHE);
@@ -218,7 +225,7 @@ attend_kernel(const __grid_constant__ Params p) {
   for (int t = tid; t < tiles; t += S::kThreads) {
     const int a = p0 + t * kTile;
     const bool seen = a < s.sink || (a + kTile > s.lo && a < s.len);
-    const int id = seen ? p.table[static_cast<long long>(b) * p.table_row + a / p.page_size] : -1;
+    const int id = !seen ? -1 : p.window == 0 ? ahead_id : p.table[static_cast<long long>(b) * p.table_row + a / p.page_size];
     const bool ok = id >= 0 && id < p.pages;
     if (seen && !ok) note_error(p.pending, W4G128_ERR_CACHE);
     s_tile[t] = ok ? id * p.page_stride + (a % p.page_size) * p.slot_stride + head * p.head_stride : -1;
@@ -591,76 +598,106 @@ attend_kernel(const __grid_constant__ Params p) {
   }
 }
 
-// Joins a row's chunks: 4 warps take the chunks by their number mod 4, each
-// sums its own in rising order, and the four sums are added in order.
-template <int D>
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ Params p) {
+// Joins a row's chunks: W warps take the chunks by their number mod W, each
+// joins its own in rising order with a running maximum, and the W are added in
+// order.  Latency is all there is to it.  A sequence alone without a window may
+// have hundreds of chunks: 8 warps, and the first 32 chunks' sums are on their
+// way while the length is read (those beyond it are not looked at); 100003
+// positions on one head take 20.4 us a call for 27.1, 32771 on 8 heads 27.9 for
+// 29.9.  A batch or a window has few chunks and many rows to join, whose idle
+// warps cost more: 4 (16 sequences, 3 new: 21.4 us, and 23.2 with 8).
+template <int D, int W>
+__global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Params p) {
   constexpr int kPer = D / 32;
-  __shared__ float s_sum[4][D];
-  __shared__ float2 s_stat[4];
+  constexpr int kBatch = 4;
+  __shared__ float s_sum[W][D];
+  __shared__ float2 s_stat[W];
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
-  if (b == 0 && i == 0 && hq == 0 && threadIdx.x == 0) publish_errors(p.status, p.pending);
-  const Seq s = sequence(p, b);
-  if (!s.ok || i >= s.n) return;
   const int head = hq / p.group, row = i * p.group + hq % p.group;
   const long long step = static_cast<long long>(p.kv_heads) * (p.max_new * p.group);
   const long long at0 = (static_cast<long long>(b) * p.splits * p.kv_heads + head) * (p.max_new * p.group) + row;
 
-  float top = kNone;
-  for (int z = threadIdx.x; z < s.chunks; z += 128) top = fmaxf(top, p.stat[at0 + z * step].x);
+  float2 st[kBatch];
+  float v[kBatch][kPer];
+  auto load = [&](int z, int end) {  // chunks z, z + W, .. below end
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-  if (lane == 0) s_stat[warp].x = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(s_stat[0].x, s_stat[1].x), fmaxf(s_stat[2].x, s_stat[3].x));
-  const float ref = top == kNone ? 0.f : top;
-  __syncthreads();
-
-  // this warp's chunks: numbers = warp mod 4, four loads in flight
-  float sum[kPer] = {}, l = 0.f;
-  const int sinks = s.sink_chunks;
-  auto add = [&](int z0, int z1, int id0) {  // chunks z0 .. z1 - 1 are numbers id0 ..
-    int z = z0 + ((warp - id0) & 3);
-    for (; z < z1; z += 16) {
-      float2 st[4];
-      float v[4][kPer];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const long long at = at0 + min(z + 4 * j, z1 - 1) * step;
-        st[j] = z + 4 * j < z1 ? p.stat[at] : make_float2(kNone, 0.f);
+    for (int j = 0; j < kBatch; ++j) {
+      if (z + W * j < end) {
+        const long long at = at0 + (z + W * j) * step;
+        st[j] = p.stat[at];
         const float* o = p.part + at * D + lane * kPer;
         if constexpr (kPer == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(o);
         else
 #pragma unroll
           for (int k = 0; k < kPer; k += 4) *reinterpret_cast<float4*>(&v[j][k]) = *reinterpret_cast<const float4*>(o + k);
       }
+    }
+  };
+  if constexpr (W == 8) load(warp, p.splits);
+  if (b == 0 && i == 0 && hq == 0 && threadIdx.x == 0) publish_errors(p.status, p.pending);
+  const Seq s = sequence(p, b);
+  if (!s.ok || i >= s.n) return;
+
+  float top = kNone, l = 0.f, sum[kPer] = {};
+  auto add = [&](int z, int end) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (z + 4 * j < z1) {
-          const float w = exp2_fast(st[j].x - ref);
-          l = fmaf(st[j].y, w, l);
+    for (int j = 0; j < kBatch; ++j) {
+      if (z + W * j < end) {
+        const float next = fmaxf(top, st[j].x), ref = next == kNone ? 0.f : next;
+        const float old = exp2_fast(top - ref), w = exp2_fast(st[j].x - ref);
+        top = next;
+        l = fmaf(st[j].y, w, l * old);
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k]);
-        }
+        for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k] * old);
       }
     }
   };
-  add(0, sinks, 0);
-  add(sinks, s.chunks, s.lo_chunk);
+  if (W == 8 || p.window == 0) {
+    if constexpr (W != 8) load(warp, s.chunks);
+    add(warp, s.chunks);
+    for (int z = warp + W * kBatch; z < s.chunks; z += W * kBatch) {
+      load(z, s.chunks);
+      add(z, s.chunks);
+    }
+  } else {  // the sinks' chunks are numbers 0 .., the others lo_chunk ..
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const int z0 = side ? s.sink_chunks : 0, end = side ? s.chunks : s.sink_chunks;
+      for (int z = z0 + ((warp - (side ? s.lo_chunk : 0)) & (W - 1)); z < end; z += W * kBatch) {
+        load(z, end);
+        add(z, end);
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < kPer; ++k) s_sum[warp][lane * kPer + k] = sum[k];
-  if (lane == 0) s_stat[warp].y = l;
+  if (lane == 0) s_stat[warp] = make_float2(top, l);
   __syncthreads();
-  l = (s_stat[0].y + s_stat[1].y) + (s_stat[2].y + s_stat[3].y);
+  top = kNone;
+#pragma unroll
+  for (int j = 0; j < W; ++j) top = fmaxf(top, s_stat[j].x);
+  const float ref = top == kNone ? 0.f : top;
+  float w[W];
+  l = 0.f;
+#pragma unroll
+  for (int j = 0; j < W; ++j) {
+    w[j] = exp2_fast(s_stat[j].x - ref);
+    l = fmaf(s_stat[j].y, w[j], l);
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + i) * p.out_row +
-                                              static_cast<long long>(hq) * D);
-  for (int k = threadIdx.x; k < D / 2; k += 128) {
-    const float x = (s_sum[0][2 * k] + s_sum[1][2 * k]) + (s_sum[2][2 * k] + s_sum[3][2 * k]);
-    const float y = (s_sum[0][2 * k + 1] + s_sum[1][2 * k + 1]) + (s_sum[2][2 * k + 1] + s_sum[3][2 * k + 1]);
-    out[k] = pack_bf16(x * inv, y * inv);
+  if (threadIdx.x < D / 2) {
+    const int k = threadIdx.x;
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+      const float2 u = *reinterpret_cast<const float2*>(&s_sum[j][2 * k]);
+      x = fmaf(u.x, w[j], x);
+      y = fmaf(u.y, w[j], y);
+    }
+    reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + i) * p.out_row + static_cast<long long>(hq) * D)[k] =
+        pack_bf16(x * inv, y * inv);
   }
 }
 
@@ -744,9 +781,13 @@ cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
                                                                               : launch_attend<D, 4>(cfg, p);
   if (e != cudaSuccess || p.splits == 1) return e;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
-  cfg.blockDim = dim3(128);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join_kernel<D>, p);
+  if (p.count == 1 && p.window == 0) {
+    cfg.blockDim = dim3(256);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, p);
+  }
+  cfg.blockDim = dim3(128);
+  return cudaLaunchKernelEx(&cfg, join_kernel<D, 4>, p);
 }
 
 }  // namespace
