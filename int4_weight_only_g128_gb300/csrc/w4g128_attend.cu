@@ -220,6 +220,41 @@ attend_kernel(const __grid_constant__ Params p) {
   const int p1 = s.chunks ? min(p0 + p.chunk, s.len) : 0;
   const int fresh = p.k_new != nullptr ? s.first : s.len;  // positions from here on come from k_new, v_new
 
+  // Q, asked for before the table is waited for: this lane's part of the A
+  // fragments of rows r and r + 8, or this thread's pieces for shared memory.
+  const int r = lane >> 2, c = lane & 3;
+  const int row0 = (rg * RT + rt) * 16 + r;
+  const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
+  const int pos_a = row0 < live_rows ? s.start + row0 / p.group : -1;  // the rows' positions
+  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.group : -1;
+  auto q_row = [&](int row) {
+    return p.q + static_cast<long long>(s.first_row + row / p.group) * p.q_row +
+           static_cast<long long>(head * p.group + row % p.group) * D;
+  };
+  constexpr int kQPer = RT * 16 * kPieces / S::kThreads;
+  static_assert(S::kQInRegs || RT * 16 * kPieces % S::kThreads == 0, "each thread loads as many pieces of Q");
+  [[maybe_unused]] uint32_t qf[S::kQInRegs ? kSteps : 1][4] = {};
+  [[maybe_unused]] uint4 q_part[S::kQInRegs ? 1 : kQPer] = {};
+  if constexpr (S::kQInRegs) {
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      if (row0 + 8 * side < live_rows) {
+        const uint32_t* from = reinterpret_cast<const uint32_t*>(q_row(row0 + 8 * side) + half * S::kHalf) + c;
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+          qf[k][side] = __ldg(from + k * 8);
+          qf[k][side + 2] = __ldg(from + k * 8 + 4);
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < kQPer; ++e) {
+      const int i = tid + e * S::kThreads, row = rg * RT * 16 + i / kPieces;
+      if (row < live_rows) q_part[e] = __ldg(reinterpret_cast<const uint4*>(q_row(row)) + i % kPieces);
+    }
+  }
+
   // where this chunk's tiles are
   const int tiles = (p1 - p0 + kTile - 1) / kTile;
   for (int t = tid; t < tiles; t += S::kThreads) {
@@ -231,46 +266,20 @@ attend_kernel(const __grid_constant__ Params p) {
     s_tile[t] = ok ? id * p.page_stride + (a % p.page_size) * p.slot_stride + head * p.head_stride : -1;
   }
 
-  // Q: this lane's part of the A fragments of rows r and r + 8.
-  const int r = lane >> 2, c = lane & 3;
-  const int row0 = (rg * RT + rt) * 16 + r;
-  const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
-  const int pos_a = row0 < live_rows ? s.start + row0 / p.group : -1;  // the rows' positions
-  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.group : -1;
   // (a negative scale goes into q's signs, a scale of 0 makes q 0)
-  uint32_t qf[S::kQInRegs ? kSteps : 1][4];
-  if constexpr (!S::kQInRegs) {
-    for (int i = tid; i < RT * 16 * kPieces; i += S::kThreads) {
-      const int j = i / kPieces, piece = i % kPieces, row = rg * RT * 16 + j;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (row < live_rows)
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<long long>(s.first_row + row / p.group) * p.q_row +
-                                                 static_cast<long long>(head * p.group + row % p.group) * D + piece * 8));
-      v.x = (v.x & p.keep_q) ^ p.flip_q;
-      v.y = (v.y & p.keep_q) ^ p.flip_q;
-      v.z = (v.z & p.keep_q) ^ p.flip_q;
-      v.w = (v.w & p.keep_q) ^ p.flip_q;
-      *reinterpret_cast<uint4*>(smem + j * S::kRowBytes + ((piece ^ (j & 7)) << 4)) = v;
-    }
-  } else {
-    const uint32_t* qa = nullptr;
-    const uint32_t* qb = nullptr;
-    if (row0 < live_rows) {
-      qa = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row0 / p.group) * p.q_row +
-                                             static_cast<long long>(head * p.group + row0 % p.group) * D + half * S::kHalf);
-    }
-    const int row1 = row0 + 8;
-    if (row1 < live_rows) {
-      qb = reinterpret_cast<const uint32_t*>(p.q + static_cast<long long>(s.first_row + row1 / p.group) * p.q_row +
-                                             static_cast<long long>(head * p.group + row1 % p.group) * D + half * S::kHalf);
-    }
-    const uint32_t flip = p.flip_q, keep = p.keep_q;
+  auto signed_q = [&](uint32_t v) { return (v & p.keep_q) ^ p.flip_q; };
+  if constexpr (S::kQInRegs) {
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k) {
-      qf[k][0] = qa ? (__ldg(qa + k * 8 + c) & keep) ^ flip : 0u;
-      qf[k][1] = qb ? (__ldg(qb + k * 8 + c) & keep) ^ flip : 0u;
-      qf[k][2] = qa ? (__ldg(qa + k * 8 + 4 + c) & keep) ^ flip : 0u;
-      qf[k][3] = qb ? (__ldg(qb + k * 8 + 4 + c) & keep) ^ flip : 0u;
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[k][i] = signed_q(qf[k][i]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kQPer; ++e) {
+      const int i = tid + e * S::kThreads, j = i / kPieces, piece = i % kPieces;
+      const uint4 v = q_part[e];
+      *reinterpret_cast<uint4*>(smem + j * S::kRowBytes + ((piece ^ (j & 7)) << 4)) =
+          make_uint4(signed_q(v.x), signed_q(v.y), signed_q(v.z), signed_q(v.w));
     }
   }
   __syncthreads();
@@ -349,21 +358,6 @@ attend_kernel(const __grid_constant__ Params p) {
   for (int i = 0; i < S::kStages - 1; ++i) {
     issue(ahead, i);
     ahead = next_tile(ahead + S::kKg);
-  }
-
-  // The new rows go to their pages; nobody reads those slots in this call.
-  if (rg == 0 && p1 > fresh) {
-    const int a = max(p0, fresh);
-    for (int i = tid; i < (p1 - a) * kPieces; i += S::kThreads) {
-      const int pos = a + i / kPieces, piece = i % kPieces;
-      const long long where = s_tile[(pos - p0) / kTile];
-      if (where < 0) continue;
-      const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
-                            static_cast<long long>(head) * D + piece * 8;
-      const long long dst = where + (pos - p0) % kTile * p.slot_stride + piece * 8;
-      *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
-      *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
-    }
   }
 
   // ldmatrix: this lane's row of a K and of a V tile, and its pieces 0, 2, 4, 6
@@ -535,7 +529,23 @@ attend_kernel(const __grid_constant__ Params p) {
     }
   }
   __syncthreads();
-  if (kg > 0) return;
+  if (kg > 0) {
+    // Meanwhile the new rows go to their pages; nobody reads those slots in this call.
+    if (rg == 0 && p1 > fresh) {
+      const int a = max(p0, fresh);
+      for (int i = tid - S::kGroup; i < (p1 - a) * kPieces; i += S::kThreads - S::kGroup) {
+        const int pos = a + i / kPieces, piece = i % kPieces;
+        const long long where = s_tile[(pos - p0) / kTile];
+        if (where < 0) continue;
+        const long long src = static_cast<long long>(s.first_row + pos - s.start) * p.kv_row +
+                              static_cast<long long>(head) * D + piece * 8;
+        const long long dst = where + (pos - p0) % kTile * p.slot_stride + piece * 8;
+        *reinterpret_cast<uint4*>(p.k_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.k_new + src));
+        *reinterpret_cast<uint4*>(p.v_cache + dst) = __ldg(reinterpret_cast<const uint4*>(p.v_new + src));
+      }
+    }
+    return;
+  }
   float2 sa[S::kKg], sb[S::kKg];
   sa[0] = make_float2(m_a, l_a);
   sb[0] = make_float2(m_b, l_b);
