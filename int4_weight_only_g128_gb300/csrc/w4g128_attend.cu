@@ -21,11 +21,14 @@
 //     ldmatrix, V by ldmatrix.trans, from rows whose 16-byte pieces are
 //     exchanged by the low bits of the position, free of bank conflicts.
 // Measured, one sequence of 32771, 8 heads of 128, 8 new tokens of 32 query
-// heads (134 MB): 33.1 us a call, 60% of the measured copy rate; the tile loop
-// streams at about 5.3 TB/s, the rest is each CTA's start (length, table, first
-// tiles: 3 us), the join of its groups and the second kernel (4 us).  The tensor
-// pipe is 29% busy, 430 instructions a warp and tile.  64 rows of 256-wide heads
-// are bound by the tile loop's latency instead (27.1 us against 7.9 us of MMA).
+// heads (134 MB): 29.8 us a call, 66% of the measured copy rate; the tile loop
+// streams at about 5.5 TB/s, the rest is each CTA's start (length, table, first
+// tiles: 3 us), the join of its groups and the second kernel (4 us).  With 64
+// rows the tile loop's latency binds: 1.9 instructions a clock, the tensor pipe
+// 38% and shared memory 60% busy (two of window 4096, 4 heads of 256, 16 new
+// tokens: 22.7 us against 7.9 us of MMA).  Not kept there: two row tiles a warp
+// at 255 registers (8 long 34.9 us, 30.5 without), two position tiles a turn of
+// the loop (22.8 and 22.7: the same).
 // Positions masked for some row hold arbitrary bits, and 0 x NaN is NaN: tiles
 // at a mask's edge are searched for non-finite values, which are then applied
 // to the rows that see them one by one.
@@ -48,6 +51,11 @@ constexpr int kTile = 16;        // positions per tile
 constexpr int kMaxChunk = 2048;  // positions per chunk, at most
 constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
+// A row's reference follows its maximum only when that is above it by more than
+// this (base 2): weights up to 2^8 cost no precision, and most tiles neither
+// exchange their maxima nor rescale the sums (per call, 16 new tokens on 64 heads
+// at 32771: 98.6 -> 89.4 us; 16 ragged sequences 21.3 -> 19.3).
+constexpr float kSlack = 8.f;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
 
 struct Params {
@@ -169,7 +177,7 @@ struct Shape {
   static constexpr int kLeft = 16 * (kHalf + 2) * 4;  // a warp's sums, maxima and sums of weights
   static constexpr int kJoin = (kKg - 1) * RT * kDs * kLeft;
   static constexpr int kBytes = kQBytes + (kRing > kJoin ? kRing : kJoin);
-  static constexpr int kExchange = kDs == 2 ? kKg * RT * 2 * 2 * 32 : 1;  // float4: [group][row tile][turn][half]..
+  static constexpr int kExchange = kDs == 2 ? kKg * RT * 2 * 32 : 1;  // float4: [group][row tile][half]..
 };
 
 template <int D, int RT>
@@ -287,7 +295,7 @@ attend_kernel(const __grid_constant__ Params p) {
   float acc[S::kHalf / 8][4];
 #pragma unroll
   for (int i = 0; i < S::kHalf / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  // running maxima of the raw scores of rows r and r + 8, and the sums of the
+  // references (running maxima, up to the slack) of the raw scores of rows r and r + 8, and the sums of the
   // weights (sum[0] and sum[2]: a product with ones)
   float m_a = kNone, m_b = kNone, sum[4] = {};
 
@@ -372,7 +380,6 @@ attend_kernel(const __grid_constant__ Params p) {
   const uint32_t q_tile = smem_addr(smem) + rt * 16 * S::kRowBytes - S::kTileBytes;
   const int last_pos = s.len - 1;  // of the sequence's last row
   int stage = 0;
-  [[maybe_unused]] int flip = 0;
   while (t < tiles) {
     cp_async_wait_group<S::kStages - 2>();
     group_sync();  // the tile is there for the group, and the stage refilled next is read out
@@ -399,15 +406,14 @@ attend_kernel(const __grid_constant__ Params p) {
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 4; ++i) sc[h][i] += odd_k[h][i];
-      if constexpr (S::kDs == 2) {  // the other half of the depth
-        float4* ex = &s_half[(((kg * RT + rt) * 2 + flip) * 2) * 32][0];
+      if constexpr (S::kDs == 2) {  // the other half of the depth (read out before the group's next barrier)
+        float4* ex = &s_half[(kg * RT + rt) * 2 * 32][0];
         ex[(half * 32 + lane) * 2] = make_float4(sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
         ex[(half * 32 + lane) * 2 + 1] = make_float4(sc[1][0], sc[1][1], sc[1][2], sc[1][3]);
         asm volatile("bar.sync %0, 64;" ::"r"(S::kKg + 1 + kg * RT + rt) : "memory");
         const float4 u = ex[((half ^ 1) * 32 + lane) * 2], v = ex[((half ^ 1) * 32 + lane) * 2 + 1];
         sc[0][0] += u.x; sc[0][1] += u.y; sc[0][2] += u.z; sc[0][3] += u.w;
         sc[1][0] += v.x; sc[1][1] += v.y; sc[1][2] += v.z; sc[1][3] += v.w;
-        flip ^= 1;  // (the next tile's exchange leaves this one alone)
       }
       const bool page_ok = s_tile[t] >= 0;
       // every row sees the whole tile
@@ -423,13 +429,14 @@ attend_kernel(const __grid_constant__ Params p) {
       }
       float ta = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
       float tb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
+      auto above = [&](float top, float m) { return (top - m) * p.scale2 > kSlack; };  // (m may be that of no score)
+      if (__any_sync(~0u, above(ta, m_a) || above(tb, m_b))) {
 #pragma unroll
-      for (int d = 1; d < 4; d <<= 1) {
-        ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
-        tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
-      }
-      if (__any_sync(~0u, ta > m_a || tb > m_b)) {  // (otherwise the factors below are 1)
-        const float na = fmaxf(m_a, ta), nb = fmaxf(m_b, tb);
+        for (int d = 1; d < 4; d <<= 1) {
+          ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
+          tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
+        }
+        const float na = above(ta, m_a) ? ta : m_a, nb = above(tb, m_b) ? tb : m_b;
         const float ga = na == m_a ? 1.f : exp2_fast((m_a - na) * p.scale2);
         const float gb = nb == m_b ? 1.f : exp2_fast((m_b - nb) * p.scale2);
         m_a = na;

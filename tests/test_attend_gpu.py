@@ -229,6 +229,23 @@ def test_window_edges_inside_a_tile_with_non_finite_values():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,new", [(64, 3), (64, 16), (128, 1), (128, 16), (256, 16)])
+@pytest.mark.parametrize("scores", [lambda p: p / 32, lambda p: p / 2, lambda p: -p / 4, lambda p: 5.5 * (p // 16),
+                                    lambda p: 5.0 * (p // 64 % 2), lambda p: 300.0 * (p == 390), lambda p: -1e4 + p / 8],
+                         ids=["slow", "fast", "falling", "steps", "to and fro", "a peak", "far below zero"])
+def test_scores_that_move_the_maximum(dim, new, scores):
+    """Scores rising by less, and by more, than the factor that the kernel lets a row's weights grow to."""
+    c = Call([(401, new), (64, new)], q_heads=8, kv_heads=2, dim=dim, fused=False, seed=new)
+    c.scale = 1.0
+    c.q[:] = 0
+    c.q.view(c.rows, 8, dim)[:, :, 0] = torch.tensor([1.0, 0.5, 1.0, 2.0] * 2, device="cuda").bfloat16()
+    for b, (n, _) in enumerate(c.seqs):
+        pos = torch.arange(n, device="cuda")
+        c.k_cache[c.table[b, pos // c.page].long(), pos % c.page, :, 0] = scores(pos.double())[:, None].bfloat16()
+    c.check()
+
+
+@pytest.mark.gpu
 def test_equal_values_come_through_exactly():
     """The weights add up to 1 as rounded: equal values give that value."""
     c = Call([(1000, 3)], dim=128, seed=2)
