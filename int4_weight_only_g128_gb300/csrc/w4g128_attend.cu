@@ -621,8 +621,9 @@ attend_kernel(const __grid_constant__ Params p) {
 // have hundreds of chunks: 8 warps, and the first 32 chunks' sums are on their
 // way while the length is read (those beyond it are not looked at); 100003
 // positions on one head take 20.4 us a call for 27.1, 32771 on 8 heads 27.9 for
-// 29.9.  A batch or a window has few chunks and many rows to join, whose idle
-// warps cost more: 4 (16 sequences, 3 new: 21.4 us, and 23.2 with 8).
+// 29.9.  A batch with more than 16 chunks a sequence does the same (two of 4099,
+// 4 heads: 11.8 for 12.7).  Others and windows have few chunks and many rows to
+// join, whose idle warps cost more: 4 (16 sequences, 3 new: 21.4, 23.2 with 8).
 template <int D, int W>
 __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Params p) {
   constexpr int kPer = D / 32;
@@ -721,18 +722,23 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Pa
 // Positions per chunk: the multiple of 64 that cuts the call's positions (span
 // x heads x sequences) into a few chunks for each SM.  One sequence: 304, as
 // many CTAs of 32 rows as the GPU holds at once.  A batch: 608, as its sequences
-// have lengths of their own, half of max_len on average.  A window: 152, its
-// spans are full and its CTAs short.  Measured, per call: one sequence of 32771,
-// 8 heads of 128, 32 rows: 33.1 us at 304, 34.0 at 264, 47.1 at 352 and 41.2 at
-// 592 (a second wave); 16 sequences of up to 9008, 4 heads of 64: 21.6 us at 608,
-// 23.1 at 760, 25.6 at 400; two of window 4096, 4 heads of 256, 64 rows: 27.1 us
-// at 152, 29.7 at 120, 39.4 at 180.
+// have lengths of their own, half of max_len on average.  A window: 304, and 152
+// for heads of 256, whose CTAs of 64 rows fill an SM.  Not less than 128 past
+// 2048 positions: the second kernel takes 32 chunks at once.  Measured, per call:
+// one sequence of 32771, 8 heads of 128, 32 rows: 33.1 us at 304, 34.0 at 264,
+// 47.1 at 352 and 41.2 at 592 (a second wave); 16 sequences of up to 9008, 4
+// heads of 64, 18 rows: 20.1 us at 608, 21.5 at 760, 22.2 at 456; 16 of 4099, 8
+// heads of 128, 4 rows: 51.2, 48.2 and 52.0.  Windows of 4096: two, 4 heads of
+// 256, 64 rows: 23.5 us at 152, 30.9 at 304; eight, 8 heads of 128, 4 rows: 35.6
+// and 29.9.  Chunks of 128 for 64: 4 of 4099, 2 heads of 256: 12.4 us for 17.5;
+// one of 2049, 8 heads of 128: 6.9 for 7.7; but one of 611: 7.4 for 6.6.
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
   const long long all = span * a.kv_heads * a.count;
-  const int target = a.window > 0 ? 152 : a.count == 1 ? 304 : 608;
-  const long long chunk = (all + 64LL * target - 1) / (64LL * target) * 64;
+  const int target = a.window > 0 ? (a.head_dim == 256 ? 152 : 304) : a.count == 1 ? 304 : 608;
+  const long long least = a.window == 0 && a.max_len > 2048 ? 128 : 64;
+  const long long chunk = std::max(least, (all + 64LL * target - 1) / (64LL * target) * 64);
   return static_cast<int>(std::min<long long>(chunk, kMaxChunk));
 }
 
@@ -799,7 +805,7 @@ cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
   if (e != cudaSuccess || p.splits == 1) return e;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
   cfg.dynamicSmemBytes = 0;
-  if (p.count == 1 && p.window == 0) {
+  if (p.window == 0 && (p.count == 1 || p.splits > 16)) {
     cfg.blockDim = dim3(256);
     return cudaLaunchKernelEx(&cfg, join_kernel<D, 8>, p);
   }
