@@ -58,6 +58,18 @@ constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
 
+// A divisor and 2^32 over it: the compiler's divide by a value that it does not
+// know is a chain of some 30 instructions, and a call's start has a dozen of them.
+struct Divisor {
+  unsigned d, m;
+};
+Divisor divisor(int d) { return {static_cast<unsigned>(d), d == 1 ? ~0u : static_cast<unsigned>((1ull << 32) / d)}; }
+// a / d for a >= 0: m falls short of 2^32 / d by less than 1, a m / 2^32 of a / d by less than 1.
+__device__ __forceinline__ int operator/(int a, Divisor by) {
+  const unsigned q = __umulhi(static_cast<unsigned>(a), by.m);
+  return static_cast<int>(q + (static_cast<unsigned>(a) - q * by.d >= by.d ? 1u : 0u));
+}
+
 struct Params {
   const uint16_t *q, *k_new, *v_new;
   uint16_t *k_cache, *v_cache;
@@ -66,6 +78,7 @@ struct Params {
   long long q_row, kv_row, out_row, page_stride, slot_stride, head_stride, table_row;
   int rows, count, q_heads, kv_heads, group, pages, page_size, max_len, max_new, window, sinks;
   int chunk, splits;  // positions per chunk; chunks a sequence may need
+  Divisor by_chunk, by_group, by_page, by_row_groups;
   float scale2;       // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
   uint32_t flip_q, keep_q;
   unsigned long long *status, *pending;
@@ -94,9 +107,9 @@ __device__ __forceinline__ Seq sequence(const Params& p, int b) {
   s.first = max(s.start, 0);
   s.lo = p.window > 0 ? max(0, s.first - p.window + 1) : 0;
   s.sink = p.window > 0 ? min(p.sinks, s.lo) : 0;
-  s.lo_chunk = s.lo / p.chunk;
-  s.sink_chunks = min((s.sink + p.chunk - 1) / p.chunk, s.lo_chunk);
-  s.chunks = s.ok && s.n > 0 && s.len > 0 ? s.sink_chunks + (s.len - 1) / p.chunk - s.lo_chunk + 1 : 0;
+  s.lo_chunk = s.lo / p.by_chunk;
+  s.sink_chunks = min((s.sink + p.chunk - 1) / p.by_chunk, s.lo_chunk);
+  s.chunks = s.ok && s.n > 0 && s.len > 0 ? s.sink_chunks + (s.len - 1) / p.by_chunk - s.lo_chunk + 1 : 0;
   return s;
 }
 
@@ -106,7 +119,7 @@ __device__ __forceinline__ bool in_range(const Params& p, int b) {
   bool ok = s.ok;
   if (ok && s.n > 0) {
     for (int a = 0; a < s.len; a += kTile) {
-      const int id = p.table[static_cast<long long>(b) * p.table_row + a / p.page_size];
+      const int id = p.table[static_cast<long long>(b) * p.table_row + a / p.by_page];
       ok = ok && ((a >= s.sink && a + kTile <= s.lo) || (id >= 0 && id < p.pages));
     }
   }
@@ -197,8 +210,8 @@ attend_kernel(const __grid_constant__ Params p) {
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
   const int kg = warp / (RT * S::kDs), rt = warp / S::kDs % RT, half = warp % S::kDs;
-  const int row_groups = (p.max_new * p.group + 16 * RT - 1) / (16 * RT);
-  const int head = blockIdx.y / row_groups, rg = blockIdx.y % row_groups;
+  const int head = static_cast<int>(blockIdx.y) / p.by_row_groups;
+  const int rg = static_cast<int>(blockIdx.y - head * p.by_row_groups.d);
   const int b = blockIdx.z, z = blockIdx.x;
 
   grid_dependency_wait();
@@ -214,7 +227,7 @@ attend_kernel(const __grid_constant__ Params p) {
   const int ahead_pos = z * p.chunk + tid * kTile;
   int ahead_id = -1;
   if (p.window == 0 && tid < p.chunk / kTile && ahead_pos < p.max_len)
-    ahead_id = p.table[static_cast<long long>(b) * p.table_row + ahead_pos / p.page_size];
+    ahead_id = p.table[static_cast<long long>(b) * p.table_row + ahead_pos / p.by_page];
   const Seq s = sequence(p, b);
   if (!s.ok) {
     if (z == 0 && blockIdx.y == 0 && tid == 0) note_error(p.pending, W4G128_ERR_CACHE);
@@ -233,11 +246,12 @@ attend_kernel(const __grid_constant__ Params p) {
   const int r = lane >> 2, c = lane & 3;
   const int row0 = (rg * RT + rt) * 16 + r;
   const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
-  const int pos_a = row0 < live_rows ? s.start + row0 / p.group : -1;  // the rows' positions
-  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.group : -1;
+  const int pos_a = row0 < live_rows ? s.start + row0 / p.by_group : -1;  // the rows' positions
+  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.by_group : -1;
   auto q_row = [&](int row) {
-    return p.q + static_cast<long long>(s.first_row + row / p.group) * p.q_row +
-           static_cast<long long>(head * p.group + row % p.group) * D;
+    const int i = row / p.by_group;
+    return p.q + static_cast<long long>(s.first_row + i) * p.q_row +
+           static_cast<long long>(head * p.group + row - i * p.group) * D;
   };
   constexpr int kQPer = RT * 16 * kPieces / S::kThreads;
   static_assert(S::kQInRegs || RT * 16 * kPieces % S::kThreads == 0, "each thread loads as many pieces of Q");
@@ -268,28 +282,13 @@ attend_kernel(const __grid_constant__ Params p) {
   for (int t = tid; t < tiles; t += S::kThreads) {
     const int a = p0 + t * kTile;
     const bool seen = a < s.sink || (a + kTile > s.lo && a < s.len);
-    const int id = !seen ? -1 : p.window == 0 ? ahead_id : p.table[static_cast<long long>(b) * p.table_row + a / p.page_size];
+    const int page = a / p.by_page;
+    const int id = !seen ? -1 : p.window == 0 ? ahead_id : p.table[static_cast<long long>(b) * p.table_row + page];
     const bool ok = id >= 0 && id < p.pages;
     if (seen && !ok) note_error(p.pending, W4G128_ERR_CACHE);
-    s_tile[t] = ok ? id * p.page_stride + (a % p.page_size) * p.slot_stride + head * p.head_stride : -1;
+    s_tile[t] = ok ? id * p.page_stride + (a - page * p.page_size) * p.slot_stride + head * p.head_stride : -1;
   }
 
-  // (a negative scale goes into q's signs, a scale of 0 makes q 0)
-  auto signed_q = [&](uint32_t v) { return (v & p.keep_q) ^ p.flip_q; };
-  if constexpr (S::kQInRegs) {
-#pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) qf[k][i] = signed_q(qf[k][i]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < kQPer; ++e) {
-      const int i = tid + e * S::kThreads, j = i / kPieces, piece = i % kPieces;
-      const uint4 v = q_part[e];
-      *reinterpret_cast<uint4*>(smem + j * S::kRowBytes + ((piece ^ (j & 7)) << 4)) =
-          make_uint4(signed_q(v.x), signed_q(v.y), signed_q(v.z), signed_q(v.w));
-    }
-  }
   __syncthreads();
 
   float acc[S::kHalf / 8][4];
@@ -367,6 +366,24 @@ attend_kernel(const __grid_constant__ Params p) {
     issue(ahead, i);
     ahead = next_tile(ahead + S::kKg);
   }
+
+  // (a negative scale goes into q's signs, a scale of 0 makes q 0)
+  auto signed_q = [&](uint32_t v) { return (v & p.keep_q) ^ p.flip_q; };
+  if constexpr (S::kQInRegs) {
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qf[k][i] = signed_q(qf[k][i]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kQPer; ++e) {
+      const int i = tid + e * S::kThreads, j = i / kPieces, piece = i % kPieces;
+      const uint4 v = q_part[e];
+      *reinterpret_cast<uint4*>(smem + j * S::kRowBytes + ((piece ^ (j & 7)) << 4)) =
+          make_uint4(signed_q(v.x), signed_q(v.y), signed_q(v.z), signed_q(v.w));
+    }
+  }
+  if constexpr (!S::kQInRegs) __syncthreads();
 
   // ldmatrix: this lane's row of a K and of a V tile, and its pieces 0, 2, 4, 6
   // (the others follow at constant distances).
@@ -600,8 +617,10 @@ attend_kernel(const __grid_constant__ Params p) {
     const float l = side ? l_b : l_a;
     if (direct) {
       const float inv = l == 0.f ? 0.f : 1.f / l;  // no visible position: zeros
-      uint32_t* o = reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + row / p.group) * p.out_row +
-                                                static_cast<long long>(head * p.group + row % p.group) * D + half * S::kHalf);
+      const int i_new = row / p.by_group;
+      uint32_t* o = reinterpret_cast<uint32_t*>(
+          p.out + static_cast<long long>(s.first_row + i_new) * p.out_row +
+          static_cast<long long>(head * p.group + row - i_new * p.group) * D + half * S::kHalf);
 #pragma unroll
       for (int i = 0; i < S::kHalf / 8; ++i) o[i * 4 + c] = pack_bf16(acc[i][2 * side] * inv, acc[i][2 * side + 1] * inv);
     } else {
@@ -633,7 +652,7 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Pa
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
-  const int head = hq / p.group, row = i * p.group + hq % p.group;
+  const int head = hq / p.by_group, row = i * p.group + hq - head * p.group;
   const long long step = static_cast<long long>(p.kv_heads) * (p.max_new * p.group);
   const long long at0 = (static_cast<long long>(b) * p.splits * p.kv_heads + head) * (p.max_new * p.group) + row;
 
@@ -786,11 +805,12 @@ size_t bytes_for(const w4g128_attend_args& a) {
 }
 
 template <int D, int RT>
-cudaError_t launch_attend(cudaLaunchConfig_t& cfg, const Params& p) {
+cudaError_t launch_attend(cudaLaunchConfig_t& cfg, Params& p) {
   using S = Shape<D, RT>;
   const cudaError_t e = cudaFuncSetAttribute(attend_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
   if (e != cudaSuccess) return e;
   const int row_groups = (p.max_new * p.group + 16 * RT - 1) / (16 * RT);
+  p.by_row_groups = divisor(row_groups);
   cfg.gridDim = dim3(p.splits, p.kv_heads * row_groups, p.count);
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kBytes;
@@ -798,7 +818,7 @@ cudaError_t launch_attend(cudaLaunchConfig_t& cfg, const Params& p) {
 }
 
 template <int D>
-cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
+cudaError_t launch_dim(cudaLaunchConfig_t& cfg, Params& p) {
   const int rows = p.max_new * p.group;
   const cudaError_t e = rows <= 16 ? launch_attend<D, 1>(cfg, p) : rows <= 32 ? launch_attend<D, 2>(cfg, p)
                                                                               : launch_attend<D, 4>(cfg, p);
@@ -844,6 +864,9 @@ int w4g128_attend(const w4g128_attend_args* a, void* ws, size_t ws_bytes, void* 
   p.window = a->window; p.sinks = a->sinks;
   p.chunk = chunk_for(*a);
   p.splits = splits_for(*a, p.chunk);
+  p.by_chunk = divisor(p.chunk);
+  p.by_group = divisor(p.group);
+  p.by_page = divisor(p.page_size);
   p.scale2 = a->scale == 0.f ? 1.f : std::fabs(a->scale) * 1.44269504088896340736f;
   p.flip_q = a->scale < 0.f ? 0x80008000u : 0u;
   p.keep_q = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
