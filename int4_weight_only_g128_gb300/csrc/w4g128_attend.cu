@@ -40,6 +40,7 @@
 #include <cstdint>
 
 #include "w4g128_ops.h"
+#include "w4g128_divide.cuh"
 #include "w4g128_internal.h"
 #include "w4g128_ptx.cuh"
 #include "w4g128_status.cuh"
@@ -57,18 +58,6 @@ constexpr float kNone = -INFINITY;
 // at 32771: 98.6 -> 89.4 us; 16 ragged sequences 21.3 -> 19.3).
 constexpr float kSlack = 8.f;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
-
-// A divisor and 2^32 over it: the compiler's divide by a value that it does not
-// know is a chain of some 30 instructions, and a call's start has a dozen of them.
-struct Divisor {
-  unsigned d, m;
-};
-Divisor divisor(int d) { return {static_cast<unsigned>(d), d == 1 ? ~0u : static_cast<unsigned>((1ull << 32) / d)}; }
-// a / d for a >= 0: m falls short of 2^32 / d by less than 1, a m / 2^32 of a / d by less than 1.
-__device__ __forceinline__ int operator/(int a, Divisor by) {
-  const unsigned q = __umulhi(static_cast<unsigned>(a), by.m);
-  return static_cast<int>(q + (static_cast<unsigned>(a) - q * by.d >= by.d ? 1u : 0u));
-}
 
 struct Params {
   const uint16_t *q, *k_new, *v_new;

@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "w4g128_ops.h"
+#include "w4g128_divide.cuh"
 #include "w4g128_internal.h"
 #include "w4g128_ptx.cuh"
 
@@ -89,6 +90,9 @@ struct Params {
   uint16_t* y;
   const uint8_t *gate_up, *down;
   int M, D, F, E, top_k, renormalize;
+  Divisor by_top_k;
+  Divisor by_per;     // units of an expert, of the launch
+  int lead;           // how far ahead its units are drawn
   unsigned* status;
   unsigned* next;     // [2]: units handed out beyond the first ones, of each expert kernel
   Lists* lists;
@@ -210,7 +214,7 @@ __device__ __forceinline__ void make_lists(const Params& p, RouteShared& s) {
   const int tid = threadIdx.x, lane = tid & 31, picks = p.M * p.top_k;
   for (int i = tid; i < picks; i += kRouteThreads) {
     const int e = s.chosen[i];  // two experts' marks share a word
-    atomicOr(reinterpret_cast<unsigned*>(s.rows) + e / 2, (1u << (i / p.top_k)) << (e % 2 * 16));
+    atomicOr(reinterpret_cast<unsigned*>(s.rows) + e / 2, (1u << (i / p.by_top_k)) << (e % 2 * 16));
   }
   __syncthreads();
   if (tid < 32) {
@@ -251,7 +255,7 @@ __device__ __forceinline__ void make_lists(const Params& p, RouteShared& s) {
   }
   __syncthreads();
   for (int i = tid; i < picks; i += kRouteThreads) {
-    const int e = s.chosen[i], m = i / p.top_k;
+    const int e = s.chosen[i], m = i / p.by_top_k;
     p.lists->pick[s.index[e] + __popc(s.rows[e] & ((1u << m) - 1u))] = static_cast<uint16_t>(i);
   }
 }
@@ -331,11 +335,12 @@ route_kernel(const __grid_constant__ Params p) {
   const int r = lane >> 2, c = lane & 3;
   // tiles of 8 experts; where there are few, up to 4 warps share one and split its depth
   const int tiles = (p.E + 7) / 8;
-  const int sub = tiles * 4 <= kRouteWarps ? 4 : tiles * 2 <= kRouteWarps ? 2 : 1;
-  const int slices = kRouteCtas * sub, slice = rank * sub + warp % sub;
-  const int steps = p.D / 32, k0 = steps * slice / slices, k1 = steps * (slice + 1) / slices;
+  const int log_sub = tiles * 4 <= kRouteWarps ? 2 : tiles * 2 <= kRouteWarps ? 1 : 0, sub = 1 << log_sub;
+  const int slices = kRouteCtas * sub, slice = rank * sub + (warp & (sub - 1));
+  const int steps = p.D / 32, k0 = steps * slice >> (3 + log_sub), k1 = steps * (slice + 1) >> (3 + log_sub);
+  static_assert(kRouteCtas == 8, "2^3");
   // the router does not depend on the kernels before: into the L2 while they finish
-  for (int t = warp / sub; t < tiles; t += kRouteWarps / sub) {
+  for (int t = warp >> log_sub; t < tiles; t += kRouteWarps >> log_sub) {
     const char* w = reinterpret_cast<const char*>(p.router + static_cast<long long>(min(t * 8 + lane % 8, p.E - 1)) * p.D);
     for (int at = k0 * 64 + lane / 8 * 128; at < k1 * 64; at += 512)
       asm volatile("prefetch.global.L2 [%0];" ::"l"(w + at));
@@ -353,7 +358,7 @@ route_kernel(const __grid_constant__ Params p) {
   const uint4* xa = reinterpret_cast<const uint4*>(p.x + static_cast<long long>(min(r, p.M - 1)) * p.D) + c;
   const uint4* xb = reinterpret_cast<const uint4*>(p.x + static_cast<long long>(min(r + 8, p.M - 1)) * p.D) + c;
   bool waited = false;
-  for (int t = warp / sub; t < tiles; t += kRouteWarps / sub) {
+  for (int t = warp >> log_sub; t < tiles; t += kRouteWarps >> log_sub) {
     // rows and experts beyond the last repeat it; nothing of theirs is kept
     const uint4* w = reinterpret_cast<const uint4*>(p.router + static_cast<long long>(min(t * 8 + r, p.E - 1)) * p.D) + c;
     float d[4] = {};
@@ -488,9 +493,11 @@ __device__ __forceinline__ void count_units(const Params& p, int entries, uint16
     if (lane == 0) *s_count = __popc(mask);
   }
   team_barrier<TEAM>(team);
-  const int each = p.M * COLS / 2, total = static_cast<int>(*s_count) * each;
-  for (int o = member * 32 + lane; o < total; o += TEAM * 32)
-    add_picks(p, o % each / (COLS / 2), places[o / each] * COLS + o % (COLS / 2) * 2);
+  const int log_rows = p.M - 1, total = static_cast<int>(*s_count) * (COLS / 2) << log_rows;  // 1 or 2 rows
+  for (int o = member * 32 + lane; o < total; o += TEAM * 32) {
+    const int at = o / (COLS / 2);
+    add_picks(p, at & log_rows, places[at >> log_rows] * COLS + o % (COLS / 2) * 2);
+  }
 }
 
 // PHASE 0: gate and up, a unit is TILES / 2 gate tiles and their up tiles; 1:
@@ -532,15 +539,13 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
   // before it is worked on, so that the copies can run ahead of it; where a
   // warp may find no item in a unit, all units are handed out evenly.
   const int share = blockIdx.x + gridDim.x * team, shares = gridDim.x * kTeams;
-  const int fewest = max(G / kParts * kMine, 1);  // items of a warp in a unit
-  const int lead = 1 + (S::kStages + fewest) / fewest;
+  const int lead = p.lead;
   const bool drawn = G >= kParts && lead < kQueue;
   static_assert(S::kStages + 2 < kQueue, "the longest lead fits the queue");
-  const int per = (PHASE == 0 ? p.F : p.D) / (kSide * kTileN);  // units of an entry
   __syncthreads();
-  const int units = lists.entries * per;
+  const int units = lists.entries * static_cast<int>(p.by_per.d);
   auto locate = [&](int u) -> uint32_t {  // entry and place, or the end
-    return u < units ? static_cast<uint32_t>(u / per) << 16 | static_cast<uint32_t>(u % per) : kEnd;
+    return u < units ? static_cast<uint32_t>(u / p.by_per) << 16 | static_cast<uint32_t>(u % p.by_per) : kEnd;
   };
   if (member == 0 && lane < kQueue) s_unit[team][lane] = locate(share + lane * shares);
   __syncthreads();
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     if (a != x_entry) {
       x_entry = a;
       const int pick = lists.pick[min(lists.first[a] + r, lists.first[a + 1] - 1)];
-      const int row = PHASE == 0 ? pick / p.top_k : pick;
+      const int row = PHASE == 0 ? pick / p.by_top_k : pick;
       x_row = (PHASE == 0 ? p.xp : p.act) + static_cast<long long>(row) * K * 2 + 16 * c;
       x_scale = (PHASE == 0 ? reinterpret_cast<const int*>(p.unscale) : reinterpret_cast<const int*>(p.act_top)) + row;
       if (PHASE == 1) x_exps = p.act_exp + static_cast<long long>(row) * (G * 8);
@@ -836,7 +841,10 @@ Layout layout(const w4g128_moe_args& a) {
 }
 
 template <int PHASE, int TILES, int TEAM, bool ADD = false>
-cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, long long units) {
+cudaError_t launch_expert(cudaLaunchConfig_t& cfg, Params& p, int sms, long long units) {
+  const int fewest = std::max((PHASE == 0 ? p.D : p.F) / kGroup / kParts * (kParts / TEAM), 1);  // items of a warp in a unit
+  p.lead = 1 + (Stream<TILES>::kStages + fewest) / fewest;
+  p.by_per = divisor((PHASE == 0 ? p.F : p.D) / ((PHASE == 0 ? TILES / 2 : TILES) * kTileN));
   constexpr int kBytes = Stream<TILES>::kBytes;
   const cudaError_t e =
       cudaFuncSetAttribute(expert_kernel<PHASE, TILES, TEAM, ADD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
@@ -850,7 +858,7 @@ cudaError_t launch_expert(cudaLaunchConfig_t& cfg, const Params& p, int sms, lon
 // Wide items, and small teams in the down projection, where there are units
 // enough (7 rows of 2176, experts of 896: gate and up 15.0 -> 13.8 us, down 11.2
 // -> 10.7 us; but one row of 5120, 1408 down: 13.6 us narrow, 13.4 wide).
-cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
+cudaError_t launch_experts(cudaLaunchConfig_t& cfg, Params& p, int sms) {
   const long long most = std::min(p.M * p.top_k, p.E);  // picked experts
   const long long gate = most * (p.F / 32), down = most * (p.D / 64);
   cudaError_t e = gate >= 3 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
@@ -865,7 +873,7 @@ cudaError_t launch_experts(cudaLaunchConfig_t& cfg, const Params& p, int sms) {
   return cudaLaunchKernelEx(&cfg, combine_kernel, p);
 }
 
-cudaError_t launch(const Params& p, cudaStream_t stream) {
+cudaError_t launch(Params& p, cudaStream_t stream) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -910,6 +918,7 @@ int w4g128_moe(const w4g128_moe_args* a, void* ws, size_t ws_bytes, void* stream
   p.gate_up = static_cast<const uint8_t*>(a->gate_up);
   p.down = static_cast<const uint8_t*>(a->down);
   p.M = a->M; p.D = a->D; p.F = a->F; p.E = a->E; p.top_k = a->top_k; p.renormalize = a->renormalize;
+  p.by_top_k = divisor(p.top_k);
   p.status = reinterpret_cast<unsigned*>(base);
   p.next = reinterpret_cast<unsigned*>(base + 16);
   p.lists = reinterpret_cast<Lists*>(base + l.lists);
