@@ -21,12 +21,12 @@
 //     ldmatrix, V by ldmatrix.trans, from rows whose 16-byte pieces are
 //     exchanged by the low bits of the position, free of bank conflicts.
 // Measured, one sequence of 32771, 8 heads of 128, 8 new tokens of 32 query
-// heads (134 MB): 29.8 us a call, 66% of the measured copy rate; the tile loop
-// streams at about 5.5 TB/s, the rest is each CTA's start (length, table, first
-// tiles: 3 us), the join of its groups and the second kernel (4 us).  With 64
-// rows the tile loop's latency binds: 1.9 instructions a clock, the tensor pipe
-// 38% and shared memory 60% busy (two of window 4096, 4 heads of 256, 16 new
-// tokens: 22.7 us against 7.9 us of MMA).  Not kept there: two row tiles a warp
+// heads (134 MB): 29.4 us a call, 67% of the measured copy rate; the tile loop
+// streams at 6.7 TB/s, the rest is each CTA's start (length, table: 2.4 us), the
+// join of its groups (1.5 us) and the second kernel (4 us).  With 64 rows the
+// tile loop's latency binds: 1.9 instructions a clock, the tensor pipe 38% and
+// shared memory 60% busy (two of window 4096, 4 heads of 256, 16 new tokens:
+// 22.7 us against 7.9 us of MMA).  Not kept there: two row tiles a warp
 // at 255 registers (8 long 34.9 us, 30.5 without), two position tiles a turn of
 // the loop (22.8 and 22.7: the same).
 // Positions masked for some row hold arbitrary bits, and 0 x NaN is NaN: tiles
@@ -733,8 +733,8 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Pa
 // have lengths of their own, half of max_len on average.  A window: 304, and 152
 // for heads of 256, whose CTAs of 64 rows fill an SM.  Not less than 128 past
 // 2048 positions: the second kernel takes 32 chunks at once.  Measured, per call:
-// one sequence of 32771, 8 heads of 128, 32 rows: 33.1 us at 304, 34.0 at 264,
-// 47.1 at 352 and 41.2 at 592 (a second wave); 16 sequences of up to 9008, 4
+// one sequence of 32771, 8 heads of 128, 32 rows: 30.6 us at 304, 38.5 at 456 (a
+// second wave); 16 sequences of up to 9008, 4
 // heads of 64, 18 rows: 20.1 us at 608, 21.5 at 760, 22.2 at 456; 16 of 4099, 8
 // heads of 128, 4 rows: 51.2, 48.2 and 52.0.  Windows of 4096: two, 4 heads of
 // 256, 64 rows: 23.5 us at 152, 30.9 at 304; eight, 8 heads of 128, 4 rows: 35.6
