@@ -713,11 +713,13 @@ int held() {
 }
 
 // The largest cluster of which the device holds one for each row at once, so
-// that no row waits for another (16 CTAs halve the counting of 8); beyond that
-// 4, where a slice still fits.
+// that no row waits for another; beyond that 4, where a slice still fits.  16
+// CTAs halve the counting of 8, but wait longer for each other: one row of 32000
+// takes 14.0 us with 16 and 13.0 with 8, of 65000 14.3 and 14.1, of 131072 15.3
+// and 15.5, of 248320 15.9 and 17.5.
 int cluster_for(int rows, int vocab) {
   static const int most16 = held<16>(), most8 = held<8>(), most6 = held<6>();  // (devices that run this are alike)
-  if (rows <= most16) return 16;
+  if (rows <= most16 && vocab > 65536) return 16;
   if (rows <= most8) return 8;
   if (rows <= most6 && slice_fits(vocab, 6)) return 6;
   return slice_fits(vocab, 4) ? 4 : 8;
