@@ -730,21 +730,22 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Pa
 // Positions per chunk: the multiple of 64 that cuts the call's positions (span
 // x heads x sequences) into a few chunks for each SM.  One sequence: 304, as
 // many CTAs of 32 rows as the GPU holds at once.  A batch: 608, as its sequences
-// have lengths of their own, half of max_len on average.  A window: 304, and 152
-// for heads of 256, whose CTAs of 64 rows fill an SM.  Not less than 128 past
-// 2048 positions: the second kernel takes 32 chunks at once.  Measured, per call:
-// one sequence of 32771, 8 heads of 128, 32 rows: 30.6 us at 304, 38.5 at 456 (a
-// second wave); 16 sequences of up to 9008, 4
-// heads of 64, 18 rows: 20.1 us at 608, 21.5 at 760, 22.2 at 456; 16 of 4099, 8
-// heads of 128, 4 rows: 51.2, 48.2 and 52.0.  Windows of 4096: two, 4 heads of
-// 256, 64 rows: 23.5 us at 152, 30.9 at 304; eight, 8 heads of 128, 4 rows: 35.6
-// and 29.9.  Chunks of 128 for 64: 4 of 4099, 2 heads of 256: 12.4 us for 17.5;
-// one of 2049, 8 heads of 128: 6.9 for 7.7; but one of 611: 7.4 for 6.6.
+// have lengths of their own, half of max_len on average, and 684 for 16 or more
+// sequences, whose CTAs even out.  A window: 304, and 152 for heads of 256, whose
+// CTAs of 64 rows fill an SM.  Not less than 128 past 2048 positions: the second
+// kernel takes 32 chunks at once.  Measured, us per call: one sequence of 32771,
+// 8 heads of 128, 32 rows: 30.6 at 304, 38.5 at 456 (a second wave).  Eight of up
+// to 6000, 8 heads of 128, 24 rows: 24.2 at 608, 28.1 at 684, 26.2 at 456.  16 of
+// up to 9001, 4 heads of 64: 18 rows 18.1 at 684, 18.4 at 608, 19.8 at 760; 6
+// rows 13.6, 14.6 and 13.5.  Windows of 4096: two, 4 heads of 256, 64 rows: 23.5
+// at 152, 30.9 at 304; eight, 8 heads of 128, 4 rows: 35.6 and 29.9.  Chunks of
+// 128 for 64: 4 of 4099, 2 heads of 256: 12.4 for 17.5; one of 2049, 8 heads of
+// 128: 6.9 for 7.7; but one of 611: 7.4 for 6.6.
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);
   const long long all = span * a.kv_heads * a.count;
-  const int target = a.window > 0 ? (a.head_dim == 256 ? 152 : 304) : a.count == 1 ? 304 : 608;
+  const int target = a.window > 0 ? (a.head_dim == 256 ? 152 : 304) : a.count == 1 ? 304 : a.count < 16 ? 608 : 684;
   const long long least = a.window == 0 && a.max_len > 2048 ? 128 : 64;
   const long long chunk = std::max(least, (all + 64LL * target - 1) / (64LL * target) * 64);
   return static_cast<int>(std::min<long long>(chunk, kMaxChunk));
