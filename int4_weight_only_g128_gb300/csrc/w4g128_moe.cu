@@ -426,8 +426,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// TILES of 16 columns per item: 2, or 4 where there are units enough for every
-// team to have several (half the loads of x and half the work per unit).
+// TILES of 16 columns per item: 4, or 2 in a down projection with few units (4:
+// half the loads of x and half the work per unit).
 template <int TILES>
 struct Stream {
   static constexpr int kStage = TILES * kBlockBytes;
@@ -855,17 +855,20 @@ cudaError_t launch_expert(cudaLaunchConfig_t& cfg, Params& p, int sms, long long
   return cudaLaunchKernelEx(&cfg, expert_kernel<PHASE, TILES, TEAM, ADD>, p);
 }
 
-// Wide items, and small teams in the down projection, where there are units
-// enough (7 rows of 2176, experts of 896: gate and up 15.0 -> 13.8 us, down 11.2
-// -> 10.7 us; but one row of 5120, 1408 down: 13.6 us narrow, 13.4 wide).
+// Gate and up in wide items (one row of 5120, 8 experts of 1408: 34.2 us a call,
+// 34.9 narrow; of 4096, 6 experts: 25.7 and 27.0).  Down wide and in small teams,
+// too, where every SM has units (one row of 7168, 8 experts of 2048: 47.2 us, 50.1
+// narrow; 16 rows of 4096, 8 experts of 4096: 51.3 and 54.8), else narrow in large
+// teams (one row of 2048, 4 experts of 768: 12.8 us, in small teams 13.4).
 cudaError_t launch_experts(cudaLaunchConfig_t& cfg, Params& p, int sms) {
   const long long most = std::min(p.M * p.top_k, p.E);  // picked experts
   const long long gate = most * (p.F / 32), down = most * (p.D / 64);
-  cudaError_t e = gate >= 3 * sms ? launch_expert<0, 4, 8>(cfg, p, sms, gate)
-                                  : launch_expert<0, 2, 8>(cfg, p, sms, 2 * gate);
+  const bool wide = down >= 2 * sms;
+  cudaError_t e = launch_expert<0, 4, 8>(cfg, p, sms, gate);
   if (e != cudaSuccess) return e;
-  if (p.M <= 2) return launch_expert<1, 2, 4, true>(cfg, p, sms, 2 * down);
-  e = down >= 4 * sms ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
+  if (p.M <= 2)
+    return wide ? launch_expert<1, 4, 4, true>(cfg, p, sms, down) : launch_expert<1, 2, 8, true>(cfg, p, sms, 2 * down);
+  e = wide ? launch_expert<1, 4, 4>(cfg, p, sms, down) : launch_expert<1, 2, 8>(cfg, p, sms, 2 * down);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((p.D / 2 + 127) / 128, p.M);
   cfg.blockDim = dim3(128);
