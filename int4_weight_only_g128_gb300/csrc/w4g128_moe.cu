@@ -45,8 +45,8 @@
 // Measured: 16 rows, 5120 x 1408, 6 of 96 experts (712 MB): 132 us a call, 80% of
 // the measured copy rate; gate and up 72 us (6.1 TB/s), down 47 us (4.7 TB/s:
 // units of 11 groups, a barrier of the team and a fold for every 2.75 items of a
-// warp).  One row, 8 of 64 experts (93 MB): 35.5 us: routing 5.1, lists and first
-// copies 2.8, gate and up 12, the change of kernels 2, down 8, adding up 2, the
+// warp).  One row, 8 of 64 experts (93 MB): 34.6 us: routing 5.0, lists and first
+// copies 2.6, gate and up 12, the change of kernels 2, down 7.5, adding up 2, the
 // rest launches: what is left above the 13.7 us of bytes is latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
