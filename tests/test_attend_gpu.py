@@ -197,6 +197,27 @@ def test_a_row_alone_gives_the_same_bits(dim, window, sinks):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 48), (256, 64)])
+@pytest.mark.parametrize("seqs", [[(4099, 9)], [(4097, 3), (130, 16), (0, 2), (2600, 1)],
+                                  [(5000 - 301 * b, (5 * b + 2) % 17) for b in range(16)]], ids=["1", "4", "16"])
+def test_many_chunks(seqs, dim, page):
+    """Lengths on both sides of 2048 and more chunks than are joined at once, for one sequence, a few and many."""
+    kw = dict(q_heads=6, kv_heads=2, dim=dim, page=page, max_len=5040)
+    c = Call(seqs, seed=9, **kw)
+    together = c.check().clone()
+    for b, (n, new) in enumerate(seqs[:4]):
+        for i in range(0, new, 4):
+            one = Call([(n - new + i + 1, 1)] + [(0, 0)] * (len(seqs) - 1), seed=9, **kw) if n >= new else None
+            if one is None:
+                continue
+            one.k_cache, one.v_cache, one.pages = c.k_cache, c.v_cache, c.pages
+            one.table = c.table[b:b + 1].repeat(len(seqs), 1)
+            r = c.offsets[b] + i
+            one.q[0], one.k_new[0], one.v_new[0] = c.q[r], c.k_new[r], c.v_new[r]
+            assert torch.equal(one.run()[0], together[r]), (b, i)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_masked_values_take_no_part(dim, bad):

@@ -167,6 +167,17 @@ def test_a_row_alone_gives_the_same_bits(shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(1, 4096, 256, 12, 6), (2, 4096, 256, 12, 6), (2, 1024, 256, 12, 2),
+                                   (1, 65536, 128, 24, 16), (2, 65536, 128, 24, 16)], ids=str)
+def test_one_and_two_rows_add_up_in_the_down_projection(shape):
+    """Few units and many, up to more than a team adds up at once."""
+    layer = Layer(*shape, seed=6)
+    y = layer.check()
+    for m in range(shape[0]):
+        assert torch.equal(layer.run(layer.x[m:m + 1], layer.residual[m:m + 1]), y[m:m + 1]), m
+
+
+@pytest.mark.gpu
 def test_every_row_on_one_expert_and_equal_logits():
     """Equal logits (a router of zeros, with either sign of zero): the lowest experts, at equal weights; 16 rows of
     one expert fill both 8-row operand tiles."""
