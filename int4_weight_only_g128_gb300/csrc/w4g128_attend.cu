@@ -204,7 +204,9 @@ attend_kernel(const __grid_constant__ Params p) {
   const int b = blockIdx.z, z = blockIdx.x;
 
   grid_dependency_wait();
-  const bool direct = p.splits == 1;  // (max_len is at most a chunk: this kernel is the call)
+  // (max_len is at most a chunk: this kernel is the call.  It reports errors itself: noted ones would stay in the
+  // pending word, which only the second kernel empties, and reach the next call on the workspace that has one)
+  const bool direct = p.splits == 1;
   if (direct && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0) {
     bool bad = false;
     for (int i = tid; i < p.count; i += S::kThreads) bad |= !in_range(p, i);
@@ -219,7 +221,7 @@ attend_kernel(const __grid_constant__ Params p) {
     ahead_id = p.table[static_cast<long long>(b) * p.table_row + ahead_pos / p.by_page];
   const Seq s = sequence(p, b);
   if (!s.ok) {
-    if (z == 0 && blockIdx.y == 0 && tid == 0) note_error(p.pending, W4G128_ERR_CACHE);
+    if (!direct && z == 0 && blockIdx.y == 0 && tid == 0) note_error(p.pending, W4G128_ERR_CACHE);
     return;
   }
   const int live_rows = s.n * p.group;
@@ -274,7 +276,7 @@ attend_kernel(const __grid_constant__ Params p) {
     const int page = a / p.by_page;
     const int id = !seen ? -1 : p.window == 0 ? ahead_id : p.table[static_cast<long long>(b) * p.table_row + page];
     const bool ok = id >= 0 && id < p.pages;
-    if (seen && !ok) note_error(p.pending, W4G128_ERR_CACHE);
+    if (seen && !ok && !direct) note_error(p.pending, W4G128_ERR_CACHE);
     s_tile[t] = ok ? id * p.page_stride + (a - page * p.page_size) * p.slot_stride + head * p.head_stride : -1;
   }
 

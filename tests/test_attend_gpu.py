@@ -443,3 +443,33 @@ def test_errors_of_calls_of_one_chunk():
         field[at] = keep
     c.table[1, 2] = -9  # behind the length: not seen
     assert torch.equal(c.run(), clean)
+
+
+@pytest.mark.gpu
+def test_an_error_stays_with_its_call():
+    """One workspace for calls of one chunk and of several, in turn: each reports its own errors alone."""
+    short = Call([(40, 2), (30, 1)], max_len=48, seed=17)
+    split = Call([(700, 2), (300, 1)], max_len=1024, seed=18)
+    nb = [w.w4g128_attend_workspace_bytes(c.args()) for c in (short, split)]
+    assert nb[0] < nb[1]  # the short one keeps no sums of chunks
+    ws = torch.full((nb[1],), 0x5A, dtype=torch.uint8, device="cuda")
+    good = [c.run().clone() for c in (short, split)]
+
+    def call(c, field=None, at=None, wrong=None):
+        keep = field[at].item() if field is not None else None
+        if field is not None:
+            field[at] = wrong
+        w.w4g128_attend(c.args(), ws)
+        torch.cuda.synchronize()
+        if field is not None:
+            field[at] = keep
+        return w.w4g128_workspace_status(ws)
+
+    for c, other in ((short, split), (split, short)):
+        for wrong in ((c.lens, 1, c.max_len + 1), (c.lens, 0, -1), (c.offsets_d, 2, 1), (c.table, (0, 1), c.pages)):
+            assert call(c, *wrong) == w.ERR_CACHE
+            assert call(other) == 0 and call(c) == 0
+            assert call(c, *wrong) == w.ERR_CACHE
+            assert call(c) == 0 and call(other) == 0
+    for c, want in zip((short, split), good):
+        assert torch.equal(c.out.view(c.rows, c.Hq, c.D), want)
