@@ -28,9 +28,12 @@
 //   gate and up: x is bf16; values down to 2^-31 of the row's largest are
 //     exact, smaller ones off by at most 2^-40 of it;
 //   down: an activation is rounded to fp16 where it is computed, scaled by its
-//     16-column tile's largest, since the row's is not known yet (2^-12
+//     16-column tile's largest, since the row's is not known yet (2^-11
 //     relative, an eighth of bf16's rounding); the tile's exponent goes along,
-//     and the operand is brought to the row's exponent when it is used.
+//     and the operand is brought to the row's exponent when it is used, by
+//     2^-24 at most and what is beyond before that.  It errs there by half a
+//     step, 2^-39 of the row's largest, and where it is stored by as much of the
+//     tile's.
 // The bias and the group minimum are undone by X = sum_k x per (row, group):
 //   sum_k x w = scale sum_k x (bias + q) + (min - bias scale) X,
 // and an MMA with an all-ones A leaves X in the registers that need it, once
@@ -72,6 +75,7 @@ constexpr int kParts = 8;             // partial sums of a unit
 constexpr size_t kStatusBytes = 256;
 constexpr uint32_t kBias = 0x64006400u;  // fp16 1024.0 twice
 constexpr uint32_t kOne = 0x3C003C00u;   // fp16 1.0 twice
+constexpr int kLeastHalf = 24;           // fp16 has no power of two below 2^-24
 
 // Picked experts in rising order with the picks (row * top_k + place, places in
 // rising expert order) that each serves: one entry for up to 8 rows, what an
@@ -663,10 +667,14 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
     next_slot = next_slot == S::kStages ? 0 : next_slot + 1;
     scale = x.scale;
     if (PHASE == 1) {  // a tile is a k step: to the row's exponent
+      int below[8], most = 0;  // binary orders between the tile's largest and the row's
 #pragma unroll
       for (int s = 0; s < 8; ++s) {
-        const int e = static_cast<int>((s < 4 ? x.exps.x : x.exps.y) >> (8 * (s % 4)) & 0xFFu);
-        const float f = __int_as_float(max(127 + e - x.scale, 0) << 23);
+        below[s] = x.scale - static_cast<int>((s < 4 ? x.exps.x : x.exps.y) >> (8 * (s % 4)) & 0xFFu);
+        most = max(most, below[s]);
+      }
+      auto lower = [&](int s, int orders) {
+        const float f = __int_as_float(max(127 - orders, 0) << 23);
         const __half2 h = __floats2half2_rn(f, f);
         const uint32_t f2 = *reinterpret_cast<const uint32_t*>(&h);
         if (s % 2) {
@@ -676,7 +684,13 @@ __global__ void __launch_bounds__(kThreads, 2) expert_kernel(const __grid_consta
           x.v[s / 2].x = hmul2(x.v[s / 2].x, f2);
           x.v[s / 2].y = hmul2(x.v[s / 2].y, f2);
         }
+      };
+      if (most > kLeastHalf) {  // rare: in two steps, the first one where fp16 has bits to spare
+#pragma unroll
+        for (int s = 0; s < 8; ++s) lower(s, max(below[s] - kLeastHalf, 0));
       }
+#pragma unroll
+      for (int s = 0; s < 8; ++s) lower(s, min(below[s], kLeastHalf));
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(S::kStages - 1) : "memory");
     __syncwarp();

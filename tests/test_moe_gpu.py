@@ -292,3 +292,36 @@ def test_logits_that_are_not_numbers_rank_last():
     ref = Layer(2, 128, 128, 4, 2, seed=10)
     ref.router[1:3] = -1e30 * torch.sign(ref.x[0].float()).bfloat16()  # far below for row 0
     assert torch.equal(got[0], ref.run()[0])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 3, 12])
+@pytest.mark.parametrize("orders", [12, 23, 25, 26, 28, 30])
+def test_activations_far_below_the_largest_of_their_row(orders, M):
+    """Activations `orders` binary orders and more below others of their row, which meet weights of zero.  What an
+    activation a may lose besides its 2^-11 is 2^-39 of the row's largest, T, where it is brought to the row's exponent
+    (and as much of its tile's, at most 2^-11 of T here, where it is stored): a share 2^-39 T / rms(a) of the small
+    ones.  A product with random weights keeps that share, and a share of 2^-11, in the mean over its columns; twice
+    that is allowed, and 2^-8 for the output's rounding."""
+    layer = Layer(M, 256, 384, 4, 2, residual=False, seed=orders)
+    up, down = layer.gate_up, layer.down
+    for t in (up.scales, up.mins):
+        t[:, :, 384:512] *= 2.0 ** orders  # the up columns of activations 0..127
+    for t in (down.scales, down.mins):
+        t[:, 0] = 0                        # and the rows of the down matrix that they meet
+    for m in (up, down):
+        for e in range(m.E):
+            w.w4g128_pack(m.codes[e], m.scales[e], m.mins[e], m.K, m.N, m.packed[e * m.each:], stream=None)
+    y, _, clear = layer.reference()
+    got = layer.check().double()
+    W = [up.matrix(e, 0)[0] for e in range(4)]
+    for r in range(M):
+        if not clear[r]:
+            continue
+        share = 0.0
+        for e in torch.topk(layer.x[r].double() @ layer.router.double().T, 2).indices.tolist():
+            h = layer.x[r].double() @ W[e]
+            a = h[:384] * torch.sigmoid(h[:384]) * h[384:]
+            share = max(share, (2.0 ** -39 * a.abs().max() / a[128:].pow(2).mean().sqrt()).item())
+        assert orders < 30 or share > 2.0 ** -9
+        assert (got[r] - y[r]).norm() <= (2.0 ** -8 + 2 * (2.0 ** -11 + share)) * y[r].norm(), r
