@@ -325,3 +325,21 @@ def test_activations_far_below_the_largest_of_their_row(orders, M):
             share = max(share, (2.0 ** -39 * a.abs().max() / a[128:].pow(2).mean().sqrt()).item())
         assert orders < 30 or share > 2.0 ** -9
         assert (got[r] - y[r]).norm() <= (2.0 ** -8 + 2 * (2.0 ** -11 + share)) * y[r].norm(), r
+
+
+def norm_errors(layer, got):
+    """|got - y| / |y| of each row whose picks are beyond doubt, for a layer without residual.  Bound: the output's
+    rounding 2^-8; the activations' 2^-11, which a product with random weights passes on in the mean, twice that
+    allowed; the three products' fp32 sums, whose terms carry a bias of 1024 (some 224 times the weights), 8 of them
+    truncated by 2^-23 in a group: 2^-12 each.  Together below 2^-8 + 2^-9."""
+    y, _, clear = layer.reference()
+    return ((got.double() - y).norm(dim=1) / y.norm(dim=1))[clear]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("renorm", [True, False])
+def test_norm_of_the_error(shape, renorm):
+    """The element bounds add up worst cases and grow past |y| with the depth; the norm of a row's error does not."""
+    layer = Layer(*shape, renorm=renorm, residual=False, seed=1 + sum(shape))
+    assert (norm_errors(layer, layer.run()) <= 2.0 ** -8 + 2.0 ** -9).all()
