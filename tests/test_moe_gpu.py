@@ -343,3 +343,42 @@ def test_norm_of_the_error(shape, renorm):
     """The element bounds add up worst cases and grow past |y| with the depth; the norm of a row's error does not."""
     layer = Layer(*shape, renorm=renorm, residual=False, seed=1 + sum(shape))
     assert (norm_errors(layer, layer.run()) <= 2.0 ** -8 + 2.0 ** -9).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,kernel", [((16, 1024, 2048, 64, 8), "gate and up"), ((16, 1152, 2048, 64, 8), "gate and up"),
+                                          ((16, 8192, 1024, 64, 8), "down"), ((5, 8192, 1152, 64, 16), "down"),
+                                          ((2, 16384, 1024, 40, 16), "down"), ((1, 20480, 1024, 24, 16), "down")], ids=str)
+def test_units_drawn_from_the_counter(shape, kernel):
+    """More units than the eight that each team knows from the start, and depths of 8 groups and more, where the rest
+    are drawn: against the reference, row by row, back to back on one workspace and replayed."""
+    M, D, F, E, k = shape
+    layer = Layer(*shape, residual=False, seed=12)
+    picked = torch.topk(layer.x.double() @ layer.router.double().T, k).indices.unique().numel()
+    ctas = 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    if kernel == "down":  # units of 64 columns, two teams a CTA
+        assert F >= 1024 and picked * (D // 64) > 8 * 2 * ctas
+    else:                 # of 32 activations, one team
+        assert D >= 1024 and picked * (F // 32) > 8 * ctas
+    y, tol, clear = layer.reference()  # (at these depths the logits' bound leaves some rows' picks in doubt)
+    got = layer.run()
+    assert clear.any() and ((got.double() - y).abs() <= tol)[clear].all()
+    assert (norm_errors(layer, got) <= 2.0 ** -8 + 2.0 ** -9).all()
+    for m in {0, M // 2, M - 1}:
+        assert torch.equal(layer.run(layer.x[m:m + 1]), got[m:m + 1]), m
+    y = torch.zeros_like(got)
+    args = layer.args(y)
+    ws = torch.empty(w.w4g128_moe_workspace_bytes(args), dtype=torch.uint8, device="cuda")
+    for _ in range(8):
+        w.w4g128_moe(args, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(y, got)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.w4g128_moe(args, ws)
+        w.w4g128_moe(args, ws)
+    for _ in range(3):
+        y.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, got)
