@@ -264,3 +264,14 @@ def test_the_cluster_size_changes_no_bit():
     for n in (1, 9, 16):
         t, l, _ = draw(z[:n], T=1.1, p=0.97, u=u[:n])
         assert np.array_equal(t, t30[:n]) and np.array_equal(l.view(np.int32), l30[:n].view(np.int32))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("filters", [dict(), dict(k=3), dict(p=0.8), dict(minp=0.2)], ids=["none", "k", "p", "min"])
+def test_u_of_1_and_above_draws_the_last_kept_token(filters):
+    """Four tokens of real weight each: the fraction just below 1 falls into the last one that the filters keep."""
+    z = np.full((5, 501), -INF)
+    z[:, [77, 3, 402, 500]] = [1.0, 0.5, 0.0, -0.5]
+    tok, _ = check(z, u=[1.0, 5.0, 1e30, INF, 1 - 2.0 ** -24], **filters)
+    assert len(set(tok.tolist())) == 1
+    assert tok[0] == {"k": 402, "p": 402, "minp": 500}.get(next(iter(filters), ""), 500)
