@@ -51,9 +51,12 @@ class _Matrix(ctypes.Structure):
                 ("K", ctypes.c_int), ("N", ctypes.c_int)]
 
 
-def exported_symbols(headers=("w4g128.h", "w4g128_probe.h")):
+def exported_symbols(headers=None):
     """Names of every function the named public headers of include/ declare
-    (the weight stream's by default; w4g128_ops.h: the operators around it)."""
+    (by default all but those of w4g128_ops.h, the operators around the weight
+    stream)."""
+    if headers is None:
+        headers = sorted(fn for fn in os.listdir(_INCLUDE) if fn.endswith(".h") and fn != "w4g128_ops.h")
     names = []
     for fn in headers:
         with open(os.path.join(_INCLUDE, fn)) as f:

@@ -184,3 +184,16 @@ def test_no_device_is_reported():
     assert sample() == E_DEVICE
     assert attend() == E_DEVICE
     assert moe() == E_DEVICE
+
+
+def test_a_header_added_later_is_named(tmp_path, monkeypatch):
+    """By default every public header but the operators', without a list to keep up."""
+    import os
+    import shutil
+    for fn in os.listdir(w._INCLUDE):
+        shutil.copy(os.path.join(w._INCLUDE, fn), tmp_path)
+    before = w.exported_symbols()
+    (tmp_path / "w4g128_later.h").write_text("W4G128_API int w4g128_later(int n);\n")
+    monkeypatch.setattr(w, "_INCLUDE", str(tmp_path))
+    assert sorted(w.exported_symbols()) == sorted(before + ["w4g128_later"])
+    assert not set(before) & set(w.exported_symbols(("w4g128_ops.h",)))
