@@ -154,7 +154,10 @@ struct Params {
 };
 
 struct Settings {
-  Pair rate;  // log2(e) / temperature
+  // log2(e) / temperature, for logits times `down`: above a temperature of 1 2^64 moves from one to the other, so that
+  // neither a difference of logits (up to 2^129) nor a rate (down to 2^-128) leaves the range where a pair is precise
+  Pair rate;
+  float down;
   float min_p, top_p, u;
   int top_k;
 };
@@ -241,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   // The row's settings, read once: a load where each is used would cost its latency there.
   const bool reads = tid == kThreads - 1;
   float T = 1.f;
-  Settings set = {{0.f, 0.f}, 0.f, 1.f, 0.f, 0};
+  Settings set = {{0.f, 0.f}, 1.f, 0.f, 1.f, 0.f, 0};
   if (reads) {
     if (p.temperature) T = p.temperature[row];
     if (p.min_p) set.min_p = p.min_p[row];
@@ -294,7 +297,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
       set.top_p = 1.f;
       set.top_k = 1;
     }
-    const double c = 1.4426950408889634 / static_cast<double>(T);
+    const bool hot = T > 1.f;
+    const double c = (hot ? 1.4426950408889634 * 18446744073709551616. : 1.4426950408889634) / static_cast<double>(T);
+    if (hot) set.down = 1.f / 18446744073709551616.f;
     const float hi = static_cast<float>(c);
     set.rate = {hi, static_cast<float>(c - static_cast<double>(hi))};
     s_set = set;
@@ -385,8 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
   auto key_at = [&](int i) { return static_cast<uint32_t>(s_run[i / kUnit]) * kUnit + (kUnit - 1 - i % kUnit); };
 
   // Weigh the occupied bins, neighbours by neighbouring threads.
-  const float vmax = value_of(maxkey);
   const Pair rate = s_set.rate;
+  const float down = s_set.down, vmax = value_of(maxkey) * down;
   for (int i = tid; i < bins; i += kThreads) {
     if (counts[i]) {
       const uint32_t key = key_at(i);
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const Params p) {
         if (maxkey == kPlusInf) {
           w = 0ull;
         } else {
-          const Pair d = two_sum(vmax, -value_of(key));
+          const Pair d = two_sum(vmax, -value_of(key) * down);
           Pair y = two_prod(d.hi, rate.hi);
           y.lo = __fadd_rn(y.lo, __fmaf_rn(d.hi, rate.lo, d.lo * rate.hi));
           w = exp2_neg(two_sum(y.hi, y.lo), table);

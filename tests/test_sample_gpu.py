@@ -275,3 +275,17 @@ def test_u_of_1_and_above_draws_the_last_kept_token(filters):
     tok, _ = check(z, u=[1.0, 5.0, 1e30, INF, 1 - 2.0 ** -24], **filters)
     assert len(set(tok.tolist())) == 1
     assert tok[0] == {"k": 402, "p": 402, "minp": 500}.get(next(iter(filters), ""), 500)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1.0 + 2.0 ** -23, 7.0, 1e20, 1e31, 1e36, 1e38, 3e38, INF])
+def test_logits_over_the_whole_range_at_high_temperatures(T):
+    """Differences of logits up to twice the largest float, and temperatures whose reciprocal is subnormal: a quotient
+    of the two is an ordinary number."""
+    vals = (np.arange(65536, dtype=np.uint32) << 16).view(np.float32)
+    vals = vals[np.isfinite(vals)].astype(np.float64)
+    rng = np.random.default_rng(10)
+    z = np.stack([rng.permutation(vals) for _ in range(8)])
+    z[4:] = np.where(np.abs(z[4:]) > 2.0 ** 100, z[4:], -INF)  # mass on the large ones alone
+    check(z, T=T, u=rng.random(8))
+    check(z, T=T, u=rng.random(8), p=0.7)
