@@ -120,7 +120,7 @@ typedef struct {
   int max_new;   /* most new rows of a sequence, 1 .. 16 */
   int window;    /* 0: none */
   int sinks;     /* first positions that stay visible behind the window; 0 without a window */
-  float scale;   /* finite */
+  float scale;   /* finite, and so is scale log2(e): up to 2.35e38 either way */
 } w4g128_attend_args;
 
 #define W4G128_MAX_SEQUENCES 1024

@@ -58,6 +58,7 @@ constexpr float kNone = -INFINITY;
 // at 32771: 98.6 -> 89.4 us; 16 ragged sequences 21.3 -> 19.3).
 constexpr float kSlack = 8.f;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
+constexpr float kLog2e = 1.44269504088896340736f;
 
 struct Params {
   const uint16_t *q, *k_new, *v_new;
@@ -769,7 +770,7 @@ int check(const w4g128_attend_args* a) {
     return W4G128_ERR_INVALID_ARG;
   if (a->rows < 1 || a->rows > (1 << 20) || a->count < 1 || a->count > W4G128_MAX_SEQUENCES || a->max_new < 1 ||
       a->max_new > W4G128_MAX_M || a->window < 0 || a->sinks < 0 || (a->sinks > 0 && a->window == 0) ||
-      !std::isfinite(a->scale))
+      !std::isfinite(a->scale * kLog2e))
     return W4G128_ERR_INVALID_ARG;
   if (a->kv_heads < 1 || a->kv_heads > 256 || a->q_heads < a->kv_heads || a->q_heads % a->kv_heads != 0 ||
       a->q_heads / a->kv_heads > 16 || (a->head_dim != 64 && a->head_dim != 128 && a->head_dim != 256))
@@ -859,7 +860,7 @@ int w4g128_attend(const w4g128_attend_args* a, void* ws, size_t ws_bytes, void* 
   p.by_chunk = divisor(p.chunk);
   p.by_group = divisor(p.group);
   p.by_page = divisor(p.page_size);
-  p.scale2 = a->scale == 0.f ? 1.f : std::fabs(a->scale) * 1.44269504088896340736f;
+  p.scale2 = a->scale == 0.f ? 1.f : std::fabs(a->scale) * kLog2e;
   p.flip_q = a->scale < 0.f ? 0x80008000u : 0u;
   p.keep_q = a->scale == 0.f ? 0u : 0xFFFFFFFFu;
   auto* base = static_cast<uint8_t*>(ws);

@@ -197,3 +197,12 @@ def test_a_header_added_later_is_named(tmp_path, monkeypatch):
     monkeypatch.setattr(w, "_INCLUDE", str(tmp_path))
     assert sorted(w.exported_symbols()) == sorted(before + ["w4g128_later"])
     assert not set(before) & set(w.exported_symbols(("w4g128_ops.h",)))
+
+
+def test_attend_refuses_a_scale_that_overflows_with_log2_e(L):
+    """The scores are taken to base 2: scale log2(e) has to be a float, too."""
+    for scale in (2.4e38, -2.4e38, 3.4e38):
+        assert attend(scale=scale) == E_INVALID, scale
+        assert w.w4g128_attend_workspace_bytes(attend_args(scale=scale)) == 0
+    for scale in (2.35e38, -2.35e38, 0.0, 1e-45):
+        assert w.w4g128_attend_workspace_bytes(attend_args(scale=scale)) > 0, scale
