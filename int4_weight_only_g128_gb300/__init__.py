@@ -357,11 +357,13 @@ class _Args(ctypes.Structure):
     """Argument struct of an operator of include/w4g128_ops.h, filled from
     keywords.  A tensor becomes its device pointer (the struct keeps the tensor
     alive); it has to be on a GPU, of the element size that the field holds,
-    and reach at least as far as the sizes say (W4G128_ERR_INVALID_ARG).  Plain
+    contiguous (where the struct has strides for it: in its last dimension), and
+    reach at least as far as the sizes say (W4G128_ERR_INVALID_ARG).  Plain
     integers are raw pointers and are not checked."""
 
     _fn = ""
     _itemsize = {}  # tensor field: bytes of an element
+    _strided = ()   # tensor fields that the struct has strides for
 
     def __init__(self, **fields):
         known = {f[0] for f in self._fields_}
@@ -373,6 +375,9 @@ class _Args(ctypes.Structure):
         for name, t in self._keep.items():
             size = self._itemsize[name]
             if not t.is_cuda or (size and t.element_size() != size):
+                raise W4G128Error(f"{self._fn} ({name})", 1)
+            rows_whole = t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1
+            if not (rows_whole if name in self._strided else t.is_contiguous()):
                 raise W4G128Error(f"{self._fn} ({name})", 1)
             need = self._reach(name)
             # the last element that the tensor's own storage holds behind its first
@@ -416,6 +421,7 @@ class SampleArgs(_Args):
                 ("rows", ctypes.c_int), ("vocab", ctypes.c_int)]
     _itemsize = {"logits": 2, "temperature": 4, "top_k": 4, "top_p": 4, "min_p": 4, "u": 4, "tokens": 4,
                  "logprobs": 4}
+    _strided = ("logits",)
 
     def _reach(self, name):
         return (self.rows - 1) * self.row_stride + self.vocab if name == "logits" else self.rows
@@ -445,6 +451,7 @@ class AttendArgs(_Args):
                                             "max_len", "max_new", "window", "sinks")] + [("scale", ctypes.c_float)]
     _itemsize = {"q": 2, "k_new": 2, "v_new": 2, "k_cache": 2, "v_cache": 2, "page_table": 4, "row_offsets": 4,
                  "lens": 4, "out": 2}
+    _strided = ("q", "k_new", "v_new", "k_cache", "v_cache", "page_table", "out")
 
     def _reach(self, name):
         if name in ("q", "out"):

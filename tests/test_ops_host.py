@@ -206,3 +206,81 @@ def test_attend_refuses_a_scale_that_overflows_with_log2_e(L):
         assert w.w4g128_attend_workspace_bytes(attend_args(scale=scale)) == 0
     for scale in (2.35e38, -2.35e38, 0.0, 1e-45):
         assert w.w4g128_attend_workspace_bytes(attend_args(scale=scale)) > 0, scale
+
+
+class OnGpu:
+    """A CPU tensor that says it is on a GPU, for the binding's checks."""
+    is_cuda = True
+
+    def __init__(self, t, index=0):
+        import torch
+        self._t, self.device = t, torch.device("cuda", index)
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+
+def gpu(*shape, dtype="float32", index=0):
+    import torch
+    return OnGpu(torch.zeros(shape, dtype=getattr(torch, dtype)), index)
+
+
+def view(t, f):
+    """A view of a tensor that says it is on a GPU."""
+    return OnGpu(f(t._t), t.device.index)
+
+
+def sample_tensors(**kw):
+    a = dict(logits=gpu(4, 100, dtype="bfloat16"), row_stride=100, u=gpu(4), tokens=gpu(4, dtype="int32"), rows=4,
+             vocab=100)
+    a.update(kw)
+    return w.SampleArgs(**a)
+
+
+def attend_tensors(**kw):
+    a = dict(q=gpu(4, 8, 64, dtype="bfloat16"), k_new=None, v_new=None, k_cache=gpu(8, 16, 2, 64, dtype="bfloat16"),
+             v_cache=gpu(8, 16, 2, 64, dtype="bfloat16"), page_table=gpu(1, 8, dtype="int32"),
+             row_offsets=gpu(2, dtype="int32"), lens=gpu(1, dtype="int32"), out=gpu(4, 8, 64, dtype="bfloat16"), q_row=512,
+             out_row=512, page_stride=2048, slot_stride=128, head_stride=64, table_row=8, rows=4, count=1, q_heads=8,
+             kv_heads=2, head_dim=64, pages=8, page_size=16, max_len=100, max_new=4, window=0, sinks=0, scale=0.125)
+    a.update(kw)
+    return w.AttendArgs(**a)
+
+
+def moe_tensors(**kw):
+    bf = lambda *s: gpu(*s, dtype="bfloat16")  # noqa: E731
+    a = dict(x=bf(2, 256), residual=bf(2, 256), y=bf(2, 256), router=bf(4, 256),
+             gate_up=gpu(4, w.w4g128_packed_bytes(256, 256), dtype="uint8"),
+             down=gpu(4, w.w4g128_packed_bytes(128, 256), dtype="uint8"), M=2, D=256, F=128, E=4, top_k=2, renormalize=1)
+    a.update(kw)
+    return w.MoEArgs(**a)
+
+
+def test_tensors_of_other_layouts_are_refused():
+    """A field without a stride wants a contiguous tensor, one with strides neighbouring elements of a row."""
+    pytest.importorskip("torch")
+    sample_tensors(), attend_tensors(), moe_tensors()  # as they should be
+    sample_tensors(logits=view(gpu(4, 200, dtype="bfloat16"), lambda t: t[:, :100]), row_stride=200)
+    attend_tensors(k_cache=view(gpu(8, 2, 16, 64, dtype="bfloat16"), lambda t: t.transpose(1, 2)), slot_stride=64,
+                   head_stride=1024)
+    attend_tensors(page_table=view(gpu(1, 9, dtype="int32"), lambda t: t[:, :8]), table_row=9)
+    sample_tensors(temperature=view(gpu(9), lambda t: t[3:7]))
+    every_other = lambda *s, dtype="float32": view(gpu(*s, 2, dtype=dtype), lambda t: t[..., 0])  # noqa: E731
+    for make, bad in ((sample_tensors, dict(u=every_other(4))),
+                      (sample_tensors, dict(temperature=every_other(4))),
+                      (sample_tensors, dict(top_k=every_other(4, dtype="int32"))),
+                      (sample_tensors, dict(tokens=every_other(4, dtype="int32"))),
+                      (sample_tensors, dict(logprobs=every_other(4))),
+                      (sample_tensors, dict(logits=view(gpu(100, 4, dtype="bfloat16"), lambda t: t.t()))),
+                      (attend_tensors, dict(q=every_other(4, 8, 64, dtype="bfloat16"))),
+                      (attend_tensors, dict(out=every_other(4, 8, 64, dtype="bfloat16"))),
+                      (attend_tensors, dict(k_cache=view(gpu(8, 16, 64, 2, dtype="bfloat16"), lambda t: t.transpose(2, 3)))),
+                      (attend_tensors, dict(page_table=every_other(1, 8, dtype="int32"))),
+                      (attend_tensors, dict(row_offsets=every_other(2, dtype="int32"))),
+                      (moe_tensors, dict(x=view(gpu(256, 2, dtype="bfloat16"), lambda t: t.t()))),
+                      (moe_tensors, dict(x=view(gpu(2, 512, dtype="bfloat16"), lambda t: t[:, :256]))),
+                      (moe_tensors, dict(y=view(gpu(2, 512, dtype="bfloat16"), lambda t: t[:, :256]))),
+                      (moe_tensors, dict(router=view(gpu(256, 4, dtype="bfloat16"), lambda t: t.t())))):
+        with pytest.raises(w.W4G128Error) as ei:
+            make(**bad)
+        assert ei.value.status == E_INVALID, bad
