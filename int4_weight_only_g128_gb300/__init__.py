@@ -358,8 +358,9 @@ class _Args(ctypes.Structure):
     keywords.  A tensor becomes its device pointer (the struct keeps the tensor
     alive); it has to be on a GPU, of the element size that the field holds,
     contiguous (where the struct has strides for it: in its last dimension), and
-    reach at least as far as the sizes say (W4G128_ERR_INVALID_ARG).  Plain
-    integers are raw pointers and are not checked."""
+    reach at least as far as the sizes say, and all tensors on one
+    (W4G128_ERR_INVALID_ARG).  Plain integers are raw pointers and are not
+    checked."""
 
     _fn = ""
     _itemsize = {}  # tensor field: bytes of an element
@@ -372,9 +373,14 @@ class _Args(ctypes.Structure):
                 raise TypeError(f"{type(self).__name__} has no field {name!r}")
         super().__init__(**{k: (_ptr(v) if k in self._itemsize else v) for k, v in fields.items()})
         self._keep = {k: v for k, v in fields.items() if k in self._itemsize and hasattr(v, "data_ptr")}
+        self._device = None  # the tensors' GPU
         for name, t in self._keep.items():
             size = self._itemsize[name]
             if not t.is_cuda or (size and t.element_size() != size):
+                raise W4G128Error(f"{self._fn} ({name})", 1)
+            if self._device is None:
+                self._device = t.device.index
+            if t.device.index != self._device:
                 raise W4G128Error(f"{self._fn} ({name})", 1)
             rows_whole = t.dim() == 0 or t.shape[-1] <= 1 or t.stride(-1) == 1
             if not (rows_whole if name in self._strided else t.is_contiguous()):
@@ -390,6 +396,19 @@ class _Args(ctypes.Structure):
         return 0
 
 
+def _check_device(fn, args, ws=None):
+    """The kernels run on the current device: the call's tensors and its workspace have to be there."""
+    on = [] if args._device is None else [("arguments", args._device)]
+    if hasattr(ws, "data_ptr"):
+        on.append(("ws", ws.device.index if ws.is_cuda else None))
+    if on:
+        import torch
+        current = torch.cuda.current_device()
+        for what, device in on:
+            if device != current:
+                raise W4G128Error(f"{fn} ({what} on another device)", 1)
+
+
 class _Step:
     """An operator call whose arguments are marshalled once, like DecodeStep:
     the struct, the workspace and the stream are fixed, `run` is one C call."""
@@ -397,6 +416,7 @@ class _Step:
     _entry = ""
 
     def __init__(self, args, ws=None, stream=None):
+        _check_device(self._entry, args, ws)
         self._keep = (args, ws)  # the buffers outlive the step
         self._args = ctypes.byref(args)
         self._fn = getattr(lib(), self._entry)
@@ -429,6 +449,7 @@ class SampleArgs(_Args):
 
 def w4g128_sample(args, stream=None):
     """One token per row (see include/w4g128_ops.h); args: SampleArgs."""
+    _check_device("w4g128_sample", args)
     _check("w4g128_sample", lib().w4g128_sample(ctypes.byref(args), _stream(stream)))
 
 
@@ -473,6 +494,7 @@ def w4g128_attend_workspace_bytes(args):
 def w4g128_attend(args, ws, ws_bytes=None, stream=None):
     """Attention of each sequence's new tokens over its pages (see include/w4g128_ops.h); args: AttendArgs."""
     wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check_device("w4g128_attend", args, ws)
     _check("w4g128_attend", lib().w4g128_attend(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
 
 
@@ -506,6 +528,7 @@ def w4g128_moe_workspace_bytes(args):
 def w4g128_moe(args, ws, ws_bytes=None, stream=None):
     """The mixture-of-experts layer (see include/w4g128_ops.h); args: MoEArgs."""
     wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check_device("w4g128_moe", args, ws)
     _check("w4g128_moe", lib().w4g128_moe(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
 
 

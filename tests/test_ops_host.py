@@ -208,6 +208,10 @@ def test_attend_refuses_a_scale_that_overflows_with_log2_e(L):
         assert w.w4g128_attend_workspace_bytes(attend_args(scale=scale)) > 0, scale
 
 
+def sample_args(**kw):
+    return w.SampleArgs(**{**dict(logits=FAKE, row_stride=100, u=FAKE, tokens=FAKE, rows=1, vocab=100), **kw})
+
+
 class OnGpu:
     """A CPU tensor that says it is on a GPU, for the binding's checks."""
     is_cuda = True
@@ -284,3 +288,40 @@ def test_tensors_of_other_layouts_are_refused():
         with pytest.raises(w.W4G128Error) as ei:
             make(**bad)
         assert ei.value.status == E_INVALID, bad
+
+
+def test_tensors_and_workspaces_of_other_devices_are_refused(monkeypatch):
+    """Tensors share a device, the current one when the call is made or marshalled; a workspace is on it, too."""
+    torch = pytest.importorskip("torch")
+    with pytest.raises(w.W4G128Error) as ei:
+        sample_tensors(u=gpu(4, index=1))
+    assert ei.value.status == E_INVALID
+    elsewhere = [attend_tensors()] * 2 + [moe_tensors()] * 2 + [sample_tensors()] * 2
+    called, strings = [], w.lib().w4g128_status_string
+
+    class Entry:
+        w4g128_status_string = staticmethod(strings)
+
+        def __getattr__(self, name):
+            return lambda *a: called.append(name) or 0
+
+    monkeypatch.setattr(w, "lib", Entry)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    ws = [gpu(64, dtype="uint8", index=i) for i in (0, 1)]
+    on_cpu = torch.zeros(64, dtype=torch.uint8)
+    calls = [lambda args, ws: w.w4g128_attend(args, ws, stream=0), lambda args, ws: w.AttendStep(args, ws, stream=0).run(),
+             lambda args, ws: w.w4g128_moe(args, ws, stream=0), lambda args, ws: w.MoEStep(args, ws, stream=0).run(),
+             lambda args, ws: w.w4g128_sample(args, stream=0), lambda args, ws: w.SampleStep(args, stream=0).run()]
+    there = {t: gpu(*s, dtype="bfloat16", index=1) for t, s in (("x", (2, 256)), ("q", (4, 8, 64)), ("logits", (4, 100)))}
+    raw = [attend_args(q=there["q"])] * 2 + [moe_args(x=there["x"])] * 2 + [sample_args(logits=there["logits"])] * 2
+    for call, good, bad in zip(calls, raw, elsewhere):
+        call(good, ws[1])
+        assert len(called) == 1
+        wrong = [(bad, ws[1])]
+        if good is not raw[-1]:  # (sampling has no workspace)
+            wrong += [(good, ws[0]), (good, on_cpu)]
+        for args, space in wrong:
+            with pytest.raises(w.W4G128Error):
+                call(args, space)
+        assert len(called) == 1
+        called.clear()
