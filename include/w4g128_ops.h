@@ -84,8 +84,11 @@ W4G128_API int w4g128_sample(const w4g128_sample_args* args, void* stream);
  * call itself reads them from k_new and v_new, not from the cache.
  *
  * A row at a negative position (more rows than the length) sees nothing: its
- * out is 0 and its key and value are not written.  Rows of no sequence are
- * left as they are.  Pages that no row of a sequence sees are not read, and
+ * out is 0 and its key and value are not written.  So is the out of a row all of
+ * whose scores are -inf.  Rows of no sequence are left as they are.  The places
+ * of the new rows differ from one another and from every other position's that
+ * the call sees: sequences may share the pages of a common prefix, not a page
+ * that one of them extends.  Pages that no row of a sequence sees are not read, and
  * their table entries may hold anything.  Masked positions take no part in a
  * row's result whatever they hold, infinities and NaN included.
  *
@@ -116,7 +119,8 @@ typedef struct {
   int head_dim;  /* 64, 128 or 256 */
   int pages;     /* pages of the cache */
   int page_size; /* a multiple of 16 */
-  int max_len;   /* the longest length that the table can hold, 1 .. 2^24: sizes the split and the workspace */
+  int max_len;   /* the longest length that the table can hold, 1 .. 2^24.  Sizes the split and the workspace: far above
+                    the lengths it costs time (one token at 4096, 8 heads of 128: 6.9 us at 4096, 26 us at 131072) */
   int max_new;   /* most new rows of a sequence, 1 .. 16 */
   int window;    /* 0: none */
   int sinks;     /* first positions that stay visible behind the window; 0 without a window */
@@ -134,8 +138,9 @@ W4G128_API size_t w4g128_attend_workspace_bytes(const w4g128_attend_args* args);
  * must overlap nothing else.  lens, row_offsets and the table are read on the
  * device, so a captured call follows them from replay to replay.  A sequence
  * whose length or row range lies outside the bounds above is left out, and a
- * page id outside 0 .. pages - 1 counts as a page that no row sees and takes
- * no new rows; both leave W4G128_ERR_CACHE in the workspace's status word
+ * page id outside 0 .. pages - 1 counts as a page whose cached positions no row
+ * sees and takes no new rows (they are seen from k_new and v_new); both leave
+ * W4G128_ERR_CACHE in the workspace's status word, until the next call on it
  * (w4g128_workspace_status).  Returns W4G128_ERR_INVALID_ARG,
  * W4G128_ERR_SHAPE, W4G128_ERR_ALIGN or W4G128_ERR_WORKSPACE for what breaks
  * the bounds above. */
@@ -156,8 +161,12 @@ W4G128_API int w4g128_attend(const w4g128_attend_args* args, void* ws, size_t ws
  * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)).  The
  * activations a are the operand of the second product and rounded for it (to
  * fp16, scaled by the largest of 16 neighbours and then of the row and expert): r
- * errs by at most 2^-11 of a and 2^-38 of the row's and expert's largest.  Only
- * the experts that some row picks are read, each once.
+ * errs by at most 2^-11 of a and 2^-38 of the row's and expert's largest.  x
+ * enters the first product exactly down to 2^-31 of its row's largest; smaller
+ * values err by at most 2^-39 of that.  An infinity in a row's x or activations
+ * makes the row NaN.  Only the experts that some row picks are read: once, and a
+ * second time, from the L2 where it still holds them, if more than 8 rows pick
+ * one.
  *
  * gate_up_e is a K = D, N = 2 F matrix (F gate columns, then F up columns),
  * down_e a K = F, N = D one, each packed as w4g128_pack writes it; the E

@@ -85,8 +85,9 @@ def lib():
 
 def lib_debug():
     """Load libw4g128_debug.so, the range-checked build of the same sources
-    (W4G128_DEBUG: every global access derived from the schedule is checked,
-    a failure recorded as W4G128_ERR_INTERNAL in the status word); for tests.
+    (W4G128_DEBUG: every global access of the weight stream derived from the
+    schedule is checked, a failure recorded as W4G128_ERR_INTERNAL in the status
+    word); for tests.
     Call its functions directly (the wrappers below use lib())."""
     global _lib_debug
     if _lib_debug is not None:

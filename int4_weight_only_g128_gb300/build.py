@@ -12,9 +12,11 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libw4g128.so")
-# The same sources with -DW4G128_DEBUG: every global access the kernels derive
-# from the schedule is range-checked, a failed check is recorded in the status
-# word and the access skipped (for tests; slower, never used by the product).
+# The same sources with -DW4G128_DEBUG: every global access the weight stream's
+# kernels derive from the schedule is range-checked, a failed check is recorded in
+# the status word and the access skipped (for tests; slower, never used by the
+# product).  The kernels of include/w4g128_ops.h have no such checks: theirs are
+# part of the product (lengths, row ranges and page ids that come from the device).
 DEBUG_BUILD = os.path.join(BUILD, "debug")
 LIB_DEBUG = os.path.join(BUILD, "libw4g128_debug.so")
 

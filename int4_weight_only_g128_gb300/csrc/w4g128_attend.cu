@@ -24,11 +24,14 @@
 // heads (134 MB): 29.4 us a call, 67% of the measured copy rate; the tile loop
 // streams at 6.7 TB/s, the rest is each CTA's start (length, table: 2.4 us), the
 // join of its groups (1.5 us) and the second kernel (4 us).  With 64 rows the
-// tile loop's latency binds: 1.9 instructions a clock, the tensor pipe 38% and
-// shared memory 60% busy (two of window 4096, 4 heads of 256, 16 new tokens:
-// 22.7 us against 7.9 us of MMA).  Not kept there: two row tiles a warp
-// at 255 registers (8 long 34.9 us, 30.5 without), two position tiles a turn of
-// the loop (22.8 and 22.7: the same).
+// tile loop's latency binds: two of window 4096, 4 heads of 256, 16 new tokens
+// take 22.6 us against 5.1 us of bytes and 1.1 us of operations at the measured
+// bf16 rate; under ncu an active SM issues 1.5 instructions a clock, its tensor
+// pipe is busy 22% and its shared memory 60% of the time.  Warp MMAs fed by
+// ldmatrix go no faster; tcgen05 with the rows as one tile of 64 or 128 would,
+// and is not built.  Not kept there: two row tiles a warp at 255 registers
+// (8 long 34.9 us, 30.5 without), two position tiles a turn of the loop (22.8
+// and 22.7: the same).
 // Positions masked for some row hold arbitrary bits, and 0 x NaN is NaN: tiles
 // at a mask's edge are searched for non-finite values, which are then applied
 // to the rows that see them one by one.
@@ -54,8 +57,8 @@ constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
 // A row's reference follows its maximum only when that is above it by more than
 // this (base 2): weights up to 2^8 cost no precision, and most tiles neither
-// exchange their maxima nor rescale the sums (per call, 16 new tokens on 64 heads
-// at 32771: 98.6 -> 89.4 us; 16 ragged sequences 21.3 -> 19.3).
+// exchange their maxima nor rescale the sums (per call, 16 new tokens of 64 heads
+// on 8 at 32771, 128 rows a head: 98.6 -> 89.4 us; 16 ragged sequences 21.3 -> 19.3).
 constexpr float kSlack = 8.f;
 constexpr uint32_t kOnes = 0x3F803F80u;  // bf16 1.0 twice
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -734,16 +737,31 @@ __global__ void __launch_bounds__(W * 32) join_kernel(const __grid_constant__ Pa
 // x heads x sequences) into a few chunks for each SM.  One sequence: 304, as
 // many CTAs of 32 rows as the GPU holds at once.  A batch: 608, as its sequences
 // have lengths of their own, half of max_len on average, and 684 for 16 or more
-// sequences, whose CTAs even out.  A window: 304, and 152 for heads of 256, whose
-// CTAs of 64 rows fill an SM.  Not less than 128 past 2048 positions: the second
-// kernel takes 32 chunks at once.  Measured, us per call: one sequence of 32771,
-// 8 heads of 128, 32 rows: 30.6 at 304, 38.5 at 456 (a second wave).  Eight of up
-// to 6000, 8 heads of 128, 24 rows: 24.2 at 608, 28.1 at 684, 26.2 at 456.  16 of
-// up to 9001, 4 heads of 64: 18 rows 18.1 at 684, 18.4 at 608, 19.8 at 760; 6
-// rows 13.6, 14.6 and 13.5.  Windows of 4096: two, 4 heads of 256, 64 rows: 23.5
-// at 152, 30.9 at 304; eight, 8 heads of 128, 4 rows: 35.6 and 29.9.  Chunks of
-// 128 for 64: 4 of 4099, 2 heads of 256: 12.4 for 17.5; one of 2049, 8 heads of
-// 128: 6.9 for 7.7; but one of 611: 7.4 for 6.6.
+// sequences, whose CTAs even out.  A window: 304, and 152 for heads of 256.  Not
+// less than 128 past 2048 positions: the second kernel takes 32 chunks at once.
+// Measured, us per call.  One sequence of 32771, 8 heads of 128, 32 rows: 30.6 at
+// 304, 38.5 at 456 (a second wave).
+// Batches of lengths up to L, at 608 and 684 (heads x width, rows a head):
+//   4 of 9001, 4 x 64, 18: 8.6 and 11.0;  8 of 6000, 8 x 128, 24: 24.2 and 28.1;
+//   8 of 6000, 8 x 128, 4 and 12: 16.4 and 15.3, 19.6 and 19.2;
+//   12 of 9001, 4 x 64, 6 and 18: 11.3 and 10.2, 15.5 and 15.3;
+//   16 and 32 of 9001, 4 x 64, 18: 18.2 and 18.0, 29.6 and 29.3;
+//   16, 24, 32 of 6000, 8 x 128, 4: 26.5 and 25.4, 37.4 and 34.5, 42.3 and 42.4;
+//   16, 32, 64 of 4000, 2 x 256, 24: 20.6 and 21.5, 30.8 and 29.2, 53.6 and 49.6;
+//   32 of 3000, 4 x 128, 24: 23.7 and 24.4;  64 of 20000, 1 x 128, 8: 39.8 and 38.3.
+// So 684 loses up to a third below 16 sequences and up to 4% from there on, and
+// gains up to 8%; 304 is slower than both by up to a half.
+// Windows of 4096 at 152 and 304, heads of 256:
+//   64 rows, 2 x 4 and 1 x 8 heads (one wave of CTAs): 22.6 and 29.1;
+//   64 rows, 8 x 2 and 8 x 4: 46.9 and 42.2, 89.7 and 75.9;
+//   4 rows, 2 x 4 and 8 x 2: 13.0 and 11.8, 23.2 and 19.0;
+// of 128: 64 rows, 1 x 8: 12.7 and 18.2;  4 rows, 2 x 8, 8 x 2 and 8 x 8: 12.4 and
+// 10.3, 13.3 and 10.7, 35.0 and 28.7.  A rule by rows and waves would serve both;
+// this one goes by the width alone.
+// Chunks of 128 for 64: 4 of 4099, 2 heads of 256: 12.4 for 17.5; one of 2049, 8
+// heads of 128: 6.9 for 7.7; but one of 611: 7.4 for 6.6.  max_len far above the
+// lengths makes few chunks: one token at 4096, 8 heads of 128: 6.9 with 4096, 26.2
+// with 131072.
 int chunk_for(const w4g128_attend_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 16);

@@ -26,7 +26,7 @@
 // 1024 + 16 q, both from one word with one shift and four LOP3 (bf16 takes two
 // shifts more: 48.4 against 46.6 us, the down projection of 16 rows of 5120).
 //   gate and up: x is bf16; values down to 2^-31 of the row's largest are
-//     exact, smaller ones off by at most 2^-40 of it;
+//     exact, smaller ones off by at most 2^-39 of it;
 //   down: an activation is rounded to fp16 where it is computed, scaled by its
 //     16-column tile's largest, since the row's is not known yet (2^-11
 //     relative, an eighth of bf16's rounding); the tile's exponent goes along,
@@ -45,10 +45,10 @@
 // 8 warps hold one part each or 4 warps two each: bits do not depend on the
 // grid, nor on which other rows share the expert.
 //
-// Measured: 16 rows, 5120 x 1408, 6 of 96 experts (712 MB): 132 us a call, 80% of
+// Measured: 16 rows, 5120 x 1408, 6 of 96 experts (712 MB): 129 us a call, 82% of
 // the measured copy rate; gate and up 72 us (6.1 TB/s), down 47 us (4.7 TB/s:
 // units of 11 groups, a barrier of the team and a fold for every 2.75 items of a
-// warp).  One row, 8 of 64 experts (93 MB): 34.6 us: routing 5.0, lists and first
+// warp).  One row, 8 of 64 experts (93 MB): 34.8 us: routing 5.0, lists and first
 // copies 2.6, gate and up 12, the change of kernels 2, down 7.5, adding up 2, the
 // rest launches: what is left above the 13.7 us of bytes is latency.
 #include <cuda_bf16.h>
@@ -80,7 +80,11 @@ constexpr int kLeastHalf = 24;           // fp16 has no power of two below 2^-24
 // Picked experts in rising order with the picks (row * top_k + place, places in
 // rising expert order) that each serves: one entry for up to 8 rows, what an
 // MMA has B columns for.  An expert of more rows has two entries; its weights
-// are then dequantised twice, and read twice, side by side, from the L2.
+// are then dequantised twice and read twice, one entry's units after the other's:
+// the second time from the L2, as far as that still holds them.  16 rows that
+// all pick 8 experts, 4096 x 14336 (94 MB each): 5% more DRAM bytes than once in
+// gate and up, 11% in down, 266 us a call against 142 with 8 rows; 4096 x 4096:
+// no more bytes, 89 us against 56.
 struct alignas(16) Lists {
   int entries;
   uint16_t expert[kMaxPicks];

@@ -25,10 +25,10 @@
 //
 // Bound: latency.  A row of 248320 logits is 0.5 MB, 0.1 us of HBM; the chain
 // load, count, merge, scan and five or six cluster barriers is what takes time.
-// Measured, one row of 248320 with top-p (16 CTAs), 15.4 us a call: launch and
+// Measured, one row of 248320 with top-p (16 CTAs), 15.1 us a call: launch and
 // clearing 1.4, counting 2.6, marks and largest 1.3, the run 1.6, merge and
 // weights 1.5, scan 1.7, top-p 1.2, draw 1.4, search 2.0.  16 rows (6 CTAs each):
-// 20.9 us, of which counting 6.4 (shared-memory atomics, 8 cycles a warp).
+// 20.8 us, of which counting 6.4 (shared-memory atomics, 8 cycles a warp).
 #include <cuda_runtime.h>
 
 #include <cstdint>
