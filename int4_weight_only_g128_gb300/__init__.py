@@ -366,6 +366,7 @@ class _Args(ctypes.Structure):
     _fn = ""
     _itemsize = {}  # tensor field: bytes of an element
     _strided = ()   # tensor fields that the struct has strides for
+    _device = None  # the tensors' GPU
 
     def __init__(self, **fields):
         known = {f[0] for f in self._fields_}
@@ -374,7 +375,6 @@ class _Args(ctypes.Structure):
                 raise TypeError(f"{type(self).__name__} has no field {name!r}")
         super().__init__(**{k: (_ptr(v) if k in self._itemsize else v) for k, v in fields.items()})
         self._keep = {k: v for k, v in fields.items() if k in self._itemsize and hasattr(v, "data_ptr")}
-        self._device = None  # the tensors' GPU
         for name, t in self._keep.items():
             size = self._itemsize[name]
             if not t.is_cuda or (size and t.element_size() != size):

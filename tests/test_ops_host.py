@@ -325,3 +325,13 @@ def test_tensors_and_workspaces_of_other_devices_are_refused(monkeypatch):
                 call(args, space)
         assert len(called) == 1
         called.clear()
+
+
+def test_structs_copied_from_bytes_are_taken():
+    """ctypes makes them without the constructor, from raw pointers."""
+    for args, call in ((sample_args(vocab=0), lambda a: w.w4g128_sample(a, stream=0)),
+                       (attend_args(head_dim=96), lambda a: w.w4g128_attend(a, FAKE, 1 << 40, stream=0)),
+                       (moe_args(D=192), lambda a: w.w4g128_moe(a, FAKE, 1 << 40, stream=0))):
+        with pytest.raises(w.W4G128Error) as ei:
+            call(type(args).from_buffer_copy(bytes(args)))
+        assert ei.value.status == E_SHAPE
