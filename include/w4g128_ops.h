@@ -158,7 +158,8 @@ W4G128_API int w4g128_attend(const w4g128_attend_args* args, void* ws, size_t ws
  *                 (renormalize = 1) or over all experts (renormalize = 0)
  *   a[m][e][f]  = r( silu(g_f) u_f ), (g, u) = x[m] . dequant(gate_up_e)
  *   y[m][n]     = bf16( residual[m][n] + sum_{e in S(m)} p[m][e] (a[m][e] . dequant(down_e))[n] )
- * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)).  The
+ * with fp32 products, sums and softmax, silu(g) = g / (1 + exp(-g)); the codes
+ * enter the sums with a bias of 1024, which every group's own sum undoes.  The
  * activations a are the operand of the second product and rounded for it (to
  * fp16, scaled by the largest of 16 neighbours and then of the row and expert): r
  * errs by at most 2^-11 of a and 2^-38 of the row's and expert's largest.  x
