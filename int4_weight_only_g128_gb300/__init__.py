@@ -20,6 +20,9 @@ __all__ = [
     "w4g128_schedule", "DecodeStep",
     "w4g128_sample", "SampleArgs", "SampleStep", "MAX_SAMPLE_ROWS", "MAX_VOCAB",
     "w4g128_attend", "w4g128_attend_workspace_bytes", "AttendArgs", "AttendStep", "MAX_SEQUENCES", "ERR_CACHE",
+    "w4g128_append", "w4g128_append_workspace_bytes", "AppendArgs", "AppendStep",
+    "w4g128_attend8", "w4g128_attend8_workspace_bytes", "Attend8Args", "Attend8Step",
+    "w4g128_penalize", "PenalizeArgs", "PenalizeStep",
     "w4g128_moe", "w4g128_moe_workspace_bytes", "MoEArgs", "MoEStep", "MAX_EXPERTS", "MAX_TOP_K",
     "MAX_M", "MAX_MATRICES", "SELFTEST_WS_BYTES", "SCHEDULE_FIELDS",
 ]
@@ -151,6 +154,16 @@ def _declare(L):
     L.w4g128_attend_workspace_bytes.argtypes = [ctypes.POINTER(AttendArgs)]
     L.w4g128_attend.restype = i
     L.w4g128_attend.argtypes = [ctypes.POINTER(AttendArgs), p, sz, p]
+    L.w4g128_append_workspace_bytes.restype = sz
+    L.w4g128_append_workspace_bytes.argtypes = [ctypes.POINTER(AppendArgs)]
+    L.w4g128_append.restype = i
+    L.w4g128_append.argtypes = [ctypes.POINTER(AppendArgs), p, sz, p]
+    L.w4g128_attend8_workspace_bytes.restype = sz
+    L.w4g128_attend8_workspace_bytes.argtypes = [ctypes.POINTER(Attend8Args)]
+    L.w4g128_attend8.restype = i
+    L.w4g128_attend8.argtypes = [ctypes.POINTER(Attend8Args), p, sz, p]
+    L.w4g128_penalize.restype = i
+    L.w4g128_penalize.argtypes = [ctypes.POINTER(PenalizeArgs), p]
     L.w4g128_moe_workspace_bytes.restype = sz
     L.w4g128_moe_workspace_bytes.argtypes = [ctypes.POINTER(MoEArgs)]
     L.w4g128_moe.restype = i
@@ -503,6 +516,144 @@ class AttendStep(_Step):
     """w4g128_attend with its arguments marshalled once: AttendStep(args, ws).run()."""
 
     _entry = "w4g128_attend"
+
+
+def _cache_reach(a, name):
+    """Elements of the fields that the operators on a paged cache share."""
+    if name in ("k_cache", "v_cache"):
+        return (a.pages - 1) * a.page_stride + (a.page_size - 1) * a.slot_stride + \
+            (a.kv_heads - 1) * a.head_stride + a.head_dim
+    if name in ("k_scale", "v_scale"):
+        return (a.pages - 1) * a.scale_page + (a.kv_heads - 1) * a.scale_head + a.page_size // max(a.block, 1)
+    if name == "page_table":
+        return (a.count - 1) * a.table_row + (a.max_len - 1) // max(a.page_size, 1) + 1
+    return a.count + 1 if name == "row_offsets" else a.count
+
+
+class AppendArgs(_Args):
+    """w4g128_append_args: bf16 q and q_out (or None), k_new, v_new; k_cache and
+    v_cache bf16 (block 0, k_scale and v_scale None) or 8-bit with float32 scales;
+    float64 freqs (or None); int32 page_table, row_offsets, lens; strides in
+    elements."""
+
+    _fn = "w4g128_append"
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "q_out", "k_new", "v_new", "k_cache", "v_cache", "k_scale",
+                                               "v_scale", "freqs", "page_table", "row_offsets", "lens")] + \
+               [(n, ctypes.c_longlong) for n in ("q_row", "q_out_row", "kv_row", "page_stride", "slot_stride",
+                                                 "head_stride", "scale_page", "scale_head", "table_row")] + \
+               [(n, ctypes.c_int) for n in ("rows", "count", "q_heads", "kv_heads", "head_dim", "rot_dim",
+                                            "interleaved", "pages", "page_size", "block", "max_len", "max_new")]
+    _itemsize = {"q": 2, "q_out": 2, "k_new": 2, "v_new": 2, "k_cache": 2, "v_cache": 2, "k_scale": 4, "v_scale": 4,
+                 "freqs": 8, "page_table": 4, "row_offsets": 4, "lens": 4}
+    _strided = ("q", "q_out", "k_new", "v_new", "k_cache", "v_cache", "k_scale", "v_scale", "page_table")
+
+    def __init__(self, **fields):
+        if fields.get("block"):
+            self._itemsize = {**type(self)._itemsize, "k_cache": 1, "v_cache": 1}
+        super().__init__(**fields)
+
+    def _reach(self, name):
+        if name in ("q", "q_out"):
+            return (self.rows - 1) * (self.q_row if name == "q" else self.q_out_row) + self.q_heads * self.head_dim
+        if name in ("k_new", "v_new"):
+            return (self.rows - 1) * self.kv_row + self.kv_heads * self.head_dim
+        return self.rot_dim // 2 if name == "freqs" else _cache_reach(self, name)
+
+
+def w4g128_append_workspace_bytes(args):
+    return int(lib().w4g128_append_workspace_bytes(ctypes.byref(args)))
+
+
+def w4g128_append(args, ws, ws_bytes=None, stream=None):
+    """Rotated queries, and rotated keys and values put into their pages (see include/w4g128_ops.h); args: AppendArgs."""
+    wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check_device("w4g128_append", args, ws)
+    _check("w4g128_append", lib().w4g128_append(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
+
+
+class AppendStep(_Step):
+    """w4g128_append with its arguments marshalled once: AppendStep(args, ws).run()."""
+
+    _entry = "w4g128_append"
+
+
+class Attend8Args(_Args):
+    """w4g128_attend8_args: bf16 q and out, 8-bit k_cache and v_cache with float32
+    k_scale and v_scale, int32 page_table, row_offsets, lens; strides in elements."""
+
+    _fn = "w4g128_attend8"
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "k_scale", "v_scale", "page_table",
+                                               "row_offsets", "lens", "out")] + \
+               [(n, ctypes.c_longlong) for n in ("q_row", "out_row", "page_stride", "slot_stride", "head_stride",
+                                                 "scale_page", "scale_head", "table_row")] + \
+               [(n, ctypes.c_int) for n in ("rows", "count", "q_heads", "kv_heads", "head_dim", "pages", "page_size",
+                                            "block", "max_len", "max_new", "window", "sinks")] + [("scale", ctypes.c_float)]
+    _itemsize = {"q": 2, "k_cache": 1, "v_cache": 1, "k_scale": 4, "v_scale": 4, "page_table": 4, "row_offsets": 4,
+                 "lens": 4, "out": 2}
+    _strided = ("q", "k_cache", "v_cache", "k_scale", "v_scale", "page_table", "out")
+
+    def _reach(self, name):
+        if name in ("q", "out"):
+            return (self.rows - 1) * (self.q_row if name == "q" else self.out_row) + self.q_heads * self.head_dim
+        return _cache_reach(self, name)
+
+
+def w4g128_attend8_workspace_bytes(args):
+    return int(lib().w4g128_attend8_workspace_bytes(ctypes.byref(args)))
+
+
+def w4g128_attend8(args, ws, ws_bytes=None, stream=None):
+    """Attention of each sequence's new tokens over its 8-bit pages (see include/w4g128_ops.h); args: Attend8Args."""
+    wb = _nbytes(ws) if ws_bytes is None else ws_bytes
+    _check_device("w4g128_attend8", args, ws)
+    _check("w4g128_attend8", lib().w4g128_attend8(ctypes.byref(args), _ptr(ws), wb, _stream(stream)))
+
+
+class Attend8Step(_Step):
+    """w4g128_attend8 with its arguments marshalled once: Attend8Step(args, ws).run()."""
+
+    _entry = "w4g128_attend8"
+
+
+class PenalizeArgs(_Args):
+    """w4g128_penalize_args: bf16 logits and out (row r at r * its stride); int32
+    history, history_len, prompt_len, int64 history_start, float32 repetition,
+    presence, frequency; int32 bias_tokens and bias_offsets, float32 bias_values;
+    int32 mask words (row r at r * mask_row).  All but logits and out may be None."""
+
+    _fn = "w4g128_penalize"
+    _fields_ = [(n, ctypes.c_void_p) for n in ("logits", "out", "history", "history_start", "history_len", "prompt_len",
+                                               "repetition", "presence", "frequency", "bias_tokens", "bias_values",
+                                               "bias_offsets", "mask")] + \
+               [(n, ctypes.c_longlong) for n in ("row_stride", "out_stride", "mask_row", "history_size")] + \
+               [(n, ctypes.c_int) for n in ("bias_size", "rows", "vocab")]
+    _itemsize = {"logits": 2, "out": 2, "history": 4, "history_start": 8, "history_len": 4, "prompt_len": 4,
+                 "repetition": 4, "presence": 4, "frequency": 4, "bias_tokens": 4, "bias_values": 4, "bias_offsets": 4,
+                 "mask": 4}
+    _strided = ("logits", "out", "mask")
+
+    def _reach(self, name):
+        if name in ("logits", "out"):
+            return (self.rows - 1) * (self.row_stride if name == "logits" else self.out_stride) + self.vocab
+        if name == "mask":
+            return (self.rows - 1) * self.mask_row + (self.vocab + 31) // 32
+        if name in ("bias_tokens", "bias_values"):
+            return self.bias_size
+        if name == "history":
+            return self.history_size
+        return self.rows + 1 if name == "bias_offsets" else self.rows
+
+
+def w4g128_penalize(args, stream=None):
+    """Penalties, biases and masks on logits (see include/w4g128_ops.h); args: PenalizeArgs."""
+    _check_device("w4g128_penalize", args)
+    _check("w4g128_penalize", lib().w4g128_penalize(ctypes.byref(args), _stream(stream)))
+
+
+class PenalizeStep(_Step):
+    """w4g128_penalize with its arguments marshalled once: PenalizeStep(args).run()."""
+
+    _entry = "w4g128_penalize"
 
 
 class MoEArgs(_Args):

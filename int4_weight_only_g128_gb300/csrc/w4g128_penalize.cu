@@ -1,0 +1,284 @@
+// Penalties, biases and masks on logits (w4g128_penalize), in one launch.
+//
+// A row is a cluster of CTAs, each with a slice of the vocabulary and, in shared
+// memory, a word for each token of it: the times it occurs in the answer, and in
+// the top bit whether it occurs at all.  The history is read once, each CTA its
+// part, and counted where a token belongs by additions to the other CTA's shared
+// memory; whole numbers, so their order does not matter.  In the same way a list's
+// biases leave their places in the list, of which the largest stays.  Then each
+// CTA goes over its slice, 8 tokens a thread at a time; the logits and mask words
+// are on their way while the tokens are counted.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "w4g128_internal.h"
+#include "w4g128_ops.h"
+#include "w4g128_ptx.cuh"
+
+namespace w4g128 {
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kAhead = 4;  // pieces of 8 logits that a thread asks for ahead
+constexpr int kMostBias = 65535;
+constexpr uint32_t kSeen = 0x80000000u;
+constexpr int kMostCtas = 16;
+
+struct Params {
+  const uint16_t* logits;
+  uint16_t* out;
+  const int* history;
+  const long long* history_start;
+  const int *history_len, *prompt_len;
+  const float *repetition, *presence, *frequency;
+  const int* bias_tokens;
+  const float* bias_values;
+  const int* bias_offsets;
+  const uint32_t* mask;
+  long long row_stride, out_stride, mask_row, history_size;
+  int bias_size, vocab, slice;  // slice: tokens a CTA, a multiple of 8
+};
+
+__device__ __forceinline__ void cluster_add(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void cluster_or(uint32_t a, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ float bf16_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ uint32_t f_bf16(float x) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) uint32_t s_words[];  // [slice] counts, if any; [slice] 16-bit places in the list, if any
+  const int tid = threadIdx.x, row = blockIdx.y;
+  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  const bool may_count = p.history != nullptr, may_bias = p.bias_tokens != nullptr;
+  uint32_t* counts = s_words;
+  uint32_t* places = may_count ? s_words + p.slice : s_words;
+
+  if (may_count)
+    for (int i = tid * 4; i < p.slice; i += kThreads * 4) *reinterpret_cast<uint4*>(counts + i) = make_uint4(0u, 0u, 0u, 0u);
+  if (may_bias)
+    for (int i = tid * 4; i < p.slice / 2; i += kThreads * 4) *reinterpret_cast<uint4*>(places + i) = make_uint4(0u, 0u, 0u, 0u);
+  if (may_count) cluster_arrive_release();  // a CTA runs and its words are 0 before another counts there
+  grid_dependency_wait();
+
+  // Pieces of 8 tokens start where the row's logits are 16-byte aligned.
+  const uint16_t* in = p.logits + row * p.row_stride;
+  uint16_t* out = p.out + row * p.out_stride;
+  const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(in) & 15u) / 2);  // piece 0 starts at token -shift
+  const bool out_whole = ((reinterpret_cast<uintptr_t>(out) & 15u) / 2) == static_cast<unsigned>(shift);
+  const int first = rank * p.slice - shift;  // this CTA's first token
+  const uint32_t* mask = p.mask != nullptr ? p.mask + row * p.mask_row : nullptr;
+  const int words = (p.vocab + 31) / 32;
+  uint4 ahead[kAhead];
+  uint32_t allowed_ahead[kAhead];
+  auto load = [&](int t0, uint4& v, uint32_t& allowed) {
+    v = make_uint4(0u, 0u, 0u, 0u);
+    allowed = 0xFFu;
+    if (t0 >= 0 && t0 + 8 <= p.vocab) {
+      v = *reinterpret_cast<const uint4*>(in + t0);
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (t0 + e >= 0 && t0 + e < p.vocab) w[e / 2] |= static_cast<uint32_t>(in[t0 + e]) << (e & 1) * 16;
+      v = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    if (mask != nullptr) {  // the 8 bits from t0 on (of a token outside: any)
+      const int w0 = t0 >> 5;
+      const uint32_t lo = w0 >= 0 && w0 < words ? mask[w0] : 0u;
+      uint32_t hi = 0u;
+      if ((t0 & 31) > 24 && w0 + 1 < words) hi = mask[w0 + 1];
+      allowed = __funnelshift_r(lo, hi, t0 & 31) & 0xFFu;
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int at = (i * kThreads + tid) * 8;
+    if (at < p.slice && first + at < p.vocab) load(first + at, ahead[i], allowed_ahead[i]);
+  }
+
+  float repetition = 1.f, presence = 0.f, frequency = 0.f;
+  if (p.repetition != nullptr) repetition = p.repetition[row];
+  if (p.presence != nullptr) presence = p.presence[row];
+  if (p.frequency != nullptr) frequency = p.frequency[row];
+  if (may_count) {
+    long long begin = p.history_start != nullptr ? p.history_start[row] : 0;
+    long long len = max(p.history_len[row], 0);
+    long long prompt = p.prompt_len != nullptr ? p.prompt_len[row] : 0;
+    // (what lies outside the buffer is not read)
+    const long long skip = begin >= 0 ? 0 : begin < -len ? len : -begin;
+    begin += skip;
+    len = min(len - skip, max(p.history_size - begin, 0ll));
+    prompt -= skip;
+    cluster_wait_acquire();
+    const uint32_t base = smem_addr(counts);
+    for (long long i = rank * kThreads + tid; i < len; i += ctas * kThreads) {
+      const int t = p.history[begin + i];
+      if (t >= 0 && t < p.vocab) {
+        const int owner = (t + shift) / p.slice;
+        const uint32_t at = cluster_map(base + (t + shift - owner * p.slice) * 4, owner);
+        if (i < prompt) cluster_or(at, kSeen);
+        else cluster_add(at, 1u);
+      }
+    }
+    cluster_arrive_release();
+  }
+  int b0 = 0, listed = 0;
+  if (may_bias) {  // each CTA looks for its own tokens
+    __syncthreads();
+    b0 = max(p.bias_offsets[row], 0);
+    listed = min(max(min(p.bias_offsets[row + 1], p.bias_size) - b0, 0), kMostBias);
+    for (int i = tid; i < listed; i += kThreads) {
+      const int t = p.bias_tokens[b0 + i], at = t - first;
+      if (t >= 0 && t < p.vocab && at >= 0 && at < p.slice) {
+        uint32_t* word = places + at / 2;
+        const int up = (at & 1) * 16;
+        uint32_t seen = *word;
+        while (((seen >> up) & 0xFFFFu) < static_cast<uint32_t>(i + 1)) {
+          const uint32_t prev = atomicCAS(word, seen, (seen & ~(0xFFFFu << up)) | static_cast<uint32_t>(i + 1) << up);
+          if (prev == seen) break;
+          seen = prev;
+        }
+      }
+    }
+    __syncthreads();
+  }
+  if (may_count) cluster_wait_acquire();
+
+  auto finish = [&](int at, const uint4& v, uint32_t allowed) {
+    const int t0 = first + at;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t c[8] = {}, place[4] = {};
+    bool plain = allowed == 0xFFu;
+    if (may_count) {
+      const uint4 a = *reinterpret_cast<const uint4*>(counts + at), b = *reinterpret_cast<const uint4*>(counts + at + 4);
+      c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
+      c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
+      plain = plain && (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) == 0u;
+    }
+    if (may_bias) {
+      const uint4 a = *reinterpret_cast<const uint4*>(places + at / 2);
+      place[0] = a.x; place[1] = a.y; place[2] = a.z; place[3] = a.w;
+      plain = plain && (a.x | a.y | a.z | a.w) == 0u;
+    }
+    if (!plain) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int up = (e & 1) * 16;
+        const uint32_t where = (place[e / 2] >> up) & 0xFFFFu;
+        uint32_t bits = (w[e / 2] >> up) & 0xFFFFu;
+        if ((allowed >> e & 1u) == 0u) {
+          bits = 0xFF80u;  // -inf
+        } else if (c[e] != 0u || where != 0u) {
+          float z = bf16_f(bits);
+          if (c[e] != 0u) z = z > 0.f ? z / repetition : z * repetition;
+          const uint32_t times = c[e] & ~kSeen;
+          if (times != 0u) {
+            z = __fsub_rn(z, __fmul_rn(frequency, static_cast<float>(times)));
+            z = __fsub_rn(z, presence);
+          }
+          if (where != 0u) z = __fadd_rn(z, p.bias_values[b0 + static_cast<int>(where) - 1]);
+          bits = f_bf16(z);
+        }
+        w[e / 2] = (w[e / 2] & ~(0xFFFFu << up)) | bits << up;
+      }
+    }
+    if (out_whole && t0 >= 0 && t0 + 8 <= p.vocab) {
+      *reinterpret_cast<uint4*>(out + t0) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (t0 + e >= 0 && t0 + e < p.vocab) out[t0 + e] = static_cast<uint16_t>(w[e / 2] >> (e & 1) * 16);
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    const int at = (i * kThreads + tid) * 8;
+    if (at < p.slice && first + at < p.vocab) finish(at, ahead[i], allowed_ahead[i]);
+  }
+  for (int at = (kAhead * kThreads + tid) * 8; at < p.slice && first + at < p.vocab; at += kThreads * 8) {
+    uint4 v;
+    uint32_t allowed;
+    load(first + at, v, allowed);
+    finish(at, v, allowed);
+  }
+}
+
+int check(const w4g128_penalize_args* a) {
+  if (a == nullptr || a->logits == nullptr || a->out == nullptr) return W4G128_ERR_INVALID_ARG;
+  if ((a->history != nullptr && a->history_len == nullptr) ||
+      (a->bias_tokens != nullptr && (a->bias_values == nullptr || a->bias_offsets == nullptr)))
+    return W4G128_ERR_INVALID_ARG;
+  if (a->rows < 1 || a->rows > W4G128_MAX_SAMPLE_ROWS || a->history_size < 0 || a->bias_size < 0 ||
+      (a->out == a->logits && a->out_stride != a->row_stride))
+    return W4G128_ERR_INVALID_ARG;
+  if (a->vocab < 1 || a->vocab > W4G128_MAX_VOCAB || a->row_stride < a->vocab || a->out_stride < a->vocab ||
+      (a->mask != nullptr && a->mask_row != 0 && a->mask_row < (a->vocab + 31) / 32))
+    return W4G128_ERR_SHAPE;
+  auto off = [](const void* q, uintptr_t n) { return (reinterpret_cast<uintptr_t>(q) & (n - 1)) != 0; };
+  if (off(a->logits, 2) || off(a->out, 2) || off(a->history_start, 8)) return W4G128_ERR_ALIGN;
+  const void* words[] = {a->history, a->history_len, a->prompt_len, a->repetition, a->presence, a->frequency,
+                         a->bias_tokens, a->bias_values, a->bias_offsets, a->mask};
+  for (const void* q : words)
+    if (off(q, 4)) return W4G128_ERR_ALIGN;
+  return W4G128_OK;
+}
+
+}  // namespace
+}  // namespace w4g128
+
+extern "C" {
+
+int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
+  using namespace w4g128;
+  int rc = check(a);
+  if (rc != W4G128_OK) return rc;
+  rc = fault_hook();
+  if (rc != W4G128_OK) return rc;
+  if (!device_is_sm103()) return W4G128_ERR_DEVICE;
+  Params p;
+  p.logits = a->logits; p.out = a->out;
+  p.history = a->history_size > 0 ? a->history : nullptr;
+  p.history_start = a->history_start; p.history_len = a->history_len; p.prompt_len = a->prompt_len;
+  p.repetition = a->repetition; p.presence = a->presence; p.frequency = a->frequency;
+  p.bias_tokens = a->bias_size > 0 ? a->bias_tokens : nullptr;
+  p.bias_values = a->bias_values; p.bias_offsets = a->bias_offsets; p.mask = a->mask;
+  p.row_stride = a->row_stride; p.out_stride = a->out_stride; p.mask_row = a->mask_row; p.history_size = a->history_size;
+  p.bias_size = a->bias_size; p.vocab = a->vocab;
+  const int ctas = kMostCtas;
+  p.slice = ((a->vocab + 7 + ctas - 1) / ctas + 7) / 8 * 8;
+  const size_t shared = (p.history ? 4 : 0) * static_cast<size_t>(p.slice) + (p.bias_tokens ? 2 : 0) * static_cast<size_t>(p.slice);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, a->rows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = shared;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const int most = 6 * (((W4G128_MAX_VOCAB + 7 + kMostCtas - 1) / kMostCtas + 7) / 8 * 8);
+  cudaError_t e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, penalize_kernel, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return W4G128_ERR_CUDA;
+  }
+  return W4G128_OK;
+}
+
+}  // extern "C"
