@@ -285,18 +285,18 @@ W4G128_API int w4g128_append(const w4g128_append_args* args, void* ws, size_t ws
  * ATTENTION OF NEW TOKENS OVER A PAGED CACHE OF 8 BITS
  *
  * w4g128_attend over a cache of e4m3 codes and scales as w4g128_append writes it
- * (or another program, with any scale from 2^-126 to 2^126):
+ * (or another program, with any normal positive scales; a value's below 2^-80
+ * counts as 2^-80):
  *   out[h] = sum_j softmax_j(scale q[h] . k_j) v_j,  k_j, v_j = code * scale of the block,
  * over the same positions.  The new tokens' keys and values are in the cache
  * already.  Scores, softmax statistics and sums are held in fp32.  Codes enter
  * the products as fp16, exactly; q as fp16 scaled by its row's and head's largest
  * value, exactly down to 2^-31 of that; the softmax weights times the values'
- * scales rounded to fp16 (2^-12), from 2^-30 of the row's largest on with an
- * absolute error of 2^-31 of that.
+ * scales rounded to fp16: by 2^-11 of their value, or 2^-31 of the row's largest.
  *
  * Row m's bits depend on its own position, query and visible codes and scales
- * alone, given the same count, q_heads, kv_heads, head_dim, max_len, max_new,
- * window and sinks.  A row at a negative position, or all of whose scores are
+ * alone, not on the other rows of the call nor on max_new, given the same count,
+ * kv_heads, head_dim, max_len, window and sinks.  A row at a negative position, or all of whose scores are
  * -inf, has out 0.  Rows of no sequence are left as they are.  Masked positions
  * take no part whatever their codes and scales hold. */
 typedef struct {

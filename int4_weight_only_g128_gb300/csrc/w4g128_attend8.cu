@@ -42,6 +42,8 @@ constexpr size_t kStatusBytes = 256;
 constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;  // a reference follows its maximum when that is above it by more (base 2)
 constexpr float kLift = 6.f;   // weights are up to 2^(kSlack + kLift): fp16 holds them down to 2^-30 of the largest
+constexpr float kLowestScale = 0x1p-80f;  // of a value: smaller ones count as this, so that weights over scales stay in range
+constexpr float kLowWeight = 0x1p-90f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
 
@@ -454,13 +456,13 @@ attend8_kernel(const __grid_constant__ Params p) {
       }
       // the scales of this lane's positions 2 c, 2 c + 1, + 8
       const float* scales = reinterpret_cast<const float*>(ring + stage_bytes + 2 * S::kTileBytes);
-      float inverse[2][2];
+      float inverse[2][2], log_v[2][2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float2 ks = *reinterpret_cast<const float2*>(scales + h * 8 + 2 * c);
         const float2 vs = *reinterpret_cast<const float2*>(scales + kTile + h * 8 + 2 * c);
-        const float v0 = fmaxf(vs.x, 0x1p-126f), v1 = fmaxf(vs.y, 0x1p-126f);
-        const float log0 = log2_fast(v0), log1 = log2_fast(v1);
+        const float v0 = fmaxf(vs.x, kLowestScale), v1 = fmaxf(vs.y, kLowestScale);
+        const float log0 = log_v[h][0] = log2_fast(v0), log1 = log_v[h][1] = log2_fast(v1);
         inverse[h][0] = inverse_fast(v0);
         inverse[h][1] = inverse_fast(v1);
         sc[h][0] = fmaf(sc[h][0] * factor_a, ks.x, log0);
@@ -510,8 +512,16 @@ attend8_kernel(const __grid_constant__ Params p) {
       for (int h = 0; h < 2; ++h) {
         const float w0 = exp2_fast(sc[h][0] + ra), w1 = exp2_fast(sc[h][1] + ra);
         const float w2 = exp2_fast(sc[h][2] + rb), w3 = exp2_fast(sc[h][3] + rb);
-        l_a = fmaf(w0, inverse[h][0], fmaf(w1, inverse[h][1], l_a));
-        l_b = fmaf(w2, inverse[h][0], fmaf(w3, inverse[h][1], l_b));
+        float u0 = w0 * inverse[h][0], u1 = w1 * inverse[h][1], u2 = w2 * inverse[h][0], u3 = w3 * inverse[h][1];
+        // (beside values of much larger scales, P may be below fp32's range and the weight not)
+        if (__any_sync(~0u, fminf(fminf(w0, w1), fminf(w2, w3)) < kLowWeight)) {
+          if (w0 < kLowWeight) u0 = exp2_fast(sc[h][0] + ra - log_v[h][0]);
+          if (w1 < kLowWeight) u1 = exp2_fast(sc[h][1] + ra - log_v[h][1]);
+          if (w2 < kLowWeight) u2 = exp2_fast(sc[h][2] + rb - log_v[h][0]);
+          if (w3 < kLowWeight) u3 = exp2_fast(sc[h][3] + rb - log_v[h][1]);
+        }
+        l_a += u0 + u1;
+        l_b += u2 + u3;
         pf[2 * h] = pack_half(w0, w1);
         pf[2 * h + 1] = pack_half(w2, w3);
       }

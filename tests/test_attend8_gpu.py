@@ -1,0 +1,398 @@
+"""Attention of new tokens over a paged cache of e4m3 codes (w4g128_attend8)
+against the definition in 64 bits, computed row by row from the dense values.
+
+The bound, per element, with A = sum_j softmax_j |v_j| (64 bits): the weights
+times the values' scales are rounded to fp16 (2^-11 relative each, or 2^-31 of
+the row's largest for what lies below fp16's normal range), the sum of weights
+is not, so that error is at most 2^-11 A and 2^-31 sum |code| times the largest
+scale; a score's fp32 sum of D products is off by (D + 4) 2^-24 scale sum|q k|,
+which moves a weight by that much relative, numerator and denominator; exp2,
+log2 and the inverse add 2^-20, the fp32 sums over L positions at most
+(L + 64) 2^-24 each; the output rounds once, 2^-8."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import int4_weight_only_g128_gb300 as w  # noqa: E402
+from paged_cases import Paged, values  # noqa: E402
+
+
+class Call(Paged):
+    def __init__(self, seqs, window=0, sinks=0, **kw):
+        super().__init__(seqs, **kw)
+        self.window, self.sinks, self.scale = window, sinks, self.D ** -0.5
+        self.out = torch.full((self.rows, self.Hq * self.D + self.pad), 7.0, dtype=torch.bfloat16, device="cuda")
+
+    def args(self, **kw):
+        return w.Attend8Args(**{**self.common(), **dict(out=self.out, out_row=self.out.stride(0), window=self.window,
+                                                        sinks=self.sinks, scale=self.scale), **kw})
+
+    def run(self, status=0, **kw):
+        args = self.args(**kw)
+        nb = w.w4g128_attend8_workspace_bytes(args)
+        assert nb > 0
+        ws = torch.full((nb,), 0x5A, dtype=torch.uint8, device="cuda")
+        w.w4g128_attend8(args, ws)
+        torch.cuda.synchronize()
+        assert w.w4g128_workspace_status(ws) == status
+        return self.out[:, :self.Hq * self.D].reshape(self.rows, self.Hq, self.D)
+
+    def dense(self, b):
+        """(k, v) [length][head][dim] of sequence b and the values' scales [length][head]."""
+        pos = torch.arange(self.seqs[b][0], device="cuda")
+        ids, slot = self.table[b, pos // self.page].long(), pos % self.page
+        ks, vs = (s[ids, :, slot // self.block].double() for s in (self.k_scale, self.v_scale))
+        return values(self.k_cache[ids, slot]) * ks[..., None], values(self.v_cache[ids, slot]) * vs[..., None], vs
+
+    def reference(self):
+        """out and its bound, [rows][head][dim] in 64 bits; rows of no sequence: NaN."""
+        out = torch.full((self.rows, self.Hq, self.D), float("nan"), dtype=torch.float64, device="cuda")
+        tol = torch.zeros_like(out)
+        G = self.Hq // self.Hkv
+        for b, (n, new) in enumerate(self.seqs):
+            k, v, vs = self.dense(b)
+            for i in range(new):
+                r, p = self.offsets[b] + i, n - new + i
+                pos = torch.arange(max(p + 1, 0), device="cuda")
+                if self.window:
+                    pos = pos[(p - pos < self.window) | (pos < self.sinks)]
+                if pos.numel() == 0:
+                    out[r] = 0
+                    continue
+                q = self.q[r].double().view(self.Hkv, G, self.D)
+                kk, vv = k[pos], v[pos]
+                a = torch.softmax(torch.einsum("hgd,lhd->hgl", q, kk) * self.scale, -1)
+                o = torch.einsum("hgl,lhd->hgd", a, vv)
+                A = torch.einsum("hgl,lhd->hgd", a, vv.abs())
+                s = (torch.einsum("hgd,lhd->hgl", q.abs(), kk.abs()).amax(-1) * abs(self.scale))[..., None]
+                e = 2 * (self.D + 4) * 2.0 ** -24 * s + 2.0 ** -20 + 2 * (pos.numel() + 64) * 2.0 ** -24
+                small = 2.0 ** -31 * (vv.abs() / vs[pos][..., None]).sum(0) * vs[pos].amax(0)[:, None]
+                out[r] = o.reshape(self.Hq, self.D)
+                tol[r] = (2.0 ** -8 * o.abs() + (A + o.abs()) * (2.0 ** -11 + e) * 1.02 + small[:, None]).reshape(self.Hq, self.D)
+        return out, tol
+
+    def check(self, **kw):
+        ref, tol = self.reference()
+        before = [t.clone() for t in (self.k_cache, self.v_cache, self.k_scale, self.v_scale)]
+        rest = self.out.clone()
+        got = self.run(**kw)
+        mine = ~torch.isnan(ref[:, 0, 0])
+        err = (got[mine].double() - ref[mine]).abs()
+        assert torch.isfinite(got[mine]).all()
+        assert (err <= tol[mine]).all(), float((err / tol[mine].clamp(min=1e-30)).max())
+        assert torch.equal(got[~mine], rest[:, :self.Hq * self.D].reshape(got.shape)[~mine])
+        assert torch.equal(self.out[:, self.Hq * self.D:], rest[:, self.Hq * self.D:])
+        for t, b in zip((self.k_cache, self.v_cache, self.k_scale, self.v_scale), before):
+            assert torch.equal(t, b)
+        return got
+
+
+LENGTHS = [(1, 1), (2, 2), (15, 3), (16, 1), (17, 5), (31, 16), (63, 1), (64, 4), (65, 2), (80, 16), (129, 7), (300, 1)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("kv_heads,group,block", [(1, 1, 16), (2, 4, 1), (1, 16, 4), (3, 5, 8)])
+def test_lengths(dim, kv_heads, group, block):
+    Call(LENGTHS, q_heads=kv_heads * group, kv_heads=kv_heads, dim=dim, block=block, seed=dim + group).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,n,new,page,block", [(64, 5003, 16, 16, 16), (128, 9001, 8, 64, 64), (256, 4097, 3, 48, 16),
+                                                  (128, 70001, 1, 256, 32), (64, 300011, 2, 64, 1)])
+def test_long(dim, n, new, page, block):
+    Call([(n, new)], q_heads=8, kv_heads=2, dim=dim, page=page, block=block, seed=n).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kv_heads,count", [(1, 1), (1, 2), (5, 1), (7, 3), (8, 2), (11, 2), (4, 20), (64, 5), (256, 3)])
+def test_splits(kv_heads, count):
+    """From one head on many clusters to many heads on one CTA each."""
+    Call([(3001 - 7 * b, 1 + b % 3) for b in range(count)], q_heads=kv_heads, kv_heads=kv_heads, dim=64, seed=kv_heads,
+         block=2).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (7, 3), (16, 16), (64, 4), (100, 70), (5000, 4), (1 << 30, 9)])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_windows_and_sinks(window, sinks, dim):
+    Call(LENGTHS + [(2000, 9), (1999, 16)], dim=dim, window=window, sinks=sinks, seed=window % 1000 + sinks,
+         page=32, block=32).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kw", [dict(head_major=True), dict(pad=8), dict(page=48, pad=64, head_major=True, block=4),
+                                dict(max_len=5000), dict(page=1024, block=64), dict(spread=12)])
+def test_layouts(kw):
+    Call([(333, 4), (20, 1), (1, 1), (150, 16)], q_heads=12, kv_heads=2, dim=128, seed=3, **kw).check()
+
+
+@pytest.mark.gpu
+def test_rows_that_see_nothing():
+    for max_len in (16, 1000):
+        c = Call([(0, 0), (0, 3), (2, 5), (40 if max_len > 16 else 9, 0), (7, 7), (0, 16)], max_len=max_len, seed=1)
+        got = c.check()
+        assert torch.equal(got[0:3], torch.zeros_like(got[0:3])) and torch.equal(got[3:6], torch.zeros_like(got[3:6]))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,window,sinks", [(64, 0, 0), (128, 0, 0), (256, 0, 0), (128, 200, 5), (64, 37, 40)])
+@pytest.mark.parametrize("count", [1, 4])
+def test_a_row_alone_gives_the_same_bits(dim, window, sinks, count):
+    """Each new token of a verify step, decoded alone from the same cache, gives its row's bits."""
+    seqs = [(1500, 16), (77, 5), (16, 16), (900, 1)][:count]
+    kw = dict(q_heads=6, kv_heads=2, dim=dim, window=window, sinks=sinks, max_len=1600, spread=4)
+    c = Call(seqs, seed=5, **kw)
+    together = c.run().clone()
+    for b, (n, new) in enumerate(seqs):
+        for i in (0, new // 2, new - 1):
+            one = Call([(n - new + i + 1, 1)] + [(0, 0)] * (count - 1), seed=5, **kw)
+            one.k_cache, one.v_cache, one.k_scale, one.v_scale, one.pages = c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.pages
+            one.table = c.table[b:b + 1].repeat(count, 1)
+            r = c.offsets[b] + i
+            one.q[0] = c.q[r]
+            assert torch.equal(one.run()[0], together[r]), (b, i)
+    assert torch.equal(c.run(), together)  # and again: deterministic
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_masked_codes_and_scales_take_no_part(dim):
+    """NaN codes and any scales behind a row's own position, before its window, in unused slots and in unseen pages;
+    the page ids of unseen pages are out of range."""
+    c = Call([(203, 8), (50, 8)], dim=dim, window=40, sinks=3, page=16, block=1, max_len=256, seed=7)
+    clean = c.check().clone()
+    bad = float("nan")
+    pos = torch.arange(3, 203 - 8 - 39, device="cuda")  # before the first row's window
+    for cache, scale in ((c.k_cache, c.k_scale), (c.v_cache, c.v_scale)):
+        cache[c.table[0, pos // 16].long(), pos % 16] = 0xFF
+        scale[c.table[0, pos // 16].long(), :, pos % 16] = bad
+        cache[c.table[0, 12].long(), 203 - 192:] = 0x7F  # slots behind the end
+        scale[c.table[0, 12].long(), :, 203 - 192:] = float("inf")
+        cache[c.table[0, 12].long(), 200 - 192] = 0x7F   # position 200: rows 0..4 of sequence 0 do not see it
+        scale[c.table[1, 3].long(), :, 49 - 48] = -float("inf")  # position 49: the last row of sequence 1 alone does
+    c.table[0, 1:9] = 10 ** 9          # whole pages that nobody sees
+    got = c.run()
+    assert torch.equal(got[:5], clean[:5]) and torch.equal(got[8:15], clean[8:15])
+    assert torch.isnan(got[5:8]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 256])
+def test_window_edges_inside_a_tile_with_nan_codes(dim):
+    """A value that the first rows still see and the last rows do not: its columns are NaN, the others as they were."""
+    c = Call([(90, 16)], dim=dim, window=30, page=16, max_len=96, seed=9)
+    clean = c.run().clone()
+    pos = 90 - 16 - 30 + 8  # seen by rows 0..7
+    cols = torch.tensor([0, 1, 2, 3, 17, 30, dim - 1], device="cuda")
+    c.v_cache[c.table[0, pos // 16].long(), pos % 16, 1, cols] = 0x7F
+    got = c.run()
+    assert torch.equal(got[8:], clean[8:])
+    want = clean[:8].clone()
+    want[:, 2:, cols] = float("nan")  # heads 2 and 3 share the key/value head 1
+    assert torch.equal(torch.isnan(got[:8]), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got[:8]), torch.nan_to_num(want))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,new", [(64, 3), (128, 1), (128, 16), (256, 16)])
+@pytest.mark.parametrize("scores", [lambda p: p / 32, lambda p: p / 2, lambda p: -p / 4, lambda p: 5.5 * (p // 16),
+                                    lambda p: 5.0 * (p // 64 % 2), lambda p: 300.0 * (p == 390), lambda p: -1e4 + p / 8],
+                         ids=["slow", "fast", "falling", "steps", "to and fro", "a peak", "far below zero"])
+def test_scores_that_move_the_maximum(dim, new, scores):
+    """Scores rising by less, and by more, than the factor that the kernel lets a row's weights grow to."""
+    from paged_cases import fresh_scale, to_codes
+    c = Call([(401, new), (64, new)], q_heads=8, kv_heads=2, dim=dim, block=1, seed=new)
+    c.scale = 1.0
+    c.q[:] = 0
+    c.q.view(c.rows, 8, dim)[:, :, 0] = torch.tensor([1.0, 0.5, 1.0, 2.0] * 2, device="cuda").bfloat16()
+    for b, (n, _) in enumerate(c.seqs):
+        pos = torch.arange(n, device="cuda")
+        s = scores(pos.double())
+        scale = fresh_scale(s.abs())
+        ids = c.table[b, pos // c.page].long()
+        c.k_cache[ids, pos % c.page, :, 0] = to_codes(s / scale)[:, None]
+        c.k_scale[ids, :, pos % c.page] = scale.float()[:, None]
+    c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("small,large", [(2.0 ** -70, 1.0), (2.0 ** -30, 2.0 ** 30), (1.0, 2.0 ** 100), (0.0, 1.0), (0.3, 0.7),
+                                         (2.0 ** -80, 2.0 ** 40), (2.0 ** -79, 2.0 ** -79)])
+def test_scales_of_any_size(small, large):
+    """Scales that are no powers of two, and neighbours of very different sizes: a value without weight in the sum
+    still has its weight in the softmax.  0 counts as 2^-80."""
+    c = Call([(200, 3), (31, 1), (1700, 2)], block=4, seed=21)
+    pick = torch.rand(c.v_scale.shape, generator=c.g, device="cuda") < 0.5
+    c.v_scale[:] = torch.where(pick, small, large) * (1 + torch.rand(c.v_scale.shape, generator=c.g, device="cuda"))
+    c.k_scale *= 1.1
+    given = c.v_scale.clone()
+    c.v_scale.clamp_(min=2.0 ** -80)
+    ref, tol = c.reference()
+    c.v_scale[:] = given
+    got = c.run()
+    mine = ~torch.isnan(ref[:, 0, 0])
+    assert ((got[mine].double() - ref[mine]).abs() <= tol[mine]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** 40])
+def test_queries_of_any_size(dim, size):
+    """q's row scaled up or down by a power of two and the keys the other way: the same scores, the same bits."""
+    c = Call([(300, 4), (40, 16)], dim=dim, seed=22)
+    want = c.run().clone()
+    c.q *= size
+    c.k_scale /= size
+    assert torch.equal(c.run(), want)
+
+
+@pytest.mark.gpu
+def test_non_finite_queries_stay_with_their_rows():
+    c = Call([(300, 4)], dim=128, seed=23)
+    want = c.run().clone()
+    c.q[1, 5] = float("nan")
+    c.q[2, 130] = float("inf")  # head 1
+    got = c.run()
+    assert torch.isnan(got[1, 0]).all() and torch.isnan(got[2, 1]).all()
+    keep = torch.ones(c.rows, c.Hq, dtype=torch.bool, device="cuda")
+    keep[1, 0] = keep[2, 1] = False
+    assert torch.equal(got[keep], want[keep])
+
+
+@pytest.mark.gpu
+def test_values_out_of_range_are_reported_and_left_out():
+    for max_len in (112, 40000):
+        c = Call([(100, 2), (60, 2), (80, 2)], max_len=max_len, seed=4)
+        clean = c.run().clone()
+
+        def again(status=w.ERR_CACHE, **kw):
+            c.out.fill_(7.0)
+            return c.run(status=status, **kw)
+
+        for wrong in (-1, max_len + 1, 2 ** 31 - 1, -2 ** 31):
+            c.lens[1] = wrong
+            got = again()
+            assert torch.equal(got[:2], clean[:2]) and torch.equal(got[4:6], clean[4:6]) and (got[2:4] == 7).all()
+        c.lens[1] = 60
+        for wrong in ((0, 2, 1, 6), (0, -1, 4, 6), (0, 2, 4, 2 ** 31 - 1), (0, 2, 4, -2 ** 31)):
+            c.offsets_d.copy_(torch.tensor(wrong, dtype=torch.int32))
+            got = again()
+            if wrong[1] == 2:
+                assert torch.equal(got[:2], clean[:2])
+        c.offsets_d.copy_(torch.tensor([0, 2, 4, 6], dtype=torch.int32))
+        for wrong in (-1, c.pages, 2 ** 31 - 1, -2 ** 31):
+            keep = c.table[1, 2].item()
+            c.table[1, 2] = wrong              # positions 32..47 of sequence 1
+            got = again()
+            assert torch.equal(got[:2], clean[:2]) and torch.equal(got[4:6], clean[4:6])
+            assert torch.isfinite(got[2:4]).all() and not torch.equal(got[2:4], clean[2:4])
+            c.table[1, 2] = keep
+        assert torch.equal(again(status=0), clean)
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Pages whose codes start beyond 2^32, scales beyond 2^31 elements."""
+    H, D, page = 8, 128, 64
+    pages = (1 << 32) // (H * D * page) + 40
+    c = Call([(200, 3)], q_heads=16, kv_heads=H, dim=D, page=page, block=64, seed=6)
+    small = c.run().clone()
+    first = pages - c.pages
+    for name in ("k_cache", "v_cache"):
+        t = torch.empty((pages, page, H, D), dtype=torch.uint8, device="cuda")
+        t[first:] = getattr(c, name)
+        setattr(c, name, t)
+    stride = (1 << 31) // first + 8
+    for name in ("k_scale", "v_scale"):
+        t = torch.empty(pages * stride, dtype=torch.float32, device="cuda").view(pages, stride)[:, :H, None]
+        t[first:] = getattr(c, name)
+        setattr(c, name, t)
+    assert first * stride >= 1 << 31
+    c.table[0, :4] += first
+    c.pages = pages
+    assert torch.equal(c.run(scale_head=1), small)
+
+
+@pytest.mark.gpu
+def test_streams_and_graph_replay_follow_the_lengths():
+    c = Call([(500, 2), (300, 1)], q_heads=8, kv_heads=2, dim=128, max_len=512, seed=8)
+    want = c.run().clone()
+    args = c.args()
+    ws = torch.empty(w.w4g128_attend8_workspace_bytes(args), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    c.out.fill_(7.0)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        w.Attend8Step(args, ws).run()
+    s.synchronize()
+    assert torch.equal(c.out.view(c.rows, c.Hq, c.D), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.w4g128_attend8(args, ws)
+    for seqs, status in (([(500, 2), (300, 1)], 0), ([(130, 2), (299, 1)], 0), ([(2, 2), (1, 1)], 0),
+                         ([(497, 2), (513, 1)], w.ERR_CACHE), ([(497, 2), (64, 1)], 0)):
+        c.seqs = seqs
+        c.lens.copy_(torch.tensor([n for n, _ in seqs], dtype=torch.int32))
+        g.replay()
+        torch.cuda.synchronize()
+        assert w.w4g128_workspace_status(ws) == status
+        if status == 0:
+            ref, tol = c.reference()
+            got = c.out.view(c.rows, c.Hq, c.D)[:3].double()
+            assert ((got - ref[:3]).abs() <= tol[:3]).all()
+
+
+@pytest.mark.gpu
+def test_workspace_is_not_exceeded():
+    for seqs, kw in (([(1000, 16), (40, 3)], dict(window=100, sinks=5)), ([(9000, 5)], dict(kv_heads=1))):
+        c = Call(seqs, q_heads=8, dim=64, seed=1, **kw)
+        args = c.args()
+        nb = w.w4g128_attend8_workspace_bytes(args)
+        whole = torch.full((nb + 8192,), 0x5A, dtype=torch.uint8, device="cuda")
+        w.w4g128_attend8(args, whole[4096:], ws_bytes=nb)
+        torch.cuda.synchronize()
+        assert (whole[:4096] == 0x5A).all() and (whole[4096 + nb:] == 0x5A).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 2.0])
+def test_scales(dim, scale):
+    """Negative scales prefer the smallest scores, 0 makes every visible position count the same."""
+    c = Call([(300, 4), (40, 16)], dim=dim, seed=12, window=150, sinks=2)
+    c.scale = scale
+    c.check()
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once():
+    calls = [Call([(3000, 8)], q_heads=16, kv_heads=4, dim=128, seed=s) for s in (13, 14)]
+    want = [c.run().clone() for c in calls]
+    steps, streams = [], [torch.cuda.Stream() for _ in calls]
+    for c, s in zip(calls, streams):
+        c.out.fill_(7.0)
+        a = c.args()
+        steps.append(w.Attend8Step(a, torch.empty(w.w4g128_attend8_workspace_bytes(a), dtype=torch.uint8, device="cuda"),
+                                   stream=s))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for st in steps:
+            st.run()
+    torch.cuda.synchronize()
+    for c, o in zip(calls, want):
+        assert torch.equal(c.out.view(c.rows, c.Hq, c.D)[:8], o[:8])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,n,new,page", [(64, 5003, 16, 16), (256, 4097, 3, 48), (128, 70001, 1, 256), (64, 300011, 2, 64)])
+def test_long_norm_of_the_error(dim, n, new, page):
+    """Over many positions the element bounds exceed the output, which is a mean of independent values.  The norm of a
+    row's error: the output's rounding, 2^-8 of each element, and the weights', 2^-11 each and without relation to the
+    values.  A tile left out shows."""
+    c = Call([(n, new)], q_heads=8, kv_heads=2, dim=dim, page=page, seed=n + 1)
+    ref, _ = c.reference()
+    got = c.run()
+    ref, got = ref[:new].flatten(1), got[:new].double().flatten(1)
+    assert ((got - ref).norm(dim=1) <= (2.0 ** -8 + 2.0 ** -10) * ref.norm(dim=1)).all()
