@@ -4,16 +4,18 @@
 // As in w4g128_attend, rows of one key/value head (new tokens x query heads that
 // share it) are the 16-row tiles of a warp MMA and the work is the cache's bytes:
 // half as many, so that what is left is latency and the conversion of the codes.
-//   * Every code is an fp16 value, so both products are fp16 x fp16 -> fp32.  q,
-//     bf16, becomes fp16 scaled by a power of two for each row (exact down to
-//     2^-31 of the row's largest value).
+//   * Q K^T takes K's codes as they are: a bf16 value has 8 bits, so q, scaled by a
+//     power of two for each row, is the sum of two e4m3 values (exactly down to
+//     2^-9 of the row's largest, with an error of 2^-17 of that below), each of which
+//     is multiplied with K by fp8 MMAs.  The softmax weights need more range and
+//     precision than that: P V is fp16 x fp16, to which V's codes are converted.
 //   * A key's scale multiplies its score.  A value's scale enters the softmax
 //     weight: with score s_j (base 2) and value scale v_j, P_j = 2^(s_j + log2 v_j - m),
 //     rounded to fp16 as an operand, and the row's sum takes P_j / v_j.  The
 //     reference m follows the maximum of s_j + log2 v_j, so P_j stays in fp16's range
 //     whatever the scales are, and depends on the row alone.
-//   * Codes are read by ldmatrix as pairs: K's depth and V's columns then come in
-//     another order than the MMA's, the same for q (laid out so) and for the result.
+//   * V's codes are read by ldmatrix as pairs, so its columns come in another order
+//     than the MMA's, and the result's with them.
 //   * The 16-position tiles of a sequence go in turn to all the groups of warps that
 //     work on it, whatever its length, so all of them have the same share and no CTA
 //     depends on how long a sequence may become.  A group keeps a ring of cp.async
@@ -43,7 +45,7 @@ constexpr float kNone = -INFINITY;
 constexpr float kSlack = 8.f;  // a reference follows its maximum when that is above it by more (base 2)
 constexpr float kLift = 6.f;   // weights are up to 2^(kSlack + kLift): fp16 holds them down to 2^-30 of the largest
 constexpr float kLowestScale = 0x1p-80f;  // of a value: smaller ones count as this, so that weights over scales stay in range
-constexpr float kLowWeight = 0x1p-90f;
+constexpr float kLowWeight = 0x1p-120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
 
@@ -118,6 +120,11 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
+__device__ __forceinline__ void mma_codes(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -126,6 +133,9 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 // 16 or 4 bytes, or zeros
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4_or_zero(uint32_t dst, const void* src, bool real) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(real ? 4 : 0) : "memory");
@@ -163,70 +173,101 @@ __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v <<
 __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t low_codes(uint32_t v) { return e4m3x2_to_half2(static_cast<uint16_t>(v)); }
 __device__ __forceinline__ uint32_t high_codes(uint32_t v) { return e4m3x2_to_half2(static_cast<uint16_t>(v >> 16)); }
+__device__ __forceinline__ float half_low(uint32_t v) {
+  float x;
+  asm("{.reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(x) : "r"(v));
+  return x;
+}
+__device__ __forceinline__ float half_high(uint32_t v) {
+  float x;
+  asm("{.reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h;}" : "=f"(x) : "r"(v));
+  return x;
+}
 // Bit 7 of each byte that is a NaN code.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t a) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 ld_cluster_v2(uint32_t a) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_v2(uint32_t a, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// KG groups of warps with tiles of their own, RT row tiles, DS warps per row tile.
+// Sums over parts with references and sums of weights of their own; top: the largest reference.
+struct Joined {
+  float top, ref, l = 0.f;
+  float4 sum = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ explicit Joined(float t) : top(t), ref(t == kNone ? 0.f : t) {}
+  __device__ __forceinline__ void add(const float2& st, const float4& v) {
+    const float w = exp2_fast(st.x - ref);
+    l = fmaf(st.y, w, l);
+    sum.x = fmaf(v.x, w, sum.x);
+    sum.y = fmaf(v.y, w, sum.y);
+    sum.z = fmaf(v.z, w, sum.z);
+    sum.w = fmaf(v.w, w, sum.w);
+  }
+  __device__ __forceinline__ float2 stat() const { return make_float2(top, l); }
+};
+
+// KG groups of warps with tiles of their own; RT row tiles, MT of them a warp; NT tiles
+// of positions a turn.  What fills a warp's schedule is several products at once:
+// two row tiles that share K's and V's fragments, or two tiles of positions.
 constexpr int groups_of(int head_dim) { return head_dim == 256 ? 2 : 4; }
 template <int D, int RT>
 struct Shape {
-  static constexpr int kDs = D == 256 ? 2 : 1;
   static constexpr int kKg = groups_of(D);
-  static constexpr int kGroup = RT * kDs * 32;  // threads of a group
+  static constexpr int kMt = D == 256 || RT == 1 ? 1 : 2;
+  static constexpr int kNt = D == 256 || (D == 128 && RT > 1) ? 1 : 2;
+  static constexpr int kGroup = RT / kMt * 32;  // threads of a group
   static constexpr int kThreads = kKg * kGroup;
+  // warps an SM, by the registers of a thread's sums: 128 of them leave room for 8, 64 for 12, 32 for 16
+  static constexpr int kSums = kMt * D / 2;
+  static constexpr int kWarps = kSums == 128 ? 8 : kSums == 64 ? 12 : 16;
+  static constexpr int kCtas = kWarps * 32 / kThreads > 0 ? kWarps * 32 / kThreads : 1;
   static constexpr int kRows = RT * 16;
   static constexpr int kTileBytes = kTile * D;  // K or V of one tile
-  static constexpr int kStageBytes = 2 * kTileBytes + 2 * kTile * 4;  // and their positions' scales
-  // stages: what 512 threads an SM (128 registers each) leave room for
-  static constexpr int kStages = RT == 1 ? (D == 64 ? 6 : D == 128 ? 3 : 2) : D == 64 ? 8 : D == 256 && RT == 2 ? 5 : 6;
-  static constexpr bool kQInRegs = D == 64;  // else its fragments are read from shared memory for each tile
-  static constexpr int kQBytes = kQInRegs ? 0 : kRows * 2 * D;
+  static constexpr int kStageBytes = kNt * (2 * kTileBytes + 2 * kTile * 4);  // and their positions' scales
+  static constexpr int kQBytes = kRows * 2 * D;
+  static constexpr int kRoom = (227 * 1024 / kCtas - 1536 - kQBytes) / kKg / kStageBytes;
+  static constexpr int kStages = kRoom < 6 ? kRoom : 6;
   static constexpr int kRing = kKg * kStages * kStageBytes;
-  static constexpr int kHalf = D / kDs;      // columns of a warp
   static constexpr int kSumRow = D + 16;     // floats of a row's sums (free of bank conflicts)
   static constexpr int kLeft = kRows * (kSumRow + 2) * 4;  // a group's sums, references and sums of weights
-  static constexpr int kBytes = kQBytes + (kRing > kKg * kLeft ? kRing : kKg * kLeft);
-  static constexpr int kExchange = kDs == 2 ? kKg * RT * 2 * 32 : 1;  // float4: [group][row tile][half]..
+  static constexpr int kBytes = kQBytes + kRing > kKg * kLeft ? kQBytes + kRing : kKg * kLeft;
+  // what a cluster's CTAs send to one another
+  static constexpr int received(int ctas) { return (kRows + ctas - 1) / ctas * ctas * (D + 2) * 4; }
+  static constexpr int kMostBytes = kBytes + (kRows + kMostCluster - 1) * (D + 2) * 4;
+  static_assert(kMostBytes + 512 <= 227 * 1024, "room for what a cluster's CTAs send");
+  static_assert(kStages >= 2, "a stage on its way while another is read");
 };
 
-template <int D, int RT>
-__global__ void __launch_bounds__(Shape<D, RT>::kThreads, 512 / Shape<D, RT>::kThreads)
+template <int D, int RT, bool ONE>  // ONE: a scale for each tile at most (blocks of 16 and more)
+__global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtas)
 attend8_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, RT>;
-  constexpr int kSteps = S::kHalf / 16;  // of Q K^T, per warp
-  constexpr int kPieces = D / 16;        // 16-byte pieces of a row of codes
+  constexpr int MT = S::kMt, NT = S::kNt;
+  constexpr int kSteps = D / 32;   // of Q K^T
+  constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kPer = 2 * kTile * kPieces / S::kGroup;  // pieces of a tile's K and V that one thread copies
   constexpr int kStep = S::kGroup / kPieces;             // rows between them
+  constexpr int kScales = NT * 2 * S::kTileBytes;        // a stage's scales
   static_assert(S::kGroup % kPieces == 0 && 2 * kTile % kStep == 0, "a thread copies one column of pieces");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float4 s_half[S::kExchange][2];
-  __shared__ float s_factor[S::kQInRegs ? 1 : S::kRows];  // a row's score factor
+  __shared__ float s_factor[S::kRows];  // a row's score factor
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
-  const int kg = warp / (RT * S::kDs), rt = warp / S::kDs % RT, half = warp % S::kDs;
+  const int kg = warp / (RT / MT), rw = warp % (RT / MT);  // this warp's rows: rw MT 16 ..
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
   const int cluster = static_cast<int>(blockIdx.x) / ctas;
 
+  if (ctas > 1) cluster_arrive_relaxed();  // a CTA runs before another sends it sums
   grid_dependency_wait();
   if (cluster == 0) {
     if (rank == 0) check_all(p);
+    if (ctas > 1) cluster_wait_acquire();
     return;
   }
   // cluster - 1 = ((b kv_heads + head) row_groups + rg) clusters + cl
-  int rest = (cluster - 1) / p.by_clusters;
+  const int rest = (cluster - 1) / p.by_clusters;
   const int cl = cluster - 1 - rest * p.clusters;
-  int up = rest / p.by_row_groups;
+  const int up = rest / p.by_row_groups;
   const int rg = rest - up * p.row_groups;
   const int b = up / p.by_kv_heads;
   const int head = up - b * p.kv_heads;
@@ -242,43 +283,34 @@ attend8_kernel(const __grid_constant__ Params p) {
     if (a < p.max_len) ids = table[a / p.by_page];
   }
   const Seq s = sequence(p, b);
-  if (!s.ok) return;
   const int live_rows = s.n * p.group;
-  if (rg * S::kRows >= live_rows) return;
+  if (!s.ok || rg * S::kRows >= live_rows) {
+    if (ctas > 1) cluster_wait_acquire();
+    return;
+  }
 
   // Q, asked for before the table is waited for.
   const int r = lane >> 2, c = lane & 3;
-  const int row0 = (rg * RT + rt) * 16 + r;
-  const bool busy = (rg * RT + rt) * 16 < live_rows;  // (of the warp)
-  const int pos_a = row0 < live_rows ? s.start + row0 / p.by_group : -1;  // the rows' positions
-  const int pos_b = row0 + 8 < live_rows ? s.start + (row0 + 8) / p.by_group : -1;
-  auto q_row = [&](int row) {
-    const int i = row / p.by_group;
-    return p.q + static_cast<long long>(s.first_row + i) * p.q_row +
-           static_cast<long long>(head * p.group + row - i * p.group) * D;
-  };
-  constexpr int kQPer = S::kQInRegs ? 1 : S::kRows * (D / 8) / S::kThreads;  // pieces of 8 values of a thread
-  static_assert(S::kQInRegs || S::kRows * (D / 8) % S::kThreads == 0, "each thread loads as many pieces of Q");
-  [[maybe_unused]] uint32_t qf[S::kQInRegs ? kSteps : 1][4] = {};
-  [[maybe_unused]] uint4 q_part[kQPer] = {};
-  if constexpr (S::kQInRegs) {
+  const int row_w = rg * S::kRows + rw * MT * 16;  // the warp's first row
+  const bool busy = row_w < live_rows;             // (of the warp)
+  int pos_a[MT], pos_b[MT];                        // the positions of rows r and r + 8
 #pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      if (row0 + 8 * side < live_rows) {
-        const uint2* from = reinterpret_cast<const uint2*>(q_row(row0 + 8 * side)) + c;
+  for (int m = 0; m < MT; ++m) {
+    const int row = row_w + m * 16 + r;
+    pos_a[m] = row < live_rows ? s.start + row / p.by_group : -1;
+    pos_b[m] = row + 8 < live_rows ? s.start + (row + 8) / p.by_group : -1;
+  }
+  constexpr int kQPer = S::kRows * (D / 8) / S::kThreads;  // pieces of 8 values of a thread
+  static_assert(S::kRows * (D / 8) % S::kThreads == 0, "each thread loads as many pieces of Q");
+  uint4 q_part[kQPer] = {};
 #pragma unroll
-        for (int k = 0; k < kSteps; ++k) {
-          const uint2 v = __ldg(from + k * 4);
-          qf[k][side] = v.x;
-          qf[k][side + 2] = v.y;
-        }
-      }
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < kQPer; ++e) {
-      const int i = tid + e * S::kThreads, row = rg * S::kRows + i / (D / 8);
-      if (row < live_rows) q_part[e] = __ldg(reinterpret_cast<const uint4*>(q_row(row)) + i % (D / 8));
+  for (int e = 0; e < kQPer; ++e) {
+    const int i = tid + e * S::kThreads, row = rg * S::kRows + i / (D / 8);
+    if (row < live_rows) {
+      const int at = row / p.by_group;
+      q_part[e] = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<long long>(s.first_row + at) * p.q_row +
+                                                       static_cast<long long>(head * p.group + row - at * p.group) * D) +
+                        i % (D / 8));
     }
   }
 
@@ -297,11 +329,6 @@ attend8_kernel(const __grid_constant__ Params p) {
   else ids = ids_from(lane);
   if (total > 32) ids_next = ids_from(32 + lane);
 
-  float acc[S::kHalf / 8][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
-#pragma unroll
-  for (int i = 0; i < S::kHalf / 8; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
-  float m_a = kNone, m_b = kNone, l_a = 0.f, l_b = 0.f;
-
   uint8_t* ring = smem + S::kQBytes + kg * S::kStages * S::kStageBytes;
   const uint32_t ring_at = smem_addr(ring);
   auto group_sync = [&] {
@@ -311,38 +338,55 @@ attend8_kernel(const __grid_constant__ Params p) {
   auto swizzled = [](int j, int piece) { return j * D + ((piece ^ (D == 64 ? (j >> 1) & 3 : j & 7)) << 4); };
 
   // A thread copies one column of pieces: rows j0, j0 + kStep, .. of K, then of V.
-  const int gl = (warp % (RT * S::kDs)) * 32 + lane;
+  const int gl = rw * 32 + lane;
   const int ch = gl % kPieces, j0 = gl / kPieces;
   const uint8_t* k_base = p.k_cache + head * p.head_stride + ch * 16;
   const long long v_off = p.v_cache - p.k_cache;
   const float* scale_base = ((gl & 16) ? p.v_scale : p.k_scale) + head * p.scale_head;
+  const long long row_step = kStep * p.slot_stride;
+  const long long first_row = j0 % kTile * p.slot_stride + (j0 >= kTile ? v_off : 0);
   uint32_t okays = 0u;  // of the tiles on their way, by their number mod 32: on a page
-  auto issue = [&](int k, int stage) {
-    if (k < total) {
-      if (k > 0 && (k & 31) == 0) {
-        ids = ids_next;
-        ids_next = ids_from(k + 32 + lane);
-      }
-      const int a = tile_of(k) * kTile, page = a / p.by_page;
-      const int id = __shfl_sync(~0u, ids, k & 31);
-      const bool ok = id >= 0 && id < p.pages;
-      okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
-      const int slot = a - page * static_cast<int>(p.by_page.d);
-      const uint8_t* src = k_base + (ok ? id * p.page_stride + slot * p.slot_stride : 0);
-      const uint32_t dst = ring_at + stage * S::kStageBytes;
+  auto issue = [&](int turn, int stage) {
+    if (turn * NT < total) {
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) {
-        const int jj = j0 + e * kStep, j = jj % kTile;
-        const bool is_v = jj >= kTile;
-        const bool real = ok && a + j < s.len;
-        cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
-                           real ? src + (is_v ? v_off : 0) + j * p.slot_stride : p.k_cache, real);
-      }
-      if (gl < 32) {
-        const int j = gl & 15;
-        const bool real = ok && a + j < s.len;
-        cp_async4_or_zero(dst + 2 * S::kTileBytes + gl * 4,
-                          real ? scale_base + id * p.scale_page + ((slot + j) >> p.block_log2) : p.k_scale, real);
+      for (int t = 0; t < NT; ++t) {
+        const int k = turn * NT + t;
+        if (t == 0 && k > 0 && (k & 31) == 0) {
+          ids = ids_next;
+          ids_next = ids_from(k + 32 + lane);
+        }
+        const int a = tile_of(k) * kTile, page = a / p.by_page;
+        const int id = __shfl_sync(~0u, ids, k & 31);
+        const bool ok = k < total && id >= 0 && id < p.pages;
+        okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
+        const int slot = a - page * static_cast<int>(p.by_page.d);
+        const uint32_t dst = ring_at + stage * S::kStageBytes + t * 2 * S::kTileBytes;
+        const uint32_t scale_dst = ring_at + stage * S::kStageBytes + kScales + (t * 32 + gl) * 4;
+        const uint8_t* src = k_base + (ok ? id * p.page_stride + slot * p.slot_stride : 0);
+        if (ok && a + kTile <= s.len) {  // a whole tile
+          src += first_row;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const int jj = j0 + e * kStep;
+            if (e * kStep == kTile) src += v_off - kTile * p.slot_stride;
+            cp_async16(dst + (jj >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
+            src += row_step;
+          }
+          if (gl < 32) cp_async4(scale_dst, scale_base + id * p.scale_page + ((slot + (gl & 15)) >> p.block_log2));
+        } else {  // zeros behind the end, and for what is no page
+#pragma unroll 1
+          for (int e = 0; e < kPer; ++e) {
+            const int jj = j0 + e * kStep, j = jj % kTile;
+            const bool is_v = jj >= kTile, real = ok && a + j < s.len;
+            cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
+                               real ? src + (is_v ? v_off : 0) + j * p.slot_stride : p.k_cache, real);
+          }
+          if (gl < 32) {
+            const int j = gl & 15;
+            const bool real = ok && a + j < s.len;
+            cp_async4_or_zero(scale_dst, real ? scale_base + id * p.scale_page + ((slot + j) >> p.block_log2) : p.k_scale, real);
+          }
+        }
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -350,280 +394,347 @@ attend8_kernel(const __grid_constant__ Params p) {
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) issue(i, i);
 
-  // q as fp16, its row's largest value brought to 2^14 .. 2^15 (a negative scale
-  // goes into q's signs, a scale of 0 makes q 0).
+  // q as the sum of two e4m3 values, its row's largest brought to 2^7 .. 2^8 (a
+  // negative scale goes into q's signs, a scale of 0 makes q 0; what is not finite is NaN).
   auto signed_q = [&](uint32_t v) { return (v & p.keep_q) ^ p.flip_q; };
   auto largest = [](uint32_t v, float top) {
     const float x = fabsf(low_f(v)), y = fabsf(high_f(v));
     return fmaxf(top, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
   };
-  auto shift_for = [](float top) {
-    return min(max(14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -112), 110);
-  };
   auto power = [](int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); };
-  float factor_a = 0.f, factor_b = 0.f;
-  if constexpr (S::kQInRegs) {
+#pragma unroll
+  for (int e = 0; e < kQPer; ++e) {
+    const int i = tid + e * S::kThreads, j = i / (D / 8), piece = i % (D / 8);
+    const uint32_t w[4] = {signed_q(q_part[e].x), signed_q(q_part[e].y), signed_q(q_part[e].z), signed_q(q_part[e].w)};
+    float top = 0.f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = largest(w[u], top);
+#pragma unroll
+    for (int d = 1; d < D / 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    const int shift = min(max(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -119), 110);
+    const float by = power(shift);
+    uint32_t coarse[4], fine[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      float x = low_f(w[u]) * by, y = high_f(w[u]) * by;
+      x = fabsf(x) < INFINITY ? x : NAN;
+      y = fabsf(y) < INFINITY ? y : NAN;
+      coarse[u] = to_e4m3x2(x, y);
+      const uint32_t h = low_codes(coarse[u]);
+      fine[u] = to_e4m3x2(x - half_low(h), y - half_high(h));
+    }
+    if (piece == 0) s_factor[j] = p.scale2 * power(-shift);
+    uint8_t* to = smem + j / 16 * 32 * D + swizzled(j % 16, piece >> 1) + (piece & 1) * 8;
+    *reinterpret_cast<uint2*>(to) = make_uint2(coarse[0] | coarse[1] << 16, coarse[2] | coarse[3] << 16);
+    *reinterpret_cast<uint2*>(to + 16 * D) = make_uint2(fine[0] | fine[1] << 16, fine[2] | fine[3] << 16);
+  }
+  __syncthreads();
+
+  float factor[MT][2];
+  float acc[MT][D / 8][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
+  float ref[MT][2], l[MT][2];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      float top = 0.f;
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k) top = largest(qf[k][side], largest(qf[k][side + 2], top));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      const int e = shift_for(top);
-      const float by = power(e);
-#pragma unroll
-      for (int k = 0; k < kSteps; ++k)
-#pragma unroll
-        for (int i = side; i < 4; i += 2) {
-          const uint32_t v = signed_q(qf[k][i]);
-          qf[k][i] = pack_half(low_f(v) * by, high_f(v) * by);
-        }
-      (side ? factor_b : factor_a) = p.scale2 * power(-e);
+      factor[m][side] = s_factor[(rw * MT + m) * 16 + r + 8 * side];
+      ref[m][side] = kNone;
+      l[m][side] = 0.f;
     }
-  } else {
 #pragma unroll
-    for (int e = 0; e < kQPer; ++e) {
-      const int i = tid + e * S::kThreads, j = i / (D / 8), piece = i % (D / 8);
-      uint32_t w[4] = {signed_q(q_part[e].x), signed_q(q_part[e].y), signed_q(q_part[e].z), signed_q(q_part[e].w)};
-      float top = 0.f;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) top = largest(w[u], top);
-#pragma unroll
-      for (int d = 1; d < D / 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      const int shift = shift_for(top);
-      const float by = power(shift);
-#pragma unroll
-      for (int u = 0; u < 4; ++u) w[u] = pack_half(low_f(w[u]) * by, high_f(w[u]) * by);
-      if (piece == 0) s_factor[j] = p.scale2 * power(-shift);
-      // The 16 depths of a step in the order in which K's pairs of pairs come: 0 1 4 5 8 9 12 13, then the others.
-      const int step = piece >> 1, odd = piece & 1;
-      uint8_t* to = smem + j * 2 * D;
-      *reinterpret_cast<uint2*>(to + (((2 * step) ^ (j & 7)) << 4) + odd * 8) = make_uint2(w[0], w[2]);
-      *reinterpret_cast<uint2*>(to + (((2 * step + 1) ^ (j & 7)) << 4) + odd * 8) = make_uint2(w[1], w[3]);
-    }
-    __syncthreads();
-    factor_a = s_factor[rt * 16 + r];
-    factor_b = s_factor[rt * 16 + r + 8];
+    for (int i = 0; i < D / 8; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
   }
 
-  // ldmatrix: this lane's row of a tile of K or V and its pieces (2 i + lane / 16),
-  // and of Q (rows 0-7, 8-15 of pieces 2 k, then of 2 k + 1).
+  // ldmatrix: this lane's row and its pieces 2 i + lane / 16, in a tile of K or V and
+  // in a row tile of Q's coarse or fine parts alike (the pieces from 8 on 128 bytes further).
   const int lj = lane & 15, lp = lane >> 4;
-  const uint32_t q_at = smem_addr(smem) + rt * 16 * 2 * D + lj * 2 * D;
+  constexpr int kAt = kPieces / 2 < 4 ? kPieces / 2 : 4;
+  uint32_t at[kAt];
+#pragma unroll
+  for (int i = 0; i < kAt; ++i) at[i] = swizzled(lj, 2 * i + lp);
+  auto piece_at = [&](int i) { return at[i % kAt] + i / kAt * 128; };
+  const uint32_t q_at = smem_addr(smem) + rw * MT * 32 * D;
   const int last_pos = s.len - 1;  // of the sequence's last row
+  const int turns = (total + NT - 1) / NT;
   int stage = 0;
 #pragma unroll 1
-  for (int k = 0; k < total; ++k) {
+  for (int turn = 0; turn < turns; ++turn) {
     cp_async_wait_group<S::kStages - 2>();
-    group_sync();  // the tile is there for the group, and the stage refilled next is read out
-    issue(k + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
-    const int stage_bytes = stage * S::kStageBytes;
-    const uint32_t tile = ring_at + stage_bytes;
-    const int a = tile_of(k) * kTile;
-    if (busy) {
-      float sc[2][4] = {}, odd_k[2][4] = {};  // two chains of products each
+    group_sync();  // the tiles are there for the group, and the stage refilled next is read out
+    issue(turn + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
+    const uint32_t tile = ring_at + stage * S::kStageBytes;
+    const uint8_t* tile_ptr = ring + stage * S::kStageBytes;
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    if (!busy) continue;
+
+    float sc[NT][MT][2][4];
+    {
+      float fine[NT][MT][2][4];
 #pragma unroll
-      for (int i = 0; i < kSteps / 2; ++i) {
-        uint32_t kb[4], qk[2][4];
-        ldmatrix4(kb, tile + swizzled(lj, half * (kPieces / S::kDs) + 2 * i + lp));
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          if constexpr (S::kQInRegs) {
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) qk[u][e] = qf[2 * i + u][e];
-          } else {
-            ldmatrix4(qk[u], q_at + (((2 * (half * kSteps + 2 * i + u) + lp) ^ (lj & 7)) << 4));
-          }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][m][h][i] = fine[t][m][h][i] = 0.f;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {  // positions 0-7 and 8-15, each with both parts of q
+        uint32_t kb[NT][4], qh[MT][4], ql[MT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ldmatrix4(kb[t], tile + t * 2 * S::kTileBytes + piece_at(i));
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          ldmatrix4(qh[m], q_at + m * 32 * D + piece_at(i));
+          ldmatrix4(ql[m], q_at + m * 32 * D + 16 * D + piece_at(i));
         }
-        mma(sc[0], qk[0], low_codes(kb[0]), high_codes(kb[0]));
-        mma(sc[1], qk[0], low_codes(kb[1]), high_codes(kb[1]));
-        mma(odd_k[0], qk[1], low_codes(kb[2]), high_codes(kb[2]));
-        mma(odd_k[1], qk[1], low_codes(kb[3]), high_codes(kb[3]));
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            mma_codes(sc[t][m][0], qh[m], kb[t][0], kb[t][2]);
+            mma_codes(sc[t][m][1], qh[m], kb[t][1], kb[t][3]);
+            mma_codes(fine[t][m][0], ql[m], kb[t][0], kb[t][2]);
+            mma_codes(fine[t][m][1], ql[m], kb[t][1], kb[t][3]);
+          }
       }
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sc[h][i] += odd_k[h][i];
-      if constexpr (S::kDs == 2) {  // the other half of the depth (read out before the group's next barrier)
-        float4* ex = &s_half[(kg * RT + rt) * 2 * 32][0];
-        ex[(half * 32 + lane) * 2] = make_float4(sc[0][0], sc[0][1], sc[0][2], sc[0][3]);
-        ex[(half * 32 + lane) * 2 + 1] = make_float4(sc[1][0], sc[1][1], sc[1][2], sc[1][3]);
-        asm volatile("bar.sync %0, 64;" ::"r"(S::kKg + 1 + kg * RT + rt) : "memory");
-        const float4 u = ex[((half ^ 1) * 32 + lane) * 2], v = ex[((half ^ 1) * 32 + lane) * 2 + 1];
-        sc[0][0] += u.x; sc[0][1] += u.y; sc[0][2] += u.z; sc[0][3] += u.w;
-        sc[1][0] += v.x; sc[1][1] += v.y; sc[1][2] += v.z; sc[1][3] += v.w;
-      }
-      // the scales of this lane's positions 2 c, 2 c + 1, + 8
-      const float* scales = reinterpret_cast<const float*>(ring + stage_bytes + 2 * S::kTileBytes);
-      float inverse[2][2], log_v[2][2];
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float2 ks = *reinterpret_cast<const float2*>(scales + h * 8 + 2 * c);
-        const float2 vs = *reinterpret_cast<const float2*>(scales + kTile + h * 8 + 2 * c);
-        const float v0 = fmaxf(vs.x, kLowestScale), v1 = fmaxf(vs.y, kLowestScale);
-        const float log0 = log_v[h][0] = log2_fast(v0), log1 = log_v[h][1] = log2_fast(v1);
-        inverse[h][0] = inverse_fast(v0);
-        inverse[h][1] = inverse_fast(v1);
-        sc[h][0] = fmaf(sc[h][0] * factor_a, ks.x, log0);
-        sc[h][1] = fmaf(sc[h][1] * factor_a, ks.y, log1);
-        sc[h][2] = fmaf(sc[h][2] * factor_b, ks.x, log0);
-        sc[h][3] = fmaf(sc[h][3] * factor_b, ks.y, log1);
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sc[t][m][h][i] += fine[t][m][h][i];
+    }
+
+    // Scores in base 2, each with its value's scale; what a row does not see is none.
+    constexpr int kOwn = ONE ? 1 : 4;  // scales of this lane's positions 2 c, 2 c + 1, + 8
+    float log_v[NT][kOwn], inverse[NT][kOwn];
+    bool inside[NT];
+    auto sees = [&](int row_pos, int pos, int t) {
+      return visible(p, row_pos, pos) && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u;
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float* scales = reinterpret_cast<const float*>(tile_ptr + kScales) + t * 2 * kTile;
+      float ks[kOwn];
+#pragma unroll
+      for (int e = 0; e < kOwn; ++e) {
+        const int j = ONE ? 0 : (e >> 1) * 8 + 2 * c + (e & 1);
+        ks[e] = scales[j];
+        const float v = fmaxf(scales[kTile + j], kLowestScale);
+        log_v[t][e] = log2_fast(v);
+        inverse[t][e] = inverse_fast(v);
       }
-      const bool page_ok = (okays >> (k & 31)) & 1u;
+      const int a = tile_of(turn * NT + t) * kTile;
       // every row sees the whole tile
-      const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && page_ok &&
-                          (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
-      auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && page_ok; };
-      if (!inside) {
+      inside[t] = s.start >= 0 && a + kTile - 1 <= s.first && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u &&
+                  (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        float f[2][kOwn];
+#pragma unroll
+        for (int e = 0; e < kOwn; ++e) {
+          f[0][e] = factor[m][0] * ks[e];
+          f[1][e] = factor[m][1] * ks[e];
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (!sees(i < 2 ? pos_a : pos_b, a + h * 8 + 2 * c + (i & 1))) sc[h][i] = kNone;
+          for (int i = 0; i < 4; ++i) {
+            const int e = ONE ? 0 : h * 2 + (i & 1);
+            sc[t][m][h][i] = fmaf(sc[t][m][h][i], f[i >> 1][e], log_v[t][e]);
+          }
       }
-      float ta = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
-      float tb = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
-      auto above = [&](float top, float m) { return top - m > kSlack; };  // (m may be that of no score)
-      if (__any_sync(~0u, above(ta, m_a) || above(tb, m_b))) {
+      if (!inside[t]) {
 #pragma unroll
-        for (int d = 1; d < 4; d <<= 1) {
-          ta = fmaxf(ta, __shfl_xor_sync(~0u, ta, d));
-          tb = fmaxf(tb, __shfl_xor_sync(~0u, tb, d));
-        }
-        const float na = above(ta, m_a) ? ta : m_a, nb = above(tb, m_b) ? tb : m_b;
-        const float ga = na == m_a ? 1.f : exp2_fast(m_a - na);
-        const float gb = nb == m_b ? 1.f : exp2_fast(m_b - nb);
-        m_a = na;
-        m_b = nb;
-        l_a *= ga;
-        l_b *= gb;
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int i = 0; i < S::kHalf / 8; ++i) {
-          acc[i][0] *= ga;
-          acc[i][1] *= ga;
-          acc[i][2] *= gb;
-          acc[i][3] *= gb;
-        }
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (!sees(i < 2 ? pos_a[m] : pos_b[m], a + h * 8 + 2 * c + (i & 1), t)) sc[t][m][h][i] = kNone;
       }
-      const float ra = m_a == kNone ? 0.f : kLift - m_a, rb = m_b == kNone ? 0.f : kLift - m_b;
-      uint32_t pf[4];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float w0 = exp2_fast(sc[h][0] + ra), w1 = exp2_fast(sc[h][1] + ra);
-        const float w2 = exp2_fast(sc[h][2] + rb), w3 = exp2_fast(sc[h][3] + rb);
-        float u0 = w0 * inverse[h][0], u1 = w1 * inverse[h][1], u2 = w2 * inverse[h][0], u3 = w3 * inverse[h][1];
-        // (beside values of much larger scales, P may be below fp32's range and the weight not)
-        if (__any_sync(~0u, fminf(fminf(w0, w1), fminf(w2, w3)) < kLowWeight)) {
-          if (w0 < kLowWeight) u0 = exp2_fast(sc[h][0] + ra - log_v[h][0]);
-          if (w1 < kLowWeight) u1 = exp2_fast(sc[h][1] + ra - log_v[h][1]);
-          if (w2 < kLowWeight) u2 = exp2_fast(sc[h][2] + rb - log_v[h][0]);
-          if (w3 < kLowWeight) u3 = exp2_fast(sc[h][3] + rb - log_v[h][1]);
-        }
-        l_a += u0 + u1;
-        l_b += u2 + u3;
-        pf[2 * h] = pack_half(w0, w1);
-        pf[2 * h + 1] = pack_half(w2, w3);
-      }
+    }
 
-      bool odd = false;  // NaN codes in a tile that not every row sees whole
-      const uint8_t* v_tile = ring + stage_bytes + S::kTileBytes;
-      if (!inside) {
-        const uint4* v = reinterpret_cast<const uint4*>(v_tile);
+    // The references, tile by tile (so that their order does not show), and the weights.
+    float gain[NT][MT][2];
+    bool moves[NT];
+    uint32_t pf[NT][MT][4];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      float top[MT][2];
+      bool above = false;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          top[m][side] = fmaxf(fmaxf(sc[t][m][0][2 * side], sc[t][m][0][2 * side + 1]),
+                               fmaxf(sc[t][m][1][2 * side], sc[t][m][1][2 * side + 1]));
+          above = above || top[m][side] - ref[m][side] > kSlack;  // (ref may be that of no score)
+          gain[t][m][side] = 1.f;
+        }
+      }
+      moves[t] = __any_sync(~0u, above);
+      if (moves[t]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            float x = top[m][side];
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+            const float was = ref[m][side], now = x - was > kSlack ? x : was;
+            gain[t][m][side] = now == was ? 1.f : exp2_fast(was - now);
+            ref[m][side] = now;
+          }
+      }
+      float least = INFINITY;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const float ra = ref[m][0] == kNone ? 0.f : kLift - ref[m][0], rb = ref[m][1] == kNone ? 0.f : kLift - ref[m][1];
+        float wt[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            wt[h][i] = exp2_fast(sc[t][m][h][i] + (i < 2 ? ra : rb));
+            least = fminf(least, wt[h][i]);
+          }
+          pf[t][m][2 * h] = pack_half(wt[h][0], wt[h][1]);
+          pf[t][m][2 * h + 1] = pack_half(wt[h][2], wt[h][3]);
+        }
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          const int i = 2 * side;
+          const float add = ONE ? ((wt[0][i] + wt[0][i + 1]) + (wt[1][i] + wt[1][i + 1])) * inverse[t][0]
+                                : (wt[0][i] * inverse[t][0] + wt[0][i + 1] * inverse[t][kOwn > 1 ? 1 : 0]) +
+                                      (wt[1][i] * inverse[t][kOwn > 1 ? 2 : 0] + wt[1][i + 1] * inverse[t][kOwn > 1 ? 3 : 0]);
+          l[m][side] = fmaf(l[m][side], gain[t][m][side], add);
+        }
+      }
+      // Beside values of much larger scales, P may be below fp32's range and the weight not.
+      if (__any_sync(~0u, least < kLowWeight)) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const float ra = ref[m][0] == kNone ? 0.f : kLift - ref[m][0], rb = ref[m][1] == kNone ? 0.f : kLift - ref[m][1];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int e = ONE ? 0 : h * 2 + (i & 1);
+              const float x = sc[t][m][h][i] + (i < 2 ? ra : rb);
+              const float w = exp2_fast(x);
+              if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[t][e]) - w * inverse[t][e];
+            }
+        }
+      }
+    }
+
+    bool odd[NT];  // NaN codes in a tile that not every row sees whole
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      odd[t] = false;
+      if (!inside[t]) {
+        const uint4* v = reinterpret_cast<const uint4*>(tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes);
+        bool found = false;
         for (int i = lane; i < S::kTileBytes / 16; i += 32) {
           const uint4 u = v[i];
-          odd |= (nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w)) != 0u;
+          found |= (nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w)) != 0u;
         }
-        odd = __any_sync(~0u, odd);
+        odd[t] = __any_sync(~0u, found);
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (moves[t]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[t][m][e >> 1];
       }
 #pragma unroll
-      for (int i = 0; i < S::kHalf / 32; ++i) {
+      for (int i = 0; i < D / 32; ++i) {
         uint32_t vb[4];
-        ldmatrix4_trans(vb, tile + S::kTileBytes + swizzled(lj, half * (kPieces / S::kDs) + 2 * i + lp));
-        if (odd) {
+        ldmatrix4_trans(vb, tile + t * 2 * S::kTileBytes + S::kTileBytes + piece_at(i));
+        if (odd[t]) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) vb[e] &= ~((nan_codes(vb[e]) >> 7) * 0xFFu);
         }
+        uint32_t even_v[4], odd_v[4];  // a column's two positions together
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vb[e] = __byte_perm(vb[e], 0u, 0x3120);  // a column's two positions together
-        mma(acc[4 * i], pf, low_codes(vb[0]), low_codes(vb[1]));
-        mma(acc[4 * i + 1], pf, high_codes(vb[0]), high_codes(vb[1]));
-        mma(acc[4 * i + 2], pf, low_codes(vb[2]), low_codes(vb[3]));
-        mma(acc[4 * i + 3], pf, high_codes(vb[2]), high_codes(vb[3]));
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t both = __byte_perm(vb[e], 0u, 0x3120);
+          even_v[e] = low_codes(both);
+          odd_v[e] = high_codes(both);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma(acc[m][4 * i], pf[t][m], even_v[0], even_v[1]);
+          mma(acc[m][4 * i + 1], pf[t][m], odd_v[0], odd_v[1]);
+          mma(acc[m][4 * i + 2], pf[t][m], even_v[2], even_v[3]);
+          mma(acc[m][4 * i + 3], pf[t][m], odd_v[2], odd_v[3]);
+        }
       }
-      if (odd) {  // a row that sees a NaN code has NaN in its column
+      if (odd[t]) {  // a row that sees a NaN code has NaN in its column
+        const uint8_t* v_tile = tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes;
+        const int a = tile_of(turn * NT + t) * kTile;
         for (int j = 0; j < kTile; ++j) {
-          const bool va = sees(pos_a, a + j), vb = sees(pos_b, a + j);
 #pragma unroll
-          for (int i = 0; i < S::kHalf / 16; ++i) {
-            const uint32_t bad =
-                nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(j, half * (kPieces / S::kDs) + i) + 4 * c));
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t bad = nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(j, i) + 4 * c));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((bad >> (8 * e + 7)) & 1u) {
-                if (va) acc[2 * i + (e & 1)][e >> 1] = NAN;
-                if (vb) acc[2 * i + (e & 1)][2 + (e >> 1)] = NAN;
+            for (int m = 0; m < MT; ++m) {
+              const bool va = sees(pos_a[m], a + j, t), vb = sees(pos_b[m], a + j, t);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((bad >> (8 * e + 7)) & 1u) {
+                  if (va) acc[m][2 * i + (e & 1)][e >> 1] = NAN;
+                  if (vb) acc[m][2 * i + (e & 1)][2 + (e >> 1)] = NAN;
+                }
               }
             }
           }
         }
       }
     }
-    stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
 #pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    l_a += __shfl_xor_sync(~0u, l_a, d);
-    l_b += __shfl_xor_sync(~0u, l_b, d);
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-  __syncthreads();  // the ring becomes the exchange
-
-  // Join the CTA's groups, then the cluster's CTAs, each time in order.
-  float* left = reinterpret_cast<float*>(smem + S::kQBytes);
-  constexpr int kLeft = S::kLeft / 4, kStat = S::kRows * S::kSumRow;
-  const int rows_here = min(S::kRows, live_rows - rg * S::kRows);
-  {
-    float* mine_left = left + kg * kLeft;
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      const int row = rt * 16 + r + 8 * side;
-      if (row < rows_here) {
-        float* to = mine_left + row * S::kSumRow + half * S::kHalf + 4 * c;
+      l[m][side] += __shfl_xor_sync(~0u, l[m][side], 1);
+      l[m][side] += __shfl_xor_sync(~0u, l[m][side], 2);
+    }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // q and the ring become the exchange
+
+  // Join the CTA's groups, then the cluster's CTAs, each time in order.
+  float* left = reinterpret_cast<float*>(smem);
+  constexpr int kLeft = S::kLeft / 4, kStat = S::kRows * S::kSumRow;
+  const int rows_here = min(S::kRows, live_rows - rg * S::kRows);
 #pragma unroll
-        for (int i = 0; i < S::kHalf / 16; ++i)
-          *reinterpret_cast<float4*>(to + 16 * i) = make_float4(acc[2 * i][2 * side], acc[2 * i + 1][2 * side],
-                                                                acc[2 * i][2 * side + 1], acc[2 * i + 1][2 * side + 1]);
-        if (c == 0 && half == 0)
-          *reinterpret_cast<float2*>(mine_left + kStat + 2 * row) = make_float2(side ? m_b : m_a, side ? l_b : l_a);
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const int row = (rw * MT + m) * 16 + r + 8 * side;
+      if (row < rows_here) {
+        float* to = left + kg * kLeft + row * S::kSumRow + 4 * c;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float4*>(to + 16 * i) = make_float4(acc[m][2 * i][2 * side], acc[m][2 * i + 1][2 * side],
+                                                                acc[m][2 * i][2 * side + 1], acc[m][2 * i + 1][2 * side + 1]);
+        if (c == 0)
+          *reinterpret_cast<float2*>(left + kg * kLeft + kStat + 2 * row) = make_float2(ref[m][side], l[m][side]);
       }
     }
-  }
   __syncthreads();
   const int units = rows_here * (D / 4);  // of 4 columns
-  float4 sum;
-  float2 st;
-  auto join = [&](auto&& stat_of, auto&& sums_of, int n) {
-    float top = kNone;
-    for (int i = 0; i < n; ++i) top = fmaxf(top, stat_of(i).x);
-    const float ref = top == kNone ? 0.f : top;
-    sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float2 t = stat_of(i);
-      const float w = exp2_fast(t.x - ref);
-      const float4 v = sums_of(i);
-      l = fmaf(t.y, w, l);
-      sum.x = fmaf(v.x, w, sum.x);
-      sum.y = fmaf(v.y, w, sum.y);
-      sum.z = fmaf(v.z, w, sum.z);
-      sum.w = fmaf(v.w, w, sum.w);
-    }
-    st = make_float2(top, l);
-  };
-  auto emit = [&](int u) {
-    const int row = rg * S::kRows + u / (D / 4), col = u % (D / 4) * 4;
+  auto emit = [&](int row, int col, const float4& sum, const float2& st) {  // (row: of this CTA's)
+    row += rg * S::kRows;
     if (p.clusters == 1) {
       const float inv = st.y == 0.f ? 0.f : 1.f / st.y;  // no visible position: zeros
       const int i = row / p.by_group;
@@ -631,64 +742,127 @@ attend8_kernel(const __grid_constant__ Params p) {
                     static_cast<long long>(head * p.group + row - i * p.group) * D + col;
       *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16(sum.x * inv, sum.y * inv), pack_bf16(sum.z * inv, sum.w * inv));
     } else {
-      const long long at =
+      const long long to =
           ((static_cast<long long>(b) * p.kv_heads + head) * p.clusters + cl) * (p.max_new * p.group) + row;
-      *reinterpret_cast<float4*>(p.part + at * D + col) = sum;
-      if (col == 0) p.stat[at] = st;
+      *reinterpret_cast<float4*>(p.part + to * D + col) = sum;
+      if (col == 0) p.stat[to] = st;
     }
   };
+  // A cluster's row is joined by its CTA of rank row % ctas, in its place row / ctas.
+  float* received = reinterpret_cast<float*>(smem + S::kBytes);
+  float2* received_stat = reinterpret_cast<float2*>(received + (S::kRows + ctas - 1) / ctas * ctas * D);
+  if (ctas > 1) cluster_wait_acquire();
   for (int u = tid; u < units; u += S::kThreads) {
     const int row = u / (D / 4), col = u % (D / 4) * 4;
-    join([&](int i) { return *reinterpret_cast<const float2*>(left + i * kLeft + kStat + 2 * row); },
-         [&](int i) { return *reinterpret_cast<const float4*>(left + i * kLeft + row * S::kSumRow + col); }, S::kKg);
+    float2 stats[S::kKg];
+    float4 sums[S::kKg];
+    float top = kNone;
+#pragma unroll
+    for (int i = 0; i < S::kKg; ++i) {
+      stats[i] = *reinterpret_cast<const float2*>(left + i * kLeft + kStat + 2 * row);
+      sums[i] = *reinterpret_cast<const float4*>(left + i * kLeft + row * S::kSumRow + col);
+      top = fmaxf(top, stats[i].x);
+    }
+    Joined joined(top);
+#pragma unroll
+    for (int i = 0; i < S::kKg; ++i) joined.add(stats[i], sums[i]);
     if (ctas == 1) {
-      emit(u);
-    } else {  // (each sum's place of group 0 is read by this thread alone; its row's statistics go to places of their own)
-      *reinterpret_cast<float4*>(left + row * S::kSumRow + col) = sum;
-      if (col == 0) *reinterpret_cast<float2*>(left + row * S::kSumRow + D) = st;
+      emit(row, col, joined.sum, joined.stat());
+    } else {
+      const int slot = row / ctas, owner = row - slot * ctas;
+      const int place = slot * ctas + rank;
+      st_cluster_v4(cluster_map(smem_addr(received + place * D + col), owner), joined.sum);
+      if (col == 0) st_cluster_v2(cluster_map(smem_addr(received_stat + place), owner), joined.stat());
     }
   }
   if (ctas == 1) return;
   cluster_arrive_release();
   cluster_wait_acquire();
-  const uint32_t left_at = smem_addr(left);
-  const int share = (units + ctas - 1) / ctas;
-  for (int v = tid; v < share && rank * share + v < units; v += S::kThreads) {
-    const int u = rank * share + v, row = u / (D / 4), col = u % (D / 4) * 4;
-    const uint32_t at = left_at + row * S::kSumRow * 4;
-    join([&](int i) { return ld_cluster_v2(cluster_map(at + D * 4, i)); },
-         [&](int i) { return ld_cluster_v4(cluster_map(at + col * 4, i)); }, ctas);
-    emit(u);
+  for (int u = tid;; u += S::kThreads) {
+    const int slot = u / (D / 4), col = u % (D / 4) * 4, row = slot * ctas + rank;
+    if (row >= rows_here) break;
+    const float2* stats = received_stat + slot * ctas;
+    const float* sums = received + slot * ctas * D + col;
+    float top = kNone;
+#pragma unroll 4
+    for (int i = 0; i < ctas; ++i) top = fmaxf(top, stats[i].x);
+    Joined joined(top);
+#pragma unroll 4
+    for (int i = 0; i < ctas; ++i) joined.add(stats[i], *reinterpret_cast<const float4*>(sums + i * D));
+    emit(row, col, joined.sum, joined.stat());
   }
-  cluster_arrive_release();  // no CTA leaves while another reads its sums
-  cluster_wait_acquire();
 }
 
-// Joins a row's clusters, in order.
+// Joins a row's CTAs (or clusters): 8 warps take them in turn and are added in order.
 template <int D>
-__global__ void __launch_bounds__(D / 2) join8_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Params p) {
+  constexpr int kWarps = 8, kPer = D / 32, kBatch = 5;
+  __shared__ float s_sum[kWarps][D];
+  __shared__ float2 s_stat[kWarps];
   grid_dependency_wait();
   const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
-  const Seq s = sequence(p, b);
-  if (!s.ok || i >= s.n) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = hq / p.by_group, row = i * p.group + hq - head * p.group;
   const int step = p.max_new * p.group;
   const long long at = (static_cast<long long>(b) * p.kv_heads + head) * p.clusters * step + row;
-  float top = kNone, l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll 8
-  for (int z = 0; z < p.clusters; ++z) {
-    const float2 st = p.stat[at + static_cast<long long>(z) * step];
-    const float2 v = *reinterpret_cast<const float2*>(p.part + (at + static_cast<long long>(z) * step) * D + 2 * threadIdx.x);
-    const float next = fmaxf(top, st.x), ref = next == kNone ? 0.f : next;
-    const float old = exp2_fast(top - ref), w = exp2_fast(st.x - ref);
-    top = next;
-    l = fmaf(st.y, w, l * old);
-    x = fmaf(v.x, w, x * old);
-    y = fmaf(v.y, w, y * old);
+  // (on their way before the sequence is known: what no CTA wrote is not looked at)
+  float2 st[kBatch];
+  float v[kBatch][kPer];
+  auto load = [&](int z) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (z + kWarps * j < p.clusters) {
+        const long long from = at + static_cast<long long>(z + kWarps * j) * step;
+        st[j] = p.stat[from];
+        const float* o = p.part + from * D + lane * kPer;
+        if constexpr (kPer == 2) *reinterpret_cast<float2*>(v[j]) = *reinterpret_cast<const float2*>(o);
+        else
+#pragma unroll
+          for (int k = 0; k < kPer; k += 4) *reinterpret_cast<float4*>(&v[j][k]) = *reinterpret_cast<const float4*>(o + k);
+      }
+    }
+  };
+  load(warp);
+  const Seq s = sequence(p, b);
+  if (!s.ok || i >= s.n) return;
+  float top = kNone, l = 0.f, sum[kPer] = {};
+  for (int z = warp; z < p.clusters; z += kWarps * kBatch) {
+    if (z > warp) load(z);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (z + kWarps * j < p.clusters) {
+        const float next = fmaxf(top, st[j].x), ref = next == kNone ? 0.f : next;
+        const float old = exp2_fast(top - ref), w = exp2_fast(st[j].x - ref);
+        top = next;
+        l = fmaf(st[j].y, w, l * old);
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k] * old);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) s_sum[warp][lane * kPer + k] = sum[k];
+  if (lane == 0) s_stat[warp] = make_float2(top, l);
+  __syncthreads();
+  if (threadIdx.x >= D / 2) return;
+  const int k = threadIdx.x;
+  top = kNone;
+#pragma unroll
+  for (int j = 0; j < kWarps; ++j) top = fmaxf(top, s_stat[j].x);
+  const float ref = top == kNone ? 0.f : top;
+  float x = 0.f, y = 0.f;
+  l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kWarps; ++j) {
+    const float w = exp2_fast(s_stat[j].x - ref);
+    const float2 u = *reinterpret_cast<const float2*>(&s_sum[j][2 * k]);
+    l = fmaf(s_stat[j].y, w, l);
+    x = fmaf(u.x, w, x);
+    y = fmaf(u.y, w, y);
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
-  reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + i) * p.out_row +
-                              static_cast<long long>(hq) * D)[threadIdx.x] = pack_bf16(x * inv, y * inv);
+  reinterpret_cast<uint32_t*>(p.out + static_cast<long long>(s.first_row + i) * p.out_row + static_cast<long long>(hq) * D)[k] =
+      pack_bf16(x * inv, y * inv);
 }
 
 // CTAs of a cluster, and clusters, of one sequence and head.  Not by max_new: a
@@ -701,11 +875,11 @@ Split split_for(const w4g128_attend8_args& a) {
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 2 * kTile);
   const long long pairs = static_cast<long long>(a.kv_heads) * a.count;
   const long long tiles = (span + kTile - 1) / kTile, groups = groups_of(a.head_dim);
-  const long long target = a.count < 16 ? 304 : 608;
+  const long long target = a.count < 16 ? 303 : 607;
   long long want = std::max<long long>(1, target / pairs);
   want = std::min(want, (tiles + groups - 1) / groups);
   if (want <= kMostCluster) return {static_cast<int>(want), 1};
-  return {8, static_cast<int>(want / 8)};
+  return {1, static_cast<int>(want)};
 }
 
 int check(const w4g128_attend8_args* a) {
@@ -747,29 +921,29 @@ size_t bytes_for(const w4g128_attend8_args& a) {
 template <int D, int RT>
 cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   using S = Shape<D, RT>;
-  cudaError_t e = cudaFuncSetAttribute(attend8_kernel<D, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kBytes);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(attend8_kernel<D, RT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  const auto kernel = p.block_log2 >= 4 ? attend8_kernel<D, RT, true> : attend8_kernel<D, RT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kMostBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   p.row_groups = (p.max_new * p.group + S::kRows - 1) / S::kRows;
   p.by_row_groups = divisor(p.row_groups);
   const long long clusters = 1 + static_cast<long long>(p.count) * p.kv_heads * p.row_groups * p.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
   cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kBytes;
-  return cudaLaunchKernelEx(&cfg, attend8_kernel<D, RT>, p);
+  cfg.dynamicSmemBytes = S::kBytes + (ctas > 1 ? S::received(ctas) : 0);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <int D>
-cudaError_t launch_dim(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, Params& p, int ctas) {
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;  // with the cluster
+cudaError_t launch_dim(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
+  cfg.numAttrs = ctas > 1 ? 2 : 1;  // with the cluster
   const int rows = p.max_new * p.group;
   const cudaError_t e = rows <= 16 ? launch<D, 1>(cfg, p, ctas) : rows <= 32 ? launch<D, 2>(cfg, p, ctas)
                                                                              : launch<D, 4>(cfg, p, ctas);
   if (e != cudaSuccess || p.clusters == 1) return e;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
-  cfg.blockDim = dim3(D / 2);
+  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, join8_kernel<D>, p);
 }
@@ -829,9 +1003,9 @@ int w4g128_attend8(const w4g128_attend8_args* a, void* ws, size_t ws_bytes, void
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.stream = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = a->head_dim == 64 ? launch_dim<64>(cfg, attr, p, split.ctas)
-                        : a->head_dim == 128 ? launch_dim<128>(cfg, attr, p, split.ctas)
-                                             : launch_dim<256>(cfg, attr, p, split.ctas);
+  cfg.attrs = attr;
+  const cudaError_t e = a->head_dim == 64 ? launch_dim<64>(cfg, p, split.ctas)
+                        : a->head_dim == 128 ? launch_dim<128>(cfg, p, split.ctas) : launch_dim<256>(cfg, p, split.ctas);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return W4G128_ERR_CUDA;
