@@ -290,11 +290,9 @@ W4G128_API int w4g128_append(const w4g128_append_args* args, void* ws, size_t ws
  *   out[h] = sum_j softmax_j(scale q[h] . k_j) v_j,  k_j, v_j = code * scale of the block,
  * over the same positions.  The new tokens' keys and values are in the cache
  * already.  Scores, softmax statistics and sums are held in fp32.  Codes enter
- * the products exactly; q as the sum of two e4m3 values scaled by its row's and
- * head's largest, exactly down to 2^-9 of that, below with an error of at most
- * 2^-17 of it (a row of q that is not finite has out NaN); the softmax weights
- * times the values' scales rounded to fp16: by 2^-11 of their value, or 2^-31 of
- * the row's largest.
+ * the products as fp16, exactly; q as fp16 scaled by its row's and head's largest
+ * value, exactly down to 2^-31 of that; the softmax weights times the values'
+ * scales rounded to fp16: by 2^-11 of their value, or 2^-31 of the row's largest.
  *
  * Row m's bits depend on its own position, query and visible codes and scales
  * alone, not on the other rows of the call nor on max_new, given the same count,

@@ -4,18 +4,19 @@
 // As in w4g128_attend, rows of one key/value head (new tokens x query heads that
 // share it) are the 16-row tiles of a warp MMA and the work is the cache's bytes:
 // half as many, so that what is left is latency and the conversion of the codes.
-//   * Q K^T takes K's codes as they are: a bf16 value has 8 bits, so q, scaled by a
-//     power of two for each row, is the sum of two e4m3 values (exactly down to
-//     2^-9 of the row's largest, with an error of 2^-17 of that below), each of which
-//     is multiplied with K by fp8 MMAs.  The softmax weights need more range and
-//     precision than that: P V is fp16 x fp16, to which V's codes are converted.
+//   * Every code is an fp16 value, so both products are fp16 x fp16 -> fp32, and the
+//     codes are converted on their way into them.  q, bf16, becomes fp16 scaled by a
+//     power of two for each row (exact down to 2^-31 of the row's largest value).
+//     (The warp MMA of e4m3 operands is made of conversions and fp16 products here:
+//     with q as the sum of two e4m3 values it took 936 instructions a tile, and 33
+//     us where this takes .)
 //   * A key's scale multiplies its score.  A value's scale enters the softmax
 //     weight: with score s_j (base 2) and value scale v_j, P_j = 2^(s_j + log2 v_j - m),
 //     rounded to fp16 as an operand, and the row's sum takes P_j / v_j.  The
 //     reference m follows the maximum of s_j + log2 v_j, so P_j stays in fp16's range
 //     whatever the scales are, and depends on the row alone.
-//   * V's codes are read by ldmatrix as pairs, so its columns come in another order
-//     than the MMA's, and the result's with them.
+//   * Codes are read by ldmatrix as pairs: K's depth and V's columns then come in
+//     another order than the MMA's, the same for q (laid out so) and for the result.
 //   * The 16-position tiles of a sequence go in turn to all the groups of warps that
 //     work on it, whatever its length, so all of them have the same share and no CTA
 //     depends on how long a sequence may become.  A group keeps a ring of cp.async
@@ -120,11 +121,6 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t a) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
 }
-__device__ __forceinline__ void mma_codes(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -173,16 +169,6 @@ __device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v <<
 __device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
 __device__ __forceinline__ uint32_t low_codes(uint32_t v) { return e4m3x2_to_half2(static_cast<uint16_t>(v)); }
 __device__ __forceinline__ uint32_t high_codes(uint32_t v) { return e4m3x2_to_half2(static_cast<uint16_t>(v >> 16)); }
-__device__ __forceinline__ float half_low(uint32_t v) {
-  float x;
-  asm("{.reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, l;}" : "=f"(x) : "r"(v));
-  return x;
-}
-__device__ __forceinline__ float half_high(uint32_t v) {
-  float x;
-  asm("{.reg .f16 l, h; mov.b32 {l, h}, %1; cvt.f32.f16 %0, h;}" : "=f"(x) : "r"(v));
-  return x;
-}
 // Bit 7 of each byte that is a NaN code.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t v) { return ((v & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ void st_cluster_v2(uint32_t a, float2 v) {
@@ -242,7 +228,7 @@ __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtas)
 attend8_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, RT>;
   constexpr int MT = S::kMt, NT = S::kNt;
-  constexpr int kSteps = D / 32;   // of Q K^T
+  constexpr int kSteps = D / 16;   // of Q K^T
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kPer = 2 * kTile * kPieces / S::kGroup;  // pieces of a tile's K and V that one thread copies
   constexpr int kStep = S::kGroup / kPieces;             // rows between them
@@ -394,8 +380,8 @@ attend8_kernel(const __grid_constant__ Params p) {
 #pragma unroll 1
   for (int i = 0; i < S::kStages - 1; ++i) issue(i, i);
 
-  // q as the sum of two e4m3 values, its row's largest brought to 2^7 .. 2^8 (a
-  // negative scale goes into q's signs, a scale of 0 makes q 0; what is not finite is NaN).
+  // q as fp16, its row's largest value brought to 2^14 .. 2^15 (a negative scale
+  // goes into q's signs, a scale of 0 makes q 0).
   auto signed_q = [&](uint32_t v) { return (v & p.keep_q) ^ p.flip_q; };
   auto largest = [](uint32_t v, float top) {
     const float x = fabsf(low_f(v)), y = fabsf(high_f(v));
@@ -411,22 +397,16 @@ attend8_kernel(const __grid_constant__ Params p) {
     for (int u = 0; u < 4; ++u) top = largest(w[u], top);
 #pragma unroll
     for (int d = 1; d < D / 8; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-    const int shift = min(max(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -119), 110);
+    const int shift = min(max(14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), -112), 110);
     const float by = power(shift);
-    uint32_t coarse[4], fine[4];
+    uint32_t half[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      float x = low_f(w[u]) * by, y = high_f(w[u]) * by;
-      x = fabsf(x) < INFINITY ? x : NAN;
-      y = fabsf(y) < INFINITY ? y : NAN;
-      coarse[u] = to_e4m3x2(x, y);
-      const uint32_t h = low_codes(coarse[u]);
-      fine[u] = to_e4m3x2(x - half_low(h), y - half_high(h));
-    }
+    for (int u = 0; u < 4; ++u) half[u] = pack_half(low_f(w[u]) * by, high_f(w[u]) * by);
     if (piece == 0) s_factor[j] = p.scale2 * power(-shift);
-    uint8_t* to = smem + j / 16 * 32 * D + swizzled(j % 16, piece >> 1) + (piece & 1) * 8;
-    *reinterpret_cast<uint2*>(to) = make_uint2(coarse[0] | coarse[1] << 16, coarse[2] | coarse[3] << 16);
-    *reinterpret_cast<uint2*>(to + 16 * D) = make_uint2(fine[0] | fine[1] << 16, fine[2] | fine[3] << 16);
+    // The 16 depths of a step in the order in which K's codes come: 0 1 4 5 8 9 12 13, then the others.
+    uint8_t* to = smem + j * 2 * D + (piece & 1) * 8;
+    *reinterpret_cast<uint2*>(to + (((piece & ~1) ^ (j & 7)) << 4)) = make_uint2(half[0], half[2]);
+    *reinterpret_cast<uint2*>(to + (((piece | 1) ^ (j & 7)) << 4)) = make_uint2(half[1], half[3]);
   }
   __syncthreads();
 
@@ -446,14 +426,16 @@ attend8_kernel(const __grid_constant__ Params p) {
   }
 
   // ldmatrix: this lane's row and its pieces 2 i + lane / 16, in a tile of K or V and
-  // in a row tile of Q's coarse or fine parts alike (the pieces from 8 on 128 bytes further).
+  // in a row tile of Q (the pieces from 8 on 128 bytes further).
   const int lj = lane & 15, lp = lane >> 4;
   constexpr int kAt = kPieces / 2 < 4 ? kPieces / 2 : 4;
   uint32_t at[kAt];
 #pragma unroll
   for (int i = 0; i < kAt; ++i) at[i] = swizzled(lj, 2 * i + lp);
   auto piece_at = [&](int i) { return at[i % kAt] + i / kAt * 128; };
-  const uint32_t q_at = smem_addr(smem) + rw * MT * 32 * D;
+  uint32_t q_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) q_at[i] = smem_addr(smem) + (rw * MT * 16 + lj) * 2 * D + (((2 * i + lp) ^ (lj & 7)) << 4);
   const int last_pos = s.len - 1;  // of the sequence's last row
   const int turns = (total + NT - 1) / NT;
   int stage = 0;
@@ -468,44 +450,33 @@ attend8_kernel(const __grid_constant__ Params p) {
     if (!busy) continue;
 
     float sc[NT][MT][2][4];
-    {
-      float fine[NT][MT][2][4];
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[t][m][h][i] = fine[t][m][h][i] = 0.f;
+          for (int i = 0; i < 4; ++i) sc[t][m][h][i] = 0.f;
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {  // positions 0-7 and 8-15, each with both parts of q
-        uint32_t kb[NT][4], qh[MT][4], ql[MT][4];
+    for (int i = 0; i < kSteps / 2; ++i) {  // 32 depths of positions 0-7 and 8-15
+      uint32_t kb[NT][4];
 #pragma unroll
-        for (int t = 0; t < NT; ++t) ldmatrix4(kb[t], tile + t * 2 * S::kTileBytes + piece_at(i));
+      for (int t = 0; t < NT; ++t) ldmatrix4(kb[t], tile + t * 2 * S::kTileBytes + piece_at(i));
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          ldmatrix4(qh[m], q_at + m * 32 * D + piece_at(i));
-          ldmatrix4(ql[m], q_at + m * 32 * D + 16 * D + piece_at(i));
-        }
+      for (int u = 0; u < 2; ++u) {
+        uint32_t qk[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) ldmatrix4(qk[m], q_at[(2 * i + u) & 3] + m * 32 * D + (2 * i + u) / 4 * 128);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            mma_codes(sc[t][m][0], qh[m], kb[t][0], kb[t][2]);
-            mma_codes(sc[t][m][1], qh[m], kb[t][1], kb[t][3]);
-            mma_codes(fine[t][m][0], ql[m], kb[t][0], kb[t][2]);
-            mma_codes(fine[t][m][1], ql[m], kb[t][1], kb[t][3]);
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t k0 = low_codes(kb[t][2 * u + h]), k1 = high_codes(kb[t][2 * u + h]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma(sc[t][m][h], qk[m], k0, k1);
           }
       }
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sc[t][m][h][i] += fine[t][m][h][i];
     }
 
     // Scores in base 2, each with its value's scale; what a row does not see is none.
