@@ -199,7 +199,7 @@ template <int D, int RT>
 struct Shape {
   static constexpr int kKg = groups_of(D);
   static constexpr int kMt = D == 256 || RT == 1 ? 1 : 2;
-  static constexpr int kNt = D == 256 || (D == 128 && RT > 1) ? 1 : 2;
+  static constexpr int kNt = D < 256 && RT == 1 ? 2 : 1;
   static constexpr int kGroup = RT / kMt * 32;  // threads of a group
   static constexpr int kThreads = kKg * kGroup;
   // warps an SM, by the registers of a thread's sums: 128 of them leave room for 8, 64 for 12, 32 for 16
@@ -314,6 +314,15 @@ attend8_kernel(const __grid_constant__ Params p) {
   if (p.window == 0) ids = lane < total ? ids : -1;
   else ids = ids_from(lane);
   if (total > 32) ids_next = ids_from(32 + lane);
+  // Of 32 tiles, one a lane: where its codes and scales are, -1 where that is no page.
+  long long codes_at, scales_at;
+  auto locate = [&](int k) {
+    const int a = tile_of(k) * kTile, slot = a - a / p.by_page * static_cast<int>(p.by_page.d);
+    const bool ok = k < total && ids >= 0 && ids < p.pages;
+    codes_at = ok ? ids * p.page_stride + slot * p.slot_stride : -1;
+    scales_at = ids * p.scale_page + (slot >> p.block_log2);
+  };
+  locate(lane);
 
   uint8_t* ring = smem + S::kQBytes + kg * S::kStages * S::kStageBytes;
   const uint32_t ring_at = smem_addr(ring);
@@ -328,7 +337,8 @@ attend8_kernel(const __grid_constant__ Params p) {
   const int ch = gl % kPieces, j0 = gl / kPieces;
   const uint8_t* k_base = p.k_cache + head * p.head_stride + ch * 16;
   const long long v_off = p.v_cache - p.k_cache;
-  const float* scale_base = ((gl & 16) ? p.v_scale : p.k_scale) + head * p.scale_head;
+  // (a tile begins a block or lies in one: its position j is in the block j / block after its first)
+  const float* scale_base = ((gl & 16) ? p.v_scale : p.k_scale) + head * p.scale_head + ((gl & 15) >> p.block_log2);
   const long long row_step = kStep * p.slot_stride;
   const long long first_row = j0 % kTile * p.slot_stride + (j0 >= kTile ? v_off : 0);
   uint32_t okays = 0u;  // of the tiles on their way, by their number mod 32: on a page
@@ -340,15 +350,15 @@ attend8_kernel(const __grid_constant__ Params p) {
         if (t == 0 && k > 0 && (k & 31) == 0) {
           ids = ids_next;
           ids_next = ids_from(k + 32 + lane);
+          locate(k + lane);
         }
-        const int a = tile_of(k) * kTile, page = a / p.by_page;
-        const int id = __shfl_sync(~0u, ids, k & 31);
-        const bool ok = k < total && id >= 0 && id < p.pages;
+        const int a = tile_of(k) * kTile;
+        const long long codes = __shfl_sync(~0u, codes_at, k & 31), scales = __shfl_sync(~0u, scales_at, k & 31);
+        const bool ok = codes >= 0;
         okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
-        const int slot = a - page * static_cast<int>(p.by_page.d);
         const uint32_t dst = ring_at + stage * S::kStageBytes + t * 2 * S::kTileBytes;
         const uint32_t scale_dst = ring_at + stage * S::kStageBytes + kScales + (t * 32 + gl) * 4;
-        const uint8_t* src = k_base + (ok ? id * p.page_stride + slot * p.slot_stride : 0);
+        const uint8_t* src = k_base + (ok ? codes : 0);
         if (ok && a + kTile <= s.len) {  // a whole tile
           src += first_row;
 #pragma unroll
@@ -358,7 +368,7 @@ attend8_kernel(const __grid_constant__ Params p) {
             cp_async16(dst + (jj >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
             src += row_step;
           }
-          if (gl < 32) cp_async4(scale_dst, scale_base + id * p.scale_page + ((slot + (gl & 15)) >> p.block_log2));
+          if (gl < 32) cp_async4(scale_dst, scale_base + scales);
         } else {  // zeros behind the end, and for what is no page
 #pragma unroll 1
           for (int e = 0; e < kPer; ++e) {
@@ -370,7 +380,7 @@ attend8_kernel(const __grid_constant__ Params p) {
           if (gl < 32) {
             const int j = gl & 15;
             const bool real = ok && a + j < s.len;
-            cp_async4_or_zero(scale_dst, real ? scale_base + id * p.scale_page + ((slot + j) >> p.block_log2) : p.k_scale, real);
+            cp_async4_or_zero(scale_dst, real ? scale_base + scales : p.k_scale, real);
           }
         }
       }
@@ -446,6 +456,7 @@ attend8_kernel(const __grid_constant__ Params p) {
     issue(turn + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
     const uint32_t tile = ring_at + stage * S::kStageBytes;
     const uint8_t* tile_ptr = ring + stage * S::kStageBytes;
+    auto there = [&](int t) { return t == 0 || turn * NT + t < total; };  // the last turn may have one tile
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
     if (!busy) continue;
 
@@ -500,8 +511,8 @@ attend8_kernel(const __grid_constant__ Params p) {
       }
       const int a = tile_of(turn * NT + t) * kTile;
       // every row sees the whole tile
-      inside[t] = s.start >= 0 && a + kTile - 1 <= s.first && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u &&
-                  (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
+      inside[t] = !there(t) || (s.start >= 0 && a + kTile - 1 <= s.first && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u &&
+                                (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         float f[2][kOwn];
@@ -535,6 +546,7 @@ attend8_kernel(const __grid_constant__ Params p) {
     uint32_t pf[NT][MT][4];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
+      if (!there(t)) break;
       float top[MT][2];
       bool above = false;
 #pragma unroll
@@ -586,7 +598,18 @@ attend8_kernel(const __grid_constant__ Params p) {
         }
       }
       // Beside values of much larger scales, P may be below fp32's range and the weight not.
-      if (__any_sync(~0u, least < kLowWeight)) {
+      // (Most of what is below it is masked, and no weight at all.)
+      bool low = least < kLowWeight;
+      if (low && !inside[t]) {
+        low = false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) low = low || (sc[t][m][h][i] > kNone && sc[t][m][h][i] - ref[m][i >> 1] < -100.f);
+      }
+      if (__any_sync(~0u, low)) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           const float ra = ref[m][0] == kNone ? 0.f : kLift - ref[m][0], rb = ref[m][1] == kNone ? 0.f : kLift - ref[m][1];
@@ -603,22 +626,9 @@ attend8_kernel(const __grid_constant__ Params p) {
       }
     }
 
-    bool odd[NT];  // NaN codes in a tile that not every row sees whole
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      odd[t] = false;
-      if (!inside[t]) {
-        const uint4* v = reinterpret_cast<const uint4*>(tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes);
-        bool found = false;
-        for (int i = lane; i < S::kTileBytes / 16; i += 32) {
-          const uint4 u = v[i];
-          found |= (nan_codes(u.x) | nan_codes(u.y) | nan_codes(u.z) | nan_codes(u.w)) != 0u;
-        }
-        odd[t] = __any_sync(~0u, found);
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
+      if (!there(t)) break;
       if (moves[t]) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -627,13 +637,18 @@ attend8_kernel(const __grid_constant__ Params p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[t][m][e >> 1];
       }
+      uint32_t nans = 0u;
 #pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
+      for (int i = 0; i < D / 32; ++i) {  // 32 columns; NaN codes in a tile that not every row sees whole are left out
         uint32_t vb[4];
         ldmatrix4_trans(vb, tile + t * 2 * S::kTileBytes + S::kTileBytes + piece_at(i));
-        if (odd[t]) {
+        if (!inside[t]) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) vb[e] &= ~((nan_codes(vb[e]) >> 7) * 0xFFu);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t bad = nan_codes(vb[e]);
+            nans |= bad;
+            vb[e] &= ~((bad >> 7) * 0xFFu);
+          }
         }
         uint32_t even_v[4], odd_v[4];  // a column's two positions together
 #pragma unroll
@@ -650,7 +665,7 @@ attend8_kernel(const __grid_constant__ Params p) {
           mma(acc[m][4 * i + 3], pf[t][m], odd_v[2], odd_v[3]);
         }
       }
-      if (odd[t]) {  // a row that sees a NaN code has NaN in its column
+      if (__any_sync(~0u, nans != 0u)) {  // a row that sees a NaN code has NaN in its column
         const uint8_t* v_tile = tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes;
         const int a = tile_of(turn * NT + t) * kTile;
         for (int j = 0; j < kTile; ++j) {
@@ -837,7 +852,13 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
 }
 
 // CTAs of a cluster, and clusters, of one sequence and head.  Not by max_new: a
-// row's sums are the same whatever rows are beside it.
+// row's sums are the same whatever rows are beside it.  As many CTAs as the GPU holds
+// of those for 32 rows (64 with heads of 256, 16 registers' worth of warps fewer):
+// 32771 on 8 heads of 128: 25.4 us with 303, 31.0 with 607, 33.3 with 151; 16 ragged
+// sequences on 4 heads of 64: 24.6 with 455, 28.3 with 607, 30.4 with 303; windows of
+// 4096 on 2 x 4 heads of 256: 21.4 with 151, 30.1 with 303.  Calls of few CTAs are
+// joined in a cluster (one sequence of 611 on 8 heads: 5.6 us, and 6.3 with a second
+// kernel); of larger ones the clusters do not fill the GPU.
 struct Split {
   int ctas, clusters;
 };
@@ -846,10 +867,9 @@ Split split_for(const w4g128_attend8_args& a) {
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 2 * kTile);
   const long long pairs = static_cast<long long>(a.kv_heads) * a.count;
   const long long tiles = (span + kTile - 1) / kTile, groups = groups_of(a.head_dim);
-  const long long target = a.count < 16 ? 303 : 607;
-  long long want = std::max<long long>(1, target / pairs);
-  want = std::min(want, (tiles + groups - 1) / groups);
-  if (want <= kMostCluster) return {static_cast<int>(want), 1};
+  const long long target = a.head_dim == 64 ? 455 : a.head_dim == 128 ? 303 : 151;
+  const long long want = std::min(std::max<long long>(1, target / pairs), (tiles + groups - 1) / groups);
+  if (want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1};
   return {1, static_cast<int>(want)};
 }
 
