@@ -1,16 +1,12 @@
 // Rotated queries, and rotated keys and values put into a paged cache
 // (w4g128_append), in one launch.
 //
-// A CTA takes 64 positions of a sequence at a multiple of 64 (so whole blocks of
-// an 8-bit cache, whose scale all of a block's rows decide) and some of the heads
-// of q, k and v.  It computes the cosines and sines of its rows once, for all its
-// heads.  A head's rows are pieces of 8 values, 16 bytes a lane; the other half of
-// a rotated pair is in another lane of the same warp (or the same piece), so it
-// comes by shuffle and every byte is read and written once.
-//   * up to 16 new rows a sequence (a decode or verify step): a warp for each
-//     head.  What takes time is the chain length -> rows -> cosines -> store.
-//   * prompts: the 8 warps share a head's rows, kept in registers between the
-//     maximum that decides an 8-bit block's scale and the codes.
+// A head's row is pieces of 8 values, 16 bytes a lane; the other half of a rotated
+// pair is in another lane of the same warp (or the same piece), so it comes by
+// shuffle, and every byte is read and written once.
+//   * up to 16 new rows a sequence (a decode or verify step): a warp for each head.
+//     What takes time is the chain length -> rows -> cosines -> store.
+//   * prompts: row by row what needs no block, by blocks what goes into 8 bits.
 // The angle p f of position p is a 64-bit integer of 2^-64 turns, p times f / 2 pi
 // rounded to that: exact modulo a turn but for p 2^-64 and the 2^-53 of f / 2 pi in
 // 64 bits.  Its multiple of a quarter turn goes into signs, so that the fp32
@@ -32,6 +28,7 @@ namespace {
 constexpr int kChunk = 64;  // positions, a multiple of every block
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
+constexpr int kWorkers = 303;  // CTAs of a prompt's call
 constexpr size_t kWorkspace = 256;
 constexpr int kLowestScale = -100;
 
@@ -44,7 +41,9 @@ struct Params {
   const int *table, *offsets, *lens;
   long long q_row, q_out_row, kv_row, page_stride, slot_stride, head_stride, scale_page, scale_head, table_row;
   int rows, count, q_heads, kv_heads, half, interleaved, pages, block_log2, max_len, max_new;
-  Divisor by_page, by_half;
+  int chunks;       // that the new rows of a sequence may touch
+  int row_workers;  // CTAs that work row by row
+  Divisor by_page, by_half, by_kv;
   unsigned long long* status;
 };
 
@@ -118,239 +117,469 @@ __device__ __forceinline__ int fresh_exponent(uint32_t top) {
 }
 __device__ __forceinline__ float exp2_of(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-template <int D, int TEAM>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Params p) {
-  constexpr int kPieces = D / 8;       // of a row
-  constexpr int kRows = 32 / kPieces;  // rows of a warp at once
-  constexpr int kMaxLive = TEAM == 1 ? kFewRows : kChunk;
-  constexpr int kPasses = kMaxLive / (kRows * TEAM);
-  constexpr int kTeams = kThreads / 32 / TEAM;
-  extern __shared__ __align__(16) float s_trig[];    // [live rows][half] cosines, then sines
-  __shared__ long long s_at[kChunk], s_block[kChunk];  // a row's slot and scale in the caches; -1: no page
-  __shared__ unsigned s_top[3][kTeams][kChunk];        // a block's magnitude, of three heads in turn
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(~0u, tid >> 5, 0);
-  const int team = warp / TEAM, member = warp % TEAM;
+// 2^-64 turns a position of one frequency.
+__device__ __forceinline__ unsigned long long turn_step(double freq) {
+  double turns = freq * 0.15915494309189533576888376337251;  // 1 / (2 pi)
+  turns -= floor(turns);
+  return __double2ull_rz(turns * 18446744073709551616.0);
+}
+// Cosine and sine of `pos` steps.
+__device__ __forceinline__ float2 turned(unsigned long long step, int pos) {
+  const unsigned long long full = static_cast<unsigned long long>(pos) * step;
+  const uint32_t turn = static_cast<uint32_t>((full + 0x80000000ull) >> 32);  // 2^-32 turns
+  const uint32_t quarter = (turn + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 0x1p-31f;  // half turns
+  float sn, cs;
+  sincospif(x, &sn, &cs);
+  const float c = (quarter & 1u) ? -sn : cs, d = (quarter & 1u) ? cs : sn;
+  return (quarter & 2u) ? make_float2(-c, -d) : make_float2(c, d);
+}
 
-  grid_dependency_wait();
-  if (blockIdx.x == gridDim.x - 1) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) check_all(p);
-    return;
-  }
-  const int b = blockIdx.z;
-  const int pair_group = p.half > 0 ? tid / p.by_half : 0;
-  const int pair = tid - pair_group * p.half;
-  double freq = 0.0;
-  if (p.half > 0) freq = p.freqs[pair];
-  const Span s = span_of(p, b);
-  if (!s.ok || s.n == 0) return;
-  const int c0 = (s.first & ~(kChunk - 1)) + static_cast<int>(blockIdx.x) * kChunk;
-  const int p0 = max(c0, s.first), p1 = min(c0 + kChunk, s.len);
-  const int live = p1 - p0;
-  if (live <= 0) return;
-  const int row0 = s.first_row + p0 - s.start;
+// A lane's piece of 8 values of a head, the pairs it belongs to and their angles.
+template <int D>
+struct Piece {
+  static constexpr int kPieces = D / 8;       // of a row
+  static constexpr int kRows = 32 / kPieces;  // rows, or heads of a row, of a warp at once
+  int sub, piece, first_pair, from;           // from: the lane with the other side of the pairs
+  bool turns, second, interleaved;
+  float c[8], s[8];  // of its pairs (interleaved: 4)
 
-  for (int i = tid; i < 3 * kTeams * kChunk; i += kThreads) (&s_top[0][0][0])[i] = 0u;
-  if (tid < live) {
-    const int pos = p0 + tid, page = pos / p.by_page;
-    const int slot = pos - page * static_cast<int>(p.by_page.d);
-    const int id = p.table[static_cast<long long>(b) * p.table_row + page];
-    const bool ok = id >= 0 && id < p.pages;
-    s_at[tid] = ok ? id * p.page_stride + slot * p.slot_stride : -1;
-    s_block[tid] = id * p.scale_page + (p.block_log2 >= 0 ? slot >> p.block_log2 : 0);
+  __device__ __forceinline__ Piece(const Params& p, int lane) {
+    sub = lane / kPieces;
+    piece = lane % kPieces;
+    const int side = p.half / 8;  // pieces of one side of the pairs
+    interleaved = p.interleaved != 0;
+    turns = piece < 2 * side;
+    second = !interleaved && piece >= side;
+    first_pair = !turns ? 0 : interleaved ? piece * 4 : (second ? piece - side : piece) * 8;
+    from = !turns || interleaved ? lane : second ? lane - side : lane + side;
   }
-  if (p.half > 0) {
-    const int groups = kThreads / p.by_half;
-    if (pair_group < groups) {
-      double turns = freq * 0.15915494309189533576888376337251;  // 1 / (2 pi)
-      turns -= floor(turns);
-      const unsigned long long step = __double2ull_rz(turns * 18446744073709551616.0);
-      for (int r = pair_group; r < live; r += groups) {
-        const unsigned long long full = static_cast<unsigned long long>(p0 + r) * step;
-        const uint32_t turn = static_cast<uint32_t>((full + 0x80000000ull) >> 32);  // 2^-32 turns
-        const uint32_t quarter = (turn + 0x20000000u) >> 30;
-        const float x = static_cast<float>(static_cast<int>(turn - (quarter << 30))) * 0x1p-31f;  // half turns
-        float sn, cs;
-        sincospif(x, &sn, &cs);
-        const float c = (quarter & 1u) ? -sn : cs, d = (quarter & 1u) ? cs : sn;
-        s_trig[r * p.half + pair] = (quarter & 2u) ? -c : c;
-        s_trig[(live + r) * p.half + pair] = (quarter & 2u) ? -d : d;
-      }
+  // Its angles, from the cosines and sines of a row.
+  __device__ __forceinline__ void look(const float* cosines, const float* sines) {
+    if (!turns) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (h == 1 && interleaved) break;
+      const float4 x = *reinterpret_cast<const float4*>(cosines + first_pair + 4 * h);
+      const float4 y = *reinterpret_cast<const float4*>(sines + first_pair + 4 * h);
+      c[4 * h] = x.x; c[4 * h + 1] = x.y; c[4 * h + 2] = x.z; c[4 * h + 3] = x.w;
+      s[4 * h] = y.x; s[4 * h + 1] = y.y; s[4 * h + 2] = y.z; s[4 * h + 3] = y.w;
     }
   }
-  __syncthreads();
-
-  const int sub = lane / kPieces, piece = lane % kPieces;
-  const int turn_pieces = p.half / 8;  // of one side of the pairs
-  auto row_of = [&](int pass) { return (pass * TEAM + member) * kRows + sub; };
-  auto rotate = [&](const uint4& raw, int r, float (&x)[8]) {
+  // All lanes of the warp; only: whether this lane's piece is rotated at all.
+  __device__ __forceinline__ void rotate(const uint4& raw, bool only, float (&x)[8]) const {
     unpack(raw, x);
-    if (p.half == 0) return;
-    if (p.interleaved) {
-      if (piece >= 2 * turn_pieces || r >= live) return;
-      const float4 c = *reinterpret_cast<const float4*>(&s_trig[r * p.half + piece * 4]);
-      const float4 d = *reinterpret_cast<const float4*>(&s_trig[(live + r) * p.half + piece * 4]);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {d.x, d.y, d.z, d.w};
+    if (interleaved) {
+      if (!turns || !only) return;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], e = x[2 * i + 1];
-        x[2 * i] = fmaf(a, cs[i], -(e * sn[i]));
-        x[2 * i + 1] = fmaf(e, cs[i], a * sn[i]);
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = fmaf(a, c[i], -(b * s[i]));
+        x[2 * i + 1] = fmaf(b, c[i], a * s[i]);
       }
       return;
     }
-    const bool second = piece >= turn_pieces;
-    const int from = piece < turn_pieces ? lane + turn_pieces : piece < 2 * turn_pieces ? lane - turn_pieces : lane;
     uint4 other;
     other.x = __shfl_sync(~0u, raw.x, from);
     other.y = __shfl_sync(~0u, raw.y, from);
     other.z = __shfl_sync(~0u, raw.z, from);
     other.w = __shfl_sync(~0u, raw.w, from);
-    if (piece >= 2 * turn_pieces || r >= live) return;
+    if (!turns || !only) return;
     float y[8];
     unpack(other, y);
-    const int i0 = (second ? piece - turn_pieces : piece) * 8;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 c = *reinterpret_cast<const float4*>(&s_trig[r * p.half + i0 + 4 * h]);
-      const float4 d = *reinterpret_cast<const float4*>(&s_trig[(live + r) * p.half + i0 + 4 * h]);
-      const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {d.x, d.y, d.z, d.w};
+    for (int i = 0; i < 8; ++i) x[i] = second ? fmaf(x[i], c[i], y[i] * s[i]) : fmaf(x[i], c[i], -(y[i] * s[i]));
+  }
+};
+
+__device__ __forceinline__ uint4 packed(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+// What is not finite becomes NaN, which takes no part in a maximum.
+__device__ __forceinline__ float magnitude(float (&x)[8]) {
+  float top = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int e = 4 * h + i;
-        x[e] = second ? fmaf(x[e], cs[i], y[e] * sn[i]) : fmaf(x[e], cs[i], -(y[e] * sn[i]));
+  for (int e = 0; e < 8; ++e) {
+    x[e] = fmaf(x[e], 0.f, x[e]);
+    top = fmaxf(top, fabsf(x[e]));
+  }
+  return top;
+}
+__device__ __forceinline__ uint2 coded(const float (&x)[8], float scale) {
+  uint32_t code[4];
+  if ((__float_as_uint(scale) & 0x007FFFFFu) == 0u) {
+    const float inverse = exp2_of(127 - static_cast<int>(__float_as_uint(scale) >> 23));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[e] = to_e4m3x2(x[2 * e] * inverse, x[2 * e + 1] * inverse);
+  } else {  // (a scale that another program set need not be a power of two)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) code[e] = to_e4m3x2(__fdiv_rn(x[2 * e], scale), __fdiv_rn(x[2 * e + 1], scale));
+  }
+  return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
+// Codes in a scale that is `factor` times smaller than before.
+__device__ __forceinline__ uint2 recoded(const uint2& old, float factor) {
+  uint32_t code[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint32_t h = e4m3x2_to_half2(static_cast<uint16_t>((e < 2 ? old.x : old.y) >> (e & 1) * 16));
+    float a, d;
+    asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(a), "=f"(d) : "r"(h));
+    code[e] = to_e4m3x2(a * factor, d * factor);
+  }
+  return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
+// The scale of a block of magnitude `top` (its bits) that has positions already (held), in the scale `was`.
+__device__ __forceinline__ float scale_for(uint32_t top, bool held, float was, bool& keeps) {
+  keeps = held && was > 0.f && __uint_as_float(top) <= kE4M3Max * was;
+  return keeps ? was : exp2_of(fresh_exponent(top));
+}
+
+// The rows of a chunk: where they go, and their cosines and sines.
+struct Rows {
+  int p0, live, row0;  // the first position, their number, the first row
+};
+__device__ __forceinline__ Rows rows_of(const Params& p, const Span& s, int chunk) {
+  const int c0 = (s.first & ~(kChunk - 1)) + chunk * kChunk;
+  Rows r;
+  r.p0 = max(c0, s.first);
+  r.live = s.ok && s.n > 0 ? min(c0 + kChunk, s.len) - r.p0 : 0;
+  r.row0 = s.first_row + r.p0 - s.start;
+  return r;
+}
+__device__ __forceinline__ void prepare_rows(const Params& p, int b, const Rows& rows, double freq, int pair, int pair_group,
+                                             long long* at, long long* block, float* trig) {
+  if (static_cast<int>(threadIdx.x) < rows.live) {
+    const int pos = rows.p0 + static_cast<int>(threadIdx.x), page = pos / p.by_page;
+    const int slot = pos - page * static_cast<int>(p.by_page.d);
+    const int id = p.table[static_cast<long long>(b) * p.table_row + page];
+    const bool ok = id >= 0 && id < p.pages;
+    at[threadIdx.x] = ok ? id * p.page_stride + slot * p.slot_stride : -1;
+    block[threadIdx.x] = id * p.scale_page + (p.block_log2 >= 0 ? slot >> p.block_log2 : 0);
+  }
+  if (p.half > 0) {
+    const int groups = kThreads / p.by_half;
+    if (pair_group < groups) {
+      const unsigned long long step = turn_step(freq);
+      for (int r = pair_group; r < rows.live; r += groups) {
+        const float2 v = turned(step, rows.p0 + r);
+        trig[r * p.half + pair] = v.x;
+        trig[(rows.live + r) * p.half + pair] = v.y;
       }
     }
-  };
-  auto packed = [&](const float (&x)[8]) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-  };
+  }
+}
 
-  const int units = 2 * p.kv_heads + p.q_heads;
-  int turn = 0;
-  for (int u0 = blockIdx.y * kTeams; u0 < units; u0 += gridDim.y * kTeams) {
-    const int u = u0 + team;
-    if (TEAM == 1 && u >= units) break;  // (one head a team: a larger team is all of the CTA)
-    const bool is_q = u >= 2 * p.kv_heads, is_v = !is_q && u >= p.kv_heads;
-    const int head = is_q ? u - 2 * p.kv_heads : is_v ? u - p.kv_heads : u;
-    const uint16_t* src = is_q ? p.q + static_cast<long long>(row0) * p.q_row
-                               : (is_v ? p.v_new : p.k_new) + static_cast<long long>(row0) * p.kv_row;
-    const long long stride = is_q ? p.q_row : p.kv_row;
-    src += static_cast<long long>(head) * D + piece * 8;
-    uint4 raw[kPasses];
+// Up to 16 new rows a sequence: a warp for each head of q, k and v.
+template <int D>
+__global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_constant__ Params p) {
+  using P = Piece<D>;
+  constexpr int kPasses = kFewRows / P::kRows, kWarps = kThreads / 32;
+  extern __shared__ __align__(16) float s_trig[];      // [live rows][half] cosines, then sines
+  __shared__ long long s_at[kFewRows], s_block[kFewRows];  // a row's slot and scale in the caches; -1: no page
+  __shared__ unsigned s_top[kWarps][kChunk];           // a block's magnitude
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);
+
+  grid_dependency_wait();
+  if (blockIdx.x == 0) {
+    if (blockIdx.y == 0 && blockIdx.z == 0) check_all(p);
+    return;
+  }
+  const int pair_group = p.half > 0 ? tid / p.by_half : 0;
+  const int pair = tid - pair_group * p.half;
+  double freq = 0.0;
+  if (p.half > 0) freq = p.freqs[pair];
+  const int b = blockIdx.z;
+  const Rows rows = rows_of(p, span_of(p, b), blockIdx.x - 1);
+  if (rows.live <= 0) return;
+  for (int i = tid; i < kWarps * kChunk; i += kThreads) (&s_top[0][0])[i] = 0u;
+  prepare_rows(p, b, rows, freq, pair, pair_group, s_at, s_block, s_trig);
+  __syncthreads();
+
+  const int u = blockIdx.y * kWarps + warp;
+  if (u >= 2 * p.kv_heads + p.q_heads) return;
+  const int live = rows.live;
+  P my(p, lane);
+  const bool is_q = u >= 2 * p.kv_heads, is_v = !is_q && u >= p.kv_heads;
+  const int head = is_q ? u - 2 * p.kv_heads : is_v ? u - p.kv_heads : u;
+  const long long stride = is_q ? p.q_row : p.kv_row;
+  const uint16_t* src = (is_q ? p.q : is_v ? p.v_new : p.k_new) + rows.row0 * stride + static_cast<long long>(head) * D + my.piece * 8;
+  uint4 raw[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = i * P::kRows + my.sub;
+    raw[i] = r < live ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  auto value = [&](int i, int r, float (&x)[8]) {  // (rows behind the last look at the last's angles)
+    const int at = min(r, live - 1);
+    if (!is_v) my.look(s_trig + at * p.half, s_trig + (live + at) * p.half);
+    my.rotate(raw[i], !is_v, x);
+  };
+  const long long in_slot = head * p.head_stride + my.piece * 8;
+  if (is_q || p.block_log2 < 0) {
+    uint16_t* out = p.q_out + rows.row0 * p.q_out_row + static_cast<long long>(head) * D + my.piece * 8;
+    uint16_t* cache = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + in_slot;
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
-      const int r = row_of(i);
-      raw[i] = r < live ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0u, 0u, 0u, 0u);
+      if (i * P::kRows >= live) break;
+      const int r = i * P::kRows + my.sub;
+      float x[8];
+      value(i, r, x);
+      if (r < live && (is_q || s_at[r] >= 0))
+        *reinterpret_cast<uint4*>(is_q ? out + r * p.q_out_row : cache + s_at[r]) = is_v ? raw[i] : packed(x);
     }
-    if (is_q) {
-      uint16_t* dst = p.q_out + static_cast<long long>(row0) * p.q_out_row + static_cast<long long>(head) * D + piece * 8;
+    return;
+  }
+
+  // 8 bits: the magnitudes of the rows' blocks, then their scales and codes.
+  float* scales = (is_v ? p.v_scale : p.k_scale) + head * p.scale_head;
+  uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + in_slot;
+  const int held = rows.p0 & ((1 << p.block_log2) - 1);  // positions that the first row's block has already
+  const bool real0 = s_at[0] >= 0;
+  float was = 0.f;
+  if (held > 0 && real0) was = scales[s_block[0]];
+  unsigned* tops = s_top[warp];
+  auto block_of = [&](int r) { return (held + r) >> p.block_log2; };
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        if (i * TEAM * kRows >= live) break;
-        const int r = row_of(i);
-        float x[8];
-        rotate(raw[i], r, x);
-        if (r < live) *reinterpret_cast<uint4*>(dst + r * p.q_out_row) = packed(x);
+  for (int i = 0; i < kPasses; ++i) {
+    if (i * P::kRows >= live) break;
+    const int r = i * P::kRows + my.sub;
+    float x[8];
+    value(i, r, x);
+    float top = magnitude(x);
+#pragma unroll
+    for (int d = 1; d < P::kPieces; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+    if (my.piece == 0 && r < live) atomicMax(&tops[block_of(r)], __float_as_uint(top));
+  }
+  __syncwarp();
+  bool keeps;
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    if (i * P::kRows >= live) break;
+    const int r = i * P::kRows + my.sub;
+    float x[8];
+    value(i, r, x);
+    if (r >= live || s_at[r] < 0) continue;
+    magnitude(x);
+    const float scale = scale_for(tops[block_of(r)], held > 0 && block_of(r) == 0, was, keeps);
+    *reinterpret_cast<uint2*>(cache + s_at[r]) = coded(x, scale);
+    if (my.piece == 0 && !keeps && (r == 0 || block_of(r) != block_of(r - 1))) scales[s_block[r]] = scale;
+  }
+  if (held > 0 && real0) {
+    const float scale = scale_for(tops[0], true, was, keeps);
+    if (!keeps) {  // what the block has goes to the larger scale
+      for (int i = my.sub; i < held; i += P::kRows) {
+        uint2* at = reinterpret_cast<uint2*>(cache + s_at[0] - (held - i) * p.slot_stride);
+        *at = recoded(*at, was / scale);
       }
-      continue;
     }
-    const long long in_slot = head * p.head_stride + piece * 8;
+  }
+}
+
+// Prompts.  Queries, and keys and values of a bf16 cache, go row by row: a warp reads
+// a row's heads as they lie and writes them as they lie, its angles in registers.
+// Keys and values of an 8-bit cache go by blocks: a CTA takes 64 positions and, one
+// after another, heads of k and v, whose rows its 8 warps keep in registers between
+// the maximum that decides a block's scale and the codes.  Both at once, each on a
+// part of the CTAs.
+template <int D>
+__device__ void append_rows(const Params& p, int worker, int workers, float* trig) {
+  using P = Piece<D>;
+  constexpr int kBatch = 4;  // pieces of a lane at once
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kSteps = D / 64;  // pairs of a lane
+  unsigned long long step[kSteps];
+#pragma unroll
+  for (int i = 0; i < kSteps; ++i) step[i] = i * 32 + lane < p.half ? turn_step(p.freqs[i * 32 + lane]) : 0ull;
+  float* cosines = trig + warp * D;
+  float* sines = cosines + D / 2;
+  P my(p, lane);
+  const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
+  const long long all = static_cast<long long>(p.count) * p.max_new;
+  for (long long item = static_cast<long long>(worker) * (kThreads / 32) + warp; item < all;
+       item += static_cast<long long>(workers) * (kThreads / 32)) {
+    const int b = static_cast<int>(item / p.max_new), i_new = static_cast<int>(item - static_cast<long long>(b) * p.max_new);
+    const Span s = span_of(p, b);
+    const int pos = s.start + i_new;
+    if (!s.ok || i_new >= s.n || pos < 0) continue;
+    const long long row = s.first_row + i_new;
+    long long at = -1;
     if (p.block_log2 < 0) {
-      uint16_t* cache = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + in_slot;
+      const int page = pos / p.by_page, id = p.table[static_cast<long long>(b) * p.table_row + page];
+      if (id >= 0 && id < p.pages) at = id * p.page_stride + (pos - page * static_cast<int>(p.by_page.d)) * p.slot_stride;
+    }
+    auto source = [&](int h) {
+      return h < p.q_heads ? p.q + row * p.q_row + static_cast<long long>(h) * D
+                           : (h < p.q_heads + p.kv_heads ? p.k_new : p.v_new) + row * p.kv_row +
+                                 static_cast<long long>((h - p.q_heads) % p.by_kv) * D;
+    };
+    uint4 raw[kBatch], next[kBatch];
+    auto load = [&](int h0, uint4 (&to)[kBatch]) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * P::kRows + my.sub;
+        if (h < heads) to[i] = *(reinterpret_cast<const uint4*>(source(h)) + my.piece);
+      }
+    };
+    load(0, next);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      if (i * 32 + lane < p.half) {
+        const float2 v = turned(step[i], pos);
+        cosines[i * 32 + lane] = v.x;
+        sines[i * 32 + lane] = v.y;
+      }
+    }
+    __syncwarp();
+    my.look(cosines, sines);
+    for (int h0 = 0; h0 < heads; h0 += kBatch * P::kRows) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+      if (h0 + kBatch * P::kRows < heads) load(h0 + kBatch * P::kRows, next);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * P::kRows + my.sub;
+        const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
+        float x[8];
+        my.rotate(raw[i], !is_v, x);
+        if (h >= heads || (!is_q && at < 0)) continue;
+        const int kv = (h - p.q_heads) % p.by_kv;
+        uint16_t* to = is_q ? p.q_out + row * p.q_out_row + static_cast<long long>(h) * D
+                            : static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + at + kv * p.head_stride;
+        *(reinterpret_cast<uint4*>(to) + my.piece) = is_v ? raw[i] : packed(x);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_constant__ Params p) {
+  using P = Piece<D>;
+  constexpr int kWarps = kThreads / 32, kWarpRows = kChunk / kWarps;  // a warp's rows of a chunk, side by side
+  constexpr int kPasses = kWarpRows / P::kRows;
+  constexpr bool kAhead = D < 256;  // the next head's rows on their way (with 256 there are no registers for them)
+  extern __shared__ __align__(16) float s_trig[];      // [live rows][half] cosines, then sines; by rows: [warp][D]
+  __shared__ long long s_at[kChunk], s_block[kChunk];  // a row's slot and scale in the caches; -1: no page
+  __shared__ unsigned s_top[3][kChunk];                // a block's magnitude, of three heads in turn
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(~0u, tid >> 5, 0);
+
+  grid_dependency_wait();
+  if (blockIdx.x == 0) {
+    check_all(p);
+    return;
+  }
+  const int worker = static_cast<int>(blockIdx.x) - 1;
+  if (worker < p.row_workers) {
+    append_rows<D>(p, worker, p.row_workers, s_trig);
+    return;
+  }
+
+  const int pair_group = p.half > 0 ? tid / p.by_half : 0;
+  const int pair = tid - pair_group * p.half;
+  double freq = 0.0;
+  if (p.half > 0) freq = p.freqs[pair];
+  P my(p, lane);
+  // An equal share of all (sequence, chunk, head), in order, chunk by chunk.
+  const int units = 2 * p.kv_heads, workers = static_cast<int>(gridDim.x) - 1 - p.row_workers;
+  const long long all = static_cast<long long>(p.count) * p.chunks * units;
+  const long long end = all * (worker - p.row_workers + 1) / workers;
+  for (long long item = all * (worker - p.row_workers) / workers; item < end;) {
+    const long long which = item / units;
+    const int u_first = static_cast<int>(item - which * units);
+    const int u_end = static_cast<int>(min(static_cast<long long>(units), u_first + (end - item)));
+    item += u_end - u_first;
+    const int b = static_cast<int>(which / p.chunks), chunk = static_cast<int>(which - static_cast<long long>(b) * p.chunks);
+    const Rows rows = rows_of(p, span_of(p, b), chunk);
+    if (rows.live <= 0) continue;
+    __syncthreads();  // the last chunk's rows are done with
+    for (int i = tid; i < 3 * kChunk; i += kThreads) (&s_top[0][0])[i] = 0u;
+    prepare_rows(p, b, rows, freq, pair, pair_group, s_at, s_block, s_trig);
+    __syncthreads();
+
+    const int live = rows.live, lead = rows.p0 & (kChunk - 1);  // rows lie `lead` into the chunk
+    const int held = rows.p0 & ((1 << p.block_log2) - 1);       // positions that the first row's block has already
+    const bool real0 = s_at[0] >= 0;
+    const bool one = (1 << p.block_log2) >= kWarpRows;  // a warp's rows share a block
+    auto row_of = [&](int i) { return warp * kWarpRows + i * P::kRows + my.sub - lead; };  // among the live ones, or outside
+    auto block_of = [&](int r) { return (lead + r) >> p.block_log2; };
+    const int block0 = block_of(0);
+    uint4 ahead[kAhead ? kPasses : 1];
+    auto load = [&](int u, int i) {
+      const uint16_t* src = (u >= p.kv_heads ? p.v_new : p.k_new) + rows.row0 * p.kv_row +
+                            static_cast<long long>(u >= p.kv_heads ? u - p.kv_heads : u) * D + my.piece * 8;
+      const int r = row_of(i);
+      return r >= 0 && r < live ? *reinterpret_cast<const uint4*>(src + r * p.kv_row) : make_uint4(0u, 0u, 0u, 0u);
+    };
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) ahead[i] = load(u_first, i);
+    }
+    int turn = 0;
+    for (int u = u_first; u < u_end; ++u) {
+      const bool is_v = u >= p.kv_heads;
+      const int head = is_v ? u - p.kv_heads : u;
+      float* scales = (is_v ? p.v_scale : p.k_scale) + head * p.scale_head;
+      uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + head * p.head_stride + my.piece * 8;
+      float was = 0.f;
+      if (held > 0 && real0) was = scales[s_block[0]];
+      unsigned* tops = s_top[turn];
+      uint4 raw[kPasses];
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        if (i * TEAM * kRows >= live) break;
+        if constexpr (kAhead) raw[i] = ahead[i];
+        else raw[i] = load(u, i);
+      }
+      if constexpr (kAhead) {
+        if (u + 1 < u_end) {
+#pragma unroll
+          for (int i = 0; i < kPasses; ++i) ahead[i] = load(u + 1, i);
+        }
+      }
+      float x[kPasses][8], top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int r = row_of(i), look = min(max(r, 0), live - 1);
+        if (!is_v) my.look(s_trig + look * p.half, s_trig + (live + look) * p.half);
+        my.rotate(raw[i], !is_v, x[i]);
+        const float t = magnitude(x[i]);
+        top = one ? fmaxf(top, t) : t;
+        if (!one) {
+#pragma unroll
+          for (int d = 1; d < P::kPieces; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          if (my.piece == 0 && r >= 0 && r < live) atomicMax(&tops[block_of(r)], __float_as_uint(top));
+        }
+      }
+      if (one) {  // (rows outside are zeros)
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+        if (lane == 0) atomicMax(&tops[(warp * kWarpRows) >> p.block_log2], __float_as_uint(top));
+      }
+      __syncthreads();
+      if (tid < kChunk) s_top[turn == 0 ? 2 : turn - 1][tid] = 0u;  // the head's after the next: nobody looks there any more, nor yet
+      turn = turn == 2 ? 0 : turn + 1;
+      bool keeps;
+      float scale = 0.f;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
         const int r = row_of(i);
-        float x[8];
-        if (!is_v) rotate(raw[i], r, x);
-        if (r < live && s_at[r] >= 0) *reinterpret_cast<uint4*>(cache + s_at[r]) = is_v ? raw[i] : packed(x);
+        if (!one || i == 0) {
+          const int block = (warp * kWarpRows + (one ? 0 : i * P::kRows + my.sub)) >> p.block_log2;
+          scale = scale_for(tops[block], held > 0 && block == block0, was, keeps);
+        }
+        if (r < 0 || r >= live || s_at[r] < 0) continue;
+        *reinterpret_cast<uint2*>(cache + s_at[r]) = coded(x[i], scale);
+        if (my.piece == 0 && !keeps && (r == 0 || block_of(r) != block_of(r - 1))) scales[s_block[r]] = scale;
       }
-      continue;
-    }
-
-    // 8 bits: the magnitudes of the rows' blocks, then their scales and codes.
-    float* scales = (is_v ? p.v_scale : p.k_scale) + head * p.scale_head;
-    uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + in_slot;
-    const int held = p0 & ((1 << p.block_log2) - 1);  // positions that the first row's block has already
-    const bool real0 = s_at[0] >= 0;
-    float was = 0.f;
-    if (held > 0 && real0) was = scales[s_block[0]];
-    unsigned* tops = s_top[turn][team];
-    const int block0 = (p0 - c0) >> p.block_log2;
-    auto block_of = [&](int r) { return (p0 - c0 + r) >> p.block_log2; };
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (i * TEAM * kRows >= live) break;
-      const int r = row_of(i);
-      float x[8];
-      if (is_v) unpack(raw[i], x);
-      else rotate(raw[i], r, x);
-      float top = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a = fabsf(x[e]);
-        top = fmaxf(top, a < INFINITY ? a : 0.f);
-      }
-#pragma unroll
-      for (int d = 1; d < kPieces; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-      if (piece == 0 && r < live) atomicMax(&tops[block_of(r)], __float_as_uint(top));
-    }
-    if constexpr (TEAM == 1) __syncwarp();
-    else __syncthreads();
-    {  // the magnitudes of the head after the next: nobody looks at them any more, nor yet
-      unsigned* later = s_top[turn == 0 ? 2 : turn - 1][team];
-      for (int i = member * 32 + lane; i < kChunk; i += TEAM * 32) later[i] = 0u;
-    }
-    turn = turn == 2 ? 0 : turn + 1;
-    // The scale of a row's block, and what turns values into codes.
-    auto scale_for = [&](int block, bool& keeps) {
-      const uint32_t top = tops[block];
-      keeps = held > 0 && block == block0 && was > 0.f && __uint_as_float(top) <= kE4M3Max * was;
-      return keeps ? was : exp2_of(fresh_exponent(top));
-    };
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (i * TEAM * kRows >= live) break;
-      const int r = row_of(i);
-      float x[8];
-      if (is_v) unpack(raw[i], x);
-      else rotate(raw[i], r, x);
-      if (r >= live || s_at[r] < 0) continue;
-      bool keeps;
-      const float scale = scale_for(block_of(r), keeps);
-      // (a scale that another program set need not be a power of two)
-      const bool power = (__float_as_uint(scale) & 0x007FFFFFu) == 0u;
-      const float inverse = 1.f / scale;
-      uint32_t code[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float a = x[2 * e], d = x[2 * e + 1];
-        a = fabsf(a) < INFINITY ? (power ? a * inverse : a / scale) : NAN;
-        d = fabsf(d) < INFINITY ? (power ? d * inverse : d / scale) : NAN;
-        code[e] = to_e4m3x2(a, d);
-      }
-      *reinterpret_cast<uint2*>(cache + s_at[r]) = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-      const bool leads = r == 0 || block_of(r) != block_of(r - 1);
-      if (piece == 0 && leads && !keeps) scales[s_block[r]] = scale;
-    }
-    if (held > 0 && real0) {
-      bool keeps;
-      const float scale = scale_for(block0, keeps);
-      if (!keeps) {  // what the block has goes to the larger scale
-        const float factor = was / scale;
-        for (int i = (member * 32 + lane) / kPieces; i < held; i += TEAM * kRows) {
-          uint2* at = reinterpret_cast<uint2*>(cache + s_at[0] - (held - i) * p.slot_stride);
-          const uint2 old = *at;
-          uint32_t code[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t h = e4m3x2_to_half2(static_cast<uint16_t>((e < 2 ? old.x : old.y) >> (e & 1) * 16));
-            float a, d;
-            asm("{.reg .f16 l, h; mov.b32 {l, h}, %2; cvt.f32.f16 %0, l; cvt.f32.f16 %1, h;}" : "=f"(a), "=f"(d) : "r"(h));
-            code[e] = to_e4m3x2(a * factor, d * factor);
+      if (held > 0 && real0) {
+        scale = scale_for(tops[block0], true, was, keeps);
+        if (!keeps) {  // what the block has goes to the larger scale
+          for (int i = warp * P::kRows + my.sub; i < held; i += kWarps * P::kRows) {
+            uint2* at = reinterpret_cast<uint2*>(cache + s_at[0] - (held - i) * p.slot_stride);
+            *at = recoded(*at, was / scale);
           }
-          *at = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
         }
       }
     }
@@ -396,28 +625,27 @@ int check(const w4g128_append_args* a) {
   return W4G128_OK;
 }
 
-template <int D, int TEAM>
-cudaError_t launch(cudaLaunchConfig_t& cfg, const Params& p) {
-  const int most = TEAM == 1 ? kFewRows : kChunk;
-  cfg.dynamicSmemBytes = static_cast<size_t>(2 * most) * p.half * sizeof(float);
-  const cudaError_t e = cudaFuncSetAttribute(append_kernel<D, TEAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             2 * kChunk * (D / 2) * static_cast<int>(sizeof(float)));
-  if (e != cudaSuccess) return e;
-  const int units = 2 * p.kv_heads + p.q_heads;
-  const int chunks = (p.max_new + kChunk - 2) / kChunk + 1;  // that the new rows may touch
-  int slices = (units + 7) / 8;
-  if (TEAM > 1) {
-    const long long ctas = static_cast<long long>(chunks) * p.count;
-    slices = static_cast<int>(std::min<long long>(units, std::max<long long>(1, (608 + ctas - 1) / ctas)));
-  }
-  cfg.gridDim = dim3(chunks + 1, slices, p.count);  // (the last chunk's first CTA looks for errors)
-  cfg.blockDim = dim3(kThreads);
-  return cudaLaunchKernelEx(&cfg, append_kernel<D, TEAM>, p);
-}
-
 template <int D>
-cudaError_t launch_dim(cudaLaunchConfig_t& cfg, const Params& p) {
-  return p.max_new <= kFewRows ? launch<D, 1>(cfg, p) : launch<D, kThreads / 32>(cfg, p);
+cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
+  p.chunks = (p.max_new + kChunk - 2) / kChunk + 1;
+  cfg.blockDim = dim3(kThreads);
+  if (p.max_new <= kFewRows) {
+    const int units = 2 * p.kv_heads + p.q_heads;
+    cfg.gridDim = dim3(p.chunks + 1, (units + kThreads / 32 - 1) / (kThreads / 32), p.count);  // (the first CTA looks for errors)
+    cfg.dynamicSmemBytes = static_cast<size_t>(2 * kFewRows) * p.half * sizeof(float);
+    return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, p);
+  }
+  const int most = 2 * kChunk * (D / 2) * static_cast<int>(sizeof(float));
+  const cudaError_t e = cudaFuncSetAttribute(append_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (e != cudaSuccess) return e;
+  // Two CTAs an SM and the one that looks for errors, shared out by the values that are read.
+  const long long row_work = p.block_log2 < 0 ? p.q_heads + 2 * p.kv_heads : p.q_heads;
+  const long long block_work = p.block_log2 < 0 ? 0 : 2 * p.kv_heads;
+  p.row_workers = static_cast<int>(std::min<long long>(block_work ? kWorkers - 1 : kWorkers,
+                                                       (kWorkers * row_work + row_work + 2 * block_work - 1) / (row_work + 2 * block_work)));
+  cfg.gridDim = dim3(1 + kWorkers);
+  cfg.dynamicSmemBytes = std::max<size_t>(static_cast<size_t>(2 * kChunk) * p.half, kThreads / 32 * D) * sizeof(float);
+  return cudaLaunchKernelEx(&cfg, append_many_kernel<D>, p);
 }
 
 }  // namespace
@@ -452,6 +680,7 @@ int w4g128_append(const w4g128_append_args* a, void* ws, size_t ws_bytes, void* 
   for (int v = a->block; v > 0; v >>= 1) ++p.block_log2;
   p.by_page = divisor(a->page_size);
   p.by_half = divisor(std::max(p.half, 1));
+  p.by_kv = divisor(a->kv_heads);
   p.status = static_cast<unsigned long long*>(ws);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -460,8 +689,7 @@ int w4g128_append(const w4g128_append_args* a, void* ws, size_t ws_bytes, void* 
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = a->head_dim == 64 ? launch_dim<64>(cfg, p)
-                        : a->head_dim == 128 ? launch_dim<128>(cfg, p) : launch_dim<256>(cfg, p);
+  const cudaError_t e = a->head_dim == 64 ? launch<64>(cfg, p) : a->head_dim == 128 ? launch<128>(cfg, p) : launch<256>(cfg, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return W4G128_ERR_CUDA;

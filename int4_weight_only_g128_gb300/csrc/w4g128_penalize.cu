@@ -1,13 +1,15 @@
 // Penalties, biases and masks on logits (w4g128_penalize), in one launch.
 //
-// A row is a cluster of CTAs, each with a slice of the vocabulary and, in shared
-// memory, a word for each token of it: the times it occurs in the answer, and in
-// the top bit whether it occurs at all.  The history is read once, each CTA its
-// part, and counted where a token belongs by additions to the other CTA's shared
-// memory; whole numbers, so their order does not matter.  In the same way a list's
-// biases leave their places in the list, of which the largest stays.  Then each
-// CTA goes over its slice, 8 tokens a thread at a time; the logits and mask words
-// are on their way while the tokens are counted.
+// A row's vocabulary is cut into slices, a CTA each.  In shared memory a CTA has a
+// word for each of its tokens: the times it occurs in the answer, and in the top bit
+// whether it occurs at all.  Every CTA reads the whole history (from the L2: 131 KB
+// for 32771 tokens) and counts its own tokens by additions of whole numbers, whose
+// order does not matter.  (Each CTA its part of the history, counted where a token
+// belongs by additions to the shared memory of a cluster's CTAs, is four times
+// slower: the frequent tokens' additions wait for one another across the cluster.)
+// In the same way a list's biases leave their places in the list, of which the
+// largest stays.  Then the CTA goes over its slice, 8 tokens a thread at a time; the
+// logits and mask words are on their way while the tokens are counted.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -21,10 +23,11 @@ namespace w4g128 {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kAhead = 4;  // pieces of 8 logits that a thread asks for ahead
+constexpr int kAhead = 2;  // pieces of 8 logits that a thread asks for ahead
+constexpr int kBatch = 8;  // loads of 4 tokens on their way at once
 constexpr int kMostBias = 65535;
 constexpr uint32_t kSeen = 0x80000000u;
-constexpr int kMostCtas = 16;
+constexpr int kMostSlice = 16384;
 
 struct Params {
   const uint16_t* logits;
@@ -41,12 +44,6 @@ struct Params {
   int bias_size, vocab, slice;  // slice: tokens a CTA, a multiple of 8
 };
 
-__device__ __forceinline__ void cluster_add(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
-__device__ __forceinline__ void cluster_or(uint32_t a, uint32_t v) {
-  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
-}
 __device__ __forceinline__ float bf16_f(uint32_t v) { return __uint_as_float(v << 16); }
 __device__ __forceinline__ uint32_t f_bf16(float x) {
   uint16_t r;
@@ -57,7 +54,7 @@ __device__ __forceinline__ uint32_t f_bf16(float x) {
 __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) uint32_t s_words[];  // [slice] counts, if any; [slice] 16-bit places in the list, if any
   const int tid = threadIdx.x, row = blockIdx.y;
-  const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
+  const int rank = blockIdx.x;
   const bool may_count = p.history != nullptr, may_bias = p.bias_tokens != nullptr;
   uint32_t* counts = s_words;
   uint32_t* places = may_count ? s_words + p.slice : s_words;
@@ -66,7 +63,6 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
     for (int i = tid * 4; i < p.slice; i += kThreads * 4) *reinterpret_cast<uint4*>(counts + i) = make_uint4(0u, 0u, 0u, 0u);
   if (may_bias)
     for (int i = tid * 4; i < p.slice / 2; i += kThreads * 4) *reinterpret_cast<uint4*>(places + i) = make_uint4(0u, 0u, 0u, 0u);
-  if (may_count) cluster_arrive_release();  // a CTA runs and its words are 0 before another counts there
   grid_dependency_wait();
 
   // Pieces of 8 tokens start where the row's logits are 16-byte aligned.
@@ -118,18 +114,37 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
     begin += skip;
     len = min(len - skip, max(p.history_size - begin, 0ll));
     prompt -= skip;
-    cluster_wait_acquire();
-    const uint32_t base = smem_addr(counts);
-    for (long long i = rank * kThreads + tid; i < len; i += ctas * kThreads) {
-      const int t = p.history[begin + i];
-      if (t >= 0 && t < p.vocab) {
-        const int owner = (t + shift) / p.slice;
-        const uint32_t at = cluster_map(base + (t + shift - owner * p.slice) * 4, owner);
-        if (i < prompt) cluster_or(at, kSeen);
-        else cluster_add(at, 1u);
+    const int* tokens = p.history + begin;
+    const long long whole = min(len, static_cast<long long>((16u - (reinterpret_cast<uintptr_t>(tokens) & 15u)) / 4 & 3u));
+    __syncthreads();
+    auto count = [&](int t, long long i) {
+      const unsigned at = static_cast<unsigned>(t) - static_cast<unsigned>(first);
+      if (at < static_cast<unsigned>(p.slice) && t >= 0 && t < p.vocab) {
+        if (i < prompt) atomicOr(&counts[at], kSeen);
+        else atomicAdd(&counts[at], 1u);
+      }
+    };
+    if (tid < whole) count(tokens[tid], tid);  // up to a 16-byte boundary
+    const int4* four = reinterpret_cast<const int4*>(tokens + whole);
+    const long long quads = (len - whole) / 4;
+    for (long long q = tid; q < quads; q += kBatch * kThreads) {
+      int4 t[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (q + j * kThreads < quads) t[j] = four[q + j * kThreads];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (q + j * kThreads < quads) {
+          const long long i = whole + 4 * (q + j * kThreads);
+          count(t[j].x, i);
+          count(t[j].y, i + 1);
+          count(t[j].z, i + 2);
+          count(t[j].w, i + 3);
+        }
       }
     }
-    cluster_arrive_release();
+    const long long rest = whole + 4 * quads + tid;
+    if (rest < len) count(tokens[rest], rest);
   }
   int b0 = 0, listed = 0;
   if (may_bias) {  // each CTA looks for its own tokens
@@ -149,9 +164,8 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
         }
       }
     }
-    __syncthreads();
   }
-  if (may_count) cluster_wait_acquire();
+  if (may_count || may_bias) __syncthreads();
 
   auto finish = [&](int at, const uint4& v, uint32_t allowed) {
     const int t0 = first + at;
@@ -253,26 +267,20 @@ int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
   p.bias_values = a->bias_values; p.bias_offsets = a->bias_offsets; p.mask = a->mask;
   p.row_stride = a->row_stride; p.out_stride = a->out_stride; p.mask_row = a->mask_row; p.history_size = a->history_size;
   p.bias_size = a->bias_size; p.vocab = a->vocab;
-  const int ctas = kMostCtas;
-  p.slice = ((a->vocab + 7 + ctas - 1) / ctas + 7) / 8 * 8;
+  p.slice = 8192;
+  const int ctas = (a->vocab + 7 + p.slice - 1) / p.slice;
   const size_t shared = (p.history ? 4 : 0) * static_cast<size_t>(p.slice) + (p.bias_tokens ? 2 : 0) * static_cast<size_t>(p.slice);
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, a->rows);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = shared;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  const int most = 6 * (((W4G128_MAX_VOCAB + 7 + kMostCtas - 1) / kMostCtas + 7) / 8 * 8);
-  cudaError_t e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * kMostSlice);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, penalize_kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
