@@ -28,7 +28,7 @@ namespace {
 constexpr int kChunk = 64;  // positions, a multiple of every block
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
-constexpr int kWorkers = 303;  // CTAs of a prompt's call
+constexpr int kWorkers = 303;  // CTAs of a prompt's call: two an SM, but the one that looks for errors
 constexpr size_t kWorkspace = 256;
 constexpr int kLowestScale = -100;
 
@@ -43,7 +43,8 @@ struct Params {
   int rows, count, q_heads, kv_heads, half, interleaved, pages, block_log2, max_len, max_new;
   int chunks;       // that the new rows of a sequence may touch
   int row_workers;  // CTAs that work row by row
-  Divisor by_page, by_half, by_kv;
+  Divisor by_page, by_half, by_kv, by_new, by_parts;
+  unsigned row_items;  // parts of rows that are worked on one by one
   unsigned long long* status;
 };
 
@@ -142,7 +143,7 @@ struct Piece {
   static constexpr int kRows = 32 / kPieces;  // rows, or heads of a row, of a warp at once
   int sub, piece, first_pair, from;           // from: the lane with the other side of the pairs
   bool turns, second, interleaved;
-  float c[8], s[8];  // of its pairs (interleaved: 4)
+  float c[8], s[8];  // of its pairs (interleaved: 4; else the sine has the sign of this lane's side)
 
   __device__ __forceinline__ Piece(const Params& p, int lane) {
     sub = lane / kPieces;
@@ -165,6 +166,9 @@ struct Piece {
       c[4 * h] = x.x; c[4 * h + 1] = x.y; c[4 * h + 2] = x.z; c[4 * h + 3] = x.w;
       s[4 * h] = y.x; s[4 * h + 1] = y.y; s[4 * h + 2] = y.z; s[4 * h + 3] = y.w;
     }
+    if (interleaved || second) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] = -s[i];
   }
   // All lanes of the warp; only: whether this lane's piece is rotated at all.
   __device__ __forceinline__ void rotate(const uint4& raw, bool only, float (&x)[8]) const {
@@ -188,7 +192,7 @@ struct Piece {
     float y[8];
     unpack(other, y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = second ? fmaf(x[i], c[i], y[i] * s[i]) : fmaf(x[i], c[i], -(y[i] * s[i]));
+    for (int i = 0; i < 8; ++i) x[i] = fmaf(x[i], c[i], y[i] * s[i]);
   }
 };
 
@@ -383,10 +387,15 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_const
 // after another, heads of k and v, whose rows its 8 warps keep in registers between
 // the maximum that decides a block's scale and the codes.  Both at once, each on a
 // part of the CTAs.
+template <int N>
+__device__ __forceinline__ void cp_async_wait_group() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+constexpr int kRowBatch = 8;  // pieces of a lane at once: 8 heads of 256, 16 of 128, 32 of 64
 template <int D>
 __device__ void append_rows(const Params& p, int worker, int workers, float* trig) {
   using P = Piece<D>;
-  constexpr int kBatch = 4;  // pieces of a lane at once
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kSteps = D / 64;  // pairs of a lane
   unsigned long long step[kSteps];
@@ -396,71 +405,89 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
   float* sines = cosines + D / 2;
   P my(p, lane);
   const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
-  const long long all = static_cast<long long>(p.count) * p.max_new;
-  for (long long item = static_cast<long long>(worker) * (kThreads / 32) + warp; item < all;
-       item += static_cast<long long>(workers) * (kThreads / 32)) {
-    const int b = static_cast<int>(item / p.max_new), i_new = static_cast<int>(item - static_cast<long long>(b) * p.max_new);
-    const Span s = span_of(p, b);
-    const int pos = s.start + i_new;
-    if (!s.ok || i_new >= s.n || pos < 0) continue;
-    const long long row = s.first_row + i_new;
+  const unsigned all = p.row_items, stride = workers * kWarps;
+  struct Item {  // a part of a row's heads
+    bool real;
+    int b, pos, h0;
+    long long row;
+    uint4 raw[kRowBatch];
+  };
+  auto load = [&](unsigned item, Item& it) {
+    it.real = false;
+    if (item >= all) return;
+    const int which = static_cast<int>(item) / p.by_parts;
+    it.h0 = (static_cast<int>(item) - which * static_cast<int>(p.by_parts.d)) * kRowBatch * P::kRows + my.sub;
+    it.b = which / p.by_new;
+    const int i_new = which - it.b * p.max_new;
+    const Span s = span_of(p, it.b);
+    it.pos = s.start + i_new;
+    it.row = s.first_row + i_new;
+    it.real = s.ok && i_new < s.n && it.pos >= 0;
+    if (!it.real) return;
+#pragma unroll
+    for (int i = 0; i < kRowBatch; ++i) {
+      const int h = it.h0 + i * P::kRows;
+      const uint16_t* from = h < p.q_heads ? p.q + it.row * p.q_row + static_cast<long long>(h) * D
+                                           : (h < p.q_heads + p.kv_heads ? p.k_new : p.v_new) + it.row * p.kv_row +
+                                                 static_cast<long long>((h - p.q_heads) % p.by_kv) * D;
+      it.raw[i] = h < heads ? *(reinterpret_cast<const uint4*>(from) + my.piece) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  Item next;
+  load(worker * kWarps + warp, next);
+  for (unsigned item = worker * kWarps + warp; item < all; item += stride) {
+    const Item it = next;
+    load(item + stride, next);  // on its way while this one is worked on
+    if (!it.real) continue;
     long long at = -1;
     if (p.block_log2 < 0) {
-      const int page = pos / p.by_page, id = p.table[static_cast<long long>(b) * p.table_row + page];
-      if (id >= 0 && id < p.pages) at = id * p.page_stride + (pos - page * static_cast<int>(p.by_page.d)) * p.slot_stride;
+      const int page = it.pos / p.by_page, id = p.table[static_cast<long long>(it.b) * p.table_row + page];
+      if (id >= 0 && id < p.pages) at = id * p.page_stride + (it.pos - page * static_cast<int>(p.by_page.d)) * p.slot_stride;
     }
-    auto source = [&](int h) {
-      return h < p.q_heads ? p.q + row * p.q_row + static_cast<long long>(h) * D
-                           : (h < p.q_heads + p.kv_heads ? p.k_new : p.v_new) + row * p.kv_row +
-                                 static_cast<long long>((h - p.q_heads) % p.by_kv) * D;
-    };
-    uint4 raw[kBatch], next[kBatch];
-    auto load = [&](int h0, uint4 (&to)[kBatch]) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * P::kRows + my.sub;
-        if (h < heads) to[i] = *(reinterpret_cast<const uint4*>(source(h)) + my.piece);
-      }
-    };
-    load(0, next);
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (i * 32 + lane < p.half) {
-        const float2 v = turned(step[i], pos);
+        const float2 v = turned(step[i], it.pos);
         cosines[i * 32 + lane] = v.x;
         sines[i * 32 + lane] = v.y;
       }
     }
     __syncwarp();
     my.look(cosines, sines);
-    for (int h0 = 0; h0 < heads; h0 += kBatch * P::kRows) {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
-      if (h0 + kBatch * P::kRows < heads) load(h0 + kBatch * P::kRows, next);
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * P::kRows + my.sub;
-        const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
-        float x[8];
-        my.rotate(raw[i], !is_v, x);
-        if (h >= heads || (!is_q && at < 0)) continue;
-        const int kv = (h - p.q_heads) % p.by_kv;
-        uint16_t* to = is_q ? p.q_out + row * p.q_out_row + static_cast<long long>(h) * D
-                            : static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + at + kv * p.head_stride;
-        *(reinterpret_cast<uint4*>(to) + my.piece) = is_v ? raw[i] : packed(x);
-      }
+    for (int i = 0; i < kRowBatch; ++i) {
+      const int h = it.h0 + i * P::kRows;
+      const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
+      float x[8];
+      my.rotate(it.raw[i], !is_v, x);
+      if (h >= heads || (!is_q && at < 0)) continue;
+      const int kv = (h - p.q_heads) % p.by_kv;
+      uint16_t* to = is_q ? p.q_out + it.row * p.q_out_row + static_cast<long long>(h) * D
+                          : static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + at + kv * p.head_stride;
+      *(reinterpret_cast<uint4*>(to) + my.piece) = is_v ? it.raw[i] : packed(x);
     }
   }
 }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) append_rows_kernel(const __grid_constant__ Params p) {
+  __shared__ __align__(16) float s_trig[kThreads / 32 * D];
+  grid_dependency_wait();
+  if (blockIdx.x == 0) check_all(p);
+  else append_rows<D>(p, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1, s_trig);
+}
+
+template <int D>
+constexpr int kBlockStages = D == 256 ? 2 : 3;
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_constant__ Params p) {
   using P = Piece<D>;
   constexpr int kWarps = kThreads / 32, kWarpRows = kChunk / kWarps;  // a warp's rows of a chunk, side by side
   constexpr int kPasses = kWarpRows / P::kRows;
-  constexpr bool kAhead = D < 256;  // the next head's rows on their way (with 256 there are no registers for them)
-  extern __shared__ __align__(16) float s_trig[];      // [live rows][half] cosines, then sines; by rows: [warp][D]
+  constexpr int kStages = kBlockStages<D>;
+  extern __shared__ __align__(16) uint8_t s_many[];    // the stages; [live rows][half] cosines, then sines
   __shared__ long long s_at[kChunk], s_block[kChunk];  // a row's slot and scale in the caches; -1: no page
   __shared__ unsigned s_top[3][kChunk];                // a block's magnitude, of three heads in turn
   const int tid = threadIdx.x, lane = tid & 31;
@@ -473,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   }
   const int worker = static_cast<int>(blockIdx.x) - 1;
   if (worker < p.row_workers) {
-    append_rows<D>(p, worker, p.row_workers, s_trig);
+    append_rows<D>(p, worker, p.row_workers, reinterpret_cast<float*>(s_many));
     return;
   }
 
@@ -482,6 +509,8 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   double freq = 0.0;
   if (p.half > 0) freq = p.freqs[pair];
   P my(p, lane);
+  uint4* ring = reinterpret_cast<uint4*>(s_many) + tid;
+  float* s_trig = reinterpret_cast<float*>(s_many + kThreads * kPasses * kStages * 16);
   // An equal share of all (sequence, chunk, head), in order, chunk by chunk.
   const int units = 2 * p.kv_heads, workers = static_cast<int>(gridDim.x) - 1 - p.row_workers;
   const long long all = static_cast<long long>(p.count) * p.chunks * units;
@@ -506,17 +535,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
     auto row_of = [&](int i) { return warp * kWarpRows + i * P::kRows + my.sub - lead; };  // among the live ones, or outside
     auto block_of = [&](int r) { return (lead + r) >> p.block_log2; };
     const int block0 = block_of(0);
-    uint4 ahead[kAhead ? kPasses : 1];
-    auto load = [&](int u, int i) {
-      const uint16_t* src = (u >= p.kv_heads ? p.v_new : p.k_new) + rows.row0 * p.kv_row +
-                            static_cast<long long>(u >= p.kv_heads ? u - p.kv_heads : u) * D + my.piece * 8;
-      const int r = row_of(i);
-      return r >= 0 && r < live ? *reinterpret_cast<const uint4*>(src + r * p.kv_row) : make_uint4(0u, 0u, 0u, 0u);
-    };
-    if constexpr (kAhead) {
+    auto issue = [&](int u, int stage) {
+      if (u < u_end) {
+        const uint16_t* src = (u >= p.kv_heads ? p.v_new : p.k_new) + rows.row0 * p.kv_row +
+                              static_cast<long long>(u >= p.kv_heads ? u - p.kv_heads : u) * D + my.piece * 8;
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) ahead[i] = load(u_first, i);
-    }
+        for (int i = 0; i < kPasses; ++i) {
+          const int r = row_of(i);
+          if (r >= 0 && r < live) cp_async16(smem_addr(ring + (stage * kPasses + i) * kThreads), src + r * p.kv_row);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < kStages - 1; ++i) issue(u_first + i, i);
+    int stage = 0;
     int turn = 0;
     for (int u = u_first; u < u_end; ++u) {
       const bool is_v = u >= p.kv_heads;
@@ -526,24 +559,15 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
       float was = 0.f;
       if (held > 0 && real0) was = scales[s_block[0]];
       unsigned* tops = s_top[turn];
-      uint4 raw[kPasses];
-#pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        if constexpr (kAhead) raw[i] = ahead[i];
-        else raw[i] = load(u, i);
-      }
-      if constexpr (kAhead) {
-        if (u + 1 < u_end) {
-#pragma unroll
-          for (int i = 0; i < kPasses; ++i) ahead[i] = load(u + 1, i);
-        }
-      }
+      issue(u + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
+      cp_async_wait_group<kStages - 1>();
       float x[kPasses][8], top = 0.f;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const int r = row_of(i), look = min(max(r, 0), live - 1);
         if (!is_v) my.look(s_trig + look * p.half, s_trig + (live + look) * p.half);
-        my.rotate(raw[i], !is_v, x[i]);
+        const uint4 raw = r >= 0 && r < live ? ring[(stage * kPasses + i) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+        my.rotate(raw, !is_v, x[i]);
         const float t = magnitude(x[i]);
         top = one ? fmaxf(top, t) : t;
         if (!one) {
@@ -557,6 +581,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
         for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
         if (lane == 0) atomicMax(&tops[(warp * kWarpRows) >> p.block_log2], __float_as_uint(top));
       }
+      stage = stage + 1 == kStages ? 0 : stage + 1;
       __syncthreads();
       if (tid < kChunk) s_top[turn == 0 ? 2 : turn - 1][tid] = 0u;  // the head's after the next: nobody looks there any more, nor yet
       turn = turn == 2 ? 0 : turn + 1;
@@ -635,16 +660,26 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
     cfg.dynamicSmemBytes = static_cast<size_t>(2 * kFewRows) * p.half * sizeof(float);
     return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, p);
   }
-  const int most = 2 * kChunk * (D / 2) * static_cast<int>(sizeof(float));
+  // Row by row: a part of a row's heads at a time, while their number fits.
+  constexpr int kHeads = kRowBatch * Piece<D>::kRows;
+  const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
+  const long long rows = static_cast<long long>(p.count) * p.max_new, parts = std::max(1, (heads + kHeads - 1) / kHeads);
+  p.by_new = divisor(p.max_new);
+  p.by_parts = divisor(rows * parts < (1ll << 30) ? static_cast<int>(parts) : 1);
+  p.row_items = heads == 0 ? 0 : static_cast<unsigned>(rows * p.by_parts.d);
+  if (p.block_log2 < 0) {
+    cfg.gridDim = dim3(1 + kWorkers);
+    return cudaLaunchKernelEx(&cfg, append_rows_kernel<D>, p);
+  }
+  const int stages = kChunk * D * 2 * kBlockStages<D>;
+  const int most = stages + kChunk * D * static_cast<int>(sizeof(float));
   const cudaError_t e = cudaFuncSetAttribute(append_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  // Two CTAs an SM and the one that looks for errors, shared out by the values that are read.
-  const long long row_work = p.block_log2 < 0 ? p.q_heads + 2 * p.kv_heads : p.q_heads;
-  const long long block_work = p.block_log2 < 0 ? 0 : 2 * p.kv_heads;
-  p.row_workers = static_cast<int>(std::min<long long>(block_work ? kWorkers - 1 : kWorkers,
-                                                       (kWorkers * row_work + row_work + 2 * block_work - 1) / (row_work + 2 * block_work)));
+  // A value of k or v costs three times a query's.
+  const long long kv_work = 3 * 2 * p.kv_heads;
+  p.row_workers = p.q_heads == 0 ? 0 : static_cast<int>(std::min<long long>(kWorkers - 1, 1 + kWorkers * p.q_heads * 2 / (2 * p.q_heads + kv_work)));
   cfg.gridDim = dim3(1 + kWorkers);
-  cfg.dynamicSmemBytes = std::max<size_t>(static_cast<size_t>(2 * kChunk) * p.half, kThreads / 32 * D) * sizeof(float);
+  cfg.dynamicSmemBytes = stages + 2 * kChunk * p.half * static_cast<int>(sizeof(float));
   return cudaLaunchKernelEx(&cfg, append_many_kernel<D>, p);
 }
 
