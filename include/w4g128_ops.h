@@ -356,7 +356,7 @@ typedef struct {
   w4g128_bf16* out;          /* row r at out + r * out_stride; may be logits, with the same stride */
   const int* history;        /* [history_size], or NULL: no histories */
   const long long* history_start; /* [rows], or NULL: 0 */
-  const int* history_len;    /* [rows]; not above 0: none.  NULL with history NULL alone */
+  const int* history_len;    /* [rows], up to 2^30; not above 0: none.  NULL with history NULL alone */
   const int* prompt_len;     /* [rows], or NULL: 0 */
   const float* repetition;   /* [rows] above 0, or NULL: 1 */
   const float* presence;     /* [rows], or NULL: 0 */

@@ -5,11 +5,13 @@
 // whether it occurs at all.  Every CTA reads the whole history (from the L2: 131 KB
 // for 32771 tokens) and counts its own tokens by additions of whole numbers, whose
 // order does not matter.  (Each CTA its part of the history, counted where a token
-// belongs by additions to the shared memory of a cluster's CTAs, is four times
-// slower: the frequent tokens' additions wait for one another across the cluster.)
-// In the same way a list's biases leave their places in the list, of which the
-// largest stays.  Then the CTA goes over its slice, 8 tokens a thread at a time; the
-// logits and mask words are on their way while the tokens are counted.
+// belongs by additions to the shared memory of a cluster's CTAs, took three times as
+// long, 19.8 us: the frequent tokens' additions wait for one another across the
+// cluster.)  In the same way a list's biases leave their places in the list, of which
+// the largest stays.  Then the CTA goes over its slice, 8 tokens a thread at a time;
+// the logits and mask words are on their way while the tokens are counted.  A chain of
+// loads (settings, history) bounds one row; 16 rows of 248320 with 4099 tokens and
+// 300 biases take 11.6 us, 4.7 of them without counting (the bytes are 2.4).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -22,12 +24,12 @@
 namespace w4g128 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kAhead = 2;  // pieces of 8 logits that a thread asks for ahead
-constexpr int kBatch = 8;  // loads of 4 tokens on their way at once
+constexpr int kBatch = 2;  // loads of 4 tokens on their way at once
+constexpr int kMostHistory = 1 << 30;
+constexpr int kNear = 512;
 constexpr int kMostBias = 65535;
 constexpr uint32_t kSeen = 0x80000000u;
-constexpr int kMostSlice = 16384;
+constexpr int kMostSlice = 8192;
 
 struct Params {
   const uint16_t* logits;
@@ -51,7 +53,10 @@ __device__ __forceinline__ uint32_t f_bf16(float x) {
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constant__ Params p) {
+template <int T>
+__global__ void __launch_bounds__(T) penalize_kernel(const __grid_constant__ Params p) {
+  constexpr int kAhead = 8192 / 8 / T;  // pieces of 8 logits that a thread asks for ahead
+  __shared__ float s_bias[kNear];       // a list's first values
   extern __shared__ __align__(16) uint32_t s_words[];  // [slice] counts, if any; [slice] 16-bit places in the list, if any
   const int tid = threadIdx.x, row = blockIdx.y;
   const int rank = blockIdx.x;
@@ -60,9 +65,9 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   uint32_t* places = may_count ? s_words + p.slice : s_words;
 
   if (may_count)
-    for (int i = tid * 4; i < p.slice; i += kThreads * 4) *reinterpret_cast<uint4*>(counts + i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid * 4; i < p.slice; i += T * 4) *reinterpret_cast<uint4*>(counts + i) = make_uint4(0u, 0u, 0u, 0u);
   if (may_bias)
-    for (int i = tid * 4; i < p.slice / 2; i += kThreads * 4) *reinterpret_cast<uint4*>(places + i) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = tid * 4; i < p.slice / 2; i += T * 4) *reinterpret_cast<uint4*>(places + i) = make_uint4(0u, 0u, 0u, 0u);
   grid_dependency_wait();
 
   // Pieces of 8 tokens start where the row's logits are 16-byte aligned.
@@ -97,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    const int at = (i * kThreads + tid) * 8;
+    const int at = (i * T + tid) * 8;
     if (at < p.slice && first + at < p.vocab) load(first + at, ahead[i], allowed_ahead[i]);
   }
 
@@ -105,57 +110,71 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   if (p.repetition != nullptr) repetition = p.repetition[row];
   if (p.presence != nullptr) presence = p.presence[row];
   if (p.frequency != nullptr) frequency = p.frequency[row];
+  const float inverse = 1.f / repetition;
+  int b0 = 0, listed = 0, listed_token = -1;
+  float listed_value = 0.f;
+  if (may_bias) {  // this thread's first entry, on its way while the history is counted
+    b0 = max(p.bias_offsets[row], 0);
+    listed = min(max(min(p.bias_offsets[row + 1], p.bias_size) - b0, 0), kMostBias);
+    if (tid < listed) {
+      listed_token = p.bias_tokens[b0 + tid];
+      listed_value = p.bias_values[b0 + tid];
+    }
+  }
   if (may_count) {
     long long begin = p.history_start != nullptr ? p.history_start[row] : 0;
-    long long len = max(p.history_len[row], 0);
-    long long prompt = p.prompt_len != nullptr ? p.prompt_len[row] : 0;
+    const int given = min(max(p.history_len[row], 0), kMostHistory);
+    int prompt = p.prompt_len != nullptr ? p.prompt_len[row] : 0;
     // (what lies outside the buffer is not read)
-    const long long skip = begin >= 0 ? 0 : begin < -len ? len : -begin;
+    const int skip = begin >= 0 ? 0 : begin < -given ? given : static_cast<int>(-begin);
     begin += skip;
-    len = min(len - skip, max(p.history_size - begin, 0ll));
-    prompt -= skip;
+    const int len = static_cast<int>(min(static_cast<long long>(given - skip), max(p.history_size - begin, 0ll)));
+    prompt = prompt > skip ? prompt - skip : 0;
     const int* tokens = p.history + begin;
-    const long long whole = min(len, static_cast<long long>((16u - (reinterpret_cast<uintptr_t>(tokens) & 15u)) / 4 & 3u));
+    const int whole = min(len, static_cast<int>((16u - (reinterpret_cast<uintptr_t>(tokens) & 15u)) / 4 & 3u));
+    // (a place before the row's first token, for a token below 0, is never written out)
+    const unsigned mine = static_cast<unsigned>(max(min(p.slice, p.vocab - first), 0));  // (the last slice may lie behind)
     __syncthreads();
-    auto count = [&](int t, long long i) {
+    auto count = [&](int t, bool asked) {
       const unsigned at = static_cast<unsigned>(t) - static_cast<unsigned>(first);
-      if (at < static_cast<unsigned>(p.slice) && t >= 0 && t < p.vocab) {
-        if (i < prompt) atomicOr(&counts[at], kSeen);
+      if (at < mine) {
+        if (asked) atomicOr(&counts[at], kSeen);
         else atomicAdd(&counts[at], 1u);
       }
     };
-    if (tid < whole) count(tokens[tid], tid);  // up to a 16-byte boundary
+    if (tid < whole) count(tokens[tid], tid < prompt);  // up to a 16-byte boundary
     const int4* four = reinterpret_cast<const int4*>(tokens + whole);
-    const long long quads = (len - whole) / 4;
-    for (long long q = tid; q < quads; q += kBatch * kThreads) {
+    const int quads = (len - whole) / 4;
+    for (int q0 = tid & ~31; q0 < quads; q0 += kBatch * T) {
       int4 t[kBatch];
 #pragma unroll
-      for (int j = 0; j < kBatch; ++j)
-        if (q + j * kThreads < quads) t[j] = four[q + j * kThreads];
+      for (int j = 0; j < kBatch; ++j) {
+        if (q0 + j * T >= quads) break;  // (of the warp)
+        const int q = q0 + j * T + (tid & 31);
+        t[j] = q < quads ? __ldg(four + q) : make_int4(-8, -8, -8, -8);
+      }
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
-        if (q + j * kThreads < quads) {
-          const long long i = whole + 4 * (q + j * kThreads);
-          count(t[j].x, i);
-          count(t[j].y, i + 1);
-          count(t[j].z, i + 2);
-          count(t[j].w, i + 3);
-        }
+        if (q0 + j * T >= quads) break;
+        const int left = prompt - whole - 4 * (q0 + j * T + (tid & 31));  // of the prompt, from here on
+        count(t[j].x, left > 0);
+        count(t[j].y, left > 1);
+        count(t[j].z, left > 2);
+        count(t[j].w, left > 3);
       }
     }
-    const long long rest = whole + 4 * quads + tid;
-    if (rest < len) count(tokens[rest], rest);
+    const int rest = whole + 4 * quads + tid;
+    if (rest < len) count(tokens[rest], rest < prompt);
   }
-  int b0 = 0, listed = 0;
   if (may_bias) {  // each CTA looks for its own tokens
-    __syncthreads();
-    b0 = max(p.bias_offsets[row], 0);
-    listed = min(max(min(p.bias_offsets[row + 1], p.bias_size) - b0, 0), kMostBias);
-    for (int i = tid; i < listed; i += kThreads) {
-      const int t = p.bias_tokens[b0 + i], at = t - first;
-      if (t >= 0 && t < p.vocab && at >= 0 && at < p.slice) {
+    if (!may_count) __syncthreads();
+    for (int i = tid; i < listed; i += T) {
+      const int t = i == tid ? listed_token : p.bias_tokens[b0 + i];
+      const unsigned at = static_cast<unsigned>(t) - static_cast<unsigned>(first);
+      if (i < kNear) s_bias[i] = i == tid ? listed_value : p.bias_values[b0 + i];
+      if (t >= 0 && t < p.vocab && at < static_cast<unsigned>(p.slice)) {
         uint32_t* word = places + at / 2;
-        const int up = (at & 1) * 16;
+        const unsigned up = (at & 1u) * 16u;
         uint32_t seen = *word;
         while (((seen >> up) & 0xFFFFu) < static_cast<uint32_t>(i + 1)) {
           const uint32_t prev = atomicCAS(word, seen, (seen & ~(0xFFFFu << up)) | static_cast<uint32_t>(i + 1) << up);
@@ -170,39 +189,44 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   auto finish = [&](int at, const uint4& v, uint32_t allowed) {
     const int t0 = first + at;
     uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t c[8] = {}, place[4] = {};
-    bool plain = allowed == 0xFFu;
+    uint32_t c[8] = {}, place[4] = {}, counted = 0u, placed = 0u;
     if (may_count) {
       const uint4 a = *reinterpret_cast<const uint4*>(counts + at), b = *reinterpret_cast<const uint4*>(counts + at + 4);
       c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
       c[4] = b.x; c[5] = b.y; c[6] = b.z; c[7] = b.w;
-      plain = plain && (a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w) == 0u;
+      counted = a.x | a.y | a.z | a.w | b.x | b.y | b.z | b.w;
     }
     if (may_bias) {
       const uint4 a = *reinterpret_cast<const uint4*>(places + at / 2);
       place[0] = a.x; place[1] = a.y; place[2] = a.z; place[3] = a.w;
-      plain = plain && (a.x | a.y | a.z | a.w) == 0u;
+      placed = a.x | a.y | a.z | a.w;
     }
-    if (!plain) {
+    if ((counted | placed) != 0u) {  // few pieces have a token of the history or of the list
+      float z[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int up = (e & 1) * 16;
-        const uint32_t where = (place[e / 2] >> up) & 0xFFFFu;
-        uint32_t bits = (w[e / 2] >> up) & 0xFFFFu;
-        if ((allowed >> e & 1u) == 0u) {
-          bits = 0xFF80u;  // -inf
-        } else if (c[e] != 0u || where != 0u) {
-          float z = bf16_f(bits);
-          if (c[e] != 0u) z = z > 0.f ? z / repetition : z * repetition;
-          const uint32_t times = c[e] & ~kSeen;
-          if (times != 0u) {
-            z = __fsub_rn(z, __fmul_rn(frequency, static_cast<float>(times)));
-            z = __fsub_rn(z, presence);
-          }
-          if (where != 0u) z = __fadd_rn(z, p.bias_values[b0 + static_cast<int>(where) - 1]);
-          bits = f_bf16(z);
+        z[e] = bf16_f((w[e / 2] >> (e & 1) * 16) & 0xFFFFu);
+        const float times = static_cast<float>(c[e] & ~kSeen);
+        float x = z[e] * (z[e] > 0.f ? inverse : repetition);
+        x = __fsub_rn(x, __fmul_rn(frequency, times));
+        x = __fsub_rn(x, times > 0.f ? presence : 0.f);
+        if (c[e] != 0u) z[e] = x;
+      }
+      if (placed != 0u) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t where = (place[e / 2] >> (e & 1) * 16) & 0xFFFFu;
+          if (where != 0u) z[e] = __fadd_rn(z[e], where <= kNear ? s_bias[where - 1] : p.bias_values[b0 + static_cast<int>(where) - 1]);
         }
-        w[e / 2] = (w[e / 2] & ~(0xFFFFu << up)) | bits << up;
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f_bf16(z[2 * e]) | f_bf16(z[2 * e + 1]) << 16;
+    }
+    if (allowed != 0xFFu) {  // -inf
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t keep = ((allowed >> 2 * e & 1u) ? 0x0000FFFFu : 0u) | ((allowed >> 2 * e & 2u) ? 0xFFFF0000u : 0u);
+        w[e] = (w[e] & keep) | (0xFF80FF80u & ~keep);
       }
     }
     if (out_whole && t0 >= 0 && t0 + 8 <= p.vocab) {
@@ -215,10 +239,10 @@ __global__ void __launch_bounds__(kThreads) penalize_kernel(const __grid_constan
   };
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) {
-    const int at = (i * kThreads + tid) * 8;
+    const int at = (i * T + tid) * 8;
     if (at < p.slice && first + at < p.vocab) finish(at, ahead[i], allowed_ahead[i]);
   }
-  for (int at = (kAhead * kThreads + tid) * 8; at < p.slice && first + at < p.vocab; at += kThreads * 8) {
+  for (int at = (kAhead * T + tid) * 8; at < p.slice && first + at < p.vocab; at += T * 8) {
     uint4 v;
     uint32_t allowed;
     load(first + at, v, allowed);
@@ -267,21 +291,27 @@ int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
   p.bias_values = a->bias_values; p.bias_offsets = a->bias_offsets; p.mask = a->mask;
   p.row_stride = a->row_stride; p.out_stride = a->out_stride; p.mask_row = a->mask_row; p.history_size = a->history_size;
   p.bias_size = a->bias_size; p.vocab = a->vocab;
-  p.slice = 8192;
+  // Slices of 8192 tokens, or of 2048 where that makes no more CTAs than two an SM (one
+  // row of 32000: 3.5 us, and 4.3 with 8192; 16 rows of 248320: 11.6, and 26 with 2048).
+  // Long histories take more threads (one row with 32771 tokens: 6.1 us, 9.0 with 512;
+  // with 613 tokens 4.0 and 3.8, 16 rows with 4099 16.2 and 11.6).
+  p.slice = static_cast<long long>(a->rows) * ((a->vocab + 7 + 2047) / 2048) <= 304 ? 2048 : kMostSlice;
   const int ctas = (a->vocab + 7 + p.slice - 1) / p.slice;
+  const bool wide = a->history_size / a->rows > 8192;
   const size_t shared = (p.history ? 4 : 0) * static_cast<size_t>(p.slice) + (p.bias_tokens ? 2 : 0) * static_cast<size_t>(p.slice);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, a->rows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(wide ? 1024 : 512);
   cfg.dynamicSmemBytes = shared;
   cfg.stream = static_cast<cudaStream_t>(stream);
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaFuncSetAttribute(penalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * kMostSlice);
-  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, penalize_kernel, p);
+  const auto kernel = wide ? penalize_kernel<1024> : penalize_kernel<512>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * kMostSlice);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, kernel, p);
   if (e != cudaSuccess) {
     cudaGetLastError();
     return W4G128_ERR_CUDA;

@@ -1,6 +1,7 @@
 """Penalties, biases and masks on logits (w4g128_penalize) against the formulas
-in 64 bits.  Each of the five fp32 operations is off by at most 2^-24 of its
-result, which is no larger than the sum of the terms' magnitudes; the output
+in 64 bits.  Each of the six fp32 operations (a division is a product with the
+inverse) is off by at most 2^-24 of its result, which is no larger than the sum of
+the terms' magnitudes; the output
 rounds once, 2^-8 of the value (of 2^-133 at least, bf16's smallest step)."""
 import pytest
 
@@ -93,7 +94,7 @@ class Call:
                 bits = (self.mask[r][:, None] >> torch.arange(32, device="cuda", dtype=torch.int32)) & 1
                 z = torch.where(bits.flatten()[:V] == 0, -float("inf"), z)
             out[r] = z
-            tol[r] = 2.0 ** -8 * z.abs() + 5 * 2.0 ** -24 * size * 1.01 + 2.0 ** -134
+            tol[r] = 2.0 ** -8 * z.abs() + 6 * 2.0 ** -24 * size * 1.01 + 2.0 ** -134
         return out, tol
 
     def check(self, without=(), **kw):
