@@ -448,6 +448,7 @@ attend8_kernel(const __grid_constant__ Params p) {
   for (int i = 0; i < 4; ++i) q_at[i] = smem_addr(smem) + (rw * MT * 16 + lj) * 2 * D + (((2 * i + lp) ^ (lj & 7)) << 4);
   const int last_pos = s.len - 1;  // of the sequence's last row
   const int turns = (total + NT - 1) / NT;
+  float log_top = kNone;  // of the tiles so far, the largest value scale (base 2)
   int stage = 0;
 #pragma unroll 1
   for (int turn = 0; turn < turns; ++turn) {
@@ -573,17 +574,20 @@ attend8_kernel(const __grid_constant__ Params p) {
             ref[m][side] = now;
           }
       }
+      // (the rounded score less the reference, which is a rounded score: the largest weight is 2^kLift, however large they are)
+      auto exponent = [&](int m, int h, int i) {
+        return sc[t][m][h][i] + (ref[m][i >> 1] == kNone ? 0.f : kLift - ref[m][i >> 1]);
+      };
       float least = INFINITY;
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        const float ra = ref[m][0] == kNone ? 0.f : kLift - ref[m][0], rb = ref[m][1] == kNone ? 0.f : kLift - ref[m][1];
         float wt[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            wt[h][i] = exp2_fast(sc[t][m][h][i] + (i < 2 ? ra : rb));
-            least = fminf(least, wt[h][i]);
+            wt[h][i] = exp2_fast(exponent(m, h, i));
+            if constexpr (!ONE) least = fminf(least, wt[h][i]);
           }
           pf[t][m][2 * h] = pack_half(wt[h][0], wt[h][1]);
           pf[t][m][2 * h + 1] = pack_half(wt[h][2], wt[h][3]);
@@ -597,32 +601,37 @@ attend8_kernel(const __grid_constant__ Params p) {
           l[m][side] = fmaf(l[m][side], gain[t][m][side], add);
         }
       }
-      // Beside values of much larger scales, P may be below fp32's range and the weight not.
-      // (Most of what is below it is masked, and no weight at all.)
-      bool low = least < kLowWeight;
-      if (low && !inside[t]) {
-        low = false;
+      // Beside values of scales 2^60 times as large and more, P may be below fp32's
+      // range and the weight not.  (Where it is below it without that, the weight is
+      // below 2^-60 of the row's sum, whose bits it does not reach.)
+      bool low;
+      if constexpr (ONE) {
+        log_top = fmaxf(log_top, log_v[t][0]);
+        low = log_top - log_v[t][0] > 60.f;
+      } else {
+        low = least < kLowWeight;
+        if (low && !inside[t]) {  // most of it is masked
+          low = false;
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) low = low || (sc[t][m][h][i] > kNone && sc[t][m][h][i] - ref[m][i >> 1] < -100.f);
+        }
+        low = __any_sync(~0u, low);
+      }
+      if (low) {
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) low = low || (sc[t][m][h][i] > kNone && sc[t][m][h][i] - ref[m][i >> 1] < -100.f);
-      }
-      if (__any_sync(~0u, low)) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const float ra = ref[m][0] == kNone ? 0.f : kLift - ref[m][0], rb = ref[m][1] == kNone ? 0.f : kLift - ref[m][1];
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
             for (int i = 0; i < 4; ++i) {
               const int e = ONE ? 0 : h * 2 + (i & 1);
-              const float x = sc[t][m][h][i] + (i < 2 ? ra : rb);
-              const float w = exp2_fast(x);
+              const float x = exponent(m, h, i), w = exp2_fast(x);
               if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[t][e]) - w * inverse[t][e];
             }
-        }
       }
     }
 
