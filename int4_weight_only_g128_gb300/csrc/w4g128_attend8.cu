@@ -49,6 +49,7 @@ constexpr float kLowestScale = 0x1p-80f;  // of a value: smaller ones count as t
 constexpr float kLowWeight = 0x1p-120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
+constexpr int kMostChunk = 128;  // tiles
 
 struct Params {
   const uint16_t* q;
@@ -59,6 +60,7 @@ struct Params {
   long long q_row, out_row, page_stride, slot_stride, head_stride, scale_page, scale_head, table_row;
   int rows, count, q_heads, kv_heads, group, pages, block_log2, max_len, max_new, window, sinks;
   int clusters, row_groups;  // of a sequence and head
+  int chunk;                 // tiles of one CTA, where a sequence is cut into chunks; or 0
   Divisor by_group, by_page, by_clusters, by_row_groups, by_kv_heads;
   float scale2;              // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
   uint32_t flip_q, keep_q;
@@ -258,8 +260,9 @@ attend8_kernel(const __grid_constant__ Params p) {
   const int b = up / p.by_kv_heads;
   const int head = up - b * p.kv_heads;
 
-  const int groups = p.clusters * ctas * S::kKg;  // of this head and sequence
-  const int mine = (cl * ctas + rank) * S::kKg + kg;
+  // All groups of this head and sequence take tiles in turn, or those of a CTA the tiles of a chunk.
+  const int groups = p.chunk > 0 ? S::kKg : p.clusters * ctas * S::kKg;
+  const int mine = p.chunk > 0 ? cl * p.chunk + kg : (cl * ctas + rank) * S::kKg + kg;
   const int* table = p.table + static_cast<long long>(b) * p.table_row;
   // Without a window the first tiles are known before the length is: their page
   // ids come along with it, a tile a lane.
@@ -270,7 +273,7 @@ attend8_kernel(const __grid_constant__ Params p) {
   }
   const Seq s = sequence(p, b);
   const int live_rows = s.n * p.group;
-  if (!s.ok || rg * S::kRows >= live_rows) {
+  if (!s.ok || rg * S::kRows >= live_rows || (p.chunk > 0 && cl > 0 && cl * p.chunk * kTile >= s.len)) {
     if (ctas > 1) cluster_wait_acquire();
     return;
   }
@@ -301,7 +304,9 @@ attend8_kernel(const __grid_constant__ Params p) {
   }
 
   // This group's tiles: every groups-th, of the sinks' and then of the others.
-  const int sink_tiles = (s.sink + kTile - 1) / kTile, end_tile = (s.len + kTile - 1) / kTile;
+  const int sink_tiles = (s.sink + kTile - 1) / kTile;
+  int end_tile = (s.len + kTile - 1) / kTile;
+  if (p.chunk > 0) end_tile = min(end_tile, (cl + 1) * p.chunk);
   const int low_tile = max(s.lo / kTile, sink_tiles);
   int of_sinks = 0, low = mine;
   if (p.window > 0) {
@@ -820,12 +825,13 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
   load(warp);
   const Seq s = sequence(p, b);
   if (!s.ok || i >= s.n) return;
+  const int parts = p.chunk > 0 ? max(1, (s.len + p.chunk * kTile - 1) / (p.chunk * kTile)) : p.clusters;  // (chunks alive)
   float top = kNone, l = 0.f, sum[kPer] = {};
-  for (int z = warp; z < p.clusters; z += kWarps * kBatch) {
+  for (int z = warp; z < parts; z += kWarps * kBatch) {
     if (z > warp) load(z);
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
-      if (z + kWarps * j < p.clusters) {
+      if (z + kWarps * j < parts) {
         const float next = fmaxf(top, st[j].x), ref = next == kNone ? 0.f : next;
         const float old = exp2_fast(top - ref), w = exp2_fast(st[j].x - ref);
         top = next;
@@ -860,16 +866,8 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
       pack_bf16(x * inv, y * inv);
 }
 
-// CTAs of a cluster, and clusters, of one sequence and head.  Not by max_new: a
-// row's sums are the same whatever rows are beside it.  As many CTAs as the GPU holds
-// of those for 32 rows (64 with heads of 256, 16 registers' worth of warps fewer):
-// 32771 on 8 heads of 128: 25.4 us with 303, 31.0 with 607, 33.3 with 151; 16 ragged
-// sequences on 4 heads of 64: 24.6 with 455, 28.3 with 607, 30.4 with 303; windows of
-// 4096 on 2 x 4 heads of 256: 21.4 with 151, 30.1 with 303.  Calls of few CTAs are
-// joined in a cluster (one sequence of 611 on 8 heads: 5.6 us, and 6.3 with a second
-// kernel); of larger ones the clusters do not fill the GPU.
 struct Split {
-  int ctas, clusters;
+  int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; tiles of a chunk, or 0
 };
 Split split_for(const w4g128_attend8_args& a) {
   long long span = a.max_len;
@@ -878,8 +876,13 @@ Split split_for(const w4g128_attend8_args& a) {
   const long long tiles = (span + kTile - 1) / kTile, groups = groups_of(a.head_dim);
   const long long target = a.head_dim == 64 ? 455 : a.head_dim == 128 ? 303 : 151;
   const long long want = std::min(std::max<long long>(1, target / pairs), (tiles + groups - 1) / groups);
-  if (want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1};
-  return {1, static_cast<int>(want)};
+  if (want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1, 0};
+  if (a.count > 1 && a.window == 0) {
+    const long long some = target * 3 / 2;
+    const long long chunk = std::min<long long>(kMostChunk, (tiles * pairs + some * groups - 1) / (some * groups) * groups);
+    return {1, static_cast<int>((tiles + chunk - 1) / chunk), static_cast<int>(chunk)};
+  }
+  return {1, static_cast<int>(want), 0};
 }
 
 int check(const w4g128_attend8_args* a) {
@@ -983,6 +986,7 @@ int w4g128_attend8(const w4g128_attend8_args* a, void* ws, size_t ws_bytes, void
   for (int v = a->block; v > 0; v >>= 1) ++p.block_log2;
   p.window = a->window; p.sinks = a->sinks;
   p.clusters = split.clusters;
+  p.chunk = split.chunk;
   p.by_clusters = divisor(split.clusters);
   p.by_kv_heads = divisor(a->kv_heads);
   p.by_group = divisor(p.group);
