@@ -49,7 +49,7 @@ constexpr float kLowestScale = 0x1p-80f;  // of a value: smaller ones count as t
 constexpr float kLowWeight = 0x1p-120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
-constexpr int kMostChunk = 32;  // blocks of tiles
+constexpr int kMostChunk = 128;  // tiles
 
 struct Params {
   const uint16_t* q;
@@ -60,8 +60,7 @@ struct Params {
   long long q_row, out_row, page_stride, slot_stride, head_stride, scale_page, scale_head, table_row;
   int rows, count, q_heads, kv_heads, group, pages, block_log2, max_len, max_new, window, sinks;
   int clusters, row_groups;  // of a sequence and head
-  int chunk;                 // blocks of one CTA, where a sequence is cut into chunks; or 0
-  int span;                  // and their positions
+  int chunk;                 // tiles of one CTA, where a sequence is cut into chunks; or 0
   Divisor by_group, by_page, by_clusters, by_row_groups, by_kv_heads;
   float scale2;              // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
   uint32_t flip_q, keep_q;
@@ -99,7 +98,6 @@ __device__ __forceinline__ bool visible(const Params& p, int row_pos, int pos) {
 __device__ void check_all(const Params& p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int parts = max(1, warps / p.count);  // warps that share a sequence
-  constexpr int kBatch = 8;
   bool bad = false;
   for (int b = warp / parts; b < p.count; b += warps / parts) {
     const Seq s = sequence(p, b);
@@ -108,16 +106,9 @@ __device__ void check_all(const Params& p) {
     const int sink_pages = (s.sink + static_cast<int>(p.by_page.d) - 1) / p.by_page;
     const int end = s.len > 0 ? (s.len - 1) / p.by_page + 1 : 0;
     const int low = max(s.lo / p.by_page, sink_pages), all = sink_pages + end - low;
-    const int* table = p.table + static_cast<long long>(b) * p.table_row;
-    for (int i = (warp % parts) * 32 + lane; i < all; i += kBatch * parts * 32) {  // (many on their way at once)
-      int id[kBatch];
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const int at = i + j * parts * 32;
-        id[j] = at < all ? table[at < sink_pages ? at : low + at - sink_pages] : 0;
-      }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) bad |= id[j] < 0 || id[j] >= p.pages;
+    for (int i = (warp % parts) * 32 + lane; i < all; i += parts * 32) {
+      const int id = p.table[static_cast<long long>(b) * p.table_row + (i < sink_pages ? i : low + i - sink_pages)];
+      bad |= id < 0 || id >= p.pages;
     }
   }
   if (__syncthreads_or(bad)) bad = true;
@@ -202,62 +193,63 @@ struct Joined {
   __device__ __forceinline__ float2 stat() const { return make_float2(top, l); }
 };
 
-// A CTA's warps take a tile of positions each for Q K^T and the softmax, and a part of
-// the columns each for P V.
-constexpr int warps_of(int head_dim) { return head_dim == 256 ? 8 : 4; }
-template <int D, int RT>  // RT row tiles of 16
+// KG groups of warps with tiles of their own; RT row tiles, MT of them a warp; NT tiles
+// of positions a turn.  What fills a warp's schedule is several products at once:
+// two row tiles that share K's and V's fragments, or two tiles of positions.
+constexpr int groups_of(int head_dim) { return head_dim == 256 ? 2 : 4; }
+template <int D, int RT>
 struct Shape {
-  static constexpr int kWarps = warps_of(D);
-  static constexpr int kThreads = kWarps * 32;
-  static constexpr int kCols = D / kWarps;  // columns of a warp
+  static constexpr int kKg = groups_of(D);
+  static constexpr int kMt = D == 256 || RT == 1 ? 1 : 2;
+  static constexpr int kNt = D < 256 && RT == 1 ? 2 : 1;
+  static constexpr int kGroup = RT / kMt * 32;  // threads of a group
+  static constexpr int kThreads = kKg * kGroup;
+  // warps an SM, by the registers of a thread's sums: 128 of them leave room for 8, 64 for 12, 32 for 16
+  static constexpr int kSums = kMt * D / 2;
+  static constexpr int kWarps = kSums == 128 ? 8 : kSums == 64 ? 12 : 16;
+  static constexpr int kCtas = kWarps * 32 / kThreads > 0 ? kWarps * 32 / kThreads : 1;
   static constexpr int kRows = RT * 16;
-  static constexpr int kTileBytes = kTile * D;                      // K or V of one tile
-  static constexpr int kTileStage = 2 * kTileBytes + 2 * kTile * 4;  // both, and their positions' scales
-  static constexpr int kStageBytes = kWarps * kTileStage;
+  static constexpr int kTileBytes = kTile * D;  // K or V of one tile
+  static constexpr int kStageBytes = kNt * (2 * kTileBytes + 2 * kTile * 4);  // and their positions' scales
   static constexpr int kQBytes = kRows * 2 * D;
-  static constexpr int kPBytes = 2 * kWarps * RT * 512;  // the weights of two turns, as fragments
-  static constexpr int kFixed = kQBytes + kPBytes;
-  // CTAs an SM: by registers (4 warps of up to 96, 128 and 168), and by room for two stages
-  static constexpr int kByRegisters = (RT == 1 ? 5 : RT == 2 ? 4 : 3) * 4 / kWarps;
-  static constexpr int kByRoom = 227 * 1024 / (kFixed + 2 * kStageBytes + 4096);
-  static constexpr int kCtas = kByRegisters < kByRoom ? kByRegisters : kByRoom;
-  static constexpr int kRoom = (227 * 1024 / kCtas - 4096 - kFixed) / kStageBytes;
-  static constexpr int kStages = kRoom < 4 ? kRoom : 4;
-  static constexpr int kBytes = kFixed + kStages * kStageBytes;
+  static constexpr int kRoom = (227 * 1024 / kCtas - 1536 - kQBytes) / kKg / kStageBytes;
+  static constexpr int kStages = kRoom < 6 ? kRoom : 6;
+  static constexpr int kRing = kKg * kStages * kStageBytes;
+  static constexpr int kSumRow = D + 16;     // floats of a row's sums (free of bank conflicts)
+  static constexpr int kLeft = kRows * (kSumRow + 2) * 4;  // a group's sums, references and sums of weights
+  static constexpr int kBytes = kQBytes + kRing > kKg * kLeft ? kQBytes + kRing : kKg * kLeft;
   // what a cluster's CTAs send to one another
   static constexpr int received(int ctas) { return (kRows + ctas - 1) / ctas * ctas * (D + 2) * 4; }
-  static constexpr int kMostReceived = (kRows + kMostCluster - 1) * (D + 2) * 4;
-  static constexpr bool kApart = D < 256;  // in a place of its own, or, where there is no room, in that of the stages
-  static_assert((kApart ? kBytes + kMostReceived : kBytes) + 4096 <= 227 * 1024 && (kApart || kMostReceived <= kBytes), "room");
-  static_assert(kCtas >= 1 && kStages >= 2, "a stage on its way while another is read");
+  static constexpr int kMostBytes = kBytes + (kRows + kMostCluster - 1) * (D + 2) * 4;
+  static_assert(kMostBytes + 512 <= 227 * 1024, "room for what a cluster's CTAs send");
+  static_assert(kStages >= 2, "a stage on its way while another is read");
 };
 
 template <int D, int RT, bool ONE>  // ONE: a scale for each tile at most (blocks of 16 and more)
 __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtas)
 attend8_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, RT>;
-  constexpr int W = S::kWarps;
+  constexpr int MT = S::kMt, NT = S::kNt;
   constexpr int kSteps = D / 16;   // of Q K^T
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
-  constexpr int kPer = 2 * kTile * kPieces / 32;  // pieces of a tile's K and V that a lane copies
-  constexpr int kStep = 32 / kPieces;             // rows between them
-  constexpr int kScales = 2 * S::kTileBytes;      // a tile's scales
+  constexpr int kPer = 2 * kTile * kPieces / S::kGroup;  // pieces of a tile's K and V that one thread copies
+  constexpr int kStep = S::kGroup / kPieces;             // rows between them
+  constexpr int kScales = NT * 2 * S::kTileBytes;        // a stage's scales
+  static_assert(S::kGroup % kPieces == 0 && 2 * kTile % kStep == 0, "a thread copies one column of pieces");
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_factor[S::kRows];    // a row's score factor
-  __shared__ float s_row[W][S::kRows];    // what the warps tell one another of a row
-  __shared__ int s_flags[2][W];           // of a turn's tiles: there; seen whole by every row
-  __shared__ float s_log[2][W];           // and, with one scale, log2 of their values'
+  __shared__ float s_factor[S::kRows];  // a row's score factor
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
+  const int kg = warp / (RT / MT), rw = warp % (RT / MT);  // this warp's rows: rw MT 16 ..
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
   const int cluster = static_cast<int>(blockIdx.x) / ctas;
 
-  if (S::kApart && ctas > 1) cluster_arrive_relaxed();  // a CTA runs before another sends it sums
+  if (ctas > 1) cluster_arrive_relaxed();  // a CTA runs before another sends it sums
   grid_dependency_wait();
   if (cluster == 0) {
     if (rank == 0) check_all(p);
-    if (S::kApart && ctas > 1) cluster_wait_acquire();
+    if (ctas > 1) cluster_wait_acquire();
     return;
   }
   // cluster - 1 = ((b kv_heads + head) row_groups + rg) clusters + cl
@@ -268,32 +260,32 @@ attend8_kernel(const __grid_constant__ Params p) {
   const int b = up / p.by_kv_heads;
   const int head = up - b * p.kv_heads;
 
-  // A sequence's tiles, W at a time (a block), go to the CTAs of this head in turn, or
-  // a chunk of them to a CTA.
-  const int step = p.chunk > 0 ? 1 : p.clusters * ctas;
-  const int start = p.chunk > 0 ? cl * p.chunk : cl * ctas + rank;
+  // All groups of this head and sequence take tiles in turn, or those of a CTA the tiles of a chunk.
+  const int groups = p.chunk > 0 ? S::kKg : p.clusters * ctas * S::kKg;
+  const int mine = p.chunk > 0 ? cl * p.chunk + kg : (cl * ctas + rank) * S::kKg + kg;
   const int* table = p.table + static_cast<long long>(b) * p.table_row;
   // Without a window the first tiles are known before the length is: their page
-  // ids come along with it, a turn's a lane.
+  // ids come along with it, a tile a lane.
   int ids = -1, ids_next = -1;
   if (p.window == 0) {
-    const int a = ((start + lane * step) * W + warp) * kTile;
+    const int a = (mine + lane * groups) * kTile;
     if (a < p.max_len) ids = table[a / p.by_page];
   }
   const Seq s = sequence(p, b);
   const int live_rows = s.n * p.group;
-  if (!s.ok || rg * S::kRows >= live_rows || (p.chunk > 0 && cl > 0 && start * W * kTile >= s.len)) {
-    if (S::kApart && ctas > 1) cluster_wait_acquire();
+  if (!s.ok || rg * S::kRows >= live_rows || (p.chunk > 0 && cl > 0 && cl * p.chunk * kTile >= s.len)) {
+    if (ctas > 1) cluster_wait_acquire();
     return;
   }
 
   // Q, asked for before the table is waited for.
   const int r = lane >> 2, c = lane & 3;
-  const int row_0 = rg * S::kRows;     // the CTA's first row
-  int pos_a[RT], pos_b[RT];            // the positions of rows r and r + 8
+  const int row_w = rg * S::kRows + rw * MT * 16;  // the warp's first row
+  const bool busy = row_w < live_rows;             // (of the warp)
+  int pos_a[MT], pos_b[MT];                        // the positions of rows r and r + 8
 #pragma unroll
-  for (int m = 0; m < RT; ++m) {
-    const int row = row_0 + m * 16 + r;
+  for (int m = 0; m < MT; ++m) {
+    const int row = row_w + m * 16 + r;
     pos_a[m] = row < live_rows ? s.start + row / p.by_group : -1;
     pos_b[m] = row + 8 < live_rows ? s.start + (row + 8) / p.by_group : -1;
   }
@@ -302,7 +294,7 @@ attend8_kernel(const __grid_constant__ Params p) {
   uint4 q_part[kQPer] = {};
 #pragma unroll
   for (int e = 0; e < kQPer; ++e) {
-    const int i = tid + e * S::kThreads, row = row_0 + i / (D / 8);
+    const int i = tid + e * S::kThreads, row = rg * S::kRows + i / (D / 8);
     if (row < live_rows) {
       const int at = row / p.by_group;
       q_part[e] = __ldg(reinterpret_cast<const uint4*>(p.q + static_cast<long long>(s.first_row + at) * p.q_row +
@@ -311,80 +303,91 @@ attend8_kernel(const __grid_constant__ Params p) {
     }
   }
 
-  // This CTA's blocks: every step-th, of the sinks' and then of the others.
-  const int sink_tiles = (s.sink + kTile - 1) / kTile, low_tile = s.lo / kTile, end_tile = (s.len + kTile - 1) / kTile;
-  int end_block = (end_tile + W - 1) / W, of_sinks = 0, low = start;
-  if (p.chunk > 0) end_block = min(end_block, start + p.chunk);
+  // This group's tiles: every groups-th, of the sinks' and then of the others.
+  const int sink_tiles = (s.sink + kTile - 1) / kTile;
+  int end_tile = (s.len + kTile - 1) / kTile;
+  if (p.chunk > 0) end_tile = min(end_tile, (cl + 1) * p.chunk);
+  const int low_tile = max(s.lo / kTile, sink_tiles);
+  int of_sinks = 0, low = mine;
   if (p.window > 0) {
-    const int sink_blocks = (sink_tiles + W - 1) / W, low_block = max(low_tile / W, sink_blocks);
-    of_sinks = start < sink_blocks ? (sink_blocks - 1 - start) / step + 1 : 0;
-    if (start < low_block) low = start + (low_block - start + step - 1) / step * step;
+    of_sinks = mine < sink_tiles ? (sink_tiles - 1 - mine) / groups + 1 : 0;
+    if (mine < low_tile) low = mine + (low_tile - mine + groups - 1) / groups * groups;
   }
-  const int turns = of_sinks + (low < end_block ? (end_block - 1 - low) / step + 1 : 0);
-  auto block_of = [&](int k) { return k < of_sinks ? start + k * step : low + (k - of_sinks) * step; };
-  auto needed = [&](int tile) { return tile < end_tile && (tile < sink_tiles || tile >= low_tile); };
-  auto ids_from = [&](int k) {
-    const int tile = block_of(k) * W + warp;
-    return k < turns && needed(tile) ? table[tile * kTile / p.by_page] : -1;
-  };
-  if (p.window == 0) ids = lane < turns && needed(block_of(lane) * W + warp) ? ids : -1;
+  const int total = of_sinks + (low < end_tile ? (end_tile - 1 - low) / groups + 1 : 0);
+  auto tile_of = [&](int k) { return k < of_sinks ? mine + k * groups : low + (k - of_sinks) * groups; };
+  auto ids_from = [&](int k) { return k < total ? table[tile_of(k) * kTile / p.by_page] : -1; };
+  if (p.window == 0) ids = lane < total ? ids : -1;
   else ids = ids_from(lane);
-  if (turns > 32) ids_next = ids_from(32 + lane);
-  // Of 32 turns, one a lane: where this warp's tile's codes and scales are, -1 where that is no page.
+  if (total > 32) ids_next = ids_from(32 + lane);
+  // Of 32 tiles, one a lane: where its codes and scales are, -1 where that is no page.
   long long codes_at, scales_at;
   auto locate = [&](int k) {
-    const int a = (block_of(k) * W + warp) * kTile, slot = a - a / p.by_page * static_cast<int>(p.by_page.d);
-    const bool ok = ids >= 0 && ids < p.pages;
+    const int a = tile_of(k) * kTile, slot = a - a / p.by_page * static_cast<int>(p.by_page.d);
+    const bool ok = k < total && ids >= 0 && ids < p.pages;
     codes_at = ok ? ids * p.page_stride + slot * p.slot_stride : -1;
     scales_at = ids * p.scale_page + (slot >> p.block_log2);
   };
   locate(lane);
 
-  uint4* p_frags = reinterpret_cast<uint4*>(smem + S::kQBytes);  // [turn & 1][warp][row tile][lane]
-  uint8_t* ring = smem + S::kFixed;
+  uint8_t* ring = smem + S::kQBytes + kg * S::kStages * S::kStageBytes;
+  const uint32_t ring_at = smem_addr(ring);
+  auto group_sync = [&] {
+    if constexpr (S::kGroup == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(kg + 1), "n"(S::kGroup) : "memory");
+  };
   auto swizzled = [](int j, int piece) { return j * D + ((piece ^ (D == 64 ? (j >> 1) & 3 : j & 7)) << 4); };
 
-  // A lane copies one column of pieces of its warp's tile: rows j0, j0 + kStep, .. of K, then of V.
-  const int ch = lane % kPieces, j0 = lane / kPieces;
-  const uint8_t* k_base = p.k_cache + head * p.head_stride + ch * 16 + j0 * p.slot_stride;
+  // A thread copies one column of pieces: rows j0, j0 + kStep, .. of K, then of V.
+  const int gl = rw * 32 + lane;
+  const int ch = gl % kPieces, j0 = gl / kPieces;
+  const uint8_t* k_base = p.k_cache + head * p.head_stride + ch * 16;
   const long long v_off = p.v_cache - p.k_cache;
-  // (a tile begins a block of slots or lies in one: its position j is in the block j / block after its first)
-  const float* scale_base = ((lane & 16) ? p.v_scale : p.k_scale) + head * p.scale_head + ((lane & 15) >> p.block_log2);
+  // (a tile begins a block or lies in one: its position j is in the block j / block after its first)
+  const float* scale_base = ((gl & 16) ? p.v_scale : p.k_scale) + head * p.scale_head + ((gl & 15) >> p.block_log2);
   const long long row_step = kStep * p.slot_stride;
-  const uint32_t own_at = smem_addr(ring) + warp * S::kTileStage;
-  uint32_t okays = 0u;  // of the turns on their way, by their number mod 32: this warp's tile is there
-  auto issue = [&](int k, int stage) {
-    if (k < turns) {
-      if (k > 0 && (k & 31) == 0) {
-        ids = ids_next;
-        ids_next = ids_from(k + 32 + lane);
-        locate(k + lane);
-      }
-      const int a = (block_of(k) * W + warp) * kTile;
-      const long long codes = __shfl_sync(~0u, codes_at, k & 31), scales = __shfl_sync(~0u, scales_at, k & 31);
-      const bool ok = codes >= 0;
-      okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
-      const uint32_t dst = own_at + stage * S::kStageBytes;
-      const uint8_t* src = k_base + codes;
-      if (ok && a + kTile <= s.len) {  // a whole tile
+  const long long first_row = j0 % kTile * p.slot_stride + (j0 >= kTile ? v_off : 0);
+  uint32_t okays = 0u;  // of the tiles on their way, by their number mod 32: on a page
+  auto issue = [&](int turn, int stage) {
+    if (turn * NT < total) {
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-          const int jj = j0 + e * kStep;
-          if (e * kStep == kTile) src += v_off - kTile * p.slot_stride;
-          cp_async16(dst + (e * kStep >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
-          src += row_step;
+      for (int t = 0; t < NT; ++t) {
+        const int k = turn * NT + t;
+        if (t == 0 && k > 0 && (k & 31) == 0) {
+          ids = ids_next;
+          ids_next = ids_from(k + 32 + lane);
+          locate(k + lane);
         }
-        cp_async4(dst + kScales + lane * 4, scale_base + scales);
-      } else if (ok) {  // zeros behind the end
+        const int a = tile_of(k) * kTile;
+        const long long codes = __shfl_sync(~0u, codes_at, k & 31), scales = __shfl_sync(~0u, scales_at, k & 31);
+        const bool ok = codes >= 0;
+        okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
+        const uint32_t dst = ring_at + stage * S::kStageBytes + t * 2 * S::kTileBytes;
+        const uint32_t scale_dst = ring_at + stage * S::kStageBytes + kScales + (t * 32 + gl) * 4;
+        const uint8_t* src = k_base + (ok ? codes : 0);
+        if (ok && a + kTile <= s.len) {  // a whole tile
+          src += first_row;
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) {
+            const int jj = j0 + e * kStep;
+            if (e * kStep == kTile) src += v_off - kTile * p.slot_stride;
+            cp_async16(dst + (jj >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
+            src += row_step;
+          }
+          if (gl < 32) cp_async4(scale_dst, scale_base + scales);
+        } else {  // zeros behind the end, and for what is no page
 #pragma unroll 1
-        for (int e = 0; e < kPer; ++e) {
-          const int j = (j0 + e * kStep) % kTile;
-          const bool is_v = e * kStep >= kTile, real = a + j < s.len;
-          cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
-                             real ? src + (is_v ? v_off : 0) + (j - j0) * p.slot_stride : p.k_cache, real);
+          for (int e = 0; e < kPer; ++e) {
+            const int jj = j0 + e * kStep, j = jj % kTile;
+            const bool is_v = jj >= kTile, real = ok && a + j < s.len;
+            cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
+                               real ? src + (is_v ? v_off : 0) + j * p.slot_stride : p.k_cache, real);
+          }
+          if (gl < 32) {
+            const int j = gl & 15;
+            const bool real = ok && a + j < s.len;
+            cp_async4_or_zero(scale_dst, real ? scale_base + scales : p.k_scale, real);
+          }
         }
-        const bool real = a + (lane & 15) < s.len;
-        cp_async4_or_zero(dst + kScales + lane * 4, real ? scale_base + scales : p.k_scale, real);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -422,84 +425,102 @@ attend8_kernel(const __grid_constant__ Params p) {
   }
   __syncthreads();
 
-  float factor[RT][2], ref[RT][2], l[RT][2];  // of rows r and r + 8: all warps have the same references
-  float acc[RT][S::kCols / 8][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
+  float factor[MT][2];
+  float acc[MT][D / 8][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
+  float ref[MT][2], l[MT][2];
 #pragma unroll
-  for (int m = 0; m < RT; ++m) {
+  for (int m = 0; m < MT; ++m) {
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      factor[m][side] = s_factor[m * 16 + r + 8 * side];
+      factor[m][side] = s_factor[(rw * MT + m) * 16 + r + 8 * side];
       ref[m][side] = kNone;
       l[m][side] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < S::kCols / 8; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+    for (int i = 0; i < D / 8; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
   }
 
-  // ldmatrix: this lane's row and its pieces 2 i + lane / 16 (the pieces from 8 on 128
-  // bytes further), in a tile of K and in a row tile of Q; in V the pieces of this
-  // warp's columns, two of a tile, or one of a tile and of the next.
+  // ldmatrix: this lane's row and its pieces 2 i + lane / 16, in a tile of K or V and
+  // in a row tile of Q (the pieces from 8 on 128 bytes further).
   const int lj = lane & 15, lp = lane >> 4;
   constexpr int kAt = kPieces / 2 < 4 ? kPieces / 2 : 4;
-  uint32_t at[kAt], q_at[4];
+  uint32_t at[kAt];
 #pragma unroll
   for (int i = 0; i < kAt; ++i) at[i] = swizzled(lj, 2 * i + lp);
+  auto piece_at = [&](int i) { return at[i % kAt] + i / kAt * 128; };
+  uint32_t q_at[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q_at[i] = smem_addr(smem) + lj * 2 * D + (((2 * i + lp) ^ (lj & 7)) << 4);
-  const uint32_t v_at = smem_addr(ring) + S::kTileBytes +
-                        (S::kCols == 32 ? swizzled(lj, 2 * warp + lp) : lp * S::kTileStage + swizzled(lj, warp));
+  for (int i = 0; i < 4; ++i) q_at[i] = smem_addr(smem) + (rw * MT * 16 + lj) * 2 * D + (((2 * i + lp) ^ (lj & 7)) << 4);
   const int last_pos = s.len - 1;  // of the sequence's last row
+  const int turns = (total + NT - 1) / NT;
   float log_top = kNone;  // of the tiles so far, the largest value scale (base 2)
   int stage = 0;
 #pragma unroll 1
   for (int turn = 0; turn < turns; ++turn) {
     cp_async_wait_group<S::kStages - 2>();
-    __syncwarp();  // this warp's tile is there
-    const int buffer = turn & 1, block = block_of(turn), a = (block * W + warp) * kTile;
-    const bool there = (okays >> (turn & 31)) & 1u;
-    // every row sees the whole tile
-    auto whole = [&](int pos) {
-      return s.start >= 0 && pos + kTile - 1 <= s.first && (p.window == 0 || last_pos - pos < p.window || pos + kTile <= p.sinks);
-    };
-    constexpr int kOwn = ONE ? 1 : 4;  // scales of this lane's positions 2 c, 2 c + 1, + 8
-    float sc[RT][2][4], log_v[kOwn], inverse[kOwn], top[RT][2];
-    bool above = false;
-    if (there) {
-      const uint32_t tile = own_at + stage * S::kStageBytes;
+    group_sync();  // the tiles are there for the group, and the stage refilled next is read out
+    issue(turn + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
+    const uint32_t tile = ring_at + stage * S::kStageBytes;
+    const uint8_t* tile_ptr = ring + stage * S::kStageBytes;
+    auto there = [&](int t) { return t == 0 || turn * NT + t < total; };  // the last turn may have one tile
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+    if (!busy) continue;
+
+    float sc[NT][MT][2][4];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) sc[m][h][0] = sc[m][h][1] = sc[m][h][2] = sc[m][h][3] = 0.f;
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int i = 0; i < kSteps / 2; ++i) {  // 32 depths of positions 0-7 and 8-15
-        uint32_t kb[4];
-        ldmatrix4(kb, tile + at[i % kAt] + i / kAt * 128);
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t k0 = low_codes(kb[2 * u]), k1 = high_codes(kb[2 * u]);
-          const uint32_t k2 = low_codes(kb[2 * u + 1]), k3 = high_codes(kb[2 * u + 1]);
+          for (int i = 0; i < 4; ++i) sc[t][m][h][i] = 0.f;
 #pragma unroll
-          for (int m = 0; m < RT; ++m) {
-            uint32_t qk[4];
-            ldmatrix4(qk, q_at[(2 * i + u) & 3] + m * 32 * D + (2 * i + u) / 4 * 128);
-            mma(sc[m][0], qk, k0, k1);
-            mma(sc[m][1], qk, k2, k3);
+    for (int i = 0; i < kSteps / 2; ++i) {  // 32 depths of positions 0-7 and 8-15
+      uint32_t kb[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) ldmatrix4(kb[t], tile + t * 2 * S::kTileBytes + piece_at(i));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint32_t qk[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) ldmatrix4(qk[m], q_at[(2 * i + u) & 3] + m * 32 * D + (2 * i + u) / 4 * 128);
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t k0 = low_codes(kb[t][2 * u + h]), k1 = high_codes(kb[t][2 * u + h]);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) mma(sc[t][m][h], qk[m], k0, k1);
           }
-        }
       }
-      // Scores in base 2, each with its value's scale; what a row does not see is none.
-      const float* scales = reinterpret_cast<const float*>(ring + stage * S::kStageBytes + warp * S::kTileStage + kScales);
+    }
+
+    // Scores in base 2, each with its value's scale; what a row does not see is none.
+    constexpr int kOwn = ONE ? 1 : 4;  // scales of this lane's positions 2 c, 2 c + 1, + 8
+    float log_v[NT][kOwn], inverse[NT][kOwn];
+    bool inside[NT];
+    auto sees = [&](int row_pos, int pos, int t) {
+      return visible(p, row_pos, pos) && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u;
+    };
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const float* scales = reinterpret_cast<const float*>(tile_ptr + kScales) + t * 2 * kTile;
       float ks[kOwn];
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
         const int j = ONE ? 0 : (e >> 1) * 8 + 2 * c + (e & 1);
         ks[e] = scales[j];
         const float v = fmaxf(scales[kTile + j], kLowestScale);
-        log_v[e] = log2_fast(v);
-        inverse[e] = inverse_fast(v);
+        log_v[t][e] = log2_fast(v);
+        inverse[t][e] = inverse_fast(v);
       }
+      const int a = tile_of(turn * NT + t) * kTile;
+      // every row sees the whole tile
+      inside[t] = !there(t) || (s.start >= 0 && a + kTile - 1 <= s.first && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u &&
+                                (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks));
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
+      for (int m = 0; m < MT; ++m) {
         float f[2][kOwn];
 #pragma unroll
         for (int e = 0; e < kOwn; ++e) {
@@ -511,248 +532,209 @@ attend8_kernel(const __grid_constant__ Params p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = ONE ? 0 : h * 2 + (i & 1);
-            sc[m][h][i] = fmaf(sc[m][h][i], f[i >> 1][e], log_v[e]);
+            sc[t][m][h][i] = fmaf(sc[t][m][h][i], f[i >> 1][e], log_v[t][e]);
           }
       }
-      if (!whole(a)) {
+      if (!inside[t]) {
 #pragma unroll
-        for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (!visible(p, i < 2 ? pos_a[m] : pos_b[m], a + h * 8 + 2 * c + (i & 1))) sc[m][h][i] = kNone;
+              if (!sees(i < 2 ? pos_a[m] : pos_b[m], a + h * 8 + 2 * c + (i & 1), t)) sc[t][m][h][i] = kNone;
       }
+    }
+
+    // The references, tile by tile (so that their order does not show), and the weights.
+    float gain[NT][MT][2];
+    bool moves[NT];
+    uint32_t pf[NT][MT][4];
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+    for (int t = 0; t < NT; ++t) {
+      if (!there(t)) break;
+      float top[MT][2];
+      bool above = false;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
-          top[m][side] = fmaxf(fmaxf(sc[m][0][2 * side], sc[m][0][2 * side + 1]), fmaxf(sc[m][1][2 * side], sc[m][1][2 * side + 1]));
+          top[m][side] = fmaxf(fmaxf(sc[t][m][0][2 * side], sc[t][m][0][2 * side + 1]),
+                               fmaxf(sc[t][m][1][2 * side], sc[t][m][1][2 * side + 1]));
           above = above || top[m][side] - ref[m][side] > kSlack;  // (ref may be that of no score)
+          gain[t][m][side] = 1.f;
         }
-    }
-    // The weights, with the references as they are; only if some row's maximum is above
-    // its reference by more than the slack, all warps agree on new ones and go back.
-    // (The rounded score less the reference, which is a rounded score: the largest weight
-    // is 2^kLift, however large they are.)
-    auto exponent = [&](int m, int h, int i) {
-      return sc[m][h][i] + (ref[m][i >> 1] == kNone ? 0.f : kLift - ref[m][i >> 1]);
-    };
-    float sums[RT][2], least = INFINITY;
-    auto weigh = [&] {
-      if (!there) return;
+      }
+      moves[t] = __any_sync(~0u, above);
+      if (moves[t]) {
 #pragma unroll
-      for (int m = 0; m < RT; ++m) {
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int side = 0; side < 2; ++side) {
+            float x = top[m][side];
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+            const float was = ref[m][side], now = x - was > kSlack ? x : was;
+            gain[t][m][side] = now == was ? 1.f : exp2_fast(was - now);
+            ref[m][side] = now;
+          }
+      }
+      // (the rounded score less the reference, which is a rounded score: the largest weight is 2^kLift, however large they are)
+      auto exponent = [&](int m, int h, int i) {
+        return sc[t][m][h][i] + (ref[m][i >> 1] == kNone ? 0.f : kLift - ref[m][i >> 1]);
+      };
+      float least = INFINITY;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
         float wt[2][4];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             wt[h][i] = exp2_fast(exponent(m, h, i));
             if constexpr (!ONE) least = fminf(least, wt[h][i]);
           }
-        p_frags[((buffer * W + warp) * RT + m) * 32 + lane] =
-            make_uint4(pack_half(wt[0][0], wt[0][1]), pack_half(wt[0][2], wt[0][3]), pack_half(wt[1][0], wt[1][1]),
-                       pack_half(wt[1][2], wt[1][3]));
+          pf[t][m][2 * h] = pack_half(wt[h][0], wt[h][1]);
+          pf[t][m][2 * h + 1] = pack_half(wt[h][2], wt[h][3]);
+        }
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           const int i = 2 * side;
-          sums[m][side] = ONE ? ((wt[0][i] + wt[0][i + 1]) + (wt[1][i] + wt[1][i + 1])) * inverse[0]
-                              : (wt[0][i] * inverse[0] + wt[0][i + 1] * inverse[kOwn > 1 ? 1 : 0]) +
-                                    (wt[1][i] * inverse[kOwn > 1 ? 2 : 0] + wt[1][i + 1] * inverse[kOwn > 1 ? 3 : 0]);
+          const float add = ONE ? ((wt[0][i] + wt[0][i + 1]) + (wt[1][i] + wt[1][i + 1])) * inverse[t][0]
+                                : (wt[0][i] * inverse[t][0] + wt[0][i + 1] * inverse[t][kOwn > 1 ? 1 : 0]) +
+                                      (wt[1][i] * inverse[t][kOwn > 1 ? 2 : 0] + wt[1][i + 1] * inverse[t][kOwn > 1 ? 3 : 0]);
+          l[m][side] = fmaf(l[m][side], gain[t][m][side], add);
         }
       }
-    };
-    weigh();
-    if (lane == 0) {
-      s_flags[buffer][warp] = there ? (whole(a) ? 3 : 1) : 0;
-      if constexpr (ONE) s_log[buffer][warp] = there ? log_v[0] : kNone;
-    }
-    if (__syncthreads_or(above)) {
+      // Beside values of scales 2^60 times as large and more, P may be below fp32's
+      // range and the weight not.  (Where it is below it without that, the weight is
+      // below 2^-60 of the row's sum, whose bits it does not reach.)
+      bool low;
+      if constexpr (ONE) {
+        log_top = fmaxf(log_top, log_v[t][0]);
+        low = log_top - log_v[t][0] > 60.f;
+      } else {
+        low = least < kLowWeight;
+        if (low && !inside[t]) {  // most of it is masked
+          low = false;
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
+          for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          float x = there ? top[m][side] : kNone;
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-          if (c == 0) s_row[warp][m * 16 + r + 8 * side] = x;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) low = low || (sc[t][m][h][i] > kNone && sc[t][m][h][i] - ref[m][i >> 1] < -100.f);
         }
-      __syncthreads();
-#pragma unroll
-      for (int m = 0; m < RT; ++m) {
-        float gain[2];
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          float x = kNone;
-#pragma unroll
-          for (int j = 0; j < W; ++j) x = fmaxf(x, s_row[j][m * 16 + r + 8 * side]);
-          const float was = ref[m][side], now = x - was > kSlack ? x : was;
-          gain[side] = now == was ? 1.f : exp2_fast(was - now);
-          ref[m][side] = now;
-          l[m][side] *= gain[side];
-        }
-#pragma unroll
-        for (int i = 0; i < S::kCols / 8; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[e >> 1];
+        low = __any_sync(~0u, low);
       }
-      least = INFINITY;
-      weigh();
-      __syncthreads();
-    }
-    if (there) {
+      if (low) {
 #pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int side = 0; side < 2; ++side) l[m][side] += sums[m][side];
-    }
-    // Beside values of scales 2^60 times as large and more, P may be below fp32's
-    // range and the weight not.  (Where it is below it without that, the weight is
-    // below 2^-60 of the row's sum, whose bits it does not reach.)
-    bool low = false;
-    if constexpr (ONE) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) log_top = fmaxf(log_top, s_log[buffer][j]);
-      low = there && log_top - log_v[0] > 60.f;
-    } else if (there) {
-      low = least < kLowWeight;
-      if (low && !whole(a)) {  // most of it is masked
-        low = false;
-#pragma unroll
-        for (int m = 0; m < RT; ++m)
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) low = low || (sc[m][h][i] > kNone && sc[m][h][i] - ref[m][i >> 1] < -100.f);
+            for (int i = 0; i < 4; ++i) {
+              const int e = ONE ? 0 : h * 2 + (i & 1);
+              const float x = exponent(m, h, i), w = exp2_fast(x);
+              if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[t][e]) - w * inverse[t][e];
+            }
       }
     }
-    if (low) {
-#pragma unroll
-      for (int m = 0; m < RT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int e = ONE ? 0 : h * 2 + (i & 1);
-            const float x = exponent(m, h, i), w = exp2_fast(x);
-            if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[e]) - w * inverse[e];
-          }
-    }
-    // (behind the barrier: every warp is done with the last turn's stage)
-    issue(turn + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
 
-    // P V of the turn's tiles in order, for this warp's columns; NaN codes in a tile
-    // that not every row sees whole are left out, and found.
-    const uint32_t v_stage = v_at + stage * S::kStageBytes;
-    auto halves = [&](const uint32_t (&vb)[4], uint32_t (&even)[4], uint32_t (&odd)[4]) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {  // a column's two positions together
-        const uint32_t both = __byte_perm(vb[e], 0u, 0x3120);
-        even[e] = low_codes(both);
-        odd[e] = high_codes(both);
+    for (int t = 0; t < NT; ++t) {
+      if (!there(t)) break;
+      if (moves[t]) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[t][m][e >> 1];
       }
-    };
-    auto clean = [&](uint32_t& v, uint32_t& nans) {
-      const uint32_t bad = nan_codes(v);
-      nans |= bad;
-      v &= ~((bad >> 7) * 0xFFu);
-    };
-    auto fragments = [&](int j, int m, uint32_t (&pf)[4]) {
-      const uint4 v = p_frags[((buffer * W + j) * RT + m) * 32 + lane];
-      pf[0] = v.x; pf[1] = v.y; pf[2] = v.z; pf[3] = v.w;
-    };
-    auto mark = [&](int j, uint32_t nans) {  // a row that sees a NaN code has NaN in its column
-      if (!__any_sync(~0u, nans != 0u)) return;
-      const uint8_t* v_tile = ring + stage * S::kStageBytes + j * S::kTileStage + S::kTileBytes;
-      const int first = (block * W + j) * kTile;
-      for (int k = 0; k < kTile; ++k) {
+      uint32_t nans = 0u;
 #pragma unroll
-        for (int i = 0; i < S::kCols / 16; ++i) {
-          const uint32_t bad =
-              nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(k, warp * (S::kCols / 16) + i) + 4 * c));
+      for (int i = 0; i < D / 32; ++i) {  // 32 columns; NaN codes in a tile that not every row sees whole are left out
+        uint32_t vb[4];
+        ldmatrix4_trans(vb, tile + t * 2 * S::kTileBytes + S::kTileBytes + piece_at(i));
+        if (!inside[t]) {
 #pragma unroll
-          for (int m = 0; m < RT; ++m) {
-            const bool va = visible(p, pos_a[m], first + k), vb = visible(p, pos_b[m], first + k);
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t bad = nan_codes(vb[e]);
+            nans |= bad;
+            vb[e] &= ~((bad >> 7) * 0xFFu);
+          }
+        }
+        uint32_t even_v[4], odd_v[4];  // a column's two positions together
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((bad >> (8 * e + 7)) & 1u) {
-                if (va) acc[m][2 * i + (e & 1)][e >> 1] = NAN;
-                if (vb) acc[m][2 * i + (e & 1)][2 + (e >> 1)] = NAN;
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t both = __byte_perm(vb[e], 0u, 0x3120);
+          even_v[e] = low_codes(both);
+          odd_v[e] = high_codes(both);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          mma(acc[m][4 * i], pf[t][m], even_v[0], even_v[1]);
+          mma(acc[m][4 * i + 1], pf[t][m], odd_v[0], odd_v[1]);
+          mma(acc[m][4 * i + 2], pf[t][m], even_v[2], even_v[3]);
+          mma(acc[m][4 * i + 3], pf[t][m], odd_v[2], odd_v[3]);
+        }
+      }
+      if (__any_sync(~0u, nans != 0u)) {  // a row that sees a NaN code has NaN in its column
+        const uint8_t* v_tile = tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes;
+        const int a = tile_of(turn * NT + t) * kTile;
+        for (int j = 0; j < kTile; ++j) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t bad = nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(j, i) + 4 * c));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+              const bool va = sees(pos_a[m], a + j, t), vb = sees(pos_b[m], a + j, t);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((bad >> (8 * e + 7)) & 1u) {
+                  if (va) acc[m][2 * i + (e & 1)][e >> 1] = NAN;
+                  if (vb) acc[m][2 * i + (e & 1)][2 + (e >> 1)] = NAN;
+                }
               }
             }
           }
         }
       }
-    };
-    if constexpr (S::kCols == 32) {
-#pragma unroll
-      for (int j = 0; j < W; ++j) {
-        const int flags = s_flags[buffer][j];
-        if (flags == 0) continue;
-        uint32_t vb[4], even[4], odd[4], nans = 0u;
-        ldmatrix4_trans(vb, v_stage + j * S::kTileStage);
-        if (flags == 1) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) clean(vb[e], nans);
-        }
-        halves(vb, even, odd);
-#pragma unroll
-        for (int m = 0; m < RT; ++m) {
-          uint32_t pf[4];
-          fragments(j, m, pf);
-          mma(acc[m][0], pf, even[0], even[1]);
-          mma(acc[m][1], pf, odd[0], odd[1]);
-          mma(acc[m][2], pf, even[2], even[3]);
-          mma(acc[m][3], pf, odd[2], odd[3]);
-        }
-        if (flags == 1) mark(j, nans);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < W; j += 2) {
-        const int flags[2] = {s_flags[buffer][j], s_flags[buffer][j + 1]};
-        uint32_t vb[4], even[4], odd[4], nans[2] = {0u, 0u};
-        ldmatrix4_trans(vb, v_stage + j * S::kTileStage);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (flags[e >> 1] == 1) clean(vb[e], nans[e >> 1]);
-        halves(vb, even, odd);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (flags[t] == 0) continue;
-#pragma unroll
-          for (int m = 0; m < RT; ++m) {
-            uint32_t pf[4];
-            fragments(j + t, m, pf);
-            mma(acc[m][0], pf, even[2 * t], even[2 * t + 1]);
-            mma(acc[m][1], pf, odd[2 * t], odd[2 * t + 1]);
-          }
-          if (flags[t] == 1) mark(j + t, nans[t]);
-        }
-      }
     }
-    stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
-
-  // A row's sum of weights, over the lanes and the warps in order.
-  __syncthreads();
 #pragma unroll
-  for (int m = 0; m < RT; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int side = 0; side < 2; ++side) {
-      float x = l[m][side];
-      x += __shfl_xor_sync(~0u, x, 1);
-      x += __shfl_xor_sync(~0u, x, 2);
-      if (c == 0) s_row[warp][m * 16 + r + 8 * side] = x;
+      l[m][side] += __shfl_xor_sync(~0u, l[m][side], 1);
+      l[m][side] += __shfl_xor_sync(~0u, l[m][side], 2);
+    }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+  __syncthreads();  // q and the ring become the exchange
+
+  // Join the CTA's groups, then the cluster's CTAs, each time in order.
+  float* left = reinterpret_cast<float*>(smem);
+  constexpr int kLeft = S::kLeft / 4, kStat = S::kRows * S::kSumRow;
+  const int rows_here = min(S::kRows, live_rows - rg * S::kRows);
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int side = 0; side < 2; ++side) {
+      const int row = (rw * MT + m) * 16 + r + 8 * side;
+      if (row < rows_here) {
+        float* to = left + kg * kLeft + row * S::kSumRow + 4 * c;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+          *reinterpret_cast<float4*>(to + 16 * i) = make_float4(acc[m][2 * i][2 * side], acc[m][2 * i + 1][2 * side],
+                                                                acc[m][2 * i][2 * side + 1], acc[m][2 * i + 1][2 * side + 1]);
+        if (c == 0)
+          *reinterpret_cast<float2*>(left + kg * kLeft + kStat + 2 * row) = make_float2(ref[m][side], l[m][side]);
+      }
     }
   __syncthreads();
-  if (!S::kApart && ctas > 1) cluster_arrive_release();  // what this CTA receives may overwrite its stages from here on
-
-  const int rows_here = min(S::kRows, live_rows - row_0);
+  const int units = rows_here * (D / 4);  // of 4 columns
   auto emit = [&](int row, int col, const float4& sum, const float2& st) {  // (row: of this CTA's)
-    row += row_0;
+    row += rg * S::kRows;
     if (p.clusters == 1) {
       const float inv = st.y == 0.f ? 0.f : 1.f / st.y;  // no visible position: zeros
       const int i = row / p.by_group;
@@ -767,33 +749,32 @@ attend8_kernel(const __grid_constant__ Params p) {
     }
   };
   // A cluster's row is joined by its CTA of rank row % ctas, in its place row / ctas.
-  float* received = reinterpret_cast<float*>(smem + (S::kApart ? S::kBytes : 0));
+  float* received = reinterpret_cast<float*>(smem + S::kBytes);
   float2* received_stat = reinterpret_cast<float2*>(received + (S::kRows + ctas - 1) / ctas * ctas * D);
   if (ctas > 1) cluster_wait_acquire();
+  for (int u = tid; u < units; u += S::kThreads) {
+    const int row = u / (D / 4), col = u % (D / 4) * 4;
+    float2 stats[S::kKg];
+    float4 sums[S::kKg];
+    float top = kNone;
 #pragma unroll
-  for (int m = 0; m < RT; ++m)
-#pragma unroll
-    for (int side = 0; side < 2; ++side) {
-      const int row = m * 16 + r + 8 * side;
-      if (row >= rows_here) continue;
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < W; ++j) sum += s_row[j][row];
-      const float2 st = make_float2(ref[m][side], sum);
-      const int slot = row / ctas, owner = row - slot * ctas, place = slot * ctas + rank;
-#pragma unroll
-      for (int i = 0; i < S::kCols / 16; ++i) {
-        const int col = warp * S::kCols + 16 * i + 4 * c;
-        const float4 v = make_float4(acc[m][2 * i][2 * side], acc[m][2 * i + 1][2 * side], acc[m][2 * i][2 * side + 1],
-                                     acc[m][2 * i + 1][2 * side + 1]);
-        if (ctas == 1) {
-          emit(row, col, v, st);
-        } else {
-          st_cluster_v4(cluster_map(smem_addr(received + place * D + col), owner), v);
-          if (col == 0) st_cluster_v2(cluster_map(smem_addr(received_stat + place), owner), st);
-        }
-      }
+    for (int i = 0; i < S::kKg; ++i) {
+      stats[i] = *reinterpret_cast<const float2*>(left + i * kLeft + kStat + 2 * row);
+      sums[i] = *reinterpret_cast<const float4*>(left + i * kLeft + row * S::kSumRow + col);
+      top = fmaxf(top, stats[i].x);
     }
+    Joined joined(top);
+#pragma unroll
+    for (int i = 0; i < S::kKg; ++i) joined.add(stats[i], sums[i]);
+    if (ctas == 1) {
+      emit(row, col, joined.sum, joined.stat());
+    } else {
+      const int slot = row / ctas, owner = row - slot * ctas;
+      const int place = slot * ctas + rank;
+      st_cluster_v4(cluster_map(smem_addr(received + place * D + col), owner), joined.sum);
+      if (col == 0) st_cluster_v2(cluster_map(smem_addr(received_stat + place), owner), joined.stat());
+    }
+  }
   if (ctas == 1) return;
   cluster_arrive_release();
   cluster_wait_acquire();
@@ -844,7 +825,7 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
   load(warp);
   const Seq s = sequence(p, b);
   if (!s.ok || i >= s.n) return;
-  const int parts = p.chunk > 0 ? max(1, (s.len + p.span - 1) / p.span) : p.clusters;  // (chunks alive)
+  const int parts = p.chunk > 0 ? max(1, (s.len + p.chunk * kTile - 1) / (p.chunk * kTile)) : p.clusters;  // (chunks alive)
   float top = kNone, l = 0.f, sum[kPer] = {};
   for (int z = warp; z < parts; z += kWarps * kBatch) {
     if (z > warp) load(z);
@@ -886,20 +867,20 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
 }
 
 struct Split {
-  int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; blocks of a chunk, or 0
+  int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; tiles of a chunk, or 0
 };
 Split split_for(const w4g128_attend8_args& a) {
   long long span = a.max_len;
   if (a.window > 0) span = std::min<long long>(span, static_cast<long long>(a.window) + a.sinks + 2 * kTile);
   const long long pairs = static_cast<long long>(a.kv_heads) * a.count;
-  const long long block = warps_of(a.head_dim) * kTile, blocks = (span + block - 1) / block;  // of tiles
-  const long long target = a.head_dim == 256 ? 151 : 607;
-  const long long want = std::min(std::max<long long>(1, target / pairs), blocks);
+  const long long tiles = (span + kTile - 1) / kTile, groups = groups_of(a.head_dim);
+  const long long target = a.head_dim == 64 ? 455 : a.head_dim == 128 ? 303 : 151;
+  const long long want = std::min(std::max<long long>(1, target / pairs), (tiles + groups - 1) / groups);
   if (want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1, 0};
-  if (a.count > 3 && a.window == 0) {
-    const long long some = target * 2;
-    const long long chunk = std::min<long long>(kMostChunk, (blocks * pairs + some - 1) / some);
-    return {1, static_cast<int>((blocks + chunk - 1) / chunk), static_cast<int>(chunk)};
+  if (a.count > 1 && a.window == 0) {
+    const long long some = target * 3 / 2;
+    const long long chunk = std::min<long long>(kMostChunk, (tiles * pairs + some * groups - 1) / (some * groups) * groups);
+    return {1, static_cast<int>((tiles + chunk - 1) / chunk), static_cast<int>(chunk)};
   }
   return {1, static_cast<int>(want), 0};
 }
@@ -944,8 +925,7 @@ template <int D, int RT>
 cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   using S = Shape<D, RT>;
   const auto kernel = p.block_log2 >= 4 ? attend8_kernel<D, RT, true> : attend8_kernel<D, RT, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       S::kBytes + (S::kApart ? S::kMostReceived : 0));
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kMostBytes);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   p.row_groups = (p.max_new * p.group + S::kRows - 1) / S::kRows;
@@ -953,7 +933,7 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   const long long clusters = 1 + static_cast<long long>(p.count) * p.kv_heads * p.row_groups * p.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
   cfg.blockDim = dim3(S::kThreads);
-  cfg.dynamicSmemBytes = S::kBytes + (S::kApart && ctas > 1 ? S::received(ctas) : 0);
+  cfg.dynamicSmemBytes = S::kBytes + (ctas > 1 ? S::received(ctas) : 0);
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -1007,7 +987,6 @@ int w4g128_attend8(const w4g128_attend8_args* a, void* ws, size_t ws_bytes, void
   p.window = a->window; p.sinks = a->sinks;
   p.clusters = split.clusters;
   p.chunk = split.chunk;
-  p.span = split.chunk * warps_of(a->head_dim) * kTile;
   p.by_clusters = divisor(split.clusters);
   p.by_kv_heads = divisor(a->kv_heads);
   p.by_group = divisor(p.group);
