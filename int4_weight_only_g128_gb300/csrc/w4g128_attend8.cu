@@ -9,7 +9,7 @@
 //     power of two for each row (exact down to 2^-31 of the row's largest value).
 //     (The warp MMA of e4m3 operands is made of conversions and fp16 products here:
 //     with q as the sum of two e4m3 values it took 936 instructions a tile, and 33
-//     us where this takes .)
+//     us where this takes 24.6.)
 //   * A key's scale multiplies its score.  A value's scale enters the softmax
 //     weight: with score s_j (base 2) and value scale v_j, P_j = 2^(s_j + log2 v_j - m),
 //     rounded to fp16 as an operand, and the row's sum takes P_j / v_j.  The
@@ -21,9 +21,18 @@
 //     work on it, whatever its length, so all of them have the same share and no CTA
 //     depends on how long a sequence may become.  A group keeps a ring of cp.async
 //     stages and a running reference and sums of its own.
-//   * The CTAs of a head are a cluster, which joins their sums through its shared
-//     memory.  Only if one cluster is too small for the call does a second kernel
-//     join several.
+//   * Few CTAs of a head are a cluster, which joins their sums through its shared
+//     memory; otherwise a second kernel joins them.
+//
+// What bounds it: one sequence of 32771 with 8 rows, 32 heads on 8 of 128 and pages of
+// 64, takes 24.6 us, 2.8 TB/s.  Its bytes alone take 9.9 us, its fp16 products 7.2.  With
+// each group's first tile alone the call takes 10.3 us: 3.3 until the first lengths and
+// ids are there, 2.2 in joining a CTA's groups and writing their sums, 2.1 in the second
+// kernel.  The loop's other 14 us are neither the copies nor the products alone (without
+// copies 1.3 us less, without the products 6 less), but both, the conversions and the
+// softmax at the 8 warps an SM whose sums the registers hold.
+// 16 ragged sequences of up to 9001 on 4 heads of 64 take 19.6 us, two with a window of
+// 4096 and 16 rows each on 4 heads of 256 20.5, one of 611 with one row 4.8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -49,7 +58,8 @@ constexpr float kLowestScale = 0x1p-80f;  // of a value: smaller ones count as t
 constexpr float kLowWeight = 0x1p-120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
-constexpr int kMostChunk = 128;  // tiles
+constexpr int kMostChunk = 64;  // tiles
+constexpr int kChunkedFrom = 4;  // sequences
 
 struct Params {
   const uint16_t* q;
@@ -98,6 +108,7 @@ __device__ __forceinline__ bool visible(const Params& p, int row_pos, int pos) {
 __device__ void check_all(const Params& p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int parts = max(1, warps / p.count);  // warps that share a sequence
+  constexpr int kBatch = 8;
   bool bad = false;
   for (int b = warp / parts; b < p.count; b += warps / parts) {
     const Seq s = sequence(p, b);
@@ -106,9 +117,16 @@ __device__ void check_all(const Params& p) {
     const int sink_pages = (s.sink + static_cast<int>(p.by_page.d) - 1) / p.by_page;
     const int end = s.len > 0 ? (s.len - 1) / p.by_page + 1 : 0;
     const int low = max(s.lo / p.by_page, sink_pages), all = sink_pages + end - low;
-    for (int i = (warp % parts) * 32 + lane; i < all; i += parts * 32) {
-      const int id = p.table[static_cast<long long>(b) * p.table_row + (i < sink_pages ? i : low + i - sink_pages)];
-      bad |= id < 0 || id >= p.pages;
+    const int* table = p.table + static_cast<long long>(b) * p.table_row;
+    for (int i = (warp % parts) * 32 + lane; i < all; i += kBatch * parts * 32) {  // (many on their way at once)
+      int id[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const int at = i + j * parts * 32;
+        id[j] = at < all ? table[at < sink_pages ? at : low + at - sink_pages] : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) bad |= id[j] < 0 || id[j] >= p.pages;
     }
   }
   if (__syncthreads_or(bad)) bad = true;
@@ -193,27 +211,31 @@ struct Joined {
   __device__ __forceinline__ float2 stat() const { return make_float2(top, l); }
 };
 
-// KG groups of warps with tiles of their own; RT row tiles, MT of them a warp; NT tiles
-// of positions a turn.  What fills a warp's schedule is several products at once:
-// two row tiles that share K's and V's fragments, or two tiles of positions.
+// KG groups of warps with tiles of their own; RT row tiles, MT of them a warp: two, which
+// share K's and V's fragments and their conversion, where a thread's sums leave room.
 constexpr int groups_of(int head_dim) { return head_dim == 256 ? 2 : 4; }
 template <int D, int RT>
 struct Shape {
   static constexpr int kKg = groups_of(D);
   static constexpr int kMt = D == 256 || RT == 1 ? 1 : 2;
-  static constexpr int kNt = D < 256 && RT == 1 ? 2 : 1;
-  static constexpr int kGroup = RT / kMt * 32;  // threads of a group
+  // Warps that share a row tile's columns, each with all its scores: two for the widest heads'
+  // few rows, which have few warps otherwise (3 of 4 rows on 4 heads: 17.6 us -> 14.8; 32 rows
+  // have 8 warps an SM either way: a batch of 16 took 20.3 us with one, 31.4 with two).
+  static constexpr int kCols = D == 256 && RT == 1 ? 2 : 1;
+  static constexpr int kGroup = RT / kMt * kCols * 32;  // threads of a group
   static constexpr int kThreads = kKg * kGroup;
   // warps an SM, by the registers of a thread's sums: 128 of them leave room for 8, 64 for 12, 32 for 16
-  static constexpr int kSums = kMt * D / 2;
+  // (16 with 64 spill: 16 ragged sequences on heads of 64 25.6 us, 20.0 with 12)
+  static constexpr int kSums = kMt * D / kCols / 2;
   static constexpr int kWarps = kSums == 128 ? 8 : kSums == 64 ? 12 : 16;
   static constexpr int kCtas = kWarps * 32 / kThreads > 0 ? kWarps * 32 / kThreads : 1;
   static constexpr int kRows = RT * 16;
   static constexpr int kTileBytes = kTile * D;  // K or V of one tile
-  static constexpr int kStageBytes = kNt * (2 * kTileBytes + 2 * kTile * 4);  // and their positions' scales
+  static constexpr int kStageBytes = 2 * kTileBytes + 2 * kTile * 4;  // K, V and their positions' scales
   static constexpr int kQBytes = kRows * 2 * D;
   static constexpr int kRoom = (227 * 1024 / kCtas - 1536 - kQBytes) / kKg / kStageBytes;
-  static constexpr int kStages = kRoom < 6 ? kRoom : 6;
+  // (3: more only take room from the L1 cache; one of 32771 24.6 us, with 6 24.8; batches 25.4, 26.8)
+  static constexpr int kStages = kRoom < 3 ? kRoom : 3;
   static constexpr int kRing = kKg * kStages * kStageBytes;
   static constexpr int kSumRow = D + 16;     // floats of a row's sums (free of bank conflicts)
   static constexpr int kLeft = kRows * (kSumRow + 2) * 4;  // a group's sums, references and sums of weights
@@ -229,19 +251,20 @@ template <int D, int RT, bool ONE>  // ONE: a scale for each tile at most (block
 __global__ void __launch_bounds__(Shape<D, RT>::kThreads, Shape<D, RT>::kCtas)
 attend8_kernel(const __grid_constant__ Params p) {
   using S = Shape<D, RT>;
-  constexpr int MT = S::kMt, NT = S::kNt;
+  constexpr int MT = S::kMt, kCols = S::kCols;
   constexpr int kSteps = D / 16;   // of Q K^T
   constexpr int kPieces = D / 16;  // 16-byte pieces of a row of codes
   constexpr int kPer = 2 * kTile * kPieces / S::kGroup;  // pieces of a tile's K and V that one thread copies
   constexpr int kStep = S::kGroup / kPieces;             // rows between them
-  constexpr int kScales = NT * 2 * S::kTileBytes;        // a stage's scales
+  constexpr int kScales = 2 * S::kTileBytes;             // a stage's scales
   static_assert(S::kGroup % kPieces == 0 && 2 * kTile % kStep == 0, "a thread copies one column of pieces");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float s_factor[S::kRows];  // a row's score factor
 
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
-  const int kg = warp / (RT / MT), rw = warp % (RT / MT);  // this warp's rows: rw MT 16 ..
+  const int kg = warp * 32 / S::kGroup, in_group = warp - kg * (S::kGroup / 32);
+  const int rw = in_group / kCols, part = in_group % kCols;  // this warp's rows: rw MT 16 .., and its part of the columns
   const int rank = static_cast<int>(cluster_ctarank()), ctas = static_cast<int>(cluster_nctarank());
   const int cluster = static_cast<int>(blockIdx.x) / ctas;
 
@@ -338,7 +361,7 @@ attend8_kernel(const __grid_constant__ Params p) {
   auto swizzled = [](int j, int piece) { return j * D + ((piece ^ (D == 64 ? (j >> 1) & 3 : j & 7)) << 4); };
 
   // A thread copies one column of pieces: rows j0, j0 + kStep, .. of K, then of V.
-  const int gl = rw * 32 + lane;
+  const int gl = in_group * 32 + lane;
   const int ch = gl % kPieces, j0 = gl / kPieces;
   const uint8_t* k_base = p.k_cache + head * p.head_stride + ch * 16;
   const long long v_off = p.v_cache - p.k_cache;
@@ -348,45 +371,41 @@ attend8_kernel(const __grid_constant__ Params p) {
   const long long first_row = j0 % kTile * p.slot_stride + (j0 >= kTile ? v_off : 0);
   uint32_t okays = 0u;  // of the tiles on their way, by their number mod 32: on a page
   auto issue = [&](int turn, int stage) {
-    if (turn * NT < total) {
+    if (turn < total) {
+      if (turn > 0 && (turn & 31) == 0) {
+        ids = ids_next;
+        ids_next = ids_from(turn + 32 + lane);
+        locate(turn + lane);
+      }
+      const int a = tile_of(turn) * kTile;
+      const long long codes = __shfl_sync(~0u, codes_at, turn & 31), scales = __shfl_sync(~0u, scales_at, turn & 31);
+      const bool ok = codes >= 0;
+      okays = (okays & ~(1u << (turn & 31))) | (ok ? 1u : 0u) << (turn & 31);
+      const uint32_t dst = ring_at + stage * S::kStageBytes;
+      const uint32_t scale_dst = dst + kScales + gl * 4;
+      const uint8_t* src = k_base + (ok ? codes : 0);
+      if (ok && a + kTile <= s.len) {  // a whole tile
+        src += first_row;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int k = turn * NT + t;
-        if (t == 0 && k > 0 && (k & 31) == 0) {
-          ids = ids_next;
-          ids_next = ids_from(k + 32 + lane);
-          locate(k + lane);
+        for (int e = 0; e < kPer; ++e) {
+          const int jj = j0 + e * kStep;
+          if (e * kStep == kTile) src += v_off - kTile * p.slot_stride;
+          cp_async16(dst + (jj >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
+          src += row_step;
         }
-        const int a = tile_of(k) * kTile;
-        const long long codes = __shfl_sync(~0u, codes_at, k & 31), scales = __shfl_sync(~0u, scales_at, k & 31);
-        const bool ok = codes >= 0;
-        okays = (okays & ~(1u << (k & 31))) | (ok ? 1u : 0u) << (k & 31);
-        const uint32_t dst = ring_at + stage * S::kStageBytes + t * 2 * S::kTileBytes;
-        const uint32_t scale_dst = ring_at + stage * S::kStageBytes + kScales + (t * 32 + gl) * 4;
-        const uint8_t* src = k_base + (ok ? codes : 0);
-        if (ok && a + kTile <= s.len) {  // a whole tile
-          src += first_row;
-#pragma unroll
-          for (int e = 0; e < kPer; ++e) {
-            const int jj = j0 + e * kStep;
-            if (e * kStep == kTile) src += v_off - kTile * p.slot_stride;
-            cp_async16(dst + (jj >= kTile ? S::kTileBytes : 0) + swizzled(jj % kTile, ch), src);
-            src += row_step;
-          }
-          if (gl < 32) cp_async4(scale_dst, scale_base + scales);
-        } else {  // zeros behind the end, and for what is no page
+        if (gl < 32) cp_async4(scale_dst, scale_base + scales);
+      } else {  // zeros behind the end, and for what is no page
 #pragma unroll 1
-          for (int e = 0; e < kPer; ++e) {
-            const int jj = j0 + e * kStep, j = jj % kTile;
-            const bool is_v = jj >= kTile, real = ok && a + j < s.len;
-            cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
-                               real ? src + (is_v ? v_off : 0) + j * p.slot_stride : p.k_cache, real);
-          }
-          if (gl < 32) {
-            const int j = gl & 15;
-            const bool real = ok && a + j < s.len;
-            cp_async4_or_zero(scale_dst, real ? scale_base + scales : p.k_scale, real);
-          }
+        for (int e = 0; e < kPer; ++e) {
+          const int jj = j0 + e * kStep, j = jj % kTile;
+          const bool is_v = jj >= kTile, real = ok && a + j < s.len;
+          cp_async16_or_zero(dst + (is_v ? S::kTileBytes : 0) + swizzled(j, ch),
+                             real ? src + (is_v ? v_off : 0) + j * p.slot_stride : p.k_cache, real);
+        }
+        if (gl < 32) {
+          const int j = gl & 15;
+          const bool real = ok && a + j < s.len;
+          cp_async4_or_zero(scale_dst, real ? scale_base + scales : p.k_scale, real);
         }
       }
     }
@@ -426,7 +445,7 @@ attend8_kernel(const __grid_constant__ Params p) {
   __syncthreads();
 
   float factor[MT][2];
-  float acc[MT][D / 8][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
+  float acc[MT][D / 8 / kCols][4];  // [2 i]: columns 16 i + 4 c, + 2 of rows r and r + 8; [2 i + 1]: + 1, + 3
   float ref[MT][2], l[MT][2];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -437,7 +456,7 @@ attend8_kernel(const __grid_constant__ Params p) {
       l[m][side] = 0.f;
     }
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
+    for (int i = 0; i < D / 8 / kCols; ++i) acc[m][i][0] = acc[m][i][1] = acc[m][i][2] = acc[m][i][3] = 0.f;
   }
 
   // ldmatrix: this lane's row and its pieces 2 i + lane / 16, in a tile of K or V and
@@ -448,253 +467,225 @@ attend8_kernel(const __grid_constant__ Params p) {
 #pragma unroll
   for (int i = 0; i < kAt; ++i) at[i] = swizzled(lj, 2 * i + lp);
   auto piece_at = [&](int i) { return at[i % kAt] + i / kAt * 128; };
+  constexpr int kColPieces = D / 32 / kCols, kColAt = kColPieces < 4 ? kColPieces : 4;  // (pairs of pieces of this warp's columns)
+  uint32_t col_at[kColAt];
+#pragma unroll
+  for (int i = 0; i < kColAt; ++i) col_at[i] = kCols == 1 ? at[i] : swizzled(lj, 2 * (i + part * kColPieces) + lp);
   uint32_t q_at[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) q_at[i] = smem_addr(smem) + (rw * MT * 16 + lj) * 2 * D + (((2 * i + lp) ^ (lj & 7)) << 4);
   const int last_pos = s.len - 1;  // of the sequence's last row
-  const int turns = (total + NT - 1) / NT;
   float log_top = kNone;  // of the tiles so far, the largest value scale (base 2)
   int stage = 0;
 #pragma unroll 1
-  for (int turn = 0; turn < turns; ++turn) {
+  for (int turn = 0; turn < total; ++turn) {
     cp_async_wait_group<S::kStages - 2>();
-    group_sync();  // the tiles are there for the group, and the stage refilled next is read out
+    group_sync();  // the tile is there for the group, and the stage refilled next is read out
     issue(turn + S::kStages - 1, stage == 0 ? S::kStages - 1 : stage - 1);
     const uint32_t tile = ring_at + stage * S::kStageBytes;
     const uint8_t* tile_ptr = ring + stage * S::kStageBytes;
-    auto there = [&](int t) { return t == 0 || turn * NT + t < total; };  // the last turn may have one tile
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
     if (!busy) continue;
 
-    float sc[NT][MT][2][4];
+    float sc[MT][2][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int m = 0; m < MT; ++m)
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sc[t][m][h][i] = 0.f;
+      for (int h = 0; h < 2; ++h) sc[m][h][0] = sc[m][h][1] = sc[m][h][2] = sc[m][h][3] = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps / 2; ++i) {  // 32 depths of positions 0-7 and 8-15
-      uint32_t kb[NT][4];
-#pragma unroll
-      for (int t = 0; t < NT; ++t) ldmatrix4(kb[t], tile + t * 2 * S::kTileBytes + piece_at(i));
+      uint32_t kb[4];
+      ldmatrix4(kb, tile + piece_at(i));
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint32_t qk[MT][4];
 #pragma unroll
         for (int m = 0; m < MT; ++m) ldmatrix4(qk[m], q_at[(2 * i + u) & 3] + m * 32 * D + (2 * i + u) / 4 * 128);
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k0 = low_codes(kb[2 * u + h]), k1 = high_codes(kb[2 * u + h]);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t k0 = low_codes(kb[t][2 * u + h]), k1 = high_codes(kb[t][2 * u + h]);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) mma(sc[t][m][h], qk[m], k0, k1);
-          }
+          for (int m = 0; m < MT; ++m) mma(sc[m][h], qk[m], k0, k1);
+        }
       }
     }
 
     // Scores in base 2, each with its value's scale; what a row does not see is none.
     constexpr int kOwn = ONE ? 1 : 4;  // scales of this lane's positions 2 c, 2 c + 1, + 8
-    float log_v[NT][kOwn], inverse[NT][kOwn];
-    bool inside[NT];
-    auto sees = [&](int row_pos, int pos, int t) {
-      return visible(p, row_pos, pos) && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u;
-    };
+    float log_v[kOwn], inverse[kOwn], ks[kOwn];
+    const float* scales = reinterpret_cast<const float*>(tile_ptr + kScales);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const float* scales = reinterpret_cast<const float*>(tile_ptr + kScales) + t * 2 * kTile;
-      float ks[kOwn];
+    for (int e = 0; e < kOwn; ++e) {
+      const int j = ONE ? 0 : (e >> 1) * 8 + 2 * c + (e & 1);
+      ks[e] = scales[j];
+      const float v = fmaxf(scales[kTile + j], kLowestScale);
+      log_v[e] = log2_fast(v);
+      inverse[e] = inverse_fast(v);
+    }
+    const int a = tile_of(turn) * kTile;
+    const bool on_page = (okays >> (turn & 31)) & 1u;
+    auto sees = [&](int row_pos, int pos) { return visible(p, row_pos, pos) && on_page; };
+    // every row sees the whole tile
+    const bool inside = s.start >= 0 && a + kTile - 1 <= s.first && on_page &&
+                        (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float f[2][kOwn];
 #pragma unroll
       for (int e = 0; e < kOwn; ++e) {
-        const int j = ONE ? 0 : (e >> 1) * 8 + 2 * c + (e & 1);
-        ks[e] = scales[j];
-        const float v = fmaxf(scales[kTile + j], kLowestScale);
-        log_v[t][e] = log2_fast(v);
-        inverse[t][e] = inverse_fast(v);
+        f[0][e] = factor[m][0] * ks[e];
+        f[1][e] = factor[m][1] * ks[e];
       }
-      const int a = tile_of(turn * NT + t) * kTile;
-      // every row sees the whole tile
-      inside[t] = !there(t) || (s.start >= 0 && a + kTile - 1 <= s.first && ((okays >> ((turn * NT + t) & 31)) & 1u) != 0u &&
-                                (p.window == 0 || last_pos - a < p.window || a + kTile <= p.sinks));
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = ONE ? 0 : h * 2 + (i & 1);
+          sc[m][h][i] = fmaf(sc[m][h][i], f[i >> 1][e], log_v[e]);
+        }
+    }
+    if (!inside) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!sees(i < 2 ? pos_a[m] : pos_b[m], a + h * 8 + 2 * c + (i & 1))) sc[m][h][i] = kNone;
+    }
+
+    // The references, and the weights.
+    float top[MT][2];
+    bool above = false;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        top[m][side] = fmaxf(fmaxf(sc[m][0][2 * side], sc[m][0][2 * side + 1]), fmaxf(sc[m][1][2 * side], sc[m][1][2 * side + 1]));
+        above = above || top[m][side] - ref[m][side] > kSlack;  // (ref may be that of no score)
+      }
+    if (__any_sync(~0u, above)) {
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        float f[2][kOwn];
+        float gain[2];
 #pragma unroll
-        for (int e = 0; e < kOwn; ++e) {
-          f[0][e] = factor[m][0] * ks[e];
-          f[1][e] = factor[m][1] * ks[e];
+        for (int side = 0; side < 2; ++side) {
+          float x = top[m][side];
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+          const float was = ref[m][side], now = x - was > kSlack ? x : was;
+          gain[side] = now == was ? 1.f : exp2_fast(was - now);
+          ref[m][side] = now;
+          l[m][side] *= gain[side];
         }
+#pragma unroll
+        for (int i = 0; i < D / 8 / kCols; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[e >> 1];
+      }
+    }
+    // (the rounded score less the reference, which is a rounded score: the largest weight is 2^kLift, however large they are)
+    auto exponent = [&](int m, int h, int i) {
+      return sc[m][h][i] + (ref[m][i >> 1] == kNone ? 0.f : kLift - ref[m][i >> 1]);
+    };
+    uint32_t pf[MT][4];
+    float least = INFINITY;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      float wt[2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          wt[h][i] = exp2_fast(exponent(m, h, i));
+          if constexpr (!ONE) least = fminf(least, wt[h][i]);
+        }
+        pf[m][2 * h] = pack_half(wt[h][0], wt[h][1]);
+        pf[m][2 * h + 1] = pack_half(wt[h][2], wt[h][3]);
+      }
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        const int i = 2 * side;
+        l[m][side] += ONE ? ((wt[0][i] + wt[0][i + 1]) + (wt[1][i] + wt[1][i + 1])) * inverse[0]
+                          : (wt[0][i] * inverse[0] + wt[0][i + 1] * inverse[kOwn > 1 ? 1 : 0]) +
+                                (wt[1][i] * inverse[kOwn > 1 ? 2 : 0] + wt[1][i + 1] * inverse[kOwn > 1 ? 3 : 0]);
+      }
+    }
+    // Beside values of scales 2^60 times as large and more, P may be below fp32's
+    // range and the weight not.  (Where it is below it without that, the weight is
+    // below 2^-60 of the row's sum, whose bits it does not reach.)
+    bool low;
+    if constexpr (ONE) {
+      log_top = fmaxf(log_top, log_v[0]);
+      low = log_top - log_v[0] > 60.f;
+    } else {
+      low = least < kLowWeight;
+      if (low && !inside) {  // most of it is masked
+        low = false;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) low = low || (sc[m][h][i] > kNone && sc[m][h][i] - ref[m][i >> 1] < -100.f);
+      }
+    }
+    if (low) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int e = ONE ? 0 : h * 2 + (i & 1);
-            sc[t][m][h][i] = fmaf(sc[t][m][h][i], f[i >> 1][e], log_v[t][e]);
+            const float x = exponent(m, h, i), w = exp2_fast(x);
+            if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[e]) - w * inverse[e];
           }
-      }
-      if (!inside[t]) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (!sees(i < 2 ? pos_a[m] : pos_b[m], a + h * 8 + 2 * c + (i & 1), t)) sc[t][m][h][i] = kNone;
-      }
     }
 
-    // The references, tile by tile (so that their order does not show), and the weights.
-    float gain[NT][MT][2];
-    bool moves[NT];
-    uint32_t pf[NT][MT][4];
+    uint32_t nans = 0u;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (!there(t)) break;
-      float top[MT][2];
-      bool above = false;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          top[m][side] = fmaxf(fmaxf(sc[t][m][0][2 * side], sc[t][m][0][2 * side + 1]),
-                               fmaxf(sc[t][m][1][2 * side], sc[t][m][1][2 * side + 1]));
-          above = above || top[m][side] - ref[m][side] > kSlack;  // (ref may be that of no score)
-          gain[t][m][side] = 1.f;
-        }
-      }
-      moves[t] = __any_sync(~0u, above);
-      if (moves[t]) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int side = 0; side < 2; ++side) {
-            float x = top[m][side];
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
-            x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
-            const float was = ref[m][side], now = x - was > kSlack ? x : was;
-            gain[t][m][side] = now == was ? 1.f : exp2_fast(was - now);
-            ref[m][side] = now;
-          }
-      }
-      // (the rounded score less the reference, which is a rounded score: the largest weight is 2^kLift, however large they are)
-      auto exponent = [&](int m, int h, int i) {
-        return sc[t][m][h][i] + (ref[m][i >> 1] == kNone ? 0.f : kLift - ref[m][i >> 1]);
-      };
-      float least = INFINITY;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        float wt[2][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            wt[h][i] = exp2_fast(exponent(m, h, i));
-            if constexpr (!ONE) least = fminf(least, wt[h][i]);
-          }
-          pf[t][m][2 * h] = pack_half(wt[h][0], wt[h][1]);
-          pf[t][m][2 * h + 1] = pack_half(wt[h][2], wt[h][3]);
-        }
-#pragma unroll
-        for (int side = 0; side < 2; ++side) {
-          const int i = 2 * side;
-          const float add = ONE ? ((wt[0][i] + wt[0][i + 1]) + (wt[1][i] + wt[1][i + 1])) * inverse[t][0]
-                                : (wt[0][i] * inverse[t][0] + wt[0][i + 1] * inverse[t][kOwn > 1 ? 1 : 0]) +
-                                      (wt[1][i] * inverse[t][kOwn > 1 ? 2 : 0] + wt[1][i + 1] * inverse[t][kOwn > 1 ? 3 : 0]);
-          l[m][side] = fmaf(l[m][side], gain[t][m][side], add);
-        }
-      }
-      // Beside values of scales 2^60 times as large and more, P may be below fp32's
-      // range and the weight not.  (Where it is below it without that, the weight is
-      // below 2^-60 of the row's sum, whose bits it does not reach.)
-      bool low;
-      if constexpr (ONE) {
-        log_top = fmaxf(log_top, log_v[t][0]);
-        low = log_top - log_v[t][0] > 60.f;
-      } else {
-        low = least < kLowWeight;
-        if (low && !inside[t]) {  // most of it is masked
-          low = false;
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) low = low || (sc[t][m][h][i] > kNone && sc[t][m][h][i] - ref[m][i >> 1] < -100.f);
-        }
-        low = __any_sync(~0u, low);
-      }
-      if (low) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int e = ONE ? 0 : h * 2 + (i & 1);
-              const float x = exponent(m, h, i), w = exp2_fast(x);
-              if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[t][e]) - w * inverse[t][e];
-            }
-      }
-    }
-
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (!there(t)) break;
-      if (moves[t]) {
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[m][i][e] *= gain[t][m][e >> 1];
-      }
-      uint32_t nans = 0u;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {  // 32 columns; NaN codes in a tile that not every row sees whole are left out
-        uint32_t vb[4];
-        ldmatrix4_trans(vb, tile + t * 2 * S::kTileBytes + S::kTileBytes + piece_at(i));
-        if (!inside[t]) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t bad = nan_codes(vb[e]);
-            nans |= bad;
-            vb[e] &= ~((bad >> 7) * 0xFFu);
-          }
-        }
-        uint32_t even_v[4], odd_v[4];  // a column's two positions together
+    for (int i = 0; i < kColPieces; ++i) {  // 32 columns; NaN codes in a tile that not every row sees whole are left out
+      uint32_t vb[4];
+      ldmatrix4_trans(vb, tile + S::kTileBytes + col_at[i % kColAt] + i / kColAt * 128);
+      if (!inside) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t both = __byte_perm(vb[e], 0u, 0x3120);
-          even_v[e] = low_codes(both);
-          odd_v[e] = high_codes(both);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          mma(acc[m][4 * i], pf[t][m], even_v[0], even_v[1]);
-          mma(acc[m][4 * i + 1], pf[t][m], odd_v[0], odd_v[1]);
-          mma(acc[m][4 * i + 2], pf[t][m], even_v[2], even_v[3]);
-          mma(acc[m][4 * i + 3], pf[t][m], odd_v[2], odd_v[3]);
+          const uint32_t bad = nan_codes(vb[e]);
+          nans |= bad;
+          vb[e] &= ~((bad >> 7) * 0xFFu);
         }
       }
-      if (__any_sync(~0u, nans != 0u)) {  // a row that sees a NaN code has NaN in its column
-        const uint8_t* v_tile = tile_ptr + t * 2 * S::kTileBytes + S::kTileBytes;
-        const int a = tile_of(turn * NT + t) * kTile;
-        for (int j = 0; j < kTile; ++j) {
+      uint32_t even_v[4], odd_v[4];  // a column's two positions together
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            const uint32_t bad = nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(j, i) + 4 * c));
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t both = __byte_perm(vb[e], 0u, 0x3120);
+        even_v[e] = low_codes(both);
+        odd_v[e] = high_codes(both);
+      }
 #pragma unroll
-            for (int m = 0; m < MT; ++m) {
-              const bool va = sees(pos_a[m], a + j, t), vb = sees(pos_b[m], a + j, t);
+      for (int m = 0; m < MT; ++m) {
+        mma(acc[m][4 * i], pf[m], even_v[0], even_v[1]);
+        mma(acc[m][4 * i + 1], pf[m], odd_v[0], odd_v[1]);
+        mma(acc[m][4 * i + 2], pf[m], even_v[2], even_v[3]);
+        mma(acc[m][4 * i + 3], pf[m], odd_v[2], odd_v[3]);
+      }
+    }
+    if (__any_sync(~0u, nans != 0u)) {  // a row that sees a NaN code has NaN in its column
+      const uint8_t* v_tile = tile_ptr + S::kTileBytes;
+      for (int j = 0; j < kTile; ++j) {
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((bad >> (8 * e + 7)) & 1u) {
-                  if (va) acc[m][2 * i + (e & 1)][e >> 1] = NAN;
-                  if (vb) acc[m][2 * i + (e & 1)][2 + (e >> 1)] = NAN;
-                }
+        for (int i = 0; i < D / 16 / kCols; ++i) {
+          const uint32_t bad =
+              nan_codes(*reinterpret_cast<const uint32_t*>(v_tile + swizzled(j, i + part * (D / 16 / kCols)) + 4 * c));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            const bool va = sees(pos_a[m], a + j), vb = sees(pos_b[m], a + j);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((bad >> (8 * e + 7)) & 1u) {
+                if (va) acc[m][2 * i + (e & 1)][e >> 1] = NAN;
+                if (vb) acc[m][2 * i + (e & 1)][2 + (e >> 1)] = NAN;
               }
             }
           }
@@ -722,12 +713,12 @@ attend8_kernel(const __grid_constant__ Params p) {
     for (int side = 0; side < 2; ++side) {
       const int row = (rw * MT + m) * 16 + r + 8 * side;
       if (row < rows_here) {
-        float* to = left + kg * kLeft + row * S::kSumRow + 4 * c;
+        float* to = left + kg * kLeft + row * S::kSumRow + part * (D / kCols) + 4 * c;
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i)
+        for (int i = 0; i < D / 16 / kCols; ++i)
           *reinterpret_cast<float4*>(to + 16 * i) = make_float4(acc[m][2 * i][2 * side], acc[m][2 * i + 1][2 * side],
                                                                 acc[m][2 * i][2 * side + 1], acc[m][2 * i + 1][2 * side + 1]);
-        if (c == 0)
+        if (c == 0 && part == 0)
           *reinterpret_cast<float2*>(left + kg * kLeft + kStat + 2 * row) = make_float2(ref[m][side], l[m][side]);
       }
     }
@@ -866,6 +857,21 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
       pack_bf16(x * inv, y * inv);
 }
 
+// How a sequence and head is shared out.  Not by max_new: a row's sums are the same
+// whatever rows are beside it.  All CTAs of one sequence take its tiles in turn: as many
+// as the GPU holds of those for 32 rows on heads of 64 and 128 (one of 32771, 8 heads of
+// 128: 24.6 us with 303, 29.4 with 220, 33.7 with 455), of those for 64 rows on heads of
+// 256 (2 with a window of 4096, 4 heads, 64 rows each: 20.5 us with 151, 28.9 with 303;
+// of 3 with 4 rows each 14.8 and 13.9; 1 of 32771 without a window 43 and 50, 27 and 22).
+// From 4 sequences on, whose lengths are their own, a CTA takes a chunk of positions, so
+// that a sequence has CTAs by its length: chunks that cut max_len of all into two or
+// three CTAs for each that the GPU holds (16 ragged on 4 heads of 64: 19.6 us with 1213,
+// 20.5 with 909, 23.9 with 1820; 16 on 8 of 128: 19.8 with 909, 25.3 with 606, 18.1 with
+// 1213, but 16 of 3000 each 25.4, 28.5 and 28.1; 8 on 4 of 256: 24.5 with 455, 23.7 with
+// 606, but of 9000 each 35.6 and 44.0).  A chunk has an end, so that the last ones of
+// long calls end together (64 ragged ones of 9000 on 8 heads of 256: 126 us with 64 tiles
+// at most, 147 with 128).  Calls of few CTAs are joined in a cluster (one of 611 on 8
+// heads: 4.8 us, and 5.6 with a second kernel).
 struct Split {
   int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; tiles of a chunk, or 0
 };
@@ -875,10 +881,12 @@ Split split_for(const w4g128_attend8_args& a) {
   const long long pairs = static_cast<long long>(a.kv_heads) * a.count;
   const long long tiles = (span + kTile - 1) / kTile, groups = groups_of(a.head_dim);
   const long long target = a.head_dim == 64 ? 455 : a.head_dim == 128 ? 303 : 151;
-  const long long want = std::min(std::max<long long>(1, target / pairs), (tiles + groups - 1) / groups);
-  if (want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1, 0};
-  if (a.count > 1 && a.window == 0) {
-    const long long some = target * 3 / 2;
+  const long long most = std::max<long long>(1, target / pairs), whole = (tiles + groups - 1) / groups;
+  const long long want = std::min(most, whole);
+  const bool chunks = a.count >= kChunkedFrom && a.window == 0 && whole > most;
+  if (!chunks && want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1, 0};
+  if (chunks) {
+    const long long some = a.head_dim == 64 ? 1213 : a.head_dim == 128 ? 909 : 455;
     const long long chunk = std::min<long long>(kMostChunk, (tiles * pairs + some * groups - 1) / (some * groups) * groups);
     return {1, static_cast<int>((tiles + chunk - 1) / chunk), static_cast<int>(chunk)};
   }
