@@ -4,9 +4,16 @@
 // A head's row is pieces of 8 values, 16 bytes a lane; the other half of a rotated
 // pair is in another lane of the same warp (or the same piece), so it comes by
 // shuffle, and every byte is read and written once.
-//   * up to 16 new rows a sequence (a decode or verify step): a warp for each head.
-//     What takes time is the chain length -> rows -> cosines -> store.
-//   * prompts: row by row what needs no block, by blocks what goes into 8 bits.
+//   * few rows (a decode or verify step): a warp for each head.  What takes time is
+//     the chain length -> rows -> cosines -> store: 2.5 us for one token, 2.7 for 16
+//     sequences of up to 3 rows in 8 bits, of which the launch alone is most.
+//   * many: row by row what needs no block, by blocks what goes into 8 bits, each on
+//     its part of the CTAs.  A prompt of 8191 rows (32 + 2 x 8 heads of 128, blocks of
+//     64) takes 41.0 us, 4.5 TB/s of the 185 MB that it reads and writes; rows alone on
+//     all CTAs would take 24, blocks alone 13.  Two prompts of 2049 rows of 16 + 2 x 4
+//     heads of 256 in bf16 take 21.8 us, 4.6 TB/s.  What bounds both is the latency of
+//     the loads and of the angles at the 16 warps an SM that the values in registers
+//     leave; the next heads are on their way meanwhile (without that 45.8 us).
 // The angle p f of position p is a 64-bit integer of 2^-64 turns, p times f / 2 pi
 // rounded to that: exact modulo a turn but for p 2^-64 and the 2^-53 of f / 2 pi in
 // 64 bits.  Its multiple of a quarter turn goes into signs, so that the fp32
@@ -28,7 +35,8 @@ namespace {
 constexpr int kChunk = 64;  // positions, a multiple of every block
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
-constexpr int kWorkers = 303;  // CTAs of a prompt's call: two an SM, but the one that looks for errors
+// CTAs of a prompt's call: two an SM, but the one that looks for errors (41.0 us for 8191 rows, and 47.3 with twice as many)
+constexpr int kWorkers = 303;
 constexpr size_t kWorkspace = 256;
 constexpr int kLowestScale = -100;
 
@@ -286,16 +294,16 @@ __global__ void __launch_bounds__(kThreads) append_few_kernel(const __grid_const
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
 
   grid_dependency_wait();
-  if (blockIdx.x == 0) {
-    if (blockIdx.y == 0 && blockIdx.z == 0) check_all(p);
+  if (blockIdx.z == 0) {
+    if (blockIdx.x == 0 && blockIdx.y == 0) check_all(p);
     return;
   }
   const int pair_group = p.half > 0 ? tid / p.by_half : 0;
   const int pair = tid - pair_group * p.half;
   double freq = 0.0;
   if (p.half > 0) freq = p.freqs[pair];
-  const int b = blockIdx.z;
-  const Rows rows = rows_of(p, span_of(p, b), blockIdx.x - 1);
+  const int b = blockIdx.z - 1;
+  const Rows rows = rows_of(p, span_of(p, b), blockIdx.x);
   if (rows.live <= 0) return;
   for (int i = tid; i < kWarps * kChunk; i += kThreads) (&s_top[0][0])[i] = 0u;
   prepare_rows(p, b, rows, freq, pair, pair_group, s_at, s_block, s_trig);
@@ -654,9 +662,15 @@ template <int D>
 cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
   p.chunks = (p.max_new + kChunk - 2) / kChunk + 1;
   cfg.blockDim = dim3(kThreads);
-  if (p.max_new <= kFewRows) {
+  // A warp for each head while there are few rows: up to 160 of up to 64 sequences in a
+  // bf16 cache (16 of 8 rows, 32 + 2 x 8 heads of 128: 4.5 us, and 4.9 row by row; of 12
+  // rows 5.6 and 5.0; 256 of one 11.5 and 5.0); in 8 bits always but for few sequences of
+  // more than 8 rows (one of 8 5.2 us, and 5.0 by blocks; of 16 8.0 and 5.1; 8 of 16 8.2
+  // and 7.5; 16 of 16 10.4 and 10.9; 256 of one 12.5 and 44).
+  const bool few = p.max_new <= kFewRows && (p.block_log2 < 0 ? p.count <= 64 && p.count * p.max_new <= 160 : p.max_new <= 8 || p.count > 8);
+  if (few) {
     const int units = 2 * p.kv_heads + p.q_heads;
-    cfg.gridDim = dim3(p.chunks + 1, (units + kThreads / 32 - 1) / (kThreads / 32), p.count);  // (the first CTA looks for errors)
+    cfg.gridDim = dim3(p.chunks, (units + kThreads / 32 - 1) / (kThreads / 32), p.count + 1);  // (the first CTA looks for errors)
     cfg.dynamicSmemBytes = static_cast<size_t>(2 * kFewRows) * p.half * sizeof(float);
     return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, p);
   }
@@ -675,7 +689,8 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
   const int most = stages + kChunk * D * static_cast<int>(sizeof(float));
   const cudaError_t e = cudaFuncSetAttribute(append_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
-  // A value of k or v costs three times a query's.
+  // A value of k or v costs three times a query's (a prompt of 8191, 32 + 2 x 8 heads of
+  // 128, 64 of them rotated pairs: 41.0 us, with twice 53.3, with four times 43.0).
   const long long kv_work = 3 * 2 * p.kv_heads;
   p.row_workers = p.q_heads == 0 ? 0 : static_cast<int>(std::min<long long>(kWorkers - 1, 1 + kWorkers * p.q_heads * 2 / (2 * p.q_heads + kv_work)));
   cfg.gridDim = dim3(1 + kWorkers);

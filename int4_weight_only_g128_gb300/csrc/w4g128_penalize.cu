@@ -5,13 +5,15 @@
 // whether it occurs at all.  Every CTA reads the whole history (from the L2: 131 KB
 // for 32771 tokens) and counts its own tokens by additions of whole numbers, whose
 // order does not matter.  (Each CTA its part of the history, counted where a token
-// belongs by additions to the shared memory of a cluster's CTAs, took three times as
-// long, 19.8 us: the frequent tokens' additions wait for one another across the
+// belongs by additions to the shared memory of a cluster's CTAs, took 19.8 us where
+// this takes 5.5: the frequent tokens' additions wait for one another across the
 // cluster.)  In the same way a list's biases leave their places in the list, of which
 // the largest stays.  Then the CTA goes over its slice, 8 tokens a thread at a time;
 // the logits and mask words are on their way while the tokens are counted.  A chain of
 // loads (settings, history) bounds one row; 16 rows of 248320 with 4099 tokens and
-// 300 biases take 11.6 us, 4.7 of them without counting (the bytes are 2.4).
+// 300 biases take 11.0 us, 1.5 TB/s (its bytes alone take 2.4 us), and 4.7 without
+// the counting, whose chain of loads, additions and barriers at three CTAs an SM is what
+// bounds it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -292,9 +294,10 @@ int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
   p.row_stride = a->row_stride; p.out_stride = a->out_stride; p.mask_row = a->mask_row; p.history_size = a->history_size;
   p.bias_size = a->bias_size; p.vocab = a->vocab;
   // Slices of 8192 tokens, or of 2048 where that makes no more CTAs than two an SM (one
-  // row of 32000: 3.5 us, and 4.3 with 8192; 16 rows of 248320: 11.6, and 26 with 2048).
-  // Long histories take more threads (one row with 32771 tokens: 6.1 us, 9.0 with 512;
-  // with 613 tokens 4.0 and 3.8, 16 rows with 4099 16.2 and 11.6).
+  // row of 32000: 3.3 us, and 4.0 with 8192; 16 rows of 248320: 11.0 us with 8192, 14.5
+  // with 4096 and 22 with 2048).  Long histories take more threads (one row with 32771
+  // tokens: 5.5 us, and 8.5 with 512; with 613 tokens 3.4 and 3.3, 16 rows with 4099 15.7
+  // and 11.0).
   p.slice = static_cast<long long>(a->rows) * ((a->vocab + 7 + 2047) / 2048) <= 304 ? 2048 : kMostSlice;
   const int ctas = (a->vocab + 7 + p.slice - 1) / p.slice;
   const bool wide = a->history_size / a->rows > 8192;

@@ -366,3 +366,29 @@ def test_streams_graphs_and_status_of_replays():
             twin.check()
             for n in ("q_out", "k_cache", "v_cache", "k_scale", "v_scale"):
                 assert torch.equal(getattr(c, n), getattr(twin, n))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,block", [(64, 0), (128, 0), (256, 0), (128, 1), (64, 16), (256, 4)])
+@pytest.mark.parametrize("new", [8, 9, 16])
+def test_few_sequences_and_many(dim, block, new):
+    """The forms for few rows and for many, on both sides of what chooses them."""
+    for count in (1, 7, 9, 10, 11):
+        seqs = [((b * 53) % 90 + 1, min((b * 7) % 90 + 1, new)) for b in range(count - 1)] + [(77, new)]
+        Call(seqs, dim=dim, block=block, max_len=100, seed=count).check()
+
+
+@pytest.mark.gpu
+def test_sequences_of_a_batch_are_sequences_alone():
+    for block in (0, 16):
+        seqs = [((b * 37) % 90 + 4, b % 3) for b in range(100)]
+        kw = dict(q_heads=4, kv_heads=2, dim=64, block=block, seed=16)
+        many, alone = Call(seqs, **kw), Call(seqs, **kw)
+        many.run()
+        lens, offsets, table = alone.lens, alone.offsets_d, alone.table
+        for b in range(len(seqs)):
+            alone.seqs, alone.lens, alone.offsets_d, alone.table = [seqs[b]], lens[b:], offsets[b:], table[b:]
+            alone.run()
+        for n in ("q_out", "k_cache", "v_cache", "k_scale", "v_scale"):
+            if getattr(many, n) is not None:
+                assert torch.equal(getattr(many, n), getattr(alone, n)), (n, block)
