@@ -396,3 +396,105 @@ def test_long_norm_of_the_error(dim, n, new, page):
     got = c.run()
     ref, got = ref[:new].flatten(1), got[:new].double().flatten(1)
     assert ((got - ref).norm(dim=1) <= (2.0 ** -8 + 2.0 ** -10) * ref.norm(dim=1)).all()
+
+
+BATCH = [(3000, 16), (1, 1), (0, 0), (5000, 3), (777, 2), (64, 16), (1024, 1), (16, 0)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,kv_heads,group,block", [(64, 2, 4, 1), (64, 1, 1, 16), (128, 3, 2, 16), (128, 2, 16, 4), (256, 2, 2, 2),
+                                                      (256, 1, 16, 16)])
+@pytest.mark.parametrize("max_len", [5000, 100000])
+def test_batches_of_ragged_sequences(dim, kv_heads, group, block, max_len):
+    """More than three sequences: a CTA takes a chunk of positions, which may lie behind the sequence's end."""
+    Call(BATCH, q_heads=kv_heads * group, kv_heads=kv_heads, dim=dim, block=block, max_len=max_len, seed=dim + group).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("max_len,lengths", [(900, (900,)), (500, (200, 333)), (6000, (5000, 9, 3000, 1111, 640))])
+def test_a_row_alone_gives_the_same_bits_in_clusters_and_chunks(dim, max_len, lengths):
+    kw = dict(q_heads=8, kv_heads=2, dim=dim, max_len=max_len, spread=4)
+    seqs = [(n, 1 + 15 * (b % 2 == 0) if n > 16 else 2) for b, n in enumerate(lengths)]
+    c = Call(seqs, seed=25, **kw)
+    together = c.run().clone()
+    for b, (n, new) in enumerate(seqs):
+        for i in sorted({0, new // 2, new - 1}):
+            one = Call([(n - new + i + 1, 1)] + [(0, 0)] * (len(seqs) - 1), seed=25, **kw)
+            one.k_cache, one.v_cache, one.k_scale, one.v_scale, one.pages = c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.pages
+            one.table = c.table[b:b + 1].repeat(len(seqs), 1)
+            r = c.offsets[b] + i
+            one.q[0] = c.q[r]
+            assert torch.equal(one.run()[0], together[r]), (b, i)
+    assert torch.equal(c.run(), together)
+
+
+@pytest.mark.gpu
+def test_values_out_of_range_in_a_batch():
+    c = Call([(2000, 2), (60, 2), (3000, 2), (80, 2), (4000, 2)], max_len=4000, seed=26)
+    clean = c.run().clone()
+    keep = c.table[2, 100].item()
+    for at, wrong in ((1, -1), (1, 4001), (3, 2 ** 31 - 1), (0, -2 ** 31)):
+        was = c.lens[at].item()
+        c.lens[at] = wrong
+        c.out.fill_(7.0)
+        got = c.run(status=w.ERR_CACHE)
+        for b in range(5):
+            rows = slice(2 * b, 2 * b + 2)
+            assert (got[rows] == 7).all() if b == at else torch.equal(got[rows], clean[rows])
+        c.lens[at] = was
+    for wrong in (-1, c.pages):
+        c.table[2, 100] = wrong
+        c.out.fill_(7.0)
+        got = c.run(status=w.ERR_CACHE)
+        assert torch.equal(got[:4], clean[:4]) and torch.equal(got[6:10], clean[6:10]) and torch.isfinite(got[4:6]).all()
+    c.table[2, 100] = keep
+    assert torch.equal(c.run(), clean)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,new", [(64, 4), (128, 4), (128, 16), (256, 1), (256, 8), (256, 10)])
+def test_nan_codes_of_few_rows_and_many(dim, new):
+    """A NaN code that every row sees makes its column NaN; one that only the last row sees, that row's."""
+    c = Call([(200, new), (40, new)], dim=dim, seed=27)
+    clean = c.run().clone()
+    for pos, seen in ((77, new), (199, 1)):
+        page = c.table[0, pos // 16].long()
+        cols = torch.tensor([0, 5, 31, 32, dim // 2 - 1, dim // 2, dim - 1], device="cuda")
+        was = c.v_cache[page, pos % 16, 1, cols].clone()
+        c.v_cache[page, pos % 16, 1, cols] = 0xFF
+        want = clean.clone()
+        want[new - seen:new, 2:, cols] = float("nan")
+        got = c.run()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+        c.v_cache[page, pos % 16, 1, cols] = was
+
+
+@pytest.mark.gpu
+def test_a_wide_batch_of_short_sequences():
+    seqs = [((b * 29) % 70, min((b * 29) % 70, b % 3)) for b in range(400)]
+    Call(seqs, q_heads=4, kv_heads=2, dim=64, seed=28).check()
+
+
+@pytest.mark.gpu
+def test_graphs_captured_with_one_workspace():
+    """Two captured calls that share a workspace, replayed one after the other."""
+    calls = [Call([(2500, 3)], q_heads=8, kv_heads=2, dim=128, seed=29), Call([(1900, 16)], q_heads=8, kv_heads=2, dim=128, seed=30,
+                                                                               max_len=2500)]
+    want = [c.run().clone() for c in calls]
+    args = [c.args() for c in calls]
+    ws = torch.empty(max(w.w4g128_attend8_workspace_bytes(a) for a in args), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for a in args:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            w.w4g128_attend8(a, ws)
+    for c in calls:
+        c.out.fill_(7.0)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    for c, o in zip(calls, want):
+        assert torch.equal(c.out.view(c.rows, c.Hq, c.D)[:c.rows - 1], o[:c.rows - 1])
