@@ -59,6 +59,7 @@ constexpr float kLowWeight = 0x1p-120f;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr int kMostCluster = 16;
 constexpr int kMostChunk = 64;  // tiles
+constexpr int kMostCtas = 16384;  // whole chunks of a call, and so many partial results
 constexpr int kChunkedFrom = 4;  // sequences
 
 struct Params {
@@ -870,7 +871,10 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
 // 1213, but 16 of 3000 each 25.4, 28.5 and 28.1; 8 on 4 of 256: 24.5 with 455, 23.7 with
 // 606, but of 9000 each 35.6 and 44.0).  A chunk has an end, so that the last ones of
 // long calls end together (64 ragged ones of 9000 on 8 heads of 256: 126 us with 64 tiles
-// at most, 147 with 128).  Calls of few CTAs are joined in a cluster (one of 611 on 8
+// at most, 147 with 128).  But max_len may be far above the lengths: there are 16384
+// whole chunks at most, most of them without a position (max_len 131072: 64 of 4000 on 8 heads
+// of 128 137 us, 183 without that limit; 256 of up to 1000 on 8 of 64 60 and 334; with a
+// limit of 8192 130 and 53, but 64 of up to 9000 on 8 of 256 299 where this takes 200).  Calls of few CTAs are joined in a cluster (one of 611 on 8
 // heads: 4.8 us, and 5.6 with a second kernel).
 struct Split {
   int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; tiles of a chunk, or 0
@@ -887,7 +891,8 @@ Split split_for(const w4g128_attend8_args& a) {
   if (!chunks && want <= kMostCluster && want * pairs <= 128) return {static_cast<int>(want), 1, 0};
   if (chunks) {
     const long long some = a.head_dim == 64 ? 1213 : a.head_dim == 128 ? 909 : 455;
-    const long long chunk = std::min<long long>(kMostChunk, (tiles * pairs + some * groups - 1) / (some * groups) * groups);
+    auto of_ctas = [&](long long n) { return (tiles * pairs + n * groups - 1) / (n * groups) * groups; };
+    const long long chunk = std::max(std::min<long long>(kMostChunk, of_ctas(some)), of_ctas(kMostCtas));
     return {1, static_cast<int>((tiles + chunk - 1) / chunk), static_cast<int>(chunk)};
   }
   return {1, static_cast<int>(want), 0};

@@ -498,3 +498,13 @@ def test_graphs_captured_with_one_workspace():
     torch.cuda.synchronize()
     for c, o in zip(calls, want):
         assert torch.equal(c.out.view(c.rows, c.Hq, c.D)[:c.rows - 1], o[:c.rows - 1])
+
+
+@pytest.mark.gpu
+def test_a_batch_far_below_its_longest_length():
+    """max_len cuts the sequences into far more chunks than they have."""
+    c = Call([(700 + 97 * b, b % 3) for b in range(40)], q_heads=8, kv_heads=4, dim=64, max_len=1 << 18, seed=31)
+    # Chunks of at least 1 / 16384 of all positions: 16384 and one more (the last, shorter one) for each of 160 pairs of
+    # a sequence and head, each with 2 x 2 rows (heads that share one, new tokens) of 64 sums, a reference and a sum.
+    assert w.w4g128_attend8_workspace_bytes(c.args()) <= 256 + (16384 + 160) * 4 * (64 + 2) * 4
+    c.check()
