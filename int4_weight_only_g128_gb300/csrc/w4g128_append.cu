@@ -399,12 +399,98 @@ template <int N>
 __device__ __forceinline__ void cp_async_wait_group() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-constexpr int kRowBatch = 8;  // pieces of a lane at once: 8 heads of 256, 16 of 128, 32 of 64
+__device__ __forceinline__ float low_f(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float high_f(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+// Two values, each operation on both (as one instruction).
+__device__ __forceinline__ unsigned long long two(float lo, float hi) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ unsigned long long two_of(uint32_t v) { return two(low_f(v), high_f(v)); }
+__device__ __forceinline__ unsigned long long mul_two(unsigned long long a, unsigned long long b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ unsigned long long fma_two(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint32_t pack_two(unsigned long long v) {
+  float lo, hi;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+  return pack_bf16(lo, hi);
+}
+
+// A lane's two pieces of 8 values of a head: both sides of 8 pairs, or, interleaved,
+// neighbours that hold 8 pairs; of what is not rotated any two.
+template <int D>
+struct Duo {
+  static constexpr int kDuos = D / 16;      // of a row
+  static constexpr int kHeads = 32 / kDuos; // of a warp at once
+  int sub, duo, first, second;              // the pieces' first values
+  bool turns, interleaved;
+  unsigned long long c[4], s[4], minus_s[4];  // of its pairs, two by two
+
+  __device__ __forceinline__ Duo(const Params& p, int lane) {
+    sub = lane / kDuos;
+    duo = lane % kDuos;
+    const int side = p.half / 8;  // pieces of one side of the pairs
+    interleaved = p.interleaved != 0;
+    turns = duo < side;
+    first = (interleaved ? 2 * duo : turns ? duo : duo + side) * 8;
+    second = interleaved ? first + 8 : first + (turns ? side : kDuos - side) * 8;
+  }
+  __device__ __forceinline__ void look(const float* cosines, const float* sines) {
+    if (!turns) return;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 x = *reinterpret_cast<const float4*>(cosines + 8 * duo + 4 * h);
+      const float4 y = *reinterpret_cast<const float4*>(sines + 8 * duo + 4 * h);
+      c[2 * h] = two(x.x, x.y); c[2 * h + 1] = two(x.z, x.w);
+      s[2 * h] = two(y.x, y.y); s[2 * h + 1] = two(y.z, y.w);
+      minus_s[2 * h] = two(-y.x, -y.y); minus_s[2 * h + 1] = two(-y.z, -y.w);
+    }
+  }
+  __device__ __forceinline__ static uint32_t turned_pair(uint32_t v, float c, float s) {
+    const float a = low_f(v), b = high_f(v);
+    return pack_bf16(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
+  }
+  __device__ __forceinline__ void rotate(uint4& one, uint4& other) const {
+    uint32_t a[4] = {one.x, one.y, one.z, one.w}, b[4] = {other.x, other.y, other.z, other.w};
+    if (interleaved) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float c0, c1, s0, s1;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(c[i]));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s[i]));
+        uint32_t& v0 = i < 2 ? a[2 * i] : b[2 * i - 4];
+        uint32_t& v1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
+        v0 = turned_pair(v0, c0, s0);
+        v1 = turned_pair(v1, c1, s1);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long x = two_of(a[i]), y = two_of(b[i]);
+        a[i] = pack_two(fma_two(x, c[i], mul_two(y, minus_s[i])));
+        b[i] = pack_two(fma_two(y, c[i], mul_two(x, s[i])));
+      }
+    }
+    one = make_uint4(a[0], a[1], a[2], a[3]);
+    other = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+};
+
+constexpr int kRowBatch = 4;  // pairs of pieces of a lane at once: 8 heads of 256, 16 of 128, 32 of 64
 template <int D>
 __device__ void append_rows(const Params& p, int worker, int workers, float* trig) {
-  using P = Piece<D>;
-  constexpr int kWarps = kThreads / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  using P = Duo<D>;
+  constexpr int kWarps = kThreads / 32, kHeads = kRowBatch * P::kHeads;
+  const int lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
   constexpr int kSteps = D / 64;  // pairs of a lane
   unsigned long long step[kSteps];
 #pragma unroll
@@ -415,43 +501,52 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
   const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
   const unsigned all = p.row_items, stride = workers * kWarps;
   struct Item {  // a part of a row's heads
-    bool real;
-    int b, pos, h0;
+    bool real, queries;  // queries: all of them
+    int pos, h0, id;     // id: of the row's page, where it is asked for
     long long row;
-    uint4 raw[kRowBatch];
+    uint4 raw[2 * kRowBatch];
   };
+  const uint16_t* q = p.q + my.sub * D;
+  uint16_t* q_out = p.q_out + my.sub * D;
   auto load = [&](unsigned item, Item& it) {
     it.real = false;
     if (item >= all) return;
     const int which = static_cast<int>(item) / p.by_parts;
-    it.h0 = (static_cast<int>(item) - which * static_cast<int>(p.by_parts.d)) * kRowBatch * P::kRows + my.sub;
-    it.b = which / p.by_new;
-    const int i_new = which - it.b * p.max_new;
-    const Span s = span_of(p, it.b);
+    const int h0 = (static_cast<int>(item) - which * static_cast<int>(p.by_parts.d)) * kHeads;
+    const int b = which / p.by_new, i_new = which - b * p.max_new;
+    const Span s = span_of(p, b);
     it.pos = s.start + i_new;
     it.row = s.first_row + i_new;
+    it.h0 = h0;
+    it.queries = h0 + kHeads <= p.q_heads;
     it.real = s.ok && i_new < s.n && it.pos >= 0;
     if (!it.real) return;
+    if (it.queries) {
+      const uint16_t* from = q + it.row * p.q_row + static_cast<long long>(h0) * D;
+#pragma unroll
+      for (int i = 0; i < kRowBatch; ++i) {
+        it.raw[2 * i] = *reinterpret_cast<const uint4*>(from + i * P::kHeads * D + my.first);
+        it.raw[2 * i + 1] = *reinterpret_cast<const uint4*>(from + i * P::kHeads * D + my.second);
+      }
+      return;
+    }
+    if (p.block_log2 < 0) it.id = p.table[static_cast<long long>(b) * p.table_row + it.pos / p.by_page];
 #pragma unroll
     for (int i = 0; i < kRowBatch; ++i) {
-      const int h = it.h0 + i * P::kRows;
+      const int h = h0 + i * P::kHeads + my.sub;
       const uint16_t* from = h < p.q_heads ? p.q + it.row * p.q_row + static_cast<long long>(h) * D
                                            : (h < p.q_heads + p.kv_heads ? p.k_new : p.v_new) + it.row * p.kv_row +
                                                  static_cast<long long>((h - p.q_heads) % p.by_kv) * D;
-      it.raw[i] = h < heads ? *(reinterpret_cast<const uint4*>(from) + my.piece) : make_uint4(0u, 0u, 0u, 0u);
+      it.raw[2 * i] = h < heads ? *reinterpret_cast<const uint4*>(from + my.first) : make_uint4(0u, 0u, 0u, 0u);
+      it.raw[2 * i + 1] = h < heads ? *reinterpret_cast<const uint4*>(from + my.second) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   Item next;
   load(worker * kWarps + warp, next);
   for (unsigned item = worker * kWarps + warp; item < all; item += stride) {
-    const Item it = next;
+    Item it = next;
     load(item + stride, next);  // on its way while this one is worked on
     if (!it.real) continue;
-    long long at = -1;
-    if (p.block_log2 < 0) {
-      const int page = it.pos / p.by_page, id = p.table[static_cast<long long>(it.b) * p.table_row + page];
-      if (id >= 0 && id < p.pages) at = id * p.page_stride + (it.pos - page * static_cast<int>(p.by_page.d)) * p.slot_stride;
-    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
@@ -464,16 +559,30 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
     __syncwarp();
     my.look(cosines, sines);
 #pragma unroll
+    for (int i = 0; i < kRowBatch; ++i)
+      if (my.turns && it.h0 + i * P::kHeads + my.sub < p.q_heads + p.kv_heads) my.rotate(it.raw[2 * i], it.raw[2 * i + 1]);
+    if (it.queries) {
+      uint16_t* to = q_out + it.row * p.q_out_row + static_cast<long long>(it.h0) * D;
+#pragma unroll
+      for (int i = 0; i < kRowBatch; ++i) {
+        *reinterpret_cast<uint4*>(to + i * P::kHeads * D + my.first) = it.raw[2 * i];
+        *reinterpret_cast<uint4*>(to + i * P::kHeads * D + my.second) = it.raw[2 * i + 1];
+      }
+      continue;
+    }
+    long long at = -1;
+    if (p.block_log2 < 0 && it.id >= 0 && it.id < p.pages)
+      at = it.id * p.page_stride + (it.pos - it.pos / p.by_page * static_cast<int>(p.by_page.d)) * p.slot_stride;
+#pragma unroll
     for (int i = 0; i < kRowBatch; ++i) {
-      const int h = it.h0 + i * P::kRows;
+      const int h = it.h0 + i * P::kHeads + my.sub;
       const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
-      float x[8];
-      my.rotate(it.raw[i], !is_v, x);
       if (h >= heads || (!is_q && at < 0)) continue;
       const int kv = (h - p.q_heads) % p.by_kv;
       uint16_t* to = is_q ? p.q_out + it.row * p.q_out_row + static_cast<long long>(h) * D
                           : static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + at + kv * p.head_stride;
-      *(reinterpret_cast<uint4*>(to) + my.piece) = is_v ? it.raw[i] : packed(x);
+      *reinterpret_cast<uint4*>(to + my.first) = it.raw[2 * i];
+      *reinterpret_cast<uint4*>(to + my.second) = it.raw[2 * i + 1];
     }
   }
 }
@@ -675,7 +784,7 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
     return cudaLaunchKernelEx(&cfg, append_few_kernel<D>, p);
   }
   // Row by row: a part of a row's heads at a time, while their number fits.
-  constexpr int kHeads = kRowBatch * Piece<D>::kRows;
+  constexpr int kHeads = kRowBatch * Duo<D>::kHeads;
   const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
   const long long rows = static_cast<long long>(p.count) * p.max_new, parts = std::max(1, (heads + kHeads - 1) / kHeads);
   p.by_new = divisor(p.max_new);
