@@ -1,19 +1,20 @@
 // Rotated queries, and rotated keys and values put into a paged cache
 // (w4g128_append), in one launch.
 //
-// A head's row is pieces of 8 values, 16 bytes a lane; the other half of a rotated
-// pair is in another lane of the same warp (or the same piece), so it comes by
-// shuffle, and every byte is read and written once.
-//   * few rows (a decode or verify step): a warp for each head.  What takes time is
-//     the chain length -> rows -> cosines -> store: 2.5 us for one token, 2.7 for 16
-//     sequences of up to 3 rows in 8 bits, of which the launch alone is most.
-//   * many: row by row what needs no block, by blocks what goes into 8 bits, each on
-//     its part of the CTAs.  A prompt of 8191 rows (32 + 2 x 8 heads of 128, blocks of
-//     64) takes 41.0 us, 4.5 TB/s of the 185 MB that it reads and writes; rows alone on
-//     all CTAs would take 24, blocks alone 13.  Two prompts of 2049 rows of 16 + 2 x 4
-//     heads of 256 in bf16 take 21.8 us, 4.6 TB/s.  What bounds both is the latency of
-//     the loads and of the angles at the 16 warps an SM that the values in registers
-//     leave; the next heads are on their way meanwhile (without that 45.8 us).
+// A head's row is pieces of 8 values, 16 bytes, and every byte is read and written once.
+//   * few rows (a decode or verify step): a warp for each head, a piece a lane; the other
+//     side of its pairs comes by shuffle.  What takes time is the chain length -> rows ->
+//     cosines -> store: 2.5 us for one token, 2.7 for 16 sequences of up to 3 rows in 8
+//     bits, of which the launch alone is most.
+//   * many: a lane has two pieces, both sides of 8 pairs, and works on two values with
+//     one instruction, since here instructions count (a piece a lane, with shuffles and
+//     an address for each, took 41.0 us where this takes 32.6).  Row by row what needs no
+//     block, by blocks what goes into 8 bits, each on its part of the CTAs.  A prompt of
+//     8191 rows (32 + 2 x 8 heads of 128, blocks of 64) takes 32.6 us, 5.6 TB/s of the 184
+//     MB that it reads and writes; of as many into bf16 (201 MB) 35.3, 5.7 TB/s.  Two
+//     prompts of 2049 rows of 16 + 2 x 4 heads of 256 in bf16 take 21.1, 4.8 TB/s, for 100
+//     MB: start and end take 3 us of it, and 12294 pieces of work on 2424 warps a sixth
+//     round for some.
 // The angle p f of position p is a 64-bit integer of 2^-64 turns, p times f / 2 pi
 // rounded to that: exact modulo a turn but for p 2^-64 and the 2^-53 of f / 2 pi in
 // 64 bits.  Its multiple of a quarter turn goes into signs, so that the fp32
@@ -35,7 +36,7 @@ namespace {
 constexpr int kChunk = 64;  // positions, a multiple of every block
 constexpr int kThreads = 256;
 constexpr int kFewRows = 16;
-// CTAs of a prompt's call: two an SM, but the one that looks for errors (41.0 us for 8191 rows, and 47.3 with twice as many)
+// CTAs of a prompt's call: two an SM, but the one that looks for errors (a third an SM, with the registers that leaves, takes 27 us where this takes 21)
 constexpr int kWorkers = 303;
 constexpr size_t kWorkspace = 256;
 constexpr int kLowestScale = -100;
@@ -407,7 +408,9 @@ __device__ __forceinline__ unsigned long long two(float lo, float hi) {
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
   return r;
 }
-__device__ __forceinline__ unsigned long long two_of(uint32_t v) { return two(low_f(v), high_f(v)); }
+__device__ __forceinline__ void split(unsigned long long v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
 __device__ __forceinline__ unsigned long long mul_two(unsigned long long a, unsigned long long b) {
   unsigned long long r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -418,12 +421,6 @@ __device__ __forceinline__ unsigned long long fma_two(unsigned long long a, unsi
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-__device__ __forceinline__ uint32_t pack_two(unsigned long long v) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-  return pack_bf16(lo, hi);
-}
-
 // A lane's two pieces of 8 values of a head: both sides of 8 pairs, or, interleaved,
 // neighbours that hold 8 pairs; of what is not rotated any two.
 template <int D>
@@ -454,35 +451,93 @@ struct Duo {
       minus_s[2 * h] = two(-y.x, -y.y); minus_s[2 * h + 1] = two(-y.z, -y.w);
     }
   }
-  __device__ __forceinline__ static uint32_t turned_pair(uint32_t v, float c, float s) {
-    const float a = low_f(v), b = high_f(v);
-    return pack_bf16(fmaf(a, c, -(b * s)), fmaf(b, c, a * s));
-  }
-  __device__ __forceinline__ void rotate(uint4& one, uint4& other) const {
-    uint32_t a[4] = {one.x, one.y, one.z, one.w}, b[4] = {other.x, other.y, other.z, other.w};
+  // The values of both pieces, two by two, rotated.
+  __device__ __forceinline__ void turn(const uint4& one, const uint4& other, unsigned long long (&x)[8]) const {
+    unpack(one, other, x);
     if (interleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float c0, c1, s0, s1;
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(c0), "=f"(c1) : "l"(c[i]));
-        asm("mov.b64 {%0, %1}, %2;" : "=f"(s0), "=f"(s1) : "l"(s[i]));
-        uint32_t& v0 = i < 2 ? a[2 * i] : b[2 * i - 4];
-        uint32_t& v1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-        v0 = turned_pair(v0, c0, s0);
-        v1 = turned_pair(v1, c1, s1);
+      for (int i = 0; i < 8; ++i) {
+        float a, b, c0, c1, s0, s1;
+        split(x[i], a, b);
+        split(c[i / 2], c0, c1);
+        split(s[i / 2], s0, s1);
+        const float cs = i & 1 ? c1 : c0, sn = i & 1 ? s1 : s0;
+        x[i] = two(fmaf(a, cs, -(b * sn)), fmaf(b, cs, a * sn));
       }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const unsigned long long x = two_of(a[i]), y = two_of(b[i]);
-        a[i] = pack_two(fma_two(x, c[i], mul_two(y, minus_s[i])));
-        b[i] = pack_two(fma_two(y, c[i], mul_two(x, s[i])));
+        const unsigned long long a = x[i], b = x[4 + i];
+        x[i] = fma_two(a, c[i], mul_two(b, minus_s[i]));
+        x[4 + i] = fma_two(b, c[i], mul_two(a, s[i]));
       }
     }
-    one = make_uint4(a[0], a[1], a[2], a[3]);
-    other = make_uint4(b[0], b[1], b[2], b[3]);
+  }
+  __device__ __forceinline__ static void unpack(const uint4& one, const uint4& other, unsigned long long (&x)[8]) {
+    const uint32_t v[8] = {one.x, one.y, one.z, one.w, other.x, other.y, other.z, other.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = two(low_f(v[i]), high_f(v[i]));
+  }
+  __device__ __forceinline__ void rotate(uint4& one, uint4& other) const {
+    unsigned long long x[8];
+    turn(one, other, x);
+    uint32_t v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float lo, hi;
+      split(x[i], lo, hi);
+      v[i] = pack_bf16(lo, hi);
+    }
+    one = make_uint4(v[0], v[1], v[2], v[3]);
+    other = make_uint4(v[4], v[5], v[6], v[7]);
   }
 };
+
+// The largest finite magnitude; what is infinite becomes NaN, which takes no part.
+__device__ __forceinline__ float magnitude_two(unsigned long long (&x)[8]) {
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo, hi;
+    split(x[i], lo, hi);
+    top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+  }
+  if (top == INFINITY) {
+    top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float lo, hi;
+      split(x[i], lo, hi);
+      lo = fmaf(lo, 0.f, lo);
+      hi = fmaf(hi, 0.f, hi);
+      x[i] = two(lo, hi);
+      top = fmaxf(top, fmaxf(fabsf(lo), fabsf(hi)));
+    }
+  }
+  return top;
+}
+// The codes of 8 values.
+__device__ __forceinline__ uint2 coded_two(const unsigned long long* x, float scale) {
+  uint32_t code[4];
+  if ((__float_as_uint(scale) & 0x007FFFFFu) == 0u) {
+    const float inverse = exp2_of(127 - static_cast<int>(__float_as_uint(scale) >> 23));
+    const unsigned long long by = two(inverse, inverse);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      split(mul_two(x[e], by), lo, hi);
+      code[e] = to_e4m3x2(lo, hi);
+    }
+  } else {  // (a scale that another program set need not be a power of two)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float lo, hi;
+      split(x[e], lo, hi);
+      code[e] = to_e4m3x2(__fdiv_rn(lo, scale), __fdiv_rn(hi, scale));
+    }
+  }
+  return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+}
 
 constexpr int kRowBatch = 4;  // pairs of pieces of a lane at once: 8 heads of 256, 16 of 128, 32 of 64
 template <int D>
@@ -595,15 +650,14 @@ __global__ void __launch_bounds__(kThreads, 2) append_rows_kernel(const __grid_c
   else append_rows<D>(p, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1, s_trig);
 }
 
-template <int D>
-constexpr int kBlockStages = D == 256 ? 2 : 3;
+constexpr int kBlockStages = 2;  // (3 take room from the L1 cache: 32.9 us for 8191 rows, and 32.6)
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_constant__ Params p) {
-  using P = Piece<D>;
+  using P = Duo<D>;
   constexpr int kWarps = kThreads / 32, kWarpRows = kChunk / kWarps;  // a warp's rows of a chunk, side by side
-  constexpr int kPasses = kWarpRows / P::kRows;
-  constexpr int kStages = kBlockStages<D>;
+  constexpr int kPasses = kWarpRows / P::kHeads;  // (a warp has as many rows at once as heads of a row above)
+  constexpr int kStages = kBlockStages;
   extern __shared__ __align__(16) uint8_t s_many[];    // the stages; [live rows][half] cosines, then sines
   __shared__ long long s_at[kChunk], s_block[kChunk];  // a row's slot and scale in the caches; -1: no page
   __shared__ unsigned s_top[3][kChunk];                // a block's magnitude, of three heads in turn
@@ -627,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   if (p.half > 0) freq = p.freqs[pair];
   P my(p, lane);
   uint4* ring = reinterpret_cast<uint4*>(s_many) + tid;
-  float* s_trig = reinterpret_cast<float*>(s_many + kThreads * kPasses * kStages * 16);
+  float* s_trig = reinterpret_cast<float*>(s_many + kThreads * kPasses * kStages * 32);
   // An equal share of all (sequence, chunk, head), in order, chunk by chunk.
   const int units = 2 * p.kv_heads, workers = static_cast<int>(gridDim.x) - 1 - p.row_workers;
   const long long all = static_cast<long long>(p.count) * p.chunks * units;
@@ -649,17 +703,20 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
     const int held = rows.p0 & ((1 << p.block_log2) - 1);       // positions that the first row's block has already
     const bool real0 = s_at[0] >= 0;
     const bool one = (1 << p.block_log2) >= kWarpRows;  // a warp's rows share a block
-    auto row_of = [&](int i) { return warp * kWarpRows + i * P::kRows + my.sub - lead; };  // among the live ones, or outside
+    auto row_of = [&](int i) { return warp * kWarpRows + i * P::kHeads + my.sub - lead; };  // among the live ones, or outside
     auto block_of = [&](int r) { return (lead + r) >> p.block_log2; };
     const int block0 = block_of(0);
     auto issue = [&](int u, int stage) {
       if (u < u_end) {
         const uint16_t* src = (u >= p.kv_heads ? p.v_new : p.k_new) + rows.row0 * p.kv_row +
-                              static_cast<long long>(u >= p.kv_heads ? u - p.kv_heads : u) * D + my.piece * 8;
+                              static_cast<long long>(u >= p.kv_heads ? u - p.kv_heads : u) * D;
 #pragma unroll
         for (int i = 0; i < kPasses; ++i) {
           const int r = row_of(i);
-          if (r >= 0 && r < live) cp_async16(smem_addr(ring + (stage * kPasses + i) * kThreads), src + r * p.kv_row);
+          if (r >= 0 && r < live) {
+            cp_async16(smem_addr(ring + (stage * kPasses + i) * 2 * kThreads), src + r * p.kv_row + my.first);
+            cp_async16(smem_addr(ring + ((stage * kPasses + i) * 2 + 1) * kThreads), src + r * p.kv_row + my.second);
+          }
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -672,25 +729,35 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
       const bool is_v = u >= p.kv_heads;
       const int head = is_v ? u - p.kv_heads : u;
       float* scales = (is_v ? p.v_scale : p.k_scale) + head * p.scale_head;
-      uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + head * p.head_stride + my.piece * 8;
+      uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + head * p.head_stride;
       float was = 0.f;
       if (held > 0 && real0) was = scales[s_block[0]];
       unsigned* tops = s_top[turn];
       issue(u + kStages - 1, stage == 0 ? kStages - 1 : stage - 1);
       cp_async_wait_group<kStages - 1>();
-      float x[kPasses][8], top = 0.f;
+      unsigned long long x[kPasses][8];
+      float top = 0.f;
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
-        const int r = row_of(i), look = min(max(r, 0), live - 1);
-        if (!is_v) my.look(s_trig + look * p.half, s_trig + (live + look) * p.half);
-        const uint4 raw = r >= 0 && r < live ? ring[(stage * kPasses + i) * kThreads] : make_uint4(0u, 0u, 0u, 0u);
-        my.rotate(raw, !is_v, x[i]);
-        const float t = magnitude(x[i]);
+        const int r = row_of(i);
+        uint4 first = make_uint4(0u, 0u, 0u, 0u), second = first;
+        if (r >= 0 && r < live) {
+          first = ring[(stage * kPasses + i) * 2 * kThreads];
+          second = ring[((stage * kPasses + i) * 2 + 1) * kThreads];
+        }
+        if (!is_v && my.turns) {
+          const int look = min(max(r, 0), live - 1);
+          my.look(s_trig + look * p.half, s_trig + (live + look) * p.half);
+          my.turn(first, second, x[i]);
+        } else {
+          P::unpack(first, second, x[i]);
+        }
+        const float t = magnitude_two(x[i]);
         top = one ? fmaxf(top, t) : t;
         if (!one) {
 #pragma unroll
-          for (int d = 1; d < P::kPieces; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-          if (my.piece == 0 && r >= 0 && r < live) atomicMax(&tops[block_of(r)], __float_as_uint(top));
+          for (int d = 1; d < P::kDuos; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          if (my.duo == 0 && r >= 0 && r < live) atomicMax(&tops[block_of(r)], __float_as_uint(top));
         }
       }
       if (one) {  // (rows outside are zeros)
@@ -708,19 +775,23 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
       for (int i = 0; i < kPasses; ++i) {
         const int r = row_of(i);
         if (!one || i == 0) {
-          const int block = (warp * kWarpRows + (one ? 0 : i * P::kRows + my.sub)) >> p.block_log2;
+          const int block = (warp * kWarpRows + (one ? 0 : i * P::kHeads + my.sub)) >> p.block_log2;
           scale = scale_for(tops[block], held > 0 && block == block0, was, keeps);
         }
         if (r < 0 || r >= live || s_at[r] < 0) continue;
-        *reinterpret_cast<uint2*>(cache + s_at[r]) = coded(x[i], scale);
-        if (my.piece == 0 && !keeps && (r == 0 || block_of(r) != block_of(r - 1))) scales[s_block[r]] = scale;
+        *reinterpret_cast<uint2*>(cache + s_at[r] + my.first) = coded_two(x[i], scale);
+        *reinterpret_cast<uint2*>(cache + s_at[r] + my.second) = coded_two(x[i] + 4, scale);
+        if (my.duo == 0 && !keeps && (r == 0 || block_of(r) != block_of(r - 1))) scales[s_block[r]] = scale;
       }
       if (held > 0 && real0) {
         scale = scale_for(tops[block0], true, was, keeps);
         if (!keeps) {  // what the block has goes to the larger scale
-          for (int i = warp * P::kRows + my.sub; i < held; i += kWarps * P::kRows) {
-            uint2* at = reinterpret_cast<uint2*>(cache + s_at[0] - (held - i) * p.slot_stride);
-            *at = recoded(*at, was / scale);
+          for (int i = warp * P::kHeads + my.sub; i < held; i += kWarps * P::kHeads) {
+            uint8_t* at = cache + s_at[0] - (held - i) * p.slot_stride;
+            for (int from : {my.first, my.second}) {
+              uint2* piece = reinterpret_cast<uint2*>(at + from);
+              *piece = recoded(*piece, was / scale);
+            }
           }
         }
       }
@@ -771,12 +842,14 @@ template <int D>
 cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
   p.chunks = (p.max_new + kChunk - 2) / kChunk + 1;
   cfg.blockDim = dim3(kThreads);
-  // A warp for each head while there are few rows: up to 160 of up to 64 sequences in a
-  // bf16 cache (16 of 8 rows, 32 + 2 x 8 heads of 128: 4.5 us, and 4.9 row by row; of 12
-  // rows 5.6 and 5.0; 256 of one 11.5 and 5.0); in 8 bits always but for few sequences of
-  // more than 8 rows (one of 8 5.2 us, and 5.0 by blocks; of 16 8.0 and 5.1; 8 of 16 8.2
-  // and 7.5; 16 of 16 10.4 and 10.9; 256 of one 12.5 and 44).
-  const bool few = p.max_new <= kFewRows && (p.block_log2 < 0 ? p.count <= 64 && p.count * p.max_new <= 160 : p.max_new <= 8 || p.count > 8);
+  // A warp for each head while there are few rows: up to 64 of up to 32 sequences, 8 of
+  // one, in a bf16 cache (16 of 4 rows, 32 + 2 x 8 heads of 128: 3.5 us, and 3.8 row by
+  // row; 64 of one 4.6 and 3.8; one of 8 3.4 and 3.8; of 16 4.7 and 3.7; 256 of one 11.5
+  // and 4.0); in 8 bits always but for few sequences of more than 4 rows (one of 4 3.7 us,
+  // and 3.9 by blocks; 4 of 8 5.3 and 4.1; 8 of 8 5.4 and 5.1; 16 of 8 6.6 and 7.5; 256 of
+  // one 12.5 and 44).
+  const bool few = p.max_new <= kFewRows && (p.block_log2 < 0 ? p.count <= 32 && p.max_new <= 8 && p.count * p.max_new <= 64
+                                                              : p.max_new <= 4 || p.count > 8);
   if (few) {
     const int units = 2 * p.kv_heads + p.q_heads;
     cfg.gridDim = dim3(p.chunks, (units + kThreads / 32 - 1) / (kThreads / 32), p.count + 1);  // (the first CTA looks for errors)
@@ -794,12 +867,12 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
     cfg.gridDim = dim3(1 + kWorkers);
     return cudaLaunchKernelEx(&cfg, append_rows_kernel<D>, p);
   }
-  const int stages = kChunk * D * 2 * kBlockStages<D>;
+  const int stages = kChunk * D * 2 * kBlockStages;
   const int most = stages + kChunk * D * static_cast<int>(sizeof(float));
   const cudaError_t e = cudaFuncSetAttribute(append_many_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   if (e != cudaSuccess) return e;
   // A value of k or v costs three times a query's (a prompt of 8191, 32 + 2 x 8 heads of
-  // 128, 64 of them rotated pairs: 41.0 us, with twice 53.3, with four times 43.0).
+  // 128, 64 rotated pairs: 32.6 us, with 2.5 times 37.6, with 3.5 times 34.3).
   const long long kv_work = 3 * 2 * p.kv_heads;
   p.row_workers = p.q_heads == 0 ? 0 : static_cast<int>(std::min<long long>(kWorkers - 1, 1 + kWorkers * p.q_heads * 2 / (2 * p.q_heads + kv_work)));
   cfg.gridDim = dim3(1 + kWorkers);
