@@ -229,7 +229,8 @@ W4G128_API int w4g128_moe(const w4g128_moe_args* args, void* ws, size_t ws_bytes
  * and those earlier positions' codes are rounded to it, which is exact down to
  * 2^-6.  Codes are rounded to nearest, ties to even; what is not finite is a NaN
  * code.  The 5 leaves new rows of a block room of a factor 7 to 14 before it
- * changes.  With block = 1 a row's codes are its own; with larger blocks they
+ * changes.  A key whose exact value lies within 2^-21 of its pair's size of the
+ * middle between two codes may become either.  With block = 1 a row's codes are its own; with larger blocks they
  * also follow the rows that share the block, and a draft row that is rejected
  * leaves the scale as it needed it.
  *
@@ -296,9 +297,9 @@ W4G128_API int w4g128_append(const w4g128_append_args* args, void* ws, size_t ws
  *
  * Row m's bits depend on its own position, query and visible codes and scales
  * alone, not on the other rows of the call nor on max_new, given the same count,
- * kv_heads, head_dim, max_len, window and sinks.  A row at a negative position, or all of whose scores are
- * -inf, has out 0.  Rows of no sequence are left as they are.  Masked positions
- * take no part whatever their codes and scales hold. */
+ * kv_heads, head_dim, max_len, window and sinks.  A row at a negative position, or
+ * all of whose scores are -inf, has out 0.  Rows of no sequence are left as they
+ * are.  Masked positions take no part whatever their codes and scales hold. */
 typedef struct {
   const w4g128_bf16* q;     /* row r, head h at r * q_row + h * head_dim */
   const void* k_cache;      /* e4m3 codes: page g, slot s, head h at g * page_stride + s * slot_stride + h * head_stride */
@@ -328,7 +329,8 @@ typedef struct {
   float scale;   /* |scale| up to 2^14 */
 } w4g128_attend8_args;
 
-/* Workspace bytes of w4g128_attend8 for these sizes.  0 for arguments it would refuse. */
+/* Workspace bytes of w4g128_attend8 for these sizes: a status word and, where several CTAs share a
+ * sequence and head, their partial results in fp32.  0 for arguments it would refuse. */
 W4G128_API size_t w4g128_attend8_workspace_bytes(const w4g128_attend8_args* args);
 
 /* The attention above.  q, the caches and out: 16-byte aligned, q_row and out_row
@@ -358,7 +360,7 @@ typedef struct {
   const long long* history_start; /* [rows], or NULL: 0 */
   const int* history_len;    /* [rows], up to 2^30; not above 0: none.  NULL with history NULL alone */
   const int* prompt_len;     /* [rows], or NULL: 0 */
-  const float* repetition;   /* [rows] above 0, or NULL: 1 */
+  const float* repetition;   /* [rows], 2^-100 .. 2^100, or NULL: 1; divided by as multiplied by its inverse */
   const float* presence;     /* [rows], or NULL: 0 */
   const float* frequency;    /* [rows], or NULL: 0 */
   const int* bias_tokens;    /* [bias_size]: row r's entries are bias_offsets[r] .. bias_offsets[r + 1] - 1; or NULL: none */
