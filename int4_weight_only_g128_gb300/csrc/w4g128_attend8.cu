@@ -31,8 +31,8 @@
 // kernel.  The loop's other 14 us are neither the copies nor the products alone (without
 // copies 1.3 us less, without the products 6 less), but both, the conversions and the
 // softmax at the 8 warps an SM whose sums the registers hold.
-// 16 ragged sequences of up to 9001 on 4 heads of 64 take 19.6 us, two with a window of
-// 4096 and 16 rows each on 4 heads of 256 20.5, one of 611 with one row 4.8.
+// 16 ragged sequences of up to 9001 on 4 heads of 64 take 18.5 us, two with a window of
+// 4096 and 16 rows each on 4 heads of 256 19.8, one of 611 with one row 4.8.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -785,10 +785,10 @@ attend8_kernel(const __grid_constant__ Params p) {
   }
 }
 
-// Joins a row's CTAs (or clusters): 8 warps take them in turn and are added in order.
-template <int D>
-__global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Params p) {
-  constexpr int kWarps = 8, kPer = D / 32, kBatch = 5;
+// Joins a row's CTAs (or clusters): the warps take them in turn and are added in order.
+template <int D, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constant__ Params p) {
+  constexpr int kPer = D / 32, kBatch = kWarps == 4 ? 5 : 3;
   __shared__ float s_sum[kWarps][D];
   __shared__ float2 s_stat[kWarps];
   grid_dependency_wait();
@@ -858,7 +858,8 @@ __global__ void __launch_bounds__(256) join8_kernel(const __grid_constant__ Para
       pack_bf16(x * inv, y * inv);
 }
 
-// How a sequence and head is shared out.  Not by max_new: a row's sums are the same
+// How a sequence and head is shared out (figures with 8 warps in the second kernel, which
+// are up to 1 us above today's).  Not by max_new: a row's sums are the same
 // whatever rows are beside it.  All CTAs of one sequence take its tiles in turn: as many
 // as the GPU holds of those for 32 rows on heads of 64 and 128 (one of 32771, 8 heads of
 // 128: 24.6 us with 303, 29.4 with 220, 33.7 with 455), of those for 64 rows on heads of
@@ -959,9 +960,12 @@ cudaError_t launch_dim(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   if (e != cudaSuccess || p.clusters == 1) return e;
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
-  cfg.blockDim = dim3(256);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, join8_kernel<D>, p);
+  // 4 warps for up to 20, which they ask for at once, otherwise 16 (18.6 us for 16 ragged
+  // sequences in 12 chunks, and 20.8 with 16; 15.0 with 8 and 13.5 with 16 for one of 100003 on one head).
+  const bool few = p.clusters <= 20;
+  cfg.blockDim = dim3(few ? 128 : 512);
+  return few ? cudaLaunchKernelEx(&cfg, join8_kernel<D, 4>, p) : cudaLaunchKernelEx(&cfg, join8_kernel<D, 16>, p);
 }
 
 }  // namespace
