@@ -53,7 +53,8 @@ struct Params {
   int chunks;       // that the new rows of a sequence may touch
   int row_workers;  // CTAs that work row by row
   Divisor by_page, by_half, by_kv, by_new, by_parts;
-  unsigned row_items;  // parts of rows that are worked on one by one
+  int ragged;          // whether some sequences are known to have fewer new rows than max_new
+  unsigned row_items;  // parts of rows that are worked on one by one, if none are
   unsigned long long* status;
 };
 
@@ -539,9 +540,55 @@ __device__ __forceinline__ uint2 coded_two(const unsigned long long* x, float sc
   return make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
 }
 
+// Of ragged sequences: sums[b] is how many rows (or chunks) those before b have, so
+// that workers share what there is.  All threads of the CTA.
+__device__ void sum_up(const Params& p, bool chunks, int* sums) {
+  __shared__ int s_warps[kThreads / 32];
+  constexpr int kPer = W4G128_MAX_SEQUENCES / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int v[kPer], sum = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int b = tid * kPer + j;
+    v[j] = 0;
+    if (b < p.count) {
+      const Span s = span_of(p, b);
+      if (s.ok && s.n > 0 && s.len > 0) v[j] = chunks ? (s.len - 1) / kChunk - s.first / kChunk + 1 : s.n;
+    }
+    sum += v[j];
+  }
+  int before = sum;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int x = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before += x;
+  }
+  if (lane == 31) s_warps[warp] = before;
+  __syncthreads();
+  before -= sum;
+  for (int i = 0; i < warp; ++i) before += s_warps[i];
+  if (tid == 0) sums[0] = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    before += v[j];
+    if (tid * kPer + j < p.count) sums[tid * kPer + j + 1] = before;
+  }
+  __syncthreads();
+}
+// The sequence that the row (or chunk) `which` of all belongs to.
+__device__ __forceinline__ int sequence_of(const int* sums, int count, int which) {
+  int lo = 0, hi = count;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (sums[mid] <= which) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 constexpr int kRowBatch = 4;  // pairs of pieces of a lane at once: 8 heads of 256, 16 of 128, 32 of 64
 template <int D>
-__device__ void append_rows(const Params& p, int worker, int workers, float* trig) {
+__device__ void append_rows(const Params& p, int worker, int workers, float* trig, int* sums) {
   using P = Duo<D>;
   constexpr int kWarps = kThreads / 32, kHeads = kRowBatch * P::kHeads;
   const int lane = threadIdx.x & 31;
@@ -554,7 +601,8 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
   float* sines = cosines + D / 2;
   P my(p, lane);
   const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
-  const unsigned all = p.row_items, stride = workers * kWarps;
+  if (p.ragged) sum_up(p, false, sums);
+  const unsigned all = p.ragged ? static_cast<unsigned>(min(sums[p.count], p.rows)) * p.by_parts.d : p.row_items, stride = workers * kWarps;
   struct Item {  // a part of a row's heads
     bool real, queries;  // queries: all of them
     int pos, h0, id;     // id: of the row's page, where it is asked for
@@ -568,7 +616,8 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
     if (item >= all) return;
     const int which = static_cast<int>(item) / p.by_parts;
     const int h0 = (static_cast<int>(item) - which * static_cast<int>(p.by_parts.d)) * kHeads;
-    const int b = which / p.by_new, i_new = which - b * p.max_new;
+    const int b = p.ragged ? sequence_of(sums, p.count, which) : which / p.by_new;
+    const int i_new = which - (p.ragged ? sums[b] : b * p.max_new);
     const Span s = span_of(p, b);
     it.pos = s.start + i_new;
     it.row = s.first_row + i_new;
@@ -645,9 +694,10 @@ __device__ void append_rows(const Params& p, int worker, int workers, float* tri
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) append_rows_kernel(const __grid_constant__ Params p) {
   __shared__ __align__(16) float s_trig[kThreads / 32 * D];
+  __shared__ int s_sums[W4G128_MAX_SEQUENCES + 1];
   grid_dependency_wait();
   if (blockIdx.x == 0) check_all(p);
-  else append_rows<D>(p, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1, s_trig);
+  else append_rows<D>(p, static_cast<int>(blockIdx.x) - 1, static_cast<int>(gridDim.x) - 1, s_trig, s_sums);
 }
 
 constexpr int kBlockStages = 2;  // (3 take room from the L1 cache: 32.9 us for 8191 rows, and 32.6)
@@ -661,6 +711,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   extern __shared__ __align__(16) uint8_t s_many[];    // the stages; [live rows][half] cosines, then sines
   __shared__ long long s_at[kChunk], s_block[kChunk];  // a row's slot and scale in the caches; -1: no page
   __shared__ unsigned s_top[3][kChunk];                // a block's magnitude, of three heads in turn
+  __shared__ int s_sums[W4G128_MAX_SEQUENCES + 1];
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(~0u, tid >> 5, 0);
 
@@ -671,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   }
   const int worker = static_cast<int>(blockIdx.x) - 1;
   if (worker < p.row_workers) {
-    append_rows<D>(p, worker, p.row_workers, reinterpret_cast<float*>(s_many));
+    append_rows<D>(p, worker, p.row_workers, reinterpret_cast<float*>(s_many), s_sums);
     return;
   }
 
@@ -684,14 +735,16 @@ __global__ void __launch_bounds__(kThreads, 2) append_many_kernel(const __grid_c
   float* s_trig = reinterpret_cast<float*>(s_many + kThreads * kPasses * kStages * 32);
   // An equal share of all (sequence, chunk, head), in order, chunk by chunk.
   const int units = 2 * p.kv_heads, workers = static_cast<int>(gridDim.x) - 1 - p.row_workers;
-  const long long all = static_cast<long long>(p.count) * p.chunks * units;
+  if (p.ragged) sum_up(p, true, s_sums);
+  const long long all = (p.ragged ? s_sums[p.count] : static_cast<long long>(p.count) * p.chunks) * units;
   const long long end = all * (worker - p.row_workers + 1) / workers;
   for (long long item = all * (worker - p.row_workers) / workers; item < end;) {
     const long long which = item / units;
     const int u_first = static_cast<int>(item - which * units);
     const int u_end = static_cast<int>(min(static_cast<long long>(units), u_first + (end - item)));
     item += u_end - u_first;
-    const int b = static_cast<int>(which / p.chunks), chunk = static_cast<int>(which - static_cast<long long>(b) * p.chunks);
+    const int b = p.ragged ? sequence_of(s_sums, p.count, static_cast<int>(which)) : static_cast<int>(which / p.chunks);
+    const int chunk = static_cast<int>(which - (p.ragged ? s_sums[b] : static_cast<long long>(b) * p.chunks));
     const Rows rows = rows_of(p, span_of(p, b), chunk);
     if (rows.live <= 0) continue;
     __syncthreads();  // the last chunk's rows are done with
@@ -859,10 +912,16 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p) {
   // Row by row: a part of a row's heads at a time, while their number fits.
   constexpr int kHeads = kRowBatch * Duo<D>::kHeads;
   const int heads = p.q_heads + (p.block_log2 < 0 ? 2 * p.kv_heads : 0);
-  const long long rows = static_cast<long long>(p.count) * p.max_new, parts = std::max(1, (heads + kHeads - 1) / kHeads);
+  const long long rows = static_cast<long long>(p.count) * p.max_new;
+  const int parts = std::max(1, (heads + kHeads - 1) / kHeads);
+  // Fewer rows than count max_new: each CTA first adds the sequences' up, so that all share
+  // what there is (a prompt of 8191 beside 63 single tokens into bf16 36.7 us, by max_new
+  // 266; into blocks of 16 48 and 1356; where all have max_new that costs up to 1.2 us: 256
+  // of one row 4.0 without, 5.2 with it).
+  p.ragged = rows > p.rows ? 1 : 0;
   p.by_new = divisor(p.max_new);
-  p.by_parts = divisor(rows * parts < (1ll << 30) ? static_cast<int>(parts) : 1);
-  p.row_items = heads == 0 ? 0 : static_cast<unsigned>(rows * p.by_parts.d);
+  p.by_parts = divisor(parts);  // (at most 2^20 rows of 576 parts)
+  p.row_items = p.ragged ? 0 : static_cast<unsigned>(rows * parts);
   if (p.block_log2 < 0) {
     cfg.gridDim = dim3(1 + kWorkers);
     return cudaLaunchKernelEx(&cfg, append_rows_kernel<D>, p);

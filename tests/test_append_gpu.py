@@ -392,3 +392,23 @@ def test_sequences_of_a_batch_are_sequences_alone():
         for n in ("q_out", "k_cache", "v_cache", "k_scale", "v_scale"):
             if getattr(many, n) is not None:
                 assert torch.equal(getattr(many, n), getattr(alone, n)), (n, block)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim,block", [(64, 0), (128, 0), (256, 16), (128, 64)])
+def test_prompts_beside_single_tokens(dim, block):
+    """One long prompt among sequences of few rows or none, wherever it stands; and prompts of one length."""
+    for at in (0, 7, 39):
+        seqs = [(3 + 5 * b, b % 3) for b in range(40)]
+        seqs[at] = (900, 850)
+        Call(seqs, dim=dim, block=block, page=64, q_heads=6, kv_heads=2, seed=at).check()
+    Call([(200, 100), (100, 100), (163, 100)], dim=dim, block=block, page=64, q_heads=6, kv_heads=2, extra_rows=0, seed=17).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [0, 16])
+def test_any_number_of_rows_allowed(block):
+    """max_new at its bound with as many sequences as there may be, and more heads than are worked on at once."""
+    seqs = [(b % 7, min(b % 7, b % 4)) for b in range(1024)]
+    Call(seqs, dim=256, block=block, q_heads=24, kv_heads=3, max_new=1 << 20, seed=18).check()
+    Call([(90, 80)], dim=256, block=block, q_heads=24, kv_heads=3, max_new=1 << 20, seed=19).check()
