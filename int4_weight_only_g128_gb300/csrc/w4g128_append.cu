@@ -8,11 +8,11 @@
 //     bits, of which the launch alone is most.
 //   * many: a lane has two pieces, both sides of 8 pairs, and works on two values with
 //     one instruction, since here instructions count (a piece a lane, with shuffles and
-//     an address for each, took 41.0 us where this takes 32.6).  Row by row what needs no
+//     an address for each, took 41.0 us where this takes 33.2).  Row by row what needs no
 //     block, by blocks what goes into 8 bits, each on its part of the CTAs.  A prompt of
-//     8191 rows (32 + 2 x 8 heads of 128, blocks of 64) takes 32.6 us, 5.6 TB/s of the 184
+//     8191 rows (32 + 2 x 8 heads of 128, blocks of 64) takes 33.2 us, 5.5 TB/s of the 184
 //     MB that it reads and writes; of as many into bf16 (201 MB) 35.3, 5.7 TB/s.  Two
-//     prompts of 2049 rows of 16 + 2 x 4 heads of 256 in bf16 take 21.1, 4.8 TB/s, for 100
+//     prompts of 2049 rows of 16 + 2 x 4 heads of 256 in bf16 take 21.4, 4.7 TB/s, for 100
 //     MB: start and end take 3 us of it, and 12294 pieces of work on 2424 warps a sixth
 //     round for some.
 // The angle p f of position p is a 64-bit integer of 2^-64 turns, p times f / 2 pi
