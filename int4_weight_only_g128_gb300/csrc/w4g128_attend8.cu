@@ -61,6 +61,7 @@ constexpr int kMostCluster = 16;
 constexpr int kMostChunk = 64;  // tiles
 constexpr int kMostCtas = 16384;  // whole chunks of a call, and so many partial results
 constexpr int kChunkedFrom = 4;  // sequences
+constexpr int kMostCheckers = 16;
 
 struct Params {
   const uint16_t* q;
@@ -71,6 +72,7 @@ struct Params {
   long long q_row, out_row, page_stride, slot_stride, head_stride, scale_page, scale_head, table_row;
   int rows, count, q_heads, kv_heads, group, pages, block_log2, max_len, max_new, window, sinks;
   int clusters, row_groups;  // of a sequence and head
+  int checkers;              // CTAs that look for errors; several leave their results to the second kernel
   int chunk;                 // tiles of one CTA, where a sequence is cut into chunks; or 0
   Divisor by_group, by_page, by_clusters, by_row_groups, by_kv_heads;
   float scale2;              // |scale| log2(e); scale < 0: q's signs are flipped, scale = 0: q counts as 0
@@ -105,9 +107,10 @@ __device__ __forceinline__ bool visible(const Params& p, int row_pos, int pos) {
   return pos <= row_pos && (p.window == 0 || row_pos - pos < p.window || pos < p.sinks);
 }
 
-// One CTA looks all lengths, row ranges and visible page ids over, beside the others.
-__device__ void check_all(const Params& p) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+// The first CTAs (one, but for many pages) look all lengths, row ranges and visible page ids over, beside the others.
+__device__ void check_all(const Params& p, int which) {
+  const int lane = threadIdx.x & 31, warps = (blockDim.x >> 5) * p.checkers;
+  const int warp = which * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int parts = max(1, warps / p.count);  // warps that share a sequence
   constexpr int kBatch = 8;
   bool bad = false;
@@ -131,7 +134,7 @@ __device__ void check_all(const Params& p) {
     }
   }
   if (__syncthreads_or(bad)) bad = true;
-  if (threadIdx.x == 0) st_relaxed_u64(p.status, bad ? W4G128_ERR_CACHE : W4G128_OK);
+  if (threadIdx.x == 0) st_relaxed_u64(p.status + (p.checkers == 1 ? 0 : 1 + which), bad ? W4G128_ERR_CACHE : W4G128_OK);
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t a) {
@@ -271,14 +274,14 @@ attend8_kernel(const __grid_constant__ Params p) {
 
   if (ctas > 1) cluster_arrive_relaxed();  // a CTA runs before another sends it sums
   grid_dependency_wait();
-  if (cluster == 0) {
-    if (rank == 0) check_all(p);
+  if (cluster < p.checkers) {
+    if (rank == 0) check_all(p, cluster);
     if (ctas > 1) cluster_wait_acquire();
     return;
   }
-  // cluster - 1 = ((b kv_heads + head) row_groups + rg) clusters + cl
-  const int rest = (cluster - 1) / p.by_clusters;
-  const int cl = cluster - 1 - rest * p.clusters;
+  // work = ((b kv_heads + head) row_groups + rg) clusters + cl
+  const int work = cluster - p.checkers, rest = work / p.by_clusters;
+  const int cl = work - rest * p.clusters;
   const int up = rest / p.by_row_groups;
   const int rg = rest - up * p.row_groups;
   const int b = up / p.by_kv_heads;
@@ -793,6 +796,14 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
   __shared__ float2 s_stat[kWarps];
   grid_dependency_wait();
   const int b = blockIdx.z, i = blockIdx.y, hq = blockIdx.x;
+  if (p.checkers > 1 && (b | i | hq) == 0 && threadIdx.x < 32) {
+    const bool bad = static_cast<int>(threadIdx.x) < p.checkers && p.status[1 + threadIdx.x] != W4G128_OK;
+    if (__any_sync(~0u, bad)) {
+      if (threadIdx.x == 0) st_relaxed_u64(p.status, W4G128_ERR_CACHE);
+    } else if (threadIdx.x == 0) {
+      st_relaxed_u64(p.status, W4G128_OK);
+    }
+  }
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int head = hq / p.by_group, row = i * p.group + hq - head * p.group;
   const int step = p.max_new * p.group;
@@ -944,7 +955,7 @@ cudaError_t launch(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   if (e != cudaSuccess) return e;
   p.row_groups = (p.max_new * p.group + S::kRows - 1) / S::kRows;
   p.by_row_groups = divisor(p.row_groups);
-  const long long clusters = 1 + static_cast<long long>(p.count) * p.kv_heads * p.row_groups * p.clusters;
+  const long long clusters = p.checkers + static_cast<long long>(p.count) * p.kv_heads * p.row_groups * p.clusters;
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ctas));
   cfg.blockDim = dim3(S::kThreads);
   cfg.dynamicSmemBytes = S::kBytes + (ctas > 1 ? S::received(ctas) : 0);
@@ -1004,6 +1015,11 @@ int w4g128_attend8(const w4g128_attend8_args* a, void* ws, size_t ws_bytes, void
   p.window = a->window; p.sinks = a->sinks;
   p.clusters = split.clusters;
   p.chunk = split.chunk;
+  // One CTA looks the page ids over, beside the others, and more from 32768 on (256
+  // sequences of 8000 on one head of 64, pages of 16: 60.6 us, and 146 with one; one of
+  // 1000003 on one head of 64: 35.9 and 69.6).
+  const long long ids = static_cast<long long>(a->count) * ((a->max_len - 1) / a->page_size + 1);
+  p.checkers = split.clusters == 1 ? 1 : static_cast<int>(std::min<long long>(kMostCheckers, std::max<long long>(1, ids / 16384)));
   p.by_clusters = divisor(split.clusters);
   p.by_kv_heads = divisor(a->kv_heads);
   p.by_group = divisor(p.group);

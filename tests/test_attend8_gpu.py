@@ -508,3 +508,24 @@ def test_a_batch_far_below_its_longest_length():
     # a sequence and head, each with 2 x 2 rows (heads that share one, new tokens) of 64 sums, a reference and a sum.
     assert w.w4g128_attend8_workspace_bytes(c.args()) <= 256 + (16384 + 160) * 4 * (64 + 2) * 4
     c.check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("max_len", [6000, 9600, 100000])
+def test_bad_pages_among_many_are_found(max_len):
+    """More page ids than one CTA looks over: any of them, and only those that some row sees."""
+    seqs = [(2000 + 50 * b, 1) for b in range(60)]
+    c = Call(seqs, q_heads=2, kv_heads=1, dim=64, max_len=max_len, seed=32)
+    clean = c.run().clone()
+    for b in (0, 17, 59):
+        last = (seqs[b][0] - 1) // 16
+        for at in (0, last // 2, last):
+            keep = c.table[b, at].item()
+            c.table[b, at] = c.pages
+            c.out.fill_(7.0)
+            got = c.run(status=w.ERR_CACHE)
+            others = torch.arange(60, device="cuda") != b
+            assert torch.equal(got[:60][others], clean[:60][others])
+            c.table[b, at] = keep
+        c.table[b, last + 1] = -1  # behind the end
+    assert torch.equal(c.run(), clean)
