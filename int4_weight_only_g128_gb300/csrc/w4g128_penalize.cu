@@ -117,7 +117,8 @@ __global__ void __launch_bounds__(T) penalize_kernel(const __grid_constant__ Par
   float listed_value = 0.f;
   if (may_bias) {  // this thread's first entry, on its way while the history is counted
     b0 = max(p.bias_offsets[row], 0);
-    listed = min(max(min(p.bias_offsets[row + 1], p.bias_size) - b0, 0), kMostBias);
+    // (both ends from 0 on before they are subtracted: an end near -2^31 would wrap)
+    listed = min(max(max(min(p.bias_offsets[row + 1], p.bias_size), 0) - b0, 0), kMostBias);
     if (tid < listed) {
       listed_token = p.bias_tokens[b0 + tid];
       listed_value = p.bias_values[b0 + tid];

@@ -194,6 +194,20 @@ def test_ranges_outside_the_buffers_are_not_read():
 
 
 @pytest.mark.gpu
+def test_list_offsets_of_any_value():
+    """Ends far below 0 behind starts above it are empty lists; entries from bias_size on count for nothing."""
+    at = [1, -2 ** 31, 3, -1, 2 ** 31 - 1, -2 ** 31 + 1, 4, 2 ** 31 - 1, -2 ** 31, 2, -2 ** 31 + 1]
+    c = Call(len(at) - 1, 1000, bias=5, seed=13)
+    size = c.bias_tokens.numel()
+    tokens = torch.arange(70000, dtype=torch.int32, device="cuda") % 1000  # every token is listed behind bias_size
+    values = torch.full((70000,), 1e4, device="cuda")
+    tokens[:size], values[:size] = c.bias_tokens, c.bias_values
+    c.bias_at = at
+    c.bias_offsets[:] = torch.tensor(at, dtype=torch.int32)
+    c.check(bias_tokens=tokens, bias_values=values)
+
+
+@pytest.mark.gpu
 def test_the_last_of_a_tokens_biases_counts():
     c = Call(2, 900, bias=400, seed=6)
     c.bias_tokens[:] = c.bias_tokens % 3 + 17  # three neighbours, many times each
