@@ -294,6 +294,8 @@ W4G128_API int w4g128_append(const w4g128_append_args* args, void* ws, size_t ws
  * the products as fp16, exactly; q as fp16 scaled by its row's and head's largest
  * value, exactly down to 2^-31 of that; the softmax weights times the values'
  * scales rounded to fp16: by 2^-11 of their value, or 2^-31 of the row's largest.
+ * The sum of weights is of their fp32 values, whatever the scales are; beside a
+ * value's scale above 2^100 weights below 2^-28 of that sum may be left out of it.
  *
  * Row m's bits depend on its own position, query and visible codes and scales
  * alone, not on the other rows of the call nor on max_new, given the same count,

@@ -14,7 +14,9 @@
 //     weight: with score s_j (base 2) and value scale v_j, P_j = 2^(s_j + log2 v_j - m),
 //     rounded to fp16 as an operand, and the row's sum takes P_j / v_j.  The
 //     reference m follows the maximum of s_j + log2 v_j, so P_j stays in fp16's range
-//     whatever the scales are, and depends on the row alone.
+//     whatever the scales are, and depends on the row alone.  Where m rises by a value
+//     scale, the sum of P_j / v_j so far is large and its factor may be below fp32's
+//     range: it is applied as its root, twice.
 //   * Codes are read by ldmatrix as pairs: K's depth and V's columns then come in
 //     another order than the MMA's, the same for q (laid out so) and for the result.
 //   * The 16-position tiles of a sequence go in turn to all the groups of warps that
@@ -199,14 +201,20 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t a, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
+// 2^(x / 2), whose square brings a sum to another reference.  A sum of weights holds P / v: from
+// 2^-122, the reference's own weight over the largest scale, to 2^118, 2^24 weights over the
+// smallest.  So where 2^x flushes to 0 its product with that sum need not; times the root twice it
+// is there for x down to -252, below which it is 2^-134 at most.
+__device__ __forceinline__ float root_of(float x) { return exp2_fast(0.5f * x); }
+
 // Sums over parts with references and sums of weights of their own; top: the largest reference.
 struct Joined {
   float top, ref, l = 0.f;
   float4 sum = {0.f, 0.f, 0.f, 0.f};
   __device__ __forceinline__ explicit Joined(float t) : top(t), ref(t == kNone ? 0.f : t) {}
   __device__ __forceinline__ void add(const float2& st, const float4& v) {
-    const float w = exp2_fast(st.x - ref);
-    l = fmaf(st.y, w, l);
+    const float root = root_of(st.x - ref), w = root * root;
+    l = fmaf(st.y * root, root, l);
     sum.x = fmaf(v.x, w, sum.x);
     sum.y = fmaf(v.y, w, sum.y);
     sum.z = fmaf(v.z, w, sum.z);
@@ -578,9 +586,11 @@ attend8_kernel(const __grid_constant__ Params p) {
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
           const float was = ref[m][side], now = x - was > kSlack ? x : was;
-          gain[side] = now == was ? 1.f : exp2_fast(was - now);
+          const float root = now == was ? 1.f : root_of(was - now);
+          gain[side] = root * root;
           ref[m][side] = now;
-          l[m][side] *= gain[side];
+          l[m][side] *= root;
+          l[m][side] *= root;
         }
 #pragma unroll
         for (int i = 0; i < D / 8 / kCols; ++i)
@@ -643,7 +653,10 @@ attend8_kernel(const __grid_constant__ Params p) {
           for (int i = 0; i < 4; ++i) {
             const int e = ONE ? 0 : h * 2 + (i & 1);
             const float x = exponent(m, h, i), w = exp2_fast(x);
-            if (w < kLowWeight) l[m][i >> 1] += exp2_fast(x - log_v[e]) - w * inverse[e];
+            if (w < kLowWeight) {  // (a sum of large scales' weights is small itself: 2^x would flush beside it)
+              const float root = root_of(x - log_v[e]);
+              l[m][i >> 1] += root * root - w * inverse[e];
+            }
           }
     }
 
@@ -836,9 +849,10 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
     for (int j = 0; j < kBatch; ++j) {
       if (z + kWarps * j < parts) {
         const float next = fmaxf(top, st[j].x), ref = next == kNone ? 0.f : next;
-        const float old = exp2_fast(top - ref), w = exp2_fast(st[j].x - ref);
+        const float old_root = root_of(top - ref), root = root_of(st[j].x - ref);
+        const float old = old_root * old_root, w = root * root;
         top = next;
-        l = fmaf(st[j].y, w, l * old);
+        l = fmaf(st[j].y * root, root, l * old_root * old_root);
 #pragma unroll
         for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k] * old);
       }
@@ -858,9 +872,9 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
   l = 0.f;
 #pragma unroll
   for (int j = 0; j < kWarps; ++j) {
-    const float w = exp2_fast(s_stat[j].x - ref);
+    const float root = root_of(s_stat[j].x - ref), w = root * root;
     const float2 u = *reinterpret_cast<const float2*>(&s_sum[j][2 * k]);
-    l = fmaf(s_stat[j].y, w, l);
+    l = fmaf(s_stat[j].y * root, root, l);
     x = fmaf(u.x, w, x);
     y = fmaf(u.y, w, y);
   }

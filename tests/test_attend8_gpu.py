@@ -529,3 +529,56 @@ def test_bad_pages_among_many_are_found(max_len):
             c.table[b, at] = keep
         c.table[b, last + 1] = -1  # behind the end
     assert torch.equal(c.run(), clean)
+
+
+def scales_far_apart(seqs, kv_heads, dim, block, order, small, large, **kw):
+    """Value scales of blocks of `small` and `large`, up to twice that, and codes up to 1."""
+    from paged_cases import to_codes
+    c = Call(seqs, q_heads=kv_heads, kv_heads=kv_heads, dim=dim, block=block, page=64, seed=33, **kw)
+    c.v_cache.copy_(to_codes(2 * torch.rand(c.v_cache.shape, generator=c.g, device="cuda").double() - 1).view(c.v_cache.dtype))
+    more = 1 + torch.rand(c.v_scale.shape, generator=c.g, device="cuda")
+    c.v_scale.fill_(small)
+    for b, (n, _) in enumerate(c.seqs):
+        pos = torch.arange(n, device="cuda") // block * block
+        pos = pos[{"small first": pos >= n // 2, "large first": pos < n // 2, "in turn": pos // 64 % 2 == 1,
+                   "one large": pos == (n - 1) // block * block}[order]]
+        c.v_scale[c.table[b, pos // 64].long(), :, pos % 64 // block] = large
+    c.v_scale *= more
+    return c
+
+
+def check_scales_far_apart(c):
+    """Beside reference()'s bound: score and logarithm of the scale add up to 2^8 at most, an fp32 sum (2^-16) of a logarithm
+    good to 2^-22 of its 2^7; a weight is off by as much relative, numerator and denominator."""
+    ref, tol = c.reference()
+    A = torch.full_like(ref, 0.0)
+    for b, (n, new) in enumerate(c.seqs):
+        _, v, _ = c.dense(b)
+        if new:
+            A[c.offsets[b]:c.offsets[b + 1]] = v.abs().amax(0).amax(-1).repeat_interleave(c.Hq // c.Hkv, 0)[None, :, None]
+    got = c.run()
+    mine = ~torch.isnan(ref[:, 0, 0])
+    tol = tol + 2 * (2.0 ** -16 + 2.0 ** -15) * A
+    err = (got[mine].double() - ref[mine]).abs()
+    assert torch.isfinite(got[mine]).all()
+    assert (err <= tol[mine]).all(), float((err / tol[mine].clamp(min=1e-300)).max())
+    # and as a whole: the weights' roundings have no relation to one another
+    for r in torch.nonzero(mine).flatten().tolist():
+        assert (got[r].double() - ref[r]).norm() <= (2.0 ** -8 + 2.0 ** -10) * ref[r].norm(), r
+
+
+FAR_FORMS = {"one CTA": ([(300, 2), (200, 1), (280, 3)], 128, 64), "cluster": ([(600, 2), (200, 3)], 2, 128),
+             "tiles of a group": ([(900, 3), (40, 1)], 64, 64), "second kernel": ([(1700, 2), (31, 1)], 2, 256),
+             "chunks": ([(5000, 3), (9, 1), (3000, 16), (1111, 2), (640, 1)], 2, 128)}
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FAR_FORMS)
+@pytest.mark.parametrize("block", [1, 4, 16, 64])
+@pytest.mark.parametrize("order", ["small first", "large first", "in turn", "one large"])
+def test_value_scales_far_apart(form, block, order):
+    """Weights of values of small scales stay in the sum beside values of scales 2^127 and more times as large, whichever
+    comes first, in one group's tiles and in another's, another CTA's or another chunk's."""
+    seqs, kv_heads, dim = FAR_FORMS[form]
+    for small, large in ((2.0 ** -80, 2.0 ** 47), (2.0 ** -80, 2.0 ** 60), (2.0 ** -40, 2.0 ** 90), (2.0 ** -80, 2.0 ** 124)):
+        check_scales_far_apart(scales_far_apart(seqs, kv_heads, dim, block, order, small, large))
