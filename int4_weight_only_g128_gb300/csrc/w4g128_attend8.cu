@@ -176,10 +176,10 @@ __device__ __forceinline__ float log2_fast(float x) {  // 2^-22
   asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float inverse_fast(float x) {  // 1 ulp
+__device__ __forceinline__ float inverse_fast(float x) {  // 1 ulp; above 2^126 too, where the inverse itself would flush
   float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(0.25f * x));
+  return 0.25f * y;
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t r;

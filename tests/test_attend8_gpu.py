@@ -582,3 +582,17 @@ def test_value_scales_far_apart(form, block, order):
     seqs, kv_heads, dim = FAR_FORMS[form]
     for small, large in ((2.0 ** -80, 2.0 ** 47), (2.0 ** -80, 2.0 ** 60), (2.0 ** -40, 2.0 ** 90), (2.0 ** -80, 2.0 ** 124)):
         check_scales_far_apart(scales_far_apart(seqs, kv_heads, dim, block, order, small, large))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("form", FAR_FORMS)
+@pytest.mark.parametrize("block", [1, 16])
+@pytest.mark.parametrize("small,large", [(2.0 ** 126, 2.0 ** 126), (2.0 ** 127, 2.0 ** 127), (2.0 ** -80, 2.0 ** 127), (1.0, 2.0 ** 126)])
+def test_value_scales_up_to_the_largest(form, block, small, large):
+    """Scales whose inverse is below fp32's normal range (codes up to 1/4, so that the outputs are finite)."""
+    from paged_cases import to_codes
+    seqs, kv_heads, dim = FAR_FORMS[form]
+    c = scales_far_apart(seqs, kv_heads, dim, block, "in turn", small, large)
+    c.v_cache.copy_(to_codes(values(c.v_cache) / 4).view(c.v_cache.dtype))
+    assert torch.isfinite(c.v_scale).all()
+    check_scales_far_apart(c)
