@@ -219,13 +219,17 @@ __device__ __forceinline__ float magnitude(float (&x)[8]) {
   }
   return top;
 }
+// A power of two whose inverse is a normal number too: up to 2^126.
+__device__ __forceinline__ bool has_inverse(float scale) {
+  return (__float_as_uint(scale) & 0x007FFFFFu) == 0u && scale < 0x1p127f;
+}
 __device__ __forceinline__ uint2 coded(const float (&x)[8], float scale) {
   uint32_t code[4];
-  if ((__float_as_uint(scale) & 0x007FFFFFu) == 0u) {
+  if (has_inverse(scale)) {
     const float inverse = exp2_of(127 - static_cast<int>(__float_as_uint(scale) >> 23));
 #pragma unroll
     for (int e = 0; e < 4; ++e) code[e] = to_e4m3x2(x[2 * e] * inverse, x[2 * e + 1] * inverse);
-  } else {  // (a scale that another program set need not be a power of two)
+  } else {  // (a scale that another program set need not be one)
 #pragma unroll
     for (int e = 0; e < 4; ++e) code[e] = to_e4m3x2(__fdiv_rn(x[2 * e], scale), __fdiv_rn(x[2 * e + 1], scale));
   }
@@ -520,7 +524,7 @@ __device__ __forceinline__ float magnitude_two(unsigned long long (&x)[8]) {
 // The codes of 8 values.
 __device__ __forceinline__ uint2 coded_two(const unsigned long long* x, float scale) {
   uint32_t code[4];
-  if ((__float_as_uint(scale) & 0x007FFFFFu) == 0u) {
+  if (has_inverse(scale)) {
     const float inverse = exp2_of(127 - static_cast<int>(__float_as_uint(scale) >> 23));
     const unsigned long long by = two(inverse, inverse);
 #pragma unroll
@@ -529,7 +533,7 @@ __device__ __forceinline__ uint2 coded_two(const unsigned long long* x, float sc
       split(mul_two(x[e], by), lo, hi);
       code[e] = to_e4m3x2(lo, hi);
     }
-  } else {  // (a scale that another program set need not be a power of two)
+  } else {  // (a scale that another program set need not be one)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       float lo, hi;

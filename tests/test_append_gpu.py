@@ -412,3 +412,22 @@ def test_any_number_of_rows_allowed(block):
     seqs = [(b % 7, min(b % 7, b % 4)) for b in range(1024)]
     Call(seqs, dim=256, block=block, q_heads=24, kv_heads=3, max_new=1 << 20, seed=18).check()
     Call([(90, 80)], dim=256, block=block, q_heads=24, kv_heads=3, max_new=1 << 20, seed=19).check()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("scale", [2.0 ** 125, 2.0 ** 126, 2.0 ** 127, 1.5 * 2.0 ** 127])
+@pytest.mark.parametrize("dim,block,seqs", [(64, 16, SEQS), (128, 64, PROMPTS), (256, 4, PROMPTS)], ids=["few", "prompts", "wide"])
+def test_blocks_that_hold_the_largest_scales(scale, dim, block, seqs):
+    """A block's scale stays where the new rows fit under it, up to the largest: its inverse is below fp32's normal range."""
+    c = Call(seqs, dim=dim, block=block, page=64, seed=20)
+    c.k_scale.fill_(scale)
+    c.v_scale.fill_(scale)
+    c.k_new.mul_(2.0 ** 124).clamp_(-2.0 ** 127, 2.0 ** 127)  # (turned: up to 2^127.5)
+    c.v_new.mul_(2.0 ** 124)
+    c.check()
+    held = [b for b, (n, new) in enumerate(seqs) if new and 0 < (n - new) % block]
+    for b in held:
+        n, new = seqs[b]
+        page, at = c.table[b, (n - new) // 64].long(), (n - new) % 64
+        assert (c.v_scale[page, :, at // block] == scale).all()
+        assert (c.v_cache[page, at].view(torch.uint8) & 0x7F != 0).any()
