@@ -294,6 +294,8 @@ W4G128_API int w4g128_append(const w4g128_append_args* args, void* ws, size_t ws
  * the products as fp16, exactly; q as fp16 scaled by its row's and head's largest
  * value, exactly down to 2^-31 of that; the softmax weights times the values'
  * scales rounded to fp16: by 2^-11 of their value, or 2^-31 of the row's largest.
+ * That holds while |scale| times a row's and head's largest |q| times a visible key's
+ * scale is up to 2^140; beyond, a score may pass fp32's range and the row become NaN.
  * The sum of weights is of their fp32 values, whatever the scales are; beside a
  * value's scale above 2^100 weights below 2^-28 of that sum may be left out of it.
  *

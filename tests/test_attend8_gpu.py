@@ -596,3 +596,19 @@ def test_value_scales_up_to_the_largest(form, block, small, large):
     c.v_cache.copy_(to_codes(values(c.v_cache) / 4).view(c.v_cache.dtype))
     assert torch.isfinite(c.v_scale).all()
     check_scales_far_apart(c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("block", [1, 16])
+def test_key_scales_up_to_the_largest(dim, block):
+    """Keys of zeros with the largest scales beside others: their score is 0 while scale, query and key scale stay within 2^140."""
+    c = Call([(300, 3), (1200, 2), (31, 1)], dim=dim, block=block, seed=34)
+    c.q.view(c.rows, c.Hq, dim)[:, :, 0] = 2.0 ** 14
+    c.scale = 0.5
+    c.k_cache[..., 0] = 0
+    zero = torch.rand(c.k_scale.shape, generator=c.g, device="cuda") < 0.3
+    slots = zero.repeat_interleave(block, 2).transpose(1, 2)  # [page][slot][head]
+    c.k_cache[slots] = 0
+    c.k_scale[zero] = 2.0 ** 127
+    c.check()
