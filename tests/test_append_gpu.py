@@ -431,3 +431,34 @@ def test_blocks_that_hold_the_largest_scales(scale, dim, block, seqs):
         page, at = c.table[b, (n - new) // 64].long(), (n - new) % 64
         assert (c.v_scale[page, :, at // block] == scale).all()
         assert (c.v_cache[page, at].view(torch.uint8) & 0x7F != 0).any()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("block", [0, 1, 16])
+@pytest.mark.parametrize("seqs", [[(9, 3), (40, 2)], [(100, 90), (33, 20)]], ids=["few", "prompts"])
+@pytest.mark.parametrize("pairs", [0, 1])
+def test_rotations_beyond_the_range_of_fp32(block, seqs, pairs):
+    """Pairs of 3e38 turn to up to 4.2e38: infinite in bf16, a NaN code in 8 bits, and no part of a block's magnitude."""
+    c = Call(seqs, dim=64, block=block, pairs=pairs, seed=21)
+    c.q.fill_(3e38)
+    c.k_new.fill_(3e38)
+    c.run()
+    top = torch.finfo(torch.float32).max
+    seen = 0
+    for b, (n, new) in enumerate(seqs):
+        rows, pos = slice(c.offsets[b], c.offsets[b] + new), torch.arange(n - new, n, device="cuda")
+        ids, slot = c.table[b, pos // c.page].long(), pos % c.page
+        for x, got in ((c.q, c.q_out[rows, :c.Hq * c.D].reshape(new, c.Hq, c.D)), (c.k_new, c.k_cache[ids, slot])):
+            y, slack = c.rotated(x[rows], pos)
+            if got.dtype == torch.bfloat16:  # bf16 rounds to infinity from 2^128 (1 - 2^-9) on
+                over, clear = y.abs() > 2.0 ** 128 * (1 - 2.0 ** -9), (y.abs() - 2.0 ** 128 * (1 - 2.0 ** -9)).abs() > slack
+                assert (torch.isinf(got) == over)[clear].all()
+            else:
+                over, clear = y.abs() > top, (y.abs() - top).abs() > slack
+                assert (torch.isnan(values(got)) == over)[clear].all()
+            seen += int((over & clear).sum())
+        if block:
+            fits = torch.where(y.abs() <= top, y.abs(), 0.0)
+            assert torch.isfinite(c.k_scale[ids, :, slot // block]).all()
+            assert (448 * c.k_scale[ids, :, slot // block].double() * (1 + 2.0 ** -20) >= fits.amax(-1) - slack.amax(-1)).all()
+    assert seen > 100
