@@ -81,7 +81,7 @@ struct Params {
   uint32_t flip_q, keep_q;
   unsigned long long* status;
   float* part;               // [count][kv_heads][clusters][max_new * group][head_dim]: unnormalised sums
-  float2* stat;              // [count][kv_heads][clusters][max_new * group]: reference and sum
+  float2* stat;              // [count][kv_heads][clusters][max_new * group]: half the reference, and the sum
 };
 
 struct Seq {
@@ -201,19 +201,18 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t a, float2 v) {
   asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y) : "memory");
 }
 
-// 2^(x / 2), whose square brings a sum to another reference.  A sum of weights holds P / v: from
-// 2^-122, the reference's own weight over the largest scale, to 2^118, 2^24 weights over the
-// smallest.  So where 2^x flushes to 0 its product with that sum need not; times the root twice it
-// is there for x down to -252, below which it is 2^-134 at most.
-__device__ __forceinline__ float root_of(float x) { return exp2_fast(0.5f * x); }
+// A sum of weights holds P / v: from 2^-122, the reference's own weight over the largest scale, to
+// 2^118, 2^24 weights over the smallest.  So where the factor 2^x that brings it to another
+// reference flushes to 0, their product need not: the sum takes the factor's root twice, and is
+// there for x down to -252, below which it is 2^-134 at most.  Parts hand on half their references.
 
-// Sums over parts with references and sums of weights of their own; top: the largest reference.
+// Sums over parts with references (halves) and sums of weights of their own; top: the largest reference.
 struct Joined {
   float top, ref, l = 0.f;
   float4 sum = {0.f, 0.f, 0.f, 0.f};
   __device__ __forceinline__ explicit Joined(float t) : top(t), ref(t == kNone ? 0.f : t) {}
   __device__ __forceinline__ void add(const float2& st, const float4& v) {
-    const float root = root_of(st.x - ref), w = root * root;
+    const float root = exp2_fast(st.x - ref), w = root * root;
     l = fmaf(st.y * root, root, l);
     sum.x = fmaf(v.x, w, sum.x);
     sum.y = fmaf(v.y, w, sum.y);
@@ -586,7 +585,7 @@ attend8_kernel(const __grid_constant__ Params p) {
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 2));
           const float was = ref[m][side], now = x - was > kSlack ? x : was;
-          const float root = now == was ? 1.f : root_of(was - now);
+          const float root = now == was ? 1.f : exp2_fast(0.5f * (was - now));
           gain[side] = root * root;
           ref[m][side] = now;
           l[m][side] *= root;
@@ -654,7 +653,7 @@ attend8_kernel(const __grid_constant__ Params p) {
             const int e = ONE ? 0 : h * 2 + (i & 1);
             const float x = exponent(m, h, i), w = exp2_fast(x);
             if (w < kLowWeight) {  // (a sum of large scales' weights is small itself: 2^x would flush beside it)
-              const float root = root_of(x - log_v[e]);
+              const float root = exp2_fast(0.5f * (x - log_v[e]));
               l[m][i >> 1] += root * root - w * inverse[e];
             }
           }
@@ -736,7 +735,7 @@ attend8_kernel(const __grid_constant__ Params p) {
           *reinterpret_cast<float4*>(to + 16 * i) = make_float4(acc[m][2 * i][2 * side], acc[m][2 * i + 1][2 * side],
                                                                 acc[m][2 * i][2 * side + 1], acc[m][2 * i + 1][2 * side + 1]);
         if (c == 0 && part == 0)
-          *reinterpret_cast<float2*>(left + kg * kLeft + kStat + 2 * row) = make_float2(ref[m][side], l[m][side]);
+          *reinterpret_cast<float2*>(left + kg * kLeft + kStat + 2 * row) = make_float2(0.5f * ref[m][side], l[m][side]);
       }
     }
   __syncthreads();
@@ -845,16 +844,22 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
   float top = kNone, l = 0.f, sum[kPer] = {};
   for (int z = warp; z < parts; z += kWarps * kBatch) {
     if (z > warp) load(z);
+    float next = top;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j)
+      if (z + kWarps * j < parts) next = fmaxf(next, st[j].x);
+    const float ref = next == kNone ? 0.f : next, old_root = exp2_fast(top - ref), old = old_root * old_root;
+    top = next;
+    l = l * old_root * old_root;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) sum[k] *= old;
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       if (z + kWarps * j < parts) {
-        const float next = fmaxf(top, st[j].x), ref = next == kNone ? 0.f : next;
-        const float old_root = root_of(top - ref), root = root_of(st[j].x - ref);
-        const float old = old_root * old_root, w = root * root;
-        top = next;
-        l = fmaf(st[j].y * root, root, l * old_root * old_root);
+        const float root = exp2_fast(st[j].x - ref), w = root * root;
+        l = fmaf(st[j].y * root, root, l);
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k] * old);
+        for (int k = 0; k < kPer; ++k) sum[k] = fmaf(v[j][k], w, sum[k]);
       }
     }
   }
@@ -872,7 +877,7 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
   l = 0.f;
 #pragma unroll
   for (int j = 0; j < kWarps; ++j) {
-    const float root = root_of(s_stat[j].x - ref), w = root * root;
+    const float root = exp2_fast(s_stat[j].x - ref), w = root * root;
     const float2 u = *reinterpret_cast<const float2*>(&s_sum[j][2 * k]);
     l = fmaf(s_stat[j].y * root, root, l);
     x = fmaf(u.x, w, x);
