@@ -4,7 +4,7 @@
 // A head's row is pieces of 8 values, 16 bytes, and every byte is read and written once.
 //   * few rows (a decode or verify step): a warp for each head, a piece a lane; the other
 //     side of its pairs comes by shuffle.  What takes time is the chain length -> rows ->
-//     cosines -> store: 2.5 us for one token, 2.7 for 16 sequences of up to 3 rows in 8
+//     cosines -> store: 2.9 us for one token, 3.1 for 16 sequences of up to 3 rows in 8
 //     bits, of which the launch alone is most.
 //   * many: a lane has two pieces, both sides of 8 pairs, and works on two values with
 //     one instruction, since here instructions count (a piece a lane, with shuffles and
@@ -12,7 +12,7 @@
 //     block, by blocks what goes into 8 bits, each on its part of the CTAs.  A prompt of
 //     8191 rows (32 + 2 x 8 heads of 128, blocks of 64) takes 33.2 us, 5.5 TB/s of the 184
 //     MB that it reads and writes; of as many into bf16 (201 MB) 35.3, 5.7 TB/s.  Two
-//     prompts of 2049 rows of 16 + 2 x 4 heads of 256 in bf16 take 21.4, 4.7 TB/s, for 100
+//     prompts of 2049 rows of 16 + 2 x 4 heads of 256 in bf16 take 21.2, 4.8 TB/s, for 100
 //     MB: start and end take 3 us of it, and 12294 pieces of work on 2424 warps a sixth
 //     round for some.
 // The angle p f of position p is a 64-bit integer of 2^-64 turns, p times f / 2 pi

@@ -9,7 +9,7 @@
 //     power of two for each row (exact down to 2^-31 of the row's largest value).
 //     (The warp MMA of e4m3 operands is made of conversions and fp16 products here:
 //     with q as the sum of two e4m3 values it took 936 instructions a tile, and 33
-//     us where this takes 24.6.)
+//     us where fp16 products took 25.6.)
 //   * A key's scale multiplies its score.  A value's scale enters the softmax
 //     weight: with score s_j (base 2) and value scale v_j, P_j = 2^(s_j + log2 v_j - m),
 //     rounded to fp16 as an operand, and the row's sum takes P_j / v_j.  The
@@ -27,14 +27,16 @@
 //     memory; otherwise a second kernel joins them.
 //
 // What bounds it: one sequence of 32771 with 8 rows, 32 heads on 8 of 128 and pages of
-// 64, takes 24.6 us, 2.8 TB/s.  Its bytes alone take 9.9 us, its fp16 products 7.2.  With
+// 64, takes 24.9 us, 2.7 TB/s.  Its bytes alone take 9.9 us, its fp16 products 7.2.  With
 // each group's first tile alone the call takes 10.3 us: 3.3 until the first lengths and
 // ids are there, 2.2 in joining a CTA's groups and writing their sums, 2.1 in the second
 // kernel.  The loop's other 14 us are neither the copies nor the products alone (without
 // copies 1.3 us less, without the products 6 less), but both, the conversions and the
 // softmax at the 8 warps an SM whose sums the registers hold.
-// 16 ragged sequences of up to 9001 on 4 heads of 64 take 18.5 us, two with a window of
-// 4096 and 16 rows each on 4 heads of 256 19.8, one of 611 with one row 4.8.
+// 16 ragged sequences of up to 9001 on 4 heads of 64 take 18.9 us, two with a window of
+// 4096 and 16 rows each on 4 heads of 256 20.5, one of 611 with one row 4.8.  The framework's
+// attention over bf16 takes 29.7, 18.2, 22.7 and 6.0 on these shapes: ragged lengths with a
+// scale for each slot gain nothing by half the bytes.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -230,13 +232,13 @@ struct Shape {
   static constexpr int kKg = groups_of(D);
   static constexpr int kMt = D == 256 || RT == 1 ? 1 : 2;
   // Warps that share a row tile's columns, each with all its scores: two for the widest heads'
-  // few rows, which have few warps otherwise (3 of 4 rows on 4 heads: 17.6 us -> 14.8; 32 rows
+  // few rows, which have few warps otherwise (3 of 4100 with 4 rows on 4 heads: 17.5 us -> 14.6; 32 rows
   // have 8 warps an SM either way: a batch of 16 took 20.3 us with one, 31.4 with two).
   static constexpr int kCols = D == 256 && RT == 1 ? 2 : 1;
   static constexpr int kGroup = RT / kMt * kCols * 32;  // threads of a group
   static constexpr int kThreads = kKg * kGroup;
   // warps an SM, by the registers of a thread's sums: 128 of them leave room for 8, 64 for 12, 32 for 16
-  // (16 with 64 spill: 16 ragged sequences on heads of 64 25.6 us, 20.0 with 12)
+  // (16 with 64 spill: 16 ragged sequences on heads of 64 23.3 us, 19.0 with 12)
   static constexpr int kSums = kMt * D / kCols / 2;
   static constexpr int kWarps = kSums == 128 ? 8 : kSums == 64 ? 12 : 16;
   static constexpr int kCtas = kWarps * 32 / kThreads > 0 ? kWarps * 32 / kThreads : 1;
@@ -245,7 +247,7 @@ struct Shape {
   static constexpr int kStageBytes = 2 * kTileBytes + 2 * kTile * 4;  // K, V and their positions' scales
   static constexpr int kQBytes = kRows * 2 * D;
   static constexpr int kRoom = (227 * 1024 / kCtas - 1536 - kQBytes) / kKg / kStageBytes;
-  // (3: more only take room from the L1 cache; one of 32771 24.6 us, with 6 24.8; batches 25.4, 26.8)
+  // (3: more only take room from the L1 cache; one of 32771 25.1 us, with 6 25.4; 16 of 3000 25.2, 26.5)
   static constexpr int kStages = kRoom < 3 ? kRoom : 3;
   static constexpr int kRing = kKg * kStages * kStageBytes;
   static constexpr int kSumRow = D + 16;     // floats of a row's sums (free of bank conflicts)
@@ -888,25 +890,30 @@ __global__ void __launch_bounds__(kWarps * 32) join8_kernel(const __grid_constan
       pack_bf16(x * inv, y * inv);
 }
 
-// How a sequence and head is shared out (figures with 8 warps in the second kernel, which
-// are up to 1 us above today's).  Not by max_new: a row's sums are the same
-// whatever rows are beside it.  All CTAs of one sequence take its tiles in turn: as many
-// as the GPU holds of those for 32 rows on heads of 64 and 128 (one of 32771, 8 heads of
-// 128: 24.6 us with 303, 29.4 with 220, 33.7 with 455), of those for 64 rows on heads of
-// 256 (2 with a window of 4096, 4 heads, 64 rows each: 20.5 us with 151, 28.9 with 303;
-// of 3 with 4 rows each 14.8 and 13.9; 1 of 32771 without a window 43 and 50, 27 and 22).
-// From 4 sequences on, whose lengths are their own, a CTA takes a chunk of positions, so
-// that a sequence has CTAs by its length: chunks that cut max_len of all into two or
-// three CTAs for each that the GPU holds (16 ragged on 4 heads of 64: 19.6 us with 1213,
-// 20.5 with 909, 23.9 with 1820; 16 on 8 of 128: 19.8 with 909, 25.3 with 606, 18.1 with
-// 1213, but 16 of 3000 each 25.4, 28.5 and 28.1; 8 on 4 of 256: 24.5 with 455, 23.7 with
-// 606, but of 9000 each 35.6 and 44.0).  A chunk has an end, so that the last ones of
-// long calls end together (64 ragged ones of 9000 on 8 heads of 256: 126 us with 64 tiles
-// at most, 147 with 128).  But max_len may be far above the lengths: there are 16384
-// whole chunks at most, most of them without a position (max_len 131072: 64 of 4000 on 8 heads
-// of 128 137 us, 183 without that limit; 256 of up to 1000 on 8 of 64 60 and 334; with a
-// limit of 8192 130 and 53, but 64 of up to 9000 on 8 of 256 299 where this takes 200).  Calls of few CTAs are joined in a cluster (one of 611 on 8
-// heads: 4.8 us, and 5.6 with a second kernel).
+// How a sequence and head is shared out.  Not by max_new: a row's sums are the same whatever
+// rows are beside it.
+//   * All CTAs of one sequence take its tiles in turn: as many as the GPU holds of those for
+//     32 rows on heads of 64 and 128 (one of 32771 with 8 rows, 8 heads of 128: 24.9 us with
+//     303, 29.8 with 220, 34.0 with 455), of those for 64 rows on heads of 256, here with 151
+//     and with 303: 2 with a window of 4096 and 64 rows each on 4 heads 20.6 us and 30.3, one
+//     of 32771 with 64 rows 44.9 and 51.4, with 4 rows 27.3 and 22.0, 3 of 4100 with 4 rows
+//     each 14.6 and 12.9.
+//   * Few CTAs are joined in a cluster (one of 611 on 8 heads: 4.9 us, and 5.7 with a second
+//     kernel).
+//   * From 4 sequences on, whose lengths are their own, a CTA takes a chunk of positions, so
+//     that a sequence has CTAs by its length: chunks that cut max_len of all into two or
+//     three CTAs for each that the GPU holds.  Heads of 64, 16 ragged on 4 heads: 19.0 us
+//     with 1213, 24.6, 20.1 and 26.5 with 606, 909 and 1820.  Heads of 128, 16 ragged of up
+//     to 6000 on 8 heads and 16 of 3000: 23.2 and 25.2 us with 909, 24.9 and 28.3 with 455,
+//     24.9 and 28.6 with 606, 25.7 and 28.3 with 1213.  Heads of 256, 8 ragged of up to 9000
+//     on 4 heads and 8 of 9000: 27.8 and 36.4 us with 455, 41.5 and 44.2 with 303, 26.4 and
+//     45.1 with 606, 23.3 and 38.6 with 909.
+//   * A chunk has an end, so that the last ones of long calls end together (64 ragged ones of
+//     up to 9000 on 8 heads of 256: 130 us with 64 tiles at most, 151 with 128).
+//   * But max_len may be far above the lengths: there are 16384 whole chunks at most, most of
+//     them without a position.  With max_len 131072, with this limit, without one and with
+//     8192: 64 of 4000 on 8 heads of 128 143 us, 190 and 130; 256 of up to 1000 on 8 of 64
+//     51, 337 and 40; 64 of up to 9000 on 8 of 256 210, 229 and 308.
 struct Split {
   int ctas, clusters, chunk;  // CTAs of a cluster; clusters of one sequence and head; tiles of a chunk, or 0
 };
@@ -991,8 +998,8 @@ cudaError_t launch_dim(cudaLaunchConfig_t& cfg, Params& p, int ctas) {
   cfg.numAttrs = 1;
   cfg.gridDim = dim3(p.q_heads, p.max_new, p.count);
   cfg.dynamicSmemBytes = 0;
-  // 4 warps for up to 20, which they ask for at once, otherwise 16 (18.6 us for 16 ragged
-  // sequences in 12 chunks, and 20.8 with 16; 15.0 with 8 and 13.5 with 16 for one of 100003 on one head).
+  // 4 warps for up to 20, which they ask for at once, otherwise 16 (16 ragged sequences in 12 chunks: 19.0 us, 20.1
+  // with 8 and 22.8 with 16; one of 100003 on one head: 14.5 with 16, 17.1 with 8 and 20.6 with 4).
   const bool few = p.clusters <= 20;
   cfg.blockDim = dim3(few ? 128 : 512);
   return few ? cudaLaunchKernelEx(&cfg, join8_kernel<D, 4>, p) : cudaLaunchKernelEx(&cfg, join8_kernel<D, 16>, p);

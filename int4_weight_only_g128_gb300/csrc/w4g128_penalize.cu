@@ -12,8 +12,9 @@
 // the logits and mask words are on their way while the tokens are counted.  A chain of
 // loads (settings, history) bounds one row; 16 rows of 248320 with 4099 tokens and
 // 300 biases take 11.0 us, 1.5 TB/s (its bytes alone take 2.4 us), and 4.7 without
-// the counting, whose chain of loads, additions and barriers at three CTAs an SM is what
-// bounds it.
+// the counting, a chain of loads, additions and barriers.  Registers (59 a thread) leave
+// two CTAs of 512 threads to an SM, 304 at once: its 496 run in two waves, the second
+// nearly as long as the first.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -294,9 +295,9 @@ int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
   p.bias_values = a->bias_values; p.bias_offsets = a->bias_offsets; p.mask = a->mask;
   p.row_stride = a->row_stride; p.out_stride = a->out_stride; p.mask_row = a->mask_row; p.history_size = a->history_size;
   p.bias_size = a->bias_size; p.vocab = a->vocab;
-  // Slices of 8192 tokens, or of 2048 where that makes no more CTAs than two an SM (one
-  // row of 32000: 3.3 us, and 4.0 with 8192; 16 rows of 248320: 11.0 us with 8192, 14.5
-  // with 4096 and 22 with 2048).  Long histories take more threads (one row with 32771
+  // Slices of 8192 tokens, or of 2048 where that makes no more CTAs than two an SM, all at
+  // once (one row of 32000: 3.3 us, and 4.0 with 8192; 16 rows of 248320: 11.0 us with 8192
+  // in two waves, 14.5 with 4096 in four and 22 with 2048 in seven).  Long histories take more threads (one row with 32771
   // tokens: 5.5 us, and 8.5 with 512; with 613 tokens 3.4 and 3.3, 16 rows with 4099 15.7
   // and 11.0).
   p.slice = static_cast<long long>(a->rows) * ((a->vocab + 7 + 2047) / 2048) <= 304 ? 2048 : kMostSlice;
