@@ -228,11 +228,12 @@ W4G128_API int w4g128_moe(const w4g128_moe_args* args, void* ws, size_t ws_bytes
  * 2^max(floor(log2 top) - 5, -100) (above every earlier one that does not fit),
  * and those earlier positions' codes are rounded to it, which is exact down to
  * 2^-6.  Codes are rounded to nearest, ties to even; what is not finite (a
- * rotated value beyond fp32's range is not) is a NaN code.  The 5 leaves new rows of a block room of a factor 7 to 14 before it
- * changes.  A key whose exact value lies within 2^-21 of its pair's size of the
- * middle between two codes may become either.  With block = 1 a row's codes are its own; with larger blocks they
- * also follow the rows that share the block, and a draft row that is rejected
- * leaves the scale as it needed it.
+ * rotated value beyond fp32's range is not) is a NaN code.  The 5 leaves new rows
+ * of a block room of a factor 7 to 14 before it changes.  A key whose exact value
+ * lies within 2^-21 of its pair's size of the middle between two codes may become
+ * either.  With block = 1 a row's codes are its own; with larger blocks they also
+ * follow the rows that share the block, and a draft row that is rejected leaves the
+ * scale as it needed it.
  *
  * Rows at negative positions and of no sequence are left as they are, in q_out
  * too, and so are the slots behind a sequence's length. */

@@ -207,8 +207,8 @@ __device__ __forceinline__ void st_cluster_v2(uint32_t a, float2 v) {
 // 2^118, 2^24 weights over the smallest.  So where the factor 2^x that brings it to another
 // reference flushes to 0, their product need not: the sum takes the factor's root twice, and is
 // there for x down to -252, below which it is 2^-134 at most.  Parts hand on half their references.
-
-// Sums over parts with references (halves) and sums of weights of their own; top: the largest reference.
+//
+// Sums over parts with (half) references and sums of weights of their own; top: the largest reference.
 struct Joined {
   float top, ref, l = 0.f;
   float4 sum = {0.f, 0.f, 0.f, 0.f};

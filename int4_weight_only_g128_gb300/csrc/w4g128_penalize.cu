@@ -297,9 +297,9 @@ int w4g128_penalize(const w4g128_penalize_args* a, void* stream) {
   p.bias_size = a->bias_size; p.vocab = a->vocab;
   // Slices of 8192 tokens, or of 2048 where that makes no more CTAs than two an SM, all at
   // once (one row of 32000: 3.3 us, and 4.0 with 8192; 16 rows of 248320: 11.0 us with 8192
-  // in two waves, 14.5 with 4096 in four and 22 with 2048 in seven).  Long histories take more threads (one row with 32771
-  // tokens: 5.5 us, and 8.5 with 512; with 613 tokens 3.4 and 3.3, 16 rows with 4099 15.7
-  // and 11.0).
+  // in two waves, 14.5 with 4096 in four and 22 with 2048 in seven).  Long histories take
+  // more threads (one row with 32771 tokens: 5.5 us, and 8.5 with 512; with 613 tokens 3.4
+  // and 3.3, 16 rows with 4099 15.7 and 11.0).
   p.slice = static_cast<long long>(a->rows) * ((a->vocab + 7 + 2047) / 2048) <= 304 ? 2048 : kMostSlice;
   const int ctas = (a->vocab + 7 + p.slice - 1) / p.slice;
   const bool wide = a->history_size / a->rows > 8192;
